@@ -31,6 +31,8 @@ __all__ = ["differential_lambda", "differential_attention", "differential_attent
            "differential_attention_train",
            "differential_attention_backward",
            "differential_attention_decode",
+           "rotary_tables", "qk_norm_rotary", "paged_cache_append",
+           "differential_attention_paged", "differential_attention_tree",
            "make_desc", "make_kv_desc", "select_kernel", "get_device_error", "version",
            "DiffattnError"]
 
@@ -578,7 +580,12 @@ def _epilogue(norm, eps, weight, bias, out_scale, H, Dv, dev):
 
 def get_device_error(device=None) -> int:
     """Synchronise the current stream and return the library's device status
-    (0, or DIFFATTN_ERR_TIMEOUT if a kernel's bounded wait ran out)."""
+    (0, DIFFATTN_ERR_TIMEOUT if a kernel's bounded wait ran out, or
+    DIFFATTN_ERR_INDEX if one met a position, length or page outside its table)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         return _lib.load().diffattn_get_device_error(_stream_handle(dev))
+
+
+from ._paged import (differential_attention_paged, differential_attention_tree,  # noqa: E402
+                     paged_cache_append, qk_norm_rotary, rotary_tables)

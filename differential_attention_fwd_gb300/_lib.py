@@ -12,6 +12,7 @@ DIFFATTN_ERR_INVALID = -1
 DIFFATTN_ERR_UNSUPPORTED = -2
 DIFFATTN_ERR_CUDA = -3
 DIFFATTN_ERR_TIMEOUT = -4
+DIFFATTN_ERR_INDEX = -5
 
 DIFFATTN_BF16 = 0
 DIFFATTN_F32 = 1
@@ -38,6 +39,12 @@ EXPORTED = (
     "diffattn_decode_workspace_bytes",
     "diffattn_decode_noalloc",
     "diffattn_workspace_bytes",
+    "diffattn_rotary",
+    "diffattn_rotary_bwd",
+    "diffattn_rotary_bwd_workspace_bytes",
+    "diffattn_paged_append",
+    "diffattn_paged_decode",
+    "diffattn_paged_workspace_bytes",
     "diffattn_select_kernel",
     "diffattn_get_device_error",
     "diffattn_selftest_timeout",
@@ -75,6 +82,40 @@ class DiffattnEpilogue(ctypes.Structure):
     _fields_ = [
         ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
         ("bias", ctypes.c_void_p), ("out_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+class DiffattnRotaryDesc(ctypes.Structure):
+    """Mirror of diffattn_rotary_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("H", ctypes.c_int64),
+        ("Hk", ctypes.c_int64), ("dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("pos64", ctypes.c_int32), ("table_rows", ctypes.c_int64), ("pos_stride", ctypes.c_int64 * 2),
+        ("q_weight_stride", ctypes.c_int64), ("k_weight_stride", ctypes.c_int64),
+        ("q1_stride", ctypes.c_int64 * 3), ("k1_stride", ctypes.c_int64 * 3),
+        ("q2_stride", ctypes.c_int64 * 3), ("k2_stride", ctypes.c_int64 * 3),
+        ("q1_grad_stride", ctypes.c_int64 * 3), ("k1_grad_stride", ctypes.c_int64 * 3),
+        ("q2_grad_stride", ctypes.c_int64 * 3), ("k2_grad_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class DiffattnPages(ctypes.Structure):
+    """Mirror of diffattn_pages."""
+    _fields_ = [
+        ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+        ("block_table_stride", ctypes.c_int64), ("k1_stride", ctypes.c_int64 * 3),
+        ("k2_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class DiffattnPagedDesc(ctypes.Structure):
+    """Mirror of diffattn_paged_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("Tq", ctypes.c_int64), ("D", ctypes.c_int64),
+        ("Dv", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kv_group", ctypes.c_int32),
+        ("q1_stride", ctypes.c_int64 * 3), ("q2_stride", ctypes.c_int64 * 3),
+        ("o_stride", ctypes.c_int64 * 3), ("mask_stride", ctypes.c_int64 * 2),
     ]
 
 
@@ -135,6 +176,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_decode_workspace_bytes.argtypes = [ctypes.POINTER(DiffattnKvDesc)]
     lib.diffattn_decode_workspace_bytes.restype = ctypes.c_size_t
+    # these take their descriptors as packed bytes too (see _paged.py)
+    lib.diffattn_rotary.argtypes = [vp] * 15
+    lib.diffattn_rotary.restype = ctypes.c_int
+    lib.diffattn_rotary_bwd.argtypes = [vp] * 21 + [ctypes.c_size_t, vp]
+    lib.diffattn_rotary_bwd.restype = ctypes.c_int
+    lib.diffattn_rotary_bwd_workspace_bytes.argtypes = [vp]
+    lib.diffattn_rotary_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.diffattn_paged_append.argtypes = [vp, i64] + [vp] * 16
+    lib.diffattn_paged_append.restype = ctypes.c_int
+    lib.diffattn_paged_decode.argtypes = [vp] * 11 + [ctypes.c_float, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.diffattn_paged_decode.restype = ctypes.c_int
+    lib.diffattn_paged_workspace_bytes.argtypes = [vp, vp]
+    lib.diffattn_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_workspace_bytes.argtypes = []
     lib.diffattn_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_fwd.restype = ctypes.c_int

@@ -2,6 +2,8 @@
 // selection, TMA tensor-map encoding and launches on the caller's stream.
 #include "diffattn.h"
 #include "kernels.h"
+#include "paged.h"
+#include "ptx.cuh"
 
 #include <cmath>
 #include <cstdint>
@@ -388,6 +390,21 @@ int backward_impl(const diffattn_desc* desc, const void* q1, const void* k1, con
                   diffattn_stream_t stream);
 
 }  // namespace
+
+int device_info(uint32_t** status, int* num_sms) {
+    DeviceState* st = nullptr;
+    const int rc = device_state(&st);
+    if (rc != DIFFATTN_OK) return rc;
+    *status = st->status;
+    *num_sms = st->num_sms;
+    return DIFFATTN_OK;
+}
+
+int encode_map_4d(CUtensorMap* m, const void* base, const int64_t dims[4], const int64_t s[3],
+                  uint32_t box_inner, uint32_t box_rows) {
+    return encode_map_t(m, base, dims[0], dims[3], dims[1], dims[2], s, box_inner, box_rows);
+}
+
 }  // namespace diffattn
 
 using namespace diffattn;
@@ -452,15 +469,6 @@ int diffattn_fwd_train(const diffattn_desc* desc, const void* q1, const void* k1
 }  // extern "C"
 
 namespace diffattn {
-namespace {
-
-// Shape and layout of one forward launch: Tq query rows over Tk keys, query
-// row i at key position i + kv_off (causal mask: keys j > i + kv_off hidden).
-struct FwdShape {
-    int64_t B, H, Hk, Tq, Tk, D, Dv, kv_off;
-    int32_t dtype;
-    const int64_t *sq1, *sk1, *sq2, *sk2, *sv, *so;
-};
 
 int check_epilogue(const diffattn_epilogue* epi, diffattn_epilogue* e) {
     *e = diffattn_epilogue{DIFFATTN_NORM_NONE, 0.f, nullptr, nullptr, 1.0f, 0};
@@ -472,6 +480,16 @@ int check_epilogue(const diffattn_epilogue* epi, diffattn_epilogue* e) {
         return DIFFATTN_ERR_INVALID;
     return DIFFATTN_OK;
 }
+
+namespace {
+
+// Shape and layout of one forward launch: Tq query rows over Tk keys, query
+// row i at key position i + kv_off (causal mask: keys j > i + kv_off hidden).
+struct FwdShape {
+    int64_t B, H, Hk, Tq, Tk, D, Dv, kv_off;
+    int32_t dtype;
+    const int64_t *sq1, *sk1, *sq2, *sk2, *sv, *so;
+};
 
 // One forward launch (arguments already checked): the tensor-core kernel when
 // the shape, pointers and strides allow it, else the CUDA-core kernel.
@@ -1142,7 +1160,7 @@ int diffattn_get_device_error(diffattn_stream_t stream) {
     if (word == 0) return DIFFATTN_OK;
     if (cudaMemset(dev->status, 0, sizeof(word)) != cudaSuccess) return DIFFATTN_ERR_CUDA;
     if (cudaDeviceSynchronize() != cudaSuccess) return DIFFATTN_ERR_CUDA;
-    return DIFFATTN_ERR_TIMEOUT;
+    return (word & kStatusTimeout) ? DIFFATTN_ERR_TIMEOUT : DIFFATTN_ERR_INDEX;
 }
 
 const char* diffattn_strerror(int code) {
@@ -1152,6 +1170,7 @@ const char* diffattn_strerror(int code) {
         case DIFFATTN_ERR_UNSUPPORTED: return "unsupported request";
         case DIFFATTN_ERR_CUDA: return "CUDA error";
         case DIFFATTN_ERR_TIMEOUT: return "a kernel wait ran out of time";
+        case DIFFATTN_ERR_INDEX: return "a position, length or page outside its table";
         default: return "unknown error code";
     }
 }

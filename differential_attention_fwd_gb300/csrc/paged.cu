@@ -1,0 +1,475 @@
+// paged.cu -- differential attention over a paged key/value cache: the pass that
+// merges partial results, and the CUDA-core kernel, which takes every type, width and
+// page size (the tensor-core kernels in paged_mma.cu and paged_tc.cu take bf16 with a
+// value width of 128).
+//
+// CUDA-core kernel: a block of 128 threads streams a unit's keys in tiles of 32 through
+// two stages of shared memory (cp.async, one tile ahead).  Per tile: each thread takes
+// one key of one branch against half of the unit's rows; each warp forms the running
+// maxima, weights and sums of its rows with a lane a key; then a thread takes one output
+// column (two for Dv > 128) of both branches and all rows over its share of the keys.
+// Everything is float32, as the float32 cache's results are.  A tile that reaches into
+// the new tokens or past the end marks hidden keys by a negative weight, which the
+// sums leave out: a hidden key's value may hold anything.
+#include "paged_plan.cuh"
+#include "kernels.h"
+#include "pdl.cuh"
+
+namespace diffattn {
+namespace paged {
+
+constexpr int THREADS = 128;
+constexpr int WARPS = THREADS / 32;
+constexpr int KT = 32;
+constexpr int MAX_RC = 16;
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// 16 bytes of shared memory as floats.
+__device__ __forceinline__ void load16(const float* p, float* x) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Shared memory of the CUDA-core kernel.  Key rows are 16 bytes longer than their
+// data, so that threads of one quarter warp read 16 bytes of eight rows from
+// different banks; widths are rounded up to 16 bytes with zeros.
+struct Layout {
+    int dpad;           // D rounded up to 16 bytes, elements
+    int krow, vrow;     // row strides, elements
+    int stage;          // bytes
+    int off_q, off_p, off_stat, total;
+};
+__host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, bool shared) {
+    const int v = 16 / es;
+    Layout l;
+    l.dpad = (D + v - 1) / v * v;
+    l.krow = l.dpad + v;
+    l.vrow = (Dv + v - 1) / v * v;
+    l.stage = KT * ((shared ? 1 : 2) * l.krow + l.vrow) * es;
+    // the stages also hold the merged O of a segment: [2][rc][Dv] floats
+    const int stages = 2 * l.stage > 8 * rc * Dv ? 2 * l.stage : 8 * rc * Dv;
+    l.off_q = (stages + 15) / 16 * 16;                          // float [2][rc][dpad]
+    l.off_p = l.off_q + 2 * rc * l.dpad * 4;                    // float [KT][2 rc]
+    l.off_stat = l.off_p + KT * 2 * rc * 4;                     // float m, l, alpha [2 rc]
+    l.total = l.off_stat + 3 * 2 * rc * 4;
+    return l;
+}
+
+template <typename T, int RC>
+__global__ void __launch_bounds__(THREADS)
+paged_simt_kernel(const PagedParams p) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scan[WARPS + 1];
+    __shared__ PagedStart start_s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int D = p.D, Dv = p.Dv;
+    const bool shared = p.k_shared != 0;
+    const Layout L = simt_layout(D, Dv, sizeof(T), RC, shared);
+    float* qs = reinterpret_cast<float*>(smem + L.off_q);
+    float* ps = reinterpret_cast<float*>(smem + L.off_p);
+    float* st_m = reinterpret_cast<float*>(smem + L.off_stat);
+    float* st_l = st_m + 2 * RC;
+    float* st_a = st_l + 2 * RC;
+    pdl_launch_dependents();
+    const PagedStart start = paged_start<THREADS>(p, KT, scan, &start_s);
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+
+    // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
+    const int CG = Dv <= 32 ? 32 : Dv <= 64 ? 64 : 128;
+    const int KG = THREADS / CG;
+    const int c0 = tid % CG, kg = tid / CG;
+    const bool two = Dv > 128;
+
+    PagedCursor cur;
+    for (cur.begin(p, start, KT); !cur.done(); cur.next(p, KT)) {
+        const int live = cur.live_tiles(p, KT);
+        const int n_new = cur.s.n_new;
+        bool bad = cur.s.bad;
+        // the rows' queries and state
+        for (int i = tid; i < 2 * RC * L.dpad; i += THREADS) {
+            const int br = i / (RC * L.dpad), r = i / L.dpad % RC, c = i % L.dpad;
+            const PagedRow x = paged_row(p, cur.hk, cur.rc, r, n_new);
+            float v = 0.f;
+            if (x.live && c < D) {
+                const T* src = br ? static_cast<const T*>(p.q2) + cur.b * p.s_q2[0] + x.h * p.s_q2[1] + x.q * p.s_q2[2]
+                                  : static_cast<const T*>(p.q1) + cur.b * p.s_q1[0] + x.h * p.s_q1[1] + x.q * p.s_q1[2];
+                v = to_float<T>(src[c]);
+            }
+            qs[i] = v;
+        }
+        if (tid < 2 * RC) { st_m[tid] = -INFINITY; st_l[tid] = 0.f; }
+        float acc[2][2][RC];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < RC; ++r) acc[i][0][r] = acc[i][1][r] = 0.f;
+
+        // Stage a tile: four threads a key row.  A row past the sequence's end or on a
+        // page outside the cache is zeros (the latter makes the segment's rows NaN).
+        auto stage = [&](int tile, int buf) {
+            const int r = tid >> 2, c4 = tid & 3;
+            const int key = (cur.tile0 + tile) * KT + r;
+            T* k1 = reinterpret_cast<T*>(smem + buf * L.stage) + r * L.krow;
+            T* k2 = k1 + KT * L.krow;
+            T* v = reinterpret_cast<T*>(smem + buf * L.stage) + (shared ? 1 : 2) * KT * L.krow + r * L.vrow;
+            int page = -1;
+            if (key < cur.s.total) {
+                page = paged_page(p, cur.b, key / p.page);
+                if (page < 0) { bad = true; atomicOr(p.status, kStatusIndex); }
+            }
+            const int64_t slot = key % p.page;
+            const T* g1 = static_cast<const T*>(p.k1) + page * p.s_k1[0] + cur.hk * p.s_k1[1] + slot * p.s_k1[2];
+            const T* g2 = static_cast<const T*>(p.k2) + page * p.s_k2[0] + cur.hk * p.s_k2[1] + slot * p.s_k2[2];
+            const T* gv = static_cast<const T*>(p.v) + page * p.s_v[0] + cur.hk * p.s_v[1] + slot * p.s_v[2];
+            if (page >= 0 && p.vec16) {
+                for (int c = c4 * V; c < D; c += 4 * V) {
+                    cp_async16(k1 + c, g1 + c);
+                    if (!shared) cp_async16(k2 + c, g2 + c);
+                }
+                for (int c = c4 * V; c < Dv; c += 4 * V) cp_async16(v + c, gv + c);
+            } else {
+                for (int c = c4; c < L.dpad; c += 4) {
+                    k1[c] = page >= 0 && c < D ? g1[c] : T(0.f);
+                    if (!shared) k2[c] = page >= 0 && c < D ? g2[c] : T(0.f);
+                }
+                for (int c = c4; c < L.vrow; c += 4) v[c] = page >= 0 && c < Dv ? gv[c] : T(0.f);
+            }
+        };
+        if (live > 0) stage(0, 0);
+        cp_async_commit();
+        for (int i = 0; i < live; ++i) {
+            if (i + 1 < live) stage(i + 1, (i + 1) & 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+            __syncthreads();
+            const T* kt = reinterpret_cast<const T*>(smem + (i & 1) * L.stage);
+            const T* vt = kt + (shared ? 1 : 2) * KT * L.krow;
+            const int key0 = (cur.tile0 + i) * KT;
+            const bool edge = key0 + KT > cur.s.before;      // some row may not see some key
+            // ---- scores: key `lane` of branch (warp & 1), rows of half (warp >> 1)
+            {
+                constexpr int HALF = RC > 1 ? RC / 2 : 1;
+                const int br = warp & 1, r0 = (warp >> 1) * HALF;
+                if (RC > 1 || warp < 2) {
+                    const T* kr = kt + (br && !shared ? KT * L.krow : 0) + lane * L.krow;
+                    const float* q = qs + (br * RC + r0) * L.dpad;
+                    float s[HALF];
+#pragma unroll
+                    for (int r = 0; r < HALF; ++r) s[r] = 0.f;
+                    for (int c = 0; c < L.dpad; c += V) {
+                        float x[V];
+                        load16(kr + c, x);
+#pragma unroll
+                        for (int r = 0; r < HALF; ++r)
+#pragma unroll
+                            for (int e = 0; e < V; ++e) s[r] = fmaf(q[r * L.dpad + c + e], x[e], s[r]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < HALF; ++r) ps[lane * 2 * RC + br * RC + r0 + r] = s[r] * p.scale_log2;
+                }
+            }
+            __syncthreads();
+            // ---- weights: a warp takes rows (branch, r) warp, warp + 4, ...
+            for (int j = warp; j < 2 * RC; j += WARPS) {
+                float s = ps[lane * 2 * RC + j];
+                bool seen = true;
+                if (edge) {
+                    const PagedRow x = paged_row(p, cur.hk, cur.rc, j % RC, n_new);
+                    const int64_t d = key0 + lane - cur.s.before;      // place among the new tokens
+                    seen = key0 + lane < cur.s.total && x.live &&
+                           (d < 0 || (p.mask ? p.mask[cur.b * p.mask_stride[0] + x.q * p.mask_stride[1] + d] != 0
+                                             : d <= x.q));
+                    if (!seen) s = -INFINITY;
+                }
+                float top = s;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float m0 = st_m[j], m = fmaxf(m0, top);
+                const float w = s == -INFINITY ? 0.f : exp2f(s - m);   // NaN scores stay NaN
+                float sum = w;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                ps[lane * 2 * RC + j] = seen ? w : -1.f;
+                __syncwarp();
+                if (lane == 0) {
+                    const float a = m0 == m ? 1.f : exp2f(m0 - m);
+                    st_m[j] = m;
+                    st_l[j] = st_l[j] * a + sum;
+                    st_a[j] = a;
+                }
+            }
+            __syncthreads();
+            // ---- O = alpha O + P V
+            if (c0 < Dv) {
+#pragma unroll
+                for (int r = 0; r < RC; ++r) {
+                    const float a1 = st_a[r], a2 = st_a[RC + r];
+                    acc[0][0][r] *= a1;
+                    acc[0][1][r] *= a2;
+                    acc[1][0][r] *= a1;
+                    acc[1][1][r] *= a2;
+                }
+                const bool second = two && c0 + 128 < Dv;
+                for (int t = kg; t < KT; t += KG) {
+                    const float x = to_float<T>(vt[t * L.vrow + c0]);
+                    const float y = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
+                    const float* w = ps + t * 2 * RC;
+                    if (!edge) {
+#pragma unroll
+                        for (int r = 0; r < RC; ++r) {
+                            acc[0][0][r] = fmaf(w[r], x, acc[0][0][r]);
+                            acc[0][1][r] = fmaf(w[RC + r], x, acc[0][1][r]);
+                            if (two) {
+                                acc[1][0][r] = fmaf(w[r], y, acc[1][0][r]);
+                                acc[1][1][r] = fmaf(w[RC + r], y, acc[1][1][r]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < RC; ++r) {
+                            if (w[r] < 0.f) continue;               // hidden
+                            acc[0][0][r] = fmaf(w[r], x, acc[0][0][r]);
+                            acc[0][1][r] = fmaf(w[RC + r], x, acc[0][1][r]);
+                            acc[1][0][r] = fmaf(w[r], y, acc[1][0][r]);
+                            acc[1][1][r] = fmaf(w[RC + r], y, acc[1][1][r]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();        // the stage and the weights are free again
+        }
+        bad = __syncthreads_or(bad);
+        cp_async_wait<0>();
+        __syncthreads();
+        // ---- the key groups' sums, in order, then the rows out
+        float* om = reinterpret_cast<float*>(smem);         // [2][RC][Dv]
+        for (int k = 0; k < KG; ++k) {
+            if (kg == k && c0 < Dv) {
+#pragma unroll
+                for (int r = 0; r < RC; ++r)
+#pragma unroll
+                    for (int br = 0; br < 2; ++br) {
+                        float* o = om + (br * RC + r) * Dv + c0;
+                        o[0] = k ? o[0] + acc[0][br][r] : acc[0][br][r];
+                        if (two && c0 + 128 < Dv) o[128] = acc[1][br][r];      // one key group then
+                    }
+            }
+            __syncthreads();
+        }
+        const int stride = 4 + 2 * Dv;
+        for (int r = warp; r < RC; r += WARPS) {
+            const PagedRow x = paged_row(p, cur.hk, cur.rc, r, n_new);
+            if (!x.live) continue;
+            const float l1 = bad ? __int_as_float(0x7fc00000) : st_l[r];
+            const float l2 = bad ? __int_as_float(0x7fc00000) : st_l[RC + r];
+            if (cur.whole()) {
+                float o1[8], o2[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = lane + 32 * j;
+                    o1[j] = c < Dv ? om[r * Dv + c] : 0.f;
+                    o2[j] = c < Dv ? om[(RC + r) * Dv + c] : 0.f;
+                }
+                paged_finish_row(p, lam, cur.b, x.h, x.q, lane, o1, l1, o2, l2);
+            } else {
+                float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * stride;
+                if (lane == 0) {
+                    part[0] = st_m[r];
+                    part[1] = l1;
+                    part[2] = st_m[RC + r];
+                    part[3] = l2;
+                }
+                for (int c = lane; c < Dv; c += 32) {
+                    part[4 + c] = om[r * Dv + c];
+                    part[4 + Dv + c] = om[(RC + r) * Dv + c];
+                }
+            }
+        }
+        if (cur.s.bad && tid == 0) atomicOr(p.status, kStatusIndex);
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merging pass: the unit that boundary c = blockIdx.x + 1 is the first to cut, if any.
+// With partial maxima m_i (log2 units), sums l_i and O_i:
+//     M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i.
+// A warp takes a row; with more than four parts all warps of the block share a row's
+// parts, in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int C_WARPS = 8;
+
+struct Merged {
+    float m[2], l[2], o[2][8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int br = 0; br < 2; ++br) {
+            m[br] = -INFINITY;
+            l[br] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[br][j] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void add(const float* part, int Dv, int lane) {
+        float x[2][8];
+#pragma unroll
+        for (int br = 0; br < 2; ++br)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = lane + 32 * j;
+                x[br][j] = c < Dv ? part[4 + br * Dv + c] : 0.f;
+            }
+#pragma unroll
+        for (int br = 0; br < 2; ++br) {
+            const float pm = part[2 * br], pl = part[2 * br + 1];
+            const float mn = fmaxf(m[br], pm);
+            const float a = m[br] == -INFINITY ? 0.f : exp2f(m[br] - mn);
+            const float c = pm == -INFINITY ? 0.f : exp2f(pm - mn);
+            // a part that saw nothing has sum 0 and O 0, or a sum of NaN (a bad page)
+            l[br] = l[br] * (m[br] == -INFINITY ? 1.f : a) + pl * (pm == -INFINITY ? 1.f : c);
+            m[br] = mn;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[br][j] = (a == 0.f ? 0.f : o[br][j] * a) + (c == 0.f ? 0.f : x[br][j] * c);
+        }
+    }
+};
+
+__global__ void __launch_bounds__(C_WARPS * 32)
+paged_combine_kernel(const PagedParams p) {
+    __shared__ float share[C_WARPS][4 + 512];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    const int64_t total = p.cum[p.B];
+    const int64_t grid = total < p.grid ? total : (int64_t)p.grid;
+    const int64_t c = blockIdx.x + 1;
+    if (c >= grid) return;
+    const int64_t t = c * total / grid;
+    int lo = 0, hi = p.B;                       // cum[lo] <= t < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (p.cum[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int b = lo;
+    const int64_t units = (int64_t)p.Hk * p.row_chunks;
+    const int64_t tiles = (p.cum[b + 1] - p.cum[b]) / units;
+    const int64_t unit = (t - p.cum[b]) / tiles;
+    const int64_t u0 = p.cum[b] + unit * tiles, u1 = u0 + tiles;
+    if (t == u0 || (c - 1) * total / grid > u0) return;
+    int64_t c1 = c;                             // the last block with tiles of the unit
+    while (c1 + 1 < grid && (c1 + 1) * total / grid < u1) ++c1;
+    const int parts = (int)(c1 - c + 2);        // of blocks c - 1 .. c1
+    const int hk = (int)(unit / p.row_chunks), rc = (int)(unit - (int64_t)hk * p.row_chunks);
+    const PagedSeq s = paged_seq(p, b);
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const int64_t stride = 4 + 2 * p.Dv;
+    auto part_of = [&](int i, int r) {
+        const int64_t slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i);
+        return p.part + (slot * p.chunk_rows + r) * stride;
+    };
+    const bool spread = parts > 4;
+    const int step = spread ? gridDim.y : gridDim.y * C_WARPS;
+    for (int r = spread ? blockIdx.y : blockIdx.y * C_WARPS + warp; r < p.chunk_rows; r += step) {
+        const PagedRow x = paged_row(p, hk, rc, r, s.n_new);
+        if (!x.live) continue;
+        Merged a;
+        a.clear();
+        if (!spread) {
+            for (int i = 0; i < parts; ++i) a.add(part_of(i, r), p.Dv, lane);
+        } else {
+#pragma unroll 2
+            for (int i = warp; i < parts; i += C_WARPS) a.add(part_of(i, r), p.Dv, lane);
+            float* mine = share[warp];
+            if (lane == 0) {
+                mine[0] = a.m[0]; mine[1] = a.l[0]; mine[2] = a.m[1]; mine[3] = a.l[1];
+            }
+#pragma unroll
+            for (int br = 0; br < 2; ++br)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (lane + 32 * j < p.Dv) mine[4 + br * p.Dv + lane + 32 * j] = a.o[br][j];
+            __syncthreads();
+            if (warp == 0) {
+                a.clear();
+                for (int w = 0; w < C_WARPS; ++w) a.add(share[w], p.Dv, lane);
+            }
+        }
+        if (!spread || warp == 0)
+            paged_finish_row(p, lam, b, x.h, x.q, lane, a.o[0], a.l[0], a.o[1], a.l[1]);
+        if (spread) __syncthreads();
+    }
+}
+
+template <typename T, int RC>
+int launch_rc(const PagedParams& p, cudaStream_t stream) {
+    const Layout L = simt_layout(p.D, p.Dv, sizeof(T), RC, p.k_shared != 0);
+    if (cudaFuncSetAttribute(paged_simt_kernel<T, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) !=
+        cudaSuccess)
+        return -1;
+    paged_simt_kernel<T, RC><<<p.grid, THREADS, L.total, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <typename T>
+int launch_t(const PagedParams& p, cudaStream_t stream) {
+    switch (p.chunk_rows) {
+        case 1: return launch_rc<T, 1>(p, stream);
+        case 2: return launch_rc<T, 2>(p, stream);
+        case 4: return launch_rc<T, 4>(p, stream);
+        case 8: return launch_rc<T, 8>(p, stream);
+        case 16: return launch_rc<T, 16>(p, stream);
+        default: return -1;
+    }
+}
+
+}  // namespace paged
+
+int paged_simt_rows(int64_t rows) {
+    for (int r = 1; r < paged::MAX_RC; r *= 2)
+        if (rows <= r) return r;
+    return paged::MAX_RC;
+}
+
+int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
+    if (p.grid < 2) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)((p.chunk_rows + 15) / 16));
+    cfg.blockDim = dim3(paged::C_WARPS * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel, p) == cudaSuccess ? 0 : -1;
+}
+
+int launch_paged_simt(const PagedParams& p, cudaStream_t stream) {
+    const int rc = p.bf16 ? paged::launch_t<__nv_bfloat16>(p, stream) : paged::launch_t<float>(p, stream);
+    return rc == 0 ? launch_paged_combine(p, stream) : rc;
+}
+
+}  // namespace diffattn

@@ -1,0 +1,125 @@
+// paged.h -- internal interface of the operators around a paged key/value cache:
+// norm and rotation of queries and keys, appending to the cache, and attention over
+// it.  Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "diffattn.h"
+
+namespace diffattn {
+
+// What a stream of head rows is for.
+enum : int {
+    kRowsDense = 0,     // norm and rotation, dense rows out
+    kRowsPaged = 1,     // norm and rotation into the paged cache
+    kRowsCopy = 2,      // values: copied into the paged cache
+};
+
+// One tensor of head rows that the rotation kernel walks: x [B, heads, T, width]
+// by strides; y by strides (dense: [0] = B, [1] = head, [2] = T; paged: [0] = page,
+// [1] = head, [2] = slot in the page).
+struct RowStream {
+    const void* x;
+    void* y;
+    int64_t sx[3], sy[3];
+    int heads, width, kind;
+    const float* weight;        // [D] or [heads, D], nullptr = 1
+    int64_t w_stride;           // 0 or D
+    // backward only: gradient of y (strides sg), and where y above takes dx
+    const void* g;
+    int64_t sg[3];
+    int grad_slot;              // 0: q weight, 1: k weight
+};
+
+struct RotaryParams {
+    RowStream s[4];
+    int n;                      // streams
+    int B, T, D, R;             // R rotated elements of each row (0: none)
+    int bf16, interleaved, norm;
+    float eps;
+    const float* cos;           // [table_rows, R / 2]
+    const float* sin;
+    int64_t table_rows;
+    const void* pos;            // nullptr: the slot (paged) or t
+    int pos64;
+    int64_t pos_stride[2];      // B, T
+    // the paged cache
+    const int32_t* lengths;     // [B] tokens before the call
+    const int32_t* new_lengths; // [B] or nullptr (T each)
+    const int32_t* table;       // [B, max_pages]
+    int64_t table_stride;
+    int64_t max_pages, num_pages, page;
+    uint32_t* status;
+    int fast;                   // 16-byte rows: the vector kernel
+    int heads_per_block;
+    int head_blocks;            // of all streams
+    // backward
+    int chunks;                 // blocks along the tokens
+    float* partial;             // [head_blocks][chunks][D]
+    float* dw[2];               // q and k weight gradients, nullptr: not wanted
+    int64_t dw_stride[2];       // 0: [D], summed over heads; D: [heads, D]
+};
+
+int launch_rotary(const RotaryParams& p, cudaStream_t stream);
+int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream);
+// Heads a block walks, and the blocks along tokens and heads, for p's sizes.
+void plan_rotary(RotaryParams* p, int num_sms);
+void plan_rotary_bwd(RotaryParams* p);
+
+// Attention over the paged cache.
+struct PagedParams {
+    int B, H, Hk, group, Tq, D, Dv;
+    int bf16;
+    int k_shared;
+    int page;                   // slots of a page
+    int64_t max_pages, num_pages;
+    const void* q1; const void* q2;
+    const void* k1; const void* k2; const void* v;
+    void* out;
+    int64_t s_q1[3], s_q2[3], s_o[3];
+    int64_t s_k1[3], s_k2[3], s_v[3];   // page, head, slot
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lengths;
+    const int32_t* q_lengths;   // nullptr: Tq each
+    const uint8_t* mask;        // tree: [B, Tq, Tq] bytes, nullptr: causal
+    int64_t mask_stride[2];
+    float scale_log2, lambda;
+    const float* lambda_dev;
+    int norm;
+    float norm_eps;
+    const float* norm_weight;
+    const float* norm_bias;
+    float out_scale;
+    uint32_t* status;
+    // The query rows of a key/value head: its heads' head_rows rows each, Tq or more
+    // (then the rest is padding), cut into row_chunks units of chunk_rows.
+    int head_rows;
+    int row_chunks;
+    int chunk_rows;
+    int vec16;                  // rows of the caches and queries are 16-byte aligned
+    int grid;                   // blocks of the first pass
+    float* part;                // [2 * grid][chunk_rows][4 + 2 Dv]
+    int64_t* cum;               // [B + 1] tiles before each sequence
+};
+
+int launch_paged_simt(const PagedParams& p, cudaStream_t stream);
+// Rows of a unit of the CUDA-core kernel, for `rows` query rows a key/value head.
+int paged_simt_rows(int64_t rows);
+constexpr int kSimtBlocksPerSm = 3;
+// Merges the partial results of the units that several blocks share.
+int launch_paged_combine(const PagedParams& p, cudaStream_t stream);
+
+// Checks an output epilogue and fills in what a NULL one means (api.cu).
+int check_epilogue(const diffattn_epilogue* epi, diffattn_epilogue* e);
+// The C-ABI layer's view of the current device (api.cu).
+int device_info(uint32_t** status, int* num_sms);
+// 4-D bf16 tensor map with 128-byte swizzling: dims {inner, rows, heads, outer},
+// element strides {outer, heads, rows} as in the descriptors.
+int encode_map_4d(CUtensorMap* m, const void* base, const int64_t dims[4], const int64_t s[3],
+                  uint32_t box_inner, uint32_t box_rows);
+
+}  // namespace diffattn

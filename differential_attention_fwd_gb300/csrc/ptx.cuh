@@ -12,6 +12,7 @@ namespace diffattn {
 // Status bits a kernel ORs into the library's device status word.
 enum : uint32_t {
     kStatusTimeout = 1u,   // a bounded wait ran out
+    kStatusIndex = 2u,     // a position, length or page outside its table (nothing was read or written there)
 };
 
 // Limits of every spin-wait: a wait gives up after this many nanoseconds of

@@ -52,6 +52,7 @@ typedef struct CUstream_st *diffattn_stream_t;
 #define DIFFATTN_ERR_UNSUPPORTED -2  /* a valid request this build has no kernel for */
 #define DIFFATTN_ERR_CUDA        -3  /* a CUDA runtime or driver call failed (incl. launch) */
 #define DIFFATTN_ERR_TIMEOUT     -4  /* a kernel's bounded wait ran out (see get_device_error) */
+#define DIFFATTN_ERR_INDEX       -5  /* a kernel met a position, length or page outside its table (see get_device_error) */
 
 /* Element types of Q1, K1, Q2, K2, V and O (all six share one type). */
 #define DIFFATTN_BF16 0   /* bfloat16 storage, fp32 accumulation, bf16 output */
@@ -458,6 +459,181 @@ int diffattn_decode_noalloc(const diffattn_kv_desc *desc, const void *q1,
                             diffattn_stream_t stream);
 
 /*
+ * Queries and keys before the operation: the norm of each head row and the
+ * position rotation.  For a row x of width D at position p, with
+ * r = (mean(x^2) + eps)^-1/2 and weights w (r = w = 1 without the norm),
+ *
+ *     n = x r w,   y_a = n_a cos - n_b sin,   y_b = n_b cos + n_a sin
+ *
+ * for the pairs (a, b) = (i, i + R/2), i < R/2, or (2i, 2i + 1) when
+ * interleaved, of the row's first R elements; the others are n.  cos and sin are
+ * entries i of row p of the tables.  float32 arithmetic, one rounding of y.
+ *
+ * B, T, D: batch, tokens, row width (1 .. 128).  H, Hk: heads of Q1, Q2 and of
+ * K1, K2.  dtype: of the rows.  rotary_dim: R, even, 0 .. D (0: no rotation, cos
+ * and sin may be NULL).  norm: DIFFATTN_NORM_NONE or DIFFATTN_NORM_RMS, eps > 0.
+ * q_weight_stride, k_weight_stride: 0 (one weight row [D] for all heads) or D (a
+ * row for each head, [H, D] or [Hk, D]).  table_rows: rows of cos and sin
+ * ([table_rows, R/2] float32, dense).  pos64: positions are int64 (else int32);
+ * pos_stride: their element strides along B and T.  *_stride: element strides of
+ * B, heads and T of the inputs, *_grad_stride of the gradients of the outputs
+ * (the backward only); innermost stride 1; >= 0.
+ */
+typedef struct {
+    int64_t B, T, D, H, Hk;
+    int32_t dtype;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t norm;
+    float eps;
+    int32_t pos64;
+    int64_t table_rows;
+    int64_t pos_stride[2];
+    int64_t q_weight_stride, k_weight_stride;
+    int64_t q1_stride[3], k1_stride[3], q2_stride[3], k2_stride[3];
+    int64_t q1_grad_stride[3], k1_grad_stride[3], q2_grad_stride[3], k2_grad_stride[3];
+} diffattn_rotary_desc;
+
+/*
+ * diffattn_rotary -- norm and rotation of Q1, K1, Q2 and K2 in one launch.
+ *
+ * q1, k1, q2, k2: the inputs; NULL for one that is not wanted (then its output is
+ * NULL too), at least one given.  q_weight (Q1 and Q2), k_weight (K1 and K2):
+ * float32 norm weights, NULL = 1.  cos, sin: the tables.  positions: of each token
+ * by pos_stride; NULL = 0 .. T-1 in every sequence.  q1_out .. k2_out: dense
+ * [B, heads, T, D]; they must not overlap the inputs.
+ * A position outside the tables gives a row of NaN and is recorded
+ * (DIFFATTN_ERR_INDEX from diffattn_get_device_error); nothing outside the tables
+ * is read.
+ * Rows that start on 16-byte boundaries with D 32, 64 or 128 (float32: 16 too) and R
+ * a multiple of 16 (float32: 8) run on the vector kernel, others a warp a row.
+ * Errors: DIFFATTN_ERR_INVALID (sizes, strides, dtype, norm, eps, an odd or large
+ * rotary_dim, missing tables, an output without its input or the reverse);
+ * DIFFATTN_ERR_UNSUPPORTED (beyond 65535 heads in all or 2^31 tokens);
+ * DIFFATTN_ERR_CUDA.
+ */
+int diffattn_rotary(const diffattn_rotary_desc *desc, const void *q1, const void *k1,
+                    const void *q2, const void *k2, const float *q_weight,
+                    const float *k_weight, const float *cos, const float *sin,
+                    const void *positions, void *q1_out, void *k1_out, void *q2_out,
+                    void *k2_out, diffattn_stream_t stream);
+
+/*
+ * diffattn_rotary_bwd -- gradients of diffattn_rotary.  dq1_out .. dk2_out:
+ * gradients of the outputs (inputs' dtype, *_grad_stride), NULL for tensors that
+ * are left out; dq1 .. dk2: dense gradients of the inputs, overwritten;
+ * dq_weight, dk_weight: float32, [D] or [heads, D] as the weights, overwritten,
+ * NULL when not wanted (they need the norm).  With u the rotation of dy by the
+ * negative angles:
+ *
+ *     dw = sum over rows of u x r      dx = r (w u - x r^2 mean(w u x))
+ *
+ * workspace: at least diffattn_rotary_bwd_workspace_bytes(desc) bytes, 16-byte
+ * aligned, no initialisation needed.  No atomics: the result is reproducible bit
+ * for bit.  Other arguments and errors as diffattn_rotary.
+ */
+int diffattn_rotary_bwd(const diffattn_rotary_desc *desc, const void *q1, const void *k1,
+                        const void *q2, const void *k2, const float *q_weight,
+                        const float *k_weight, const float *cos, const float *sin,
+                        const void *positions, const void *dq1_out, const void *dk1_out,
+                        const void *dq2_out, const void *dk2_out, void *dq1, void *dk1,
+                        void *dq2, void *dk2, float *dq_weight, float *dk_weight,
+                        void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
+
+/* Bytes of workspace diffattn_rotary_bwd needs, 0 for an invalid descriptor. */
+size_t diffattn_rotary_bwd_workspace_bytes(const diffattn_rotary_desc *desc);
+
+/*
+ * A paged key/value cache.  K1, K2: [num_pages, Hk, page_size, D], V:
+ * [num_pages, Hk, page_size, Dv], by element strides ([0] = page, [1] = head, [2] =
+ * slot; innermost 1).  The cached token i of sequence b is in slot i % page_size of
+ * page block_table[b][i / page_size] (int32, [B, max_pages], row stride
+ * block_table_stride); entries past a sequence's tokens are not read.  The two
+ * branches may share one key tensor (the same pointer and strides as K1 and K2).
+ */
+typedef struct {
+    int64_t num_pages, page_size, max_pages, block_table_stride;
+    int64_t k1_stride[3], k2_stride[3], v_stride[3];
+} diffattn_pages;
+
+/*
+ * diffattn_paged_append -- new keys and values into the paged cache, the keys
+ * normed and rotated on the way as diffattn_rotary does.
+ *
+ * desc: B, T (new tokens a sequence, at most), D, Hk, dtype, rotary_dim,
+ * interleaved, norm, eps, pos64, table_rows, pos_stride, k_weight_stride,
+ * k1_stride, k2_stride as in diffattn_rotary; H, q strides and gradient strides are
+ * not read.  Dv, v_stride: width (0 = 2 D, at most 256) and strides of the new
+ * values [B, Hk, T, Dv].  k1, k2, v: the new rows; k2 and k2_cache NULL (or the
+ * same as k1 and k1_cache) when the branches share their keys.
+ * lengths: [B] int32, tokens cached before the call: token t of sequence b goes to
+ * cache index lengths[b] + t.  new_lengths: [B] int32 or NULL: only the first
+ * new_lengths[b] tokens of a sequence are written.  positions: for the rotation,
+ * NULL = the cache index (a tree of drafted tokens passes its depths).
+ * A token whose index, page or position is out of range is not written, and is
+ * recorded (DIFFATTN_ERR_INDEX).  Two tokens of one call must not have one slot.
+ * One launch.  Errors as diffattn_rotary, plus DIFFATTN_ERR_INVALID for bad pages.
+ */
+int diffattn_paged_append(const diffattn_rotary_desc *desc, int64_t Dv,
+                          const int64_t v_stride[3], const diffattn_pages *pages,
+                          const void *k1, const void *k2, const void *v,
+                          const float *k_weight, const float *cos, const float *sin,
+                          const void *positions, const int32_t *lengths,
+                          const int32_t *new_lengths, const int32_t *block_table,
+                          void *k1_cache, void *k2_cache, void *v_cache,
+                          diffattn_stream_t stream);
+
+/*
+ * Attention of new tokens over the paged cache.  Q1, Q2: [B, H, Tq, D]; O: [B, H,
+ * Tq, Dv] (Dv 0 = 2 D, at most 256); H heads of queries over H / kv_group of keys
+ * and values.  Tq 1 .. 1024.  Strides as in diffattn_desc.  mask_stride: element
+ * strides of the tree mask along B and its rows.
+ */
+typedef struct {
+    int64_t B, H, Tq, D, Dv;
+    int32_t dtype;
+    int32_t kv_group;
+    int64_t q1_stride[3], q2_stride[3], o_stride[3];
+    int64_t mask_stride[2];
+} diffattn_paged_desc;
+
+/* Bytes of workspace diffattn_paged_decode needs, 0 for an invalid descriptor. */
+size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc *desc, const diffattn_pages *pages);
+
+/*
+ * diffattn_paged_decode -- O = (softmax(Q1 K1^T / sqrt(D) + M) - lambda
+ * softmax(Q2 K2^T / sqrt(D) + M)) V of the new tokens of each sequence over its
+ * cached ones and each other, then the optional epilogue `epi`.
+ *
+ * lengths: [B] int32, tokens cached before the new ones, whose keys and values are
+ * in the cache behind them (cache index lengths[b] + i).  q_lengths: [B] int32 or
+ * NULL (Tq each): sequence b has q_lengths[b] new tokens; rows of O past them are
+ * left as they were, and a sequence with none is not read.
+ * tree_mask: NULL: new token i sees every cached token and new tokens 0 .. i.
+ * Else device bytes [B, Tq, Tq] by mask_stride: new token i sees new token j where
+ * the byte is not zero (and every cached token); Tq <= 64.  What a row does not see
+ * has no influence on it, NaN and infinities included; a row that sees nothing
+ * gives zeros (before the epilogue).
+ * A length, or a page that a sequence needs, outside the table gives rows of NaN
+ * for that sequence and is recorded (DIFFATTN_ERR_INDEX); nothing outside the
+ * cache is read.
+ * workspace: at least diffattn_paged_workspace_bytes bytes, 16-byte aligned, no
+ * initialisation needed; calls that may run at the same time use different ones.
+ * Two launches; no atomics on results.  lambda, lambda_dev, epi as diffattn_decode.
+ * Errors: DIFFATTN_ERR_INVALID (NULL pointers, sizes, strides, dtype, kv_group,
+ * non-finite lambda, bad epilogue or pages, a tree with Tq > 64, a missing, small or
+ * misaligned workspace); DIFFATTN_ERR_UNSUPPORTED (Tq > 1024, sizes beyond the
+ * int32 index range); DIFFATTN_ERR_CUDA.
+ */
+int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages *pages,
+                          const void *q1, const void *k1_cache, const void *q2,
+                          const void *k2_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *lengths,
+                          const int32_t *q_lengths, const uint8_t *tree_mask, float lambda,
+                          const float *lambda_dev, const diffattn_epilogue *epi, void *out,
+                          void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
+
+/*
  * diffattn_select_kernel -- which kernel diffattn_fwd would launch for this
  * descriptor and these pointers (DIFFATTN_KERNEL_*), or a negative error code
  * if the arguments are invalid.  Host only; touches no GPU state.
@@ -472,8 +648,9 @@ int diffattn_select_kernel(const diffattn_desc *desc, const void *q1,
  * since the previous call (DIFFATTN_ERR_TIMEOUT), and clear that record.
  * Every wait inside the kernels has an iteration and time limit; on expiry
  * the kernel records the failure, stops issuing work, releases what it holds
- * and returns, leaving the CUDA context usable.  Returns DIFFATTN_OK when no
- * wait ran out, DIFFATTN_ERR_CUDA if the synchronisation itself fails.
+ * and returns, leaving the CUDA context usable.  Likewise DIFFATTN_ERR_INDEX when
+ * a kernel met a position, length or page outside its table.  Returns DIFFATTN_OK
+ * when there was neither, DIFFATTN_ERR_CUDA if the synchronisation itself fails.
  */
 int diffattn_get_device_error(diffattn_stream_t stream);
 
