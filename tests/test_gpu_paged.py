@@ -52,7 +52,7 @@ class Problem:
             for cache, rows in zip(caches, (self.k1[b], self.k2[b], self.v[b])):
                 full = torch.full((Hk, n * page, rows.shape[-1]), float("nan"), dtype=dt)
                 full[:, :totals[b]] = rows
-                cache[ids] = full.reshape(Hk, n, page, -1).transpose(0, 1)
+                cache[ids] = full.reshape(Hk, n, page, rows.shape[-1]).transpose(0, 1)
         if shared:
             self.k2 = self.k1
         self.caches = [c.cuda() for c in caches]
