@@ -160,6 +160,33 @@ void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, P
     n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, dv);
 }
 
+// Whether the tensor-core kernels take the shape and the cache's layout: bf16, value
+// width 128, Q/K width 64 or 128, pages of a multiple of 16 slots, and strides (with the
+// bases, checked at the call) that TMA takes.
+bool tc_shape(const diffattn_paged_desc& d, const diffattn_pages& g) {
+    if (d.dtype != DIFFATTN_BF16 || (d.Dv == 0 ? 2 * d.D : d.Dv) != 128 || (d.D != 64 && d.D != 128) ||
+        g.page_size % 16 != 0)
+        return false;
+    for (const int64_t* s : {g.k1_stride, g.k2_stride, g.v_stride})
+        for (int i = 0; i < 3; ++i)
+            if (s[i] % 8 != 0 || s[i] <= 0 || s[i] >= (int64_t(1) << 38)) return false;
+    return true;
+}
+
+// The plan of the tensor-core kernel for up to 16 rows: a block an SM.
+void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, PagedPlan* n) {
+    const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
+    const int64_t rows = group * d.Tq;
+    n->head_rows = (int)d.Tq;
+    n->row_chunks = (int)((rows + kMmaRows - 1) / kMmaRows);
+    n->chunk_rows = (int)((rows + n->row_chunks - 1) / n->row_chunks);
+    n->tile = kMmaTile;
+    n->grid = sms;
+    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
+    if (tiles < n->grid) n->grid = (int)tiles;
+    n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);
+}
+
 int device_sms() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -286,8 +313,14 @@ int diffattn_paged_append(const diffattn_rotary_desc* desc, int64_t Dv, const in
 size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc* desc, const diffattn_pages* pages) {
     if (check_paged(desc, pages) != DIFFATTN_OK) return 0;
     PagedPlan n;
-    plan_simt(*desc, *pages, device_sms(), &n);
-    return n.bytes;
+    const int sms = device_sms();
+    plan_simt(*desc, *pages, sms, &n);
+    size_t bytes = n.bytes;
+    if (tc_shape(*desc, *pages)) {
+        plan_mma(*desc, *pages, sms, &n);
+        if (n.bytes > bytes) bytes = n.bytes;
+    }
+    return bytes;
 }
 
 int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages* pages, const void* q1,
@@ -313,7 +346,9 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
     PagedPlan n;
-    plan_simt(d, *pages, sms, &n);
+    const bool tc = tc_shape(d, *pages) && aligned16(k1_cache) && aligned16(k2_cache) && aligned16(v_cache);
+    if (tc) plan_mma(d, *pages, sms, &n);
+    else plan_simt(d, *pages, sms, &n);
     if (workspace_bytes < n.bytes) return DIFFATTN_ERR_INVALID;
     p.B = (int)d.B;
     p.H = (int)d.H;
@@ -356,12 +391,26 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.out_scale = e.out_scale;
     p.vec16 = p.D * es % 16 == 0 && p.Dv * es % 16 == 0 && rows16(p.k1, p.s_k1, es) && rows16(p.k2, p.s_k2, es) &&
               rows16(p.v, p.s_v, es);
+    p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
     p.cum = static_cast<int64_t*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (size_t)((d.B + 1) * 8 + 15) / 16 * 16);
     p.head_rows = n.head_rows;
     p.chunk_rows = n.chunk_rows;
     p.row_chunks = n.row_chunks;
     p.grid = n.grid;
+    if (tc) {
+        // boxes that stay inside one page and divide the tile
+        int box = kMmaTile;
+        while (p.page % box != 0) box /= 2;
+        CUtensorMap maps[3];
+        const int64_t kd[4] = {p.D, p.page, p.Hk, p.num_pages}, vd[4] = {p.Dv, p.page, p.Hk, p.num_pages};
+        if (encode_map_4d(&maps[0], p.k1, kd, p.s_k1, 64, box) != DIFFATTN_OK ||
+            encode_map_4d(&maps[1], p.k2, kd, p.s_k2, 64, box) != DIFFATTN_OK ||
+            encode_map_4d(&maps[2], p.v, vd, p.s_v, 64, box) != DIFFATTN_OK)
+            return DIFFATTN_ERR_CUDA;
+        return launch_paged_mma(maps, p, box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
+                                                                                           : DIFFATTN_ERR_CUDA;
+    }
     return launch_paged_simt(p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 

@@ -100,7 +100,8 @@ struct PagedParams {
     int head_rows;
     int row_chunks;
     int chunk_rows;
-    int vec16;                  // rows of the caches and queries are 16-byte aligned
+    int vec16;                  // rows of the caches are 16-byte aligned,
+    int q16;                    // and of the queries
     int grid;                   // blocks of the first pass
     float* part;                // [2 * grid][chunk_rows][4 + 2 Dv]
     int64_t* cum;               // [B + 1] tiles before each sequence
@@ -110,6 +111,11 @@ int launch_paged_simt(const PagedParams& p, cudaStream_t stream);
 // Rows of a unit of the CUDA-core kernel, for `rows` query rows a key/value head.
 int paged_simt_rows(int64_t rows);
 constexpr int kSimtBlocksPerSm = 3;
+// The tensor-core kernel of up to 16 rows a unit: maps of K1, K2 and V with boxes of
+// 64 columns x box_rows slots.
+constexpr int kMmaRows = 16;
+constexpr int kMmaTile = 128;
+int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream);
 // Merges the partial results of the units that several blocks share.
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream);
 
