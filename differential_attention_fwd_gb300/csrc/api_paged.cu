@@ -187,6 +187,34 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
     n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);
 }
 
+// The tcgen05 kernel's plan, for more rows than that (and for one more reason: the
+// 16-row kernel would read the cache once for each 16 of them): whole heads in units of
+// up to 128 rows, each head's tokens padded to a multiple of 8.
+bool wants_tc(const diffattn_paged_desc& d) {
+    const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
+    return group * d.Tq > kMmaRows;
+}
+void plan_tc(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, PagedPlan* n) {
+    const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
+    if (d.Tq <= kTcRows) {
+        n->head_rows = (int)((d.Tq + 7) / 8 * 8);
+        int64_t heads = kTcRows / n->head_rows;
+        if (heads > group) heads = group;
+        n->row_chunks = (int)((group + heads - 1) / heads);
+        heads = (group + n->row_chunks - 1) / n->row_chunks;        // evenly filled
+        n->chunk_rows = (int)heads * n->head_rows;
+    } else {
+        n->head_rows = (int)((d.Tq + kTcRows - 1) / kTcRows * kTcRows);
+        n->chunk_rows = kTcRows;
+        n->row_chunks = (int)(group * (n->head_rows / kTcRows));
+    }
+    n->tile = kTcTile;
+    n->grid = sms;
+    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
+    if (tiles < n->grid) n->grid = (int)tiles;
+    n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);
+}
+
 int device_sms() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -319,6 +347,10 @@ size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc* desc, const dif
     if (tc_shape(*desc, *pages)) {
         plan_mma(*desc, *pages, sms, &n);
         if (n.bytes > bytes) bytes = n.bytes;
+        if (wants_tc(*desc)) {
+            plan_tc(*desc, *pages, sms, &n);
+            if (n.bytes > bytes) bytes = n.bytes;
+        }
     }
     return bytes;
 }
@@ -347,7 +379,13 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     if (rc != DIFFATTN_OK) return rc;
     PagedPlan n;
     const bool tc = tc_shape(d, *pages) && aligned16(k1_cache) && aligned16(k2_cache) && aligned16(v_cache);
-    if (tc) plan_mma(d, *pages, sms, &n);
+    // the queries go through TMA too, from 16-byte aligned rows
+    bool tcgen = tc && wants_tc(d) && aligned16(q1) && aligned16(q2);
+    for (const int64_t* s : {d.q1_stride, d.q2_stride})
+        for (int i = 0; i < 3; ++i)
+            if ((i == 0 ? d.B : i == 1 ? d.H : d.Tq) > 1 && (s[i] <= 0 || s[i] % 8 != 0)) tcgen = false;
+    if (tcgen) plan_tc(d, *pages, sms, &n);
+    else if (tc) plan_mma(d, *pages, sms, &n);
     else plan_simt(d, *pages, sms, &n);
     if (workspace_bytes < n.bytes) return DIFFATTN_ERR_INVALID;
     p.B = (int)d.B;
@@ -400,14 +438,23 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.grid = n.grid;
     if (tc) {
         // boxes that stay inside one page and divide the tile
-        int box = kMmaTile;
+        int box = n.tile;
         while (p.page % box != 0) box /= 2;
-        CUtensorMap maps[3];
+        CUtensorMap maps[5];
         const int64_t kd[4] = {p.D, p.page, p.Hk, p.num_pages}, vd[4] = {p.Dv, p.page, p.Hk, p.num_pages};
         if (encode_map_4d(&maps[0], p.k1, kd, p.s_k1, 64, box) != DIFFATTN_OK ||
             encode_map_4d(&maps[1], p.k2, kd, p.s_k2, 64, box) != DIFFATTN_OK ||
             encode_map_4d(&maps[2], p.v, vd, p.s_v, 64, box) != DIFFATTN_OK)
             return DIFFATTN_ERR_CUDA;
+        if (tcgen) {
+            const int q_box = p.head_rows < kTcRows ? p.head_rows : kTcRows;
+            const int64_t qd[4] = {p.D, p.Tq, p.H, p.B};
+            if (encode_map_4d(&maps[3], q1, qd, p.s_q1, 64, q_box) != DIFFATTN_OK ||
+                encode_map_4d(&maps[4], q2, qd, p.s_q2, 64, q_box) != DIFFATTN_OK)
+                return DIFFATTN_ERR_CUDA;
+            return launch_paged_tc(maps, p, box, q_box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
+                                                                                                     : DIFFATTN_ERR_CUDA;
+        }
         return launch_paged_mma(maps, p, box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
                                                                                            : DIFFATTN_ERR_CUDA;
     }

@@ -116,6 +116,11 @@ constexpr int kSimtBlocksPerSm = 3;
 constexpr int kMmaRows = 16;
 constexpr int kMmaTile = 128;
 int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream);
+// The tcgen05 kernel of up to 128 rows a unit: maps of K1, K2, V (boxes of 64 columns x
+// box_rows slots), Q1 and Q2 (boxes of 64 columns x q_box tokens).
+constexpr int kTcRows = 128;
+constexpr int kTcTile = 64;
+int launch_paged_tc(const CUtensorMap* maps, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream);
 // Merges the partial results of the units that several blocks share.
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream);
 

@@ -1,0 +1,589 @@
+// paged_tc.cu -- differential attention over a paged cache for more than 16 query rows a
+// key/value head (trees of drafted tokens, chunks of a prefill): bf16, value width 128,
+// Q/K width 64 or 128, pages of a multiple of 16 slots, on tcgen05.
+//
+// A unit is up to 128 query rows of the heads that share a key/value head: each head's
+// new tokens, padded to a multiple of 8 rows, one head after another in the MMA's M, so
+// that a tree of 61 tokens of two heads fills one tile and its cache is read once.  Per
+// 64 keys: S_b = Q_b K_b^T (M = 128, N = 64) into one of two TMEM buffers a branch, the
+// weights by one warpgroup a branch (a row a thread, lazily moved maximum), written over
+// S_b as bf16, and O_b += P_b V.  The work is cut by the lengths on the device (see
+// paged_plan.cuh), and every role walks the block's segments on its own.
+//
+// What bounds it at 128 full rows: a 64-key tile takes about 1,000 cycles of tensor-core
+// work, 1,000 of the exponential unit and 1,400 of an SM's share of the HBM rate, which
+// the ring's 160 KB in flight cover.
+//
+// Warp roles (384 threads):
+//   warps 0-3, 4-7   weights and results of branch 1, 2 (TMEM lanes 0-127)
+//   warp 8           TMA producer: a lane a page of the tile
+//   warps 9, 10      MMA issue for branch 1, 2; warp 9 allocates TMEM
+//   warp 11          makes the values of tiles that reach into the new tokens safe
+//
+// A product with a weight of zero is not zero where the value is NaN or infinite, and the
+// cache behind a sequence's end, or a drafted token that a row does not see, may hold
+// either.  So in those tiles (the last one or two of a sequence) warp 11 puts zeros for
+// rows past the end, and for single values that are not finite it puts zeros and marks
+// the key; the results' warps then add such a value to the rows that see its key.
+#include "paged_plan.cuh"
+#include "kernels.h"
+#include "pdl.cuh"
+#include "tile_softmax.cuh"
+
+namespace diffattn {
+namespace ptc {
+
+using tc::tile_exp2;
+using tc::tile_row_max;
+
+constexpr int BM = 128;
+constexpr int KT = 64;
+constexpr int DV = 128;
+constexpr int THREADS = 384;
+// launched at 168 registers a thread: 256 x 200 + 128 x 104 = 384 x 168
+constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
+static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "register split");
+constexpr uint32_t Q_PANEL = BM * 128;          // 16 KB
+constexpr uint32_t K_PANEL = KT * 128;          // 8 KB: 64 keys x 64 columns
+constexpr uint32_t V_BYTES = 2 * K_PANEL;
+constexpr int VST = 5;                          // value stages
+constexpr int KST_MAX = 5;
+constexpr int SEGS = 8;                         // segments whose flags are kept apart
+constexpr int FLAGS = 18;                       // tiles that reach into the new tokens: (1024 + 63) / 64 + 1
+// A finite stand-in for the maximum of a row that has seen nothing.
+constexpr float NOTHING = -1e30f;
+
+template <int HD, bool KS>
+struct Cfg {
+    static constexpr int KP = HD / 64;
+    static constexpr int NK = KS ? 1 : 2;
+    static constexpr uint32_t Q_BYTES = KP * Q_PANEL;               // a branch
+    static constexpr uint32_t K_BYTES = KP * K_PANEL;               // a branch's key tile
+    static constexpr uint32_t K_STAGE = NK * K_BYTES;               // 8, 16 or 32 KB
+    static constexpr int KST = HD == 128 && !KS ? 2 : KST_MAX;
+    static constexpr uint32_t OFF_K = 2 * Q_BYTES;
+    static constexpr uint32_t OFF_V = OFF_K + KST * K_STAGE;
+    static constexpr uint32_t OFF_BAR = OFF_V + VST * V_BYTES;
+};
+
+enum : int {
+    B_Q_FULL, B_Q_EMPTY,
+    B_K_FULL, B_K_EMPTY = B_K_FULL + KST_MAX,
+    B_V_FULL = B_K_EMPTY + KST_MAX, B_V_EMPTY = B_V_FULL + VST, B_V_SAFE = B_V_EMPTY + VST,
+    B_S_FULL = B_V_SAFE + VST,                  // [branch][buffer]
+    B_P_FULL = B_S_FULL + 4,                    // [branch][buffer]
+    B_PV_DONE = B_P_FULL + 4,                   // [branch]
+    B_O_FULL = B_PV_DONE + 2, B_O_EMPTY,
+    B_ROWS_OUT, B_ROWS_READ,                    // a whole unit's rows written, and read back
+    B_FINAL,                                    // [branch]
+    NUM_BARS = B_FINAL + 2
+};
+constexpr uint32_t REL_TMEM = NUM_BARS * 8;
+constexpr uint32_t REL_ABORT = REL_TMEM + 4;
+constexpr uint32_t REL_BAD = REL_ABORT + 4;                         // uint32 [SEGS]
+constexpr uint32_t REL_FLAGS = (REL_BAD + SEGS * 4 + 7) & ~7u;      // uint64 [SEGS][FLAGS]
+constexpr uint32_t REL_ANY = REL_FLAGS + SEGS * FLAGS * 8;          // uint32 [SEGS]
+constexpr uint32_t REL_END = REL_ANY + SEGS * 4;
+template <int HD, bool KS>
+constexpr uint32_t smem_bytes() { return Cfg<HD, KS>::OFF_BAR + REL_END + 1024; }
+static_assert(smem_bytes<128, true>() <= 232448 - 256 && smem_bytes<64, false>() <= 232448 - 256 &&
+              smem_bytes<128, false>() <= 232448 - 256, "shared memory");
+
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_O = 256;
+constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, KT, 0, 0);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, DV, 0, 1);
+__device__ __forceinline__ uint32_t tm_s(int br, int buf) { return br * 128 + buf * 64; }
+
+__device__ __forceinline__ bool bf16_finite(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
+
+// Bits of the 64 keys from k0 on that a row sees (bit d of `tree`: new token d).
+__device__ __forceinline__ uint64_t tile_mask(const PagedParams& p, const PagedSeq& s, int k0, int q, uint64_t tree) {
+    auto low = [](int64_t n) -> uint64_t { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
+    const int64_t off = s.before - k0;          // keys of the tile before the new tokens, < 64
+    uint64_t m;
+    if (p.mask) m = off <= 0 ? (off <= -64 ? 0 : tree >> -off) : (tree << off) | low(off);
+    else m = low(off + q + 1);
+    return m & low((int64_t)s.total - k0);
+}
+
+template <int HD, bool KS>
+__global__ void __launch_bounds__(THREADS, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
+                const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
+                const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int box_rows, const int q_box) {
+    using C = Cfg<HD, KS>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t scan[THREADS / 32 + 1];
+    __shared__ PagedStart start_s;
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + REL_TMEM);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_BAR + REL_ABORT);
+    volatile uint32_t* bad_seg = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_BAR + REL_BAD);
+    volatile uint64_t* flags = reinterpret_cast<volatile uint64_t*>(smem + C::OFF_BAR + REL_FLAGS);
+    volatile uint32_t* any_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_BAR + REL_ANY);
+    const uint32_t warp = warp_id();
+    const uint32_t lane = threadIdx.x & 31;
+    const AbortState ab{abort_flag, p.status};
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < KST_MAX; ++i) mbar_init(&bars[B_K_EMPTY + i], 2);
+        for (int i = 0; i < VST; ++i) mbar_init(&bars[B_V_EMPTY + i], 3);   // both products, and warp 11
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[B_P_FULL + i], 4);
+        mbar_init(&bars[B_Q_EMPTY], 2);
+        mbar_init(&bars[B_O_FULL], 2);
+        mbar_init(&bars[B_O_EMPTY], 8);
+        mbar_init(&bars[B_ROWS_OUT], 8);
+        mbar_init(&bars[B_ROWS_READ], 8);
+        for (int i = 0; i < SEGS; ++i) bad_seg[i] = any_flag[i] = 0;
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    // rows of the query tiles that no head fills stay zero: their scores must be finite
+    for (uint32_t i = threadIdx.x; i < 2 * C::Q_BYTES / 16; i += THREADS)
+        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 9) {
+        tmem_alloc(tmem_ptr, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const PagedStart start = paged_start<THREADS>(p, KT, scan, &start_s);     // with its barriers
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_ptr;
+    const uint64_t lim = 200ull * 1000ull * 1000ull;
+    PagedCursor cur;
+
+    if (warp >= 8) {
+        regs_dec<REGS_OTHER>();
+        cur.begin(p, start, KT);
+        if (warp == 8) {
+            // ------------------------------------------------------------ producer
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q1);
+                tma_prefetch_desc(&tm_q2);
+                tma_prefetch_desc(&tm_k1);
+                tma_prefetch_desc(&tm_k2);
+                tma_prefetch_desc(&tm_v);
+            }
+            constexpr int Q_LEAD = (C::KST < VST ? C::KST : VST) - 1;   // tiles that may go ahead of their queries
+            const int boxes = KT / box_rows;
+            uint32_t kst = 0, kph = 1, vst = 0, vph = 1, nk = 0, nv = 0, nq = 0;
+            bool ok = true;
+            int seg = -1;                       // segments with tiles, as every role counts them
+            for (; ok && !cur.done(); cur.next(p, KT)) {
+                const int live = cur.live_tiles(p, KT);
+                if (cur.s.bad && lane == 0) atomicOr(p.status, kStatusIndex);
+                if (live == 0) continue;
+                ++seg;
+                if (lane == 0) bad_seg[seg % SEGS] = 0;
+                // the unit's queries: a box a head and panel, once the last segment's scores are done
+                bool have_q = false;
+                auto load_q = [&](bool wait) -> bool {
+                    if (nq > 0) {
+                        const uint32_t par = (nq - 1) & 1;
+                        if (wait) {
+                            if (!mbar_wait_warp(&bars[B_Q_EMPTY], par, ab)) return false;
+                        } else if (!__all_sync(0xffffffffu, mbar_test(&bars[B_Q_EMPTY], par))) {
+                            return true;
+                        }
+                    }
+                    have_q = true;
+                    ++nq;
+                    if (lane == 0) {
+                        const int row0 = cur.rc * p.chunk_rows;
+                        const int h0 = row0 / p.head_rows, q0 = row0 % p.head_rows;
+                        const int heads = min((p.chunk_rows + p.head_rows - 1) / p.head_rows, p.group - h0);
+                        mbar_arrive_expect_tx(&bars[B_Q_FULL], heads * C::KP * 2 * q_box * 128);
+                        for (int h = 0; h < heads; ++h)
+#pragma unroll
+                            for (int pn = 0; pn < C::KP; ++pn) {
+                                uint8_t* dst = smem + pn * Q_PANEL + h * p.head_rows * 128;
+                                tma_load_4d(dst, &tm_q1, &bars[B_Q_FULL], pn * 64, q0, cur.hk * p.group + h0 + h, cur.b);
+                                tma_load_4d(dst + C::Q_BYTES, &tm_q2, &bars[B_Q_FULL], pn * 64, q0,
+                                            cur.hk * p.group + h0 + h, cur.b);
+                            }
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto look = [&](int i) -> int {     // the page of this lane's box
+                    const int key = (cur.tile0 + i) * KT + (int)lane * box_rows;
+                    if (i >= live || (int)lane >= boxes || key >= cur.s.total) return -2;
+                    return paged_page(p, cur.b, key / p.page);
+                };
+                int page = look(0);
+                for (int i = 0; i < live; ++i) {
+                    const int now = page;
+                    page = look(i + 1);
+                    if (!have_q && !(ok = load_q(i >= Q_LEAD))) break;
+                    const int key = (cur.tile0 + i) * KT + (int)lane * box_rows;
+                    const int slot = key % p.page;
+                    const unsigned have = __ballot_sync(0xffffffffu, now >= 0);
+                    if (__any_sync(0xffffffffu, now == -1) && lane == 0) {
+                        bad_seg[seg % SEGS] = 1;
+                        atomicOr(p.status, kStatusIndex);
+                    }
+                    const uint32_t rows = __popc(have) * box_rows;
+                    if (!(ok = mbar_wait_warp(&bars[B_K_EMPTY + kst], kph, ab))) break;
+                    if (lane == 0) {
+                        if (rows) mbar_arrive_expect_tx(&bars[B_K_FULL + kst], rows * 128 * C::KP * C::NK);
+                        else mbar_arrive(&bars[B_K_FULL + kst]);
+                    }
+                    __syncwarp();
+                    if (now >= 0) {
+                        uint8_t* dst = smem + C::OFF_K + kst * C::K_STAGE + lane * box_rows * 128;
+#pragma unroll
+                        for (int pn = 0; pn < C::KP; ++pn) {
+                            tma_load_4d(dst + pn * K_PANEL, &tm_k1, &bars[B_K_FULL + kst], pn * 64, slot, cur.hk, now);
+                            if (!KS)
+                                tma_load_4d(dst + C::K_BYTES + pn * K_PANEL, &tm_k2, &bars[B_K_FULL + kst], pn * 64, slot,
+                                            cur.hk, now);
+                        }
+                    }
+                    ++nk;
+                    if (++kst == (uint32_t)C::KST) { kst = 0; kph ^= 1; }
+                    if (!(ok = mbar_wait_warp(&bars[B_V_EMPTY + vst], vph, ab))) break;
+                    if (lane == 0) {
+                        if (rows) mbar_arrive_expect_tx(&bars[B_V_FULL + vst], rows * 128 * 2);
+                        else mbar_arrive(&bars[B_V_FULL + vst]);
+                    }
+                    __syncwarp();
+                    if (now >= 0) {
+                        uint8_t* dst = smem + C::OFF_V + vst * V_BYTES + lane * box_rows * 128;
+                        tma_load_4d(dst, &tm_v, &bars[B_V_FULL + vst], 0, slot, cur.hk, now);
+                        tma_load_4d(dst + K_PANEL, &tm_v, &bars[B_V_FULL + vst], 64, slot, cur.hk, now);
+                    }
+                    ++nv;
+                    if (++vst == (uint32_t)VST) { vst = 0; vph ^= 1; }
+                }
+                if (ok && !have_q) ok = load_q(true);
+            }
+            // no copy may be in flight when the block ends
+            if (nq) mbar_wait_teardown(&bars[B_Q_FULL], (nq - 1) & 1, lim);
+            for (uint32_t t = nk > (uint32_t)C::KST ? nk - C::KST : 0; t < nk; ++t)
+                mbar_wait_teardown(&bars[B_K_FULL + t % C::KST], (t / C::KST) & 1, lim);
+            for (uint32_t t = nv > (uint32_t)VST ? nv - VST : 0; t < nv; ++t)
+                mbar_wait_teardown(&bars[B_V_FULL + t % VST], (t / VST) & 1, lim);
+            __syncwarp();
+        } else if (warp == 11) {
+            // ------------------------------------------- values that must not be multiplied
+            uint32_t vst = 0, vph = 0;
+            bool ok = true;
+            int seg = -1;
+            for (; ok && !cur.done(); cur.next(p, KT)) {
+                const int live = cur.live_tiles(p, KT);
+                if (live == 0) continue;
+                ++seg;
+                const int edge0 = (int)(cur.s.before / KT);         // the first tile with a new token
+                if (lane < FLAGS) flags[(seg % SEGS) * FLAGS + lane] = 0;
+                if (lane == 0) any_flag[seg % SEGS] = 0;
+                __syncwarp();
+                for (int i = 0; i < live; ++i) {
+                    const int tile = cur.tile0 + i;
+                    if (!(ok = mbar_wait_warp(&bars[B_V_FULL + vst], vph, ab))) break;
+                    if (tile >= edge0) {
+                        uint8_t* vt = smem + C::OFF_V + vst * V_BYTES;
+                        uint32_t lo = 0, hi = 0;            // keys with a value that is not finite
+                        for (int j = 0; j < KT / 2; ++j) {
+                            const int key = 2 * j + (int)(lane >> 4), c = lane & 15;
+                            uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * K_PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+                            const uint4 x = *at;
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            const bool past = tile * KT + key >= cur.s.total;
+                            bool odd = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (!bf16_finite(w[e])) { odd = true; w[e] &= 0xffff0000u; }
+                                if (!bf16_finite(w[e] >> 16)) { odd = true; w[e] &= 0x0000ffffu; }
+                            }
+                            if (past) *at = make_uint4(0, 0, 0, 0);
+                            else if (odd) *at = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (odd && !past) {
+                                if (key < 32) lo |= 1u << key;
+                                else hi |= 1u << (key - 32);
+                            }
+                        }
+                        lo = __reduce_or_sync(0xffffffffu, lo);
+                        hi = __reduce_or_sync(0xffffffffu, hi);
+                        if ((lo | hi) && lane == 0 && tile - edge0 < FLAGS) {
+                            flags[(seg % SEGS) * FLAGS + tile - edge0] = (uint64_t)hi << 32 | lo;
+                            any_flag[seg % SEGS] = 1;
+                        }
+                        fence_proxy_async_smem();
+                        __threadfence_block();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[B_V_SAFE + vst]);
+                    }
+                    // every stage passes here, so that this warp never falls a phase behind
+                    if (lane == 0) mbar_arrive(&bars[B_V_EMPTY + vst]);
+                    if (++vst == (uint32_t)VST) { vst = 0; vph ^= 1; }
+                }
+            }
+        } else {
+            // --------------------------------------------- MMA issue, one warp a branch
+            const int br = warp - 9;
+            if (elect_one()) {
+                const uint64_t qdesc = sdesc_sw128(smem_u32(smem + br * C::Q_BYTES), 16, 1024);
+                const uint64_t kdesc = sdesc_sw128(smem_u32(smem + C::OFF_K + (KS ? 0 : br) * C::K_BYTES), 16, 1024);
+                const uint64_t vdesc = sdesc_sw128(smem_u32(smem + C::OFF_V), K_PANEL, 1024);
+                const uint32_t d_o = tmem_base + TM_O + br * 128;
+                uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qph = 0, oeph = 0, pph = 0, safeph = 0;
+                bool ok = true, first = true;
+                auto issue_s = [&](uint32_t stage, int buf) {
+                    const uint32_t d = tmem_base + tm_s(br, buf);
+                    const uint64_t kd = kdesc + ((stage * C::K_STAGE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t pn = kk >> 2, ks = kk & 3;
+                        mma_ss(d, qdesc + pn * (Q_PANEL >> 4) + 2 * ks, kd + pn * (K_PANEL >> 4) + 2 * ks, IDESC_S, kk > 0);
+                    }
+                    mma_commit(&bars[B_S_FULL + 2 * br + buf]);
+                    mma_commit(&bars[B_K_EMPTY + stage]);
+                };
+                for (; ok && !cur.done(); cur.next(p, KT)) {
+                    const int n = cur.live_tiles(p, KT);
+                    if (n == 0) continue;
+                    const int edge0 = (int)(cur.s.before / KT);
+                    if (!(ok = mbar_wait(&bars[B_Q_FULL], qph, ab))) break;
+                    qph ^= 1;
+                    for (int t = 0; t < 2 && t < n; ++t) {
+                        if (!(ok = mbar_wait(&bars[B_K_FULL + kst], kph, ab))) break;
+                        tc_fence_after();
+                        issue_s(kst, t);
+                        if (++kst == (uint32_t)C::KST) { kst = 0; kph ^= 1; }
+                    }
+                    if (!ok) break;
+                    if (n <= 2) mma_commit(&bars[B_Q_EMPTY]);
+                    for (int j = 0; j < n; ++j) {
+                        const int buf = j & 1;
+                        if (!(ok = mbar_wait(&bars[B_V_FULL + vst], vph, ab))) break;
+                        if (cur.tile0 + j >= edge0) {
+                            if (!(ok = mbar_wait(&bars[B_V_SAFE + vst], (safeph >> vst) & 1u, ab))) break;
+                            safeph ^= 1u << vst;
+                        }
+                        if (j + 2 < n && !(ok = mbar_wait(&bars[B_K_FULL + kst], kph, ab))) break;
+                        if (j == 0 && !first) {
+                            if (!(ok = mbar_wait(&bars[B_O_EMPTY], oeph, ab))) break;
+                            oeph ^= 1;
+                        }
+                        if (!(ok = mbar_wait(&bars[B_P_FULL + 2 * br + buf], (pph >> buf) & 1u, ab))) break;
+                        pph ^= 1u << buf;
+                        tc_fence_after();
+                        const uint64_t vd = vdesc + ((vst * V_BYTES) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            mma_ts(d_o, tmem_base + tm_s(br, buf) + kk * 8, vd + 128 * kk, IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(&bars[B_PV_DONE + br]);
+                        mma_commit(&bars[B_V_EMPTY + vst]);
+                        if (++vst == (uint32_t)VST) { vst = 0; vph ^= 1; }
+                        if (j + 2 < n) {
+                            issue_s(kst, buf);
+                            if (++kst == (uint32_t)C::KST) { kst = 0; kph ^= 1; }
+                            if (j + 3 == n) mma_commit(&bars[B_Q_EMPTY]);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(&bars[B_O_FULL]);
+                    first = false;
+                }
+                mma_commit(&bars[B_FINAL + br]);        // before TMEM is freed
+                mbar_wait_teardown(&bars[B_FINAL + br], 0, lim);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------ weights and results
+        regs_inc<REGS_SOFTMAX>();
+        cur.begin(p, start, KT);
+        const int br = warp >> 2;
+        const uint32_t quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
+        const uint32_t tO = lane_base + TM_O + br * 128;
+        const float sl2 = p.scale_log2;
+        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        uint32_t sph = 0, ofph = 0, wph = 0, rph = 0;
+        uint32_t pv_count = 0;
+        bool ok = true, wrote_whole = false;
+        int seg = -1;
+        for (; ok && !cur.done(); cur.next(p, KT)) {
+            const int live = cur.live_tiles(p, KT);
+            if (live > 0) ++seg;
+            const PagedSeq s = cur.s;
+            const PagedRow x = paged_row(p, cur.hk, cur.rc, row, s.n_new);
+            const bool mine = x.live && row < p.chunk_rows;
+            uint64_t tree = 0;
+            if (p.mask && mine && (int64_t)(cur.tile0 + live) * KT > s.before) tree = paged_mask_bits(p, cur.b, x.q, s.n_new);
+            float m_run = NOTHING, l = 0.f;
+            for (int j = 0; j < live; ++j) {
+                const int buf = j & 1;
+                const uint32_t tS = lane_base + tm_s(br, buf);
+                if (!(ok = mbar_wait_warp(&bars[B_S_FULL + 2 * br + buf], (sph >> buf) & 1u, ab))) break;
+                sph ^= 1u << buf;
+                tc_fence_after();
+                uint32_t u[64];
+                tmem_ld32(tS + 0, &u[0]);
+                tmem_ld32(tS + 32, &u[32]);
+                tmem_wait_ld();
+                float sc[64];
+#pragma unroll
+                for (int c = 0; c < 64; ++c) sc[c] = __uint_as_float(u[c]);
+                const int k0 = (cur.tile0 + j) * KT;
+                if (k0 + KT > s.before) {
+                    const uint64_t vis = mine ? tile_mask(p, s, k0, x.q, tree) : 0;
+                    const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        sc[c] = ((c < 32 ? lo : hi) >> (c & 31) & 1u) ? sc[c] : -INFINITY;
+                }
+                float alpha = 1.0f;
+                bool rescale = false;
+                if (j == 0) m_run = fmaxf(tile_row_max(sc) * sl2, NOTHING);
+                uint32_t pk[32];
+                float tsum = tile_exp2(sc, sl2, m_run, pk);
+                tmem_st32(tS, &pk[0]);
+                if (j > 0 && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
+                    const float mxs = tile_row_max(sc) * sl2;
+                    if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
+                        const float m_new = fmaxf(m_run, mxs);
+                        alpha = ex2_approx(m_run - m_new);
+                        l *= alpha;
+                        m_run = m_new;
+                        rescale = true;
+                        tsum = tile_exp2(sc, sl2, m_run, pk);
+                        tmem_wait_st();
+                        tmem_st32(tS, &pk[0]);
+                    }
+                }
+                if (rescale) {
+                    if (!(ok = mbar_wait_warp(&bars[B_PV_DONE + br], (pv_count + j - 1) & 1u, ab))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c4 * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tO + c4 * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                l += tsum;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_P_FULL + 2 * br + buf]);
+            }
+            if (!ok) break;
+            pv_count += live;
+            // ---- the row's partial result; a unit that is whole is read back and finished
+            if (live > 0) {
+                if (!(ok = mbar_wait_warp(&bars[B_O_FULL], ofph, ab))) break;
+                ofph ^= 1;
+                tc_fence_after();
+            }
+            if (wrote_whole) {              // its rows have been read by every warp
+                if (!(ok = mbar_wait_warp(&bars[B_ROWS_READ], rph, ab))) break;
+                rph ^= 1;
+                wrote_whole = false;
+            }
+            if (s.bad || (live > 0 && bad_seg[seg % SEGS])) l = __int_as_float(0x7fc00000);
+            const bool odd = live > 0 && any_flag[seg % SEGS] != 0;
+            float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row) * (4 + 2 * DV);
+            if (mine) *reinterpret_cast<float2*>(part + 2 * br) = make_float2(m_run, l);
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t o[32];
+                if (live > 0) {
+                    tmem_ld32(tO + c4 * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (c4 == 3 && live > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[B_O_EMPTY]);
+                }
+                if (odd && mine) {
+                    // values that are not finite, of keys that this row sees
+                    const int edge0 = (int)(s.before / KT);
+                    for (int f = 0; f < FLAGS; ++f) {
+                        uint64_t keys = flags[(seg % SEGS) * FLAGS + f];
+                        if (keys) keys &= tile_mask(p, s, (edge0 + f) * KT, x.q, tree);
+                        while (keys) {
+                            const int key = (edge0 + f) * KT + __ffsll(keys) - 1;
+                            keys &= keys - 1;
+                            const int page = paged_page(p, cur.b, key / p.page);
+                            if (page < 0) continue;
+                            const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                                static_cast<const __nv_bfloat16*>(p.v) + page * p.s_v[0] + cur.hk * p.s_v[1] +
+                                (int64_t)(key % p.page) * p.s_v[2] + c4 * 32);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const uint32_t w = v[i];
+                                if (!bf16_finite(w)) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(w << 16));
+                            }
+                        }
+                    }
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(part + 4 + br * DV + c4 * 32 + 4 * i) =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            if (cur.whole()) {
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_ROWS_OUT]);
+                if (!(ok = mbar_wait_warp(&bars[B_ROWS_OUT], wph, ab))) break;
+                wph ^= 1;
+                for (int r = warp; r < p.chunk_rows; r += 8) {
+                    const PagedRow y = paged_row(p, cur.hk, cur.rc, r, s.n_new);
+                    if (!y.live) continue;
+                    const float* src = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * (4 + 2 * DV);
+                    float o1[8], o2[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o1[i] = i < DV / 32 ? src[4 + lane + 32 * i] : 0.f;
+                        o2[i] = i < DV / 32 ? src[4 + DV + lane + 32 * i] : 0.f;
+                    }
+                    paged_finish_row(p, lam, cur.b, y.h, y.q, lane, o1, src[1], o2, src[3]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_ROWS_READ]);
+                wrote_whole = true;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem_base, TMEM_COLS);
+}
+
+template <int HD, bool KS>
+int launch_hd(const CUtensorMap* m, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream) {
+    constexpr uint32_t smem = smem_bytes<HD, KS>();
+    if (cudaFuncSetAttribute(paged_tc_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return -1;
+    paged_tc_kernel<HD, KS><<<p.grid, THREADS, smem, stream>>>(m[3], m[4], m[0], m[1], m[2], p, box_rows, q_box);
+    return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
+}
+
+}  // namespace ptc
+
+int launch_paged_tc(const CUtensorMap* maps, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream) {
+    if (p.D == 64) return p.k_shared ? ptc::launch_hd<64, true>(maps, p, box_rows, q_box, stream)
+                                     : ptc::launch_hd<64, false>(maps, p, box_rows, q_box, stream);
+    return p.k_shared ? ptc::launch_hd<128, true>(maps, p, box_rows, q_box, stream)
+                      : ptc::launch_hd<128, false>(maps, p, box_rows, q_box, stream);
+}
+
+}  // namespace diffattn
