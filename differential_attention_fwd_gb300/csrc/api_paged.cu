@@ -136,13 +136,16 @@ int check_paged(const diffattn_paged_desc* d, const diffattn_pages* g) {
         return DIFFATTN_ERR_INVALID;
     const int rc = check_pages(g);
     if (rc != DIFFATTN_OK) return rc;
+    // tiles of a sequence over its units (16 rows a unit, 32 keys a tile at least) in 31 bits
+    const double keys = (double)g->max_pages * g->page_size + 1024;
+    if (keys > INT32_MAX / 2 || keys / 32 * (double)d->H * (1.0 + d->Tq) > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
     if (d->Tq > 1024 || d->B > (1 << 24) || d->H > (1 << 20) || d->B * d->H > (1ll << 31) / 1024)
         return DIFFATTN_ERR_UNSUPPORTED;
     return DIFFATTN_OK;
 }
 
 size_t part_bytes(const PagedPlan& n, int64_t dv) {
-    return (size_t)2 * n.grid * n.chunk_rows * (4 + 2 * dv) * sizeof(float);
+    return (size_t)2 * n.grid * n.chunk_rows * paged_part_floats((int)dv) * sizeof(float);
 }
 
 // The plan of the CUDA-core kernel; the grid is what `sms` multiprocessors hold at
@@ -173,7 +176,7 @@ bool tc_shape(const diffattn_paged_desc& d, const diffattn_pages& g) {
     return true;
 }
 
-// The plan of the tensor-core kernel for up to 16 rows: a block an SM.
+// The plan of the tensor-core kernel for up to 16 rows.
 void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, PagedPlan* n) {
     const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
     const int64_t rows = group * d.Tq;
@@ -181,7 +184,7 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
     n->row_chunks = (int)((rows + kMmaRows - 1) / kMmaRows);
     n->chunk_rows = (int)((rows + n->row_chunks - 1) / n->row_chunks);
     n->tile = kMmaTile;
-    n->grid = sms;
+    n->grid = sms * kMmaBlocksPerSm;
     const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
     if (tiles < n->grid) n->grid = (int)tiles;
     n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);

@@ -279,7 +279,7 @@ paged_simt_kernel(const PagedParams p) {
             }
             __syncthreads();
         }
-        const int stride = 4 + 2 * Dv;
+        const int stride = paged_part_floats(Dv), width = paged_part_width(Dv);
         for (int r = warp; r < RC; r += WARPS) {
             const PagedRow x = paged_row(p, cur.hk, cur.rc, r, n_new);
             if (!x.live) continue;
@@ -293,7 +293,7 @@ paged_simt_kernel(const PagedParams p) {
                     o1[j] = c < Dv ? om[r * Dv + c] : 0.f;
                     o2[j] = c < Dv ? om[(RC + r) * Dv + c] : 0.f;
                 }
-                paged_finish_row(p, lam, cur.b, x.h, x.q, lane, o1, l1, o2, l2);
+                paged_finish_row<8>(p, lam, cur.b, x.h, x.q, lane, o1, l1, o2, l2);
             } else {
                 float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * stride;
                 if (lane == 0) {
@@ -304,7 +304,7 @@ paged_simt_kernel(const PagedParams p) {
                 }
                 for (int c = lane; c < Dv; c += 32) {
                     part[4 + c] = om[r * Dv + c];
-                    part[4 + Dv + c] = om[(RC + r) * Dv + c];
+                    part[4 + width + c] = om[(RC + r) * Dv + c];
                 }
             }
         }
@@ -317,56 +317,23 @@ paged_simt_kernel(const PagedParams p) {
 // Merging pass: the unit that boundary c = blockIdx.x + 1 is the first to cut, if any.
 // With partial maxima m_i (log2 units), sums l_i and O_i:
 //     M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i.
-// A warp takes a row; with more than four parts all warps of the block share a row's
-// parts, in a fixed order.
+// A row is taken by one warp, or with many parts (a long sequence over many blocks) by
+// two, four or all eight, each adding its share of them: the time is the latency of
+// reading the parts from L2, which then overlap.  The order of the sums is fixed.
 // ---------------------------------------------------------------------------
 constexpr int C_WARPS = 8;
 
-struct Merged {
-    float m[2], l[2], o[2][8];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int br = 0; br < 2; ++br) {
-            m[br] = -INFINITY;
-            l[br] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[br][j] = 0.f;
-        }
-    }
-    __device__ __forceinline__ void add(const float* part, int Dv, int lane) {
-        float x[2][8];
-#pragma unroll
-        for (int br = 0; br < 2; ++br)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = lane + 32 * j;
-                x[br][j] = c < Dv ? part[4 + br * Dv + c] : 0.f;
-            }
-#pragma unroll
-        for (int br = 0; br < 2; ++br) {
-            const float pm = part[2 * br], pl = part[2 * br + 1];
-            const float mn = fmaxf(m[br], pm);
-            const float a = m[br] == -INFINITY ? 0.f : exp2f(m[br] - mn);
-            const float c = pm == -INFINITY ? 0.f : exp2f(pm - mn);
-            // a part that saw nothing has sum 0 and O 0, or a sum of NaN (a bad page)
-            l[br] = l[br] * (m[br] == -INFINITY ? 1.f : a) + pl * (pm == -INFINITY ? 1.f : c);
-            m[br] = mn;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[br][j] = (a == 0.f ? 0.f : o[br][j] * a) + (c == 0.f ? 0.f : x[br][j] * c);
-        }
-    }
-};
-
+template <int J>
 __global__ void __launch_bounds__(C_WARPS * 32)
 paged_combine_kernel(const PagedParams p) {
-    __shared__ float share[C_WARPS][4 + 512];
+    __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const int64_t total = p.cum[p.B];
     const int64_t grid = total < p.grid ? total : (int64_t)p.grid;
     const int64_t c = blockIdx.x + 1;
     if (c >= grid) return;
-    const int64_t t = c * total / grid;
+    const int64_t t = c * total / grid, before = (c - 1) * total / grid;
     int lo = 0, hi = p.B;                       // cum[lo] <= t < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -374,52 +341,92 @@ paged_combine_kernel(const PagedParams p) {
         else hi = mid;
     }
     const int b = lo;
-    const int64_t units = (int64_t)p.Hk * p.row_chunks;
-    const int64_t tiles = (p.cum[b + 1] - p.cum[b]) / units;
-    const int64_t unit = (t - p.cum[b]) / tiles;
-    const int64_t u0 = p.cum[b] + unit * tiles, u1 = u0 + tiles;
-    if (t == u0 || (c - 1) * total / grid > u0) return;
-    int64_t c1 = c;                             // the last block with tiles of the unit
+    const int units = p.Hk * p.row_chunks;
+    const int64_t cum = p.cum[b];
+    const int tiles = (int)((p.cum[b + 1] - cum) / units);
+    const int unit = (int)(t - cum) / tiles;
+    const int64_t u0 = cum + (int64_t)unit * tiles, u1 = u0 + tiles;
+    if (t == u0 || before > u0) return;
+    // the last block with tiles of the unit, c1: its range begins before u1
+    int64_t c1 = u1 * grid / total;             // its range begins at u1 or before
+    while (c1 * total / grid >= u1) --c1;
     while (c1 + 1 < grid && (c1 + 1) * total / grid < u1) ++c1;
     const int parts = (int)(c1 - c + 2);        // of blocks c - 1 .. c1
-    const int hk = (int)(unit / p.row_chunks), rc = (int)(unit - (int64_t)hk * p.row_chunks);
+    const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
     const PagedSeq s = paged_seq(p, b);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
-    const int64_t stride = 4 + 2 * p.Dv;
-    auto part_of = [&](int i, int r) {
-        const int64_t slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i);
-        return p.part + (slot * p.chunk_rows + r) * stride;
-    };
-    const bool spread = parts > 4;
-    const int step = spread ? gridDim.y : gridDim.y * C_WARPS;
-    for (int r = spread ? blockIdx.y : blockIdx.y * C_WARPS + warp; r < p.chunk_rows; r += step) {
+    const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
+    const int W = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : C_WARPS;
+    const int sub = warp % W;
+    const int step = gridDim.y * (C_WARPS / W);
+    for (int r0 = blockIdx.y * (C_WARPS / W); r0 < p.chunk_rows; r0 += step) {
+        const int r = r0 + warp / W;
         const PagedRow x = paged_row(p, hk, rc, r, s.n_new);
-        if (!x.live) continue;
-        Merged a;
-        a.clear();
-        if (!spread) {
-            for (int i = 0; i < parts; ++i) a.add(part_of(i, r), p.Dv, lane);
-        } else {
-#pragma unroll 2
-            for (int i = warp; i < parts; i += C_WARPS) a.add(part_of(i, r), p.Dv, lane);
-            float* mine = share[warp];
-            if (lane == 0) {
-                mine[0] = a.m[0]; mine[1] = a.l[0]; mine[2] = a.m[1]; mine[3] = a.l[1];
+        const bool live = x.live && r < p.chunk_rows;
+        auto part_of = [&](int i) {
+            const int64_t slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i);
+            return p.part + (slot * p.chunk_rows + r) * stride;
+        };
+        float o[2][J], l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) o[0][j] = o[1][j] = 0.f;
+        if (live) {
+            float m[2] = {-INFINITY, -INFINITY};
+            for (int i = lane; i < parts; i += 32) {
+                const float4 st = *reinterpret_cast<const float4*>(part_of(i));
+                m[0] = fmaxf(m[0], st.x);
+                m[1] = fmaxf(m[1], st.z);
             }
 #pragma unroll
-            for (int br = 0; br < 2; ++br)
+            for (int k = 16; k > 0; k >>= 1) {
+                m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], k));
+                m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], k));
+            }
+            // where nothing was seen m_i is -inf, and l_i 0 (or NaN: a bad page) as it is
+            const float m1 = m[0] == -INFINITY ? 0.f : m[0], m2 = m[1] == -INFINITY ? 0.f : m[1];
+            for (int i = lane; i < parts; i += 32) {
+                const float4 st = *reinterpret_cast<const float4*>(part_of(i));
+                l[0] += st.y * (st.x == -INFINITY ? 1.f : exp2f(st.x - m1));
+                l[1] += st.w * (st.z == -INFINITY ? 1.f : exp2f(st.z - m2));
+            }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (lane + 32 * j < p.Dv) mine[4 + br * p.Dv + lane + 32 * j] = a.o[br][j];
-            __syncthreads();
-            if (warp == 0) {
-                a.clear();
-                for (int w = 0; w < C_WARPS; ++w) a.add(share[w], p.Dv, lane);
+            for (int k = 16; k > 0; k >>= 1) {
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+                l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+            }
+#pragma unroll 4
+            for (int i = sub; i < parts; i += W) {
+                const float* src = part_of(i);
+                const float4 st = *reinterpret_cast<const float4*>(src);
+                const float w1 = st.x == -INFINITY ? 0.f : exp2f(st.x - m1);
+                const float w2 = st.z == -INFINITY ? 0.f : exp2f(st.z - m2);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int col = lane + 32 * j;
+                    if (col < p.Dv) {
+                        if (w1 != 0.f) o[0][j] = fmaf(w1, src[4 + col], o[0][j]);
+                        if (w2 != 0.f) o[1][j] = fmaf(w2, src[4 + width + col], o[1][j]);
+                    }
+                }
             }
         }
-        if (!spread || warp == 0)
-            paged_finish_row(p, lam, b, x.h, x.q, lane, a.o[0], a.l[0], a.o[1], a.l[1]);
-        if (spread) __syncthreads();
+        if (W > 1) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                share[warp][32 * j + lane] = o[0][j];
+                share[warp][32 * (J + j) + lane] = o[1][j];
+            }
+            __syncthreads();
+            if (sub == 0)
+                for (int w = 1; w < W; ++w)
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        o[0][j] += share[warp + w][32 * j + lane];
+                        o[1][j] += share[warp + w][32 * (J + j) + lane];
+                    }
+        }
+        if (live && sub == 0) paged_finish_row<J>(p, lam, b, x.h, x.q, lane, o[0], l[0], o[1], l[1]);
+        if (W > 1) __syncthreads();
     }
 }
 
@@ -456,7 +463,7 @@ int paged_simt_rows(int64_t rows) {
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     if (p.grid < 2) return 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)((p.chunk_rows + 15) / 16));
+    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)((p.chunk_rows + 3) / 4));
     cfg.blockDim = dim3(paged::C_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -464,7 +471,8 @@ int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel, p) == cudaSuccess ? 0 : -1;
+    return (p.Dv <= 128 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4>, p)
+                        : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8>, p)) == cudaSuccess ? 0 : -1;
 }
 
 int launch_paged_simt(const PagedParams& p, cudaStream_t stream) {

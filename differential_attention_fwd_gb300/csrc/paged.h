@@ -103,9 +103,14 @@ struct PagedParams {
     int vec16;                  // rows of the caches are 16-byte aligned,
     int q16;                    // and of the queries
     int grid;                   // blocks of the first pass
-    float* part;                // [2 * grid][chunk_rows][4 + 2 Dv]
+    float* part;                // [2 * grid][chunk_rows][paged_part_floats(Dv)]
     int64_t* cum;               // [B + 1] tiles before each sequence
 };
+
+// Floats of one row's partial result: m_1, l_1, m_2, l_2, O_1 and O_2, each O's width
+// rounded up to even so that rows stay 16-byte aligned.
+__host__ __device__ constexpr int paged_part_width(int Dv) { return (Dv + 1) / 2 * 2; }
+__host__ __device__ constexpr int paged_part_floats(int Dv) { return 4 + 2 * paged_part_width(Dv); }
 
 int launch_paged_simt(const PagedParams& p, cudaStream_t stream);
 // Rows of a unit of the CUDA-core kernel, for `rows` query rows a key/value head.
@@ -114,7 +119,8 @@ constexpr int kSimtBlocksPerSm = 3;
 // The tensor-core kernel of up to 16 rows a unit: maps of K1, K2 and V with boxes of
 // 64 columns x box_rows slots.
 constexpr int kMmaRows = 16;
-constexpr int kMmaTile = 128;
+constexpr int kMmaTile = 64;
+constexpr int kMmaBlocksPerSm = 2;
 int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream);
 // The tcgen05 kernel of up to 128 rows a unit: maps of K1, K2, V (boxes of 64 columns x
 // box_rows slots), Q1 and Q2 (boxes of 64 columns x q_box tokens).

@@ -5,14 +5,15 @@
 // Bound by HBM: a key costs 4 D + 256 bytes (2 D + 256 with shared keys) and 4 (D + 128)
 // operations a row, 192 FLOP a byte short of what the tensor cores could do even at 16
 // rows.  So the design is about never leaving the memory idle:
-//   - One producer warp streams the block's tiles of 128 keys through TMA into a ring
+//   - One producer warp streams the block's tiles of 64 keys through TMA into a ring
 //     that takes most of shared memory, across unit boundaries, two or more tiles ahead.
 //     A lane a page: box i of a tile is the part of it in one page.
-//   - Eight consumer warps take 16 keys of each tile each, and run on their own: a warp
+//   - Four consumer warps take 16 keys of each tile each, and run on their own: a warp
 //     keeps its own running maximum, sum and O (16 rows x 128 columns of both branches,
 //     128 registers a thread), so a tile needs no barrier but the ring's two.  They meet
-//     once a segment, when the eight partial results are merged in the stage that was
+//     once a segment, when the four partial results are merged in the stage that was
 //     read last.
+//   - Two blocks an SM: one streams while the other starts or merges a segment.
 //   - The products are warp-level (m16n8k16): at this size they are a quarter of the
 //     time that the tile's bytes take, and P goes from the score's accumulators to the
 //     next product's operand in registers.  A tcgen05 product would want 128 keys as its
@@ -29,24 +30,25 @@
 namespace diffattn {
 namespace pmma {
 
-constexpr int CONSUMERS = 8;                    // warps
-// A third warpgroup for the producer (three of its warps idle), which gives registers to
-// the consumers: 256 x 232 + 128 x 40 = 384 x 168, what the block is launched with.
-constexpr int THREADS = 384;
-constexpr uint32_t REGS_CONSUMER = 232, REGS_PRODUCER = 40;
-static_assert(256 * REGS_CONSUMER + 128 * REGS_PRODUCER <= THREADS * 168, "register split");
-constexpr int KT = 128;
+constexpr int CONSUMERS = 4;                    // warps
+// A second warpgroup for the producer (three of its warps idle), which gives registers to
+// the consumers: 128 x 224 + 128 x 32 = 256 x 128, what the block is launched with.
+constexpr int THREADS = 256;
+constexpr int BLOCKS_PER_SM = kMmaBlocksPerSm;
+constexpr uint32_t REGS_CONSUMER = 224, REGS_PRODUCER = 32;
+static_assert(128 * REGS_CONSUMER + 128 * REGS_PRODUCER <= THREADS * 128, "register split");
+constexpr int KT = kMmaTile;
 constexpr int SLICE = KT / CONSUMERS;           // keys of a warp
 constexpr int NR = 16;                          // rows of a unit
 constexpr int DV = 128;
-constexpr int PANEL = KT * 128;                 // 16 KB: 128 keys x 64 columns
+constexpr int PANEL = KT * 128;                 // 8 KB: 64 keys x 64 columns
 
 template <int HD, bool KS>
 struct Cfg {
     static constexpr int KP = HD / 64;                          // panels of a key tile
     static constexpr int NK = KS ? 1 : 2;
-    static constexpr int STAGE = (NK * KP + 2) * PANEL;         // 48, 64 or 96 KB
-    static constexpr int NST = STAGE <= 48 * 1024 ? 4 : STAGE <= 64 * 1024 ? 3 : 2;
+    static constexpr int STAGE = (NK * KP + 2) * PANEL;         // 24, 32 or 48 KB
+    static constexpr int NST = 96 * 1024 / STAGE;
     static constexpr int OFF_V = NK * KP * PANEL;
     static constexpr int OFF_Q = NST * STAGE;                   // [branch][panel] 16 rows x 128 bytes
     static constexpr int Q_PANEL = NR * 128;
@@ -55,7 +57,7 @@ struct Cfg {
     static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;      // abort, bad flags by stage
     static constexpr int SMEM = OFF_MISC + 64 + 1024;
     static constexpr int ROUND = STAGE / CONSUMERS / (2 * DV * 4);  // rows merged at once
-    static_assert(SMEM <= 232448 - 256, "shared memory");
+    static_assert(BLOCKS_PER_SM * (SMEM + 256 + 1024) <= 228 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint32_t slice_mask(const PagedParams& p, const Paged
 }
 
 template <int HD, bool KS>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM)
 paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int box_rows) {
     using C = Cfg<HD, KS>;
@@ -414,68 +416,53 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                 }
             }
         named_bar_sync(1, 32 * CONSUMERS);      // every warp is done with the stage, too
-        float scale[2][2];
-#pragma unroll
-        for (int br = 0; br < 2; ++br)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < CONSUMERS; ++w) top = fmaxf(top, stat[w * 4 * NR + br * NR + r0 + 8 * h]);
-                scale[br][h] = m[br][h] == -INFINITY ? 0.f : ex2_approx(m[br][h] - top);
-            }
+        // Unscaled: this runs once a segment, cold, so it costs by its instructions.
         float* buf = reinterpret_cast<float*>(smem + st * C::STAGE);     // [warp][row of the round][branch][DV]
         for (int row0 = 0; row0 < p.chunk_rows; row0 += C::ROUND) {
-            if (live > 0) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = r0 + 8 * h - row0;
-                    if (r < 0 || r >= C::ROUND || !(h ? lb : la)) continue;
+            for (int h = 0; h < 2; ++h) {
+                const int r = r0 + 8 * h - row0;
+                if (live == 0 || r < 0 || r >= C::ROUND || !(h ? lb : la)) continue;
+                float* dst = buf + (warp * C::ROUND + r) * 2 * DV + 2 * (lane & 3);
 #pragma unroll
-                    for (int br = 0; br < 2; ++br)
+                for (int br = 0; br < 2; ++br)
 #pragma unroll
-                        for (int n = 0; n < DV / 8; ++n)
-                            *reinterpret_cast<float2*>(buf + ((warp * C::ROUND + r) * 2 + br) * DV + 8 * n + 2 * (lane & 3)) =
-                                scale[br][h] == 0.f ? make_float2(0.f, 0.f)
-                                                    : make_float2(o[br][n][2 * h] * scale[br][h], o[br][n][2 * h + 1] * scale[br][h]);
-                }
+                    for (int n = 0; n < DV / 8; ++n)
+                        *reinterpret_cast<float2*>(dst + br * DV + 8 * n) = make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
             }
             named_bar_sync(1, 32 * CONSUMERS);
             for (int r = warp; r < C::ROUND && row0 + r < p.chunk_rows; r += CONSUMERS) {
                 const PagedRow x = paged_row(p, cur.hk, cur.rc, row0 + r, s.n_new);
                 if (!x.live) continue;
-                float a[2][8], mt[2], lt[2];
+                float mt[2], lt[2], wt[2][CONSUMERS], a[2][DV / 32];
 #pragma unroll
                 for (int br = 0; br < 2; ++br) {
-                    mt[br] = -INFINITY;
+                    const float* ms = stat + br * NR + row0 + r;
+                    mt[br] = fmaxf(fmaxf(ms[0], ms[4 * NR]), fmaxf(ms[8 * NR], ms[12 * NR]));
                     lt[br] = 0.f;
 #pragma unroll
-                    for (int w = 0; w < CONSUMERS; ++w) mt[br] = fmaxf(mt[br], stat[w * 4 * NR + br * NR + row0 + r]);
-#pragma unroll
                     for (int w = 0; w < CONSUMERS; ++w) {
-                        const float mw = stat[w * 4 * NR + br * NR + row0 + r], lw = stat[w * 4 * NR + (2 + br) * NR + row0 + r];
-                        lt[br] += mw == -INFINITY ? lw : lw * ex2_approx(mw - mt[br]);     // 0 or NaN where nothing was seen
+                        const float mw = ms[w * 4 * NR], lw = ms[(w * 4 + 2) * NR];
+                        wt[br][w] = mw == -INFINITY ? 0.f : ex2_approx(mw - mt[br]);
+                        lt[br] += mw == -INFINITY ? lw : lw * wt[br][w];       // 0 or NaN where nothing was seen
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        a[br][j] = 0.f;
-                        if (j < DV / 32 && live > 0) {
+                    for (int j = 0; j < DV / 32; ++j) a[br][j] = 0.f;
+                }
+                if (live > 0) {
 #pragma unroll
-                            for (int w = 0; w < CONSUMERS; ++w)
-                                a[br][j] += buf[((w * C::ROUND + r) * 2 + br) * DV + lane + 32 * j];
-                        }
-                    }
+                    for (int w = 0; w < CONSUMERS; ++w)
+#pragma unroll
+                        for (int br = 0; br < 2; ++br)
+#pragma unroll
+                            for (int j = 0; j < DV / 32; ++j)
+                                a[br][j] = fmaf(wt[br][w], buf[((w * C::ROUND + r) * 2 + br) * DV + lane + 32 * j], a[br][j]);
                 }
                 if (cur.whole()) {
-                    paged_finish_row(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
+                    paged_finish_row<DV / 32>(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
                 } else {
                     float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row0 + r) * (4 + 2 * DV);
-                    if (lane == 0) {
-                        part[0] = mt[0];
-                        part[1] = lt[0];
-                        part[2] = mt[1];
-                        part[3] = lt[1];
-                    }
+                    if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(mt[0], lt[0], mt[1], lt[1]);
 #pragma unroll
                     for (int br = 0; br < 2; ++br)
 #pragma unroll

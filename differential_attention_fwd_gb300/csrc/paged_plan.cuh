@@ -106,7 +106,7 @@ __device__ __forceinline__ PagedStart paged_start(const PagedParams& p, int kt, 
 // A block's segments in turn.
 struct PagedCursor {
     int64_t left;               // tiles of the block's range not yet handed out
-    int64_t local;              // place among the sequence's tiles
+    int local;                  // place among the sequence's tiles (fewer than 2^31: checked on the host)
     int b, unit;                // unit of the sequence (hk * row_chunks + row chunk)
     int hk, rc;
     int tile0, n;               // the segment's tiles within the unit
@@ -117,7 +117,7 @@ struct PagedCursor {
         const int64_t grid = st.total < gridDim.x ? st.total : (int64_t)gridDim.x;
         left = blockIdx.x < grid ? (blockIdx.x + 1) * st.total / grid - st.first : 0;
         b = st.b;
-        local = st.local;
+        local = (int)st.local;
         if (left > 0) load(p, kt);
     }
     __device__ __forceinline__ void load(const PagedParams& p, int kt) {
@@ -126,8 +126,8 @@ struct PagedCursor {
         cut(p);
     }
     __device__ __forceinline__ void cut(const PagedParams& p) {
-        unit = (int)(local / tiles);
-        tile0 = (int)(local - (int64_t)unit * tiles);
+        unit = local / tiles;
+        tile0 = local - unit * tiles;
         n = (int)(left < tiles - tile0 ? left : tiles - tile0);
         hk = unit / p.row_chunks;
         rc = unit - hk * p.row_chunks;
@@ -137,7 +137,7 @@ struct PagedCursor {
         left -= n;
         local += n;
         if (left <= 0) return;
-        if (local == (int64_t)tiles * p.Hk * p.row_chunks) {
+        if (local == tiles * p.Hk * p.row_chunks) {
             local = 0;
             do {
                 if (++b >= p.B) { left = 0; return; }   // never with tiles left
@@ -185,16 +185,18 @@ __device__ __forceinline__ uint64_t paged_mask_bits(const PagedParams& p, int b,
     return bits;
 }
 
-// One row's output from O_b / l_b of both branches: columns lane + 32 j, j < 8.
+// One row's output from O_b and l_b of both branches: columns lane + 32 j, j < J.
+template <int J>
 __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam, int b, int h, int q, int lane,
-                                                 const float (&o1)[8], float l1, const float (&o2)[8], float l2) {
-    float y[8];
+                                                 const float (&o1)[J], float l1, const float (&o2)[J], float l2) {
+    const float i1 = l1 == 0.f ? 0.f : 1.f / l1;       // a row that saw nothing gives 0
+    const float i2 = l2 == 0.f ? 0.f : 1.f / l2;
+    float y[J];
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float a = l1 == 0.f ? 0.f : o1[j] / l1;      // a row that saw nothing gives 0
-        const float c = l2 == 0.f ? 0.f : o2[j] / l2;
-        y[j] = fmaf(-lam, c, a);                           // exactly 0 where the branches are alike and lambda is 1
+    for (int j = 0; j < J; ++j) {
+        // the branches rounded alike, so that alike branches cancel exactly at lambda = 1
+        y[j] = fmaf(-lam, __fmul_rn(o2[j], i2), __fmul_rn(o1[j], i1));
         if (lane + 32 * j >= p.Dv) y[j] = 0.f;
         sum += y[j];
     }
@@ -207,7 +209,7 @@ __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam
         }
         float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < J; ++j)
             if (lane + 32 * j < p.Dv) {
                 y[j] -= mean;
                 ss = fmaf(y[j], y[j], ss);
@@ -216,11 +218,11 @@ __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = 1.0f / sqrtf(ss / p.Dv + p.norm_eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= r;
+        for (int j = 0; j < J; ++j) y[j] *= r;
     }
     const int64_t at = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < J; ++j) {
         const int c = lane + 32 * j;
         if (c >= p.Dv) continue;
         float v = y[j];

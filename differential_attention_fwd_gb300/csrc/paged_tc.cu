@@ -548,13 +548,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                     const PagedRow y = paged_row(p, cur.hk, cur.rc, r, s.n_new);
                     if (!y.live) continue;
                     const float* src = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * (4 + 2 * DV);
-                    float o1[8], o2[8];
+                    float o1[DV / 32], o2[DV / 32];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o1[i] = i < DV / 32 ? src[4 + lane + 32 * i] : 0.f;
-                        o2[i] = i < DV / 32 ? src[4 + DV + lane + 32 * i] : 0.f;
+                    for (int i = 0; i < DV / 32; ++i) {
+                        o1[i] = src[4 + lane + 32 * i];
+                        o2[i] = src[4 + DV + lane + 32 * i];
                     }
-                    paged_finish_row(p, lam, cur.b, y.h, y.q, lane, o1, src[1], o2, src[3]);
+                    paged_finish_row<DV / 32>(p, lam, cur.b, y.h, y.q, lane, o1, src[1], o2, src[3]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_ROWS_READ]);
