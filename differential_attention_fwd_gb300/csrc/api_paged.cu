@@ -145,7 +145,7 @@ int check_paged(const diffattn_paged_desc* d, const diffattn_pages* g) {
 }
 
 size_t part_bytes(const PagedPlan& n, int64_t dv) {
-    return (size_t)2 * n.grid * n.chunk_rows * paged_part_floats((int)dv) * sizeof(float);
+    return n.grid * sizeof(PagedJoin) + (size_t)2 * n.grid * n.chunk_rows * paged_part_floats((int)dv) * sizeof(float);
 }
 
 // The plan of the CUDA-core kernel; the grid is what `sms` multiprocessors hold at
@@ -160,7 +160,7 @@ void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, P
     n->grid = sms * kSimtBlocksPerSm;
     const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
     if (tiles < n->grid) n->grid = (int)tiles;
-    n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, dv);
+    n->bytes = part_bytes(*n, dv);
 }
 
 // Whether the tensor-core kernels take the shape and the cache's layout: bf16, value
@@ -187,7 +187,7 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
     n->grid = sms * kMmaBlocksPerSm;
     const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
     if (tiles < n->grid) n->grid = (int)tiles;
-    n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);
+    n->bytes = part_bytes(*n, 128);
 }
 
 // The tcgen05 kernel's plan, for more rows than that (and for one more reason: the
@@ -215,7 +215,7 @@ void plan_tc(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pag
     n->grid = sms;
     const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
     if (tiles < n->grid) n->grid = (int)tiles;
-    n->bytes = (size_t)((d.B + 1) * 8 + 15) / 16 * 16 + part_bytes(*n, 128);
+    n->bytes = part_bytes(*n, 128);
 }
 
 int device_sms() {
@@ -433,8 +433,8 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.vec16 = p.D * es % 16 == 0 && p.Dv * es % 16 == 0 && rows16(p.k1, p.s_k1, es) && rows16(p.k2, p.s_k2, es) &&
               rows16(p.v, p.s_v, es);
     p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
-    p.cum = static_cast<int64_t*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (size_t)((d.B + 1) * 8 + 15) / 16 * 16);
+    p.joins = static_cast<PagedJoin*>(workspace);
+    p.part = reinterpret_cast<float*>(p.joins + n.grid);
     p.head_rows = n.head_rows;
     p.chunk_rows = n.chunk_rows;
     p.row_chunks = n.row_chunks;

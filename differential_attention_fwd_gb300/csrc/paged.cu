@@ -104,9 +104,11 @@ paged_simt_kernel(const PagedParams p) {
     const bool two = Dv > 128;
 
     PagedCursor cur;
+    if (tid == 0) cur.no_join(p);
     for (cur.begin(p, start, KT); !cur.done(); cur.next(p, KT)) {
         const int live = cur.live_tiles(p, KT);
         const int n_new = cur.s.n_new;
+        if (tid == 0) cur.join(p, start_s.total);
         bool bad = cur.s.bad;
         // the rows' queries and state
         for (int i = tid; i < 2 * RC * L.dpad; i += THREADS) {
@@ -314,7 +316,8 @@ paged_simt_kernel(const PagedParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Merging pass: the unit that boundary c = blockIdx.x + 1 is the first to cut, if any.
+// Merging pass: the unit that block c = blockIdx.x of the first pass started and did not
+// finish, if any.
 // With partial maxima m_i (log2 units), sums l_i and O_i:
 //     M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i.
 // A row is taken by one warp, or with many parts (a long sequence over many blocks) by
@@ -329,31 +332,11 @@ paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int64_t total = p.cum[p.B];
-    const int64_t grid = total < p.grid ? total : (int64_t)p.grid;
-    const int64_t c = blockIdx.x + 1;
-    if (c >= grid) return;
-    const int64_t t = c * total / grid, before = (c - 1) * total / grid;
-    int lo = 0, hi = p.B;                       // cum[lo] <= t < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.cum[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const int b = lo;
-    const int units = p.Hk * p.row_chunks;
-    const int64_t cum = p.cum[b];
-    const int tiles = (int)((p.cum[b + 1] - cum) / units);
-    const int unit = (int)(t - cum) / tiles;
-    const int64_t u0 = cum + (int64_t)unit * tiles, u1 = u0 + tiles;
-    if (t == u0 || before > u0) return;
-    // the last block with tiles of the unit, c1: its range begins before u1
-    int64_t c1 = u1 * grid / total;             // its range begins at u1 or before
-    while (c1 * total / grid >= u1) --c1;
-    while (c1 + 1 < grid && (c1 + 1) * total / grid < u1) ++c1;
-    const int parts = (int)(c1 - c + 2);        // of blocks c - 1 .. c1
+    const int c = blockIdx.x;
+    const int4 join = *reinterpret_cast<const int4*>(p.joins + c);
+    const int parts = join.x, b = join.y, unit = join.z, n_new = join.w;
+    if (parts == 0) return;
     const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
-    const PagedSeq s = paged_seq(p, b);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
     const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
     const int W = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : C_WARPS;
@@ -361,10 +344,10 @@ paged_combine_kernel(const PagedParams p) {
     const int step = gridDim.y * (C_WARPS / W);
     for (int r0 = blockIdx.y * (C_WARPS / W); r0 < p.chunk_rows; r0 += step) {
         const int r = r0 + warp / W;
-        const PagedRow x = paged_row(p, hk, rc, r, s.n_new);
+        const PagedRow x = paged_row(p, hk, rc, r, n_new);
         const bool live = x.live && r < p.chunk_rows;
         auto part_of = [&](int i) {
-            const int64_t slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i);
+            const int64_t slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
             return p.part + (slot * p.chunk_rows + r) * stride;
         };
         float o[2][J], l[2] = {0.f, 0.f};
@@ -394,19 +377,24 @@ paged_combine_kernel(const PagedParams p) {
                 l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
                 l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
             }
+            // no branch on the weight: the loads of all columns and of several parts go
+            // out together (a part that saw nothing holds zeros)
 #pragma unroll 4
             for (int i = sub; i < parts; i += W) {
                 const float* src = part_of(i);
-                const float4 st = *reinterpret_cast<const float4*>(src);
-                const float w1 = st.x == -INFINITY ? 0.f : exp2f(st.x - m1);
-                const float w2 = st.z == -INFINITY ? 0.f : exp2f(st.z - m2);
+                float x[2][J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const int col = lane + 32 * j;
-                    if (col < p.Dv) {
-                        if (w1 != 0.f) o[0][j] = fmaf(w1, src[4 + col], o[0][j]);
-                        if (w2 != 0.f) o[1][j] = fmaf(w2, src[4 + width + col], o[1][j]);
-                    }
+                    const int col = min(lane + 32 * j, p.Dv - 1);
+                    x[0][j] = src[4 + col];
+                    x[1][j] = src[4 + width + col];
+                }
+                const float4 st = *reinterpret_cast<const float4*>(src);
+                const float w1 = exp2f(st.x - m1), w2 = exp2f(st.z - m2);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    o[0][j] = fmaf(w1, x[0][j], o[0][j]);
+                    o[1][j] = fmaf(w2, x[1][j], o[1][j]);
                 }
             }
         }
@@ -461,9 +449,9 @@ int paged_simt_rows(int64_t rows) {
 }
 
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
-    if (p.grid < 2) return 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.grid - 1), (unsigned)((p.chunk_rows + 3) / 4));
+    // a block a row where few rows may have many parts, else four rows a block
+    cfg.gridDim = dim3((unsigned)p.grid, (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
     cfg.blockDim = dim3(paged::C_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -69,6 +69,12 @@ int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream);
 void plan_rotary(RotaryParams* p, int num_sms);
 void plan_rotary_bwd(RotaryParams* p);
 
+// A unit that block c started and did not finish, for the merging pass: its parts are
+// in slots 2 c + 1, 2 (c + 1), ... 2 (c + parts - 1).  parts = 0: there is none.
+struct alignas(16) PagedJoin {
+    int parts, b, unit, n_new;
+};
+
 // Attention over the paged cache.
 struct PagedParams {
     int B, H, Hk, group, Tq, D, Dv;
@@ -104,7 +110,7 @@ struct PagedParams {
     int q16;                    // and of the queries
     int grid;                   // blocks of the first pass
     float* part;                // [2 * grid][chunk_rows][paged_part_floats(Dv)]
-    int64_t* cum;               // [B + 1] tiles before each sequence
+    struct PagedJoin* joins;    // [grid] what the merging pass has to do
 };
 
 // Floats of one row's partial result: m_1, l_1, m_2, l_2, O_1 and O_2, each O's width

@@ -32,10 +32,10 @@ namespace pmma {
 
 constexpr int CONSUMERS = 4;                    // warps
 // A second warpgroup for the producer (three of its warps idle), which gives registers to
-// the consumers: 128 x 224 + 128 x 32 = 256 x 128, what the block is launched with.
+// the consumers: 128 x 216 + 128 x 40 = 256 x 128, what the block is launched with.
 constexpr int THREADS = 256;
 constexpr int BLOCKS_PER_SM = kMmaBlocksPerSm;
-constexpr uint32_t REGS_CONSUMER = 224, REGS_PRODUCER = 32;
+constexpr uint32_t REGS_CONSUMER = 216, REGS_PRODUCER = 40;
 static_assert(128 * REGS_CONSUMER + 128 * REGS_PRODUCER <= THREADS * 128, "register split");
 constexpr int KT = kMmaTile;
 constexpr int SLICE = KT / CONSUMERS;           // keys of a warp
@@ -139,6 +139,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             tma_prefetch_desc(&tm_k2);
             tma_prefetch_desc(&tm_v);
         }
+        if (lane == 0) cur.no_join(p);
         const int boxes = KT / box_rows;
         uint32_t armed = 0;                     // tiles issued
         int st = 0;
@@ -146,6 +147,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         bool ok = true;
         for (; ok && !cur.done(); cur.next(p, KT)) {
             const int live = cur.live_tiles(p, KT);
+            if (lane == 0) cur.join(p, start_s.total);
             // the page of this lane's box, one tile ahead
             auto look = [&](int i) -> int {
                 const int key = (cur.tile0 + i) * KT + lane * box_rows;

@@ -63,7 +63,7 @@ struct PagedStart {
 };
 
 // Every thread of the block calls this; `scratch` holds THREADS / 32 + 1 int64_t and
-// a PagedStart in shared memory.  Block 0 also writes p.cum for the merging pass.
+// a PagedStart in shared memory.
 template <int THREADS>
 __device__ __forceinline__ PagedStart paged_start(const PagedParams& p, int kt, int64_t* scratch, PagedStart* result) {
     constexpr int WARPS = THREADS / 32;
@@ -94,11 +94,9 @@ __device__ __forceinline__ PagedStart paged_start(const PagedParams& p, int kt, 
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
         const int64_t n = paged_seq_tiles(paged_seq(p, b), kt) * units;
-        if (blockIdx.x == 0) p.cum[b] = at;
         if (first >= at && first < at + n) *result = PagedStart{total, first, b, first - at};
         at += n;
     }
-    if (blockIdx.x == 0 && tid == THREADS - 1) p.cum[p.B] = total;
     __syncthreads();
     return *result;
 }
@@ -149,6 +147,21 @@ struct PagedCursor {
     }
     __device__ __forceinline__ bool whole() const { return n == tiles; }
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0); }
+    // One thread of the block, at each of its segments and once before them: leaves word
+    // for the merging pass.  The unit's last tile is in the block before the first one
+    // that begins at its end or later.
+    __device__ __forceinline__ void no_join(const PagedParams& p) const { p.joins[blockIdx.x].parts = 0; }
+    __device__ __forceinline__ void join(const PagedParams& p, int64_t total) const {
+        if (tile0 != 0 || whole()) return;
+        const int64_t grid = total < gridDim.x ? total : (int64_t)gridDim.x;
+        // the block's range ends with this segment: the unit goes on at tile `end` of the
+        // launch, and ends `rest` tiles later
+        const int64_t end = (int64_t)(blockIdx.x + 1) * total / grid, last = end + (tiles - n) - 1;
+        int64_t c = last * grid / total;                // a block that begins at `last` or before
+        while (c + 1 < grid && (c + 1) * total / grid <= last) ++c;
+        while (c * total / grid > last) --c;
+        p.joins[blockIdx.x] = PagedJoin{(int)(c - blockIdx.x) + 1, b, unit, s.n_new};
+    }
     // The segment's tiles that some row of its chunk may see: later ones hold only
     // keys behind the chunk's last query.
     __device__ __forceinline__ int live_tiles(const PagedParams& p, int kt) const {

@@ -172,10 +172,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             const int boxes = KT / box_rows;
             uint32_t kst = 0, kph = 1, vst = 0, vph = 1, nk = 0, nv = 0, nq = 0;
             bool ok = true;
+            if (lane == 0) cur.no_join(p);
             int seg = -1;                       // segments with tiles, as every role counts them
             for (; ok && !cur.done(); cur.next(p, KT)) {
                 const int live = cur.live_tiles(p, KT);
                 if (cur.s.bad && lane == 0) atomicOr(p.status, kStatusIndex);
+                if (lane == 0) cur.join(p, start_s.total);
                 if (live == 0) continue;
                 ++seg;
                 if (lane == 0) bad_seg[seg % SEGS] = 0;
