@@ -122,7 +122,7 @@ bool same3(const int64_t a[3], const int64_t b[3]) { return a[0] == b[0] && a[1]
 // attention over the paged cache
 // ---------------------------------------------------------------------------
 struct PagedPlan {
-    int chunk_rows = 0, head_rows = 0, row_chunks = 0, tile = 0, grid = 0;
+    int chunk_rows = 0, head_rows = 0, row_chunks = 0, tile = 0, workers = 0;
     size_t bytes = 0;
 };
 
@@ -136,20 +136,28 @@ int check_paged(const diffattn_paged_desc* d, const diffattn_pages* g) {
         return DIFFATTN_ERR_INVALID;
     const int rc = check_pages(g);
     if (rc != DIFFATTN_OK) return rc;
-    // tiles of a sequence over its units (16 rows a unit, 32 keys a tile at least) in 31 bits
-    const double keys = (double)g->max_pages * g->page_size + 1024;
-    if (keys > INT32_MAX / 2 || keys / 32 * (double)d->H * (1.0 + d->Tq) > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
+    // the tiles of all units in 31 bits, 16 keys a tile and 16 rows a unit at least
+    const double keys = (double)g->max_pages * g->page_size, rows = (double)group * d->Tq;
+    if (keys > INT32_MAX / 2 || d->B * (keys / 16 + 1) * (double)(d->H / group) * (rows / 16 + 1) > INT32_MAX)
+        return DIFFATTN_ERR_UNSUPPORTED;
     if (d->Tq > 1024 || d->B > (1 << 24) || d->H > (1 << 20) || d->B * d->H > (1ll << 31) / 1024)
         return DIFFATTN_ERR_UNSUPPORTED;
     return DIFFATTN_OK;
 }
 
 size_t part_bytes(const PagedPlan& n, int64_t dv) {
-    return n.grid * sizeof(PagedJoin) + (size_t)2 * n.grid * n.chunk_rows * paged_part_floats((int)dv) * sizeof(float);
+    return n.workers * sizeof(PagedJoin) + (size_t)2 * n.workers * n.chunk_rows * paged_part_floats((int)dv) * sizeof(float);
 }
 
-// The plan of the CUDA-core kernel; the grid is what `sms` multiprocessors hold at
-// once, or fewer if there cannot be that many tiles.
+// `workers`, or fewer if there cannot be that many tiles.
+int fewer(const diffattn_paged_desc& d, const diffattn_pages& g, const PagedPlan* n, int workers) {
+    const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
+    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
+    return tiles < workers ? (int)tiles : workers;
+}
+
+// The plan of the CUDA-core kernel; its blocks are what `sms` multiprocessors hold at
+// once.
 void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, PagedPlan* n) {
     const int64_t dv = d.Dv == 0 ? 2 * d.D : d.Dv;
     const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
@@ -157,9 +165,7 @@ void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, P
     n->chunk_rows = paged_simt_rows(group * d.Tq);
     n->row_chunks = (int)((group * d.Tq + n->chunk_rows - 1) / n->chunk_rows);
     n->tile = 32;
-    n->grid = sms * kSimtBlocksPerSm;
-    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
-    if (tiles < n->grid) n->grid = (int)tiles;
+    n->workers = fewer(d, g, n, sms * kSimtBlocksPerSm);
     n->bytes = part_bytes(*n, dv);
 }
 
@@ -184,9 +190,7 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
     n->row_chunks = (int)((rows + kMmaRows - 1) / kMmaRows);
     n->chunk_rows = (int)((rows + n->row_chunks - 1) / n->row_chunks);
     n->tile = kMmaTile;
-    n->grid = sms * kMmaBlocksPerSm;
-    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
-    if (tiles < n->grid) n->grid = (int)tiles;
+    n->workers = sms * (n->chunk_rows <= 8 ? kMmaWarps : kMmaWarps / 4);
     n->bytes = part_bytes(*n, 128);
 }
 
@@ -212,9 +216,7 @@ void plan_tc(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pag
         n->row_chunks = (int)(group * (n->head_rows / kTcRows));
     }
     n->tile = kTcTile;
-    n->grid = sms;
-    const double tiles = (double)d.B * (d.H / group) * n->row_chunks * ((double)g.max_pages * g.page_size / n->tile + 1);
-    if (tiles < n->grid) n->grid = (int)tiles;
+    n->workers = fewer(d, g, n, sms);
     n->bytes = part_bytes(*n, 128);
 }
 
@@ -433,12 +435,15 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.vec16 = p.D * es % 16 == 0 && p.Dv * es % 16 == 0 && rows16(p.k1, p.s_k1, es) && rows16(p.k2, p.s_k2, es) &&
               rows16(p.v, p.s_v, es);
     p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
+    p.o4 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(d.o_stride[0] * es) | (uintptr_t)(d.o_stride[1] * es) |
+            (uintptr_t)(d.o_stride[2] * es)) % 4 == 0;
     p.joins = static_cast<PagedJoin*>(workspace);
-    p.part = reinterpret_cast<float*>(p.joins + n.grid);
+    p.part = reinterpret_cast<float*>(p.joins + n.workers);
     p.head_rows = n.head_rows;
     p.chunk_rows = n.chunk_rows;
     p.row_chunks = n.row_chunks;
-    p.grid = n.grid;
+    p.workers = n.workers;
+    p.solo = n.chunk_rows <= 8;
     if (tc) {
         // boxes that stay inside one page and divide the tile
         int box = n.tile;
@@ -458,7 +463,7 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
             return launch_paged_tc(maps, p, box, q_box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
                                                                                                      : DIFFATTN_ERR_CUDA;
         }
-        return launch_paged_mma(maps, p, box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
+        return launch_paged_mma(maps, p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
                                                                                            : DIFFATTN_ERR_CUDA;
     }
     return launch_paged_simt(p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;

@@ -22,6 +22,7 @@ constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 constexpr int KT = 32;
 constexpr int MAX_RC = 16;
+constexpr int SNAP = 2;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(THREADS)
 paged_simt_kernel(const PagedParams p) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scan[WARPS + 1];
-    __shared__ PagedStart start_s;
+    __shared__ int scan[WARPS];
+    __shared__ PagedBlock<1> blk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.D, Dv = p.Dv;
     const bool shared = p.k_shared != 0;
@@ -94,7 +95,7 @@ paged_simt_kernel(const PagedParams p) {
     float* st_l = st_m + 2 * RC;
     float* st_a = st_l + 2 * RC;
     pdl_launch_dependents();
-    const PagedStart start = paged_start<THREADS>(p, KT, scan, &start_s);
+    paged_start<THREADS, 1>(p, KT, 1, p.workers, 1, SNAP, scan, &blk);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
@@ -104,11 +105,11 @@ paged_simt_kernel(const PagedParams p) {
     const bool two = Dv > 128;
 
     PagedCursor cur;
-    if (tid == 0) cur.no_join(p);
-    for (cur.begin(p, start, KT); !cur.done(); cur.next(p, KT)) {
+    if (tid == 0) PagedCursor::no_join(p, blockIdx.x);
+    for (cur.begin(p, blk, 0, blockIdx.x, KT); !cur.done(); cur.next(p, KT)) {
         const int live = cur.live_tiles(p, KT);
         const int n_new = cur.s.n_new;
-        if (tid == 0) cur.join(p, start_s.total);
+        if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP);
         bool bad = cur.s.bad;
         // the rows' queries and state
         for (int i = tid; i < 2 * RC * L.dpad; i += THREADS) {
@@ -316,8 +317,7 @@ paged_simt_kernel(const PagedParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Merging pass: the unit that block c = blockIdx.x of the first pass started and did not
-// finish, if any.
+// Merging pass: the units that workers c of the first pass started and did not finish.
 // With partial maxima m_i (log2 units), sums l_i and O_i:
 //     M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i.
 // A row is taken by one warp, or with many parts (a long sequence over many blocks) by
@@ -325,6 +325,7 @@ paged_simt_kernel(const PagedParams p) {
 // reading the parts from L2, which then overlap.  The order of the sums is fixed.
 // ---------------------------------------------------------------------------
 constexpr int C_WARPS = 8;
+constexpr int kJoinsPerBlock = 4;
 
 template <int J>
 __global__ void __launch_bounds__(C_WARPS * 32)
@@ -332,12 +333,21 @@ paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int c = blockIdx.x;
-    const int4 join = *reinterpret_cast<const int4*>(p.joins + c);
-    const int parts = join.x, b = join.y, unit = join.z, n_new = join.w;
-    if (parts == 0) return;
-    const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    // the words of this block's workers, all at once: most of them say that there is nothing
+    int4 joins[kJoinsPerBlock];
+#pragma unroll
+    for (int k = 0; k < kJoinsPerBlock; ++k) {
+        const int c = blockIdx.x + k * gridDim.x;
+        joins[k] = c < p.workers ? *reinterpret_cast<const int4*>(p.joins + c) : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll 1
+    for (int k = 0; k < kJoinsPerBlock; ++k) {
+    const int c = blockIdx.x + k * gridDim.x;
+    const int4 join = k == 0 ? joins[0] : k == 1 ? joins[1] : k == 2 ? joins[2] : joins[3];
+    const int parts = join.x, b = join.y, unit = join.z, n_new = join.w;
+    if (parts == 0) continue;
+    const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
     const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
     const int W = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : C_WARPS;
     const int sub = warp % W;
@@ -416,6 +426,7 @@ paged_combine_kernel(const PagedParams p) {
         if (live && sub == 0) paged_finish_row<J>(p, lam, b, x.h, x.q, lane, o[0], l[0], o[1], l[1]);
         if (W > 1) __syncthreads();
     }
+    }
 }
 
 template <typename T, int RC>
@@ -424,7 +435,7 @@ int launch_rc(const PagedParams& p, cudaStream_t stream) {
     if (cudaFuncSetAttribute(paged_simt_kernel<T, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) !=
         cudaSuccess)
         return -1;
-    paged_simt_kernel<T, RC><<<p.grid, THREADS, L.total, stream>>>(p);
+    paged_simt_kernel<T, RC><<<p.workers, THREADS, L.total, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
@@ -451,7 +462,7 @@ int paged_simt_rows(int64_t rows) {
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     // a block a row where few rows may have many parts, else four rows a block
-    cfg.gridDim = dim3((unsigned)p.grid, (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
+    cfg.gridDim = dim3((unsigned)((p.workers + paged::kJoinsPerBlock - 1) / paged::kJoinsPerBlock), (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
     cfg.blockDim = dim3(paged::C_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -69,7 +69,7 @@ int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream);
 void plan_rotary(RotaryParams* p, int num_sms);
 void plan_rotary_bwd(RotaryParams* p);
 
-// A unit that block c started and did not finish, for the merging pass: its parts are
+// A unit that worker c started and did not finish, for the merging pass: its parts are
 // in slots 2 c + 1, 2 (c + 1), ... 2 (c + parts - 1).  parts = 0: there is none.
 struct alignas(16) PagedJoin {
     int parts, b, unit, n_new;
@@ -108,9 +108,11 @@ struct PagedParams {
     int chunk_rows;
     int vec16;                  // rows of the caches are 16-byte aligned,
     int q16;                    // and of the queries
-    int grid;                   // blocks of the first pass
-    float* part;                // [2 * grid][chunk_rows][paged_part_floats(Dv)]
-    struct PagedJoin* joins;    // [grid] what the merging pass has to do
+    int o4;                     // output rows are 4-byte aligned
+    int solo;                   // units of up to 8 rows, which one warp can take alone
+    int workers;                // that share the first pass, at most
+    float* part;                // [2 * workers][chunk_rows][paged_part_floats(Dv)]
+    struct PagedJoin* joins;    // [workers] what the merging pass has to do
 };
 
 // Floats of one row's partial result: m_1, l_1, m_2, l_2, O_1 and O_2, each O's width
@@ -123,11 +125,11 @@ int launch_paged_simt(const PagedParams& p, cudaStream_t stream);
 int paged_simt_rows(int64_t rows);
 constexpr int kSimtBlocksPerSm = 3;
 // The tensor-core kernel of up to 16 rows a unit: maps of K1, K2 and V with boxes of
-// 64 columns x box_rows slots.
+// 64 columns x 16 slots.
 constexpr int kMmaRows = 16;
-constexpr int kMmaTile = 64;
-constexpr int kMmaBlocksPerSm = 2;
-int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream);
+constexpr int kMmaTile = 16;
+constexpr int kMmaWarps = 8;            // of an SM: as many workers, or one for each four
+int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream);
 // The tcgen05 kernel of up to 128 rows a unit: maps of K1, K2, V (boxes of 64 columns x
 // box_rows slots), Q1 and Q2 (boxes of 64 columns x q_box tokens).
 constexpr int kTcRows = 128;

@@ -5,15 +5,18 @@
 // Bound by HBM: a key costs 4 D + 256 bytes (2 D + 256 with shared keys) and 4 (D + 128)
 // operations a row, 192 FLOP a byte short of what the tensor cores could do even at 16
 // rows.  So the design is about never leaving the memory idle:
-//   - One producer warp streams the block's tiles of 64 keys through TMA into a ring
-//     that takes most of shared memory, across unit boundaries, two or more tiles ahead.
-//     A lane a page: box i of a tile is the part of it in one page.
-//   - Four consumer warps take 16 keys of each tile each, and run on their own: a warp
-//     keeps its own running maximum, sum and O (16 rows x 128 columns of both branches,
-//     128 registers a thread), so a tile needs no barrier but the ring's two.  They meet
-//     once a segment, when the four partial results are merged in the stage that was
-//     read last.
-//   - Two blocks an SM: one streams while the other starts or merges a segment.
+//   - A warp takes 16 keys at a time and keeps its rows' running maximum, sum and O (16
+//     rows x 128 columns of both branches, 128 registers a thread) for itself, so a tile
+//     needs no barrier.
+//   - A second warp streams its slices of 16 keys through TMA into a ring of its own,
+//     across unit boundaries.  A slice lies in one page.  Eight such pairs an SM keep 130
+//     to 190 KB in flight, more than the HBM rate times its latency.
+//   - With many units (a batch of short sequences) a worker is one warp, which writes its
+//     rows from its registers at a unit's end.  With few, four warps share a worker's
+//     tiles of 64 keys and merge their results in shared memory at its end, so that the
+//     merging pass has a quarter of the parts.  (2048 units of 100 keys: 78 us with four
+//     warps a worker, whose merge takes 2 us a unit, 51 with one.  16 units of 16384:
+//     33 us with four, 42 with one, the difference in the merging pass.)
 //   - The products are warp-level (m16n8k16): at this size they are a quarter of the
 //     time that the tile's bytes take, and P goes from the score's accumulators to the
 //     next product's operand in registers.  A tcgen05 product would want 128 keys as its
@@ -30,34 +33,42 @@
 namespace diffattn {
 namespace pmma {
 
-constexpr int CONSUMERS = 4;                    // warps
-// A second warpgroup for the producer (three of its warps idle), which gives registers to
-// the consumers: 128 x 216 + 128 x 40 = 256 x 128, what the block is launched with.
-constexpr int THREADS = 256;
-constexpr int BLOCKS_PER_SM = kMmaBlocksPerSm;
+constexpr int WARPS = kMmaWarps;                // pairs of warps; one block an SM
+constexpr int GROUP = 4;                        // warps that share a worker's tiles, where units are few
+// The producers' warpgroups give registers to the consumers': 256 x 216 + 256 x 40 =
+// 512 x 128, what the block is launched with.
+constexpr int THREADS = 2 * 32 * WARPS;
 constexpr uint32_t REGS_CONSUMER = 216, REGS_PRODUCER = 40;
-static_assert(128 * REGS_CONSUMER + 128 * REGS_PRODUCER <= THREADS * 128, "register split");
-constexpr int KT = kMmaTile;
-constexpr int SLICE = KT / CONSUMERS;           // keys of a warp
+static_assert(256 * REGS_CONSUMER + 256 * REGS_PRODUCER <= THREADS * 128, "register split");
+constexpr int KT = kMmaTile;                    // keys of a slice
 constexpr int NR = 16;                          // rows of a unit
+constexpr int WARP_ROWS = 8;                    // most rows of a unit where a worker is one warp
 constexpr int DV = 128;
-constexpr int PANEL = KT * 128;                 // 8 KB: 64 keys x 64 columns
+constexpr int PANEL = KT * 128;                 // 2 KB: 16 keys x 64 columns
+// Slices a worker of one warp takes at least, and tiles of four: fewer workers have fewer
+// parts to merge.  Slices or tiles at a unit's end that are not worth another part.
+constexpr int MIN_SLICES = 2, MIN_TILES = 1, SNAP_SLICES = 4, SNAP_TILES = 1;
 
+// Shared memory: a ring for each pair, the queries (one warp a worker: 8 rows a warp;
+// else 16 rows a group, and the maxima and sums of its warps), barriers.
 template <int HD, bool KS>
 struct Cfg {
     static constexpr int KP = HD / 64;                          // panels of a key tile
     static constexpr int NK = KS ? 1 : 2;
-    static constexpr int STAGE = (NK * KP + 2) * PANEL;         // 24, 32 or 48 KB
-    static constexpr int NST = 96 * 1024 / STAGE;
+    static constexpr int STAGE = (NK * KP + 2) * PANEL;         // 6, 8 or 12 KB
+    static constexpr int NST = 24 * 1024 / STAGE;               // 4, 3 or 2
+    static constexpr int RING = NST * STAGE;
     static constexpr int OFF_V = NK * KP * PANEL;
-    static constexpr int OFF_Q = NST * STAGE;                   // [branch][panel] 16 rows x 128 bytes
-    static constexpr int Q_PANEL = NR * 128;
-    static constexpr int OFF_STAT = OFF_Q + 2 * KP * Q_PANEL;   // float [warp][m, l][branch][row]
-    static constexpr int OFF_BAR = OFF_STAT + CONSUMERS * 2 * 2 * NR * 4;
-    static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;      // abort, bad flags by stage
-    static constexpr int SMEM = OFF_MISC + 64 + 1024;
-    static constexpr int ROUND = STAGE / CONSUMERS / (2 * DV * 4);  // rows merged at once
-    static_assert(BLOCKS_PER_SM * (SMEM + 256 + 1024) <= 228 * 1024, "shared memory");
+    static constexpr int Q_PANEL = NR * 128;                    // [branch][panel] 16 rows x 128 bytes of a group,
+    static constexpr int Q_WARP = 2 * KP * WARP_ROWS * 128;     // or 8 rows x 128 bytes of a warp
+    static constexpr int OFF_Q = WARPS * RING;
+    static constexpr int OFF_STAT = 2 * KP * Q_PANEL;           // behind a group's queries: float [warp][m, l][branch][row]
+    static constexpr int OFF_BAR = OFF_Q + WARPS * Q_WARP;      // [warp] full [NST], empty [NST]
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * 2 * NST * 8;  // abort, bad flags [warp][NST]
+    static constexpr int SMEM = OFF_MISC + 4 + WARPS * NST * 4 + 1024;
+    static constexpr int ROUND = STAGE / (2 * DV * 4);          // rows merged at once
+    static_assert(OFF_STAT + GROUP * 4 * NR * 4 <= GROUP * Q_WARP, "a group's queries and sums");
+    static_assert(SMEM + 512 <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -93,94 +104,114 @@ __device__ __forceinline__ uint32_t slice_mask(const PagedParams& p, const Paged
         m = off <= 0 ? (uint32_t)(tree >> -off) : ((uint32_t)tree << off) | ((1u << off) - 1);
     } else {
         const int64_t n = off + q + 1;
-        m = n <= 0 ? 0 : n >= SLICE ? 0xffffu : (1u << n) - 1;
+        m = n <= 0 ? 0 : n >= KT ? 0xffffu : (1u << n) - 1;
     }
     const int n = s.total - k0;
-    return m & (n >= SLICE ? 0xffffu : (1u << n) - 1);
+    return m & (n >= KT ? 0xffffu : (1u << n) - 1);
+}
+
+// The sum of v over the block, to every thread.
+__device__ __forceinline__ int block_sum(int v, int* scratch) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) sum += scratch[i];
+    __syncthreads();
+    return sum;
 }
 
 template <int HD, bool KS>
-__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM)
+__global__ void __launch_bounds__(THREADS, 1)
 paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
-                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int box_rows) {
+                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
     using C = Cfg<HD, KS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t scan[THREADS / 32 + 1];
-    __shared__ PagedStart start_s;
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sbase = smem_u32(smem);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty = full + C::NST;
-    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
-    volatile uint32_t* bad_stage = abort_flag + 1;              // [NST]
-    float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);
+    __shared__ int scan[THREADS / 32];
+    __shared__ PagedBlock<WARPS> blk;
+    uint8_t* smem_block = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_block + C::OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int w = warp % WARPS;                 // the pair
+    uint8_t* ring = smem_block + w * C::RING;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_block + C::OFF_BAR) + w * 2 * C::NST;
+    uint64_t* empty = full + C::NST;
+    volatile uint32_t* bad_stage = abort_flag + 1 + w * C::NST;
     const AbortState ab{abort_flag, p.status};
     pdl_launch_dependents();
-    if (tid == 0) {
-        for (int i = 0; i < C::NST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], CONSUMERS);
-            bad_stage[i] = 0;
-        }
-        *abort_flag = 0;
+    if (warp < WARPS && lane < C::NST) {
+        mbar_init(&full[lane], 1);
+        mbar_init(&empty[lane], 1);
+        bad_stage[lane] = 0;
+        if (tid == 0) *abort_flag = 0;
         fence_mbar_init();
     }
-    const PagedStart start = paged_start<THREADS>(p, KT, scan, &start_s);     // its barriers order the above
+    // one warp a worker where that makes at most two workers a unit, and if the unit's rows
+    // allow it (p.solo)
+    int active = 0;
+    if (p.solo)
+        for (int b = tid; b < p.B; b += THREADS) active += paged_seq(p, b).n_new != 0;
+    const bool solo = p.solo && (int64_t)block_sum(active, scan) * p.Hk * p.row_chunks * 2 >= p.workers;
+    const int kt = solo ? KT : GROUP * KT, snap = solo ? SNAP_SLICES : SNAP_TILES;
+    const int nw = solo ? WARPS : WARPS / GROUP;                // workers of the block
+    paged_start<THREADS, WARPS>(p, kt, nw, gridDim.x * nw, solo ? MIN_SLICES : MIN_TILES, snap, scan, &blk);
+    const int mine = solo ? w : w / GROUP;
+    const int worker = blockIdx.x * nw + mine;
+    const int first_key = solo ? 0 : w % GROUP * KT;            // of the warp's slice in a tile
     PagedCursor cur;
 
-    if (warp >= CONSUMERS) {
+    if (warp >= WARPS) {
         // ---------------------------------------------------------------- producer
         regs_dec<REGS_PRODUCER>();
-        if (warp > CONSUMERS) return;
-        cur.begin(p, start, KT);
+        cur.begin(p, blk, mine, worker, kt);
+        const bool scribe = lane == 0 && (solo || w % GROUP == 0);
         if (lane == 0) {
             tma_prefetch_desc(&tm_k1);
             tma_prefetch_desc(&tm_k2);
             tma_prefetch_desc(&tm_v);
         }
-        if (lane == 0) cur.no_join(p);
-        const int boxes = KT / box_rows;
-        uint32_t armed = 0;                     // tiles issued
+        if (scribe) {
+            PagedCursor::no_join(p, worker);
+            // one warp in four of these writes: the rest of the words, for workers that are not
+            if (!solo)
+                for (int c = gridDim.x * nw + worker; c < p.workers; c += gridDim.x * nw) PagedCursor::no_join(p, c);
+        }
+        uint32_t armed = 0;                     // slices issued
         int st = 0;
         uint32_t ph = 1;                        // the first pass over the ring finds it free
         bool ok = true;
-        for (; ok && !cur.done(); cur.next(p, KT)) {
-            const int live = cur.live_tiles(p, KT);
-            if (lane == 0) cur.join(p, start_s.total);
-            // the page of this lane's box, one tile ahead
-            auto look = [&](int i) -> int {
-                const int key = (cur.tile0 + i) * KT + lane * box_rows;
-                if (i >= live || lane >= boxes || key >= cur.s.total) return -2;        // nothing to load
-                return paged_page(p, cur.b, key / p.page);
-            };
-            int page = look(0);
+        for (; ok && !cur.done(); cur.next(p, kt)) {
+            const int live = cur.live_tiles(p, kt);
+            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, snap);
+            int page = 0;                       // of tile i0 + lane's slice, looked up 32 at a time
             for (int i = 0; i < live; ++i) {
-                const int now = page;
-                page = look(i + 1);
+                if ((i & 31) == 0) {
+                    const int key = (cur.tile0 + i + lane) * kt + first_key;
+                    page = -2;                  // nothing to load
+                    if (i + lane < live && key < cur.s.total) page = paged_page(p, cur.b, key / p.page);
+                }
+                const int now = __shfl_sync(0xffffffffu, page, i & 31);
                 if (!(ok = mbar_wait_warp(&empty[st], ph, ab))) break;
-                const unsigned have = __ballot_sync(0xffffffffu, now >= 0);
-                const bool bad = __any_sync(0xffffffffu, now == -1);
                 if (lane == 0) {
-                    if (bad) atomicOr(p.status, kStatusIndex);
-                    bad_stage[st] = bad;
-                    const uint32_t bytes = __popc(have) * box_rows * 128 * (C::NK * C::KP + 2);
-                    if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
-                    else mbar_arrive(&full[st]);
+                    bad_stage[st] = now == -1;
+                    if (now < 0) {
+                        if (now == -1) atomicOr(p.status, kStatusIndex);
+                        mbar_arrive(&full[st]);
+                    } else {
+                        mbar_arrive_expect_tx(&full[st], C::STAGE);
+                        const int slot = ((cur.tile0 + i) * kt + first_key) % p.page;
+                        uint8_t* dst = ring + st * C::STAGE;
+#pragma unroll
+                        for (int pn = 0; pn < C::KP; ++pn) {
+                            tma_load_4d(dst + pn * PANEL, &tm_k1, &full[st], pn * 64, slot, cur.hk, now);
+                            if (!KS) tma_load_4d(dst + (C::KP + pn) * PANEL, &tm_k2, &full[st], pn * 64, slot, cur.hk, now);
+                        }
+                        tma_load_4d(dst + C::OFF_V, &tm_v, &full[st], 0, slot, cur.hk, now);
+                        tma_load_4d(dst + C::OFF_V + PANEL, &tm_v, &full[st], 64, slot, cur.hk, now);
+                    }
                 }
                 __syncwarp();
-                if (now >= 0) {
-                    const int key = (cur.tile0 + i) * KT + lane * box_rows;
-                    const int slot = key % p.page;
-                    uint8_t* dst = smem + st * C::STAGE + lane * box_rows * 128;
-#pragma unroll
-                    for (int pn = 0; pn < C::KP; ++pn) {
-                        tma_load_4d(dst + pn * PANEL, &tm_k1, &full[st], pn * 64, slot, cur.hk, now);
-                        if (!KS) tma_load_4d(dst + (C::KP + pn) * PANEL, &tm_k2, &full[st], pn * 64, slot, cur.hk, now);
-                    }
-                    tma_load_4d(dst + C::OFF_V, &tm_v, &full[st], 0, slot, cur.hk, now);
-                    tma_load_4d(dst + C::OFF_V + PANEL, &tm_v, &full[st], 64, slot, cur.hk, now);
-                }
                 ++armed;
                 if (++st == C::NST) { st = 0; ph ^= 1; }
             }
@@ -193,48 +224,60 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 
     // -------------------------------------------------------------------- consumers
     regs_inc<REGS_CONSUMER>();
-    cur.begin(p, start, KT);
+    cur.begin(p, blk, mine, worker, kt);
     const float sl2 = p.scale_log2;
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
     const int r0 = lane >> 2;                   // this thread's rows r0 and r0 + 8
-    // lane addresses of the ldmatrix operands within the warp's 16 rows of a panel
-    const int krow = warp * SLICE + (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
-    const int vrow = warp * SLICE + (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
-    const int qrow = (lane & 7) + (((lane >> 3) & 1) << 3), qch = lane >> 4;
+    const int bar = 1 + w / GROUP;              // the group's barrier
+    // the worker's queries: [branch][panel] rows of 128 bytes
+    const int q_panel = solo ? WARP_ROWS * 128 : C::Q_PANEL;
+    uint8_t* qs = smem_block + C::OFF_Q + (solo ? w * C::Q_WARP : w / GROUP * GROUP * C::Q_WARP);
+    float* stat = reinterpret_cast<float*>(qs + C::OFF_STAT);   // of the group
+    // lane addresses of the ldmatrix operands; alone, rows 8 to 15 read rows 0 to 7 again
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
+    const int qrow = (lane & 7) + (solo ? 0 : ((lane >> 3) & 1) << 3), qch = lane >> 4;
+    const uint32_t sring = smem_u32(ring), sq = smem_u32(qs);
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;                             // after a failed wait: no more work, but every barrier
-    for (; !cur.done(); cur.next(p, KT)) {
-        const int live = cur.live_tiles(p, KT);
+    for (; !cur.done(); cur.next(p, kt)) {
+        const int live = cur.live_tiles(p, kt);
         const PagedSeq s = cur.s;
         bool bad = s.bad;
-        if (bad && tid == 0) atomicOr(p.status, kStatusIndex);
+        if (bad && lane == 0) atomicOr(p.status, kStatusIndex);
         // ---- the unit's queries, zeros for padding rows
-        for (int i = tid; i < NR * 2 * (HD / 8); i += 32 * CONSUMERS) {
-            const int c = i % (HD / 8), br = i / (HD / 8) & 1, r = i / (HD / 4);
-            const PagedRow x = paged_row(p, cur.hk, cur.rc, r, s.n_new);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (x.live && r < p.chunk_rows) {
-                const __nv_bfloat16* src =
-                    br ? static_cast<const __nv_bfloat16*>(p.q2) + cur.b * p.s_q2[0] + x.h * p.s_q2[1] + x.q * p.s_q2[2]
-                       : static_cast<const __nv_bfloat16*>(p.q1) + cur.b * p.s_q1[0] + x.h * p.s_q1[1] + x.q * p.s_q1[2];
-                src += c * 8;
-                if (p.q16) {
-                    w = *reinterpret_cast<const uint4*>(src);
-                } else {
-                    const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
-                    w = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                   e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+        {
+            constexpr int QCH = HD / 8;         // 16-byte chunks of a row
+            const int threads = solo ? 32 : GROUP * 32, t0 = solo ? lane : tid % (GROUP * 32);
+            const int c = t0 % (2 * QCH) % QCH, br = t0 % (2 * QCH) / QCH;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(br ? p.q2 : p.q1) + c * 8;
+            const int64_t sb = br ? p.s_q2[0] : p.s_q1[0], sh = br ? p.s_q2[1] : p.s_q1[1], sq_ = br ? p.s_q2[2] : p.s_q1[2];
+            src += cur.b * sb;
+            const int rows = solo ? WARP_ROWS : NR, step = threads / (2 * QCH);
+#pragma unroll 4
+            for (int r = t0 / (2 * QCH); r < rows; r += step) {
+                const PagedRow x = paged_row(p, cur.hk, cur.rc, r, s.n_new);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (x.live && r < p.chunk_rows) {
+                    const __nv_bfloat16* at = src + x.h * sh + x.q * sq_;
+                    if (p.q16) {
+                        v = *reinterpret_cast<const uint4*>(at);
+                    } else {
+                        const uint16_t* e = reinterpret_cast<const uint16_t*>(at);
+                        v = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                       e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                    }
                 }
+                *reinterpret_cast<uint4*>(qs + (br * C::KP + (c >> 3)) * q_panel + sw128(r, c & 7)) = v;
             }
-            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (br * C::KP + (c >> 3)) * C::Q_PANEL + sw128(r, c & 7)) = w;
         }
-        named_bar_sync(1, 32 * CONSUMERS);
+        if (solo) __syncwarp();
+        else named_bar_sync(bar, GROUP * 32);
         const PagedRow ra = paged_row(p, cur.hk, cur.rc, r0, s.n_new);
         const PagedRow rb = paged_row(p, cur.hk, cur.rc, r0 + 8, s.n_new);
         const bool la = ra.live && r0 < p.chunk_rows, lb = rb.live && r0 + 8 < p.chunk_rows;
         uint64_t ta = 0, tb = 0;
-        if (p.mask && (cur.tile0 + live) * KT > s.before) {
+        if (p.mask && (int64_t)(cur.tile0 + live) * kt > s.before) {
             if (la) ta = paged_mask_bits(p, cur.b, ra.q, s.n_new);
             if (lb) tb = paged_mask_bits(p, cur.b, rb.q, s.n_new);
         }
@@ -249,10 +292,11 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         }
         for (int i = 0; i < live; ++i) {
             ok = ok && mbar_wait_warp(&full[st], ph, ab);
-            if (bad_stage[st]) bad = true;
-            const int k0 = (cur.tile0 + i) * KT + warp * SLICE;
-            const uint32_t stage = sbase + st * C::STAGE;
-            if (ok && k0 < s.total) {
+            const int k0 = (cur.tile0 + i) * kt + first_key;
+            const uint32_t stage = sring + st * C::STAGE;
+            if (bad_stage[st]) {
+                bad = true;                     // nothing was loaded
+            } else if (ok && k0 < s.total) {
                 // ---- S_b = Q_b K_b^T, 16 rows x 16 keys
                 float sc[2][2][4];
 #pragma unroll
@@ -267,13 +311,13 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                         if (br == 0 || !KS)
                             ldsm4(stage + (br * C::KP + (kk >> 2)) * PANEL + sw128(krow, 2 * (kk & 3) + kch), kf);
                         uint32_t qf[4];         // read again for each slice: registers hold O
-                        ldsm4(sbase + C::OFF_Q + (br * C::KP + (kk >> 2)) * C::Q_PANEL + sw128(qrow, 2 * (kk & 3) + qch), qf);
+                        ldsm4(sq + (br * C::KP + (kk >> 2)) * q_panel + sw128(qrow, 2 * (kk & 3) + qch), qf);
                         mma16816(sc[br][0], qf, kf[0], kf[1]);
                         mma16816(sc[br][1], qf, kf[2], kf[3]);
                     }
                 }
                 // ---- P = 2^(S - m): element e of part n is row r0 + 8 (e >> 1), key 8 n + 2 (lane & 3) + (e & 1)
-                const bool edge = k0 + SLICE > s.before;
+                const bool edge = k0 + KT > s.before;
                 uint32_t seen[2] = {0xffffu, 0xffffu};
                 if (edge) {
                     seen[0] = slice_mask(p, s, k0, la, ra.q, ta);
@@ -332,7 +376,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     // Values that a row does not see may be anything, and the product's 0 x NaN
                     // is NaN.  Rows past the end become zeros; elsewhere a value that is not
                     // finite is taken out of the tile and added here to the rows that see it.
-                    uint8_t* vt = smem + st * C::STAGE + C::OFF_V + warp * SLICE * 128;
+                    uint8_t* vt = ring + st * C::STAGE + C::OFF_V;
                     for (int j = 0; j < 8; ++j) {
                         const int key = 2 * j + (lane >> 4), c = lane & 15;
                         uint8_t* at = vt + (c >> 3) * PANEL + sw128(key, c & 7);
@@ -396,107 +440,189 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     }
                 }
             }
-            if (i + 1 < live) {                 // the segment's last stage is freed after the merge
+            if (solo || i + 1 < live) {         // a group's last stage is freed after its merge
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
                 if (++st == C::NST) { st = 0; ph ^= 1; }
             }
         }
-        // ---- merge the warps: their maxima and sums, then O in rounds of ROUND rows through
-        // the stage that was read last
 #pragma unroll
         for (int br = 0; br < 2; ++br)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float x = l[br][h];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (bad) x = __int_as_float(0x7fc00000);
-                if ((lane & 3) == 0) {
-                    stat[(warp * 2 + 0) * 2 * NR + br * NR + r0 + 8 * h] = m[br][h];
-                    stat[(warp * 2 + 1) * 2 * NR + br * NR + r0 + 8 * h] = x;
-                }
+                l[br][h] += __shfl_xor_sync(0xffffffffu, l[br][h], 1);
+                l[br][h] += __shfl_xor_sync(0xffffffffu, l[br][h], 2);
+                if (bad || !ok) l[br][h] = __int_as_float(0x7fc00000);
             }
-        named_bar_sync(1, 32 * CONSUMERS);      // every warp is done with the stage, too
-        // Unscaled: this runs once a segment, cold, so it costs by its instructions.
-        float* buf = reinterpret_cast<float*>(smem + st * C::STAGE);     // [warp][row of the round][branch][DV]
-        for (int row0 = 0; row0 < p.chunk_rows; row0 += C::ROUND) {
+        if (!solo) {
+            // ---- merge the group's warps: their maxima and sums, then O in rounds of ROUND
+            // rows through the stages that were read last.  Cold code, once a segment: it
+            // costs by its instructions, so O goes out unscaled.
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = r0 + 8 * h - row0;
-                if (live == 0 || r < 0 || r >= C::ROUND || !(h ? lb : la)) continue;
-                float* dst = buf + (warp * C::ROUND + r) * 2 * DV + 2 * (lane & 3);
+            for (int br = 0; br < 2; ++br)
 #pragma unroll
-                for (int br = 0; br < 2; ++br)
-#pragma unroll
-                    for (int n = 0; n < DV / 8; ++n)
-                        *reinterpret_cast<float2*>(dst + br * DV + 8 * n) = make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
-            }
-            named_bar_sync(1, 32 * CONSUMERS);
-            for (int r = warp; r < C::ROUND && row0 + r < p.chunk_rows; r += CONSUMERS) {
-                const PagedRow x = paged_row(p, cur.hk, cur.rc, row0 + r, s.n_new);
-                if (!x.live) continue;
-                float mt[2], lt[2], wt[2][CONSUMERS], a[2][DV / 32];
-#pragma unroll
-                for (int br = 0; br < 2; ++br) {
-                    const float* ms = stat + br * NR + row0 + r;
-                    mt[br] = fmaxf(fmaxf(ms[0], ms[4 * NR]), fmaxf(ms[8 * NR], ms[12 * NR]));
-                    lt[br] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < CONSUMERS; ++w) {
-                        const float mw = ms[w * 4 * NR], lw = ms[(w * 4 + 2) * NR];
-                        wt[br][w] = mw == -INFINITY ? 0.f : ex2_approx(mw - mt[br]);
-                        lt[br] += mw == -INFINITY ? lw : lw * wt[br][w];       // 0 or NaN where nothing was seen
+                for (int h = 0; h < 2; ++h)
+                    if ((lane & 3) == 0) {
+                        stat[(w % GROUP * 2 + 0) * 2 * NR + br * NR + r0 + 8 * h] = m[br][h];
+                        stat[(w % GROUP * 2 + 1) * 2 * NR + br * NR + r0 + 8 * h] = l[br][h];
                     }
+            // [row of the round][branch][DV], each warp's in its own ring
+            float* buf = reinterpret_cast<float*>(ring + st * C::STAGE);
+            // where the group's warps have theirs: all have walked as many stages
+            const float* bufs = reinterpret_cast<const float*>(smem_block + w / GROUP * GROUP * C::RING + st * C::STAGE);
+            for (int row0 = 0; row0 < p.chunk_rows; row0 += C::ROUND) {
 #pragma unroll
-                    for (int j = 0; j < DV / 32; ++j) a[br][j] = 0.f;
-                }
-                if (live > 0) {
-#pragma unroll
-                    for (int w = 0; w < CONSUMERS; ++w)
-#pragma unroll
-                        for (int br = 0; br < 2; ++br)
-#pragma unroll
-                            for (int j = 0; j < DV / 32; ++j)
-                                a[br][j] = fmaf(wt[br][w], buf[((w * C::ROUND + r) * 2 + br) * DV + lane + 32 * j], a[br][j]);
-                }
-                if (cur.whole()) {
-                    paged_finish_row<DV / 32>(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
-                } else {
-                    float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row0 + r) * (4 + 2 * DV);
-                    if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(mt[0], lt[0], mt[1], lt[1]);
+                for (int h = 0; h < 2; ++h) {
+                    const int r = r0 + 8 * h - row0;
+                    if (live == 0 || r < 0 || r >= C::ROUND || !(h ? lb : la)) continue;
+                    float* dst = buf + r * 2 * DV + 2 * (lane & 3);
 #pragma unroll
                     for (int br = 0; br < 2; ++br)
 #pragma unroll
-                        for (int j = 0; j < DV / 32; ++j) part[4 + br * DV + lane + 32 * j] = a[br][j];
+                        for (int n = 0; n < DV / 8; ++n)
+                            *reinterpret_cast<float2*>(dst + br * DV + 8 * n) = make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
+                }
+                named_bar_sync(bar, GROUP * 32);
+                for (int r = w % GROUP; r < C::ROUND && row0 + r < p.chunk_rows; r += GROUP) {
+                    const PagedRow x = paged_row(p, cur.hk, cur.rc, row0 + r, s.n_new);
+                    if (!x.live) continue;
+                    float mt[2], lt[2], wt[2][GROUP], a[2][DV / 32];
+#pragma unroll
+                    for (int br = 0; br < 2; ++br) {
+                        const float* ms = stat + br * NR + row0 + r;
+                        mt[br] = fmaxf(fmaxf(ms[0], ms[4 * NR]), fmaxf(ms[8 * NR], ms[12 * NR]));
+                        lt[br] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < GROUP; ++k) {
+                            const float mw = ms[k * 4 * NR], lw = ms[(k * 4 + 2) * NR];
+                            wt[br][k] = mw == -INFINITY ? 0.f : ex2_approx(mw - mt[br]);
+                            lt[br] += mw == -INFINITY ? lw : lw * wt[br][k];       // 0 or NaN where nothing was seen
+                        }
+#pragma unroll
+                        for (int j = 0; j < DV / 32; ++j) a[br][j] = 0.f;
+                    }
+                    if (live > 0) {
+#pragma unroll
+                        for (int k = 0; k < GROUP; ++k)
+#pragma unroll
+                            for (int br = 0; br < 2; ++br)
+#pragma unroll
+                                for (int j = 0; j < DV / 32; ++j)
+                                    a[br][j] = fmaf(wt[br][k], bufs[k * (C::RING / 4) + (r * 2 + br) * DV + lane + 32 * j], a[br][j]);
+                    }
+                    if (cur.whole()) {
+                        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+                        paged_finish_row<DV / 32>(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
+                    } else {
+                        float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row0 + r) * paged_part_floats(DV);
+                        if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(mt[0], lt[0], mt[1], lt[1]);
+#pragma unroll
+                        for (int br = 0; br < 2; ++br)
+#pragma unroll
+                            for (int j = 0; j < DV / 32; ++j) part[4 + br * DV + lane + 32 * j] = a[br][j];
+                    }
+                }
+                fence_proxy_async_smem();       // before TMA writes the stages again
+                named_bar_sync(bar, GROUP * 32);
+            }
+            if (live > 0) {
+                if (lane == 0) mbar_arrive(&empty[st]);
+                if (++st == C::NST) { st = 0; ph ^= 1; }
+            }
+            continue;
+        }
+        // ---- alone: the rows out of the registers, finished, or as a partial result
+        const bool whole = cur.whole();
+        {
+            constexpr int h = 0;                // up to 8 rows
+            const bool live_row = la;
+            if (!whole) {
+                float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + r0 + 8 * h) * paged_part_floats(DV);
+                if (live_row) {
+                    if ((lane & 3) == 0) *reinterpret_cast<float4*>(part) = make_float4(m[0][h], l[0][h], m[1][h], l[1][h]);
+#pragma unroll
+                    for (int br = 0; br < 2; ++br)
+#pragma unroll
+                        for (int n = 0; n < DV / 8; ++n)
+                            *reinterpret_cast<float2*>(part + 4 + br * DV + 8 * n + 2 * (lane & 3)) =
+                                make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
+                }
+                __syncwarp();                   // before the next unit's queries overwrite these
+                continue;
+            }
+            const PagedRow x = ra;
+            const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+            const float i1 = l[0][h] == 0.f ? 0.f : 1.f / l[0][h], i2 = l[1][h] == 0.f ? 0.f : 1.f / l[1][h];
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < DV / 8; ++n)
+#pragma unroll
+                for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                    o[0][n][e] = fmaf(-lam, __fmul_rn(o[1][n][e], i2), __fmul_rn(o[0][n][e], i1));
+                    sum += o[0][n][e];
+                }
+            if (p.norm != kNormNone) {          // of the row's four threads
+                float mean = 0.f, ss = 0.f;
+                if (p.norm == kNormGroup) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    mean = sum / DV;
+                }
+#pragma unroll
+                for (int n = 0; n < DV / 8; ++n)
+#pragma unroll
+                    for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                        o[0][n][e] -= mean;
+                        ss = fmaf(o[0][n][e], o[0][n][e], ss);
+                    }
+                ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+                ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+                const float r = 1.0f / sqrtf(ss / DV + p.norm_eps);
+#pragma unroll
+                for (int n = 0; n < DV / 8; ++n) {
+                    o[0][n][2 * h] *= r;
+                    o[0][n][2 * h + 1] *= r;
                 }
             }
-            fence_proxy_async_smem();
-            named_bar_sync(1, 32 * CONSUMERS);
+            const int64_t at = cur.b * p.s_o[0] + x.h * p.s_o[1] + x.q * p.s_o[2] + 2 * (lane & 3);
+            const int64_t ch = (int64_t)x.h * DV + 2 * (lane & 3);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+            if (live_row)
+#pragma unroll
+            for (int n = 0; n < DV / 8; ++n) {
+                float y0 = o[0][n][2 * h], y1 = o[0][n][2 * h + 1];
+                if (p.norm_weight) { y0 *= p.norm_weight[ch + 8 * n]; y1 *= p.norm_weight[ch + 8 * n + 1]; }
+                if (p.norm_bias) { y0 += p.norm_bias[ch + 8 * n]; y1 += p.norm_bias[ch + 8 * n + 1]; }
+                y0 *= p.out_scale;
+                y1 *= p.out_scale;
+                if (p.o4) {
+                    *reinterpret_cast<uint32_t*>(out + 8 * n) = pack_bf16x2(y0, y1);
+                } else {
+                    out[8 * n] = __float2bfloat16_rn(y0);
+                    out[8 * n + 1] = __float2bfloat16_rn(y1);
+                }
+            }
         }
-        if (live > 0) {
-            if (lane == 0) mbar_arrive(&empty[st]);
-            if (++st == C::NST) { st = 0; ph ^= 1; }
-        }
+        __syncwarp();                           // before the next unit's queries overwrite these
     }
 }
 
 template <int HD, bool KS>
-int launch_hd(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream) {
+int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
     constexpr int smem = Cfg<HD, KS>::SMEM;
     if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    paged_mma_kernel<HD, KS><<<p.grid, THREADS, smem, stream>>>(maps[0], maps[1], maps[2], p, box_rows);
+    paged_mma_kernel<HD, KS><<<p.workers / (p.solo ? WARPS : WARPS / GROUP), THREADS, smem, stream>>>(maps[0], maps[1], maps[2], p);
     return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
 }
 
 }  // namespace pmma
 
-int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, int box_rows, cudaStream_t stream) {
-    if (p.D == 64) return p.k_shared ? pmma::launch_hd<64, true>(maps, p, box_rows, stream)
-                                     : pmma::launch_hd<64, false>(maps, p, box_rows, stream);
-    return p.k_shared ? pmma::launch_hd<128, true>(maps, p, box_rows, stream)
-                      : pmma::launch_hd<128, false>(maps, p, box_rows, stream);
+int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
+    if (p.D == 64) return p.k_shared ? pmma::launch_hd<64, true>(maps, p, stream)
+                                     : pmma::launch_hd<64, false>(maps, p, stream);
+    return p.k_shared ? pmma::launch_hd<128, true>(maps, p, stream)
+                      : pmma::launch_hd<128, false>(maps, p, stream);
 }
 
 }  // namespace diffattn

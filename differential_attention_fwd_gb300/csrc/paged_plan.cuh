@@ -1,16 +1,19 @@
 // paged_plan.cuh -- how the attention over a paged cache is cut into work, shared by
 // its kernels and the pass that merges their partial results.
 //
-// The lengths are on the device, so the host launches a fixed grid and every block
-// finds its own share.  A unit is (sequence, key/value head, row chunk) with the
-// sequence's tiles of KT keys; the units' tiles are laid end to end, sequence by
-// sequence, and of `total` tiles block c takes c * total / G .. (c + 1) * total / G,
-// G = min(grid, total): equal to within one tile, whatever the lengths.  A block's
-// range falls into segments, each of one unit.  A segment that holds its whole unit
-// is finished by its block; one that does not leaves a partial result: in slot
-// 2 c + 1 if the unit starts in it (it is then the block's last), else in slot 2 c
-// (the block's first).  So the workspace grows with the grid and not with the batch,
-// and the merging pass takes one block a boundary.
+// The lengths are on the device, so the host launches a fixed number of workers (blocks,
+// groups of warps, or warps) and every one finds its own share.  A unit is (sequence,
+// key/value head, row chunk) with the sequence's tiles of KT keys; the units' tiles are
+// laid end to end, sequence by sequence, and of `total` tiles every worker takes
+// total / G in a row, or one more, whatever the lengths; G is all workers, or fewer so
+// that each has min_tiles.  A boundary that falls within `snap` tiles of a unit's end
+// moves there: so little work is not worth a unit in two parts.
+//
+// A worker's range falls into segments, each of one unit.  A segment that holds its whole
+// unit is finished by its worker; one that does not leaves a partial result: in slot
+// 2 c + 1 if the unit starts in it (it is then the worker's last), else in slot 2 c (the
+// worker's first).  So the workspace grows with the workers and not with the batch, and a
+// merging pass has at most one unit a worker to join.
 #pragma once
 
 #include "kernels.h"
@@ -46,7 +49,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
     return s;
 }
 
-__device__ __forceinline__ int64_t paged_seq_tiles(const PagedSeq& s, int kt) { return (s.total + kt - 1) / kt; }
+__device__ __forceinline__ int paged_seq_tiles(const PagedSeq& s, int kt) { return (s.total + kt - 1) / kt; }
 
 // The page of a key's slot, or -1 if its table entry is out of range.  `key` is below
 // the sequence's total, so the entry exists.
@@ -55,78 +58,124 @@ __device__ __forceinline__ int paged_page(const PagedParams& p, int b, int index
     return pg >= 0 && pg < p.num_pages ? pg : -1;
 }
 
-struct PagedStart {
-    int64_t total;      // tiles of all units
-    int64_t first;      // the block's first tile,
-    int b;              // its sequence, and
-    int64_t local;      // its place among the sequence's tiles
+// The division of a launch.  All counts are below 2^31 (checked on the host).
+struct PagedShares {
+    int total;          // tiles of all units
+    int workers;        // that take tiles
+    int each, more;     // `more` of them take each + 1 tiles, the others each
+    __device__ __forceinline__ void set(int t, int most, int min_tiles) {
+        total = t;
+        workers = min(most, max(t / min_tiles, t > 0 ? 1 : 0));
+        each = workers ? t / workers : 0;
+        more = t - each * workers;
+    }
+    // Where worker c's share begins before it is moved to a unit's end; `total` for a
+    // worker that takes none.
+    __device__ __forceinline__ int bound(int c) const { return c < workers ? c * each + min(c, more) : total; }
+    // The last worker whose share begins at `tile` or before.
+    __device__ __forceinline__ int worker_at(int tile) const {
+        const int turn = more * (each + 1);
+        return tile < turn ? tile / (each + 1) : more + (tile - turn) / each;
+    }
 };
 
-// Every thread of the block calls this; `scratch` holds THREADS / 32 + 1 int64_t and
-// a PagedStart in shared memory.
-template <int THREADS>
-__device__ __forceinline__ PagedStart paged_start(const PagedParams& p, int kt, int64_t* scratch, PagedStart* result) {
+// Where a worker's range starts: the launch's tile, its sequence, and its place among the
+// sequence's tiles (all of them: the range starts with the next sequence that has any).
+struct PagedStart {
+    int tile, b, local;
+};
+
+// What a block knows of its workers, in shared memory.
+template <int NW>
+struct PagedBlock {
+    PagedShares shares;
+    PagedStart start[NW + 1];       // of its workers, and of the one after them
+};
+
+// Every thread of the block calls this.  `scratch`: THREADS / 32 ints in shared memory.
+// `nw` <= NW: workers of this block.
+template <int THREADS, int NW>
+__device__ __forceinline__ void paged_start(const PagedParams& p, int kt, int nw, int most, int min_tiles, int snap,
+                                            int* scratch, PagedBlock<NW>* out) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t units = (int64_t)p.Hk * p.row_chunks;
+    const int units = p.Hk * p.row_chunks;
     const int per = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = b0; b < b1; ++b) sum += paged_seq_tiles(paged_seq(p, b), kt) * units;
-    int64_t incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    int64_t at = before + incl - sum;          // tiles before this thread's sequences
-    const int64_t grid = total < gridDim.x ? total : (int64_t)gridDim.x;
-    const int64_t first = blockIdx.x < grid ? blockIdx.x * total / grid : total;
-    if (tid == 0) *result = PagedStart{total, total, p.B, 0};
-    __syncthreads();
-    for (int b = b0; b < b1; ++b) {
-        const int64_t n = paged_seq_tiles(paged_seq(p, b), kt) * units;
-        if (first >= at && first < at + n) *result = PagedStart{total, first, b, first - at};
-        at += n;
+    const int at0 = before + incl - sum;        // tiles before this thread's sequences
+    PagedShares sh;
+    sh.set(total, most, min_tiles);
+    if (tid == 0) out->shares = sh;
+    if (tid <= nw && sh.bound(blockIdx.x * nw + tid) >= total) out->start[tid] = PagedStart{total, p.B, 0};
+    for (int w = 0; w <= nw; ++w) {
+        const int first = sh.bound(blockIdx.x * nw + w);
+        if (first >= total || first < at0 || first >= at0 + sum) continue;
+        int at = at0;
+        for (int b = b0; b < b1; ++b) {
+            const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+            if (first < at + tiles * units) {
+                const int off = (first - at) % tiles;       // in its unit
+                const int move = off <= snap ? -off : tiles - off <= snap ? tiles - off : 0;
+                out->start[w] = PagedStart{first + move, b, first + move - at};
+                break;
+            }
+            at += tiles * units;
+        }
     }
     __syncthreads();
-    return *result;
 }
 
-// A block's segments in turn.
+// A worker's segments in turn.
 struct PagedCursor {
-    int64_t left;               // tiles of the block's range not yet handed out
-    int local;                  // place among the sequence's tiles (fewer than 2^31: checked on the host)
-    int b, unit;                // unit of the sequence (hk * row_chunks + row chunk)
-    int hk, rc;
+    int left;                   // tiles of the worker's range not yet handed out
+    int local;                  // place among the sequence's tiles
+    int worker;
+    int b;
+    int hk, rc;                 // the segment's unit: key/value head and row chunk
     int tile0, n;               // the segment's tiles within the unit
     int tiles;                  // the unit's
     PagedSeq s;
 
-    __device__ __forceinline__ void begin(const PagedParams& p, const PagedStart& st, int kt) {
-        const int64_t grid = st.total < gridDim.x ? st.total : (int64_t)gridDim.x;
-        left = blockIdx.x < grid ? (blockIdx.x + 1) * st.total / grid - st.first : 0;
-        b = st.b;
-        local = (int)st.local;
-        if (left > 0) load(p, kt);
-    }
-    __device__ __forceinline__ void load(const PagedParams& p, int kt) {
+    // The `w`-th worker of the block, worker c of the launch.
+    template <int NW>
+    __device__ __forceinline__ void begin(const PagedParams& p, const PagedBlock<NW>& blk, int w, int c, int kt) {
+        worker = c;
+        left = blk.start[w + 1].tile - blk.start[w].tile;
+        b = blk.start[w].b;
+        local = blk.start[w].local;
+        if (left <= 0) return;
         s = paged_seq(p, b);
-        tiles = (int)paged_seq_tiles(s, kt);
-        cut(p);
+        tiles = paged_seq_tiles(s, kt);
+        enter(p, kt);
     }
-    __device__ __forceinline__ void cut(const PagedParams& p) {
-        unit = local / tiles;
+    __device__ __forceinline__ void enter(const PagedParams& p, int kt) {
+        if (local == tiles * p.Hk * p.row_chunks) {
+            local = 0;
+            do {
+                if (++b >= p.B) { left = 0; return; }   // never with tiles left
+                s = paged_seq(p, b);
+            } while (s.n_new == 0);
+            tiles = paged_seq_tiles(s, kt);
+        }
+        const int unit = local / tiles;
         tile0 = local - unit * tiles;
-        n = (int)(left < tiles - tile0 ? left : tiles - tile0);
+        n = min(left, tiles - tile0);
         hk = unit / p.row_chunks;
         rc = unit - hk * p.row_chunks;
     }
@@ -134,33 +183,19 @@ struct PagedCursor {
     __device__ __forceinline__ void next(const PagedParams& p, int kt) {
         left -= n;
         local += n;
-        if (left <= 0) return;
-        if (local == tiles * p.Hk * p.row_chunks) {
-            local = 0;
-            do {
-                if (++b >= p.B) { left = 0; return; }   // never with tiles left
-                s = paged_seq(p, b);
-            } while (s.n_new == 0);
-            tiles = (int)paged_seq_tiles(s, kt);
-        }
-        cut(p);
+        if (left > 0) enter(p, kt);
     }
     __device__ __forceinline__ bool whole() const { return n == tiles; }
-    __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0); }
-    // One thread of the block, at each of its segments and once before them: leaves word
-    // for the merging pass.  The unit's last tile is in the block before the first one
-    // that begins at its end or later.
-    __device__ __forceinline__ void no_join(const PagedParams& p) const { p.joins[blockIdx.x].parts = 0; }
-    __device__ __forceinline__ void join(const PagedParams& p, int64_t total) const {
+    __device__ __forceinline__ int slot() const { return 2 * worker + (tile0 == 0 ? 1 : 0); }
+    // One thread of the worker, at each of its segments, and no_join once before them:
+    // leaves word for the merging pass.  A unit that starts here and does not end here is
+    // this range's last, and the workers that go on with it are those whose bounds fall
+    // into it and were not moved to its ends.  `end`: where this range ends.
+    __device__ __forceinline__ static void no_join(const PagedParams& p, int c) { p.joins[c].parts = 0; }
+    __device__ __forceinline__ void join(const PagedParams& p, const PagedShares& sh, int end, int snap) const {
         if (tile0 != 0 || whole()) return;
-        const int64_t grid = total < gridDim.x ? total : (int64_t)gridDim.x;
-        // the block's range ends with this segment: the unit goes on at tile `end` of the
-        // launch, and ends `rest` tiles later
-        const int64_t end = (int64_t)(blockIdx.x + 1) * total / grid, last = end + (tiles - n) - 1;
-        int64_t c = last * grid / total;                // a block that begins at `last` or before
-        while (c + 1 < grid && (c + 1) * total / grid <= last) ++c;
-        while (c * total / grid > last) --c;
-        p.joins[blockIdx.x] = PagedJoin{(int)(c - blockIdx.x) + 1, b, unit, s.n_new};
+        const int u1 = end - n + tiles;
+        p.joins[worker] = PagedJoin{sh.worker_at(u1 - snap - 1) - worker + 1, b, hk * p.row_chunks + rc, s.n_new};
     }
     // The segment's tiles that some row of its chunk may see: later ones hold only
     // keys behind the chunk's last query.
@@ -194,7 +229,13 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int hk, int 
 __device__ __forceinline__ uint64_t paged_mask_bits(const PagedParams& p, int b, int q, int n_new) {
     const uint8_t* m = p.mask + b * p.mask_stride[0] + q * p.mask_stride[1];
     uint64_t bits = 0;
-    for (int j = 0; j < n_new; ++j) bits |= (uint64_t)(m[j] != 0) << j;
+    // 16 loads at a time: one after another their latencies would add up
+    for (int j0 = 0; j0 < n_new; j0 += 16) {
+        uint32_t part = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part |= (uint32_t)(j0 + j < n_new ? m[j0 + j] != 0 : 0) << j;
+        bits |= (uint64_t)part << j0;
+    }
     return bits;
 }
 

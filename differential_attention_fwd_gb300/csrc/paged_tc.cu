@@ -39,6 +39,7 @@ using tc::tile_row_max;
 constexpr int BM = 128;
 constexpr int KT = 64;
 constexpr int DV = 128;
+constexpr int SNAP = 3;
 constexpr int THREADS = 384;
 // launched at 168 registers a thread: 256 x 200 + 128 x 104 = 384 x 168
 constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
@@ -97,6 +98,17 @@ __device__ __forceinline__ uint32_t tm_s(int br, int buf) { return br * 128 + bu
 
 __device__ __forceinline__ bool bf16_finite(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
 
+// A bf16 pair with zeros for what is not finite.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    if (!bf16_finite(w)) w &= 0xffff0000u;
+    if (!bf16_finite(w >> 16)) w &= 0x0000ffffu;
+    return w;
+}
+// 16-byte chunk c (of 16) of a key's value row in a staged tile.
+__device__ __forceinline__ uint4* value_at(uint8_t* vt, int key, int c) {
+    return reinterpret_cast<uint4*>(vt + (c >> 3) * K_PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+}
+
 // Bits of the 64 keys from k0 on that a row sees (bit d of `tree`: new token d).
 __device__ __forceinline__ uint64_t tile_mask(const PagedParams& p, const PagedSeq& s, int k0, int q, uint64_t tree) {
     auto low = [](int64_t n) -> uint64_t { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
@@ -114,8 +126,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int box_rows, const int q_box) {
     using C = Cfg<HD, KS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t scan[THREADS / 32 + 1];
-    __shared__ PagedStart start_s;
+    __shared__ int scan[THREADS / 32];
+    __shared__ PagedBlock<1> blk;
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + REL_TMEM);
@@ -150,7 +162,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         tmem_relinquish();
     }
     tc_fence_before();
-    const PagedStart start = paged_start<THREADS>(p, KT, scan, &start_s);     // with its barriers
+    paged_start<THREADS, 1>(p, KT, 1, p.workers, 1, SNAP, scan, &blk);     // with its barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
     const uint64_t lim = 200ull * 1000ull * 1000ull;
@@ -158,7 +170,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
 
     if (warp >= 8) {
         regs_dec<REGS_OTHER>();
-        cur.begin(p, start, KT);
+        cur.begin(p, blk, 0, blockIdx.x, KT);
         if (warp == 8) {
             // ------------------------------------------------------------ producer
             if (lane == 0) {
@@ -172,12 +184,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             const int boxes = KT / box_rows;
             uint32_t kst = 0, kph = 1, vst = 0, vph = 1, nk = 0, nv = 0, nq = 0;
             bool ok = true;
-            if (lane == 0) cur.no_join(p);
+            if (lane == 0) PagedCursor::no_join(p, blockIdx.x);
             int seg = -1;                       // segments with tiles, as every role counts them
             for (; ok && !cur.done(); cur.next(p, KT)) {
                 const int live = cur.live_tiles(p, KT);
                 if (cur.s.bad && lane == 0) atomicOr(p.status, kStatusIndex);
-                if (lane == 0) cur.join(p, start_s.total);
+                if (lane == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP);
                 if (live == 0) continue;
                 ++seg;
                 if (lane == 0) bad_seg[seg % SEGS] = 0;
@@ -288,24 +300,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                     if (!(ok = mbar_wait_warp(&bars[B_V_FULL + vst], vph, ab))) break;
                     if (tile >= edge0) {
                         uint8_t* vt = smem + C::OFF_V + vst * V_BYTES;
+                        // eight reads at a time; what is found is almost always nothing
                         uint32_t lo = 0, hi = 0;            // keys with a value that is not finite
-                        for (int j = 0; j < KT / 2; ++j) {
-                            const int key = 2 * j + (int)(lane >> 4), c = lane & 15;
-                            uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * K_PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-                            const uint4 x = *at;
-                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            const bool past = tile * KT + key >= cur.s.total;
-                            bool odd = false;
+                        for (int j0 = 0; j0 < KT / 2; j0 += 8) {
+                            uint4 x[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (!bf16_finite(w[e])) { odd = true; w[e] &= 0xffff0000u; }
-                                if (!bf16_finite(w[e] >> 16)) { odd = true; w[e] &= 0x0000ffffu; }
-                            }
-                            if (past) *at = make_uint4(0, 0, 0, 0);
-                            else if (odd) *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (odd && !past) {
-                                if (key < 32) lo |= 1u << key;
-                                else hi |= 1u << (key - 32);
+                            for (int j = 0; j < 8; ++j)
+                                x[j] = *value_at(vt, 2 * (j0 + j) + (int)(lane >> 4), lane & 15);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int key = 2 * (j0 + j) + (int)(lane >> 4);
+                                const bool past = tile * KT + key >= cur.s.total;
+                                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                                bool odd = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) odd |= !bf16_finite(w[e]) | !bf16_finite(w[e] >> 16);
+                                if (past) {
+                                    *value_at(vt, key, lane & 15) = make_uint4(0, 0, 0, 0);
+                                } else if (odd) {
+                                    *value_at(vt, key, lane & 15) = make_uint4(finite_only(w[0]), finite_only(w[1]),
+                                                                               finite_only(w[2]), finite_only(w[3]));
+                                    if (key < 32) lo |= 1u << key;
+                                    else hi |= 1u << (key - 32);
+                                }
                             }
                         }
                         lo = __reduce_or_sync(0xffffffffu, lo);
@@ -399,7 +416,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     } else {
         // ------------------------------------------------------ weights and results
         regs_inc<REGS_SOFTMAX>();
-        cur.begin(p, start, KT);
+        cur.begin(p, blk, 0, blockIdx.x, KT);
         const int br = warp >> 2;
         const uint32_t quad = warp & 3;
         const int row = quad * 32 + lane;
@@ -546,6 +563,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 if (lane == 0) mbar_arrive(&bars[B_ROWS_OUT]);
                 if (!(ok = mbar_wait_warp(&bars[B_ROWS_OUT], wph, ab))) break;
                 wph ^= 1;
+#pragma unroll 2
                 for (int r = warp; r < p.chunk_rows; r += 8) {
                     const PagedRow y = paged_row(p, cur.hk, cur.rc, r, s.n_new);
                     if (!y.live) continue;
@@ -575,7 +593,7 @@ int launch_hd(const CUtensorMap* m, const PagedParams& p, int box_rows, int q_bo
     constexpr uint32_t smem = smem_bytes<HD, KS>();
     if (cudaFuncSetAttribute(paged_tc_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return -1;
-    paged_tc_kernel<HD, KS><<<p.grid, THREADS, smem, stream>>>(m[3], m[4], m[0], m[1], m[2], p, box_rows, q_box);
+    paged_tc_kernel<HD, KS><<<p.workers, THREADS, smem, stream>>>(m[3], m[4], m[0], m[1], m[2], p, box_rows, q_box);
     return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
 }
 
