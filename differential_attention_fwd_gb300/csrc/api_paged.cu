@@ -190,7 +190,7 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
     n->row_chunks = (int)((rows + kMmaRows - 1) / kMmaRows);
     n->chunk_rows = (int)((rows + n->row_chunks - 1) / n->row_chunks);
     n->tile = kMmaTile;
-    n->workers = sms * (n->chunk_rows <= 8 ? kMmaWarps : kMmaWarps / 4);
+    n->workers = sms * kMmaBlocks * (n->chunk_rows <= paged_solo_rows((int)d.D) ? kMmaWarps : 1);
     n->bytes = part_bytes(*n, 128);
 }
 
@@ -443,10 +443,11 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.chunk_rows = n.chunk_rows;
     p.row_chunks = n.row_chunks;
     p.workers = n.workers;
-    p.solo = n.chunk_rows <= 8;
+    p.sparse_joins = tc && !tcgen && n.chunk_rows <= paged_solo_rows(p.D);
+    p.solo_workers = sms * kMmaBlocks * kMmaWarps;
     if (tc) {
         // boxes that stay inside one page and divide the tile
-        int box = n.tile;
+        int box = tcgen ? kTcTile : 16;          // a slice of the 16-row kernel
         while (p.page % box != 0) box /= 2;
         CUtensorMap maps[5];
         const int64_t kd[4] = {p.D, p.page, p.Hk, p.num_pages}, vd[4] = {p.Dv, p.page, p.Hk, p.num_pages};

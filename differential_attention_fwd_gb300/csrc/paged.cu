@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(THREADS)
 paged_simt_kernel(const PagedParams p) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int scan[WARPS];
+    __shared__ int scan[2 * WARPS];
     __shared__ PagedBlock<1> blk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.D, Dv = p.Dv;
@@ -95,7 +95,7 @@ paged_simt_kernel(const PagedParams p) {
     float* st_l = st_m + 2 * RC;
     float* st_a = st_l + 2 * RC;
     pdl_launch_dependents();
-    paged_start<THREADS, 1>(p, KT, 1, p.workers, 1, SNAP, scan, &blk);
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, scan), KT, 1, p.workers, 1, SNAP, &blk);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
@@ -364,11 +364,32 @@ paged_combine_kernel(const PagedParams p) {
 #pragma unroll
         for (int j = 0; j < J; ++j) o[0][j] = o[1][j] = 0.f;
         if (live) {
+            // Loads first, and all that fit: the pass is the latency of L2, met once if no
+            // load waits for another's value.  So no branch on a weight either (a part that
+            // saw nothing holds zeros).
+            constexpr int AHEAD = 4;
+            float x[AHEAD][2][J];
+            float4 st[AHEAD];
+            auto load = [&](int i, int k) {
+                const float* src = part_of(min(i, parts - 1));
+                st[k] = *reinterpret_cast<const float4*>(src);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int col = min(lane + 32 * j, p.Dv - 1);
+                    x[k][0][j] = src[4 + col];
+                    x[k][1][j] = src[4 + width + col];
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) load(sub + k * W, k);
             float m[2] = {-INFINITY, -INFINITY};
-            for (int i = lane; i < parts; i += 32) {
-                const float4 st = *reinterpret_cast<const float4*>(part_of(i));
-                m[0] = fmaxf(m[0], st.x);
-                m[1] = fmaxf(m[1], st.z);
+            const float4 own = *reinterpret_cast<const float4*>(part_of(min(lane, parts - 1)));
+            m[0] = own.x;
+            m[1] = own.z;
+            for (int i = lane + 32; i < parts; i += 32) {
+                const float4 s4 = *reinterpret_cast<const float4*>(part_of(i));
+                m[0] = fmaxf(m[0], s4.x);
+                m[1] = fmaxf(m[1], s4.z);
             }
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) {
@@ -378,33 +399,29 @@ paged_combine_kernel(const PagedParams p) {
             // where nothing was seen m_i is -inf, and l_i 0 (or NaN: a bad page) as it is
             const float m1 = m[0] == -INFINITY ? 0.f : m[0], m2 = m[1] == -INFINITY ? 0.f : m[1];
             for (int i = lane; i < parts; i += 32) {
-                const float4 st = *reinterpret_cast<const float4*>(part_of(i));
-                l[0] += st.y * (st.x == -INFINITY ? 1.f : exp2f(st.x - m1));
-                l[1] += st.w * (st.z == -INFINITY ? 1.f : exp2f(st.z - m2));
+                const float4 s4 = i < 32 ? own : *reinterpret_cast<const float4*>(part_of(i));
+                l[0] += s4.y * (s4.x == -INFINITY ? 1.f : exp2f(s4.x - m1));
+                l[1] += s4.w * (s4.z == -INFINITY ? 1.f : exp2f(s4.z - m2));
             }
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) {
                 l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
                 l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
             }
-            // no branch on the weight: the loads of all columns and of several parts go
-            // out together (a part that saw nothing holds zeros)
-#pragma unroll 4
-            for (int i = sub; i < parts; i += W) {
-                const float* src = part_of(i);
-                float x[2][J];
+            for (int i = sub; i < parts; i += AHEAD * W) {
+                if (i > sub) {
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int col = min(lane + 32 * j, p.Dv - 1);
-                    x[0][j] = src[4 + col];
-                    x[1][j] = src[4 + width + col];
+                    for (int k = 0; k < AHEAD; ++k) load(i + k * W, k);
                 }
-                const float4 st = *reinterpret_cast<const float4*>(src);
-                const float w1 = exp2f(st.x - m1), w2 = exp2f(st.z - m2);
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    o[0][j] = fmaf(w1, x[0][j], o[0][j]);
-                    o[1][j] = fmaf(w2, x[1][j], o[1][j]);
+                for (int k = 0; k < AHEAD; ++k) {
+                    if (i + k * W >= parts) continue;
+                    const float w1 = exp2f(st[k].x - m1), w2 = exp2f(st[k].z - m2);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        o[0][j] = fmaf(w1, x[k][0][j], o[0][j]);
+                        o[1][j] = fmaf(w2, x[k][1][j], o[1][j]);
+                    }
                 }
             }
         }
@@ -462,7 +479,9 @@ int paged_simt_rows(int64_t rows) {
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     // a block a row where few rows may have many parts, else four rows a block
-    cfg.gridDim = dim3((unsigned)((p.workers + paged::kJoinsPerBlock - 1) / paged::kJoinsPerBlock), (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
+    // one word a block, but where most workers may not exist (paged_mma.cu)
+    const int words = p.sparse_joins ? paged::kJoinsPerBlock : 1;
+    cfg.gridDim = dim3((unsigned)((p.workers + words - 1) / words), (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
     cfg.blockDim = dim3(paged::C_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -109,8 +109,9 @@ struct PagedParams {
     int vec16;                  // rows of the caches are 16-byte aligned,
     int q16;                    // and of the queries
     int o4;                     // output rows are 4-byte aligned
-    int solo;                   // units of up to 8 rows, which one warp can take alone
+    int solo_workers;           // warps of the launch: one is a worker where units are many
     int workers;                // that share the first pass, at most
+    int sparse_joins;           // a quarter of them may be all there are
     float* part;                // [2 * workers][chunk_rows][paged_part_floats(Dv)]
     struct PagedJoin* joins;    // [workers] what the merging pass has to do
 };
@@ -127,8 +128,11 @@ constexpr int kSimtBlocksPerSm = 3;
 // The tensor-core kernel of up to 16 rows a unit: maps of K1, K2 and V with boxes of
 // 64 columns x 16 slots.
 constexpr int kMmaRows = 16;
-constexpr int kMmaTile = 16;
-constexpr int kMmaWarps = 8;            // of an SM: as many workers, or one for each four
+constexpr int kMmaTile = 64;
+constexpr int kMmaWarps = 4;            // of a block: as many workers, or one
+constexpr int kMmaBlocks = 2;           // an SM
+// Most rows of a unit that one warp takes alone (their queries are in its shared memory).
+__host__ __device__ constexpr int paged_solo_rows(int D) { return D == 64 ? 8 : 4; }
 int launch_paged_mma(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream);
 // The tcgen05 kernel of up to 128 rows a unit: maps of K1, K2, V (boxes of 64 columns x
 // box_rows slots), Q1 and Q2 (boxes of 64 columns x q_box tokens).

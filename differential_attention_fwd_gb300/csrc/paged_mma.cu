@@ -9,8 +9,11 @@
 //     rows x 128 columns of both branches, 128 registers a thread) for itself, so a tile
 //     needs no barrier.
 //   - A second warp streams its slices of 16 keys through TMA into a ring of its own,
-//     across unit boundaries.  A slice lies in one page.  Eight such pairs an SM keep 130
-//     to 190 KB in flight, more than the HBM rate times its latency.
+//     across unit boundaries.  A slice lies in one page.  Two blocks of four such pairs
+//     an SM keep 130 to 190 KB in flight, more than the HBM rate times its latency.
+//   - SMs stream at different rates (the slowest 20 % behind the fastest), so there are
+//     more blocks than fit at once, and an SM that is done sooner gets another; the other
+//     block of the SM streams while it starts.
 //   - With many units (a batch of short sequences) a worker is one warp, which writes its
 //     rows from its registers at a unit's end.  With few, four warps share a worker's
 //     tiles of 64 keys and merge their results in shared memory at its end, so that the
@@ -33,24 +36,21 @@
 namespace diffattn {
 namespace pmma {
 
-constexpr int WARPS = kMmaWarps;                // pairs of warps; one block an SM
-constexpr int GROUP = 4;                        // warps that share a worker's tiles, where units are few
-// The producers' warpgroups give registers to the consumers': 256 x 216 + 256 x 40 =
-// 512 x 128, what the block is launched with.
+constexpr int WARPS = kMmaWarps;                // pairs of warps of a block; two blocks an SM
+// The producers' warpgroup gives registers to the consumers': 128 x 216 + 128 x 40 =
+// 256 x 128, what the block is launched with.
 constexpr int THREADS = 2 * 32 * WARPS;
 constexpr uint32_t REGS_CONSUMER = 216, REGS_PRODUCER = 40;
-static_assert(256 * REGS_CONSUMER + 256 * REGS_PRODUCER <= THREADS * 128, "register split");
-constexpr int KT = kMmaTile;                    // keys of a slice
+static_assert(128 * REGS_CONSUMER + 128 * REGS_PRODUCER <= THREADS * 128, "register split");
+constexpr int KT = kMmaTile;                    // keys of a tile: four slices
+constexpr int SLICE = 16;
 constexpr int NR = 16;                          // rows of a unit
-constexpr int WARP_ROWS = 8;                    // most rows of a unit where a worker is one warp
 constexpr int DV = 128;
-constexpr int PANEL = KT * 128;                 // 2 KB: 16 keys x 64 columns
-// Slices a worker of one warp takes at least, and tiles of four: fewer workers have fewer
-// parts to merge.  Slices or tiles at a unit's end that are not worth another part.
-constexpr int MIN_SLICES = 2, MIN_TILES = 1, SNAP_SLICES = 4, SNAP_TILES = 1;
+constexpr int PANEL = SLICE * 128;              // 2 KB: 16 keys x 64 columns
+constexpr int SNAP = 1;                         // tiles at a unit's end that are not worth another part
 
-// Shared memory: a ring for each pair, the queries (one warp a worker: 8 rows a warp;
-// else 16 rows a group, and the maxima and sums of its warps), barriers.
+// Shared memory: a ring for each pair, the queries (one warp a worker: WARP_ROWS a warp;
+// else 16 rows of the block, and the maxima and sums of its warps), barriers.
 template <int HD, bool KS>
 struct Cfg {
     static constexpr int KP = HD / 64;                          // panels of a key tile
@@ -59,16 +59,17 @@ struct Cfg {
     static constexpr int NST = 24 * 1024 / STAGE;               // 4, 3 or 2
     static constexpr int RING = NST * STAGE;
     static constexpr int OFF_V = NK * KP * PANEL;
-    static constexpr int Q_PANEL = NR * 128;                    // [branch][panel] 16 rows x 128 bytes of a group,
-    static constexpr int Q_WARP = 2 * KP * WARP_ROWS * 128;     // or 8 rows x 128 bytes of a warp
+    static constexpr int WARP_ROWS = paged_solo_rows(HD);
+    static constexpr int Q_PANEL = NR * 128;                    // [branch][panel] 16 rows x 128 bytes of the block,
+    static constexpr int Q_WARP = 2 * KP * WARP_ROWS * 128;     // or WARP_ROWS x 128 bytes of a warp
     static constexpr int OFF_Q = WARPS * RING;
-    static constexpr int OFF_STAT = 2 * KP * Q_PANEL;           // behind a group's queries: float [warp][m, l][branch][row]
-    static constexpr int OFF_BAR = OFF_Q + WARPS * Q_WARP;      // [warp] full [NST], empty [NST]
+    static constexpr int OFF_STAT = OFF_Q + WARPS * Q_WARP;     // float [warp][m, l][branch][row]
+    static constexpr int OFF_BAR = OFF_STAT + WARPS * 4 * NR * 4;   // [warp] full [NST], empty [NST]
     static constexpr int OFF_MISC = OFF_BAR + WARPS * 2 * NST * 8;  // abort, bad flags [warp][NST]
     static constexpr int SMEM = OFF_MISC + 4 + WARPS * NST * 4 + 1024;
     static constexpr int ROUND = STAGE / (2 * DV * 4);          // rows merged at once
-    static_assert(OFF_STAT + GROUP * 4 * NR * 4 <= GROUP * Q_WARP, "a group's queries and sums");
-    static_assert(SMEM + 512 <= 232448, "shared memory");
+    static_assert(2 * KP * Q_PANEL <= WARPS * Q_WARP, "the block's queries");
+    static_assert(2 * (SMEM + 512 + 1024) <= 228 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -104,31 +105,19 @@ __device__ __forceinline__ uint32_t slice_mask(const PagedParams& p, const Paged
         m = off <= 0 ? (uint32_t)(tree >> -off) : ((uint32_t)tree << off) | ((1u << off) - 1);
     } else {
         const int64_t n = off + q + 1;
-        m = n <= 0 ? 0 : n >= KT ? 0xffffu : (1u << n) - 1;
+        m = n <= 0 ? 0 : n >= SLICE ? 0xffffu : (1u << n) - 1;
     }
     const int n = s.total - k0;
-    return m & (n >= KT ? 0xffffu : (1u << n) - 1);
-}
-
-// The sum of v over the block, to every thread.
-__device__ __forceinline__ int block_sum(int v, int* scratch) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) sum += scratch[i];
-    __syncthreads();
-    return sum;
+    return m & (n >= SLICE ? 0xffffu : (1u << n) - 1);
 }
 
 template <int HD, bool KS>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 2)
 paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
     using C = Cfg<HD, KS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int scan[THREADS / 32];
+    __shared__ int scan[2 * THREADS / 32];
     __shared__ PagedBlock<WARPS> blk;
     uint8_t* smem_block = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_block + C::OFF_MISC);
@@ -147,25 +136,23 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         if (tid == 0) *abort_flag = 0;
         fence_mbar_init();
     }
-    // one warp a worker where that makes at most two workers a unit, and if the unit's rows
-    // allow it (p.solo)
-    int active = 0;
-    if (p.solo)
-        for (int b = tid; b < p.B; b += THREADS) active += paged_seq(p, b).n_new != 0;
-    const bool solo = p.solo && (int64_t)block_sum(active, scan) * p.Hk * p.row_chunks * 2 >= p.workers;
-    const int kt = solo ? KT : GROUP * KT, snap = solo ? SNAP_SLICES : SNAP_TILES;
-    const int nw = solo ? WARPS : WARPS / GROUP;                // workers of the block
-    paged_start<THREADS, WARPS>(p, kt, nw, gridDim.x * nw, solo ? MIN_SLICES : MIN_TILES, snap, scan, &blk);
-    const int mine = solo ? w : w / GROUP;
+    // One warp a worker where that makes at most two workers a unit, and if the unit's rows
+    // allow it.  (The barriers in here order the above.)
+    const PagedScan found = paged_scan<THREADS>(p, KT, scan);
+    const bool solo = p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
+    const int nw = solo ? WARPS : 1;                            // workers of the block
+    paged_locate<WARPS>(p, found, KT, nw, gridDim.x * nw, 1, SNAP, &blk);
+    const int mine = solo ? w : 0;
     const int worker = blockIdx.x * nw + mine;
-    const int first_key = solo ? 0 : w % GROUP * KT;            // of the warp's slice in a tile
+    // the warp's slices in a tile: all four, or one
+    const int slices = solo ? KT / SLICE : 1, slice0 = solo ? 0 : w;
     PagedCursor cur;
 
     if (warp >= WARPS) {
         // ---------------------------------------------------------------- producer
         regs_dec<REGS_PRODUCER>();
-        cur.begin(p, blk, mine, worker, kt);
-        const bool scribe = lane == 0 && (solo || w % GROUP == 0);
+        cur.begin(p, blk, mine, worker, KT);
+        const bool scribe = lane == 0 && (solo || w == 0);
         if (lane == 0) {
             tma_prefetch_desc(&tm_k1);
             tma_prefetch_desc(&tm_k2);
@@ -173,21 +160,23 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         }
         if (scribe) {
             PagedCursor::no_join(p, worker);
-            // one warp in four of these writes: the rest of the words, for workers that are not
+            // the words of workers that there are not
             if (!solo)
-                for (int c = gridDim.x * nw + worker; c < p.workers; c += gridDim.x * nw) PagedCursor::no_join(p, c);
+                for (int c = gridDim.x + worker; c < p.workers; c += gridDim.x) PagedCursor::no_join(p, c);
         }
         uint32_t armed = 0;                     // slices issued
         int st = 0;
         uint32_t ph = 1;                        // the first pass over the ring finds it free
         bool ok = true;
-        for (; ok && !cur.done(); cur.next(p, kt)) {
-            const int live = cur.live_tiles(p, kt);
-            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, snap);
-            int page = 0;                       // of tile i0 + lane's slice, looked up 32 at a time
+        for (; ok && !cur.done(); cur.next(p, KT)) {
+            const int live = cur.live_tiles(p, KT) * slices;
+            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, SNAP);
+            int page = 0;                       // of slice i0 + lane, looked up 32 at a time
             for (int i = 0; i < live; ++i) {
+                // slice i of the warp: the key it starts with
+                auto key_of = [&](int k) { return solo ? cur.tile0 * KT + k * SLICE : (cur.tile0 + k) * KT + slice0 * SLICE; };
                 if ((i & 31) == 0) {
-                    const int key = (cur.tile0 + i + lane) * kt + first_key;
+                    const int key = key_of(i + lane);
                     page = -2;                  // nothing to load
                     if (i + lane < live && key < cur.s.total) page = paged_page(p, cur.b, key / p.page);
                 }
@@ -200,7 +189,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                         mbar_arrive(&full[st]);
                     } else {
                         mbar_arrive_expect_tx(&full[st], C::STAGE);
-                        const int slot = ((cur.tile0 + i) * kt + first_key) % p.page;
+                        const int slot = key_of(i) % p.page;
                         uint8_t* dst = ring + st * C::STAGE;
 #pragma unroll
                         for (int pn = 0; pn < C::KP; ++pn) {
@@ -224,36 +213,35 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 
     // -------------------------------------------------------------------- consumers
     regs_inc<REGS_CONSUMER>();
-    cur.begin(p, blk, mine, worker, kt);
+    cur.begin(p, blk, mine, worker, KT);
     const float sl2 = p.scale_log2;
     const int r0 = lane >> 2;                   // this thread's rows r0 and r0 + 8
-    const int bar = 1 + w / GROUP;              // the group's barrier
     // the worker's queries: [branch][panel] rows of 128 bytes
-    const int q_panel = solo ? WARP_ROWS * 128 : C::Q_PANEL;
-    uint8_t* qs = smem_block + C::OFF_Q + (solo ? w * C::Q_WARP : w / GROUP * GROUP * C::Q_WARP);
-    float* stat = reinterpret_cast<float*>(qs + C::OFF_STAT);   // of the group
-    // lane addresses of the ldmatrix operands; alone, rows 8 to 15 read rows 0 to 7 again
+    const int q_panel = solo ? C::WARP_ROWS * 128 : C::Q_PANEL;
+    uint8_t* qs = smem_block + C::OFF_Q + (solo ? w * C::Q_WARP : 0);
+    float* stat = reinterpret_cast<float*>(smem_block + C::OFF_STAT);
+    // lane addresses of the ldmatrix operands; alone, the other rows read the first ones again
     const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
     const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
-    const int qrow = (lane & 7) + (solo ? 0 : ((lane >> 3) & 1) << 3), qch = lane >> 4;
+    const int qrow = solo ? lane & (C::WARP_ROWS - 1) : (lane & 7) + (((lane >> 3) & 1) << 3), qch = lane >> 4;
     const uint32_t sring = smem_u32(ring), sq = smem_u32(qs);
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;                             // after a failed wait: no more work, but every barrier
-    for (; !cur.done(); cur.next(p, kt)) {
-        const int live = cur.live_tiles(p, kt);
+    for (; !cur.done(); cur.next(p, KT)) {
+        const int live = cur.live_tiles(p, KT) * slices;
         const PagedSeq s = cur.s;
         bool bad = s.bad;
         if (bad && lane == 0) atomicOr(p.status, kStatusIndex);
         // ---- the unit's queries, zeros for padding rows
         {
             constexpr int QCH = HD / 8;         // 16-byte chunks of a row
-            const int threads = solo ? 32 : GROUP * 32, t0 = solo ? lane : tid % (GROUP * 32);
+            const int threads = solo ? 32 : WARPS * 32, t0 = solo ? lane : tid;
             const int c = t0 % (2 * QCH) % QCH, br = t0 % (2 * QCH) / QCH;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(br ? p.q2 : p.q1) + c * 8;
             const int64_t sb = br ? p.s_q2[0] : p.s_q1[0], sh = br ? p.s_q2[1] : p.s_q1[1], sq_ = br ? p.s_q2[2] : p.s_q1[2];
             src += cur.b * sb;
-            const int rows = solo ? WARP_ROWS : NR, step = threads / (2 * QCH);
+            const int rows = solo ? C::WARP_ROWS : NR, step = threads / (2 * QCH);
 #pragma unroll 4
             for (int r = t0 / (2 * QCH); r < rows; r += step) {
                 const PagedRow x = paged_row(p, cur.hk, cur.rc, r, s.n_new);
@@ -272,12 +260,12 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             }
         }
         if (solo) __syncwarp();
-        else named_bar_sync(bar, GROUP * 32);
+        else named_bar_sync(1, WARPS * 32);
         const PagedRow ra = paged_row(p, cur.hk, cur.rc, r0, s.n_new);
         const PagedRow rb = paged_row(p, cur.hk, cur.rc, r0 + 8, s.n_new);
         const bool la = ra.live && r0 < p.chunk_rows, lb = rb.live && r0 + 8 < p.chunk_rows;
         uint64_t ta = 0, tb = 0;
-        if (p.mask && (int64_t)(cur.tile0 + live) * kt > s.before) {
+        if (p.mask && (int64_t)(cur.tile0 + cur.n) * KT > s.before) {
             if (la) ta = paged_mask_bits(p, cur.b, ra.q, s.n_new);
             if (lb) tb = paged_mask_bits(p, cur.b, rb.q, s.n_new);
         }
@@ -292,7 +280,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         }
         for (int i = 0; i < live; ++i) {
             ok = ok && mbar_wait_warp(&full[st], ph, ab);
-            const int k0 = (cur.tile0 + i) * kt + first_key;
+            const int k0 = solo ? cur.tile0 * KT + i * SLICE : (cur.tile0 + i) * KT + slice0 * SLICE;
             const uint32_t stage = sring + st * C::STAGE;
             if (bad_stage[st]) {
                 bad = true;                     // nothing was loaded
@@ -317,7 +305,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     }
                 }
                 // ---- P = 2^(S - m): element e of part n is row r0 + 8 (e >> 1), key 8 n + 2 (lane & 3) + (e & 1)
-                const bool edge = k0 + KT > s.before;
+                const bool edge = k0 + SLICE > s.before;
                 uint32_t seen[2] = {0xffffu, 0xffffu};
                 if (edge) {
                     seen[0] = slice_mask(p, s, k0, la, ra.q, ta);
@@ -440,7 +428,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     }
                 }
             }
-            if (solo || i + 1 < live) {         // a group's last stage is freed after its merge
+            if (solo || i + 1 < live) {         // a shared unit's last stage is freed after its merge
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
                 if (++st == C::NST) { st = 0; ph ^= 1; }
@@ -455,7 +443,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                 if (bad || !ok) l[br][h] = __int_as_float(0x7fc00000);
             }
         if (!solo) {
-            // ---- merge the group's warps: their maxima and sums, then O in rounds of ROUND
+            // ---- merge the block's warps: their maxima and sums, then O in rounds of ROUND
             // rows through the stages that were read last.  Cold code, once a segment: it
             // costs by its instructions, so O goes out unscaled.
 #pragma unroll
@@ -463,13 +451,13 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if ((lane & 3) == 0) {
-                        stat[(w % GROUP * 2 + 0) * 2 * NR + br * NR + r0 + 8 * h] = m[br][h];
-                        stat[(w % GROUP * 2 + 1) * 2 * NR + br * NR + r0 + 8 * h] = l[br][h];
+                        stat[(w * 2 + 0) * 2 * NR + br * NR + r0 + 8 * h] = m[br][h];
+                        stat[(w * 2 + 1) * 2 * NR + br * NR + r0 + 8 * h] = l[br][h];
                     }
             // [row of the round][branch][DV], each warp's in its own ring
             float* buf = reinterpret_cast<float*>(ring + st * C::STAGE);
-            // where the group's warps have theirs: all have walked as many stages
-            const float* bufs = reinterpret_cast<const float*>(smem_block + w / GROUP * GROUP * C::RING + st * C::STAGE);
+            // where the others have theirs: all have walked as many stages
+            const float* bufs = reinterpret_cast<const float*>(smem_block + st * C::STAGE);
             for (int row0 = 0; row0 < p.chunk_rows; row0 += C::ROUND) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -482,18 +470,18 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                         for (int n = 0; n < DV / 8; ++n)
                             *reinterpret_cast<float2*>(dst + br * DV + 8 * n) = make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
                 }
-                named_bar_sync(bar, GROUP * 32);
-                for (int r = w % GROUP; r < C::ROUND && row0 + r < p.chunk_rows; r += GROUP) {
+                named_bar_sync(1, WARPS * 32);
+                for (int r = w; r < C::ROUND && row0 + r < p.chunk_rows; r += WARPS) {
                     const PagedRow x = paged_row(p, cur.hk, cur.rc, row0 + r, s.n_new);
                     if (!x.live) continue;
-                    float mt[2], lt[2], wt[2][GROUP], a[2][DV / 32];
+                    float mt[2], lt[2], wt[2][WARPS], a[2][DV / 32];
 #pragma unroll
                     for (int br = 0; br < 2; ++br) {
                         const float* ms = stat + br * NR + row0 + r;
                         mt[br] = fmaxf(fmaxf(ms[0], ms[4 * NR]), fmaxf(ms[8 * NR], ms[12 * NR]));
                         lt[br] = 0.f;
 #pragma unroll
-                        for (int k = 0; k < GROUP; ++k) {
+                        for (int k = 0; k < WARPS; ++k) {
                             const float mw = ms[k * 4 * NR], lw = ms[(k * 4 + 2) * NR];
                             wt[br][k] = mw == -INFINITY ? 0.f : ex2_approx(mw - mt[br]);
                             lt[br] += mw == -INFINITY ? lw : lw * wt[br][k];       // 0 or NaN where nothing was seen
@@ -503,7 +491,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     }
                     if (live > 0) {
 #pragma unroll
-                        for (int k = 0; k < GROUP; ++k)
+                        for (int k = 0; k < WARPS; ++k)
 #pragma unroll
                             for (int br = 0; br < 2; ++br)
 #pragma unroll
@@ -523,7 +511,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     }
                 }
                 fence_proxy_async_smem();       // before TMA writes the stages again
-                named_bar_sync(bar, GROUP * 32);
+                named_bar_sync(1, WARPS * 32);
             }
             if (live > 0) {
                 if (lane == 0) mbar_arrive(&empty[st]);
@@ -610,9 +598,11 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 template <int HD, bool KS>
 int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
     constexpr int smem = Cfg<HD, KS>::SMEM;
+    // workers are warps where one warp may be one
+    const int blocks = p.workers / (p.chunk_rows <= Cfg<HD, KS>::WARP_ROWS ? WARPS : 1);
     if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    paged_mma_kernel<HD, KS><<<p.workers / (p.solo ? WARPS : WARPS / GROUP), THREADS, smem, stream>>>(maps[0], maps[1], maps[2], p);
+    paged_mma_kernel<HD, KS><<<blocks, THREADS, smem, stream>>>(maps[0], maps[1], maps[2], p);
     return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
 }
 

@@ -92,42 +92,69 @@ struct PagedBlock {
     PagedStart start[NW + 1];       // of its workers, and of the one after them
 };
 
-// Every thread of the block calls this.  `scratch`: THREADS / 32 ints in shared memory.
-// `nw` <= NW: workers of this block.
-template <int THREADS, int NW>
-__device__ __forceinline__ void paged_start(const PagedParams& p, int kt, int nw, int most, int min_tiles, int snap,
-                                            int* scratch, PagedBlock<NW>* out) {
+// The tiles and active units before and in each thread's sequences.  Every thread of the
+// block calls this; `scratch`: 2 * THREADS / 32 ints in shared memory.
+struct PagedScan {
+    int b0, b1;         // the thread's sequences,
+    int at, sum;        // the tiles before them and in them
+    int total, units;   // of the launch
+};
+template <int THREADS>
+__device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, int* scratch) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int units = p.Hk * p.row_chunks;
+    const int per_seq = p.Hk * p.row_chunks;
     const int per = (p.B + THREADS - 1) / THREADS;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += paged_seq_tiles(paged_seq(p, b), kt) * units;
-    int incl = sum;
+    PagedScan s;
+    s.b0 = min(p.B, tid * per);
+    s.b1 = min(p.B, s.b0 + per);
+    s.sum = 0;
+    int active = 0;
+    for (int b = s.b0; b < s.b1; ++b) {
+        const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+        s.sum += tiles * per_seq;
+        active += tiles ? per_seq : 0;
+    }
+    int incl = s.sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31) scratch[warp] = incl;
+    active = __reduce_add_sync(0xffffffffu, active);
+    if (lane == 31) {
+        scratch[warp] = incl;
+        scratch[WARPS + warp] = active;
+    }
     __syncthreads();
-    int before = 0, total = 0;
+    int before = 0;
+    s.total = s.units = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += scratch[w];
-        total += scratch[w];
+        s.total += scratch[w];
+        s.units += scratch[WARPS + w];
     }
-    const int at0 = before + incl - sum;        // tiles before this thread's sequences
+    s.at = before + incl - s.sum;
+    return s;
+}
+
+// Where the block's `nw` <= NW workers start, of `most` in the launch, and the one after.
+// Every thread calls this, and it ends with a barrier.
+template <int NW>
+__device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedScan& s, int kt, int nw, int most,
+                                             int min_tiles, int snap, PagedBlock<NW>* out) {
+    const int tid = threadIdx.x;
+    const int units = p.Hk * p.row_chunks;
     PagedShares sh;
-    sh.set(total, most, min_tiles);
+    sh.set(s.total, most, min_tiles);
     if (tid == 0) out->shares = sh;
-    if (tid <= nw && sh.bound(blockIdx.x * nw + tid) >= total) out->start[tid] = PagedStart{total, p.B, 0};
+    if (tid <= nw && sh.bound(blockIdx.x * nw + tid) >= s.total) out->start[tid] = PagedStart{s.total, p.B, 0};
     for (int w = 0; w <= nw; ++w) {
         const int first = sh.bound(blockIdx.x * nw + w);
-        if (first >= total || first < at0 || first >= at0 + sum) continue;
-        int at = at0;
-        for (int b = b0; b < b1; ++b) {
+        if (first >= s.total || first < s.at || first >= s.at + s.sum) continue;
+        int at = s.at;
+        for (int b = s.b0; b < s.b1; ++b) {
             const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
             if (first < at + tiles * units) {
                 const int off = (first - at) % tiles;       // in its unit

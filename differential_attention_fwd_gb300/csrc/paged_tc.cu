@@ -126,7 +126,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int box_rows, const int q_box) {
     using C = Cfg<HD, KS>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int scan[THREADS / 32];
+    __shared__ int scan[2 * THREADS / 32];
     __shared__ PagedBlock<1> blk;
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -162,7 +162,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_start<THREADS, 1>(p, KT, 1, p.workers, 1, SNAP, scan, &blk);     // with its barriers
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, scan), KT, 1, p.workers, 1, SNAP, &blk);    // with their barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
     const uint64_t lim = 200ull * 1000ull * 1000ull;
