@@ -176,7 +176,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_decode_workspace_bytes.argtypes = [ctypes.POINTER(DiffattnKvDesc)]
     lib.diffattn_decode_workspace_bytes.restype = ctypes.c_size_t
-    # these take their descriptors as packed bytes too (see _paged.py)
+    # (called from csrc/binding.cpp; here for tests of the ABI)
     lib.diffattn_rotary.argtypes = [vp] * 15
     lib.diffattn_rotary.restype = ctypes.c_int
     lib.diffattn_rotary_bwd.argtypes = [vp] * 21 + [ctypes.c_size_t, vp]

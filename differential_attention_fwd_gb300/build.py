@@ -5,6 +5,10 @@ into differential_attention_fwd_gb300/libdiffattn.so.  Objects go to
 _build/ at the repository root.  A rebuild happens only when a source or
 header is newer than the library.
 
+csrc/binding.cpp, the Python binding of the paged-cache operators, is compiled with
+the host compiler against torch's headers into _binding.so beside the library,
+which it calls.
+
 build(variant="waitprof") makes a second library, libdiffattn_waitprof.so,
 from the same sources compiled with -DDIFFATTN_WAIT_PROFILE: its forward
 kernel also counts the cycles each warp role spends waiting on barriers
@@ -19,6 +23,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +31,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdiffattn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 VARIANTS = {
     None: (LIB, BUILD, []),
     "waitprof": (os.path.join(PKG, "libdiffattn_waitprof.so"), os.path.join(BUILD, "waitprof"),
@@ -48,8 +54,32 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _binding_command(obj: str):
+    """(compile, link) commands of the binding, for the torch that is installed."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+                "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    link = [cxx, "-shared", obj, "-o", BINDING + ".tmp", "-L", PKG, "-l:libdiffattn.so", "-L", lib, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
+def _run(cmd, what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) +
+    return _sources() + [os.path.join(CSRC, "binding.cpp")] + sorted(glob.glob(os.path.join(CSRC, "*.h")) +
                                glob.glob(os.path.join(CSRC, "*.cuh")) +
                                glob.glob(os.path.join(INCLUDE, "*.h")))
 
@@ -65,7 +95,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           variant=None) -> str:
     """Compile and link; returns the library path."""
     lib, objdir, defines = VARIANTS[variant]
-    if not force and up_to_date(lib):
+    if not force and up_to_date(lib) and (variant or up_to_date(BINDING)):
         return lib
     cc = nvcc()
     os.makedirs(objdir, exist_ok=True)
@@ -80,7 +110,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
         return obj, r.stdout + r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = os.path.join(objdir, "binding.cpp.o")
+        if not variant:
+            compile_binding, link_binding = _binding_command(binding)
+            bound = ex.submit(_run, compile_binding, "the binding does not compile")
         results = list(ex.map(compile_one, _sources()))
+        if not variant:
+            bound.result()
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
@@ -91,6 +127,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if not variant:
+        _run(link_binding, "the binding does not link")
+        os.replace(BINDING + ".tmp", BINDING)
     return lib
 
 

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import differential_attention_fwd_gb300 as da
-from differential_attention_fwd_gb300 import _lib, _paged
+from differential_attention_fwd_gb300 import _lib
 from differential_attention_fwd_gb300 import build as build_mod
 
 FAKE = 0x10000
@@ -62,17 +62,13 @@ def rotary(lib, d, x=(1, 1, 1, 1), y=(1, 1, 1, 1), qw=None, kw=None, cos=p(20), 
     return lib.diffattn_rotary(None if d is None else ctypes.byref(d), *xs, qw, kw, cos, sin, None, *ys, None)
 
 
-def test_packed_descriptors_have_the_structs_layout():
-    d = rotary_desc(q1_stride=(1, 2, 3), k1_stride=(4, 5, 6), q2_stride=(7, 8, 9), k2_stride=(10, 11, 12),
-                    q1_grad_stride=(13, 14, 15), k2_grad_stride=(16, 17, 18), pos_stride=(19, 20), pos64=1,
-                    q_weight_stride=64, k_weight_stride=0, interleaved=1)
-    packed = _paged._ROTARY.pack(2, 5, 64, 4, 2, 0, 64, 1, 1, 1e-6, 1, 100, 19, 20, 64, 0, *range(1, 13), 13, 14, 15,
-                                 0, 0, 0, 0, 0, 0, 16, 17, 18)
-    assert packed == bytes(d)
-    g = pages(k1_stride=(1, 2, 3), k2_stride=(4, 5, 6), v_stride=(7, 8, 9))
-    assert _paged._PAGES.pack(50, 16, 10, 10, *range(1, 10)) == bytes(g)
-    a = paged_desc(q1_stride=(1, 2, 3), q2_stride=(4, 5, 6), o_stride=(7, 8, 9), mask_stride=(10, 11))
-    assert _paged._PAGED.pack(2, 4, 3, 64, 128, 0, 2, *range(1, 12)) == bytes(a)
+def test_descriptor_layouts():
+    # as the header lists the fields, with natural alignment
+    R, G, P = _lib.DiffattnRotaryDesc, _lib.DiffattnPages, _lib.DiffattnPagedDesc
+    assert ctypes.sizeof(R) == 5 * 8 + 4 * 4 + 4 + 4 + 8 + 2 * 8 + 2 * 8 + 8 * 3 * 8
+    assert R.table_rows.offset == 5 * 8 + 6 * 4 and R.q1_grad_stride.offset == ctypes.sizeof(R) - 4 * 3 * 8
+    assert ctypes.sizeof(G) == 4 * 8 + 3 * 3 * 8
+    assert ctypes.sizeof(P) == 5 * 8 + 2 * 4 + 3 * 3 * 8 + 2 * 8 and P.q1_stride.offset == 48
 
 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(T=0), dict(D=0), dict(D=129), dict(dtype=2), dict(rotary_dim=65),
