@@ -101,10 +101,8 @@ int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const void* q1,
     return DIFFATTN_OK;
 }
 
-// Partial rows of the weight gradients: head blocks x chunks, at most this many
-// (plan_rotary_bwd asks for 2432 in all, one a head block at least and rounded up).
 size_t rotary_bwd_bytes(const diffattn_rotary_desc* d) {
-    return (size_t)(2 * (d->H + d->Hk) + 2 * 2432) * d->D * sizeof(float);
+    return rotary_bwd_floats(d->B, d->T, d->D, 2 * (d->H + d->Hk)) * sizeof(float);
 }
 
 int check_pages(const diffattn_pages* g) {

@@ -58,7 +58,7 @@ struct RotaryParams {
     int head_blocks;            // of all streams
     // backward
     int chunks;                 // blocks along the tokens
-    float* partial;             // [head_blocks][chunks][D]
+    float* partial;             // [rows][chunks][D]: a row a head, or a block of heads
     float* dw[2];               // q and k weight gradients, nullptr: not wanted
     int64_t dw_stride[2];       // 0: [D], summed over heads; D: [heads, D]
 };
@@ -68,6 +68,8 @@ int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream);
 // Heads a block walks, and the blocks along tokens and heads, for p's sizes.
 void plan_rotary(RotaryParams* p, int num_sms);
 void plan_rotary_bwd(RotaryParams* p);
+// Floats of the weight gradients' partial rows, at most, for `heads` heads in all.
+size_t rotary_bwd_floats(int64_t B, int64_t T, int64_t D, int64_t heads);
 
 // A unit that worker c started and did not finish, for the merging pass: its parts are
 // in slots 2 c + 1, 2 (c + 1), ... 2 (c + parts - 1).  parts = 0: there is none.

@@ -20,12 +20,14 @@
 // would be as much traffic as x itself.
 #include "paged.h"
 #include "ptx.cuh"
+#include "pdl.cuh"
 
 namespace diffattn {
 namespace rot {
 
 constexpr int THREADS = 256;
 constexpr int MAX_D = 128;
+constexpr int BWD_STEPS = 4;    // rows of each group of lanes in a backward block's chunk
 
 template <typename T>
 struct Vec;
@@ -33,8 +35,11 @@ template <>
 struct Vec<float> {
     static constexpr int N = 4;
     __device__ static __forceinline__ void load(const float* p, float* x) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        unpack(*reinterpret_cast<const uint4*>(p), x);
+    }
+    __device__ static __forceinline__ void unpack(uint4 v, float* x) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
     }
     __device__ static __forceinline__ void store(float* p, const float* x) {
         *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -45,8 +50,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ static __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
+    __device__ static __forceinline__ void unpack(uint4 v, float* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -141,6 +145,13 @@ __device__ __forceinline__ void from_pairs(const float* e0, const float* e1, flo
     }
 }
 
+// Heads of the streams before stream i: where its rows begin among the partial rows by head.
+__device__ __forceinline__ int block_row(const RotaryParams& p, int i) {
+    int n = 0;
+    for (int j = 0; j < i; ++j) n += p.s[j].heads;
+    return n;
+}
+
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
@@ -168,7 +179,13 @@ __device__ __forceinline__ void load_turn(const RotaryParams& p, int64_t pos, in
 
 // ---------------------------------------------------------------------------
 // forward and append
+//
+// A thread's loads are what hides the HBM's latency: four heads' chunks (128 bytes) go
+// out together, the first four before the token's position is even known, since the
+// chain position - table row - arithmetic is as long as theirs.
 // ---------------------------------------------------------------------------
+constexpr int AHEAD = 4;        // heads
+
 template <typename T, int G, bool INTER>
 __global__ void __launch_bounds__(THREADS)
 rotary_kernel(const RotaryParams p) {
@@ -182,77 +199,103 @@ rotary_kernel(const RotaryParams p) {
     const bool paged = s.kind != kRowsDense;
     // the lanes of a group share a token; a group past the last token only takes
     // part in the warp's shuffles
-    const int64_t tok = (int64_t)blockIdx.x * TOKENS + threadIdx.x / G;
-    const bool in = tok < (int64_t)p.B * p.T;
-    const int b = in ? (int)(tok / p.T) : 0;
-    const int t = in ? (int)(tok - (int64_t)b * p.T) : 0;
-    Token k = find_token(p, b, t, paged);
-    k.live = k.live && in;
-    if (k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
-    const bool write = k.live && (k.ok || !paged);
+    const int tok = blockIdx.x * TOKENS + threadIdx.x / G;
+    const bool in = tok < p.B * p.T;
+    const int b = in ? tok / p.T : 0;
+    const int t = in ? tok - b * p.T : 0;
     const T* x0 = static_cast<const T*>(s.x) + b * s.sx[0] + t * s.sx[2];
-    T* y0 = static_cast<T*>(s.y) + (paged ? k.page * s.sy[0] + k.slot * s.sy[2] : b * s.sy[0] + t * s.sy[2]);
     if (s.kind == kRowsCopy) {
-        if (!write) return;
-        for (int h = head0; h < head1; ++h)
-            for (int c = g * V; c < s.width; c += G * V)
-                *reinterpret_cast<uint4*>(y0 + h * s.sy[1] + c) =
-                    *reinterpret_cast<const uint4*>(x0 + h * s.sx[1] + c);
+        const Token k = find_token(p, b, t, true);
+        if (in && k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
+        if (!in || !k.live || !k.ok) return;
+        T* y0 = static_cast<T*>(s.y) + k.page * s.sy[0] + k.slot * s.sy[2];
+        // two heads and two chunks at a time
+        for (int h = head0; h < head1; h += 2)
+            for (int c = g * V; c < s.width; c += 2 * G * V) {
+                uint4 v[2][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (h + i < head1 && c + j * G * V < s.width)
+                            v[i][j] = *reinterpret_cast<const uint4*>(x0 + (h + i) * s.sx[1] + c + j * G * V);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (h + i < head1 && c + j * G * V < s.width)
+                            *reinterpret_cast<uint4*>(y0 + (h + i) * s.sy[1] + c + j * G * V) = v[i][j];
+            }
         return;
     }
     int oa, ob;
     const bool turn = chunk_offsets<V, INTER>(g, p.R, &oa, &ob);
+    uint4 raw[AHEAD][2];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+            if (in && h + i < head1) {
+                raw[i][0] = *reinterpret_cast<const uint4*>(x0 + (h + i) * s.sx[1] + oa);
+                raw[i][1] = *reinterpret_cast<const uint4*>(x0 + (h + i) * s.sx[1] + ob);
+            }
+        }
+    };
+    load(head0);
+    Token k = find_token(p, b, t, paged);
+    k.live = k.live && in;
+    if (k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
+    const bool write = k.live && (k.ok || !paged);
+    T* y0 = static_cast<T*>(s.y) + (paged ? k.page * s.sy[0] + k.slot * s.sy[2] : b * s.sy[0] + t * s.sy[2]);
     float cs[V], sn[V];
     load_turn<V>(p, k.pos, g, turn && k.live && k.ok, cs, sn);
     const float fill = k.ok ? 0.f : __int_as_float(0x7fc00000);   // a position outside the table: NaN
     float w[2 * V];
     const bool weighted = p.norm && s.weight;
-    if (weighted && s.w_stride == 0) {
+    auto load_weight = [&](const float* at) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
-            Vec<float>::load(s.weight + oa + i, w + i);
-            Vec<float>::load(s.weight + ob + i, w + V + i);
+            Vec<float>::load(at + oa + i, w + i);
+            Vec<float>::load(at + ob + i, w + V + i);
         }
-    }
-#pragma unroll 2
-    for (int h = head0; h < head1; ++h) {
-        float c[2 * V] = {};
-        if (k.live) {
-            Vec<T>::load(x0 + h * s.sx[1] + oa, c);
-            Vec<T>::load(x0 + h * s.sx[1] + ob, c + V);
-        }
-        if (p.norm) {
-            float ss = 0.f;
+    };
+    if (weighted && s.w_stride == 0) load_weight(s.weight);
+    for (int h0 = head0; h0 < head1; h0 += AHEAD) {
+        if (h0 > head0) load(h0);
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) ss = fmaf(c[i], c[i], ss);
-            const float r = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
-            if (weighted) {
-                if (s.w_stride) {
+        for (int i = 0; i < AHEAD; ++i) {
+            const int h = h0 + i;
+            if (h >= head1) break;
+            float c[2 * V];
+            Vec<T>::unpack(raw[i][0], c);
+            Vec<T>::unpack(raw[i][1], c + V);
+            if (p.norm) {
+                float ss = 0.f;
 #pragma unroll
-                    for (int i = 0; i < V; i += 4) {
-                        Vec<float>::load(s.weight + h * s.w_stride + oa + i, w + i);
-                        Vec<float>::load(s.weight + h * s.w_stride + ob + i, w + V + i);
-                    }
+                for (int e = 0; e < 2 * V; ++e) ss = fmaf(c[e], c[e], ss);
+                const float r = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
+                if (weighted) {
+                    if (s.w_stride) load_weight(s.weight + h * s.w_stride);
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e) c[e] *= r * w[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e) c[e] *= r;
                 }
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) c[i] *= r * w[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) c[i] *= r;
             }
-        }
-        float e0[V], e1[V];
-        to_pairs<V, INTER>(c, e0, e1);
+            float e0[V], e1[V];
+            to_pairs<V, INTER>(c, e0, e1);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float u = e0[i] * cs[i] - e1[i] * sn[i] + fill;
-            e1[i] = e1[i] * cs[i] + e0[i] * sn[i] + fill;
-            e0[i] = u;
-        }
-        from_pairs<V, INTER>(e0, e1, c);
-        if (write) {
-            Vec<T>::store(y0 + h * s.sy[1] + oa, c);
-            Vec<T>::store(y0 + h * s.sy[1] + ob, c + V);
+            for (int e = 0; e < V; ++e) {
+                const float u = e0[e] * cs[e] - e1[e] * sn[e] + fill;
+                e1[e] = e1[e] * cs[e] + e0[e] * sn[e] + fill;
+                e0[e] = u;
+            }
+            from_pairs<V, INTER>(e0, e1, c);
+            if (write) {
+                Vec<T>::store(y0 + h * s.sy[1] + oa, c);
+                Vec<T>::store(y0 + h * s.sy[1] + ob, c + V);
+            }
         }
     }
 }
@@ -318,112 +361,171 @@ rotary_any_kernel(const RotaryParams p) {
 // backward: with u = R(p)^T dy (the rotation by the negative angle),
 //     dw = sum over rows of u x r,
 //     dx = r (w u - x r^2 mean(w u x)).
-// Reads x and dy, writes dx: bound by HBM.  A block walks a chunk of the tokens and
-// a few heads, one when the weights differ by head; each lane keeps the dw of its own
-// 2 V channels in registers, and a block leaves one partial row, so the sum's order
-// is fixed and no atomics are needed.
+// Reads x and dy, writes dx: bound by HBM.  A block takes a chunk of the tokens, whose
+// cosines and sines it keeps in shared memory (read for each head from L2 they were as
+// much traffic as dy, behind the position's own latency: 105 us at B2 T4099, 40 heads of
+// 128, where the tokens came first and each head had blocks of its own), and walks some
+// heads over it, the next row of x and dy on its way while one is computed.  Each lane
+// keeps the dw of its own 2 V channels in registers, for a head or for all of them, and a
+// block leaves one partial row for each: the sum's order is fixed, without atomics.
 // ---------------------------------------------------------------------------
 template <typename T, int G, bool INTER>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 2)
 rotary_bwd_kernel(const RotaryParams p) {
     constexpr int V = Vec<T>::N;
     constexpr int GROUPS = THREADS / G;
     constexpr int D = G * 2 * V;
-    __shared__ float red[GROUPS * D];
-    const int g = threadIdx.x % G, group = threadIdx.x / G;
+    extern __shared__ __align__(16) float smem_f[];
+    float* turns = smem_f;                                  // [token of the chunk][cos R/2, sin R/2]
+    float* red = turns + BWD_STEPS * GROUPS * p.R;          // [warp][D]
+    int2* where = reinterpret_cast<int2*>(red + THREADS / 32 * D);      // (b, t) of the tokens; b < 0: none,
+    const int g = threadIdx.x % G, group = threadIdx.x / G;             // t < 0: a position outside the tables (~t)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
     int head0;
     const int si = find_stream(p, blockIdx.y, &head0);
     const RowStream& s = p.s[si];
     const int head1 = min(s.heads, head0 + p.heads_per_block);
+    const int half = p.R / 2;
+    // ---- the chunk's tokens and their tables
+    const int tok0 = blockIdx.x * BWD_STEPS * GROUPS;
+    for (int i = threadIdx.x; i < BWD_STEPS * GROUPS; i += THREADS) {
+        int2 bt = make_int2(-1, 0);
+        if (tok0 + i < p.B * p.T) {
+            bt.x = (tok0 + i) / p.T;
+            bt.y = tok0 + i - bt.x * p.T;
+            if (!find_token(p, bt.x, bt.y, false).ok) {
+                atomicOr(p.status, kStatusIndex);
+                bt.y = ~bt.y;
+            }
+        }
+        where[i] = bt;
+    }
+    for (int i = threadIdx.x; i < BWD_STEPS * GROUPS * (half / 4); i += THREADS) {
+        const int k = i / (half / 4), c = i % (half / 4) * 4;
+        if (tok0 + k >= p.B * p.T) continue;
+        const int b = (tok0 + k) / p.T;
+        const Token at = find_token(p, b, tok0 + k - b * p.T, false);
+        if (!at.ok) continue;
+        *reinterpret_cast<float4*>(turns + k * p.R + c) = *reinterpret_cast<const float4*>(p.cos + at.pos * half + c);
+        *reinterpret_cast<float4*>(turns + k * p.R + half + c) = *reinterpret_cast<const float4*>(p.sin + at.pos * half + c);
+    }
     int oa, ob;
     const bool turn = chunk_offsets<V, INTER>(g, p.R, &oa, &ob);
     const bool weighted = p.norm && s.weight;
+    const bool want = p.norm && p.dw[s.grad_slot];
+    const bool by_head = want && p.dw_stride[s.grad_slot] != 0;
     float w[2 * V], dw[2 * V];
 #pragma unroll
     for (int i = 0; i < 2 * V; ++i) { w[i] = 1.f; dw[i] = 0.f; }
-    if (weighted && s.w_stride == 0) {
+    auto load_weight = [&](const float* at) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
-            Vec<float>::load(s.weight + oa + i, w + i);
-            Vec<float>::load(s.weight + ob + i, w + V + i);
+            Vec<float>::load(at + oa + i, w + i);
+            Vec<float>::load(at + ob + i, w + V + i);
         }
-    }
-    const int64_t tokens = (int64_t)p.B * p.T;
-    // every group of the block makes the same number of steps: the sums below are
-    // warp-wide
-    for (int64_t base = (int64_t)blockIdx.x * GROUPS; base < tokens; base += (int64_t)gridDim.x * GROUPS) {
-        const int64_t tok = base + group;
-        const bool in = tok < tokens;
-        const int b = in ? (int)(tok / p.T) : 0;
-        const int t = in ? (int)(tok - (int64_t)b * p.T) : 0;
-        const Token k = find_token(p, b, t, false);
-        if (in && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
-        float cs[V], sn[V];
-        load_turn<V>(p, k.pos, g, turn && in && k.ok, cs, sn);
-        const float fill = k.ok ? 0.f : __int_as_float(0x7fc00000);
-        const T* x0 = static_cast<const T*>(s.x) + b * s.sx[0] + t * s.sx[2];
-        const T* g0 = static_cast<const T*>(s.g) + b * s.sg[0] + t * s.sg[2];
-        T* y0 = static_cast<T*>(s.y) + b * s.sy[0] + t * s.sy[2];
-#pragma unroll 2
-        for (int h = head0; h < head1; ++h) {
-            float x[2 * V] = {}, u[2 * V] = {};
-            if (in) {
-                if (p.norm) {
-                    Vec<T>::load(x0 + h * s.sx[1] + oa, x);
-                    Vec<T>::load(x0 + h * s.sx[1] + ob, x + V);
-                }
-                Vec<T>::load(g0 + h * s.sg[1] + oa, u);
-                Vec<T>::load(g0 + h * s.sg[1] + ob, u + V);
-            }
-            float e0[V], e1[V];
+    };
+    if (weighted && s.w_stride == 0) load_weight(s.weight);
+    // the partial row of the block's head h (or of all its heads): sums of the groups in a
+    // fixed order
+    auto leave = [&](int row) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+            float v = dw[i];
+#pragma unroll
+            for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane < G) red[warp * D + (i < V ? oa + i : ob + i - V)] = v;
+            dw[i] = 0.f;
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < D; c += THREADS) {
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < THREADS / 32; ++j) sum += red[j * D + c];
+            p.partial[((int64_t)row * gridDim.x + blockIdx.x) * D + c] = sum;
+        }
+        __syncthreads();
+    };
+    __syncthreads();
+    struct Raw { uint4 x[2], g[2]; };
+    const int n = (head1 - head0) * BWD_STEPS;              // rows of this group: head by head
+    auto load = [&](int i, Raw& r) {
+        const int2 bt = i < n ? where[(i % BWD_STEPS) * GROUPS + group] : make_int2(-1, 0);
+        r.x[0] = r.x[1] = r.g[0] = r.g[1] = make_uint4(0, 0, 0, 0);
+        if (bt.x < 0) return;
+        const int h = head0 + i / BWD_STEPS, t = bt.y < 0 ? ~bt.y : bt.y;
+        if (p.norm) {
+            const T* x = static_cast<const T*>(s.x) + bt.x * s.sx[0] + h * s.sx[1] + t * s.sx[2];
+            r.x[0] = *reinterpret_cast<const uint4*>(x + oa);
+            r.x[1] = *reinterpret_cast<const uint4*>(x + ob);
+        }
+        const T* gr = static_cast<const T*>(s.g) + bt.x * s.sg[0] + h * s.sg[1] + t * s.sg[2];
+        r.g[0] = *reinterpret_cast<const uint4*>(gr + oa);
+        r.g[1] = *reinterpret_cast<const uint4*>(gr + ob);
+    };
+    auto compute = [&](int i, const Raw& r) {
+        const int k = (i % BWD_STEPS) * GROUPS + group;
+        const int2 bt = where[k];
+        const int h = head0 + i / BWD_STEPS, t = bt.y < 0 ? ~bt.y : bt.y;
+        float x[2 * V], u[2 * V], e0[V], e1[V];
+        Vec<T>::unpack(r.g[0], u);
+        Vec<T>::unpack(r.g[1], u + V);
+        Vec<T>::unpack(r.x[0], x);
+        Vec<T>::unpack(r.x[1], x + V);
+        if (turn) {
             to_pairs<V, INTER>(u, e0, e1);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float v = e0[i] * cs[i] + e1[i] * sn[i] + fill;
-                e1[i] = e1[i] * cs[i] - e0[i] * sn[i] + fill;
-                e0[i] = v;
+            for (int e = 0; e < V; e += 4) {
+                float c[4], sn[4];
+                Vec<float>::load(turns + k * p.R + g * V + e, c);
+                Vec<float>::load(turns + k * p.R + half + g * V + e, sn);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v = e0[e + q] * c[q] + e1[e + q] * sn[q];
+                    e1[e + q] = e1[e + q] * c[q] - e0[e + q] * sn[q];
+                    e0[e + q] = v;
+                }
             }
             from_pairs<V, INTER>(e0, e1, u);
-            if (p.norm) {
-                if (weighted && s.w_stride) {
+        }
+        if (bt.x < 0 || bt.y < 0) {                         // no token: nothing; no position: NaN
+            const float v = bt.x < 0 ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
-                    for (int i = 0; i < V; i += 4) {
-                        Vec<float>::load(s.weight + h * s.w_stride + oa + i, w + i);
-                        Vec<float>::load(s.weight + h * s.w_stride + ob + i, w + V + i);
-                    }
-                }
-                float ss = 0.f, sx = 0.f;
+            for (int e = 0; e < 2 * V; ++e) u[e] = v;
+        }
+        if (p.norm) {
+            if (weighted && s.w_stride && i % BWD_STEPS == 0) load_weight(s.weight + h * s.w_stride);
+            float ss = 0.f, sx = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    sx = fmaf(w[i] * u[i], x[i], sx);
-                }
-                const float r = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
-                const float m = group_sum<G>(sx) / p.D * r * r;
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    dw[i] = fmaf(u[i] * r, x[i], dw[i]);
-                    u[i] = r * (w[i] * u[i] - x[i] * m);
-                }
+            for (int e = 0; e < 2 * V; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                sx = fmaf(w[e] * u[e], x[e], sx);
             }
-            if (in) {
-                Vec<T>::store(y0 + h * s.sy[1] + oa, u);
-                Vec<T>::store(y0 + h * s.sy[1] + ob, u + V);
+            const float rr = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
+            const float m = group_sum<G>(sx) / p.D * rr * rr;
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e) {
+                dw[e] = fmaf(u[e] * rr, x[e], dw[e]);
+                u[e] = rr * (w[e] * u[e] - x[e] * m);
             }
         }
+        if (bt.x >= 0) {
+            T* y = static_cast<T*>(s.y) + bt.x * s.sy[0] + h * s.sy[1] + t * s.sy[2];
+            Vec<T>::store(y + oa, u);
+            Vec<T>::store(y + ob, u + V);
+        }
+        if (by_head && i % BWD_STEPS == BWD_STEPS - 1) leave(block_row(p, si) + h);
+    };
+    static_assert(BWD_STEPS % 2 == 0, "rows in pairs");
+    Raw a, b;
+    load(0, a);
+    for (int i = 0; i < n; i += 2) {
+        load(i + 1, b);
+        compute(i, a);
+        load(i + 2, a);
+        compute(i + 1, b);
     }
-    if (!p.norm || !p.dw[s.grad_slot]) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        red[group * D + oa + i] = dw[i];
-        red[group * D + ob + i] = dw[V + i];
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < D; c += THREADS) {
-        float sum = 0.f;
-        for (int j = 0; j < GROUPS; ++j) sum += red[j * D + c];
-        p.partial[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * D + c] = sum;
-    }
+    if (want && !by_head) leave(block_row(p, si) + head0);
 }
 
 template <typename T>
@@ -438,6 +540,7 @@ rotary_bwd_any_kernel(const RotaryParams p) {
     const int si = find_stream(p, blockIdx.y, &head0);      // one head a block here
     const RowStream& s = p.s[si];
     const float* w = p.norm && s.weight ? s.weight + head0 * s.w_stride : nullptr;
+    pdl_launch_dependents();
     const int half = p.R / 2;
     const int64_t tokens = (int64_t)p.B * p.T;
     float dw[E] = {};
@@ -493,6 +596,7 @@ rotary_bwd_any_kernel(const RotaryParams p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) row[lane + 32 * e] = dw[e];
     __syncthreads();
+    // one head a block: its number among all heads is the block's
     for (int c = threadIdx.x; c < p.D; c += THREADS) {
         float sum = 0.f;
         for (int j = 0; j < WARPS; ++j) sum += rows[j][c];
@@ -500,36 +604,53 @@ rotary_bwd_any_kernel(const RotaryParams p) {
     }
 }
 
-// dw from the blocks' partial rows: one block an output row (a head, or all of them),
-// the q weight's rows first.  Eight parts of the partials, then their sum: a fixed order.
-constexpr int RED_PARTS = 8;
-__global__ void __launch_bounds__(RED_PARTS * MAX_D)
+// dw from the blocks' partial rows: a block an output row (a head, or all of them), the q
+// weight's rows first, with the partial rows spread over its warps and lanes' columns.  The
+// order of the sums is fixed.
+constexpr int RED_THREADS = 1024;
+__global__ void __launch_bounds__(RED_THREADS)
 rotary_dw_kernel(const RotaryParams p, int q_rows) {
-    __shared__ float red[RED_PARTS][MAX_D];
+    __shared__ float red[RED_THREADS];
+    pdl_wait();
     const int slot = (int)blockIdx.x < q_rows ? 0 : 1;
     const int out_row = slot ? blockIdx.x - q_rows : blockIdx.x;
-    const int c = threadIdx.x % MAX_D, part = threadIdx.x / MAX_D;
+    const bool by_head = p.dw_stride[slot] != 0;
+    const int cols = p.D <= 32 ? 32 : p.D <= 64 ? 64 : 128, parts = RED_THREADS / cols;
+    const int c = threadIdx.x % cols, part = threadIdx.x / cols;
     float sum = 0.f;
-    int block0 = 0;
+    int heads = 0;
     for (int i = 0; i < p.n; ++i) {
-        const int nb = (p.s[i].heads + p.heads_per_block - 1) / p.heads_per_block;
         if (p.s[i].grad_slot == slot && c < p.D) {
-            const int first = p.dw_stride[slot] ? block0 + out_row : block0;
-            const int last = p.dw_stride[slot] ? first + 1 : block0 + nb;
-            const float* src = p.partial + (int64_t)first * p.chunks * p.D + c;
-            const int n = (last - first) * p.chunks;
-            for (int j = part; j < n; j += RED_PARTS) sum += src[(int64_t)j * p.D];
+            // the head's row, or those of the first heads of the blocks
+            const int rows = by_head ? 1 : (p.s[i].heads + p.heads_per_block - 1) / p.heads_per_block;
+            const int first = heads + (by_head ? out_row : 0);
+            const int n = rows * p.chunks;
+#pragma unroll 8
+            for (int j = part; j < n; j += parts) {
+                const int r = j / p.chunks;
+                sum += p.partial[((int64_t)(first + r * p.heads_per_block) * p.chunks + j - r * p.chunks) * p.D + c];
+            }
         }
-        block0 += nb;
+        heads += p.s[i].heads;
     }
-    red[part][c] = sum;
+    red[threadIdx.x] = sum;
     __syncthreads();
     if (part == 0 && c < p.D) {
         float total = 0.f;
-#pragma unroll
-        for (int i = 0; i < RED_PARTS; ++i) total += red[i][c];
+        for (int i = 0; i < parts; ++i) total += red[i * cols + c];
         p.dw[slot][out_row * p.dw_stride[slot] + c] = total;
     }
+}
+
+template <typename T, int G, bool INTER>
+int launch_bwd(const RotaryParams& p, dim3 grid, cudaStream_t stream) {
+    constexpr int D = G * 2 * Vec<T>::N, GROUPS = THREADS / G;
+    const auto bytes = [](int R) { return (BWD_STEPS * GROUPS * R + THREADS / 32 * D) * 4 + BWD_STEPS * GROUPS * 8; };
+    if (cudaFuncSetAttribute(rotary_bwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(D)) !=
+        cudaSuccess)
+        return -1;
+    rotary_bwd_kernel<T, G, INTER><<<grid, THREADS, bytes(p.R), stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 template <typename T, bool INTER>
@@ -540,8 +661,8 @@ int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
     const dim3 grid((unsigned)(backward ? p.chunks : (tokens * G + THREADS - 1) / THREADS), (unsigned)p.head_blocks);
 #define DIFFATTN_ROTARY(GG)                                                               \
     if (G == GG) {                                                                        \
-        if (backward) rotary_bwd_kernel<T, GG, INTER><<<grid, THREADS, 0, stream>>>(p);   \
-        else rotary_kernel<T, GG, INTER><<<grid, THREADS, 0, stream>>>(p);                \
+        if (backward) return launch_bwd<T, GG, INTER>(p, grid, stream);                   \
+        rotary_kernel<T, GG, INTER><<<grid, THREADS, 0, stream>>>(p);                     \
         return cudaGetLastError() == cudaSuccess ? 0 : -1;                                \
     }
     DIFFATTN_ROTARY(2)
@@ -580,8 +701,8 @@ void set_head_blocks(RotaryParams* p, int hpb) {
 
 }  // namespace rot
 
-// Enough blocks for a few waves of every SM, then as many heads a block as that
-// leaves (16 at most: the registers that hold the token's cosines are paid for by then).
+// As many heads a block as leave a few blocks for every SM (16 at most: the registers that
+// hold the token's cosines are paid for by then), in whole batches of loads.
 void plan_rotary(RotaryParams* p, int num_sms) {
     int heads = 0;
     for (int i = 0; i < p->n; ++i) heads += p->s[i].heads;
@@ -589,20 +710,37 @@ void plan_rotary(RotaryParams* p, int num_sms) {
     if (p->fast) {
         const int lanes = p->D / (p->bf16 ? 16 : 8);
         const int64_t blocks = ((int64_t)p->B * p->T * lanes + rot::THREADS - 1) / rot::THREADS * heads;
-        const int64_t want = blocks / (16ll * num_sms);
-        hpb = want < 1 ? 1 : want > 16 ? 16 : (int)want;
+        const int64_t want = blocks / (8ll * num_sms);
+        hpb = want < 1 ? 1 : want < rot::AHEAD ? (int)want : want > 16 ? 16 : (int)want / rot::AHEAD * rot::AHEAD;
     }
     rot::set_head_blocks(p, hpb);
 }
 
-// The backward's blocks must not depend on the GPU: the workspace is sized for them.
+// The backward's blocks must not depend on the GPU, since the workspace is sized for
+// them: about 1200, of 8 heads at most.  Its partial rows: one a chunk and head where the
+// weights differ by head, else one a chunk and block.
 void plan_rotary_bwd(RotaryParams* p) {
-    const bool per_head = p->norm && ((p->dw[0] && p->dw_stride[0]) || (p->dw[1] && p->dw_stride[1]));
-    rot::set_head_blocks(p, !p->fast || per_head ? 1 : 4);
     const int groups = p->fast ? rot::THREADS / (p->D / (p->bf16 ? 16 : 8)) : rot::THREADS / 32;
-    const int64_t steps = ((int64_t)p->B * p->T + groups - 1) / groups;
-    int64_t chunks = (2432 + p->head_blocks - 1) / p->head_blocks;
-    p->chunks = (int)(chunks < steps ? chunks : steps);
+    const int64_t tokens = (int64_t)p->B * p->T;
+    int heads = 0;
+    for (int i = 0; i < p->n; ++i) heads += p->s[i].heads;
+    if (!p->fast) {                         // a head a block, and chunks in strides
+        rot::set_head_blocks(p, 1);
+        const int64_t steps = (tokens + groups - 1) / groups, chunks = (2432 + heads - 1) / heads;
+        p->chunks = (int)(chunks < steps ? chunks : steps);
+        return;
+    }
+    const int per = groups * rot::BWD_STEPS;
+    p->chunks = (int)((tokens + per - 1) / per);
+    const int64_t want = (int64_t)p->chunks * heads / 1216;
+    rot::set_head_blocks(p, want < 1 ? 1 : want > 8 ? 8 : (int)want);
+}
+
+size_t rotary_bwd_floats(int64_t B, int64_t T, int64_t D, int64_t heads) {
+    // at most: chunks of the fewest tokens a block takes (16 groups a step), a row a head
+    const int64_t chunks = (B * T + 16 * rot::BWD_STEPS - 1) / (16 * rot::BWD_STEPS);
+    const int64_t fast = chunks * heads, any = 2432 + heads;
+    return (size_t)((fast > any ? fast : any) * D);
 }
 
 int launch_rotary(const RotaryParams& p, cudaStream_t stream) { return rot::launch(p, false, stream); }
@@ -614,8 +752,16 @@ int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream) {
     for (int i = 0; i < p.n; ++i) heads[p.s[i].grad_slot] = p.s[i].heads;
     const int q_rows = !p.dw[0] ? 0 : p.dw_stride[0] ? heads[0] : 1;
     const int k_rows = !p.dw[1] ? 0 : p.dw_stride[1] ? heads[1] : 1;
-    rot::rotary_dw_kernel<<<q_rows + k_rows, rot::RED_PARTS * rot::MAX_D, 0, stream>>>(p, q_rows);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(q_rows + k_rows));
+    cfg.blockDim = dim3(rot::RED_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rot::rotary_dw_kernel, p, q_rows) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace diffattn

@@ -167,6 +167,32 @@ def test_shared_keys_and_left_out_tensors():
     assert torch.count_nonzero(gk) == 0 and torch.count_nonzero(gq) > 0
 
 
+@pytest.mark.parametrize("D,H,Hk,T", [(64, 5, 3, 150), (128, 9, 2, 300), (48, 3, 2, 40)])
+@pytest.mark.parametrize("q_heads", [True, False])
+def test_a_weight_by_head_beside_a_shared_one(D, H, Hk, T, q_heads):
+    """Q's weight by head and K's for all heads, and the reverse: each gradient is the one it
+    has with both weights laid out its way."""
+    g = torch.Generator().manual_seed(D + T)
+    xs = [rows(g, "f32", 2, n, T, D) for n in (H, Hk, H, Hk)]
+    cos, sin = da.rotary_tables(T, D, device="cuda")
+    dys = [torch.randn(x.shape, generator=g).cuda() for x in xs]
+    qw, kw = ((1 + 0.3 * torch.randn(D, generator=g)).cuda() for _ in range(2))
+
+    def grads(q_by_head, k_by_head):
+        a = (qw.expand(H, D) if q_by_head else qw).clone().requires_grad_()
+        b = (kw.expand(Hk, D) if k_by_head else kw).clone().requires_grad_()
+        out = da.qk_norm_rotary(*xs, cos, sin, q_weight=a, k_weight=b)
+        return torch.autograd.grad(out, [a, b], dys)
+
+    mixed = grads(q_heads, not q_heads)
+    assert torch.equal(mixed[0], grads(q_heads, q_heads)[0])
+    assert torch.equal(mixed[1], grads(not q_heads, not q_heads)[1])
+    by_head, shared = grads(True, True), grads(False, False)
+    for a, b, n in zip(by_head, shared, (H, Hk)):
+        # the same terms in another order: N u of their sizes, about (4 B T n) half of |w x u|
+        assert ((a.double().sum(0) - b.double()).abs() <= 2.0 ** -24 * 4 * T * n * 40).all()
+
+
 def test_broadcast_rows_and_float16_weights():
     """A row tensor expanded over the batch (stride 0) and weights of another type."""
     g = torch.Generator().manual_seed(2)
