@@ -45,6 +45,7 @@ void fill_rotary(RotaryParams* p, const diffattn_rotary_desc& d, const float* co
     p->interleaved = d.interleaved != 0;
     p->norm = d.norm == DIFFATTN_NORM_RMS;
     p->eps = d.eps;
+    p->inv_D = 1.0f / (float)d.D;       // exact where the vector kernel takes D
     p->cos = cos;
     p->sin = sin;
     p->table_rows = d.table_rows;

@@ -39,7 +39,7 @@ struct RotaryParams {
     int n;                      // streams
     int B, T, D, R;             // R rotated elements of each row (0: none)
     int bf16, interleaved, norm;
-    float eps;
+    float eps, inv_D;
     const float* cos;           // [table_rows, R / 2]
     const float* sin;
     int64_t table_rows;

@@ -29,20 +29,19 @@ constexpr int THREADS = 256;
 constexpr int MAX_D = 128;
 constexpr int BWD_STEPS = 4;    // rows of each group of lanes in a backward block's chunk
 
+// 16 bytes of elements, N of them, as N / 2 packed pairs of floats (two elements an
+// instruction: at an SM's share of the HBM rate the arithmetic is half of the time).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
-    __device__ static __forceinline__ void load(const float* p, float* x) {
-        unpack(*reinterpret_cast<const uint4*>(p), x);
+    __device__ static __forceinline__ void unpack(uint4 v, uint64_t* x) {
+        x[0] = f2_from_bits(v.x, v.y);
+        x[1] = f2_from_bits(v.z, v.w);
     }
-    __device__ static __forceinline__ void unpack(uint4 v, float* x) {
-        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
-        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
-    }
-    __device__ static __forceinline__ void store(float* p, const float* x) {
-        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    __device__ static __forceinline__ uint4 pack(const uint64_t* x) {
+        return make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
     }
     __device__ static __forceinline__ float get(float v) { return v; }
     __device__ static __forceinline__ float put(float v) { return v; }
@@ -50,17 +49,16 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ static __forceinline__ void unpack(uint4 v, float* x) {
+    __device__ static __forceinline__ void unpack(uint4 v, uint64_t* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = f2_from_bits(w[i] << 16, w[i] & 0xffff0000u);
     }
-    __device__ static __forceinline__ void store(__nv_bfloat16* p, const float* x) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    __device__ static __forceinline__ uint4 pack(const uint64_t* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f2_lo(x[i]), f2_hi(x[i]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ static __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
     __device__ static __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
@@ -127,22 +125,53 @@ __device__ __forceinline__ bool chunk_offsets(int g, int R, int* a, int* b) {
     return turn;
 }
 
-// One row's pairs (e0, e1) from its two chunks and back.
-template <int V, bool INTER>
-__device__ __forceinline__ void to_pairs(const float* c, float* e0, float* e1) {
+// V floats as V / 2 packed pairs.
+template <int V>
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t* x) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        e0[i] = INTER ? c[2 * i] : c[i];
-        e1[i] = INTER ? c[2 * i + 1] : c[V + i];
+    for (int i = 0; i < V / 4; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+        x[2 * i] = f2_from_bits(v.x, v.y);
+        x[2 * i + 1] = f2_from_bits(v.z, v.w);
     }
 }
+
+// Turn the lane's V pairs of elements, c[0 .. V/2) from its first chunk and c[V/2 .. V)
+// from its second, by the angles with these cosines and sines (negated for the backward).
 template <int V, bool INTER>
-__device__ __forceinline__ void from_pairs(const float* e0, const float* e1, float* c) {
+__device__ __forceinline__ void rotate(uint64_t* c, const uint64_t* cs, const uint64_t* sn, bool back) {
+    if constexpr (INTER) {
+        // both elements of a pair are in one register pair
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        c[INTER ? 2 * i : i] = e0[i];
-        c[INTER ? 2 * i + 1 : V + i] = e1[i];
+        for (int i = 0; i < V; ++i) {
+            const float co = i & 1 ? f2_hi(cs[i / 2]) : f2_lo(cs[i / 2]);
+            const float s0 = i & 1 ? f2_hi(sn[i / 2]) : f2_lo(sn[i / 2]), si = back ? -s0 : s0;
+            const float a = f2_lo(c[i]), b = f2_hi(c[i]);
+            c[i] = f2_pack(a * co - b * si, b * co + a * si);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const uint64_t a = c[i], b = c[V / 2 + i];
+            const uint64_t p = f2_mul(a, sn[i]), q = f2_mul(b, sn[i]);
+            if (back) {
+                c[i] = f2_fma(a, cs[i], q);
+                c[V / 2 + i] = f2_sub(f2_mul(b, cs[i]), p);
+            } else {
+                c[i] = f2_sub(f2_mul(a, cs[i]), q);
+                c[V / 2 + i] = f2_fma(b, cs[i], p);
+            }
+        }
     }
+}
+
+// Sum of both halves of V packed pairs.
+template <int V>
+__device__ __forceinline__ float pair_sum(const uint64_t* x) {
+    uint64_t s = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) s = f2_add(s, x[i]);
+    return f2_lo(s) + f2_hi(s);
 }
 
 // Heads of the streams before stream i: where its rows begin among the partial rows by head.
@@ -159,24 +188,6 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// cos and sin of the lane's V pairs (1 and 0 where nothing turns).
-template <int V>
-__device__ __forceinline__ void load_turn(const RotaryParams& p, int64_t pos, int g, bool turn, float* cs, float* sn) {
-    if (turn) {
-        const int64_t at = pos * (p.R / 2) + g * V;
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(p.cos + at + i);
-            const float4 s = *reinterpret_cast<const float4*>(p.sin + at + i);
-            cs[i] = c.x; cs[i + 1] = c.y; cs[i + 2] = c.z; cs[i + 3] = c.w;
-            sn[i] = s.x; sn[i + 1] = s.y; sn[i + 2] = s.z; sn[i + 3] = s.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // forward and append
 //
@@ -187,7 +198,7 @@ __device__ __forceinline__ void load_turn(const RotaryParams& p, int64_t pos, in
 constexpr int AHEAD = 4;        // heads
 
 template <typename T, int G, bool INTER>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 3)
 rotary_kernel(const RotaryParams p) {
     constexpr int V = Vec<T>::N;
     constexpr int TOKENS = THREADS / G;
@@ -247,54 +258,47 @@ rotary_kernel(const RotaryParams p) {
     if (k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
     const bool write = k.live && (k.ok || !paged);
     T* y0 = static_cast<T*>(s.y) + (paged ? k.page * s.sy[0] + k.slot * s.sy[2] : b * s.sy[0] + t * s.sy[2]);
-    float cs[V], sn[V];
-    load_turn<V>(p, k.pos, g, turn && k.live && k.ok, cs, sn);
-    const float fill = k.ok ? 0.f : __int_as_float(0x7fc00000);   // a position outside the table: NaN
-    float w[2 * V];
+    uint64_t cs[V / 2], sn[V / 2];
+    const bool turned = turn && k.live && k.ok;
+    if (turned) {
+        load_pairs<V>(p.cos + k.pos * (p.R / 2) + g * V, cs);
+        load_pairs<V>(p.sin + k.pos * (p.R / 2) + g * V, sn);
+    }
     const bool weighted = p.norm && s.weight;
-    auto load_weight = [&](const float* at) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            Vec<float>::load(at + oa + i, w + i);
-            Vec<float>::load(at + ob + i, w + V + i);
-        }
-    };
-    if (weighted && s.w_stride == 0) load_weight(s.weight);
     for (int h0 = head0; h0 < head1; h0 += AHEAD) {
         if (h0 > head0) load(h0);
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int h = h0 + i;
             if (h >= head1) break;
-            float c[2 * V];
+            uint64_t c[V];
             Vec<T>::unpack(raw[i][0], c);
-            Vec<T>::unpack(raw[i][1], c + V);
+            Vec<T>::unpack(raw[i][1], c + V / 2);
             if (p.norm) {
-                float ss = 0.f;
+                uint64_t sq[V];
 #pragma unroll
-                for (int e = 0; e < 2 * V; ++e) ss = fmaf(c[e], c[e], ss);
-                const float r = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
-                if (weighted) {
-                    if (s.w_stride) load_weight(s.weight + h * s.w_stride);
+                for (int e = 0; e < V; ++e) sq[e] = f2_mul(c[e], c[e]);
+                const float r = rsqrtf(group_sum<G>(pair_sum<V>(sq)) * p.inv_D + p.eps);
+                const uint64_t r2 = f2_pack(r, r);
+                if (weighted) {             // from L1: the registers are worth more blocks an SM
+                    uint64_t w[V];
+                    load_pairs<V>(s.weight + h * s.w_stride + oa, w);
+                    load_pairs<V>(s.weight + h * s.w_stride + ob, w + V / 2);
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) c[e] *= r * w[e];
+                    for (int e = 0; e < V; ++e) c[e] = f2_mul(c[e], f2_mul(r2, w[e]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) c[e] *= r;
+                    for (int e = 0; e < V; ++e) c[e] = f2_mul(c[e], r2);
                 }
             }
-            float e0[V], e1[V];
-            to_pairs<V, INTER>(c, e0, e1);
+            if (turned) rotate<V, INTER>(c, cs, sn, false);
+            if (!k.ok) {                    // a position outside the tables
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float u = e0[e] * cs[e] - e1[e] * sn[e] + fill;
-                e1[e] = e1[e] * cs[e] + e0[e] * sn[e] + fill;
-                e0[e] = u;
+                for (int e = 0; e < V; ++e) c[e] = 0x7fc000007fc00000ull;
             }
-            from_pairs<V, INTER>(e0, e1, c);
             if (write) {
-                Vec<T>::store(y0 + h * s.sy[1] + oa, c);
-                Vec<T>::store(y0 + h * s.sy[1] + ob, c + V);
+                *reinterpret_cast<uint4*>(y0 + h * s.sy[1] + oa) = Vec<T>::pack(c);
+                *reinterpret_cast<uint4*>(y0 + h * s.sy[1] + ob) = Vec<T>::pack(c + V / 2);
             }
         }
     }
@@ -415,28 +419,19 @@ rotary_bwd_kernel(const RotaryParams p) {
     const bool weighted = p.norm && s.weight;
     const bool want = p.norm && p.dw[s.grad_slot];
     const bool by_head = want && p.dw_stride[s.grad_slot] != 0;
-    float w[2 * V], dw[2 * V];
-#pragma unroll
-    for (int i = 0; i < 2 * V; ++i) { w[i] = 1.f; dw[i] = 0.f; }
-    auto load_weight = [&](const float* at) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            Vec<float>::load(at + oa + i, w + i);
-            Vec<float>::load(at + ob + i, w + V + i);
-        }
-    };
-    if (weighted && s.w_stride == 0) load_weight(s.weight);
+    uint64_t dw[V] = {};
     // the partial row of the block's head h (or of all its heads): sums of the groups in a
     // fixed order
     auto leave = [&](int row) {
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
-            float v = dw[i];
+            float v = i & 1 ? f2_hi(dw[i / 2]) : f2_lo(dw[i / 2]);
 #pragma unroll
             for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane < G) red[warp * D + (i < V ? oa + i : ob + i - V)] = v;
-            dw[i] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[i] = 0;
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += THREADS) {
             float sum = 0.f;
@@ -467,52 +462,46 @@ rotary_bwd_kernel(const RotaryParams p) {
         const int k = (i % BWD_STEPS) * GROUPS + group;
         const int2 bt = where[k];
         const int h = head0 + i / BWD_STEPS, t = bt.y < 0 ? ~bt.y : bt.y;
-        float x[2 * V], u[2 * V], e0[V], e1[V];
+        uint64_t x[V], u[V];
         Vec<T>::unpack(r.g[0], u);
-        Vec<T>::unpack(r.g[1], u + V);
-        Vec<T>::unpack(r.x[0], x);
-        Vec<T>::unpack(r.x[1], x + V);
+        Vec<T>::unpack(r.g[1], u + V / 2);
         if (turn) {
-            to_pairs<V, INTER>(u, e0, e1);
-#pragma unroll
-            for (int e = 0; e < V; e += 4) {
-                float c[4], sn[4];
-                Vec<float>::load(turns + k * p.R + g * V + e, c);
-                Vec<float>::load(turns + k * p.R + half + g * V + e, sn);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float v = e0[e + q] * c[q] + e1[e + q] * sn[q];
-                    e1[e + q] = e1[e + q] * c[q] - e0[e + q] * sn[q];
-                    e0[e + q] = v;
-                }
-            }
-            from_pairs<V, INTER>(e0, e1, u);
+            uint64_t cs[V / 2], sn[V / 2];
+            load_pairs<V>(turns + k * p.R + g * V, cs);
+            load_pairs<V>(turns + k * p.R + half + g * V, sn);
+            rotate<V, INTER>(u, cs, sn, true);
         }
         if (bt.x < 0 || bt.y < 0) {                         // no token: nothing; no position: NaN
-            const float v = bt.x < 0 ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) u[e] = v;
+            for (int e = 0; e < V; ++e) u[e] = bt.x < 0 ? 0ull : 0x7fc000007fc00000ull;
         }
         if (p.norm) {
-            if (weighted && s.w_stride && i % BWD_STEPS == 0) load_weight(s.weight + h * s.w_stride);
-            float ss = 0.f, sx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-                ss = fmaf(x[e], x[e], ss);
-                sx = fmaf(w[e] * u[e], x[e], sx);
+            Vec<T>::unpack(r.x[0], x);
+            Vec<T>::unpack(r.x[1], x + V / 2);
+            uint64_t g2[V], s1 = 0, s2 = 0;                 // w u, and the sums of x x and w u x
+            if (weighted) {
+                load_pairs<V>(s.weight + h * s.w_stride + oa, g2);
+                load_pairs<V>(s.weight + h * s.w_stride + ob, g2 + V / 2);
             }
-            const float rr = 1.0f / sqrtf(group_sum<G>(ss) / p.D + p.eps);
-            const float m = group_sum<G>(sx) / p.D * rr * rr;
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-                dw[e] = fmaf(u[e] * rr, x[e], dw[e]);
-                u[e] = rr * (w[e] * u[e] - x[e] * m);
+            for (int e = 0; e < V; ++e) {
+                g2[e] = weighted ? f2_mul(g2[e], u[e]) : u[e];
+                s1 = f2_fma(x[e], x[e], s1);
+                s2 = f2_fma(g2[e], x[e], s2);
+            }
+            const float rr = rsqrtf(group_sum<G>(f2_lo(s1) + f2_hi(s1)) * p.inv_D + p.eps);
+            const float m = -(group_sum<G>(f2_lo(s2) + f2_hi(s2)) * p.inv_D * rr * rr * rr);
+            const uint64_t rr2 = f2_pack(rr, rr), m2 = f2_pack(m, m);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                dw[e] = f2_fma(f2_mul(u[e], rr2), x[e], dw[e]);
+                u[e] = f2_fma(x[e], m2, f2_mul(g2[e], rr2));
             }
         }
         if (bt.x >= 0) {
             T* y = static_cast<T*>(s.y) + bt.x * s.sy[0] + h * s.sy[1] + t * s.sy[2];
-            Vec<T>::store(y + oa, u);
-            Vec<T>::store(y + ob, u + V);
+            *reinterpret_cast<uint4*>(y + oa) = Vec<T>::pack(u);
+            *reinterpret_cast<uint4*>(y + ob) = Vec<T>::pack(u + V / 2);
         }
         if (by_head && i % BWD_STEPS == BWD_STEPS - 1) leave(block_row(p, si) + h);
     };
