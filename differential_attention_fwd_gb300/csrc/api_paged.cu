@@ -32,6 +32,9 @@ int check_rotary(const diffattn_rotary_desc* d, const float* cos, const float* s
         (d->k_weight_stride != 0 && d->k_weight_stride != d->D))
         return DIFFATTN_ERR_INVALID;
     if (d->B > INT32_MAX || d->T > INT32_MAX || d->B * d->T > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
+    // rows of the backward's kernels are counted in 31 bits
+    if (d->H >= 0 && d->Hk >= 0 && 2.0 * (d->B * d->T / 16 + 16) * (double)(d->H + d->Hk) > INT32_MAX)
+        return DIFFATTN_ERR_UNSUPPORTED;
     return DIFFATTN_OK;
 }
 
@@ -39,6 +42,7 @@ void fill_rotary(RotaryParams* p, const diffattn_rotary_desc& d, const float* co
                  const void* positions) {
     p->B = (int)d.B;
     p->T = (int)d.T;
+    p->by_T.set((uint32_t)d.T);
     p->D = (int)d.D;
     p->R = d.rotary_dim;
     p->bf16 = d.dtype == DIFFATTN_BF16;
@@ -290,7 +294,7 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc* desc, const void* q1, const 
     int sms = 0;
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
-    plan_rotary_bwd(&p);
+    plan_rotary_bwd(&p, sms);
     return launch_rotary_bwd(p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 

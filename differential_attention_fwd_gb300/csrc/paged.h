@@ -34,10 +34,27 @@ struct RowStream {
     int grad_slot;              // 0: q weight, 1: k weight
 };
 
+// Division of numbers below 2^31 by a divisor that the host knows.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+    void set(uint32_t d) {
+        shift = 0;
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+#endif
+};
+
 struct RotaryParams {
     RowStream s[4];
     int n;                      // streams
     int B, T, D, R;             // R rotated elements of each row (0: none)
+    FastDiv by_T, by_heads;
     int bf16, interleaved, norm;
     float eps, inv_D;
     const float* cos;           // [table_rows, R / 2]
@@ -55,10 +72,11 @@ struct RotaryParams {
     uint32_t* status;
     int fast;                   // 16-byte rows: the vector kernel
     int heads_per_block;
-    int head_blocks;            // of all streams
+    int head_blocks;            // of all streams (backward, vector kernel: blocks in all)
     // backward
-    int chunks;                 // blocks along the tokens
-    float* partial;             // [rows][chunks][D]: a row a head, or a block of heads
+    int chunks;                 // of the tokens
+    int heads;                  // of all streams
+    float* partial;             // [chunks][heads][D]
     float* dw[2];               // q and k weight gradients, nullptr: not wanted
     int64_t dw_stride[2];       // 0: [D], summed over heads; D: [heads, D]
 };
@@ -67,7 +85,7 @@ int launch_rotary(const RotaryParams& p, cudaStream_t stream);
 int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream);
 // Heads a block walks, and the blocks along tokens and heads, for p's sizes.
 void plan_rotary(RotaryParams* p, int num_sms);
-void plan_rotary_bwd(RotaryParams* p);
+void plan_rotary_bwd(RotaryParams* p, int num_sms);
 // Floats of the weight gradients' partial rows, at most, for `heads` heads in all.
 size_t rotary_bwd_floats(int64_t B, int64_t T, int64_t D, int64_t heads);
 

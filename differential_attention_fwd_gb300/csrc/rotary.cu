@@ -27,7 +27,8 @@ namespace rot {
 
 constexpr int THREADS = 256;
 constexpr int MAX_D = 128;
-constexpr int BWD_STEPS = 4;    // rows of each group of lanes in a backward block's chunk
+constexpr int BWD_STEPS = 3;    // rows of each group of lanes in an item of the backward,
+constexpr int BWD_STAGES = 3;   // and rows on their way
 
 // 16 bytes of elements, N of them, as N / 2 packed pairs of floats (two elements an
 // instruction: at an SM's share of the HBM rate the arithmetic is half of the time).
@@ -174,13 +175,6 @@ __device__ __forceinline__ float pair_sum(const uint64_t* x) {
     return f2_lo(s) + f2_hi(s);
 }
 
-// Heads of the streams before stream i: where its rows begin among the partial rows by head.
-__device__ __forceinline__ int block_row(const RotaryParams& p, int i) {
-    int n = 0;
-    for (int j = 0; j < i; ++j) n += p.s[j].heads;
-    return n;
-}
-
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
@@ -212,7 +206,7 @@ rotary_kernel(const RotaryParams p) {
     // part in the warp's shuffles
     const int tok = blockIdx.x * TOKENS + threadIdx.x / G;
     const bool in = tok < p.B * p.T;
-    const int b = in ? tok / p.T : 0;
+    const int b = in ? p.by_T.div(tok) : 0;
     const int t = in ? tok - b * p.T : 0;
     const T* x0 = static_cast<const T*>(s.x) + b * s.sx[0] + t * s.sx[2];
     if (s.kind == kRowsCopy) {
@@ -365,14 +359,34 @@ rotary_any_kernel(const RotaryParams p) {
 // backward: with u = R(p)^T dy (the rotation by the negative angle),
 //     dw = sum over rows of u x r,
 //     dx = r (w u - x r^2 mean(w u x)).
-// Reads x and dy, writes dx: bound by HBM.  A block takes a chunk of the tokens, whose
-// cosines and sines it keeps in shared memory (read for each head from L2 they were as
-// much traffic as dy, behind the position's own latency: 105 us at B2 T4099, 40 heads of
-// 128, where the tokens came first and each head had blocks of its own), and walks some
-// heads over it, the next row of x and dy on its way while one is computed.  Each lane
-// keeps the dw of its own 2 V channels in registers, for a head or for all of them, and a
-// block leaves one partial row for each: the sum's order is fixed, without atomics.
+// Reads x and dy, writes dx: bound by HBM.  An item is one head over a chunk of tokens
+// (BWD_STEPS rows for each group of lanes); the items are laid out head by head, chunk by
+// chunk, and every block, two an SM, takes an equal run of them.  A chunk's cosines and
+// sines stay in shared memory for its heads: read for each head from L2 they were as much
+// traffic as dy, behind the position's own latency.  Rows of x and dy come by cp.async,
+// BWD_STAGES ahead, each thread's own (96 KB an SM on their way; one row ahead in registers
+// kept the HBM at 2.8 TB/s), and so do an item's weights.  Each lane keeps the dw of its
+// own 2 V channels in registers, and an item leaves one partial row: the sum's order is
+// fixed, without atomics.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Shared memory of a backward block, in floats: ring, tables, sums, weights, flags.
+struct BwdLayout {
+    int turns, red, weights, fine, total;
+};
+__host__ __device__ constexpr BwdLayout bwd_layout(int groups, int D, int R) {
+    BwdLayout l{};
+    l.turns = BWD_STAGES * 4 * THREADS * 4;                 // ring: [stage][x, x, dy, dy][thread] of 16 bytes
+    l.red = l.turns + BWD_STEPS * groups * R;               // [token of the chunk][cos R/2, sin R/2]
+    l.weights = l.red + THREADS / 32 * D;                   // [warp][D]
+    l.fine = l.weights + 2 * D;                             // [item & 1][D]
+    l.total = l.fine + BWD_STEPS * groups;                  // int [token]: its position is in the tables
+    return l;
+}
+
 template <typename T, int G, bool INTER>
 __global__ void __launch_bounds__(THREADS, 2)
 rotary_bwd_kernel(const RotaryParams p) {
@@ -380,49 +394,80 @@ rotary_bwd_kernel(const RotaryParams p) {
     constexpr int GROUPS = THREADS / G;
     constexpr int D = G * 2 * V;
     extern __shared__ __align__(16) float smem_f[];
-    float* turns = smem_f;                                  // [token of the chunk][cos R/2, sin R/2]
-    float* red = turns + BWD_STEPS * GROUPS * p.R;          // [warp][D]
-    int2* where = reinterpret_cast<int2*>(red + THREADS / 32 * D);      // (b, t) of the tokens; b < 0: none,
-    const int g = threadIdx.x % G, group = threadIdx.x / G;             // t < 0: a position outside the tables (~t)
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const BwdLayout L = bwd_layout(GROUPS, D, p.R);
+    uint4* ring = reinterpret_cast<uint4*>(smem_f);
+    float* turns = smem_f + L.turns;
+    float* red = smem_f + L.red;
+    float* weights = smem_f + L.weights;
+    int* fine = reinterpret_cast<int*>(smem_f + L.fine);
+    const int tid = threadIdx.x, g = tid % G, group = tid / G;
+    const int lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
-    int head0;
-    const int si = find_stream(p, blockIdx.y, &head0);
-    const RowStream& s = p.s[si];
-    const int head1 = min(s.heads, head0 + p.heads_per_block);
     const int half = p.R / 2;
-    // ---- the chunk's tokens and their tables
-    const int tok0 = blockIdx.x * BWD_STEPS * GROUPS;
-    for (int i = threadIdx.x; i < BWD_STEPS * GROUPS; i += THREADS) {
-        int2 bt = make_int2(-1, 0);
-        if (tok0 + i < p.B * p.T) {
-            bt.x = (tok0 + i) / p.T;
-            bt.y = tok0 + i - bt.x * p.T;
-            if (!find_token(p, bt.x, bt.y, false).ok) {
-                atomicOr(p.status, kStatusIndex);
-                bt.y = ~bt.y;
-            }
-        }
-        where[i] = bt;
-    }
-    for (int i = threadIdx.x; i < BWD_STEPS * GROUPS * (half / 4); i += THREADS) {
-        const int k = i / (half / 4), c = i % (half / 4) * 4;
-        if (tok0 + k >= p.B * p.T) continue;
-        const int b = (tok0 + k) / p.T;
-        const Token at = find_token(p, b, tok0 + k - b * p.T, false);
-        if (!at.ok) continue;
-        *reinterpret_cast<float4*>(turns + k * p.R + c) = *reinterpret_cast<const float4*>(p.cos + at.pos * half + c);
-        *reinterpret_cast<float4*>(turns + k * p.R + half + c) = *reinterpret_cast<const float4*>(p.sin + at.pos * half + c);
-    }
+    const int tokens = p.B * p.T;
+    const int items = p.chunks * p.heads;                   // checked on the host to fit
+    const int row0 = (int)((int64_t)blockIdx.x * items / gridDim.x) * BWD_STEPS;
+    const int row1 = (int)((int64_t)(blockIdx.x + 1) * items / gridDim.x) * BWD_STEPS;
     int oa, ob;
     const bool turn = chunk_offsets<V, INTER>(g, p.R, &oa, &ob);
-    const bool weighted = p.norm && s.weight;
-    const bool want = p.norm && p.dw[s.grad_slot];
-    const bool by_head = want && p.dw_stride[s.grad_slot] != 0;
     uint64_t dw[V] = {};
-    // the partial row of the block's head h (or of all its heads): sums of the groups in a
-    // fixed order
-    auto leave = [&](int row) {
+
+    // Row i of this group: its stream and head, and its token; b < 0: there is none.
+    struct Row {
+        int item, step, si, h, b, t;
+    };
+    auto row_of = [&](int i) {
+        Row r;
+        r.item = i / BWD_STEPS;
+        r.step = i - r.item * BWD_STEPS;
+        const int chunk = p.by_heads.div(r.item);
+        r.h = r.item - chunk * p.heads;
+        for (r.si = 0; r.h >= p.s[r.si].heads; ++r.si) r.h -= p.s[r.si].heads;
+        const int tok = (chunk * BWD_STEPS + r.step) * GROUPS + group;
+        r.b = tok < tokens ? p.by_T.div(tok) : -1;
+        r.t = tok - r.b * p.T;
+        return r;
+    };
+    auto load = [&](int i) {
+        if (i < row1) {
+            const Row r = row_of(i);
+            const RowStream& s = p.s[r.si];
+            uint4* at = ring + (i % BWD_STAGES) * 4 * THREADS + tid;
+            if (r.b >= 0) {
+                if (p.norm) {
+                    const T* x = static_cast<const T*>(s.x) + r.b * s.sx[0] + r.h * s.sx[1] + r.t * s.sx[2];
+                    cp_async16(at, x + oa);
+                    cp_async16(at + THREADS, x + ob);
+                }
+                const T* gr = static_cast<const T*>(s.g) + r.b * s.sg[0] + r.h * s.sg[1] + r.t * s.sg[2];
+                cp_async16(at + 2 * THREADS, gr + oa);
+                cp_async16(at + 3 * THREADS, gr + ob);
+            }
+            if (r.step == 0 && s.weight && tid < D / 4)
+                cp_async16(weights + (r.item & 1) * D + 4 * tid, s.weight + r.h * s.w_stride + 4 * tid);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // The tables of a chunk's tokens; the caller has the barriers.
+    auto enter = [&](int chunk) {
+        const int tok0 = chunk * (BWD_STEPS * GROUPS), per = max(half / 4, 1);
+        for (int i = tid; i < BWD_STEPS * GROUPS * per; i += THREADS) {
+            const int k = i / per, c = (i - k * per) * 4;
+            if (tok0 + k >= tokens) continue;
+            const int b = p.by_T.div(tok0 + k);
+            const Token at = find_token(p, b, tok0 + k - b * p.T, false);
+            if (c == 0) {
+                fine[k] = at.ok;
+                if (!at.ok) atomicOr(p.status, kStatusIndex);
+            }
+            if (!at.ok || half == 0) continue;
+            *reinterpret_cast<float4*>(turns + k * p.R + c) = *reinterpret_cast<const float4*>(p.cos + at.pos * half + c);
+            *reinterpret_cast<float4*>(turns + k * p.R + half + c) = *reinterpret_cast<const float4*>(p.sin + at.pos * half + c);
+        }
+    };
+    // The item's partial row: sums of the groups in a fixed order.  (The next write of `red`
+    // comes after the next item's first barrier.)
+    auto leave = [&](int item) {
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
             float v = i & 1 ? f2_hi(dw[i / 2]) : f2_lo(dw[i / 2]);
@@ -433,59 +478,59 @@ rotary_bwd_kernel(const RotaryParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[i] = 0;
         __syncthreads();
-        for (int c = threadIdx.x; c < D; c += THREADS) {
+        for (int c = tid; c < D; c += THREADS) {
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < THREADS / 32; ++j) sum += red[j * D + c];
-            p.partial[((int64_t)row * gridDim.x + blockIdx.x) * D + c] = sum;
+            p.partial[(int64_t)item * D + c] = sum;         // [chunk][head]
         }
-        __syncthreads();
     };
-    __syncthreads();
-    struct Raw { uint4 x[2], g[2]; };
-    const int n = (head1 - head0) * BWD_STEPS;              // rows of this group: head by head
-    auto load = [&](int i, Raw& r) {
-        const int2 bt = i < n ? where[(i % BWD_STEPS) * GROUPS + group] : make_int2(-1, 0);
-        r.x[0] = r.x[1] = r.g[0] = r.g[1] = make_uint4(0, 0, 0, 0);
-        if (bt.x < 0) return;
-        const int h = head0 + i / BWD_STEPS, t = bt.y < 0 ? ~bt.y : bt.y;
-        if (p.norm) {
-            const T* x = static_cast<const T*>(s.x) + bt.x * s.sx[0] + h * s.sx[1] + t * s.sx[2];
-            r.x[0] = *reinterpret_cast<const uint4*>(x + oa);
-            r.x[1] = *reinterpret_cast<const uint4*>(x + ob);
+#pragma unroll
+    for (int i = 0; i < BWD_STAGES - 1; ++i) load(row0 + i);
+    int chunk = -1;
+    for (int i = row0; i < row1; ++i) {
+        load(i + BWD_STAGES - 1);
+        const Row r = row_of(i);
+        const RowStream& s = p.s[r.si];
+        asm volatile("cp.async.wait_group %0;" ::"n"(BWD_STAGES - 1) : "memory");
+        if (r.step == 0) {                  // a new item: its weights are there, and its tables
+            __syncthreads();
+            if (p.by_heads.div(r.item) != chunk) {
+                enter(chunk = p.by_heads.div(r.item));
+                __syncthreads();
+            }
         }
-        const T* gr = static_cast<const T*>(s.g) + bt.x * s.sg[0] + h * s.sg[1] + t * s.sg[2];
-        r.g[0] = *reinterpret_cast<const uint4*>(gr + oa);
-        r.g[1] = *reinterpret_cast<const uint4*>(gr + ob);
-    };
-    auto compute = [&](int i, const Raw& r) {
-        const int k = (i % BWD_STEPS) * GROUPS + group;
-        const int2 bt = where[k];
-        const int h = head0 + i / BWD_STEPS, t = bt.y < 0 ? ~bt.y : bt.y;
+        const uint4* at = ring + (i % BWD_STAGES) * 4 * THREADS + tid;
+        const int k = r.step * GROUPS + group;
+        const bool none = r.b < 0;
         uint64_t x[V], u[V];
-        Vec<T>::unpack(r.g[0], u);
-        Vec<T>::unpack(r.g[1], u + V / 2);
+        Vec<T>::unpack(at[2 * THREADS], u);
+        Vec<T>::unpack(at[3 * THREADS], u + V / 2);
         if (turn) {
             uint64_t cs[V / 2], sn[V / 2];
             load_pairs<V>(turns + k * p.R + g * V, cs);
             load_pairs<V>(turns + k * p.R + half + g * V, sn);
             rotate<V, INTER>(u, cs, sn, true);
         }
-        if (bt.x < 0 || bt.y < 0) {                         // no token: nothing; no position: NaN
+        if (none || !fine[k]) {                             // no token: nothing; no position: NaN
 #pragma unroll
-            for (int e = 0; e < V; ++e) u[e] = bt.x < 0 ? 0ull : 0x7fc000007fc00000ull;
+            for (int e = 0; e < V; ++e) u[e] = none ? 0ull : 0x7fc000007fc00000ull;
         }
         if (p.norm) {
-            Vec<T>::unpack(r.x[0], x);
-            Vec<T>::unpack(r.x[1], x + V / 2);
+            Vec<T>::unpack(at[0], x);
+            Vec<T>::unpack(at[THREADS], x + V / 2);
+            if (none) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[e] = 0ull;
+            }
             uint64_t g2[V], s1 = 0, s2 = 0;                 // w u, and the sums of x x and w u x
-            if (weighted) {
-                load_pairs<V>(s.weight + h * s.w_stride + oa, g2);
-                load_pairs<V>(s.weight + h * s.w_stride + ob, g2 + V / 2);
+            if (s.weight) {
+                load_pairs<V>(weights + (r.item & 1) * D + oa, g2);
+                load_pairs<V>(weights + (r.item & 1) * D + ob, g2 + V / 2);
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                g2[e] = weighted ? f2_mul(g2[e], u[e]) : u[e];
+                g2[e] = s.weight ? f2_mul(g2[e], u[e]) : u[e];
                 s1 = f2_fma(x[e], x[e], s1);
                 s2 = f2_fma(g2[e], x[e], s2);
             }
@@ -498,23 +543,13 @@ rotary_bwd_kernel(const RotaryParams p) {
                 u[e] = f2_fma(x[e], m2, f2_mul(g2[e], rr2));
             }
         }
-        if (bt.x >= 0) {
-            T* y = static_cast<T*>(s.y) + bt.x * s.sy[0] + h * s.sy[1] + t * s.sy[2];
+        if (!none) {
+            T* y = static_cast<T*>(s.y) + r.b * s.sy[0] + r.h * s.sy[1] + r.t * s.sy[2];
             *reinterpret_cast<uint4*>(y + oa) = Vec<T>::pack(u);
             *reinterpret_cast<uint4*>(y + ob) = Vec<T>::pack(u + V / 2);
         }
-        if (by_head && i % BWD_STEPS == BWD_STEPS - 1) leave(block_row(p, si) + h);
-    };
-    static_assert(BWD_STEPS % 2 == 0, "rows in pairs");
-    Raw a, b;
-    load(0, a);
-    for (int i = 0; i < n; i += 2) {
-        load(i + 1, b);
-        compute(i, a);
-        load(i + 2, a);
-        compute(i + 1, b);
+        if (r.step == BWD_STEPS - 1 && p.norm && p.dw[s.grad_slot]) leave(r.item);
     }
-    if (want && !by_head) leave(block_row(p, si) + head0);
 }
 
 template <typename T>
@@ -589,7 +624,7 @@ rotary_bwd_any_kernel(const RotaryParams p) {
     for (int c = threadIdx.x; c < p.D; c += THREADS) {
         float sum = 0.f;
         for (int j = 0; j < WARPS; ++j) sum += rows[j][c];
-        p.partial[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * p.D + c] = sum;
+        p.partial[((int64_t)blockIdx.x * p.heads + blockIdx.y) * p.D + c] = sum;
     }
 }
 
@@ -610,14 +645,12 @@ rotary_dw_kernel(const RotaryParams p, int q_rows) {
     int heads = 0;
     for (int i = 0; i < p.n; ++i) {
         if (p.s[i].grad_slot == slot && c < p.D) {
-            // the head's row, or those of the first heads of the blocks
-            const int rows = by_head ? 1 : (p.s[i].heads + p.heads_per_block - 1) / p.heads_per_block;
-            const int first = heads + (by_head ? out_row : 0);
+            const int rows = by_head ? 1 : p.s[i].heads, first = heads + (by_head ? out_row : 0);
             const int n = rows * p.chunks;
 #pragma unroll 8
             for (int j = part; j < n; j += parts) {
-                const int r = j / p.chunks;
-                sum += p.partial[((int64_t)(first + r * p.heads_per_block) * p.chunks + j - r * p.chunks) * p.D + c];
+                const int chunk = j / rows;
+                sum += p.partial[((int64_t)chunk * p.heads + first + j - chunk * rows) * p.D + c];
             }
         }
         heads += p.s[i].heads;
@@ -634,7 +667,7 @@ rotary_dw_kernel(const RotaryParams p, int q_rows) {
 template <typename T, int G, bool INTER>
 int launch_bwd(const RotaryParams& p, dim3 grid, cudaStream_t stream) {
     constexpr int D = G * 2 * Vec<T>::N, GROUPS = THREADS / G;
-    const auto bytes = [](int R) { return (BWD_STEPS * GROUPS * R + THREADS / 32 * D) * 4 + BWD_STEPS * GROUPS * 8; };
+    const auto bytes = [](int R) { return bwd_layout(GROUPS, D, R).total * 4; };
     if (cudaFuncSetAttribute(rotary_bwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(D)) !=
         cudaSuccess)
         return -1;
@@ -647,7 +680,8 @@ int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
     constexpr int V = Vec<T>::N;
     const int G = p.D / (2 * V);
     const int64_t tokens = (int64_t)p.B * p.T;
-    const dim3 grid((unsigned)(backward ? p.chunks : (tokens * G + THREADS - 1) / THREADS), (unsigned)p.head_blocks);
+    const dim3 grid((unsigned)(backward ? p.head_blocks : (tokens * G + THREADS - 1) / THREADS),
+                    backward ? 1u : (unsigned)p.head_blocks);
 #define DIFFATTN_ROTARY(GG)                                                               \
     if (G == GG) {                                                                        \
         if (backward) return launch_bwd<T, GG, INTER>(p, grid, stream);                   \
@@ -705,24 +739,22 @@ void plan_rotary(RotaryParams* p, int num_sms) {
     rot::set_head_blocks(p, hpb);
 }
 
-// The backward's blocks must not depend on the GPU, since the workspace is sized for
-// them: about 1200, of 8 heads at most.  Its partial rows: one a chunk and head where the
-// weights differ by head, else one a chunk and block.
-void plan_rotary_bwd(RotaryParams* p) {
-    const int groups = p->fast ? rot::THREADS / (p->D / (p->bf16 ? 16 : 8)) : rot::THREADS / 32;
+// The backward's items (see rotary_bwd_kernel), and its blocks: two an SM (head_blocks).
+void plan_rotary_bwd(RotaryParams* p, int num_sms) {
+    p->heads = 0;
+    for (int i = 0; i < p->n; ++i) p->heads += p->s[i].heads;
+    p->by_heads.set((uint32_t)p->heads);
     const int64_t tokens = (int64_t)p->B * p->T;
-    int heads = 0;
-    for (int i = 0; i < p->n; ++i) heads += p->s[i].heads;
     if (!p->fast) {                         // a head a block, and chunks in strides
         rot::set_head_blocks(p, 1);
-        const int64_t steps = (tokens + groups - 1) / groups, chunks = (2432 + heads - 1) / heads;
+        const int64_t steps = (tokens + 7) / 8, chunks = (2432 + p->heads - 1) / p->heads;
         p->chunks = (int)(chunks < steps ? chunks : steps);
         return;
     }
-    const int per = groups * rot::BWD_STEPS;
+    const int per = rot::THREADS / (p->D / (p->bf16 ? 16 : 8)) * rot::BWD_STEPS;
     p->chunks = (int)((tokens + per - 1) / per);
-    const int64_t want = (int64_t)p->chunks * heads / 1216;
-    rot::set_head_blocks(p, want < 1 ? 1 : want > 8 ? 8 : (int)want);
+    const int64_t items = (int64_t)p->chunks * p->heads;
+    p->head_blocks = (int)(items < 2 * num_sms ? items : 2 * num_sms);
 }
 
 size_t rotary_bwd_floats(int64_t B, int64_t T, int64_t D, int64_t heads) {

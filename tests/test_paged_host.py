@@ -88,6 +88,7 @@ def test_rotary_argument_refusals(lib):
     assert rotary(lib, rotary_desc(), cos=None) == INVALID
     assert rotary(lib, rotary_desc(norm=0), qw=p(30)) == INVALID
     assert rotary(lib, rotary_desc(B=1 << 20, T=1 << 20)) == UNSUPPORTED
+    assert rotary(lib, rotary_desc(B=1 << 15, T=1 << 15, H=300)) == UNSUPPORTED
     assert rotary(lib, rotary_desc(H=40000)) == UNSUPPORTED
 
 
