@@ -440,6 +440,7 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
     p.o4 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(d.o_stride[0] * es) | (uintptr_t)(d.o_stride[1] * es) |
             (uintptr_t)(d.o_stride[2] * es)) % 4 == 0;
+    p.o16 = rows16(out, d.o_stride, es);
     p.joins = static_cast<PagedJoin*>(workspace);
     p.part = reinterpret_cast<float*>(p.joins + n.workers);
     p.head_rows = n.head_rows;

@@ -327,13 +327,16 @@ paged_simt_kernel(const PagedParams p) {
 constexpr int C_WARPS = 8;
 constexpr int kJoinsPerBlock = 4;
 
-template <int J>
-__global__ void __launch_bounds__(C_WARPS * 32)
+// J columns a lane; VEC: J = 4 of them in a row, for a value width of 128 in bf16 (two
+// 16-byte reads a part instead of eight of 4 bytes).
+template <int J, bool VEC>
+__global__ void __launch_bounds__(C_WARPS * 32, J == 4 ? 4 : 2)
 paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
     // the words of this block's workers, all at once: most of them say that there is nothing
     int4 joins[kJoinsPerBlock];
 #pragma unroll
@@ -343,106 +346,122 @@ paged_combine_kernel(const PagedParams p) {
     }
 #pragma unroll 1
     for (int k = 0; k < kJoinsPerBlock; ++k) {
-    const int c = blockIdx.x + k * gridDim.x;
-    const int4 join = k == 0 ? joins[0] : k == 1 ? joins[1] : k == 2 ? joins[2] : joins[3];
-    const int parts = join.x, b = join.y, unit = join.z, n_new = join.w;
-    if (parts == 0) continue;
-    const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
-    const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
-    const int W = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : C_WARPS;
-    const int sub = warp % W;
-    const int step = gridDim.y * (C_WARPS / W);
-    for (int r0 = blockIdx.y * (C_WARPS / W); r0 < p.chunk_rows; r0 += step) {
-        const int r = r0 + warp / W;
-        const PagedRow x = paged_row(p, hk, rc, r, n_new);
-        const bool live = x.live && r < p.chunk_rows;
-        auto part_of = [&](int i) {
-            const int64_t slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-            return p.part + (slot * p.chunk_rows + r) * stride;
-        };
-        float o[2][J], l[2] = {0.f, 0.f};
+        const int c = blockIdx.x + k * gridDim.x;
+        const int4 join = k == 0 ? joins[0] : k == 1 ? joins[1] : k == 2 ? joins[2] : joins[3];
+        const int parts = join.x, b = join.y, unit = join.z, n_new = join.w;
+        if (parts == 0) continue;
+        const int hk = unit / p.row_chunks, rc = unit - hk * p.row_chunks;
+        const int W = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : C_WARPS;
+        const int sub = warp % W;
+        const int step = gridDim.y * (C_WARPS / W);
+        for (int r0 = blockIdx.y * (C_WARPS / W); r0 < p.chunk_rows; r0 += step) {
+            const int r = r0 + warp / W;
+            const PagedRow x = paged_row(p, hk, rc, r, n_new);
+            const bool live = x.live && r < p.chunk_rows;
+            auto part_of = [&](int i) {
+                const int64_t slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
+                return p.part + (slot * p.chunk_rows + r) * stride;
+            };
+            float o[2][J], l[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[0][j] = o[1][j] = 0.f;
-        if (live) {
-            // Loads first, and all that fit: the pass is the latency of L2, met once if no
-            // load waits for another's value.  So no branch on a weight either (a part that
-            // saw nothing holds zeros).
-            constexpr int AHEAD = 4;
-            float x[AHEAD][2][J];
-            float4 st[AHEAD];
-            auto load = [&](int i, int k) {
-                const float* src = part_of(min(i, parts - 1));
-                st[k] = *reinterpret_cast<const float4*>(src);
+            for (int j = 0; j < J; ++j) o[0][j] = o[1][j] = 0.f;
+            if (live) {
+                // Loads first, and all that fit: the pass is the latency of L2, met once if
+                // no load waits for another's value.  So no branch on a weight either (a
+                // part that saw nothing holds zeros).
+                constexpr int AHEAD = 2;
+                float4 v[AHEAD][2][(J + 3) / 4];
+                float4 st[AHEAD];
+                auto load = [&](int i, int k) {
+                    const float* src = part_of(min(i, parts - 1));
+                    st[k] = *reinterpret_cast<const float4*>(src);
+#pragma unroll
+                    for (int br = 0; br < 2; ++br) {
+                        const float* at = src + 4 + br * width;
+                        if constexpr (VEC) {
+                            v[k][br][0] = *reinterpret_cast<const float4*>(at + 4 * lane);
+                        } else {
+                            float* f = reinterpret_cast<float*>(v[k][br]);
+#pragma unroll
+                            for (int j = 0; j < J; ++j) f[j] = at[min(lane + 32 * j, p.Dv - 1)];
+                        }
+                    }
+                };
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) load(sub + k * W, k);
+                float m[2], m1, m2;
+                // where nothing was seen m_i is -inf, and l_i 0 (or NaN: a bad page) as it is
+                auto add_l = [&](float4 s4) {
+                    l[0] += s4.y * (s4.x == -INFINITY ? 1.f : exp2f(s4.x - m1));
+                    l[1] += s4.w * (s4.z == -INFINITY ? 1.f : exp2f(s4.z - m2));
+                };
+                if (parts == 2) {               // the most common: every lane has both
+                    m[0] = fmaxf(st[0].x, st[1].x);
+                    m[1] = fmaxf(st[0].z, st[1].z);
+                    m1 = m[0] == -INFINITY ? 0.f : m[0];
+                    m2 = m[1] == -INFINITY ? 0.f : m[1];
+                    add_l(st[0]);
+                    add_l(st[1]);
+                } else {
+                    const float4 own = *reinterpret_cast<const float4*>(part_of(min(lane, parts - 1)));
+                    m[0] = own.x;
+                    m[1] = own.z;
+                    for (int i = lane + 32; i < parts; i += 32) {
+                        const float4 s4 = *reinterpret_cast<const float4*>(part_of(i));
+                        m[0] = fmaxf(m[0], s4.x);
+                        m[1] = fmaxf(m[1], s4.z);
+                    }
+#pragma unroll
+                    for (int k = 16; k > 0; k >>= 1) {
+                        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], k));
+                        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], k));
+                    }
+                    m1 = m[0] == -INFINITY ? 0.f : m[0];
+                    m2 = m[1] == -INFINITY ? 0.f : m[1];
+                    for (int i = lane; i < parts; i += 32)
+                        add_l(i < 32 ? own : *reinterpret_cast<const float4*>(part_of(i)));
+#pragma unroll
+                    for (int k = 16; k > 0; k >>= 1) {
+                        l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+                        l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+                    }
+                }
+                for (int i = sub; i < parts; i += AHEAD * W) {
+                    if (i > sub) {
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k) load(i + k * W, k);
+                    }
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k) {
+                        if (i + k * W >= parts) continue;
+                        const float w[2] = {exp2f(st[k].x - m1), exp2f(st[k].z - m2)};
+#pragma unroll
+                        for (int br = 0; br < 2; ++br) {
+                            const float* f = reinterpret_cast<const float*>(v[k][br]);
+#pragma unroll
+                            for (int j = 0; j < J; ++j) o[br][j] = fmaf(w[br], f[j], o[br][j]);
+                        }
+                    }
+                }
+            }
+            if (W > 1) {
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const int col = min(lane + 32 * j, p.Dv - 1);
-                    x[k][0][j] = src[4 + col];
-                    x[k][1][j] = src[4 + width + col];
+                    share[warp][32 * j + lane] = o[0][j];
+                    share[warp][32 * (J + j) + lane] = o[1][j];
                 }
-            };
+                __syncthreads();
+                if (sub == 0)
+                    for (int w = 1; w < W; ++w)
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) load(sub + k * W, k);
-            float m[2] = {-INFINITY, -INFINITY};
-            const float4 own = *reinterpret_cast<const float4*>(part_of(min(lane, parts - 1)));
-            m[0] = own.x;
-            m[1] = own.z;
-            for (int i = lane + 32; i < parts; i += 32) {
-                const float4 s4 = *reinterpret_cast<const float4*>(part_of(i));
-                m[0] = fmaxf(m[0], s4.x);
-                m[1] = fmaxf(m[1], s4.z);
+                        for (int j = 0; j < J; ++j) {
+                            o[0][j] += share[warp + w][32 * j + lane];
+                            o[1][j] += share[warp + w][32 * (J + j) + lane];
+                        }
             }
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) {
-                m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], k));
-                m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], k));
-            }
-            // where nothing was seen m_i is -inf, and l_i 0 (or NaN: a bad page) as it is
-            const float m1 = m[0] == -INFINITY ? 0.f : m[0], m2 = m[1] == -INFINITY ? 0.f : m[1];
-            for (int i = lane; i < parts; i += 32) {
-                const float4 s4 = i < 32 ? own : *reinterpret_cast<const float4*>(part_of(i));
-                l[0] += s4.y * (s4.x == -INFINITY ? 1.f : exp2f(s4.x - m1));
-                l[1] += s4.w * (s4.z == -INFINITY ? 1.f : exp2f(s4.z - m2));
-            }
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) {
-                l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
-                l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
-            }
-            for (int i = sub; i < parts; i += AHEAD * W) {
-                if (i > sub) {
-#pragma unroll
-                    for (int k = 0; k < AHEAD; ++k) load(i + k * W, k);
-                }
-#pragma unroll
-                for (int k = 0; k < AHEAD; ++k) {
-                    if (i + k * W >= parts) continue;
-                    const float w1 = exp2f(st[k].x - m1), w2 = exp2f(st[k].z - m2);
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        o[0][j] = fmaf(w1, x[k][0][j], o[0][j]);
-                        o[1][j] = fmaf(w2, x[k][1][j], o[1][j]);
-                    }
-                }
-            }
+            if (live && sub == 0) paged_finish_row<J, VEC>(p, lam, b, x.h, x.q, lane, o[0], l[0], o[1], l[1]);
+            if (W > 1) __syncthreads();
         }
-        if (W > 1) {
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                share[warp][32 * j + lane] = o[0][j];
-                share[warp][32 * (J + j) + lane] = o[1][j];
-            }
-            __syncthreads();
-            if (sub == 0)
-                for (int w = 1; w < W; ++w)
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        o[0][j] += share[warp + w][32 * j + lane];
-                        o[1][j] += share[warp + w][32 * (J + j) + lane];
-                    }
-        }
-        if (live && sub == 0) paged_finish_row<J>(p, lam, b, x.h, x.q, lane, o[0], l[0], o[1], l[1]);
-        if (W > 1) __syncthreads();
-    }
     }
 }
 
@@ -478,10 +497,10 @@ int paged_simt_rows(int64_t rows) {
 
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    // a block a row where few rows may have many parts, else four rows a block
+    // a block a row where few rows may have many parts, else a row a warp
     // one word a block, but where most workers may not exist (paged_mma.cu)
     const int words = p.sparse_joins ? paged::kJoinsPerBlock : 1;
-    cfg.gridDim = dim3((unsigned)((p.workers + words - 1) / words), (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 3) / 4));
+    cfg.gridDim = dim3((unsigned)((p.workers + words - 1) / words), (unsigned)(p.chunk_rows <= 16 ? p.chunk_rows : (p.chunk_rows + 7) / 8));
     cfg.blockDim = dim3(paged::C_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -489,8 +508,10 @@ int launch_paged_combine(const PagedParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (p.Dv <= 128 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4>, p)
-                        : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8>, p)) == cudaSuccess ? 0 : -1;
+    const cudaError_t e = p.Dv == 128 && p.bf16 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true>, p)
+                          : p.Dv <= 128         ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, false>, p)
+                                                : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8, false>, p);
+    return e == cudaSuccess ? 0 : -1;
 }
 
 int launch_paged_simt(const PagedParams& p, cudaStream_t stream) {

@@ -128,7 +128,7 @@ struct PagedParams {
     int chunk_rows;
     int vec16;                  // rows of the caches are 16-byte aligned,
     int q16;                    // and of the queries
-    int o4;                     // output rows are 4-byte aligned
+    int o4, o16;                // output rows are 4-byte, 16-byte aligned
     int solo_workers;           // warps of the launch: one is a worker where units are many
     int workers;                // that share the first pass, at most
     int sparse_joins;           // a quarter of them may be all there are

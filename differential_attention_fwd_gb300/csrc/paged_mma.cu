@@ -266,8 +266,11 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         const bool la = ra.live && r0 < p.chunk_rows, lb = rb.live && r0 + 8 < p.chunk_rows;
         uint64_t ta = 0, tb = 0;
         if (p.mask && (int64_t)(cur.tile0 + cur.n) * KT > s.before) {
-            if (la) ta = paged_mask_bits(p, cur.b, ra.q, s.n_new);
-            if (lb) tb = paged_mask_bits(p, cur.b, rb.q, s.n_new);
+            // lane r reads row r's, then each thread takes its two rows'
+            const PagedRow x = paged_row(p, cur.hk, cur.rc, lane & 15, s.n_new);
+            const uint64_t bits = paged_mask_bits<NR>(p, cur.b, x.q, x.live && (lane & 15) < p.chunk_rows, s.n_new, lane);
+            ta = __shfl_sync(0xffffffffu, bits, r0);
+            tb = __shfl_sync(0xffffffffu, bits, r0 + 8);
         }
         float o[2][DV / 8][4];
         float m[2][2], l[2][2];

@@ -252,33 +252,52 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int hk, int 
     return x;
 }
 
-// Which of the new tokens row q sees, as bits (tree; Tq <= 64).
-__device__ __forceinline__ uint64_t paged_mask_bits(const PagedParams& p, int b, int q, int n_new) {
-    const uint8_t* m = p.mask + b * p.mask_stride[0] + q * p.mask_stride[1];
+// Which of the new tokens each lane's row q sees, as bits (tree; Tq <= 64), for the lanes
+// below N whose row is live; the others get 0.  The whole warp calls this: it reads one
+// row after another, a byte a lane, all of them at once (a row a thread, byte by byte,
+// took 3 to 5 us at a segment's start).
+template <int N>
+__device__ __forceinline__ uint64_t paged_mask_bits(const PagedParams& p, int b, int q, bool live, int n_new, int lane) {
+    const uint8_t* m = p.mask + b * p.mask_stride[0];
     uint64_t bits = 0;
-    // 16 loads at a time: one after another their latencies would add up
-    for (int j0 = 0; j0 < n_new; j0 += 16) {
-        uint32_t part = 0;
+    constexpr int AT_ONCE = N < 16 ? N : 16;
+    const int c0 = min(lane, n_new - 1), c1 = min(lane + 32, n_new - 1);
+    const uint32_t has0 = n_new >= 32 ? ~0u : (1u << n_new) - 1;
+    const uint32_t has1 = n_new <= 32 ? 0u : n_new >= 64 ? ~0u : (1u << (n_new - 32)) - 1;
+    const int64_t at = live ? q * p.mask_stride[1] : 0;
+    for (int r0 = 0; r0 < N; r0 += AT_ONCE) {
+        // no branch around a load, so that none waits for another
+        uint8_t x[AT_ONCE][2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part |= (uint32_t)(j0 + j < n_new ? m[j0 + j] != 0 : 0) << j;
-        bits |= (uint64_t)part << j0;
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t row = __shfl_sync(0xffffffffu, at, r0 + i);
+            x[i][0] = m[row + c0];
+            x[i][1] = m[row + c1];
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const uint32_t lo = __ballot_sync(0xffffffffu, x[i][0] != 0), hi = __ballot_sync(0xffffffffu, x[i][1] != 0);
+            if (lane == r0 + i && live) bits = (uint64_t)(hi & has1) << 32 | (lo & has0);
+        }
     }
     return bits;
 }
 
-// One row's output from O_b and l_b of both branches: columns lane + 32 j, j < J.
-template <int J>
+// One row's output from O_b and l_b of both branches: columns lane + 32 j, j < J, or
+// J lane + j where ROWWISE.
+template <int J, bool ROWWISE = false>
 __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam, int b, int h, int q, int lane,
                                                  const float (&o1)[J], float l1, const float (&o2)[J], float l2) {
     const float i1 = l1 == 0.f ? 0.f : 1.f / l1;       // a row that saw nothing gives 0
     const float i2 = l2 == 0.f ? 0.f : 1.f / l2;
+    const auto col = [&](int j) { return ROWWISE ? J * lane + j : lane + 32 * j; };
     float y[J];
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         // the branches rounded alike, so that alike branches cancel exactly at lambda = 1
         y[j] = fmaf(-lam, __fmul_rn(o2[j], i2), __fmul_rn(o1[j], i1));
-        if (lane + 32 * j >= p.Dv) y[j] = 0.f;
+        if (col(j) >= p.Dv) y[j] = 0.f;
         sum += y[j];
     }
     if (p.norm != kNormNone) {
@@ -291,7 +310,7 @@ __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            if (lane + 32 * j < p.Dv) {
+            if (col(j) < p.Dv) {
                 y[j] -= mean;
                 ss = fmaf(y[j], y[j], ss);
             }
@@ -304,14 +323,22 @@ __device__ __forceinline__ void paged_finish_row(const PagedParams& p, float lam
     const int64_t at = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int c = lane + 32 * j;
+        const int c = col(j);
         if (c >= p.Dv) continue;
         float v = y[j];
         if (p.norm_weight) v *= p.norm_weight[(int64_t)h * p.Dv + c];
         if (p.norm_bias) v += p.norm_bias[(int64_t)h * p.Dv + c];
         v *= p.out_scale;
+        y[j] = v;
+        if (ROWWISE && p.o4) continue;
         if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at + c] = __float2bfloat16_rn(v);
         else static_cast<float*>(p.out)[at + c] = v;
+    }
+    if constexpr (ROWWISE) {                    // bf16, all columns live
+        if (p.o4)
+#pragma unroll
+            for (int j = 0; j < J; j += 2)
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at + col(j)) = pack_bf16x2(y[j], y[j + 1]);
     }
 }
 

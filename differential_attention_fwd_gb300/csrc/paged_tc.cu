@@ -75,7 +75,7 @@ enum : int {
     B_P_FULL = B_S_FULL + 4,                    // [branch][buffer]
     B_PV_DONE = B_P_FULL + 4,                   // [branch]
     B_O_FULL = B_PV_DONE + 2, B_O_EMPTY,
-    B_ROWS_OUT, B_ROWS_READ,                    // a whole unit's rows written, and read back
+    B_ROWS,                                     // sums exchanged between the warpgroups
     B_FINAL,                                    // [branch]
     NUM_BARS = B_FINAL + 2
 };
@@ -97,6 +97,22 @@ constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, DV, 0, 1);
 __device__ __forceinline__ uint32_t tm_s(int br, int buf) { return br * 128 + buf * 64; }
 
 __device__ __forceinline__ bool bf16_finite(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
+
+// The 32 x 32 words that a warp holds, a row a lane, turned: lane j's o[i] goes to lane i's
+// o[j].  Five rounds that swap ever smaller halves between lanes.
+__device__ __forceinline__ void transpose32(uint32_t (&o)[32], uint32_t lane) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i & m) continue;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[i] : o[i + m], m);
+            if (up) o[i] = got;
+            else o[i + m] = got;
+        }
+    }
+}
 
 // A bf16 pair with zeros for what is not finite.
 __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
@@ -147,8 +163,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         mbar_init(&bars[B_Q_EMPTY], 2);
         mbar_init(&bars[B_O_FULL], 2);
         mbar_init(&bars[B_O_EMPTY], 8);
-        mbar_init(&bars[B_ROWS_OUT], 8);
-        mbar_init(&bars[B_ROWS_READ], 8);
+        mbar_init(&bars[B_ROWS], 8);
         for (int i = 0; i < SEGS; ++i) bad_seg[i] = any_flag[i] = 0;
         *abort_flag = 0;
         fence_mbar_init();
@@ -312,9 +327,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                                 const int key = 2 * (j0 + j) + (int)(lane >> 4);
                                 const bool past = tile * KT + key >= cur.s.total;
                                 const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                                bool odd = false;
+                                // an exponent of ones carries into the sign's place
+                                uint32_t ones = 0;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) odd |= !bf16_finite(w[e]) | !bf16_finite(w[e] >> 16);
+                                for (int e = 0; e < 4; ++e) ones |= (w[e] & 0x7f807f80u) + 0x00800080u;
+                                const bool odd = (ones & 0x80008000u) != 0;
                                 if (past) {
                                     *value_at(vt, key, lane & 15) = make_uint4(0, 0, 0, 0);
                                 } else if (odd) {
@@ -421,12 +438,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         const uint32_t quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
-        const uint32_t tO = lane_base + TM_O + br * 128;
+        const uint32_t tO = lane_base + TM_O + br * 128;     // this branch's O
         const float sl2 = p.scale_log2;
         const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
-        uint32_t sph = 0, ofph = 0, wph = 0, rph = 0;
+        uint32_t sph = 0, ofph = 0, wph = 0;
         uint32_t pv_count = 0;
-        bool ok = true, wrote_whole = false;
+        bool ok = true;
         int seg = -1;
         for (; ok && !cur.done(); cur.next(p, KT)) {
             const int live = cur.live_tiles(p, KT);
@@ -435,7 +452,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             const PagedRow x = paged_row(p, cur.hk, cur.rc, row, s.n_new);
             const bool mine = x.live && row < p.chunk_rows;
             uint64_t tree = 0;
-            if (p.mask && mine && (int64_t)(cur.tile0 + live) * KT > s.before) tree = paged_mask_bits(p, cur.b, x.q, s.n_new);
+            if (p.mask && (int64_t)(cur.tile0 + live) * KT > s.before)
+                tree = paged_mask_bits<32>(p, cur.b, x.q, mine, s.n_new, lane);
             float m_run = NOTHING, l = 0.f;
             for (int j = 0; j < live; ++j) {
                 const int buf = j & 1;
@@ -498,40 +516,61 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             }
             if (!ok) break;
             pv_count += live;
-            // ---- the row's partial result; a unit that is whole is read back and finished
             if (live > 0) {
                 if (!(ok = mbar_wait_warp(&bars[B_O_FULL], ofph, ab))) break;
                 ofph ^= 1;
                 tc_fence_after();
             }
-            if (wrote_whole) {              // its rows have been read by every warp
-                if (!(ok = mbar_wait_warp(&bars[B_ROWS_READ], rph, ab))) break;
-                rph ^= 1;
-                wrote_whole = false;
-            }
+            // Every exchange between the warps is a phase of one barrier.
+            auto exchange = [&]() -> bool {
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_ROWS]);
+                const bool got = mbar_wait_warp(&bars[B_ROWS], wph, ab);
+                wph ^= 1;
+                return got;
+            };
+            // a segment without tiles: the last one's exchanges must be over before its places
+            // are written again (with tiles, the weights' barriers see to that)
+            if (live == 0 && !(ok = exchange())) break;
             if (s.bad || (live > 0 && bad_seg[seg % SEGS])) l = __int_as_float(0x7fc00000);
             const bool odd = live > 0 && any_flag[seg % SEGS] != 0;
-            float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row) * (4 + 2 * DV);
+            float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row) * paged_part_floats(DV);
             if (mine) *reinterpret_cast<float2*>(part + 2 * br) = make_float2(m_run, l);
+            // O may be overwritten once every warp has read its share of it
+            auto release_o = [&]() {
+                if (live == 0) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_O_EMPTY]);
+            };
+            if (!cur.whole() || odd) {
+                // ---- a partial result: this branch's 128 columns of the row.  A row a lane, as
+                // TMEM gives it, is 32 lines a store (4 us a segment), so it is turned within
+                // the warp to a row a store.  Loops that stay loops, here and below: this code
+                // runs once or twice a block, and its first fetch is what it costs (17 us for
+                // the first segment with the four column groups unrolled).
+                const unsigned rows = __ballot_sync(0xffffffffu, mine);
+                float* at = p.part + ((int64_t)cur.slot() * p.chunk_rows + quad * 32) * paged_part_floats(DV) + 4 + br * DV + lane;
+#pragma unroll 1
+                for (int c = 0; c < DV; c += 32) {
+                    uint32_t o[32] = {};
+                    if (live > 0) {
+                        tmem_ld32(tO + c, o);
+                        tmem_wait_ld();
+                    }
+                    transpose32(o, lane);
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-                uint32_t o[32];
-                if (live > 0) {
-                    tmem_ld32(tO + c4 * 32, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                    for (int i = 0; i < 32; ++i)
+                        if (rows >> i & 1u) at[i * paged_part_floats(DV) + c] = __uint_as_float(o[i]);
                 }
-                if (c4 == 3 && live > 0) {
-                    tc_fence_before();
+                release_o();
+                if (odd) {
+                    // to the row, the values that are not finite of keys that it sees
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[B_O_EMPTY]);
-                }
-                if (odd && mine) {
-                    // values that are not finite, of keys that this row sees
                     const int edge0 = (int)(s.before / KT);
-                    for (int f = 0; f < FLAGS; ++f) {
+#pragma unroll 1
+                    for (int f = 0; mine && f < FLAGS; ++f) {
                         uint64_t keys = flags[(seg % SEGS) * FLAGS + f];
                         if (keys) keys &= tile_mask(p, s, (edge0 + f) * KT, x.q, tree);
                         while (keys) {
@@ -541,33 +580,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                             if (page < 0) continue;
                             const uint16_t* v = reinterpret_cast<const uint16_t*>(
                                 static_cast<const __nv_bfloat16*>(p.v) + page * p.s_v[0] + cur.hk * p.s_v[1] +
-                                (int64_t)(key % p.page) * p.s_v[2] + c4 * 32);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const uint32_t w = v[i];
-                                if (!bf16_finite(w)) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(w << 16));
-                            }
+                                (int64_t)(key % p.page) * p.s_v[2]);
+#pragma unroll 1
+                            for (int c = 0; c < DV; ++c)
+                                if (!bf16_finite(v[c])) part[4 + br * DV + c] += __uint_as_float((uint32_t)v[c] << 16);
                         }
                     }
                 }
-                if (mine) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(part + 4 + br * DV + c4 * 32 + 4 * i) =
-                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                }
-            }
-            if (cur.whole()) {
-                __threadfence_block();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_ROWS_OUT]);
-                if (!(ok = mbar_wait_warp(&bars[B_ROWS_OUT], wph, ab))) break;
-                wph ^= 1;
-#pragma unroll 2
+                if (!cur.whole()) continue;
+                // a whole unit with such a value is finished from the workspace
+                if (!(ok = exchange())) break;
+#pragma unroll 1
                 for (int r = warp; r < p.chunk_rows; r += 8) {
                     const PagedRow y = paged_row(p, cur.hk, cur.rc, r, s.n_new);
                     if (!y.live) continue;
-                    const float* src = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * (4 + 2 * DV);
+                    const volatile float* src = p.part + ((int64_t)cur.slot() * p.chunk_rows + r) * paged_part_floats(DV);
                     float o1[DV / 32], o2[DV / 32];
 #pragma unroll
                     for (int i = 0; i < DV / 32; ++i) {
@@ -576,9 +603,80 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                     }
                     paged_finish_row<DV / 32>(p, lam, cur.b, y.h, y.q, lane, o1, src[1], o2, src[3]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_ROWS_READ]);
-                wrote_whole = true;
+                if (!(ok = exchange())) break;
+                continue;
+            }
+            // ---- a whole unit: this warpgroup takes 64 columns of both branches' O.  The
+            // other's sums come through the row's place in the workspace: shared memory is full.
+            if (!(ok = exchange())) break;
+            const volatile float* sums = part;
+            float i1 = 0.f, i2 = 0.f;
+            if (mine) {
+                const float l1 = sums[1], l2 = sums[3];
+                i1 = l1 == 0.f ? 0.f : 1.f / l1;            // a row that saw nothing gives 0
+                i2 = l2 == 0.f ? 0.f : 1.f / l2;
+            }
+            const int c0 = br * 64;
+            float y[64];
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t o1[32] = {}, o2[32] = {};
+                if (live > 0) {
+                    tmem_ld32(lane_base + TM_O + c0 + c, o1);
+                    tmem_ld32(lane_base + TM_O + 128 + c0 + c, o2);
+                    tmem_wait_ld();
+                }
+                if (c == 32) release_o();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    y[c + i] = fmaf(-lam, __fmul_rn(__uint_as_float(o2[i]), i2), __fmul_rn(__uint_as_float(o1[i]), i1));
+                    sum += y[c + i];
+                }
+            }
+            if (p.norm != kNormNone) {
+                float mean = 0.f;
+                if (p.norm == kNormGroup) {
+                    if (mine) part[4 + br] = sum;
+                    if (!(ok = exchange())) break;
+                    if (mine) mean = (sums[4] + sums[5]) / DV;
+                }
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    y[i] -= mean;
+                    ss = fmaf(y[i], y[i], ss);
+                }
+                if (mine) part[6 + br] = ss;
+                if (!(ok = exchange())) break;
+                if (mine) {
+                    const float r = 1.0f / sqrtf((sums[6] + sums[7]) / DV + p.norm_eps);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) y[i] *= r;
+                }
+            }
+            if (mine) {
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + cur.b * p.s_o[0] + x.h * p.s_o[1] + x.q * p.s_o[2] + c0;
+                const float* wt = p.norm_weight ? p.norm_weight + (int64_t)x.h * DV + c0 : nullptr;
+                const float* bias = p.norm_bias ? p.norm_bias + (int64_t)x.h * DV + c0 : nullptr;
+#pragma unroll
+                for (int i = 0; i < 64; i += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = y[i + e];
+                        if (wt) v[e] *= wt[i + e];
+                        if (bias) v[e] += bias[i + e];
+                        v[e] *= p.out_scale;
+                    }
+                    if (p.o16) {
+                        *reinterpret_cast<uint4*>(out + i) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) out[i + e] = __float2bfloat16_rn(v[e]);
+                    }
+                }
             }
         }
     }
