@@ -141,7 +141,7 @@ int check_paged(const diffattn_paged_desc* d, const diffattn_pages* g) {
     if (rc != DIFFATTN_OK) return rc;
     // the tiles of all units in 31 bits, 16 keys a tile and 16 rows a unit at least
     const double keys = (double)g->max_pages * g->page_size, rows = (double)group * d->Tq;
-    if (keys > INT32_MAX / 2 || d->B * (keys / 16 + 1) * (double)(d->H / group) * (rows / 16 + 1) > INT32_MAX)
+    if (keys > INT32_MAX / 2 || d->B * (keys / 16 + 8) * (double)(d->H / group) * (rows / 16 + 1) > INT32_MAX)
         return DIFFATTN_ERR_UNSUPPORTED;
     if (d->Tq > 1024 || d->B > (1 << 24) || d->H > (1 << 20) || d->B * d->H > (1ll << 31) / 1024)
         return DIFFATTN_ERR_UNSUPPORTED;

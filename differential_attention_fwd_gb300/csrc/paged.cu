@@ -23,6 +23,7 @@ constexpr int WARPS = THREADS / 32;
 constexpr int KT = 32;
 constexpr int MAX_RC = 16;
 constexpr int SNAP = 2;
+constexpr int EXTRA = 1;                        // what a unit's start costs, in tiles
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -95,7 +96,7 @@ paged_simt_kernel(const PagedParams p) {
     float* st_l = st_m + 2 * RC;
     float* st_a = st_l + 2 * RC;
     pdl_launch_dependents();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, scan), KT, 1, p.workers, 1, SNAP, &blk);
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, 1, SNAP, &blk);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
@@ -106,10 +107,10 @@ paged_simt_kernel(const PagedParams p) {
 
     PagedCursor cur;
     if (tid == 0) PagedCursor::no_join(p, blockIdx.x);
-    for (cur.begin(p, blk, 0, blockIdx.x, KT); !cur.done(); cur.next(p, KT)) {
+    for (cur.begin(p, blk, 0, blockIdx.x, KT, EXTRA); !cur.done(); cur.next(p, KT, EXTRA)) {
         const int live = cur.live_tiles(p, KT);
         const int n_new = cur.s.n_new;
-        if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP);
+        if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP, EXTRA);
         bool bad = cur.s.bad;
         // the rows' queries and state
         for (int i = tid; i < 2 * RC * L.dpad; i += THREADS) {

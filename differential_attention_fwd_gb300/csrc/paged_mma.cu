@@ -48,6 +48,7 @@ constexpr int NR = 16;                          // rows of a unit
 constexpr int DV = 128;
 constexpr int PANEL = SLICE * 128;              // 2 KB: 16 keys x 64 columns
 constexpr int SNAP = 1;                         // tiles at a unit's end that are not worth another part
+constexpr int EXTRA = 1;                        // what a unit's start costs, in tiles
 
 // Shared memory: a ring for each pair, the queries (one warp a worker: WARP_ROWS a warp;
 // else 16 rows of the block, and the maxima and sums of its warps), barriers.
@@ -138,10 +139,10 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     }
     // One warp a worker where that makes at most two workers a unit, and if the unit's rows
     // allow it.  (The barriers in here order the above.)
-    const PagedScan found = paged_scan<THREADS>(p, KT, scan);
+    const PagedScan found = paged_scan<THREADS>(p, KT, EXTRA, scan);
     const bool solo = p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
     const int nw = solo ? WARPS : 1;                            // workers of the block
-    paged_locate<WARPS>(p, found, KT, nw, gridDim.x * nw, 1, SNAP, &blk);
+    paged_locate<WARPS>(p, found, KT, EXTRA, nw, gridDim.x * nw, 1, SNAP, &blk);
     const int mine = solo ? w : 0;
     const int worker = blockIdx.x * nw + mine;
     // the warp's slices in a tile: all four, or one
@@ -151,7 +152,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     if (warp >= WARPS) {
         // ---------------------------------------------------------------- producer
         regs_dec<REGS_PRODUCER>();
-        cur.begin(p, blk, mine, worker, KT);
+        cur.begin(p, blk, mine, worker, KT, EXTRA);
         const bool scribe = lane == 0 && (solo || w == 0);
         if (lane == 0) {
             tma_prefetch_desc(&tm_k1);
@@ -168,9 +169,9 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         int st = 0;
         uint32_t ph = 1;                        // the first pass over the ring finds it free
         bool ok = true;
-        for (; ok && !cur.done(); cur.next(p, KT)) {
+        for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
             const int live = cur.live_tiles(p, KT) * slices;
-            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, SNAP);
+            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, SNAP, EXTRA);
             int page = 0;                       // of slice i0 + lane, looked up 32 at a time
             for (int i = 0; i < live; ++i) {
                 // slice i of the warp: the key it starts with
@@ -213,7 +214,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 
     // -------------------------------------------------------------------- consumers
     regs_inc<REGS_CONSUMER>();
-    cur.begin(p, blk, mine, worker, KT);
+    cur.begin(p, blk, mine, worker, KT, EXTRA);
     const float sl2 = p.scale_log2;
     const int r0 = lane >> 2;                   // this thread's rows r0 and r0 + 8
     // the worker's queries: [branch][panel] rows of 128 bytes
@@ -228,7 +229,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;                             // after a failed wait: no more work, but every barrier
-    for (; !cur.done(); cur.next(p, KT)) {
+    for (; !cur.done(); cur.next(p, KT, EXTRA)) {
         const int live = cur.live_tiles(p, KT) * slices;
         const PagedSeq s = cur.s;
         bool bad = s.bad;

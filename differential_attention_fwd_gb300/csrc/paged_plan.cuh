@@ -100,7 +100,7 @@ struct PagedScan {
     int total, units;   // of the launch
 };
 template <int THREADS>
-__device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, int* scratch) {
+__device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, int extra, int* scratch) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_seq = p.Hk * p.row_chunks;
@@ -112,7 +112,7 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
     int active = 0;
     for (int b = s.b0; b < s.b1; ++b) {
         const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
-        s.sum += tiles * per_seq;
+        s.sum += tiles ? (tiles + extra) * per_seq : 0;
         active += tiles ? per_seq : 0;
     }
     int incl = s.sum;
@@ -142,7 +142,7 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
 // Where the block's `nw` <= NW workers start, of `most` in the launch, and the one after.
 // Every thread calls this, and it ends with a barrier.
 template <int NW>
-__device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedScan& s, int kt, int nw, int most,
+__device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedScan& s, int kt, int extra, int nw, int most,
                                              int min_tiles, int snap, PagedBlock<NW>* out) {
     const int tid = threadIdx.x;
     const int units = p.Hk * p.row_chunks;
@@ -155,10 +155,12 @@ __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedSc
         if (first >= s.total || first < s.at || first >= s.at + s.sum) continue;
         int at = s.at;
         for (int b = s.b0; b < s.b1; ++b) {
-            const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+            int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+            if (tiles == 0) continue;
+            tiles += extra;
             if (first < at + tiles * units) {
                 const int off = (first - at) % tiles;       // in its unit
-                const int move = off <= snap ? -off : tiles - off <= snap ? tiles - off : 0;
+                const int move = off <= extra + snap ? -off : tiles - off <= snap ? tiles - off : 0;
                 out->start[w] = PagedStart{first + move, b, first + move - at};
                 break;
             }
@@ -175,13 +177,14 @@ struct PagedCursor {
     int worker;
     int b;
     int hk, rc;                 // the segment's unit: key/value head and row chunk
-    int tile0, n;               // the segment's tiles within the unit
+    int tile0, n;               // the segment's tiles within the unit,
+    int step;                   // and how many they count as
     int tiles;                  // the unit's
     PagedSeq s;
 
     // The `w`-th worker of the block, worker c of the launch.
     template <int NW>
-    __device__ __forceinline__ void begin(const PagedParams& p, const PagedBlock<NW>& blk, int w, int c, int kt) {
+    __device__ __forceinline__ void begin(const PagedParams& p, const PagedBlock<NW>& blk, int w, int c, int kt, int extra) {
         worker = c;
         left = blk.start[w + 1].tile - blk.start[w].tile;
         b = blk.start[w].b;
@@ -189,10 +192,10 @@ struct PagedCursor {
         if (left <= 0) return;
         s = paged_seq(p, b);
         tiles = paged_seq_tiles(s, kt);
-        enter(p, kt);
+        enter(p, kt, extra);
     }
-    __device__ __forceinline__ void enter(const PagedParams& p, int kt) {
-        if (local == tiles * p.Hk * p.row_chunks) {
+    __device__ __forceinline__ void enter(const PagedParams& p, int kt, int extra) {
+        if (local == (tiles + extra) * p.Hk * p.row_chunks) {
             local = 0;
             do {
                 if (++b >= p.B) { left = 0; return; }   // never with tiles left
@@ -200,17 +203,18 @@ struct PagedCursor {
             } while (s.n_new == 0);
             tiles = paged_seq_tiles(s, kt);
         }
-        const int unit = local / tiles;
-        tile0 = local - unit * tiles;
-        n = min(left, tiles - tile0);
+        const int counts = tiles + extra, unit = local / counts, off = local - unit * counts;
+        step = min(left, counts - off);
+        tile0 = max(0, off - extra);
+        n = off + step - extra - tile0;
         hk = unit / p.row_chunks;
         rc = unit - hk * p.row_chunks;
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
-    __device__ __forceinline__ void next(const PagedParams& p, int kt) {
-        left -= n;
-        local += n;
-        if (left > 0) enter(p, kt);
+    __device__ __forceinline__ void next(const PagedParams& p, int kt, int extra) {
+        left -= step;
+        local += step;
+        if (left > 0) enter(p, kt, extra);
     }
     __device__ __forceinline__ bool whole() const { return n == tiles; }
     __device__ __forceinline__ int slot() const { return 2 * worker + (tile0 == 0 ? 1 : 0); }
@@ -219,9 +223,9 @@ struct PagedCursor {
     // this range's last, and the workers that go on with it are those whose bounds fall
     // into it and were not moved to its ends.  `end`: where this range ends.
     __device__ __forceinline__ static void no_join(const PagedParams& p, int c) { p.joins[c].parts = 0; }
-    __device__ __forceinline__ void join(const PagedParams& p, const PagedShares& sh, int end, int snap) const {
+    __device__ __forceinline__ void join(const PagedParams& p, const PagedShares& sh, int end, int snap, int extra) const {
         if (tile0 != 0 || whole()) return;
-        const int u1 = end - n + tiles;
+        const int u1 = end - step + tiles + extra;
         p.joins[worker] = PagedJoin{sh.worker_at(u1 - snap - 1) - worker + 1, b, hk * p.row_chunks + rc, s.n_new};
     }
     // The segment's tiles that some row of its chunk may see: later ones hold only

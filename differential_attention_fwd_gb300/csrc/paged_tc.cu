@@ -40,6 +40,7 @@ constexpr int BM = 128;
 constexpr int KT = 64;
 constexpr int DV = 128;
 constexpr int SNAP = 3;
+constexpr int EXTRA = 6;                        // what a unit's start costs, in tiles
 constexpr int THREADS = 384;
 // launched at 168 registers a thread: 256 x 200 + 128 x 104 = 384 x 168
 constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
@@ -177,7 +178,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, scan), KT, 1, p.workers, 1, SNAP, &blk);    // with their barriers
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, 1, SNAP, &blk);    // with their barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
     const uint64_t lim = 200ull * 1000ull * 1000ull;
@@ -185,7 +186,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
 
     if (warp >= 8) {
         regs_dec<REGS_OTHER>();
-        cur.begin(p, blk, 0, blockIdx.x, KT);
+        cur.begin(p, blk, 0, blockIdx.x, KT, EXTRA);
         if (warp == 8) {
             // ------------------------------------------------------------ producer
             if (lane == 0) {
@@ -201,10 +202,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             bool ok = true;
             if (lane == 0) PagedCursor::no_join(p, blockIdx.x);
             int seg = -1;                       // segments with tiles, as every role counts them
-            for (; ok && !cur.done(); cur.next(p, KT)) {
+            for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
                 const int live = cur.live_tiles(p, KT);
                 if (cur.s.bad && lane == 0) atomicOr(p.status, kStatusIndex);
-                if (lane == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP);
+                if (lane == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP, EXTRA);
                 if (live == 0) continue;
                 ++seg;
                 if (lane == 0) bad_seg[seg % SEGS] = 0;
@@ -302,7 +303,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             uint32_t vst = 0, vph = 0;
             bool ok = true;
             int seg = -1;
-            for (; ok && !cur.done(); cur.next(p, KT)) {
+            for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
                 const int live = cur.live_tiles(p, KT);
                 if (live == 0) continue;
                 ++seg;
@@ -379,7 +380,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                     mma_commit(&bars[B_S_FULL + 2 * br + buf]);
                     mma_commit(&bars[B_K_EMPTY + stage]);
                 };
-                for (; ok && !cur.done(); cur.next(p, KT)) {
+                for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
                     const int n = cur.live_tiles(p, KT);
                     if (n == 0) continue;
                     const int edge0 = (int)(cur.s.before / KT);
@@ -433,7 +434,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     } else {
         // ------------------------------------------------------ weights and results
         regs_inc<REGS_SOFTMAX>();
-        cur.begin(p, blk, 0, blockIdx.x, KT);
+        cur.begin(p, blk, 0, blockIdx.x, KT, EXTRA);
         const int br = warp >> 2;
         const uint32_t quad = warp & 3;
         const int row = quad * 32 + lane;
@@ -445,7 +446,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         uint32_t pv_count = 0;
         bool ok = true;
         int seg = -1;
-        for (; ok && !cur.done(); cur.next(p, KT)) {
+        for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
             const int live = cur.live_tiles(p, KT);
             if (live > 0) ++seg;
             const PagedSeq s = cur.s;
