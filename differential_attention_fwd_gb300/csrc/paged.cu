@@ -113,16 +113,14 @@ paged_simt_kernel(const PagedParams p) {
         if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP, EXTRA);
         bool bad = cur.s.bad;
         // the rows' queries and state
-        for (int i = tid; i < 2 * RC * L.dpad; i += THREADS) {
-            const int br = i / (RC * L.dpad), r = i / L.dpad % RC, c = i % L.dpad;
+#pragma unroll
+        for (int j0 = 0; j0 < 2 * RC; j0 += WARPS) {
+            const int j = j0 + warp, br = j / RC, r = j % RC;      // a warp a row
+            if (j >= 2 * RC) break;
             const PagedRow x = paged_row(p, cur.hk, cur.rc, r, n_new);
-            float v = 0.f;
-            if (x.live && c < D) {
-                const T* src = br ? static_cast<const T*>(p.q2) + cur.b * p.s_q2[0] + x.h * p.s_q2[1] + x.q * p.s_q2[2]
-                                  : static_cast<const T*>(p.q1) + cur.b * p.s_q1[0] + x.h * p.s_q1[1] + x.q * p.s_q1[2];
-                v = to_float<T>(src[c]);
-            }
-            qs[i] = v;
+            const T* src = br ? static_cast<const T*>(p.q2) + cur.b * p.s_q2[0] + x.h * p.s_q2[1] + x.q * p.s_q2[2]
+                              : static_cast<const T*>(p.q1) + cur.b * p.s_q1[0] + x.h * p.s_q1[1] + x.q * p.s_q1[2];
+            for (int c = lane; c < L.dpad; c += 32) qs[j * L.dpad + c] = x.live && c < D ? to_float<T>(src[c]) : 0.f;
         }
         if (tid < 2 * RC) { st_m[tid] = -INFINITY; st_l[tid] = 0.f; }
         float acc[2][2][RC];
@@ -131,19 +129,20 @@ paged_simt_kernel(const PagedParams p) {
 #pragma unroll
             for (int r = 0; r < RC; ++r) acc[i][0][r] = acc[i][1][r] = 0.f;
 
-        // Stage a tile: four threads a key row.  A row past the sequence's end or on a
-        // page outside the cache is zeros (the latter makes the segment's rows NaN).
-        auto stage = [&](int tile, int buf) {
+        // Stage a tile: four threads a key row, whose page was looked up a tile before.  A row
+        // past the sequence's end or on a page outside the cache is zeros (the latter makes
+        // the segment's rows NaN).
+        auto look = [&](int tile) -> int {
+            const int key = (cur.tile0 + tile) * KT + (tid >> 2);
+            return tile < live && key < cur.s.total ? paged_page(p, cur.b, key / p.page) : -2;
+        };
+        auto stage = [&](int tile, int buf, int page) {
             const int r = tid >> 2, c4 = tid & 3;
             const int key = (cur.tile0 + tile) * KT + r;
             T* k1 = reinterpret_cast<T*>(smem + buf * L.stage) + r * L.krow;
             T* k2 = k1 + KT * L.krow;
             T* v = reinterpret_cast<T*>(smem + buf * L.stage) + (shared ? 1 : 2) * KT * L.krow + r * L.vrow;
-            int page = -1;
-            if (key < cur.s.total) {
-                page = paged_page(p, cur.b, key / p.page);
-                if (page < 0) { bad = true; atomicOr(p.status, kStatusIndex); }
-            }
+            if (page == -1) { bad = true; atomicOr(p.status, kStatusIndex); }
             const int64_t slot = key % p.page;
             const T* g1 = static_cast<const T*>(p.k1) + page * p.s_k1[0] + cur.hk * p.s_k1[1] + slot * p.s_k1[2];
             const T* g2 = static_cast<const T*>(p.k2) + page * p.s_k2[0] + cur.hk * p.s_k2[1] + slot * p.s_k2[2];
@@ -162,11 +161,14 @@ paged_simt_kernel(const PagedParams p) {
                 for (int c = c4; c < L.vrow; c += 4) v[c] = page >= 0 && c < Dv ? gv[c] : T(0.f);
             }
         };
-        if (live > 0) stage(0, 0);
+        int page = look(0);
+        if (live > 0) stage(0, 0, page);
         cp_async_commit();
+        page = look(1);
         for (int i = 0; i < live; ++i) {
-            if (i + 1 < live) stage(i + 1, (i + 1) & 1);
+            if (i + 1 < live) stage(i + 1, (i + 1) & 1, page);
             cp_async_commit();
+            page = look(i + 2);
             cp_async_wait<1>();
             __syncthreads();
             const T* kt = reinterpret_cast<const T*>(smem + (i & 1) * L.stage);
@@ -189,40 +191,67 @@ paged_simt_kernel(const PagedParams p) {
 #pragma unroll
                         for (int r = 0; r < HALF; ++r)
 #pragma unroll
-                            for (int e = 0; e < V; ++e) s[r] = fmaf(q[r * L.dpad + c + e], x[e], s[r]);
+                            for (int e = 0; e < V; e += 4) {     // four queries a read, the same for all lanes
+                                const float4 y = *reinterpret_cast<const float4*>(q + r * L.dpad + c + e);
+                                s[r] = fmaf(y.x, x[e], s[r]);
+                                s[r] = fmaf(y.y, x[e + 1], s[r]);
+                                s[r] = fmaf(y.z, x[e + 2], s[r]);
+                                s[r] = fmaf(y.w, x[e + 3], s[r]);
+                            }
                     }
 #pragma unroll
                     for (int r = 0; r < HALF; ++r) ps[lane * 2 * RC + br * RC + r0 + r] = s[r] * p.scale_log2;
                 }
             }
             __syncthreads();
-            // ---- weights: a warp takes rows (branch, r) warp, warp + 4, ...
-            for (int j = warp; j < 2 * RC; j += WARPS) {
-                float s = ps[lane * 2 * RC + j];
-                bool seen = true;
-                if (edge) {
-                    const PagedRow x = paged_row(p, cur.hk, cur.rc, j % RC, n_new);
-                    const int64_t d = key0 + lane - cur.s.before;      // place among the new tokens
-                    seen = key0 + lane < cur.s.total && x.live &&
-                           (d < 0 || (p.mask ? p.mask[cur.b * p.mask_stride[0] + x.q * p.mask_stride[1] + d] != 0
-                                             : d <= x.q));
-                    if (!seen) s = -INFINITY;
+            // ---- weights: a warp takes rows (branch, r) warp, warp + 4, ..., all at once: one
+            // after another their shuffles' latencies would be most of the tile's time
+            {
+                constexpr int NJ = (2 * RC + WARPS - 1) / WARPS;
+                float s[NJ], top[NJ], w[NJ], sum[NJ], m0[NJ];
+                bool seen[NJ];
+#pragma unroll
+                for (int k = 0; k < NJ; ++k) {
+                    const int j = min(warp + k * WARPS, 2 * RC - 1);
+                    s[k] = ps[lane * 2 * RC + j];
+                    seen[k] = true;
+                    if (edge) {
+                        const PagedRow x = paged_row(p, cur.hk, cur.rc, j % RC, n_new);
+                        const int64_t d = key0 + lane - cur.s.before;      // place among the new tokens
+                        seen[k] = key0 + lane < cur.s.total && x.live &&
+                                  (d < 0 || (p.mask ? p.mask[cur.b * p.mask_stride[0] + x.q * p.mask_stride[1] + d] != 0
+                                                    : d <= x.q));
+                        if (!seen[k]) s[k] = -INFINITY;
+                    }
+                    top[k] = s[k];
+                    m0[k] = st_m[j];
                 }
-                float top = s;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m0 = st_m[j], m = fmaxf(m0, top);
-                const float w = s == -INFINITY ? 0.f : exp2f(s - m);   // NaN scores stay NaN
-                float sum = w;
+                for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                ps[lane * 2 * RC + j] = seen ? w : -1.f;
+                    for (int k = 0; k < NJ; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+#pragma unroll
+                for (int k = 0; k < NJ; ++k) {
+                    top[k] = fmaxf(m0[k], top[k]);
+                    w[k] = s[k] == -INFINITY ? 0.f : exp2f(s[k] - top[k]);   // NaN scores stay NaN
+                    sum[k] = w[k];
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                    for (int k = 0; k < NJ; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
                 __syncwarp();
-                if (lane == 0) {
-                    const float a = m0 == m ? 1.f : exp2f(m0 - m);
-                    st_m[j] = m;
-                    st_l[j] = st_l[j] * a + sum;
-                    st_a[j] = a;
+#pragma unroll
+                for (int k = 0; k < NJ; ++k) {
+                    const int j = warp + k * WARPS;
+                    if (j >= 2 * RC) break;
+                    ps[lane * 2 * RC + j] = seen[k] ? w[k] : -1.f;
+                    if (lane == 0) {
+                        const float a = m0[k] == top[k] ? 1.f : exp2f(m0[k] - top[k]);
+                        st_m[j] = top[k];
+                        st_l[j] = st_l[j] * a + sum[k];
+                        st_a[j] = a;
+                    }
                 }
             }
             __syncthreads();
@@ -240,7 +269,15 @@ paged_simt_kernel(const PagedParams p) {
                 for (int t = kg; t < KT; t += KG) {
                     const float x = to_float<T>(vt[t * L.vrow + c0]);
                     const float y = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
-                    const float* w = ps + t * 2 * RC;
+                    float w[2 * RC];
+                    if constexpr (RC > 1) {
+#pragma unroll
+                        for (int r = 0; r < 2 * RC; r += 4)
+                            *reinterpret_cast<float4*>(w + r) = *reinterpret_cast<const float4*>(ps + t * 2 * RC + r);
+                    } else {
+                        w[0] = ps[2 * t];
+                        w[1] = ps[2 * t + 1];
+                    }
                     if (!edge) {
 #pragma unroll
                         for (int r = 0; r < RC; ++r) {
