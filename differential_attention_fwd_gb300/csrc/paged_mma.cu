@@ -27,8 +27,10 @@
 //     the dense decode, 0.83 of the copy rate).
 //
 // Weights are 2^(s - m) against a running maximum that moves only when some weight would
-// pass 2^8; they are rounded to bf16 for the product with V (half a step of 2^-8, as
-// everywhere on the tensor cores), while their sum is taken unrounded in float32.
+// pass 2^8.  They go to the product with V as two bf16 parts, the rounded weight and what
+// the rounding left (2^-16 together): with one part the branches' difference was off by
+// 2.1e-3 of itself, more than the output's own rounding (1.7e-3), and the second product
+// costs nothing here, since the tile's bytes take longer.
 #include "paged_plan.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -354,15 +356,19 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                             }
                         }
                 }
-                uint32_t pa[2][4];
+                uint32_t pa[2][4], pb[2][4];
 #pragma unroll
                 for (int br = 0; br < 2; ++br) {
                     l[br][0] += (pr[br][0][0] + pr[br][0][1]) + (pr[br][1][0] + pr[br][1][1]);
                     l[br][1] += (pr[br][0][2] + pr[br][0][3]) + (pr[br][1][2] + pr[br][1][3]);
-                    pa[br][0] = pack_bf16x2(pr[br][0][0], pr[br][0][1]);
-                    pa[br][1] = pack_bf16x2(pr[br][0][2], pr[br][0][3]);
-                    pa[br][2] = pack_bf16x2(pr[br][1][0], pr[br][1][1]);
-                    pa[br][3] = pack_bf16x2(pr[br][1][2], pr[br][1][3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = pr[br][i >> 1][2 * (i & 1)], b = pr[br][i >> 1][2 * (i & 1) + 1];
+                        pa[br][i] = pack_bf16x2(a, b);
+                        // what the rounding left: 0 where the weight is not finite
+                        const float da = a - __uint_as_float(pa[br][i] << 16), db = b - __uint_as_float(pa[br][i] & 0xffff0000u);
+                        pb[br][i] = pack_bf16x2(fabsf(a) < INFINITY ? da : 0.f, fabsf(b) < INFINITY ? db : 0.f);
+                    }
                 }
                 if (edge) {
                     // Values that a row does not see may be anything, and the product's 0 x NaN
@@ -429,6 +435,8 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     for (int br = 0; br < 2; ++br) {
                         mma16816(o[br][2 * n], pa[br], vf[0], vf[1]);
                         mma16816(o[br][2 * n + 1], pa[br], vf[2], vf[3]);
+                        mma16816(o[br][2 * n], pb[br], vf[0], vf[1]);
+                        mma16816(o[br][2 * n + 1], pb[br], vf[2], vf[3]);
                     }
                 }
             }
