@@ -365,9 +365,8 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     for (int i = 0; i < 4; ++i) {
                         const float a = pr[br][i >> 1][2 * (i & 1)], b = pr[br][i >> 1][2 * (i & 1) + 1];
                         pa[br][i] = pack_bf16x2(a, b);
-                        // what the rounding left: 0 where the weight is not finite
-                        const float da = a - __uint_as_float(pa[br][i] << 16), db = b - __uint_as_float(pa[br][i] & 0xffff0000u);
-                        pb[br][i] = pack_bf16x2(fabsf(a) < INFINITY ? da : 0.f, fabsf(b) < INFINITY ? db : 0.f);
+                        pb[br][i] = pack_bf16x2(a - __uint_as_float(pa[br][i] << 16),    // what the rounding left
+                                                b - __uint_as_float(pa[br][i] & 0xffff0000u));
                     }
                 }
                 if (edge) {

@@ -33,7 +33,6 @@
 namespace diffattn {
 namespace ptc {
 
-using tc::tile_exp2;
 using tc::tile_row_max;
 
 constexpr int BM = 128;
@@ -113,6 +112,26 @@ __device__ __forceinline__ void transpose32(uint32_t (&o)[32], uint32_t lane) {
             else o[i + m] = got;
         }
     }
+}
+
+// P = 2^(s * scale_log2 - m) for one thread's 64 scores, and the sum of P.  Rounded to one
+// bf16, P would put an error of 2e-3 of the result's size into long caches, where the means
+// of the two branches cancel; so it is the sum of two: pk[0..31] and what is left, pk[32..63].
+__device__ __forceinline__ float tile_weights(const float (&s)[64], float sl2, float m, uint32_t (&pk)[64]) {
+    const uint64_t scale2 = f2_pack(sl2, sl2);
+    const uint64_t negm2 = f2_pack(-m, -m);
+    uint64_t rsum[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        const uint64_t x = f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), scale2, negm2);
+        const uint64_t w = f2_pack(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
+        rsum[c & 3] = f2_add(rsum[c & 3], w);
+        pk[c] = pack_bf16x2(f2_lo(w), f2_hi(w));
+        const uint64_t d = f2_sub(w, f2_pack(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
+        pk[32 + c] = pack_bf16x2(f2_lo(d), f2_hi(d));
+    }
+    const uint64_t r = f2_add(f2_add(rsum[0], rsum[1]), f2_add(rsum[2], rsum[3]));
+    return f2_lo(r) + f2_hi(r);
 }
 
 // A bf16 pair with zeros for what is not finite.
@@ -411,8 +430,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                         tc_fence_after();
                         const uint64_t vd = vdesc + ((vst * V_BYTES) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            mma_ts(d_o, tmem_base + tm_s(br, buf) + kk * 8, vd + 128 * kk, IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < KT / 8; ++kk)     // both parts of the weights, after one another
+                            mma_ts(d_o, tmem_base + tm_s(br, buf) + kk * 8, vd + 128 * (kk % (KT / 16)), IDESC_PV,
+                                   (j > 0 || kk > 0) ? 1u : 0u);
                         mma_commit(&bars[B_PV_DONE + br]);
                         mma_commit(&bars[B_V_EMPTY + vst]);
                         if (++vst == (uint32_t)VST) { vst = 0; vph ^= 1; }
@@ -480,9 +500,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 float alpha = 1.0f;
                 bool rescale = false;
                 if (j == 0) m_run = fmaxf(tile_row_max(sc) * sl2, NOTHING);
-                uint32_t pk[32];
-                float tsum = tile_exp2(sc, sl2, m_run, pk);
-                tmem_st32(tS, &pk[0]);
+                uint32_t pk[64];
+                auto put = [&](const uint32_t (&w)[64]) {
+                    tmem_st32(tS, &w[0]);
+                    tmem_st32(tS + 32, &w[32]);
+                };
+                float tsum = tile_weights(sc, sl2, m_run, pk);
+                put(pk);
                 if (j > 0 && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
                     const float mxs = tile_row_max(sc) * sl2;
                     if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
@@ -491,9 +515,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                         l *= alpha;
                         m_run = m_new;
                         rescale = true;
-                        tsum = tile_exp2(sc, sl2, m_run, pk);
+                        tsum = tile_weights(sc, sl2, m_run, pk);
                         tmem_wait_st();
-                        tmem_st32(tS, &pk[0]);
+                        put(pk);
                     }
                 }
                 if (rescale) {
