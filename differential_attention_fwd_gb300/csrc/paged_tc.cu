@@ -10,9 +10,13 @@
 // S_b as bf16, and O_b += P_b V.  The work is cut by the lengths on the device (see
 // paged_plan.cuh), and every role walks the block's segments on its own.
 //
-// What bounds it at 128 full rows: a 64-key tile takes about 1,000 cycles of tensor-core
-// work, 1,000 of the exponential unit and 1,400 of an SM's share of the HBM rate, which
-// the ring's 160 KB in flight cover.
+// What bounds it: the tensor core's operands in shared memory, at 128 bytes a cycle.  A
+// 64-key tile of head width 128 reads 96 KB for the scores (Q is read again for each tile;
+// TMEM is full, so it cannot lie there), 64 KB of V for both parts of the weights of both
+// branches, and the copies write 32 KB: 1,540 cycles of the 1,700 that a tile takes, beside
+// 1,000 of the exponential unit and 1,000 of an SM's share of the HBM rate.  The row count
+// hardly matters: 16 sequences of 8192 keys, 8 key/value heads take 102 us with 9 tokens and
+// 120 with 64, and leaving out the weights of padding rows changed neither.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7   weights and results of branch 1, 2 (TMEM lanes 0-127)
@@ -28,12 +32,9 @@
 #include "paged_plan.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
-#include "tile_softmax.cuh"
 
 namespace diffattn {
 namespace ptc {
-
-using tc::tile_row_max;
 
 constexpr int BM = 128;
 constexpr int KT = 64;
@@ -114,23 +115,41 @@ __device__ __forceinline__ void transpose32(uint32_t (&o)[32], uint32_t lane) {
     }
 }
 
-// P = 2^(s * scale_log2 - m) for one thread's 64 scores, and the sum of P.  Rounded to one
-// bf16, P would put an error of 2e-3 of the result's size into long caches, where the means
-// of the two branches cancel; so it is the sum of two: pk[0..31] and what is left, pk[32..63].
-__device__ __forceinline__ float tile_weights(const float (&s)[64], float sl2, float m, uint32_t (&pk)[64]) {
+// Maximum of 32 scores, in three chains.
+__device__ __forceinline__ float half_max(const uint32_t (&s)[32]) {
+    auto f = [&](int i) { return __uint_as_float(s[i]); };
+    float a = fmaxf(f(0), f(1)), b = f(2), c = f(3);
+#pragma unroll
+    for (int i = 4; i < 28; i += 6) {
+        a = fmax3(a, f(i), f(i + 1));
+        b = fmax3(b, f(i + 2), f(i + 3));
+        c = fmax3(c, f(i + 4), f(i + 5));
+    }
+    a = fmax3(a, f(28), f(29));
+    b = fmax3(b, f(30), f(31));
+    return fmax3(a, b, c);
+}
+// A pair of weights as two bf16 parts, what the first leaves in the second.
+__device__ __forceinline__ void split2(uint64_t w, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(f2_lo(w), f2_hi(w));
+    const uint64_t d = f2_sub(w, f2_pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+    lo = pack_bf16x2(f2_lo(d), f2_hi(d));
+}
+// P = 2^(s * scale_log2 - m) for 32 scores, and the sum of P.  Rounded to one bf16, P would
+// put an error of 2e-3 of the result's size into long caches, where the means of the two
+// branches cancel; so it is the sum of two: pk[0..15] and what is left, pk[16..31].
+__device__ __forceinline__ float half_weights(const uint32_t (&s)[32], float sl2, float m, uint32_t (&pk)[32]) {
     const uint64_t scale2 = f2_pack(sl2, sl2);
     const uint64_t negm2 = f2_pack(-m, -m);
-    uint64_t rsum[4] = {0, 0, 0, 0};
+    uint64_t rsum[2] = {0, 0};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        const uint64_t x = f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), scale2, negm2);
+    for (int c = 0; c < 16; ++c) {
+        const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, negm2);
         const uint64_t w = f2_pack(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
-        rsum[c & 3] = f2_add(rsum[c & 3], w);
-        pk[c] = pack_bf16x2(f2_lo(w), f2_hi(w));
-        const uint64_t d = f2_sub(w, f2_pack(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
-        pk[32 + c] = pack_bf16x2(f2_lo(d), f2_hi(d));
+        rsum[c & 1] = f2_add(rsum[c & 1], w);
+        split2(w, pk[c], pk[16 + c]);
     }
-    const uint64_t r = f2_add(f2_add(rsum[0], rsum[1]), f2_add(rsum[2], rsum[3]));
+    const uint64_t r = f2_add(rsum[0], rsum[1]);
     return f2_lo(r) + f2_hi(r);
 }
 
@@ -430,8 +449,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                         tc_fence_after();
                         const uint64_t vd = vdesc + ((vst * V_BYTES) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < KT / 8; ++kk)     // both parts of the weights, after one another
-                            mma_ts(d_o, tmem_base + tm_s(br, buf) + kk * 8, vd + 128 * (kk % (KT / 16)), IDESC_PV,
+                        for (int kk = 0; kk < KT / 8; ++kk)     // a half: 32 keys' first parts, then their second ones
+                            mma_ts(d_o, tmem_base + tm_s(br, buf) + kk * 8, vd + 128 * (kk / 4 * 2 + kk % 2), IDESC_PV,
                                    (j > 0 || kk > 0) ? 1u : 0u);
                         mma_commit(&bars[B_PV_DONE + br]);
                         mma_commit(&bars[B_V_EMPTY + vst]);
@@ -482,59 +501,65 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 if (!(ok = mbar_wait_warp(&bars[B_S_FULL + 2 * br + buf], (sph >> buf) & 1u, ab))) break;
                 sph ^= 1u << buf;
                 tc_fence_after();
-                uint32_t u[64];
-                tmem_ld32(tS + 0, &u[0]);
-                tmem_ld32(tS + 32, &u[32]);
-                tmem_wait_ld();
-                float sc[64];
-#pragma unroll
-                for (int c = 0; c < 64; ++c) sc[c] = __uint_as_float(u[c]);
                 const int k0 = (cur.tile0 + j) * KT;
-                if (k0 + KT > s.before) {
-                    const uint64_t vis = mine ? tile_mask(p, s, k0, x.q, tree) : 0;
-                    const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+                const bool edge = k0 + KT > s.before;
+                const uint64_t vis = edge && mine ? tile_mask(p, s, k0, x.q, tree) : 0;
+                // A loop over the tile's halves that stays one: each 32 keys' weights go over
+                // their scores, 16 columns a part.  Unrolled, the warps waited for instructions
+                // a fifth of the time.
+#pragma unroll 1
+                for (int h = 0; ok && h < 2; ++h) {
+                    uint32_t sc[32], pk[32];
+                    tmem_ld32(tS + 32 * h, sc);
+                    tmem_wait_ld();
+                    if (edge) {
+                        const uint32_t seen = (uint32_t)(vis >> (32 * h));
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        sc[c] = ((c < 32 ? lo : hi) >> (c & 31) & 1u) ? sc[c] : -INFINITY;
-                }
-                float alpha = 1.0f;
-                bool rescale = false;
-                if (j == 0) m_run = fmaxf(tile_row_max(sc) * sl2, NOTHING);
-                uint32_t pk[64];
-                auto put = [&](const uint32_t (&w)[64]) {
-                    tmem_st32(tS, &w[0]);
-                    tmem_st32(tS + 32, &w[32]);
-                };
-                float tsum = tile_weights(sc, sl2, m_run, pk);
-                put(pk);
-                if (j > 0 && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
-                    const float mxs = tile_row_max(sc) * sl2;
-                    if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
-                        const float m_new = fmaxf(m_run, mxs);
-                        alpha = ex2_approx(m_run - m_new);
-                        l *= alpha;
-                        m_run = m_new;
-                        rescale = true;
-                        tsum = tile_weights(sc, sl2, m_run, pk);
-                        tmem_wait_st();
-                        put(pk);
+                        for (int c = 0; c < 32; ++c) sc[c] = (seen >> c & 1u) ? sc[c] : 0xff800000u;
                     }
-                }
-                if (rescale) {
-                    if (!(ok = mbar_wait_warp(&bars[B_PV_DONE + br], (pv_count + j - 1) & 1u, ab))) break;
-                    tc_fence_after();
+                    const bool first = j == 0 && h == 0;
+                    if (first) m_run = fmaxf(half_max(sc) * sl2, NOTHING);
+                    float tsum = half_weights(sc, sl2, m_run, pk);
+                    if (!first && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
+                        const float mxs = half_max(sc) * sl2;
+                        if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
+                            const float m_new = fmaxf(m_run, mxs);
+                            const float alpha = ex2_approx(m_run - m_new);
+                            l *= alpha;
+                            m_run = m_new;
+                            tsum = half_weights(sc, sl2, m_run, pk);
+                            uint32_t o[32];
+                            if (h == 1) {       // the first half's weights
+                                tmem_wait_st();
+                                tmem_ld32(tS, o);
+                                tmem_wait_ld();
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c4 * 32, o);
-                        tmem_wait_ld();
+                                for (int i = 0; i < 16; ++i) {
+                                    auto both = [&](uint32_t a, uint32_t b) { return (__uint_as_float(a) + __uint_as_float(b)) * alpha; };
+                                    split2(f2_pack(both(o[i] << 16, o[16 + i] << 16),
+                                                   both(o[i] & 0xffff0000u, o[16 + i] & 0xffff0000u)), o[i], o[16 + i]);
+                                }
+                                tmem_st32(tS, o);
+                            }
+                            if (j > 0) {        // and O
+                                ok = mbar_wait_warp(&bars[B_PV_DONE + br], (pv_count + j - 1) & 1u, ab);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c4 = 0; ok && c4 < 4; ++c4) {
+                                    tmem_ld32(tO + c4 * 32, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + c4 * 32, o);
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                    tmem_st32(tO + c4 * 32, o);
+                                }
+                            }
+                        }
                     }
+                    tmem_st32(tS + 32 * h, pk);
+                    l += tsum;
                 }
+                if (!ok) break;
                 tmem_wait_st();
-                l += tsum;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_P_FULL + 2 * br + buf]);
