@@ -10,8 +10,8 @@ squares in any order, a division, a root, an inverse), each n by two more roundi
 each y = n_a cos - n_b sin by three: |y - y*| <= h |y*| + (D / 2 + 10) u (|n_a| + |n_b|).
 
 Attention: with A_b the weights and S = A_1 |V| + |lambda| A_2 |V| (elementwise),
-  bf16: each weight is rounded to bf16 once before the product with V (h S in all) and
-        the output once (h |o|);
+  bf16: each weight enters the product with V as two bf16 parts, the second the rounded
+        rest of the first: h^2 S in all; the output is rounded once, h (|o| + the rest);
   both: a score is off by D u sum_i |q_i k_i| / sqrt(D) (a sum of D products) and two
         roundings of scale and maximum, its exponential by 4 u more, and sums over n
         keys by n u relative: each weight by
@@ -91,10 +91,9 @@ def attention_rows(q1, k1, q2, k2, v, seen, lam, dtype):
         size = size + abs(f) * prod.abs().sum(1)
         z = (q.abs() @ k.abs().T / math.sqrt(D)).masked_fill(~seen, 0.0).amax(-1, keepdim=True)
         e = torch.maximum(torch.as_tensor(e, dtype=v.dtype), U * (n + 2 * D * z + 2 * z + 16))
-    bound = (2 * e + 4 * U) * size + half_step(dtype) * o.abs()
-    if dtype == torch.bfloat16:
-        bound = bound + half_step(dtype) * size
-    return o, bound
+    h = half_step(dtype)
+    parts = h * h if dtype == torch.bfloat16 else 0.0
+    return o, (1 + h) * (2 * e + 4 * U + parts) * size + h * o.abs()
 
 
 def epilogue(o, bound, norm, eps, weight, bias, scale, dtype):

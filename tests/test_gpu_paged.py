@@ -29,7 +29,7 @@ class Problem:
     """Caches with the sequences' pages in a random order; unused slots and pages hold NaN."""
 
     def __init__(self, dtype, D, Dv, shared, H, Hk, Tq, lens, page, new=None, tree=False, seed=0, layout="head",
-                 scale=1.0):
+                 scale=1.0, slope=0.0, spikes=False):
         g = torch.Generator().manual_seed(seed + 1000 * D + Tq)
         dt = DT[dtype]
         B = len(lens)
@@ -44,6 +44,11 @@ class Problem:
         at = 0
         self.k1, self.k2, self.v = ([torch.randn(Hk, t, n, generator=g).to(dt) * s for t in totals]
                                     for n, s in ((D, scale), (D, scale), (Dv, 1.0)))
+        if slope or spikes:     # scores that rise or fall along the keys, and a few that stand out
+            for k in (*self.k1, *self.k2):
+                along = torch.arange(k.shape[1], dtype=torch.float32)[None, :, None]
+                tall = torch.where(torch.rand(Hk, k.shape[1], 1, generator=g) < 1 / 40, 6.0, 0.0) if spikes else 0.0
+                k += (slope * along + tall).to(dt)
         caches = [torch.full((pool, Hk, page, n), float("nan"), dtype=dt) for n in (D, D, Dv)]
         for b, n in enumerate(need):
             ids = order[at:at + n]
@@ -66,6 +71,8 @@ class Problem:
             self.caches = [off(c) for c in self.caches]
         self.shared = shared
         self.q1, self.q2 = ((torch.randn(B, Tq, H, D, generator=g) * scale).to(dt).cuda().transpose(1, 2) for _ in range(2))
+        if slope or spikes:
+            self.q1, self.q2 = self.q1.abs(), self.q2.abs()
         self.tree = None
         if tree:
             back = torch.randint(1, 5, (B, Tq), generator=g)
@@ -172,6 +179,34 @@ def test_long_context_is_split_and_joined(head):
     for Tq, tree in ((1, False), (4, False), (40, True)):
         pb = Problem(*head, 1, 1, Tq, [9000], 64, tree=tree, scale=2.0)
         pb.check(pb.run(), what=f"{head} {Tq}")
+
+
+@pytest.mark.parametrize("head", HEADS)
+@pytest.mark.parametrize("slope,spikes", [(0.04, False), (-0.04, False), (0.01, True), (0.0, True)])
+def test_moving_maximum(head, slope, spikes):
+    """Scores that pass the running maximum by more than 2^8 within a tile, between tiles and
+    between the parts of a split sequence."""
+    for Tq, lens in ((1, [300, 33, 1500]), (5, [100, 700]), (24, [257, 40, 600])):
+        pb = Problem(*head, 2, 1, Tq, lens, 16, slope=slope if max(lens) < 1000 else slope / 3, spikes=spikes)
+        pb.check(pb.run(), what=f"{head} {Tq}")
+
+
+@pytest.mark.parametrize("head", HEADS)
+@pytest.mark.parametrize("Tq", [1, 20])
+@pytest.mark.parametrize("at", [5, 250])
+def test_visible_values_that_are_not_finite(head, Tq, at):
+    """A NaN or an infinity that every row sees (inf - lambda inf) reaches its column alone."""
+    pb = Problem(*head, 2, 1, Tq, [300], 16)
+    clean = pb.run()
+    pg, row = int(pb.table[0, at // 16]), at % 16
+    for value in (float("nan"), float("inf"), -float("inf")):
+        old = pb.caches[2][pg, 0, row, 7].clone()
+        pb.caches[2][pg, 0, row, 7] = value
+        out = pb.run()
+        pb.caches[2][pg, 0, row, 7] = old
+        assert torch.isnan(out[..., 7]).all(), value
+        out[..., 7] = clean[..., 7]
+        pb.check(out, what=f"{value}")
 
 
 @pytest.mark.parametrize("head", HEADS)
