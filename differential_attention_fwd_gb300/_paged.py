@@ -89,7 +89,8 @@ def paged_cache_append(k1: torch.Tensor, k2: Optional[torch.Tensor], value: torc
     sequence.  k2 and k2_cache None (or k1 and k1_cache again): the branches share
     their keys.  lengths: [B] int32, tokens cached before the call; token t goes to
     index lengths[b] + t.  new_lengths: [B] int32, the first new_lengths[b] tokens are
-    written (None: all T).  positions: for the rotation, None = the index.
+    written (None: all T).  positions: for the rotation, None = the index.  No two
+    tokens of a call may have one slot, and the new rows may not lie in the caches.
     A token whose index, page or position is out of range is not written and is
     reported by get_device_error.  Forward only."""
     (_native or _load()).append(k1, k2, value, k1_cache, k2_cache, v_cache, block_table, lengths, new_lengths, cos, sin,
@@ -111,7 +112,8 @@ def differential_attention_paged(q1: torch.Tensor, k1_cache: torch.Tensor, q2: t
     the new tokens' keys and values behind them.  New token i of sequence b sees the
     lengths[b] tokens before and new tokens 0 .. i.  q_lengths: [B] int32, sequence b
     has only its first q_lengths[b] new tokens (0: an idle place of the batch): the
-    rows of `out` past them are left as they were (zeros in a fresh output).
+    rows of `out` past them are left as they were (zeros in a fresh output); it may not
+    overlap the inputs.
     coefficient and the epilogue (norm .. out_scale) as differential_attention.
 
     A length, or a page that a sequence needs, out of range gives that sequence rows

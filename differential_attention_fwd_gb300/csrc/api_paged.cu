@@ -31,7 +31,9 @@ int check_rotary(const diffattn_rotary_desc* d, const float* cos, const float* s
     if ((d->q_weight_stride != 0 && d->q_weight_stride != d->D) ||
         (d->k_weight_stride != 0 && d->k_weight_stride != d->D))
         return DIFFATTN_ERR_INVALID;
-    if (d->B > INT32_MAX || d->T > INT32_MAX || d->B * d->T > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
+    // token indices, and those of a last block's threads past them, in 31 bits
+    constexpr int64_t kMaxTokens = 1 << 30;
+    if (d->B > kMaxTokens || d->T > kMaxTokens || d->B * d->T > kMaxTokens) return DIFFATTN_ERR_UNSUPPORTED;
     // rows of the backward's kernels are counted in 31 bits
     if (d->H >= 0 && d->Hk >= 0 && 2.0 * (d->B * d->T / 16 + 16) * (double)(d->H + d->Hk) > INT32_MAX)
         return DIFFATTN_ERR_UNSUPPORTED;
@@ -119,6 +121,13 @@ int check_pages(const diffattn_pages* g) {
     return DIFFATTN_OK;
 }
 
+// Whether rows of these sizes and strides have a place each (a stride of 0 gives many one).
+bool apart(const int64_t n[3], const int64_t s[3]) {
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && s[i] == 0) return false;
+    return true;
+}
+
 bool same3(const int64_t a[3], const int64_t b[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
 
 // ---------------------------------------------------------------------------
@@ -172,6 +181,13 @@ void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, P
     n->bytes = part_bytes(*n, dv);
 }
 
+// Strides that TMA takes, of the dimensions that are stepped.
+bool tma_strides(const int64_t n[3], const int64_t s[3]) {
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] % 8 != 0 || s[i] <= 0 || s[i] >= (int64_t(1) << 38))) return false;
+    return true;
+}
+
 // Whether the tensor-core kernels take the shape and the cache's layout: bf16, value
 // width 128, Q/K width 64 or 128, pages of a multiple of 16 slots, and strides (with the
 // bases, checked at the call) that TMA takes.
@@ -179,10 +195,8 @@ bool tc_shape(const diffattn_paged_desc& d, const diffattn_pages& g) {
     if (d.dtype != DIFFATTN_BF16 || (d.Dv == 0 ? 2 * d.D : d.Dv) != 128 || (d.D != 64 && d.D != 128) ||
         g.page_size % 16 != 0)
         return false;
-    for (const int64_t* s : {g.k1_stride, g.k2_stride, g.v_stride})
-        for (int i = 0; i < 3; ++i)
-            if (s[i] % 8 != 0 || s[i] <= 0 || s[i] >= (int64_t(1) << 38)) return false;
-    return true;
+    const int64_t n[3] = {g.num_pages, d.H / (d.kv_group > 1 ? d.kv_group : 1), g.page_size};
+    return tma_strides(n, g.k1_stride) && tma_strides(n, g.k2_stride) && tma_strides(n, g.v_stride);
 }
 
 // The plan of the tensor-core kernel for up to 16 rows.
@@ -303,11 +317,13 @@ int diffattn_paged_append(const diffattn_rotary_desc* desc, int64_t Dv, const in
                           const float* k_weight, const float* cos, const float* sin, const void* positions,
                           const int32_t* lengths, const int32_t* new_lengths, const int32_t* block_table,
                           void* k1_cache, void* k2_cache, void* v_cache, diffattn_stream_t stream) {
-    int rc = check_rotary(desc, cos, sin, true);
+    if (!desc) return DIFFATTN_ERR_INVALID;
+    diffattn_rotary_desc d = *desc;
+    d.H = 0;                            // not read
+    int rc = check_rotary(&d, cos, sin, true);
     if (rc != DIFFATTN_OK) return rc;
     rc = check_pages(pages);
     if (rc != DIFFATTN_OK) return rc;
-    const diffattn_rotary_desc& d = *desc;
     const int64_t dv = Dv == 0 ? 2 * d.D : Dv;
     if (dv < 1 || dv > 256 || d.Hk < 1 || !v_stride || !nonneg(v_stride) || !k1 || !v || !lengths || !block_table ||
         !k1_cache || !v_cache || (k_weight && d.norm == DIFFATTN_NORM_NONE))
@@ -317,6 +333,10 @@ int diffattn_paged_append(const diffattn_rotary_desc* desc, int64_t Dv, const in
                                                same3(d.k1_stride, d.k2_stride) &&
                                                same3(pages->k1_stride, pages->k2_stride));
     if (!shared && (!k2 || !k2_cache || k2_cache == k1_cache)) return DIFFATTN_ERR_INVALID;
+    const int64_t slots[3] = {pages->num_pages, d.Hk, pages->page_size};
+    if (v_cache == k1_cache || v_cache == k2_cache || !apart(slots, pages->k1_stride) || !apart(slots, pages->v_stride) ||
+        (!shared && !apart(slots, pages->k2_stride)))
+        return DIFFATTN_ERR_INVALID;
     RotaryParams p{};
     fill_rotary(&p, d, cos, sin, positions);
     const int es = p.bf16 ? 2 : 4;
@@ -380,6 +400,8 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     if (rc != DIFFATTN_OK) return rc;
     if (!workspace || !aligned16(workspace)) return DIFFATTN_ERR_INVALID;
     const diffattn_paged_desc& d = *desc;
+    const int64_t rows[3] = {d.B, d.H, d.Tq};
+    if (!apart(rows, d.o_stride)) return DIFFATTN_ERR_INVALID;
     const int64_t es = d.dtype == DIFFATTN_BF16 ? 2 : 4;
     PagedParams p{};
     int sms = 0;
@@ -388,10 +410,8 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     PagedPlan n;
     const bool tc = tc_shape(d, *pages) && aligned16(k1_cache) && aligned16(k2_cache) && aligned16(v_cache);
     // the queries go through TMA too, from 16-byte aligned rows
-    bool tcgen = tc && wants_tc(d) && aligned16(q1) && aligned16(q2);
-    for (const int64_t* s : {d.q1_stride, d.q2_stride})
-        for (int i = 0; i < 3; ++i)
-            if ((i == 0 ? d.B : i == 1 ? d.H : d.Tq) > 1 && (s[i] <= 0 || s[i] % 8 != 0)) tcgen = false;
+    const bool tcgen = tc && wants_tc(d) && aligned16(q1) && aligned16(q2) && tma_strides(rows, d.q1_stride) &&
+                       tma_strides(rows, d.q2_stride);
     if (tcgen) plan_tc(d, *pages, sms, &n);
     else if (tc) plan_mma(d, *pages, sms, &n);
     else plan_simt(d, *pages, sms, &n);

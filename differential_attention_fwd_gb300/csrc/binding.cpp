@@ -496,15 +496,16 @@ PyObject* append(PyObject* const* a) {
     if (!shared) strides3(d.k2_stride, k[1]);
     int64_t vs[3];
     strides3(vs, v);
+    // in-place: what autograd saved of the cache before will no longer be it, and an
+    // inference tensor outside of inference mode refuses
+    c.k1.unsafeGetTensorImpl()->bump_version();
+    if (!shared) c.k2.unsafeGetTensorImpl()->bump_version();
+    c.v.unsafeGetTensorImpl()->bump_version();
     check(diffattn_paged_append(&d, c.Dv, vs, &c.pages, ptr(k[0]), ptr(k[1]), ptr(v), fptr(r.kw), fptr(r.cos), fptr(r.sin),
                                 ptr(r.pos), lengths.const_data_ptr<int32_t>(),
                                 fresh.defined() ? fresh.const_data_ptr<int32_t>() : nullptr, c.table_ptr(), ptr(c.k1),
                                 shared ? nullptr : ptr(c.k2), ptr(c.v), stream_of(dev)),
           "diffattn_paged_append");
-    // in-place: what autograd saved of the cache before is no longer it
-    c.k1.unsafeGetTensorImpl()->bump_version();
-    if (!shared) c.k2.unsafeGetTensorImpl()->bump_version();
-    c.v.unsafeGetTensorImpl()->bump_version();
     Py_RETURN_NONE;
 }
 
@@ -574,6 +575,7 @@ PyObject* attention(PyObject* const* a) {
         if (out.size(0) != c.B || out.size(1) != H || out.size(2) != Tq || out.size(3) != c.Dv || !inner_ok(out))
             bad_value("out must be [B, H, Tq, Dv] with a contiguous innermost dimension");
         if (wants_grad({&out})) bad_value("out takes no gradient");
+        out.unsafeGetTensorImpl()->bump_version();
     }
     strides3(d.q1_stride, q1);
     strides3(d.q2_stride, q2);
@@ -606,7 +608,6 @@ PyObject* attention(PyObject* const* a) {
                                 (size_t)ws.numel(), stream_of(dev)),
           "diffattn_paged_decode");
     if (!is_none(a[10])) {
-        out.unsafeGetTensorImpl()->bump_version();
         Py_INCREF(a[10]);
         return a[10];
     }

@@ -509,7 +509,7 @@ typedef struct {
  * a multiple of 16 (float32: 8) run on the vector kernel, others a warp a row.
  * Errors: DIFFATTN_ERR_INVALID (sizes, strides, dtype, norm, eps, an odd or large
  * rotary_dim, missing tables, an output without its input or the reverse);
- * DIFFATTN_ERR_UNSUPPORTED (beyond 65535 heads in all or 2^31 tokens);
+ * DIFFATTN_ERR_UNSUPPORTED (beyond 65535 heads in all or 2^30 tokens);
  * DIFFATTN_ERR_CUDA.
  */
 int diffattn_rotary(const diffattn_rotary_desc *desc, const void *q1, const void *k1,
@@ -568,11 +568,14 @@ typedef struct {
  * same as k1 and k1_cache) when the branches share their keys.
  * lengths: [B] int32, tokens cached before the call: token t of sequence b goes to
  * cache index lengths[b] + t.  new_lengths: [B] int32 or NULL: only the first
- * new_lengths[b] tokens of a sequence are written.  positions: for the rotation,
- * NULL = the cache index (a tree of drafted tokens passes its depths).
+ * new_lengths[b] tokens of a sequence are written (none below 0, all above T).
+ * positions: for the rotation, NULL = the cache index (a tree of drafted tokens passes
+ * its depths).
  * A token whose index, page or position is out of range is not written, and is
- * recorded (DIFFATTN_ERR_INDEX).  Two tokens of one call must not have one slot.
- * One launch.  Errors as diffattn_rotary, plus DIFFATTN_ERR_INVALID for bad pages.
+ * recorded (DIFFATTN_ERR_INDEX).  Two tokens of one call must not have one slot, and
+ * the caches must not overlap each other or the new rows.
+ * One launch.  Errors as diffattn_rotary, plus DIFFATTN_ERR_INVALID for bad pages,
+ * one pointer for two caches, and a stride of 0 between slots of a cache.
  */
 int diffattn_paged_append(const diffattn_rotary_desc *desc, int64_t Dv,
                           const int64_t v_stride[3], const diffattn_pages *pages,
@@ -613,16 +616,18 @@ size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc *desc, const dif
  * Else device bytes [B, Tq, Tq] by mask_stride: new token i sees new token j where
  * the byte is not zero (and every cached token); Tq <= 64.  What a row does not see
  * has no influence on it, NaN and infinities included; a row that sees nothing
- * gives zeros (before the epilogue).
+ * gives zeros (before the epilogue).  A value that is not finite makes its column NaN
+ * for the rows that see it (inf - lambda inf; at lambda < 0 it may be an infinity).
  * A length, or a page that a sequence needs, outside the table gives rows of NaN
  * for that sequence and is recorded (DIFFATTN_ERR_INDEX); nothing outside the
  * cache is read.
+ * O must not overlap the inputs.
  * workspace: at least diffattn_paged_workspace_bytes bytes, 16-byte aligned, no
  * initialisation needed; calls that may run at the same time use different ones.
  * Two launches; no atomics on results.  lambda, lambda_dev, epi as diffattn_decode.
  * Errors: DIFFATTN_ERR_INVALID (NULL pointers, sizes, strides, dtype, kv_group,
- * non-finite lambda, bad epilogue or pages, a tree with Tq > 64, a missing, small or
- * misaligned workspace); DIFFATTN_ERR_UNSUPPORTED (Tq > 1024, sizes beyond the
+ * non-finite lambda, bad epilogue or pages, a stride of 0 between rows of O, a tree
+ * with Tq > 64, a missing, small or misaligned workspace); DIFFATTN_ERR_UNSUPPORTED (Tq > 1024, sizes beyond the
  * int32 index range); DIFFATTN_ERR_CUDA.
  */
 int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages *pages,

@@ -416,6 +416,39 @@ def test_more_than_2_31_elements():
         pb.check(pb.run(), what=f"Tq={Tq}")
 
 
+def test_inference_mode():
+    """A decode step in inference mode; a cache made there is not written outside of it."""
+    pb = Problem("bf16", 64, 128, False, 4, 2, 3, [10, 20], 16)
+    want = pb.run()
+    k, v = pb.k1[0][None, :, :1].cuda().expand(2, 2, 1, 64), pb.v[0][None, :, :1].cuda().expand(2, 2, 1, 128)
+    n = torch.tensor(pb.lens, dtype=torch.int32).cuda()
+    with torch.inference_mode():
+        made = [c.clone() for c in pb.caches]
+        da.paged_cache_append(k, k.clone(), v, *made, pb.table.cuda(), n - 1)
+        assert not torch.equal(made[2].nan_to_num(), pb.caches[2].nan_to_num())
+        assert torch.equal(pb.run(), want)
+    before = [c.clone() for c in made]
+    with torch.no_grad(), pytest.raises(RuntimeError, match="inference"):
+        da.paged_cache_append(k, k.clone(), v, *made, pb.table.cuda(), n)
+    for a, b in zip(made, before):
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+def test_strides_of_single_heads_and_pages():
+    """Dimensions of one element may have any stride: the tensor cores' copies never step them."""
+    for Tq in (1, 20):
+        pb = Problem("bf16", 64, 128, False, 1, 1, Tq, [30 - Tq], 32)
+        want = pb.run()
+        pb.check(want)
+        page = [int(pb.table[0, 0])] * 3
+        pb.caches = [c[p:p + 1].as_strided((1, 1, *c.shape[2:]), (0, 1, c.stride(2), 1), c[p].storage_offset())
+                     for c, p in zip(pb.caches, page)]
+        pb.table = torch.zeros(1, 1, dtype=torch.int32)
+        q = [x.as_strided(x.shape, (3, 0, x.stride(2), 1)) for x in (pb.q1, pb.q2)]
+        pb.q1, pb.q2 = q
+        assert torch.equal(pb.run(), want)
+
+
 def test_refusals():
     pb = Problem("bf16", 64, 128, False, 4, 2, 3, [10, 20], 16)
     k1, k2, v = pb.caches

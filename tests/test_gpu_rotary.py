@@ -348,3 +348,33 @@ def test_large_offsets():
     da.paged_cache_append(k, k, k, kc, kc, kc.clone(), table, torch.tensor([126], dtype=torch.int32, device="cuda"))
     assert torch.equal(kc[-1, :, 126:], k[0]) and torch.count_nonzero(kc[-1, :, :126]) == 0
     assert torch.count_nonzero(kc[:-1].view(torch.int16)) == 0
+
+
+def test_more_than_2_31_elements():
+    """Rows whose elements lie past 2^31, with gradients: the first and last tokens'."""
+    T, H, D = (1 << 23) + 37, 2, 128
+    assert T * H * D > 2 ** 31
+    g = torch.Generator().manual_seed(5)
+    x = torch.zeros(1, T, H, D, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    dy = torch.zeros_like(x)
+    ends = torch.cat([torch.arange(5), torch.arange(T - 40, T)])
+    some, up = (torch.randn(1, H, len(ends), D, generator=g).to(torch.bfloat16) for _ in range(2))
+    x[:, :, ends.cuda()], dy[:, :, ends.cuda()] = some.cuda(), up.cuda()
+    cos, sin = da.rotary_tables(64, D)
+    pos = (torch.arange(T) % 64).int()
+    w = (1 + 0.1 * torch.randn(D, generator=g)).cuda().requires_grad_()
+    x.requires_grad_()
+    y = da.qk_norm_rotary(x, None, None, None, cos.cuda(), sin.cuda(), pos.cuda(), q_weight=w)[0]
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    args = (some.double(), d64(w), cos.double(), sin.double(), pos[ends].long()[None], False, "rms", EPS)
+    want, bound = ref.norm_rotate(*args)
+    assert_within(y[:, :, ends.cuda()].detach(), want, bound, "bf16", "y")
+    want, want_dw, size = ref.norm_rotate_backward(*args, up.double())
+    # bounds as in test_forward_and_backward
+    r = 1 / torch.sqrt((some.double() ** 2).mean(-1, keepdim=True) + EPS)
+    d = up.double().abs().amax(-1, keepdim=True) * 4 * r * d64(w).abs().max() * (1.5 * D + 16)
+    assert_within(dx[:, :, ends.cuda()], want, ref.U * d, "bf16", "dx")
+    want_dw, size = want_dw.sum(0), size.sum(0)
+    tol = ref.U * ((2 * D + 40) * size.max() + H * len(ends) * size)
+    assert ((d64(dw) - want_dw).abs() <= tol).all()
+    assert not dx[:, :, 5:T - 40].any()

@@ -88,6 +88,7 @@ def test_rotary_argument_refusals(lib):
     assert rotary(lib, rotary_desc(), cos=None) == INVALID
     assert rotary(lib, rotary_desc(norm=0), qw=p(30)) == INVALID
     assert rotary(lib, rotary_desc(B=1 << 20, T=1 << 20)) == UNSUPPORTED
+    assert rotary(lib, rotary_desc(B=1, T=(1 << 30) + 1, H=1, Hk=1)) == UNSUPPORTED
     assert rotary(lib, rotary_desc(B=1 << 15, T=1 << 15, H=300)) == UNSUPPORTED
     assert rotary(lib, rotary_desc(H=40000)) == UNSUPPORTED
 
@@ -132,6 +133,15 @@ def test_append_refusals(lib):
         assert append(g=pages(**kw)) == INVALID
     assert append(g=pages(page_size=1 << 21)) == UNSUPPORTED
     assert append(d=rotary_desc(Hk=30000)) == UNSUPPORTED
+    # one place for two tokens, and one cache twice
+    k, v = (16 * 128, 16 * 64, 64), (16 * 256, 16 * 128, 128)
+    for i in range(3):
+        for name, s in (("k1_stride", k), ("k2_stride", k), ("v_stride", v)):
+            good = dict(k1_stride=k, k2_stride=k, v_stride=v)
+            good[name] = tuple(0 if j == i else s[j] for j in range(3))
+            assert append(g=pages(**good)) == INVALID, (name, i)
+    good = dict(k1_stride=k, k2_stride=k, v_stride=v)
+    assert append(g=pages(**good), vc=p(5)) == INVALID and append(g=pages(**good), vc=p(6)) == INVALID
 
 
 def decode(lib, d=None, g=None, ws=p(40), n=1 << 30, mask=None, lam=0.5, epi=None, **miss):
@@ -160,6 +170,8 @@ def test_decode_argument_refusals(lib):
     assert decode(lib, paged_desc(Tq=65), mask=p(8)) == INVALID
     assert decode(lib, paged_desc(Tq=1025)) == UNSUPPORTED
     assert decode(lib, g=pages(num_pages=1 << 31)) == UNSUPPORTED
+    for o in ((0, 128, 512), (4 * 3 * 128, 0, 128), (4 * 3 * 128, 128, 0)):
+        assert decode(lib, paged_desc(o_stride=o)) == INVALID
     assert lib.diffattn_paged_workspace_bytes(ctypes.byref(paged_desc()), ctypes.byref(pages())) > 0
 
 
