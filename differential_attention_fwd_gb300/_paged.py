@@ -66,9 +66,9 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
     None = 1.  Arithmetic in float32, one rounding at the end.
 
     Returns (q1, k1, q2, k2), contiguous, None where None was given.  Differentiable
-    in the rows and the weights.  (Captured into a CUDA graph, take gradients with
-    torch.autograd.grad, or with leaves that no eager graph still holds: torch's
-    gradient accumulation otherwise joins the capture to the other graph's stream.)
+    in the rows and the weights.  (A backward pass captured into a CUDA graph must not
+    add to leaves that an eager graph on the default stream still holds: torch would join
+    that stream to the capture, so this is an error.  torch.autograd.grad is free of it.)
     """
     return (_native or _load()).rotary(q1, k1, q2, k2, cos, sin, positions, norm, norm_eps, q_weight, k_weight,
                                        interleaved)

@@ -13,6 +13,7 @@
 #include <mutex>
 #include <optional>
 #include <string>
+#include <unordered_set>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -20,11 +21,14 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/utils.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/saved_variable.h>
 
@@ -225,6 +229,37 @@ void rotary_forward(const Rotary& r, const Tensor (&x)[4], Tensor (&y)[4], at::D
           "diffattn_rotary");
 }
 
+// In a capture: whether this backward pass goes on to add to the .grad of a leaf whose
+// accumulation belongs to the default stream, because an eager graph of that leaf made it
+// there and still lives.  torch would then make the default stream wait inside the capture,
+// which CUDA forbids and the process does not survive.
+bool joins_default_stream(const torch::autograd::Node& from) {
+    using namespace torch::autograd;
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return false;
+    const auto* task = get_current_graph_task_exec_info();      // empty: every node runs
+    std::unordered_set<const Node*> seen;
+    std::vector<const Node*> todo{&from};
+    while (!todo.empty()) {
+        const Node* n = todo.back();
+        todo.pop_back();
+        for (const Edge& e : n->next_edges()) {
+            Node* next = e.function.get();
+            if (!next || !seen.insert(next).second) continue;
+            if (task && !task->empty()) {
+                const auto it = task->find(next);
+                if (it == task->end() || !it->second.needed_) continue;
+            }
+            if (dynamic_cast<AccumulateGrad*>(next)) {
+                const auto stream = next->stream();
+                if (stream && stream->id() == 0) return true;
+            } else {
+                todo.push_back(next);
+            }
+        }
+    }
+    return false;
+}
+
 // The autograd node: backward through diffattn_rotary_bwd.  Its inputs are the rows that
 // were given, then the weights; its outputs the rotated rows.
 struct RotaryBackward : public torch::autograd::Node {
@@ -239,6 +274,9 @@ struct RotaryBackward : public torch::autograd::Node {
         TORCH_CHECK(!released, "qk_norm_rotary: backward a second time through a graph whose saved tensors were freed; "
                                "pass retain_graph=True the first time");
         TORCH_CHECK(!at::GradMode::is_enabled(), "qk_norm_rotary is differentiable once (no create_graph)");
+        TORCH_CHECK(!joins_default_stream(*this), "qk_norm_rotary: this captured backward pass would add to the .grad of a "
+                    "leaf that a graph made outside the capture, on the default stream, still holds; drop that graph (or "
+                    "make it on another stream), or take the gradients with torch.autograd.grad");
         Rotary c = r;
         // unpacking checks that nothing saved was changed in place
         if (c.R > 0) {

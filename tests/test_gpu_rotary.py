@@ -259,6 +259,39 @@ def test_capture_and_other_streams():
     assert not torch.equal(first[0], held[0])
 
 
+def test_captured_backward_beside_a_living_graph():
+    """Gradients added in a capture to leaves that an eager graph holds: refused where that
+    graph was made on the default stream, right where it was made on another."""
+    g = torch.Generator().manual_seed(9)
+    x = rows(g, "bf16", 2, 4, 50, 64, "head")
+    cos, sin = da.rotary_tables(50, 64, device="cuda")
+    dy = torch.randn(x.shape, generator=g).to(torch.bfloat16).cuda()
+    for where in ("default", "side"):
+        leaf = x.clone().requires_grad_()
+        w = torch.ones(64, device="cuda").requires_grad_()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side if where == "side" else torch.cuda.default_stream()):
+            eager = da.qk_norm_rotary(leaf * 1, None, None, None, cos, sin, q_weight=w)[0]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+
+        def captured():
+            with torch.cuda.graph(graph, stream=side if where == "side" else None):
+                da.qk_norm_rotary(leaf * 1, None, None, None, cos, sin, q_weight=w)[0].backward(dy)
+
+        if where == "default":
+            with pytest.raises(RuntimeError, match="default stream"):
+                captured()
+            assert leaf.grad is None and w.grad is None
+            continue
+        captured()
+        graph.replay()
+        want = torch.autograd.grad(eager, [leaf, w], dy)
+        torch.cuda.synchronize()
+        assert torch.equal(leaf.grad, want[0]) and torch.equal(w.grad, want[1])
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
