@@ -99,20 +99,15 @@ __device__ __forceinline__ uint32_t tm_s(int br, int buf) { return br * 128 + bu
 
 __device__ __forceinline__ bool bf16_finite(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
 
-// The 32 x 32 words that a warp holds, a row a lane, turned: lane j's o[i] goes to lane i's
-// o[j].  Five rounds that swap ever smaller halves between lanes.
-__device__ __forceinline__ void transpose32(uint32_t (&o)[32], uint32_t lane) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        const bool up = lane & m;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i & m) continue;
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[i] : o[i + m], m);
-            if (up) o[i] = got;
-            else o[i + m] = got;
-        }
-    }
+// 16 rows x 32 columns of TMEM: of each 8 columns, words 4 i .. 4 i + 3 of lane t are row
+// t / 4, columns 2 (t % 4) and the next, and the same of row t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
 }
 
 // Maximum of 32 scores, in three chains.
@@ -595,24 +590,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 if (lane == 0) mbar_arrive(&bars[B_O_EMPTY]);
             };
             if (!cur.whole() || odd) {
-                // ---- a partial result: this branch's 128 columns of the row.  A row a lane, as
-                // TMEM gives it, is 32 lines a store (4 us a segment), so it is turned within
-                // the warp to a row a store.  Loops that stay loops, here and below: this code
-                // runs once or twice a block, and its first fetch is what it costs (17 us for
-                // the first segment with the four column groups unrolled).
+                // ---- a partial result: this branch's 128 columns of the row, read from TMEM so
+                // that four lanes hold 32 bytes of a row: a row a lane is 32 lines a store (4 us a
+                // segment), and turning that by shuffles took as long.  Loops that stay loops,
+                // here and below: this code runs once or twice a block, and its first fetch is
+                // what it costs (17 us for the first segment with everything unrolled).
                 const unsigned rows = __ballot_sync(0xffffffffu, mine);
-                float* at = p.part + ((int64_t)cur.slot() * p.chunk_rows + quad * 32) * paged_part_floats(DV) + 4 + br * DV + lane;
+                float* at = p.part + ((int64_t)cur.slot() * p.chunk_rows + quad * 32 + (lane >> 2)) * paged_part_floats(DV) + 4 +
+                            br * DV + 2 * (lane & 3);
 #pragma unroll 1
-                for (int c = 0; c < DV; c += 32) {
-                    uint32_t o[32] = {};
+                for (int i = 0; i < 2 * DV / 32; ++i) {
+                    const int r0 = i & 1 ? 16 : 0, c = (i >> 1) * 32;
+                    uint32_t o[16] = {};
                     if (live > 0) {
-                        tmem_ld32(tO + c, o);
+                        tmem_ld_rows16(tO + ((uint32_t)r0 << 16) + c, o);
                         tmem_wait_ld();
                     }
-                    transpose32(o, lane);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (rows >> i & 1u) at[i * paged_part_floats(DV) + c] = __uint_as_float(o[i]);
+                    for (int k = 0; k < 2; ++k)
+                        if (rows >> (r0 + 8 * k + (lane >> 2)) & 1u)
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                *reinterpret_cast<float2*>(at + (r0 + 8 * k) * paged_part_floats(DV) + c + 8 * n) =
+                                    make_float2(__uint_as_float(o[4 * n + 2 * k]), __uint_as_float(o[4 * n + 2 * k + 1]));
                 }
                 release_o();
                 if (odd) {
