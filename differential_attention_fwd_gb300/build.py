@@ -67,7 +67,7 @@ def _binding_command(obj: str):
                 "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
                 "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     link = [cxx, "-shared", obj, "-o", BINDING + ".tmp", "-L", PKG, "-l:libdiffattn.so", "-L", lib, "-lc10", "-lc10_cuda",
-            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 
 
