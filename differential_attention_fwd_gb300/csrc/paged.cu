@@ -63,6 +63,8 @@ struct Layout {
     int stage;          // bytes
     int off_q, off_p, off_stat, total;
 };
+// Floats of a key's weights: 4 x an odd number, so that keys of 32 lanes spread over the banks.
+__host__ __device__ constexpr int weights_row(int rc) { return rc > 2 ? 2 * rc + 4 : 2 * rc; }
 __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, bool shared) {
     const int v = 16 / es;
     Layout l;
@@ -73,8 +75,8 @@ __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, boo
     // the stages also hold the merged O of a segment: [2][rc][Dv] floats
     const int stages = 2 * l.stage > 8 * rc * Dv ? 2 * l.stage : 8 * rc * Dv;
     l.off_q = (stages + 15) / 16 * 16;                          // float [2][rc][dpad]
-    l.off_p = l.off_q + 2 * rc * l.dpad * 4;                    // float [KT][2 rc]
-    l.off_stat = l.off_p + KT * 2 * rc * 4;                     // float m, l, alpha [2 rc]
+    l.off_p = l.off_q + 2 * rc * l.dpad * 4;                    // float [KT][weights_row(rc)]
+    l.off_stat = l.off_p + KT * weights_row(rc) * 4;                     // float m, l, alpha [2 rc]
     l.total = l.off_stat + 3 * 2 * rc * 4;
     return l;
 }
@@ -82,7 +84,7 @@ __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, boo
 template <typename T, int RC>
 __global__ void __launch_bounds__(THREADS)
 paged_simt_kernel(const PagedParams p) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), PS = weights_row(RC);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scan[2 * WARPS];
     __shared__ PagedBlock<1> blk;
@@ -96,7 +98,7 @@ paged_simt_kernel(const PagedParams p) {
     float* st_l = st_m + 2 * RC;
     float* st_a = st_l + 2 * RC;
     pdl_launch_dependents();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, 1, SNAP, &blk);
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
@@ -110,8 +112,15 @@ paged_simt_kernel(const PagedParams p) {
     for (cur.begin(p, blk, 0, blockIdx.x, KT, EXTRA); !cur.done(); cur.next(p, KT, EXTRA)) {
         const int live = cur.live_tiles(p, KT);
         const int n_new = cur.s.n_new;
-        if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP, EXTRA);
+        if (tid == 0) cur.join(p, blk.shares, blk.start[1].tile, EXTRA);
         bool bad = cur.s.bad;
+        // The page of the row that a thread stages of a tile (four threads a key row), a tile
+        // ahead; the first two beside the queries.
+        auto look = [&](int tile) -> int {
+            const int key = (cur.tile0 + tile) * KT + (tid >> 2);
+            return tile < live && key < cur.s.total ? paged_page(p, cur.b, key / p.page) : -2;
+        };
+        int page = look(0), next = look(1);
         // the rows' queries and state
 #pragma unroll
         for (int j0 = 0; j0 < 2 * RC; j0 += WARPS) {
@@ -129,13 +138,8 @@ paged_simt_kernel(const PagedParams p) {
 #pragma unroll
             for (int r = 0; r < RC; ++r) acc[i][0][r] = acc[i][1][r] = 0.f;
 
-        // Stage a tile: four threads a key row, whose page was looked up a tile before.  A row
-        // past the sequence's end or on a page outside the cache is zeros (the latter makes
-        // the segment's rows NaN).
-        auto look = [&](int tile) -> int {
-            const int key = (cur.tile0 + tile) * KT + (tid >> 2);
-            return tile < live && key < cur.s.total ? paged_page(p, cur.b, key / p.page) : -2;
-        };
+        // A row past the sequence's end or on a page outside the cache is zeros (the latter
+        // makes the segment's rows NaN).
         auto stage = [&](int tile, int buf, int page) {
             const int r = tid >> 2, c4 = tid & 3;
             const int key = (cur.tile0 + tile) * KT + r;
@@ -161,10 +165,9 @@ paged_simt_kernel(const PagedParams p) {
                 for (int c = c4; c < L.vrow; c += 4) v[c] = page >= 0 && c < Dv ? gv[c] : T(0.f);
             }
         };
-        int page = look(0);
         if (live > 0) stage(0, 0, page);
         cp_async_commit();
-        page = look(1);
+        page = next;
         for (int i = 0; i < live; ++i) {
             if (i + 1 < live) stage(i + 1, (i + 1) & 1, page);
             cp_async_commit();
@@ -200,7 +203,7 @@ paged_simt_kernel(const PagedParams p) {
                             }
                     }
 #pragma unroll
-                    for (int r = 0; r < HALF; ++r) ps[lane * 2 * RC + br * RC + r0 + r] = s[r] * p.scale_log2;
+                    for (int r = 0; r < HALF; ++r) ps[lane * PS + br * RC + r0 + r] = s[r] * p.scale_log2;
                 }
             }
             __syncthreads();
@@ -213,7 +216,7 @@ paged_simt_kernel(const PagedParams p) {
 #pragma unroll
                 for (int k = 0; k < NJ; ++k) {
                     const int j = min(warp + k * WARPS, 2 * RC - 1);
-                    s[k] = ps[lane * 2 * RC + j];
+                    s[k] = ps[lane * PS + j];
                     seen[k] = true;
                     if (edge) {
                         const PagedRow x = paged_row(p, cur.hk, cur.rc, j % RC, n_new);
@@ -245,7 +248,7 @@ paged_simt_kernel(const PagedParams p) {
                 for (int k = 0; k < NJ; ++k) {
                     const int j = warp + k * WARPS;
                     if (j >= 2 * RC) break;
-                    ps[lane * 2 * RC + j] = seen[k] ? w[k] : -1.f;
+                    ps[lane * PS + j] = seen[k] ? w[k] : -1.f;
                     if (lane == 0) {
                         const float a = m0[k] == top[k] ? 1.f : exp2f(m0[k] - top[k]);
                         st_m[j] = top[k];
@@ -266,19 +269,24 @@ paged_simt_kernel(const PagedParams p) {
                     acc[1][1][r] *= a2;
                 }
                 const bool second = two && c0 + 128 < Dv;
-                for (int t = kg; t < KT; t += KG) {
-                    const float x = to_float<T>(vt[t * L.vrow + c0]);
-                    const float y = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
-                    float w[2 * RC];
+                auto value = [&](int t, float& x, float& y, float (&w)[2 * RC]) {
+                    x = to_float<T>(vt[t * L.vrow + c0]);
+                    y = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
                     if constexpr (RC > 1) {
 #pragma unroll
                         for (int r = 0; r < 2 * RC; r += 4)
-                            *reinterpret_cast<float4*>(w + r) = *reinterpret_cast<const float4*>(ps + t * 2 * RC + r);
+                            *reinterpret_cast<float4*>(w + r) = *reinterpret_cast<const float4*>(ps + t * PS + r);
                     } else {
-                        w[0] = ps[2 * t];
-                        w[1] = ps[2 * t + 1];
+                        w[0] = ps[t * PS];
+                        w[1] = ps[t * PS + 1];
                     }
-                    if (!edge) {
+                };
+                if (!edge) {
+                    // two keys at a time, so that one's reads pass while the other's are used
+#pragma unroll 2
+                    for (int t = kg; t < KT; t += KG) {
+                        float x, y, w[2 * RC];
+                        value(t, x, y, w);
 #pragma unroll
                         for (int r = 0; r < RC; ++r) {
                             acc[0][0][r] = fmaf(w[r], x, acc[0][0][r]);
@@ -288,7 +296,12 @@ paged_simt_kernel(const PagedParams p) {
                                 acc[1][1][r] = fmaf(w[RC + r], y, acc[1][1][r]);
                             }
                         }
-                    } else {
+                    }
+                } else {
+#pragma unroll 1
+                    for (int t = kg; t < KT; t += KG) {
+                        float x, y, w[2 * RC];
+                        value(t, x, y, w);
 #pragma unroll
                         for (int r = 0; r < RC; ++r) {
                             if (w[r] < 0.f) continue;               // hidden

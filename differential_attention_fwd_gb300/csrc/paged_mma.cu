@@ -144,7 +144,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     const PagedScan found = paged_scan<THREADS>(p, KT, EXTRA, scan);
     const bool solo = p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
     const int nw = solo ? WARPS : 1;                            // workers of the block
-    paged_locate<WARPS>(p, found, KT, EXTRA, nw, gridDim.x * nw, 1, SNAP, &blk);
+    paged_locate<WARPS>(p, found, KT, EXTRA, nw, gridDim.x * nw, SNAP, &blk);
     const int mine = solo ? w : 0;
     const int worker = blockIdx.x * nw + mine;
     // the warp's slices in a tile: all four, or one
@@ -173,7 +173,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         bool ok = true;
         for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
             const int live = cur.live_tiles(p, KT) * slices;
-            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, SNAP, EXTRA);
+            if (scribe) cur.join(p, blk.shares, blk.start[mine + 1].tile, EXTRA);
             int page = 0;                       // of slice i0 + lane, looked up 32 at a time
             for (int i = 0; i < live; ++i) {
                 // slice i of the warp: the key it starts with

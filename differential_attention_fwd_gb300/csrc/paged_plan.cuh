@@ -5,9 +5,9 @@
 // groups of warps, or warps) and every one finds its own share.  A unit is (sequence,
 // key/value head, row chunk) with the sequence's tiles of KT keys; the units' tiles are
 // laid end to end, sequence by sequence, and of `total` tiles every worker takes
-// total / G in a row, or one more, whatever the lengths; G is all workers, or fewer so
-// that each has min_tiles.  A boundary that falls within `snap` tiles of a unit's end
-// moves there: so little work is not worth a unit in two parts.
+// total / G in a row, or one more, whatever the lengths (fewer workers where there are
+// fewer tiles).  A boundary that falls within `snap` tiles of a unit's end moves there:
+// so little work is not worth a unit in two parts, unless it is much of a share.
 //
 // A worker's range falls into segments, each of one unit.  A segment that holds its whole
 // unit is finished by its worker; one that does not leaves a partial result: in slot
@@ -63,11 +63,13 @@ struct PagedShares {
     int total;          // tiles of all units
     int workers;        // that take tiles
     int each, more;     // `more` of them take each + 1 tiles, the others each
-    __device__ __forceinline__ void set(int t, int most, int min_tiles) {
+    int snap;
+    __device__ __forceinline__ void set(int t, int most, int most_snap) {
         total = t;
-        workers = min(most, max(t / min_tiles, t > 0 ? 1 : 0));
+        workers = min(most, t);
         each = workers ? t / workers : 0;
         more = t - each * workers;
+        snap = min(most_snap, each / 4);
     }
     // Where worker c's share begins before it is moved to a unit's end; `total` for a
     // worker that takes none.
@@ -143,11 +145,11 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
 // Every thread calls this, and it ends with a barrier.
 template <int NW>
 __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedScan& s, int kt, int extra, int nw, int most,
-                                             int min_tiles, int snap, PagedBlock<NW>* out) {
+                                             int snap, PagedBlock<NW>* out) {
     const int tid = threadIdx.x;
     const int units = p.Hk * p.row_chunks;
     PagedShares sh;
-    sh.set(s.total, most, min_tiles);
+    sh.set(s.total, most, snap);
     if (tid == 0) out->shares = sh;
     if (tid <= nw && sh.bound(blockIdx.x * nw + tid) >= s.total) out->start[tid] = PagedStart{s.total, p.B, 0};
     for (int w = 0; w <= nw; ++w) {
@@ -160,7 +162,7 @@ __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedSc
             tiles += extra;
             if (first < at + tiles * units) {
                 const int off = (first - at) % tiles;       // in its unit
-                const int move = off <= extra + snap ? -off : tiles - off <= snap ? tiles - off : 0;
+                const int move = off <= extra + sh.snap ? -off : tiles - off <= sh.snap ? tiles - off : 0;
                 out->start[w] = PagedStart{first + move, b, first + move - at};
                 break;
             }
@@ -223,10 +225,10 @@ struct PagedCursor {
     // this range's last, and the workers that go on with it are those whose bounds fall
     // into it and were not moved to its ends.  `end`: where this range ends.
     __device__ __forceinline__ static void no_join(const PagedParams& p, int c) { p.joins[c].parts = 0; }
-    __device__ __forceinline__ void join(const PagedParams& p, const PagedShares& sh, int end, int snap, int extra) const {
+    __device__ __forceinline__ void join(const PagedParams& p, const PagedShares& sh, int end, int extra) const {
         if (tile0 != 0 || whole()) return;
         const int u1 = end - step + tiles + extra;
-        p.joins[worker] = PagedJoin{sh.worker_at(u1 - snap - 1) - worker + 1, b, hk * p.row_chunks + rc, s.n_new};
+        p.joins[worker] = PagedJoin{sh.worker_at(u1 - sh.snap - 1) - worker + 1, b, hk * p.row_chunks + rc, s.n_new};
     }
     // The segment's tiles that some row of its chunk may see: later ones hold only
     // keys behind the chunk's last query.

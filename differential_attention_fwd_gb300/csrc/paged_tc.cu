@@ -211,7 +211,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, 1, SNAP, &blk);    // with their barriers
+    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);    // with their barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
     const uint64_t lim = 200ull * 1000ull * 1000ull;
@@ -238,7 +238,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
                 const int live = cur.live_tiles(p, KT);
                 if (cur.s.bad && lane == 0) atomicOr(p.status, kStatusIndex);
-                if (lane == 0) cur.join(p, blk.shares, blk.start[1].tile, SNAP, EXTRA);
+                if (lane == 0) cur.join(p, blk.shares, blk.start[1].tile, EXTRA);
                 if (live == 0) continue;
                 ++seg;
                 if (lane == 0) bad_seg[seg % SEGS] = 0;
