@@ -379,9 +379,12 @@ constexpr int C_WARPS = 8;
 constexpr int kJoinsPerBlock = 4;
 
 // J columns a lane; VEC: J = 4 of them in a row, for a value width of 128 in bf16 (two
-// 16-byte reads a part instead of eight of 4 bytes).
-template <int J, bool VEC>
-__global__ void __launch_bounds__(C_WARPS * 32, J == 4 ? 4 : 2)
+// 16-byte reads a part instead of eight of 4 bytes).  AHEAD: parts read at once.  Four for
+// units of up to 16 rows, which may have many parts and leave the SMs empty (one sequence
+// of 517 keys: 14.1 us in all with two, 13.2 with four); two for those of 128, whose rows
+// want the warps that fewer registers allow (61 tokens over 16 x 8192: 117.5, 118.2 with four).
+template <int J, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(C_WARPS * 32, J > 4 ? 2 : AHEAD > 2 ? 3 : 4)
 paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -420,7 +423,6 @@ paged_combine_kernel(const PagedParams p) {
                 // Loads first, and all that fit: the pass is the latency of L2, met once if
                 // no load waits for another's value.  So no branch on a weight either (a
                 // part that saw nothing holds zeros).
-                constexpr int AHEAD = 2;
                 float4 v[AHEAD][2][(J + 3) / 4];
                 float4 st[AHEAD];
                 auto load = [&](int i, int k) {
@@ -570,9 +572,12 @@ int launch_paged_combine(const PagedParams& params, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = p.Dv == 128 && p.bf16 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true>, p)
-                          : p.Dv <= 128         ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, false>, p)
-                                                : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8, false>, p);
+    const bool vec = p.Dv == 128 && p.bf16;
+    const cudaError_t e =
+        vec && p.chunk_rows > 16 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true, 2>, p)
+        : vec                    ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true, 4>, p)
+        : p.Dv <= 128            ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, false, 4>, p)
+                                 : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8, false, 2>, p);
     return e == cudaSuccess ? 0 : -1;
 }
 
