@@ -11,15 +11,15 @@
 //   - A second warp streams its slices of 16 keys through TMA into a ring of its own,
 //     across unit boundaries.  A slice lies in one page.  Two blocks of four such pairs
 //     an SM keep 130 to 190 KB in flight, more than the HBM rate times its latency.
-//   - SMs stream at different rates (the slowest 20 % behind the fastest), so there are
-//     more blocks than fit at once, and an SM that is done sooner gets another; the other
-//     block of the SM streams while it starts.
+//   - SMs stream at different rates (the slowest 20 % behind the fastest), which is what
+//     is left of a long call: blocks end between 99 and 119 us of 120.  Twice the blocks in
+//     waves cost more by their starts (133 us).
 //   - With many units (a batch of short sequences) a worker is one warp, which writes its
 //     rows from its registers at a unit's end.  With few, four warps share a worker's
 //     tiles of 64 keys and merge their results in shared memory at its end, so that the
 //     merging pass has a quarter of the parts.  (2048 units of 100 keys: 78 us with four
-//     warps a worker, whose merge takes 2 us a unit, 51 with one.  16 units of 16384:
-//     33 us with four, 42 with one, the difference in the merging pass.)
+//     warps a worker, whose merge takes 2 us a unit, 51 with one, 39 with what followed.
+//     16 units of 16384: 33 us with four, 42 with one, the difference in the merging pass.)
 //   - The products are warp-level (m16n8k16): at this size they are a quarter of the
 //     time that the tile's bytes take, and P goes from the score's accumulators to the
 //     next product's operand in registers.  A tcgen05 product would want 128 keys as its
@@ -30,7 +30,12 @@
 // pass 2^8.  They go to the product with V as two bf16 parts, the rounded weight and what
 // the rounding left (2^-16 together): with one part the branches' difference was off by
 // 2.1e-3 of itself, more than the output's own rounding (1.7e-3), and the second product
-// costs nothing here, since the tile's bytes take longer.
+// costs nothing here, since the tile's bytes take longer (5 % at 4 rows of head width 128).
+//
+// Measured, both launches: 16 sequences of up to 8192 keys, 16 heads, D = 64, 710 MB of
+// cache: 124 us, 0.84 of the copy rate; 4 of 65536, 8 key/value heads, shared keys, D = 128:
+// 122 us, 0.86; one of 517: 13.4 us, the latency of the two launches, the lengths, a page
+// and its keys in turn.
 #include "paged_plan.cuh"
 #include "kernels.h"
 #include "pdl.cuh"

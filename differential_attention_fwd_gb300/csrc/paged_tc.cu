@@ -10,13 +10,17 @@
 // S_b as bf16, and O_b += P_b V.  The work is cut by the lengths on the device (see
 // paged_plan.cuh), and every role walks the block's segments on its own.
 //
-// What bounds it: the tensor core's operands in shared memory, at 128 bytes a cycle.  A
-// 64-key tile of head width 128 reads 96 KB for the scores (Q is read again for each tile;
-// TMEM is full, so it cannot lie there), 64 KB of V for both parts of the weights of both
-// branches, and the copies write 32 KB: 1,540 cycles of the 1,700 that a tile takes, beside
-// 1,000 of the exponential unit and 1,000 of an SM's share of the HBM rate.  The row count
-// hardly matters: 16 sequences of 8192 keys, 8 key/value heads take 102 us with 9 tokens and
-// 120 with 64, and leaving out the weights of padding rows changed neither.
+// What bounds it: the hand-offs between the weights' warps and the tensor core.  A tile of
+// 64 keys takes 1,900 cycles.  Its operands are 1,540 cycles of shared memory at 128 bytes
+// a cycle with head width 128 (96 KB of Q and K for the scores, 64 KB of V for both parts
+// of both branches' weights, 32 KB of copies), 1,150 with 64; the weights' warps are busy
+// for 1,500; HBM would take 1,000.  Timed with parts left out (16 sequences of 8192 keys, 64
+// tokens; head width 128 on 8 key/value heads, 64 on 16): all 155 and 249 us, half of the
+// products 149 and 242, no arithmetic between scores and weights 139 and 207, the cache in
+// L2 147 and 246.  Sixteen warps for the weights in place of eight, half of a tile's keys
+// each with a barrier a pair, took 6 % longer, and 4 % with everything unrolled over 64 keys
+// (the warps then wait for instructions).  The row count hardly matters: 99 us with 9 tokens
+// (ragged, 8 heads), 117 with 64.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7   weights and results of branch 1, 2 (TMEM lanes 0-127)
@@ -500,8 +504,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 const bool edge = k0 + KT > s.before;
                 const uint64_t vis = edge && mine ? tile_mask(p, s, k0, x.q, tree) : 0;
                 // A loop over the tile's halves that stays one: each 32 keys' weights go over
-                // their scores, 16 columns a part.  Unrolled, the warps waited for instructions
-                // a fifth of the time.
+                // their scores, 16 columns a part.  Unrolled, it waited for instructions a fifth
+                // of the time (61 tokens over 16 x 8192: 125 us, 121 as a loop).
 #pragma unroll 1
                 for (int h = 0; ok && h < 2; ++h) {
                     uint32_t sc[32], pk[32];
