@@ -177,7 +177,7 @@ void plan_simt(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, P
     n->chunk_rows = paged_simt_rows(group * d.Tq);
     n->row_chunks = (int)((group * d.Tq + n->chunk_rows - 1) / n->chunk_rows);
     n->tile = 32;
-    n->workers = fewer(d, g, n, sms * kSimtBlocksPerSm);
+    n->workers = fewer(d, g, n, sms * paged_simt_blocks((int)d.D, (int)dv, d.dtype == DIFFATTN_BF16 ? 2 : 4, n->chunk_rows));
     n->bytes = part_bytes(*n, dv);
 }
 

@@ -70,7 +70,7 @@ struct Layout {
     int off_q, off_p, off_stat, total;
 };
 // Floats of a key's weights: 4 x an odd number, so that keys of 32 lanes spread over the banks.
-__host__ __device__ constexpr int weights_row(int rc) { return rc > 2 ? 2 * rc + 4 : 2 * rc; }
+__host__ __device__ constexpr int weights_row(int rc) { return rc > 1 && rc % 4 == 0 ? 2 * rc + 4 : 2 * rc; }
 __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, bool shared) {
     const int v = 16 / es;
     Layout l;
@@ -87,8 +87,11 @@ __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, boo
     return l;
 }
 
-template <typename T, int RC>
-__global__ void __launch_bounds__(THREADS)
+// TWO: value widths above 128 (a thread has two columns).  Without, four blocks an SM, whose
+// latencies hide one another: 9 rows a key/value head (4 sequences of up to 8348 keys, 16
+// heads, D = 32, float32) take 272 us with two, which 255 registers leave, 151 with four.
+template <typename T, int RC, bool TWO>
+__global__ void __launch_bounds__(THREADS, TWO ? 1 : kSimtBlocksPerSm)
 paged_simt_kernel(const PagedParams p) {
     constexpr int V = 16 / sizeof(T), PS = weights_row(RC);
     extern __shared__ __align__(16) uint8_t smem[];
@@ -111,7 +114,6 @@ paged_simt_kernel(const PagedParams p) {
     const int CG = Dv <= 32 ? 32 : Dv <= 64 ? 64 : 128;
     const int KG = THREADS / CG;
     const int c0 = tid % CG, kg = tid / CG;
-    const bool two = Dv > 128;
 
     PagedCursor cur;
     if (tid == 0) PagedCursor::no_join(p, blockIdx.x);
@@ -138,9 +140,10 @@ paged_simt_kernel(const PagedParams p) {
             for (int c = lane; c < L.dpad; c += 32) qs[j * L.dpad + c] = x.live && c < D ? to_float<T>(src[c]) : 0.f;
         }
         if (tid < 2 * RC) { st_m[tid] = -INFINITY; st_l[tid] = 0.f; }
-        float acc[2][2][RC];
+        constexpr int COLS = TWO ? 2 : 1;
+        float acc[COLS][2][RC];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < COLS; ++i)
 #pragma unroll
             for (int r = 0; r < RC; ++r) acc[i][0][r] = acc[i][1][r] = 0.f;
 
@@ -269,15 +272,16 @@ paged_simt_kernel(const PagedParams p) {
 #pragma unroll
                 for (int r = 0; r < RC; ++r) {
                     const float a1 = st_a[r], a2 = st_a[RC + r];
-                    acc[0][0][r] *= a1;
-                    acc[0][1][r] *= a2;
-                    acc[1][0][r] *= a1;
-                    acc[1][1][r] *= a2;
+#pragma unroll
+                    for (int i = 0; i < COLS; ++i) {
+                        acc[i][0][r] *= a1;
+                        acc[i][1][r] *= a2;
+                    }
                 }
-                const bool second = two && c0 + 128 < Dv;
-                auto value = [&](int t, float& x, float& y, float (&w)[2 * RC]) {
-                    x = to_float<T>(vt[t * L.vrow + c0]);
-                    y = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
+                const bool second = TWO && c0 + 128 < Dv;
+                auto value = [&](int t, float (&x)[COLS], float (&w)[2 * RC]) {
+                    x[0] = to_float<T>(vt[t * L.vrow + c0]);
+                    if constexpr (TWO) x[1] = second ? to_float<T>(vt[t * L.vrow + c0 + 128]) : 0.f;
                     if constexpr (RC > 1) {
 #pragma unroll
                         for (int r = 0; r < 2 * RC; r += 4)
@@ -291,30 +295,29 @@ paged_simt_kernel(const PagedParams p) {
                     // two keys at a time, so that one's reads pass while the other's are used
 #pragma unroll 2
                     for (int t = kg; t < KT; t += KG) {
-                        float x, y, w[2 * RC];
-                        value(t, x, y, w);
+                        float x[COLS], w[2 * RC];
+                        value(t, x, w);
 #pragma unroll
-                        for (int r = 0; r < RC; ++r) {
-                            acc[0][0][r] = fmaf(w[r], x, acc[0][0][r]);
-                            acc[0][1][r] = fmaf(w[RC + r], x, acc[0][1][r]);
-                            if (two) {
-                                acc[1][0][r] = fmaf(w[r], y, acc[1][0][r]);
-                                acc[1][1][r] = fmaf(w[RC + r], y, acc[1][1][r]);
+                        for (int i = 0; i < COLS; ++i)
+#pragma unroll
+                            for (int r = 0; r < RC; ++r) {
+                                acc[i][0][r] = fmaf(w[r], x[i], acc[i][0][r]);
+                                acc[i][1][r] = fmaf(w[RC + r], x[i], acc[i][1][r]);
                             }
-                        }
                     }
                 } else {
 #pragma unroll 1
                     for (int t = kg; t < KT; t += KG) {
-                        float x, y, w[2 * RC];
-                        value(t, x, y, w);
+                        float x[COLS], w[2 * RC];
+                        value(t, x, w);
 #pragma unroll
                         for (int r = 0; r < RC; ++r) {
                             if (w[r] < 0.f) continue;               // hidden
-                            acc[0][0][r] = fmaf(w[r], x, acc[0][0][r]);
-                            acc[0][1][r] = fmaf(w[RC + r], x, acc[0][1][r]);
-                            acc[1][0][r] = fmaf(w[r], y, acc[1][0][r]);
-                            acc[1][1][r] = fmaf(w[RC + r], y, acc[1][1][r]);
+#pragma unroll
+                            for (int i = 0; i < COLS; ++i) {
+                                acc[i][0][r] = fmaf(w[r], x[i], acc[i][0][r]);
+                                acc[i][1][r] = fmaf(w[RC + r], x[i], acc[i][1][r]);
+                            }
                         }
                     }
                 }
@@ -334,7 +337,8 @@ paged_simt_kernel(const PagedParams p) {
                     for (int br = 0; br < 2; ++br) {
                         float* o = om + (br * RC + r) * Dv + c0;
                         o[0] = k ? o[0] + acc[0][br][r] : acc[0][br][r];
-                        if (two && c0 + 128 < Dv) o[128] = acc[1][br][r];      // one key group then
+                        if constexpr (TWO)                                      // one key group then
+                            if (c0 + 128 < Dv) o[128] = acc[1][br][r];
                     }
             }
             __syncthreads();
@@ -527,10 +531,9 @@ paged_combine_kernel(const PagedParams p) {
 template <typename T, int RC>
 int launch_rc(const PagedParams& p, cudaStream_t stream) {
     const Layout L = simt_layout(p.D, p.Dv, sizeof(T), RC, p.k_shared != 0);
-    if (cudaFuncSetAttribute(paged_simt_kernel<T, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) !=
-        cudaSuccess)
-        return -1;
-    paged_simt_kernel<T, RC><<<p.workers, THREADS, L.total, stream>>>(p);
+    const auto kernel = p.Dv > 128 ? paged_simt_kernel<T, RC, true> : paged_simt_kernel<T, RC, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) != cudaSuccess) return -1;
+    kernel<<<p.workers, THREADS, L.total, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
@@ -540,7 +543,9 @@ int launch_t(const PagedParams& p, cudaStream_t stream) {
         case 1: return launch_rc<T, 1>(p, stream);
         case 2: return launch_rc<T, 2>(p, stream);
         case 4: return launch_rc<T, 4>(p, stream);
+        case 6: return launch_rc<T, 6>(p, stream);
         case 8: return launch_rc<T, 8>(p, stream);
+        case 12: return launch_rc<T, 12>(p, stream);
         case 16: return launch_rc<T, 16>(p, stream);
         default: return -1;
     }
@@ -549,9 +554,15 @@ int launch_t(const PagedParams& p, cudaStream_t stream) {
 }  // namespace paged
 
 int paged_simt_rows(int64_t rows) {
-    for (int r = 1; r < paged::MAX_RC; r *= 2)
+    for (int r : {1, 2, 4, 6, 8, 12})
         if (rows <= r) return r;
     return paged::MAX_RC;
+}
+
+int paged_simt_blocks(int D, int Dv, int es, int rows) {
+    const int fit = 227 * 1024 / (paged::simt_layout(D, Dv, es, rows, false).total + 1024 + 256);
+    const int most = Dv > 128 ? 2 : kSimtBlocksPerSm;
+    return fit < 1 ? 1 : fit < most ? fit : most;
 }
 
 int launch_paged_combine(const PagedParams& params, cudaStream_t stream) {

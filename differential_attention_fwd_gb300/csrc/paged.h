@@ -145,7 +145,9 @@ __host__ __device__ constexpr int paged_part_floats(int Dv) { return 4 + 2 * pag
 int launch_paged_simt(const PagedParams& p, cudaStream_t stream);
 // Rows of a unit of the CUDA-core kernel, for `rows` query rows a key/value head.
 int paged_simt_rows(int64_t rows);
-constexpr int kSimtBlocksPerSm = 3;
+constexpr int kSimtBlocksPerSm = 4;
+// Blocks of it that an SM holds at once (elements of `es` bytes, `rows` of a unit).
+int paged_simt_blocks(int D, int Dv, int es, int rows);
 // The tensor-core kernel of up to 16 rows a unit: maps of K1, K2 and V with boxes of
 // 64 columns x 16 slots.
 constexpr int kMmaRows = 16;
