@@ -99,6 +99,7 @@ struct PagedBlock {
 struct PagedScan {
     int b0, b1;         // the thread's sequences,
     int at, sum;        // the tiles before them and in them
+    int tiles;          // of a unit of its last sequence with any
     int total, units;   // of the launch
 };
 template <int THREADS>
@@ -110,12 +111,13 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
     PagedScan s;
     s.b0 = min(p.B, tid * per);
     s.b1 = min(p.B, s.b0 + per);
-    s.sum = 0;
+    s.sum = s.tiles = 0;
     int active = 0;
     for (int b = s.b0; b < s.b1; ++b) {
         const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
         s.sum += tiles ? (tiles + extra) * per_seq : 0;
         active += tiles ? per_seq : 0;
+        s.tiles = tiles ? tiles : s.tiles;
     }
     int incl = s.sum;
 #pragma unroll
@@ -157,7 +159,8 @@ __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedSc
         if (first >= s.total || first < s.at || first >= s.at + s.sum) continue;
         int at = s.at;
         for (int b = s.b0; b < s.b1; ++b) {
-            int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+            // with a sequence a thread its tiles are known
+            int tiles = s.b1 - s.b0 == 1 ? s.tiles : paged_seq_tiles(paged_seq(p, b), kt);
             if (tiles == 0) continue;
             tiles += extra;
             if (first < at + tiles * units) {

@@ -193,17 +193,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     const uint32_t lane = threadIdx.x & 31;
     const AbortState ab{abort_flag, p.status};
     pdl_launch_dependents();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bars[i], 1);
-        for (int i = 0; i < KST_MAX; ++i) mbar_init(&bars[B_K_EMPTY + i], 2);
-        for (int i = 0; i < VST; ++i) mbar_init(&bars[B_V_EMPTY + i], 3);   // both products, and warp 11
-        for (int i = 0; i < 4; ++i) mbar_init(&bars[B_P_FULL + i], 4);
-        mbar_init(&bars[B_Q_EMPTY], 2);
-        mbar_init(&bars[B_O_FULL], 2);
-        mbar_init(&bars[B_O_EMPTY], 8);
-        mbar_init(&bars[B_ROWS], 8);
-        for (int i = 0; i < SEGS; ++i) bad_seg[i] = any_flag[i] = 0;
-        *abort_flag = 0;
+    if (threadIdx.x < NUM_BARS) {
+        const int i = threadIdx.x;
+        int arrivals = 1;
+        if ((i >= B_K_EMPTY && i < B_K_EMPTY + KST_MAX) || i == B_Q_EMPTY || i == B_O_FULL) arrivals = 2;   // both products
+        if (i >= B_V_EMPTY && i < B_V_EMPTY + VST) arrivals = 3;        // and warp 11
+        if (i >= B_P_FULL && i < B_P_FULL + 4) arrivals = 4;            // a branch's warps
+        if (i == B_O_EMPTY || i == B_ROWS) arrivals = 8;                // both branches'
+        mbar_init(&bars[i], arrivals);
+        if (i < SEGS) bad_seg[i] = any_flag[i] = 0;
+        if (i == 0) *abort_flag = 0;
         fence_mbar_init();
     }
     // rows of the query tiles that no head fills stay zero: their scores must be finite
