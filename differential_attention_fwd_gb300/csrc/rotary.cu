@@ -415,7 +415,7 @@ rotary_bwd_kernel(const RotaryParams p) {
     const int row1 = (int)((int64_t)(blockIdx.x + 1) * items / gridDim.x) * BWD_STEPS;
     int oa, ob;
     const bool turn = chunk_offsets<V, INTER>(g, p.R, &oa, &ob);
-    uint64_t dw[V] = {};
+    uint64_t dw[V];
 
     // Row i of this group: its stream and head, and its token; b < 0: there is none.
     struct Row {
@@ -480,8 +480,6 @@ rotary_bwd_kernel(const RotaryParams p) {
             for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane < G) red[warp * D + (i < V ? oa + i : ob + i - V)] = v;
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) dw[i] = 0;
         __syncthreads();
         for (int c = tid; c < D; c += THREADS) {
             float sum = 0.f;
@@ -499,6 +497,8 @@ rotary_bwd_kernel(const RotaryParams p) {
         const RowStream& s = p.s[r.si];
         asm volatile("cp.async.wait_group %0;" ::"n"(BWD_STAGES - 1) : "memory");
         if (r.step == 0) {                  // a new item: its weights are there, and its tables
+#pragma unroll
+            for (int e = 0; e < V; ++e) dw[e] = 0;
             __syncthreads();
             if (p.by_heads.div(r.item) != chunk) {
                 enter(chunk = p.by_heads.div(r.item));

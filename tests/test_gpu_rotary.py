@@ -193,6 +193,30 @@ def test_a_weight_by_head_beside_a_shared_one(D, H, Hk, T, q_heads):
         assert ((a.double().sum(0) - b.double()).abs() <= 2.0 ** -24 * 4 * T * n * 40).all()
 
 
+@pytest.mark.parametrize("D,R", [(64, 64), (128, 64), (48, 24)])
+@pytest.mark.parametrize("only", ["q", "k"])
+@pytest.mark.parametrize("other", ["none", "fixed"])
+def test_the_gradient_of_one_weight_alone(D, R, only, other):
+    """One of the weights wants a gradient; the other is left out or wants none."""
+    g = torch.Generator().manual_seed(D + R)
+    B, H, Hk, T = 2, 3, 2, 12007                # several heads a block
+    xs = [rows(g, "bf16", B, n, T, D) for n in (H, Hk, H, Hk)]
+    cos, sin = da.rotary_tables(T, R, device="cuda")
+    w = (1 + 0.3 * torch.randn(D, generator=g)).cuda().requires_grad_()
+    fixed = (1 + 0.3 * torch.randn(D, generator=g)).cuda() if other == "fixed" else None
+    weights = dict(q_weight=w, k_weight=fixed) if only == "q" else dict(q_weight=fixed, k_weight=w)
+    outs = da.qk_norm_rotary(*xs, cos, sin, **weights, norm_eps=EPS)
+    dys = [torch.randn(o.shape, generator=g).to(torch.bfloat16).cuda() for o in outs]
+    dw, = torch.autograd.grad(outs, [w], dys)
+    want, size, n = 0, 0, 0
+    pos = torch.arange(T)[None].expand(B, T)
+    for x, dy in list(zip(xs, dys))[0 if only == "q" else 1::2]:
+        _, d, m = ref.norm_rotate_backward(d64(x), d64(w), d64(cos), d64(sin), pos, False, "rms", EPS, d64(dy))
+        want, size, n = want + d.sum(0), size + m.sum(0), n + x.shape[0] * x.shape[1] * T
+    tol = ref.U * ((2 * D + 40) * size.max() + n * size)
+    assert ((d64(dw) - want).abs() <= tol).all()
+
+
 def test_broadcast_rows_and_float16_weights():
     """A row tensor expanded over the batch (stride 0) and weights of another type."""
     g = torch.Generator().manual_seed(2)
