@@ -116,6 +116,7 @@ class DiffattnPagedDesc(ctypes.Structure):
         ("Dv", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kv_group", ctypes.c_int32),
         ("q1_stride", ctypes.c_int64 * 3), ("q2_stride", ctypes.c_int64 * 3),
         ("o_stride", ctypes.c_int64 * 3), ("mask_stride", ctypes.c_int64 * 2),
+        ("zero_rest", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 

@@ -144,7 +144,8 @@ int check_paged(const diffattn_paged_desc* d, const diffattn_pages* g) {
     const int64_t dv = d->Dv == 0 ? 2 * d->D : d->Dv;
     const int64_t group = d->kv_group > 1 ? d->kv_group : 1;
     if (d->kv_group < 0 || d->H % group != 0 || dv < 1 || dv > 256 || !nonneg(d->q1_stride) ||
-        !nonneg(d->q2_stride) || !nonneg(d->o_stride) || d->mask_stride[0] < 0 || d->mask_stride[1] < 0)
+        !nonneg(d->q2_stride) || !nonneg(d->o_stride) || d->mask_stride[0] < 0 || d->mask_stride[1] < 0 ||
+        d->zero_rest < 0 || d->zero_rest > 1 || d->reserved != 0)
         return DIFFATTN_ERR_INVALID;
     const int rc = check_pages(g);
     if (rc != DIFFATTN_OK) return rc;
@@ -446,6 +447,7 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     p.table_stride = pages->block_table_stride;
     p.lengths = lengths;
     p.q_lengths = q_lengths;
+    p.zero_rest = q_lengths && d.zero_rest;
     p.mask = tree_mask;
     p.mask_stride[0] = d.mask_stride[0];
     p.mask_stride[1] = d.mask_stride[1];

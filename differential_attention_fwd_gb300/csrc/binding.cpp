@@ -610,8 +610,8 @@ PyObject* attention(PyObject* const* a) {
     q2 = inner(q2);
     Tensor out;
     if (is_none(a[10])) {
-        // rows past a sequence's queries are left alone: they are zeros in a fresh output
-        out = q_lengths.defined() ? at::zeros({c.B, H, Tq, c.Dv}, c.k1.options()) : fresh_tensor({c.B, H, Tq, c.Dv}, type, dev);
+        out = fresh_tensor({c.B, H, Tq, c.Dv}, type, dev);
+        d.zero_rest = 1;                    // rows past a sequence's queries: left alone only in a given output
     } else {
         out = need(a[10], "out", 4, type, dev);
         if (out.size(0) != c.B || out.size(1) != H || out.size(2) != Tq || out.size(3) != c.Dv || !inner_ok(out))

@@ -389,6 +389,21 @@ paged_simt_kernel(const PagedParams p) {
 constexpr int C_WARPS = 8;
 constexpr int kJoinsPerBlock = 4;
 
+// Zeros for the rows past a sequence's queries, a warp a row.
+__device__ __forceinline__ void zero_rest(const PagedParams& p, int warp, int warps, int lane) {
+    const int64_t rows = (int64_t)p.B * p.H * p.Tq;
+    for (int64_t i = warp; i < rows; i += warps) {
+        const int64_t bh = i / p.Tq;
+        const int q = (int)(i - bh * p.Tq), b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+        if (q < paged_seq(p, b).n_new) continue;
+        const int64_t at = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2];
+        for (int c = lane; c < p.Dv; c += 32) {
+            if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at + c] = __float2bfloat16_rn(0.f);
+            else static_cast<float*>(p.out)[at + c] = 0.f;
+        }
+    }
+}
+
 // J columns a lane; VEC: J = 4 of them in a row, for a value width of 128 in bf16 (two
 // 16-byte reads a part instead of eight of 4 bytes).  AHEAD: parts read at once.  Four for
 // units of up to 16 rows, which may have many parts and leave the SMs empty (one sequence
@@ -399,6 +414,9 @@ __global__ void __launch_bounds__(C_WARPS * 32, J > 4 ? 2 : AHEAD > 2 ? 3 : 4)
 paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // before the first pass is over: it does not touch these rows
+    if (p.zero_rest)
+        zero_rest(p, (blockIdx.y * gridDim.x + blockIdx.x) * C_WARPS + warp, gridDim.x * gridDim.y * C_WARPS, lane);
     pdl_wait();
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
     const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);

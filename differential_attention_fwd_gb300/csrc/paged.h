@@ -132,6 +132,7 @@ struct PagedParams {
     int solo_workers;           // warps of the launch: one is a worker where units are many
     int workers;                // that share the first pass, at most
     int sparse_joins;           // a quarter of them may be all there are
+    int zero_rest;              // rows past a sequence's queries are zeroed
     int join_block, join_step;  // merging pass: its block b takes words b join_block + k join_step
     float* part;                // [2 * workers][chunk_rows][paged_part_floats(Dv)]
     struct PagedJoin* joins;    // [workers] what the merging pass has to do

@@ -590,7 +590,8 @@ int diffattn_paged_append(const diffattn_rotary_desc *desc, int64_t Dv,
  * Attention of new tokens over the paged cache.  Q1, Q2: [B, H, Tq, D]; O: [B, H,
  * Tq, Dv] (Dv 0 = 2 D, at most 256); H heads of queries over H / kv_group of keys
  * and values.  Tq 1 .. 1024.  Strides as in diffattn_desc.  mask_stride: element
- * strides of the tree mask along B and its rows.
+ * strides of the tree mask along B and its rows.  zero_rest: 1 = rows of O past a
+ * sequence's q_lengths are set to zero, 0 = they are left as they were.  reserved: 0.
  */
 typedef struct {
     int64_t B, H, Tq, D, Dv;
@@ -598,6 +599,8 @@ typedef struct {
     int32_t kv_group;
     int64_t q1_stride[3], q2_stride[3], o_stride[3];
     int64_t mask_stride[2];
+    int32_t zero_rest;
+    int32_t reserved;
 } diffattn_paged_desc;
 
 /* Bytes of workspace diffattn_paged_decode needs, 0 for an invalid descriptor. */
@@ -611,7 +614,7 @@ size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc *desc, const dif
  * lengths: [B] int32, tokens cached before the new ones, whose keys and values are
  * in the cache behind them (cache index lengths[b] + i).  q_lengths: [B] int32 or
  * NULL (Tq each): sequence b has q_lengths[b] new tokens; rows of O past them are
- * left as they were, and a sequence with none is not read.
+ * left as they were (or zeroed: zero_rest), and a sequence with none is not read.
  * tree_mask: NULL: new token i sees every cached token and new tokens 0 .. i.
  * Else device bytes [B, Tq, Tq] by mask_stride: new token i sees new token j where
  * the byte is not zero (and every cached token); Tq <= 64.  What a row does not see

@@ -68,7 +68,7 @@ def test_descriptor_layouts():
     assert ctypes.sizeof(R) == 5 * 8 + 4 * 4 + 4 + 4 + 8 + 2 * 8 + 2 * 8 + 8 * 3 * 8
     assert R.table_rows.offset == 5 * 8 + 6 * 4 and R.q1_grad_stride.offset == ctypes.sizeof(R) - 4 * 3 * 8
     assert ctypes.sizeof(G) == 4 * 8 + 3 * 3 * 8
-    assert ctypes.sizeof(P) == 5 * 8 + 2 * 4 + 3 * 3 * 8 + 2 * 8 and P.q1_stride.offset == 48
+    assert ctypes.sizeof(P) == 5 * 8 + 2 * 4 + 3 * 3 * 8 + 2 * 8 + 2 * 4 and P.q1_stride.offset == 48
 
 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(T=0), dict(D=0), dict(D=129), dict(dtype=2), dict(rotary_dim=65),
@@ -155,7 +155,8 @@ def decode(lib, d=None, g=None, ws=p(40), n=1 << 30, mask=None, lam=0.5, epi=Non
 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(H=0), dict(Tq=0), dict(D=0), dict(D=129), dict(Dv=257), dict(Dv=-1),
                                 dict(dtype=3), dict(kv_group=3), dict(kv_group=-1), dict(q1_stride=(-1, 0, 0)),
-                                dict(o_stride=(0, 0, -1)), dict(mask_stride=(0, -1))])
+                                dict(o_stride=(0, 0, -1)), dict(mask_stride=(0, -1)), dict(zero_rest=2), dict(zero_rest=-1),
+                                dict(reserved=1)])
 def test_decode_refusals(lib, kw):
     assert lib.diffattn_paged_workspace_bytes(ctypes.byref(paged_desc(**kw)), ctypes.byref(pages())) == 0
     assert decode(lib, paged_desc(**kw)) == INVALID
