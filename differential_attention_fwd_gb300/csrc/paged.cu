@@ -107,6 +107,7 @@ paged_simt_kernel(const PagedParams p) {
     float* st_m = reinterpret_cast<float*>(smem + L.off_stat);
     float* st_l = st_m + 2 * RC;
     float* st_a = st_l + 2 * RC;
+    pdl_wait();                     // before the merging pass may start, which writes too
     pdl_launch_dependents();
     paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(C_WARPS * 32, J > 4 ? 2 : AHEAD > 2 ? 3 : 4)
 paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
     // before the first pass is over: it does not touch these rows
     if (p.zero_rest)
         zero_rest(p, (blockIdx.y * gridDim.x + blockIdx.x) * C_WARPS + warp, gridDim.x * gridDim.y * C_WARPS, lane);
@@ -552,8 +554,7 @@ int launch_rc(const PagedParams& p, cudaStream_t stream) {
     const Layout L = simt_layout(p.D, p.Dv, sizeof(T), RC, p.k_shared != 0);
     const auto kernel = p.Dv > 128 ? paged_simt_kernel<T, RC, true> : paged_simt_kernel<T, RC, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) != cudaSuccess) return -1;
-    kernel<<<p.workers, THREADS, L.total, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return pdl_launch(kernel, dim3(p.workers), THREADS, L.total, stream, p);
 }
 
 template <typename T>
@@ -598,28 +599,17 @@ int launch_paged_combine(const PagedParams& params, cudaStream_t stream) {
     const int blocks = (p.workers + words - 1) / words;
     p.join_block = sparse ? 1 : words;
     p.join_step = sparse ? blocks : words > 1 ? 1 : p.workers;
-    cudaLaunchConfig_t cfg = {};
     // Along the rows: a block a row where all blocks fit at once (few units, which may have
     // many parts: then all of a block's warps share a row's), at least a row a warp.  One unit
     // of 24 rows in 152 parts: 74 us in all with three blocks, 25 with 24.
     const int joins = (int)(units < p.workers ? units : p.workers), fit = p.solo_workers / 2;
     const int most = p.chunk_rows, least = most <= 16 ? most : (most + paged::C_WARPS - 1) / paged::C_WARPS;
     const int rows = fit / joins < least ? least : fit / joins > most ? most : fit / joins;
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)rows);
-    cfg.blockDim = dim3(paged::C_WARPS * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const bool vec = p.Dv == 128 && p.bf16;
-    const cudaError_t e =
-        vec && p.chunk_rows > 16 ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true, 2>, p)
-        : vec                    ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, true, 4>, p)
-        : p.Dv <= 128            ? cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<4, false, 4>, p)
-                                 : cudaLaunchKernelEx(&cfg, paged::paged_combine_kernel<8, false, 2>, p);
-    return e == cudaSuccess ? 0 : -1;
+    const auto kernel = p.Dv == 128 && p.bf16 ? (most > 16 ? paged::paged_combine_kernel<4, true, 2>
+                                                           : paged::paged_combine_kernel<4, true, 4>)
+                        : p.Dv <= 128         ? paged::paged_combine_kernel<4, false, 4>
+                                              : paged::paged_combine_kernel<8, false, 2>;
+    return pdl_launch(kernel, dim3((unsigned)blocks, (unsigned)rows), paged::C_WARPS * 32, 0, stream, p);
 }
 
 int launch_paged_simt(const PagedParams& p, cudaStream_t stream) {

@@ -136,7 +136,6 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     uint64_t* empty = full + C::NST;
     volatile uint32_t* bad_stage = abort_flag + 1 + w * C::NST;
     const AbortState ab{abort_flag, p.status};
-    pdl_launch_dependents();
     if (warp < WARPS && lane < C::NST) {
         mbar_init(&full[lane], 1);
         mbar_init(&empty[lane], 1);
@@ -144,6 +143,8 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
         if (tid == 0) *abort_flag = 0;
         fence_mbar_init();
     }
+    pdl_wait();                                 // before the merging pass may start, which writes too
+    pdl_launch_dependents();
     // One warp a worker where that makes at most two workers a unit, and if the unit's rows
     // allow it.  (The barriers in here order the above.)
     const PagedScan found = paged_scan<THREADS>(p, KT, EXTRA, scan);
@@ -618,8 +619,8 @@ int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream
     const int blocks = p.workers / (p.chunk_rows <= Cfg<HD, KS>::WARP_ROWS ? WARPS : 1);
     if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    paged_mma_kernel<HD, KS><<<blocks, THREADS, smem, stream>>>(maps[0], maps[1], maps[2], p);
-    return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
+    const int rc = pdl_launch(paged_mma_kernel<HD, KS>, dim3(blocks), THREADS, smem, stream, maps[0], maps[1], maps[2], p);
+    return rc == 0 ? launch_paged_combine(p, stream) : rc;
 }
 
 }  // namespace pmma

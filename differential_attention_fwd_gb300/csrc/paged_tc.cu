@@ -192,7 +192,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     const uint32_t warp = warp_id();
     const uint32_t lane = threadIdx.x & 31;
     const AbortState ab{abort_flag, p.status};
-    pdl_launch_dependents();
     if (threadIdx.x < NUM_BARS) {
         const int i = threadIdx.x;
         int arrivals = 1;
@@ -214,6 +213,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         tmem_relinquish();
     }
     tc_fence_before();
+    pdl_wait();                                 // before the merging pass may start, which writes too
+    pdl_launch_dependents();
     paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);    // with their barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
@@ -744,8 +745,9 @@ int launch_hd(const CUtensorMap* m, const PagedParams& p, int box_rows, int q_bo
     constexpr uint32_t smem = smem_bytes<HD, KS>();
     if (cudaFuncSetAttribute(paged_tc_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return -1;
-    paged_tc_kernel<HD, KS><<<p.workers, THREADS, smem, stream>>>(m[3], m[4], m[0], m[1], m[2], p, box_rows, q_box);
-    return cudaGetLastError() == cudaSuccess ? launch_paged_combine(p, stream) : -1;
+    const int rc = pdl_launch(paged_tc_kernel<HD, KS>, dim3(p.workers), THREADS, smem, stream, m[3], m[4], m[0], m[1], m[2],
+                              p, box_rows, q_box);
+    return rc == 0 ? launch_paged_combine(p, stream) : rc;
 }
 
 }  // namespace ptc
