@@ -202,6 +202,8 @@ rotary_kernel(const RotaryParams p) {
     constexpr int V = Vec<T>::N;
     constexpr int TOKENS = THREADS / G;
     const int g = threadIdx.x % G;
+    pdl_wait();
+    pdl_launch_dependents();
     int head0;
     const int si = find_stream(p, blockIdx.y, &head0);
     const RowStream& s = p.s[si];
@@ -311,6 +313,8 @@ rotary_any_kernel(const RotaryParams p) {
     __shared__ float rows[WARPS][MAX_D];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     float* row = rows[warp];
+    pdl_wait();
+    pdl_launch_dependents();
     int head0;
     const int si = find_stream(p, blockIdx.y, &head0);      // one head a block here
     const RowStream& s = p.s[si];
@@ -690,8 +694,7 @@ int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
 #define DIFFATTN_ROTARY(GG)                                                               \
     if (G == GG) {                                                                        \
         if (backward) return launch_bwd<T, GG, INTER>(p, grid, stream);                   \
-        rotary_kernel<T, GG, INTER><<<grid, THREADS, 0, stream>>>(p);                     \
-        return cudaGetLastError() == cudaSuccess ? 0 : -1;                                \
+        return pdl_launch(rotary_kernel<T, GG, INTER>, grid, THREADS, 0, stream, p);      \
     }
     DIFFATTN_ROTARY(2)
     DIFFATTN_ROTARY(4)
@@ -711,13 +714,10 @@ int launch(const RotaryParams& p, bool backward, cudaStream_t stream) {
     constexpr int WARPS = THREADS / 32;
     const int64_t tokens = (int64_t)p.B * p.T;
     const dim3 grid((unsigned)(backward ? p.chunks : (tokens + WARPS - 1) / WARPS), (unsigned)p.head_blocks);
-    if (backward) {
-        if (p.bf16) rotary_bwd_any_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p);
-        else rotary_bwd_any_kernel<float><<<grid, THREADS, 0, stream>>>(p);
-    } else {
-        if (p.bf16) rotary_any_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p);
-        else rotary_any_kernel<float><<<grid, THREADS, 0, stream>>>(p);
-    }
+    if (!backward)
+        return pdl_launch(p.bf16 ? rotary_any_kernel<__nv_bfloat16> : rotary_any_kernel<float>, grid, THREADS, 0, stream, p);
+    if (p.bf16) rotary_bwd_any_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p);
+    else rotary_bwd_any_kernel<float><<<grid, THREADS, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
@@ -778,16 +778,7 @@ int launch_rotary_bwd(const RotaryParams& p, cudaStream_t stream) {
     for (int i = 0; i < p.n; ++i) heads[p.s[i].grad_slot] = p.s[i].heads;
     const int q_rows = !p.dw[0] ? 0 : p.dw_stride[0] ? heads[0] : 1;
     const int k_rows = !p.dw[1] ? 0 : p.dw_stride[1] ? heads[1] : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(q_rows + k_rows));
-    cfg.blockDim = dim3(rot::RED_THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rot::rotary_dw_kernel, p, q_rows) == cudaSuccess ? 0 : -1;
+    return pdl_launch(rot::rotary_dw_kernel, dim3((unsigned)(q_rows + k_rows)), rot::RED_THREADS, 0, stream, p, q_rows);
 }
 
 }  // namespace diffattn

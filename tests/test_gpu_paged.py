@@ -358,6 +358,58 @@ def test_graph_replay_follows_the_lengths(head, Tq):
         assert torch.equal(outs[0], want) and torch.equal(outs[1], want), new
 
 
+def test_captured_with_forks_and_copies():
+    """A step captured between other streams' work, copies and fills: kernels that may start
+    early wait for what comes before them, whatever it is."""
+    g = torch.Generator().manual_seed(21)
+    B, H, Hk, D, page, n = 3, 4, 2, 64, 16, 40
+    cos, sin = da.rotary_tables(128, D, device="cuda")
+    table = torch.randperm(B * 4, generator=g).reshape(B, 4).int().cuda()
+    k_pages, v_pages = (torch.zeros(B * 4, Hk, page, w, dtype=torch.bfloat16, device="cuda") for w in (D, 2 * D))
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q_src, k_src, v_src = (torch.zeros(B, h, n, w, dtype=torch.bfloat16, device="cuda") for h, w in ((H, D), (Hk, D), (Hk, 2 * D)))
+    q, k, v = (torch.zeros_like(t) for t in (q_src, k_src, v_src))
+    out = torch.zeros(B, H, n, 2 * D, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            k.copy_(k_src)
+            v.copy_(v_src)
+        q.copy_(q_src)
+        lens.zero_()
+        a, _, b, _ = da.qk_norm_rotary(q, None, q * 2, None, cos, sin)
+        main.wait_stream(side)
+        da.paged_cache_append(k, None, v, k_pages, None, v_pages, table, lens, None, cos, sin, norm="rms")
+        o = da.differential_attention_paged(a, k_pages, b, None, v_pages, table, lens, 0.5)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            out.copy_(o)
+        tree = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+        t = da.differential_attention_tree(a, k_pages, b, None, v_pages, table, lens, tree, 0.5)
+        main.wait_stream(side)
+        return t
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tree_out = step()
+    for i in range(3):
+        for t in (q_src, k_src, v_src):
+            t.copy_(torch.randn(t.shape, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, got_tree = out.clone(), tree_out.clone()
+        r = da.qk_norm_rotary(q_src, k_src, q_src * 2, k_src, cos, sin)
+        want = da.differential_attention(*r, v_src, 0.5)
+        # both within their roundings of the exact result: weights' and outputs' of the dense one
+        assert (got.float() - want.float()).abs().max() <= 4 * 2.0 ** -8 * 6
+        assert torch.equal(got, got_tree)
+
+
 def test_results_do_not_depend_on_the_run():
     pb = Problem("bf16", 64, 128, False, 4, 2, 6, [3000, 10, 700], 16)
     a = pb.run()
