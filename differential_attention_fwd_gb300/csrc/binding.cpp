@@ -3,7 +3,7 @@
 //
 // A decode step makes these calls for every layer, with kernels of a few microseconds, so
 // the host's time a call is what a user sees.  Checking a dozen tensors and packing a
-// descriptor from Python took 35 to 60 us on the CPU beside a GB300; this takes 6 to 15.
+// descriptor from Python took 35 to 60 us on the CPU beside a GB300; this takes 4 to 12.
 // The gradient of the norm and rotation is an autograd node in C++ for the same reason.
 //
 // Every function takes its arguments by position, as _paged.py passes them.

@@ -13,7 +13,7 @@
 // sums leave out: a hidden key's value may hold anything.
 //
 // Bound, where it is used (float32 caches and other widths of small models), by latency: 4
-// sequences of up to 2900 keys, 3 tokens, 4 key/value heads, D = 32 take 21.9 us.  Of those
+// sequences of up to 2900 keys, 3 tokens, 4 key/value heads, D = 32 take 22.2 us.  Of those
 // 1.6 go to the lengths and the division, 2.8 to the first queries, 2 to a page and its keys,
 // 2.5 to each of two tiles, 1.3 to the block's sums, and 6 to the merging pass; HBM would
 // take 2.3.  At length by shared memory and the exchanges of the softmax: 9 tokens, 16

@@ -19,10 +19,12 @@
 // table row (4 R bytes) is as large as a bf16 head row: read for each head from L2 it
 // would be as much traffic as x itself.
 //
-// Measured: 2 x 8192 tokens of 64 heads of 64 in bf16 take 52.3 us (5.2 TB/s, 0.77 of the
+// Measured: 2 x 8192 tokens of 64 heads of 64 in bf16 take 51.5 us (5.3 TB/s, 0.78 of the
 // copy rate; half of an SM's issue slots are arithmetic and conversions, see Vec); a decode
-// step of 16 tokens 3 us and an append of as many 3.2, a launch's latency; 4 x 2047 tokens
-// appended with 8 heads of 128 16.2 us (3.6 TB/s: a fifth of it is the start of the grid).
+// step of 16 tokens 2.8 us and an append of as many 2.9, a launch's latency; 4 x 2047 tokens
+// appended with 8 heads of 128 15.5 us (3.7 TB/s: a fourth of it is the grid's start and
+// end).  The kernels start while the stream's last one ends and wait for it before they
+// read (calls among others: 18.5 to 16.0 us for that append).
 #include "paged.h"
 #include "ptx.cuh"
 #include "pdl.cuh"
