@@ -444,8 +444,8 @@ def test_decode_step_as_used():
             o = da.differential_attention_tree(a, caches[0], b, caches[1], caches[2], table, lens, chain, 0.6)
         else:
             o = da.differential_attention_paged(a, caches[0], b, caches[1], caches[2], table, lens, 0.6)
-        # both round their weights and outputs to bf16 once: twice 2^-8 of |A| |V| (at most
-        # 1.6 max|v| = 8) and of the output
+        # the dense one rounds its weights to bf16 once, both their outputs: 2^-8 of |A| |V|
+        # (at most 1.6 max|v| = 8) and twice of the output
         assert ((o.float() - want[:, :, new].float()).abs() <= 4 * 2.0 ** -8 * 8).all()
         assert (o.float() - want[:, :, new].float()).abs().mean() <= 2.0 ** -8
         lens += step
