@@ -119,7 +119,8 @@ __device__ __forceinline__ uint32_t slice_mask(const PagedParams& p, const Paged
     return m & (n >= SLICE ? 0xffffu : (1u << n) - 1);
 }
 
-template <int HD, bool KS>
+// HR: 1 for units of up to 8 rows, whose threads have no second row, else 2.
+template <int HD, bool KS, int HR>
 __global__ void __launch_bounds__(THREADS, 2)
 paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -282,11 +283,14 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             tb = __shfl_sync(0xffffffffu, bits, r0 + 8);
         }
         float o[2][DV / 8][4];
-        float m[2][2], l[2][2];
+        float m[2][HR], l[2][HR];
 #pragma unroll
         for (int br = 0; br < 2; ++br) {
-            m[br][0] = m[br][1] = -INFINITY;
-            l[br][0] = l[br][1] = 0.f;
+#pragma unroll
+            for (int h = 0; h < HR; ++h) {
+                m[br][h] = -INFINITY;
+                l[br][h] = 0.f;
+            }
 #pragma unroll
             for (int n = 0; n < DV / 8; ++n) o[br][n][0] = o[br][n][1] = o[br][n][2] = o[br][n][3] = 0.f;
         }
@@ -323,14 +327,14 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     seen[0] = slice_mask(p, s, k0, la, ra.q, ta);
                     seen[1] = slice_mask(p, s, k0, lb, rb.q, tb);
                 }
-                float pr[2][2][4];
+                float pr[2][2][2 * HR];
                 bool big = false;
 #pragma unroll
                 for (int br = 0; br < 2; ++br)
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 2 * HR; ++e) {
                             const bool vis = seen[e >> 1] >> (8 * n + 2 * (lane & 3) + (e & 1)) & 1u;
                             const float x = vis ? sc[br][n][e] * sl2 : -INFINITY;
                             sc[br][n][e] = x;
@@ -341,7 +345,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 #pragma unroll
                     for (int br = 0; br < 2; ++br)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < HR; ++h) {
                             float x = fmaxf(fmaxf(sc[br][0][2 * h], sc[br][0][2 * h + 1]),
                                             fmaxf(sc[br][1][2 * h], sc[br][1][2 * h + 1]));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -365,10 +369,15 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                 uint32_t pa[2][4], pb[2][4];
 #pragma unroll
                 for (int br = 0; br < 2; ++br) {
-                    l[br][0] += (pr[br][0][0] + pr[br][0][1]) + (pr[br][1][0] + pr[br][1][1]);
-                    l[br][1] += (pr[br][0][2] + pr[br][0][3]) + (pr[br][1][2] + pr[br][1][3]);
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+                        l[br][h] += (pr[br][0][2 * h] + pr[br][0][2 * h + 1]) + (pr[br][1][2 * h] + pr[br][1][2 * h + 1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        if ((i & 1) >= HR) {            // the rows that there are not
+                            pa[br][i] = pb[br][i] = 0;
+                            continue;
+                        }
                         const float a = pr[br][i >> 1][2 * (i & 1)], b = pr[br][i >> 1][2 * (i & 1) + 1];
                         pa[br][i] = pack_bf16x2(a, b);
                         pb[br][i] = pack_bf16x2(a - __uint_as_float(pa[br][i] << 16),    // what the rounding left
@@ -396,11 +405,11 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                             const int fk = 2 * j + (from >> 4);             // key, and first column
                             const int fc = (from & 15) * 8;
                             const int src = (lane & ~3) | ((fk & 7) >> 1);
-                            float pk[2][2];
+                            float pk[2][HR];
 #pragma unroll
                             for (int br = 0; br < 2; ++br)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
+                                for (int h = 0; h < HR; ++h) {
                                     const float x0 = (fk & 1) ? pr[br][0][2 * h + 1] : pr[br][0][2 * h];
                                     const float x1 = (fk & 1) ? pr[br][1][2 * h + 1] : pr[br][1][2 * h];
                                     pk[br][h] = __shfl_sync(0xffffffffu, fk >= 8 ? x1 : x0, src);
@@ -412,7 +421,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                             for (int n = 0; n < DV / 8; ++n)
                                 if (n == fc / 8)
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
+                                    for (int e = 0; e < 2 * HR; ++e)
                                         if (!isfinite(vv[e & 1]) && (seen[e >> 1] >> fk & 1u)) {
                                             o[0][n][e] = fmaf(pk[0][e >> 1], vv[e & 1], o[0][n][e]);
                                             o[1][n][e] = fmaf(pk[1][e >> 1], vv[e & 1], o[1][n][e]);
@@ -454,7 +463,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 #pragma unroll
         for (int br = 0; br < 2; ++br)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < HR; ++h) {
                 l[br][h] += __shfl_xor_sync(0xffffffffu, l[br][h], 1);
                 l[br][h] += __shfl_xor_sync(0xffffffffu, l[br][h], 2);
                 if (bad || !ok) l[br][h] = __int_as_float(0x7fc00000);
@@ -466,7 +475,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
 #pragma unroll
             for (int br = 0; br < 2; ++br)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < HR; ++h)
                     if ((lane & 3) == 0) {
                         stat[(w * 2 + 0) * 2 * NR + br * NR + r0 + 8 * h] = m[br][h];
                         stat[(w * 2 + 1) * 2 * NR + br * NR + r0 + 8 * h] = l[br][h];
@@ -477,7 +486,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             const float* bufs = reinterpret_cast<const float*>(smem_block + st * C::STAGE);
             for (int row0 = 0; row0 < p.chunk_rows; row0 += C::ROUND) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < HR; ++h) {
                     const int r = r0 + 8 * h - row0;
                     if (live == 0 || r < 0 || r >= C::ROUND || !(h ? lb : la)) continue;
                     float* dst = buf + r * 2 * DV + 2 * (lane & 3);
@@ -612,15 +621,20 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     }
 }
 
-template <int HD, bool KS>
-int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
+template <int HD, bool KS, int HR>
+int launch_rows(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
     constexpr int smem = Cfg<HD, KS>::SMEM;
     // workers are warps where one warp may be one
     const int blocks = p.workers / (p.chunk_rows <= Cfg<HD, KS>::WARP_ROWS ? WARPS : 1);
-    if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS, HR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    const int rc = pdl_launch(paged_mma_kernel<HD, KS>, dim3(blocks), THREADS, smem, stream, maps[0], maps[1], maps[2], p);
+    const int rc = pdl_launch(paged_mma_kernel<HD, KS, HR>, dim3(blocks), THREADS, smem, stream, maps[0], maps[1], maps[2], p);
     return rc == 0 ? launch_paged_combine(p, stream) : rc;
+}
+
+template <int HD, bool KS>
+int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
+    return p.chunk_rows <= 8 ? launch_rows<HD, KS, 1>(maps, p, stream) : launch_rows<HD, KS, 2>(maps, p, stream);
 }
 
 }  // namespace pmma
