@@ -18,7 +18,7 @@
 //     rows from its registers at a unit's end.  With few, four warps share a worker's
 //     tiles of 64 keys and merge their results in shared memory at its end, so that the
 //     merging pass has a quarter of the parts.  (2048 units of 100 keys: 78 us with four
-//     warps a worker, whose merge takes 2 us a unit, 51 with one, 39 with what followed.
+//     warps a worker, whose merge takes 2 us a unit, 51 with one, 36 with what followed.
 //     16 units of 16384: 33 us with four, 42 with one, the difference in the merging pass.)
 //   - The products are warp-level (m16n8k16): at this size they are a quarter of the
 //     time that the tile's bytes take, and P goes from the score's accumulators to the
@@ -33,9 +33,11 @@
 // costs nothing here, since the tile's bytes take longer (5 % at 4 rows of head width 128).
 //
 // Measured, both launches: 16 sequences of up to 8192 keys, 16 heads, D = 64, 710 MB of
-// cache: 124 us, 0.84 of the copy rate; 4 of 65536, 8 key/value heads, shared keys, D = 128:
-// 122 us, 0.86; one of 517: 13.4 us, the latency of the two launches, the lengths, a page
-// and its keys in turn.
+// cache: 122 us, 0.86 of the copy rate; 4 of 65536, 8 key/value heads, shared keys, D = 128:
+// 118 us, 0.89; one of 517: 12.7 us, the latency of the two launches, the lengths, a page
+// and its keys in turn.  A warp is busy with a slice of 16 keys for 2,500 cycles of the
+// 3,000 that HBM allows it, which is what is left of mid-length calls (64 x 1000, 16 heads:
+// 78 us of 49): the next step is the products' other order, keys as their 16 rows.
 #include "paged_plan.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -363,25 +365,37 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                             for (int n = 0; n < DV / 8; ++n) {
                                 o[br][n][2 * h] *= a;
                                 o[br][n][2 * h + 1] *= a;
+                                if (HR == 1) {          // second parts
+                                    o[br][n][2] *= a;
+                                    o[br][n][3] *= a;
+                                }
                             }
                         }
                 }
+                // The weights' two parts.  A warp alone has up to 8 rows, and its second parts go
+                // into the product's other 8: half of the products (2048 units of 100 keys: 37.5
+                // to 36 us; 1024 of 1000: 80.6 to 78.3).  Four warps together have the time, and
+                // are better off with a steady pace: SMs that wait for nothing but HBM take it
+                // from one another (V2 head, 4 x 65536: 118 us, 124 with half of the products).
                 uint32_t pa[2][4], pb[2][4];
 #pragma unroll
                 for (int br = 0; br < 2; ++br) {
 #pragma unroll
-                    for (int h = 0; h < HR; ++h)
+                    for (int h = 0; h < HR; ++h) {
                         l[br][h] += (pr[br][0][2 * h] + pr[br][0][2 * h + 1]) + (pr[br][1][2 * h] + pr[br][1][2 * h + 1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if ((i & 1) >= HR) {            // the rows that there are not
-                            pa[br][i] = pb[br][i] = 0;
-                            continue;
+                        for (int n = 0; n < 2; ++n) {
+                            const float a = pr[br][n][2 * h], b = pr[br][n][2 * h + 1];
+                            const uint32_t hi = pack_bf16x2(a, b);
+                            const uint32_t lo = pack_bf16x2(a - __uint_as_float(hi << 16),      // what the rounding left
+                                                            b - __uint_as_float(hi & 0xffff0000u));
+                            pa[br][2 * n + h] = hi;
+                            pb[br][2 * n + h] = lo;
+                            if (HR == 1) {
+                                pa[br][2 * n + 1] = solo ? lo : 0;
+                                pb[br][2 * n + 1] = 0;
+                            }
                         }
-                        const float a = pr[br][i >> 1][2 * (i & 1)], b = pr[br][i >> 1][2 * (i & 1) + 1];
-                        pa[br][i] = pack_bf16x2(a, b);
-                        pb[br][i] = pack_bf16x2(a - __uint_as_float(pa[br][i] << 16),    // what the rounding left
-                                                b - __uint_as_float(pa[br][i] & 0xffff0000u));
                     }
                 }
                 if (edge) {
@@ -449,8 +463,10 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                     for (int br = 0; br < 2; ++br) {
                         mma16816(o[br][2 * n], pa[br], vf[0], vf[1]);
                         mma16816(o[br][2 * n + 1], pa[br], vf[2], vf[3]);
-                        mma16816(o[br][2 * n], pb[br], vf[0], vf[1]);
-                        mma16816(o[br][2 * n + 1], pb[br], vf[2], vf[3]);
+                        if (HR == 2 || !solo) {
+                            mma16816(o[br][2 * n], pb[br], vf[0], vf[1]);
+                            mma16816(o[br][2 * n + 1], pb[br], vf[2], vf[3]);
+                        }
                     }
                 }
             }
@@ -459,6 +475,15 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                 if (lane == 0) mbar_arrive(&empty[st]);
                 if (++st == C::NST) { st = 0; ph ^= 1; }
             }
+        }
+        if (HR == 1 && solo) {
+#pragma unroll
+            for (int br = 0; br < 2; ++br)
+#pragma unroll
+                for (int n = 0; n < DV / 8; ++n) {
+                    o[br][n][0] += o[br][n][2];
+                    o[br][n][1] += o[br][n][3];
+                }
         }
 #pragma unroll
         for (int br = 0; br < 2; ++br)
