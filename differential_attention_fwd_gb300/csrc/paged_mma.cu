@@ -20,11 +20,10 @@
 //     merging pass has a quarter of the parts.  (2048 units of 100 keys: 78 us with four
 //     warps a worker, whose merge takes 2 us a unit, 51 with one, 36 with what followed.
 //     16 units of 16384: 33 us with four, 42 with one, the difference in the merging pass.)
-//   - The products are warp-level (m16n8k16): at this size they are a quarter of the
-//     time that the tile's bytes take, and P goes from the score's accumulators to the
-//     next product's operand in registers.  A tcgen05 product would want 128 keys as its
-//     M and P through shared memory with two block-wide barriers a tile (the layout of
-//     the dense decode, 0.83 of the copy rate).
+//   - The products are warp-level (m16n8k16): P goes from the score's accumulators to the
+//     next product's operand in registers, and no warp waits for another.  A tcgen05
+//     product would want 128 keys as its M and P through shared memory with two block-wide
+//     barriers a tile (the layout of the dense decode, 0.83 of the copy rate).
 //
 // Weights are 2^(s - m) against a running maximum that moves only when some weight would
 // pass 2^8.  They go to the product with V as two bf16 parts, the rounded weight and what
