@@ -22,7 +22,9 @@ bool dtype_ok(int32_t d) { return d == DIFFATTN_BF16 || d == DIFFATTN_F32; }
 
 // The checks of a rotary descriptor that need no tensors.
 int check_rotary(const diffattn_rotary_desc* d, const float* cos, const float* sin, bool tables) {
-    if (!d || d->B < 1 || d->T < 1 || d->D < 1 || d->D > 128 || !dtype_ok(d->dtype)) return DIFFATTN_ERR_INVALID;
+    // H and Hk count where their tensors are left out too: the backward's workspace goes by both
+    if (!d || d->B < 1 || d->T < 1 || d->D < 1 || d->D > 128 || d->H < 0 || d->Hk < 0 || !dtype_ok(d->dtype))
+        return DIFFATTN_ERR_INVALID;
     if (d->rotary_dim < 0 || d->rotary_dim > d->D || d->rotary_dim % 2 != 0) return DIFFATTN_ERR_INVALID;
     if (d->norm != DIFFATTN_NORM_NONE && d->norm != DIFFATTN_NORM_RMS) return DIFFATTN_ERR_INVALID;
     if (d->norm != DIFFATTN_NORM_NONE && !(std::isfinite(d->eps) && d->eps > 0.f)) return DIFFATTN_ERR_INVALID;
@@ -35,7 +37,7 @@ int check_rotary(const diffattn_rotary_desc* d, const float* cos, const float* s
     constexpr int64_t kMaxTokens = 1 << 30;
     if (d->B > kMaxTokens || d->T > kMaxTokens || d->B * d->T > kMaxTokens) return DIFFATTN_ERR_UNSUPPORTED;
     // rows of the backward's kernels are counted in 31 bits
-    if (d->H >= 0 && d->Hk >= 0 && 2.0 * (d->B * d->T / 16 + 16) * (double)(d->H + d->Hk) > INT32_MAX)
+    if (2.0 * (d->B * d->T / 16 + 16) * ((double)d->H + (double)d->Hk) > INT32_MAX)
         return DIFFATTN_ERR_UNSUPPORTED;
     return DIFFATTN_OK;
 }
@@ -273,8 +275,8 @@ int diffattn_rotary(const diffattn_rotary_desc* desc, const void* q1, const void
 }
 
 size_t diffattn_rotary_bwd_workspace_bytes(const diffattn_rotary_desc* desc) {
-    if (check_rotary(desc, nullptr, nullptr, false) != DIFFATTN_OK || desc->H < 0 || desc->Hk < 0 ||
-        desc->H > kMaxHeads || desc->Hk > kMaxHeads)
+    if (check_rotary(desc, nullptr, nullptr, false) != DIFFATTN_OK || desc->H > kMaxHeads ||
+        desc->Hk > kMaxHeads)
         return 0;
     return rotary_bwd_bytes(desc);
 }

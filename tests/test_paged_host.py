@@ -113,6 +113,20 @@ def test_rotary_backward_refusals(lib):
     assert bwd(rotary_desc(), x=(1, 0, 1, 0), dys=(1, 0, 1, 0), dkw=p(31)) == INVALID
 
 
+@pytest.mark.parametrize("kw", [dict(H=-2), dict(Hk=-2), dict(H=-1, Hk=-1), dict(H=-(1 << 40))])
+def test_rotary_negative_head_counts(lib, kw):
+    """A negative count is refused where its tensors are left out too: the backward's workspace goes
+    by both.  (A workspace of one byte, so that no call can get as far as a GPU.)"""
+    for T in (5, 1 << 20):
+        d = rotary_desc(B=1, T=T, **kw)
+        for x in ((0, 1, 0, 0), (0, 1, 0, 1), (1, 0, 1, 0)):
+            assert rotary(lib, d, x=x, y=x) == INVALID, (kw, T, x)
+            xs, ys, gs = ([p(j + i) if g else None for i, g in enumerate(x)] for j in (0, 4, 8))
+            assert lib.diffattn_rotary_bwd(ctypes.byref(d), *xs, None, None, p(20), p(21), None, *gs, *ys, None, None,
+                                           p(40), 1, None) == INVALID
+        assert lib.diffattn_rotary_bwd_workspace_bytes(ctypes.byref(d)) == 0
+
+
 def test_append_refusals(lib):
     def append(d=None, Dv=128, vs=(0, 0, 0), g=None, k2=p(1), k2c=p(6), **miss):
         a = dict(k1=p(0), v=p(2), lens=p(3), table=p(4), k1c=p(5), vc=p(7), kw=None)
