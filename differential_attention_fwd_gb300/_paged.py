@@ -63,7 +63,8 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
     [B, T]; None: 0 .. T-1.  A position outside the tables gives a row of NaN and is
     reported by get_device_error.
     norm: "rms" or None; q_weight and k_weight: [D] (for every head) or [heads, D],
-    None = 1.  Arithmetic in float32, one rounding at the end.
+    None = 1; one whose rows are left out is not used and gets no gradient.
+    Arithmetic in float32, one rounding at the end.
 
     Returns (q1, k1, q2, k2), contiguous, None where None was given.  Differentiable
     in the rows and the weights.  (A backward pass captured into a CUDA graph must not

@@ -137,15 +137,19 @@ Tensor plain_f32(const Tensor& t) {
     return t.to(at::kFloat).contiguous();
 }
 
-// A norm weight [D] or [heads, D]: float32 and dense, and its head stride.
+// A norm weight [D] or [heads, D]: float32 and dense, and its head stride.  With no rows of its
+// kind (heads = 0) it is looked at and left out: nothing reads it, and it has no gradient.
 Tensor norm_weight(PyObject* o, const char* name, int64_t heads, int64_t D, at::Device dev, Tensor* given, int64_t* stride) {
     *stride = 0;
     if (is_none(o)) return {};
     const Tensor& w = tensor(o, name);
-    if (w.device() != dev || !((w.dim() == 1 && w.size(0) == D) || (w.dim() == 2 && w.size(0) == heads && w.size(1) == D)))
-        bad_value(std::string(name) + " must be [D] = (" + std::to_string(D) + ",) or [heads, D] = (" + std::to_string(heads) +
-                  ", " + std::to_string(D) + ") on the inputs' device, got " + text(w.sizes()));
+    if (w.device() != dev ||
+        !((w.dim() == 1 && w.size(0) == D) || (w.dim() == 2 && (w.size(0) == heads || heads == 0) && w.size(1) == D)))
+        bad_value(std::string(name) + " must be [D] = (" + std::to_string(D) + ",) or [heads, D] = (" +
+                  (heads ? std::to_string(heads) : "heads") + ", " + std::to_string(D) + ") on the inputs' device, got " +
+                  text(w.sizes()));
     if (!at::isFloatingType(w.scalar_type())) bad_value(std::string(name) + " must be a floating tensor");
+    if (heads == 0) return {};
     *stride = w.dim() == 2 ? D : 0;
     *given = w;
     return plain_f32(w);

@@ -1,0 +1,71 @@
+"""GPU tests of calls of qk_norm_rotary and paged_cache_append that their signatures allow
+beside the ordinary ones: what is refused, what is left out, what autograd keeps."""
+import pytest
+import torch
+
+import differential_attention_fwd_gb300 as da
+from differential_attention_fwd_gb300 import build as build_mod
+from tests import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build_mod.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    da.get_device_error()
+    yield
+    assert da.get_device_error() == 0
+
+
+def rows(g, B, H, T, D, dtype=torch.float32):
+    return torch.randn(B, T, H, D, generator=g).to(dtype).cuda().transpose(1, 2)
+
+
+def d64(t):
+    return t.detach().cpu().double()
+
+
+@pytest.mark.parametrize("D", [64, 48])
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("side", ["q", "k"])
+def test_a_weight_whose_rows_are_left_out(D, per_head, side):
+    """Both weights trainable, rows of one kind alone: the other weight is not used, as in a
+    formula that does not name it, and the used one's gradient is the formula's."""
+    g = torch.Generator().manual_seed(D)
+    B, T, H, Hk = 2, 7, 3, 2
+    n = H if side == "q" else Hk
+    xs = [rows(g, B, n, T, D) for _ in range(2)]
+    used = (1 + 0.3 * torch.randn(*((n, D) if per_head else (D,)), generator=g)).cuda().requires_grad_()
+    other = torch.ones(*((5, D) if per_head else (D,)), device="cuda", requires_grad=True)
+    cos, sin = da.rotary_tables(T, D, device="cuda")
+    args = (xs[0], None, xs[1], None) if side == "q" else (None, xs[0], None, xs[1])
+    weights = dict(q_weight=used, k_weight=other) if side == "q" else dict(q_weight=other, k_weight=used)
+    out = [y for y in da.qk_norm_rotary(*args, cos, sin, norm_eps=EPS, **weights) if y is not None]
+    dys = [torch.randn(y.shape, generator=g).cuda() for y in out]
+    got, none = torch.autograd.grad(out, [used, other], dys, retain_graph=True, allow_unused=True)
+    assert none is None
+    torch.autograd.backward(out, dys)
+    assert other.grad is None and torch.equal(used.grad, got)
+    pos = torch.arange(T)[None].expand(B, T)
+    want = size = 0
+    for x, dy in zip(xs, dys):
+        _, dw, s = ref.norm_rotate_backward(d64(x), d64(used), d64(cos), d64(sin), pos, False, "rms", EPS, d64(dy))
+        want, size = want + (dw if per_head else dw.sum(0)), size + (s if per_head else s.sum(0))
+    # a term is off by (D/2 + 10) u of twice its size at most, a sum of N terms by N u
+    terms = 2 * B * T * (1 if per_head else n)
+    assert ((d64(got) - want).abs() <= ref.U * ((2 * D + 40) * size.amax(-1, keepdim=True) + terms * size)).all()
+    # a weight that is not used asks for no graph
+    alone = dict(q_weight=used.detach(), k_weight=other) if side == "q" else dict(q_weight=other, k_weight=used.detach())
+    assert not any(y.requires_grad for y in da.qk_norm_rotary(*args, cos, sin, **alone) if y is not None)
+    # and is looked at all the same
+    bad = "k_weight" if side == "q" else "q_weight"
+    for w in (torch.ones(D + 1, device="cuda"), torch.ones(2, D + 1, device="cuda"), torch.ones(D)):
+        with pytest.raises(ValueError, match=bad):
+            da.qk_norm_rotary(*args, cos, sin, **{bad: w})
