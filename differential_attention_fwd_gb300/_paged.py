@@ -67,7 +67,8 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
     Arithmetic in float32, one rounding at the end.
 
     Returns (q1, k1, q2, k2), contiguous, None where None was given.  Differentiable
-    in the rows and the weights.  (A backward pass captured into a CUDA graph must not
+    in the rows and the weights, backward and once; dual tensors of forward-mode
+    differentiation are refused, here and in the calls below.  (A backward pass captured into a CUDA graph must not
     add to leaves that an eager graph on the default stream still holds: torch would join
     that stream to the capture, so this is an error.  torch.autograd.grad is free of it.)
     """

@@ -18,6 +18,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -128,6 +129,14 @@ Tensor fresh_tensor(at::IntArrayRef sizes, at::ScalarType type, at::Device dev) 
 
 diffattn_stream_t stream_of(at::Device dev) {
     return reinterpret_cast<diffattn_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+}
+
+// Refuses dual tensors: nothing here has a forward-mode derivative, and a result without a
+// tangent would be taken for a constant.
+void no_tangent(std::initializer_list<const Tensor*> ts, const char* what) {
+    if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+    for (const Tensor* t : ts)
+        if (t->defined() && t->_fw_grad(0).defined()) bad_value(std::string(what) + " has no forward-mode derivative");
 }
 
 // float32 and dense.
@@ -380,6 +389,7 @@ PyObject* rotary(PyObject* const* a) {
     r.qw = norm_weight(a[9], "q_weight", r.H, r.D, dev, &r.qw_given, &r.qws);
     r.kw = norm_weight(a[10], "k_weight", r.Hk, r.D, dev, &r.kw_given, &r.kws);
     r.interleaved = PyObject_IsTrue(a[11]) == 1;
+    no_tangent({&in[0], &in[1], &in[2], &in[3], &r.cos, &r.sin, &r.qw_given, &r.kw_given}, "qk_norm_rotary");
     const c10::cuda::OptionalCUDAGuard guard(dev);
     bool grad = false;
     if (at::GradMode::is_enabled()) {
@@ -529,6 +539,7 @@ PyObject* append(PyObject* const* a) {
     if (!r.norm && !is_none(a[14])) bad_value("k_weight needs norm='rms'");
     r.kw = norm_weight(a[14], "k_weight", r.Hk, r.D, dev, &r.kw_given, &r.kws);
     r.interleaved = PyObject_IsTrue(a[15]) == 1;
+    no_tangent({&k[0], &k[1], &v, &c.k1, &c.k2, &c.v, &r.cos, &r.sin, &r.kw_given}, "paged_cache_append");
     if (wants_grad({&k[0], &k[1], &v, &c.k1, &c.k2, &c.v, &r.kw_given}))
         bad_value("paged_cache_append is forward only: call it under torch.no_grad() or detach its inputs");
     const c10::cuda::OptionalCUDAGuard guard(dev);
@@ -554,6 +565,8 @@ PyObject* append(PyObject* const* a) {
           "diffattn_paged_append");
     Py_RETURN_NONE;
 }
+
+const char* const kAttention = "attention over a paged cache";
 
 PyObject* attention(PyObject* const* a) {
     // q1, k1_cache, q2, k2_cache, v_cache, block_table, lengths, q_lengths, tree_mask, coefficient, out, norm, norm_eps,
@@ -598,6 +611,7 @@ PyObject* attention(PyObject* const* a) {
     if (THPVariable_Check(a[9])) {
         const Tensor& t = THPVariable_Unpack(a[9]);
         if (t.numel() != 1) bad_value("coefficient must be a scalar");
+        no_tangent({&t}, kAttention);
         if (wants_grad({&t})) bad_value("attention over a paged cache is forward only: detach the coefficient");
         if (t.is_cuda()) {
             if (t.device() != dev) bad_value("coefficient tensor must be on the inputs' device");
@@ -608,6 +622,7 @@ PyObject* attention(PyObject* const* a) {
     } else {
         lam = (float)number(a[9], "coefficient");
     }
+    no_tangent({&q1, &q2, &c.k1, &c.k2, &c.v}, kAttention);
     if (wants_grad({&q1, &q2, &c.k1, &c.k2, &c.v}))
         bad_value("attention over a paged cache is forward only: call it under torch.no_grad() or detach its inputs");
     q1 = inner(q1);
@@ -620,6 +635,7 @@ PyObject* attention(PyObject* const* a) {
         out = need(a[10], "out", 4, type, dev);
         if (out.size(0) != c.B || out.size(1) != H || out.size(2) != Tq || out.size(3) != c.Dv || !inner_ok(out))
             bad_value("out must be [B, H, Tq, Dv] with a contiguous innermost dimension");
+        no_tangent({&out}, kAttention);
         if (wants_grad({&out})) bad_value("out takes no gradient");
         out.unsafeGetTensorImpl()->bump_version();
     }
@@ -638,6 +654,7 @@ PyObject* attention(PyObject* const* a) {
         if (t.device() != dev || !((t.dim() == 2 && t.size(0) == H && t.size(1) == c.Dv) || (t.dim() == 1 && t.size(0) == H * c.Dv)))
             bad_value(std::string(name) + " must be [H, Dv] = (" + std::to_string(H) + ", " + std::to_string(c.Dv) +
                       ") on the inputs' device");
+        no_tangent({&t}, kAttention);
         if (wants_grad({&t})) bad_value("attention over a paged cache is forward only: detach the norm's weights");
         affine[i] = plain_f32(t);
     }

@@ -69,3 +69,44 @@ def test_a_weight_whose_rows_are_left_out(D, per_head, side):
     for w in (torch.ones(D + 1, device="cuda"), torch.ones(2, D + 1, device="cuda"), torch.ones(D)):
         with pytest.raises(ValueError, match=bad):
             da.qk_norm_rotary(*args, cos, sin, **{bad: w})
+
+
+def test_dual_tensors_are_refused():
+    """Forward-mode differentiation: a result without a tangent would be a derivative of zero."""
+    import torch.autograd.forward_ad as fwad
+    g = torch.Generator().manual_seed(1)
+    B, H, T, D, page = 2, 2, 3, 64, 16
+    q, k = rows(g, B, H, T, D, torch.bfloat16), rows(g, B, H, T, D, torch.bfloat16)
+    v = rows(g, B, H, T, 2 * D, torch.bfloat16)
+    w = torch.ones(D, device="cuda")
+    cos, sin = da.rotary_tables(page, D, device="cuda")
+    kc, vc = (torch.zeros(B, H, page, n, dtype=torch.bfloat16, device="cuda") for n in (D, 2 * D))
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    nw = torch.ones(H, 2 * D, device="cuda")
+    lam = torch.tensor(0.5, device="cuda")
+    out = torch.empty(B, H, T, 2 * D, dtype=torch.bfloat16, device="cuda")
+    calls = [
+        (lambda q, k, c, s, qw, kw: da.qk_norm_rotary(q, k, q, None, c, s, q_weight=qw, k_weight=kw), [q, k, cos, sin, w, w]),
+        (lambda k, v, kc, vc, c, s, kw: da.paged_cache_append(k, None, v, kc, None, vc, table, lens, None, c, s, norm="rms",
+                                                              k_weight=kw), [k, v, kc, vc, cos, sin, w]),
+        (lambda q, kc, vc, lam, nw, nb, out: da.differential_attention_paged(
+            q, kc, q, None, vc, table, lens, lam, norm="rms", norm_weight=nw, norm_bias=nb, out=out),
+         [q, kc, vc, lam, nw, nw, out]),
+        (lambda q, kc, vc, lam: da.differential_attention_tree(
+            q, kc, q, None, vc, table, lens, torch.ones(T, T, dtype=torch.bool, device="cuda"), lam), [q, kc, vc, lam]),
+    ]
+    for call, args in calls:
+        call(*args)
+        for i, a in enumerate(args):
+            with fwad.dual_level():
+                duals = [fwad.make_dual(a, torch.ones_like(a)) if j == i else x for j, x in enumerate(args)]
+                for grad in (True, False):              # forward mode has a switch of its own
+                    with torch.set_grad_enabled(grad), pytest.raises(ValueError, match="forward-mode"):
+                        call(*duals)
+        torch.cuda.synchronize()
+    # a dual level with no dual tensor among the arguments, and one that is over
+    with fwad.dual_level():
+        want = da.qk_norm_rotary(q, None, None, None, cos, sin)[0]
+        fwad.make_dual(q, torch.ones_like(q))
+    assert torch.equal(da.qk_norm_rotary(q, None, None, None, cos, sin)[0], want)
