@@ -287,14 +287,24 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc* desc, const void* q1, const 
                         const void* dq2_out, const void* dk2_out, void* dq1, void* dk1, void* dq2, void* dk2,
                         float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
                         diffattn_stream_t stream) {
-    RotaryParams p{};
-    int rc = build_rotary(&p, desc, q1, k1, q2, k2, q_weight, k_weight, cos, sin, positions, dq1, dk1, dq2, dk2);
-    if (rc != DIFFATTN_OK) return rc;
+    if (!desc) return DIFFATTN_ERR_INVALID;
+    diffattn_rotary_desc d = *desc;
     const void* x[4] = {q1, k1, q2, k2};
     const void* g[4] = {dq1_out, dk1_out, dq2_out, dk2_out};
-    const int64_t* sg[4] = {desc->q1_grad_stride, desc->k1_grad_stride, desc->q2_grad_stride, desc->k2_grad_stride};
-    for (int i = 0, n = 0; i < 4; ++i) {
+    int64_t* sx[4] = {d.q1_stride, d.k1_stride, d.q2_stride, d.k2_stride};
+    const int64_t* sg[4] = {d.q1_grad_stride, d.k1_grad_stride, d.q2_grad_stride, d.k2_grad_stride};
+    for (int i = 0; i < 4; ++i) {
+        if (!x[i] && g[i] && d.norm == DIFFATTN_NORM_NONE) {
+            // a rotation's gradient does not depend on the rows, and the kernels do not read them
+            x[i] = g[i];
+            copy3(sx[i], sg[i]);
+        }
         if ((x[i] != nullptr) != (g[i] != nullptr)) return DIFFATTN_ERR_INVALID;
+    }
+    RotaryParams p{};
+    int rc = build_rotary(&p, &d, x[0], x[1], x[2], x[3], q_weight, k_weight, cos, sin, positions, dq1, dk1, dq2, dk2);
+    if (rc != DIFFATTN_OK) return rc;
+    for (int i = 0, n = 0; i < 4; ++i) {
         if (!x[i]) continue;
         if (!nonneg(sg[i])) return DIFFATTN_ERR_INVALID;
         p.s[n].g = g[i];
@@ -302,14 +312,14 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc* desc, const void* q1, const 
         if (!rows16(g[i], sg[i], p.bf16 ? 2 : 4)) p.fast = 0;
         ++n;
     }
-    if ((dq_weight || dk_weight) && desc->norm == DIFFATTN_NORM_NONE) return DIFFATTN_ERR_INVALID;
+    if ((dq_weight || dk_weight) && d.norm == DIFFATTN_NORM_NONE) return DIFFATTN_ERR_INVALID;
     if ((dq_weight && !q1 && !q2) || (dk_weight && !k1 && !k2)) return DIFFATTN_ERR_INVALID;
-    if (!workspace || workspace_bytes < rotary_bwd_bytes(desc) || !aligned16(workspace)) return DIFFATTN_ERR_INVALID;
+    if (!workspace || workspace_bytes < rotary_bwd_bytes(&d) || !aligned16(workspace)) return DIFFATTN_ERR_INVALID;
     p.partial = static_cast<float*>(workspace);
     p.dw[0] = dq_weight;
     p.dw[1] = dk_weight;
-    p.dw_stride[0] = desc->q_weight_stride;
-    p.dw_stride[1] = desc->k_weight_stride;
+    p.dw_stride[0] = d.q_weight_stride;
+    p.dw_stride[1] = d.k_weight_stride;
     int sms = 0;
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;

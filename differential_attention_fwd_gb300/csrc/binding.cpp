@@ -283,7 +283,9 @@ struct RotaryBackward : public torch::autograd::Node {
     Rotary r;
     torch::autograd::SavedVariable x[4], w[2], tables[3];      // tables: cos, sin, positions
     bool given[4] = {}, weight[2] = {};
+    // without the norm the rows themselves are not saved: the gradient does not depend on them
     std::vector<int64_t> sizes[4];
+    std::optional<at::Device> dev;
     bool released = false;
 
     torch::autograd::variable_list apply(torch::autograd::variable_list&& grads) override {
@@ -309,18 +311,19 @@ struct RotaryBackward : public torch::autograd::Node {
         if (weight[1]) c.kw = plain_f32(wt[1]);
         diffattn_rotary_desc d = c.desc();
         Tensor xs[4], gs[4], dx[4];
-        std::optional<at::Device> dev;
+        const at::ScalarType type = c.dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat;
         int out = 0;
         for (int i = 0; i < 4; ++i) {
             if (!given[i]) continue;
-            xs[i] = x[i].unpack();
-            dev = xs[i].device();
+            if (c.norm) {
+                xs[i] = x[i].unpack();
+                strides3(row_stride(d, i), xs[i]);
+            }
             Tensor g = grads[out++];
-            if (!g.defined()) g = at::zeros(xs[i].sizes(), xs[i].options());
-            gs[i] = inner(g.scalar_type() == xs[i].scalar_type() ? g : g.to(xs[i].scalar_type()));
-            strides3(row_stride(d, i), xs[i]);
+            if (!g.defined()) g = at::zeros(sizes[i], at::TensorOptions().dtype(type).device(*dev));
+            gs[i] = inner(g.scalar_type() == type ? g : g.to(type));
             strides3(grad_stride(d, i), gs[i]);
-            dx[i] = fresh_tensor(xs[i].sizes(), xs[i].scalar_type(), *dev);
+            dx[i] = fresh_tensor(sizes[i], type, *dev);
         }
         Tensor dw[2];
         for (int i = 0; i < 2; ++i)
@@ -411,8 +414,10 @@ PyObject* rotary(PyObject* const* a) {
             node->given[i] = in[i].defined();
             if (!in[i].defined()) continue;
             from.push_back(in[i]);
-            node->x[i] = torch::autograd::SavedVariable(x[i], false);
+            node->sizes[i] = in[i].sizes().vec();
+            if (r.norm) node->x[i] = torch::autograd::SavedVariable(x[i], false);
         }
+        node->dev = dev;
         const Tensor ws[2] = {r.qw_given, r.kw_given};
         for (int i = 0; i < 2; ++i) {
             node->weight[i] = ws[i].defined();

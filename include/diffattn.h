@@ -521,7 +521,8 @@ int diffattn_rotary(const diffattn_rotary_desc *desc, const void *q1, const void
 /*
  * diffattn_rotary_bwd -- gradients of diffattn_rotary.  dq1_out .. dk2_out:
  * gradients of the outputs (inputs' dtype, *_grad_stride), NULL for tensors that
- * are left out; dq1 .. dk2: dense gradients of the inputs, overwritten;
+ * are left out; q1 .. k2: the inputs, which are not read without the norm and may
+ * then all be NULL (their strides are not read either); dq1 .. dk2: dense gradients of the inputs, overwritten;
  * dq_weight, dk_weight: float32, [D] or [heads, D] as the weights, overwritten,
  * NULL when not wanted (they need the norm).  With u the rotation of dy by the
  * negative angles:

@@ -110,3 +110,43 @@ def test_dual_tensors_are_refused():
         want = da.qk_norm_rotary(q, None, None, None, cos, sin)[0]
         fwad.make_dual(q, torch.ones_like(q))
     assert torch.equal(da.qk_norm_rotary(q, None, None, None, cos, sin)[0], want)
+
+
+@pytest.mark.parametrize("D,R", [(64, 64), (48, 24)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows_changed_in_place_after_a_rotation(D, R, interleaved):
+    """Without the norm the gradient does not depend on the rows: they are not kept, and may be
+    changed; with it a change is an error."""
+    g = torch.Generator().manual_seed(D)
+    B, H, Hk, T = 2, 3, 2, 9
+    xs = [rows(g, B, n, T, D, torch.bfloat16) for n in (H, Hk, H, Hk)]
+    cos, sin = da.rotary_tables(T, R, device="cuda")
+    pos = torch.arange(T)[None].expand(B, T)
+
+    def call(norm):
+        leaves = [x.clone().requires_grad_() for x in xs]
+        inner = [x * 1 for x in leaves]                 # not leaves: these may change in place
+        args = dict(norm=norm, norm_eps=EPS, interleaved=interleaved)
+        saved = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t.dim()) or t, lambda t: t):
+            da.qk_norm_rotary(*inner, cos, sin, **args)
+        assert saved.count(4) == (4 if norm else 0)
+        out = da.qk_norm_rotary(*inner, cos, sin, **args)
+        with torch.no_grad():
+            for x in inner:
+                x.fill_(float("nan"))
+        return leaves, out
+
+    leaves, out = call(None)
+    # one output is not used: a gradient that never comes is zero
+    dys = [torch.randn(y.shape, generator=g).to(torch.bfloat16).cuda() for y in out[:3]]
+    grads = torch.autograd.grad(out[:3], leaves, dys)
+    assert torch.count_nonzero(grads[3]) == 0
+    for dx, dy in zip(grads, dys):
+        want, _, _ = ref.norm_rotate_backward(None, None, d64(cos), d64(sin), pos, interleaved, None, EPS, d64(dy))
+        # three float32 roundings of |dy_a| + |dy_b| <= 2 max|dy|, and the result's
+        bound = 3 * ref.U * 2 * d64(dy).abs().amax(-1, keepdim=True) + 2.0 ** -8 * want.abs()
+        assert ((d64(dx) - want).abs() <= bound).all()
+    leaves, out = call("rms")
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out, leaves, [torch.ones_like(y) for y in out])
