@@ -33,6 +33,8 @@
 // either.  So in those tiles (the last one or two of a sequence) warp 11 puts zeros for
 // rows past the end, and for single values that are not finite it puts zeros and marks
 // the key; the results' warps then add such a value to the rows that see its key.
+#include <cfloat>
+
 #include "paged_plan.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -56,8 +58,15 @@ constexpr int VST = 5;                          // value stages
 constexpr int KST_MAX = 5;
 constexpr int SEGS = 8;                         // segments whose flags are kept apart
 constexpr int FLAGS = 18;                       // tiles that reach into the new tokens: (1024 + 63) / 64 + 1
-// A finite stand-in for the maximum of a row that has seen nothing.
-constexpr float NOTHING = -1e30f;
+// A finite stand-in for the maximum of a row that has seen nothing: no score is lower.
+constexpr float NOTHING = -FLT_MAX;
+// What the sum of 32 weights may reach before the maximum m is looked at again.  The exponent s *
+// scale - m is one fused operation, so the highest score's is not 0 but what m's own rounding left:
+// nothing up to 2^24, but from 2^31 on an infinity or no weight at all.  Beyond 2^24 the limit is
+// below any sum, and the weights are formed again with the product rounded as m was.  (Two
+// operations for every score: 3 % of the time of 64 tokens over 16 x 8192, for scores that no
+// ordinary head has.)
+__device__ __forceinline__ float sum_limit(float m) { return fabsf(m) < 16777216.f || m == NOTHING ? 256.f : -1.f; }
 
 template <int HD, bool KS>
 struct Cfg {
@@ -493,7 +502,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             uint64_t tree = 0;
             if (p.mask && (int64_t)(cur.tile0 + live) * KT > s.before)
                 tree = paged_mask_bits<32>(p, cur.b, x.q, mine, s.n_new, lane);
-            float m_run = NOTHING, l = 0.f;
+            float m_run = NOTHING, l = 0.f, limit = 256.f;
             for (int j = 0; j < live; ++j) {
                 const int buf = j & 1;
                 const uint32_t tS = lane_base + tm_s(br, buf);
@@ -517,16 +526,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                         for (int c = 0; c < 32; ++c) sc[c] = (seen >> c & 1u) ? sc[c] : 0xff800000u;
                     }
                     const bool first = j == 0 && h == 0;
-                    if (first) m_run = fmaxf(half_max(sc) * sl2, NOTHING);
+                    if (first) {
+                        m_run = fmaxf(half_max(sc) * sl2, NOTHING);
+                        limit = sum_limit(m_run);
+                    }
                     float tsum = half_weights(sc, sl2, m_run, pk);
-                    if (!first && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
+                    if (__any_sync(0xffffffffu, !(tsum <= limit))) {
                         const float mxs = half_max(sc) * sl2;
-                        if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
+                        const bool move = __any_sync(0xffffffffu, mxs > m_run + 8.0f);
+                        float alpha = 1.f;
+                        if (move) {
                             const float m_new = fmaxf(m_run, mxs);
-                            const float alpha = ex2_approx(m_run - m_new);
+                            alpha = ex2_approx(m_run - m_new);
                             l *= alpha;
                             m_run = m_new;
-                            tsum = half_weights(sc, sl2, m_run, pk);
+                            limit = sum_limit(m_run);
+                        }
+                        if (move || __any_sync(0xffffffffu, limit < 0.f)) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                sc[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sc[c]), sl2), -m_run));
+                            tsum = half_weights(sc, 1.f, 0.f, pk);
+                        }
+                        if (move) {
                             uint32_t o[32];
                             if (h == 1) {       // the first half's weights
                                 tmem_wait_st();
