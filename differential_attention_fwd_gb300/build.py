@@ -7,7 +7,8 @@ header is newer than the library.
 
 csrc/binding.cpp, the Python binding of the paged-cache operators, is compiled with
 the host compiler against torch's headers into _binding.so beside the library,
-which it calls.
+which it calls.  Either is made again by itself, and an error of the binding leaves
+the library in place: the C ABI needs nothing but nvcc.
 
 build(variant="waitprof") makes a second library, libdiffattn_waitprof.so,
 from the same sources compiled with -DDIFFATTN_WAIT_PROFILE: its forward
@@ -78,24 +79,34 @@ def _run(cmd, what: str) -> str:
     return r.stdout + r.stderr
 
 
+def _headers():
+    return sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
 def _deps():
-    return _sources() + [os.path.join(CSRC, "binding.cpp")] + sorted(glob.glob(os.path.join(CSRC, "*.h")) +
-                               glob.glob(os.path.join(CSRC, "*.cuh")) +
-                               glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + _headers()
+
+
+def _newer(lib: str, deps) -> bool:
+    return os.path.exists(lib) and all(os.path.getmtime(p) <= os.path.getmtime(lib) for p in deps)
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib):
-        return False
-    t = os.path.getmtime(lib)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(lib, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_headers()])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           variant=None) -> str:
-    """Compile and link; returns the library path."""
+    """Compile and link what is not up to date; returns the library path.  The library needs nvcc
+    alone, and is in place before the binding (which needs torch's headers) can fail."""
     lib, objdir, defines = VARIANTS[variant]
-    if not force and up_to_date(lib) and (variant or up_to_date(BINDING)):
+    with_lib = force or not up_to_date(lib)
+    with_binding = variant is None and (force or not binding_up_to_date())
+    if not with_lib and not with_binding:
         return lib
     cc = nvcc()
     os.makedirs(objdir, exist_ok=True)
@@ -109,26 +120,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
+    def compile_binding():
+        compile_, link = _binding_command(os.path.join(objdir, "binding.cpp.o"))
+        _run(compile_, "the binding does not compile")
+        return link
+
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        binding = os.path.join(objdir, "binding.cpp.o")
-        if not variant:
-            compile_binding, link_binding = _binding_command(binding)
-            bound = ex.submit(_run, compile_binding, "the binding does not compile")
-        results = list(ex.map(compile_one, _sources()))
-        if not variant:
-            bound.result()
+        link_binding = ex.submit(compile_binding) if with_binding else None
+        results = list(ex.map(compile_one, _sources())) if with_lib else []
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
-    tmp = lib + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib)
-    if not variant:
-        _run(link_binding, "the binding does not link")
+    if with_lib:
+        tmp = lib + ".tmp"
+        cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
+    if with_binding:
+        _run(link_binding.result(), "the binding does not link")
         os.replace(BINDING + ".tmp", BINDING)
     return lib
 
