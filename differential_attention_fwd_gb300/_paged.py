@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from . import _lib
+from . import _lib, build
 
 _native = None
 
@@ -26,6 +26,10 @@ def _load():
         if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")):
             raise RuntimeError("_binding.so is missing: build the CUDA library first "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
+        made_for = build.binding_torch()
+        if made_for not in (None, build.torch_version()):
+            raise RuntimeError(f"_binding.so was built for torch {made_for}, and torch {build.torch_version()} is installed: "
+                               "build it again (python -c 'import __graft_entry__ as g; g.build()')")
         _native = importlib.import_module("._binding", __package__)
         _native.set_error(_lib.DiffattnError)
     return _native

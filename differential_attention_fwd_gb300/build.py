@@ -7,8 +7,9 @@ header is newer than the library.
 
 csrc/binding.cpp, the Python binding of the paged-cache operators, is compiled with
 the host compiler against torch's headers into _binding.so beside the library,
-which it calls.  Either is made again by itself, and an error of the binding leaves
-the library in place: the C ABI needs nothing but nvcc.
+which it calls; it fits that torch alone, whose version _build/binding.torch keeps.
+Either is made again by itself, and an error of the binding leaves the library in
+place: the C ABI needs nothing but nvcc.
 
 build(variant="waitprof") makes a second library, libdiffattn_waitprof.so,
 from the same sources compiled with -DDIFFATTN_WAIT_PROFILE: its forward
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -95,8 +97,29 @@ def up_to_date(lib: str = LIB) -> bool:
     return _newer(lib, _deps())
 
 
+def torch_version():
+    """The version of the torch that is installed (without importing it), or None."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "binding.torch")
+
+
+def binding_torch():
+    """The version of the torch that the binding was built for, or None where it is not known."""
+    if not os.path.exists(_stamp()):
+        return None
+    with open(_stamp()) as f:
+        return f.read()
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_headers()])
+    return (_newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_headers()]) and
+            binding_torch() is not None and binding_torch() == torch_version())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
@@ -142,6 +165,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     if with_binding:
         _run(link_binding.result(), "the binding does not link")
         os.replace(BINDING + ".tmp", BINDING)
+        with open(_stamp(), "w") as f:
+            f.write(torch_version() or "")
     return lib
 
 

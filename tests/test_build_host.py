@@ -1,11 +1,12 @@
 """CPU tests of the build: the library does not wait for the binding, and each is made again
-when what it was made from has changed.  The compilers are stood in for."""
+when what it was made from or for has changed.  The compilers are stood in for."""
 import os
 import subprocess
 from types import SimpleNamespace
 
 import pytest
 
+from differential_attention_fwd_gb300 import _paged
 from differential_attention_fwd_gb300 import build as build_mod
 
 
@@ -62,3 +63,23 @@ def test_only_what_is_stale_is_made(fake):
     assert fake.ran == ["binding.cpp.o", "binding.so.tmp"]
     build_mod.build(force=True)
     assert {"rotary.cu.o", "lib.so.tmp"} <= set(fake.ran)
+
+
+def test_another_torch_makes_the_binding_again(fake, monkeypatch):
+    build_mod.build()
+    fake.ran.clear()
+    monkeypatch.setattr(build_mod, "torch_version", lambda: "1.0")
+    build_mod.build()
+    assert fake.ran == ["binding.cpp.o", "binding.so.tmp"]
+    build_mod.build()
+    assert len(fake.ran) == 2
+
+
+def test_a_binding_for_another_torch_is_not_loaded(monkeypatch):
+    build_mod.build()
+    monkeypatch.setattr(_paged, "_native", None)
+    monkeypatch.setattr(build_mod, "torch_version", lambda: "1.0")
+    with pytest.raises(RuntimeError, match="build it again"):
+        _paged._load()
+    monkeypatch.undo()
+    assert _paged._load() is not None
