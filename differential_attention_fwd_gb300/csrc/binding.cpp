@@ -103,6 +103,15 @@ double number(PyObject* o, const char* name) {
     return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        bad_type(std::string(name) + " must be a truth value");
+    }
+    return v == 1;
+}
+
 // The code of a norm's name; `group` where the output epilogue allows it.
 int32_t norm_code(PyObject* o, bool group) {
     if (is_none(o)) return DIFFATTN_NORM_NONE;
@@ -391,7 +400,7 @@ PyObject* rotary(PyObject* const* a) {
     if (!r.norm && !(is_none(a[9]) && is_none(a[10]))) bad_value("q_weight and k_weight need norm='rms'");
     r.qw = norm_weight(a[9], "q_weight", r.H, r.D, dev, &r.qw_given, &r.qws);
     r.kw = norm_weight(a[10], "k_weight", r.Hk, r.D, dev, &r.kw_given, &r.kws);
-    r.interleaved = PyObject_IsTrue(a[11]) == 1;
+    r.interleaved = truth(a[11], "interleaved");
     no_tangent({&in[0], &in[1], &in[2], &in[3], &r.cos, &r.sin, &r.qw_given, &r.kw_given}, "qk_norm_rotary");
     const c10::cuda::OptionalCUDAGuard guard(dev);
     bool grad = false;
@@ -543,7 +552,7 @@ PyObject* append(PyObject* const* a) {
     r.set_norm(a[12], a[13]);
     if (!r.norm && !is_none(a[14])) bad_value("k_weight needs norm='rms'");
     r.kw = norm_weight(a[14], "k_weight", r.Hk, r.D, dev, &r.kw_given, &r.kws);
-    r.interleaved = PyObject_IsTrue(a[15]) == 1;
+    r.interleaved = truth(a[15], "interleaved");
     no_tangent({&k[0], &k[1], &v, &c.k1, &c.k2, &c.v, &r.cos, &r.sin, &r.kw_given}, "paged_cache_append");
     if (wants_grad({&k[0], &k[1], &v, &c.k1, &c.k2, &c.v, &r.kw_given}))
         bad_value("paged_cache_append is forward only: call it under torch.no_grad() or detach its inputs");

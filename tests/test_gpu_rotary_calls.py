@@ -150,3 +150,19 @@ def test_rows_changed_in_place_after_a_rotation(D, R, interleaved):
     leaves, out = call("rms")
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         torch.autograd.grad(out, leaves, [torch.ones_like(y) for y in out])
+
+
+def test_interleaved_that_is_no_truth_value():
+    g = torch.Generator().manual_seed(1)
+    k, v = rows(g, 1, 2, 3, 64), rows(g, 1, 2, 3, 128)
+    kc, vc = (torch.zeros(2, 2, 16, n, device="cuda") for n in (64, 128))
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cos, sin = da.rotary_tables(16, 64, device="cuda")
+    several = torch.zeros(2)
+    with pytest.raises(TypeError, match="interleaved"):
+        da.qk_norm_rotary(k, None, None, None, cos, sin, interleaved=several)
+    with pytest.raises(TypeError, match="interleaved"):
+        da.paged_cache_append(k, None, v, kc, None, vc, table, lens, None, cos, sin, interleaved=several)
+    assert torch.count_nonzero(kc) == 0
+    a, b = (da.qk_norm_rotary(k, None, None, None, cos, sin, interleaved=i)[0] for i in (1, True))
+    assert torch.equal(a, b)
