@@ -69,6 +69,7 @@ struct Cfg {
     static constexpr int RING = NST * STAGE;
     static constexpr int OFF_V = NK * KP * PANEL;
     static constexpr int WARP_ROWS = paged_solo_rows(HD);
+    static_assert(WARP_ROWS <= 8, "a warp alone has one row a thread: HR = 1");
     static constexpr int Q_PANEL = NR * 128;                    // [branch][panel] 16 rows x 128 bytes of the block,
     static constexpr int Q_WARP = 2 * KP * WARP_ROWS * 128;     // or WARP_ROWS x 128 bytes of a warp
     static constexpr int OFF_Q = WARPS * RING;
@@ -150,7 +151,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     // One warp a worker where that makes at most two workers a unit, and if the unit's rows
     // allow it.  (The barriers in here order the above.)
     const PagedScan found = paged_scan<THREADS>(p, KT, EXTRA, scan);
-    const bool solo = p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
+    const bool solo = HR == 1 && p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
     const int nw = solo ? WARPS : 1;                            // workers of the block
     paged_locate<WARPS>(p, found, KT, EXTRA, nw, gridDim.x * nw, SNAP, &blk);
     const int mine = solo ? w : 0;
@@ -570,65 +571,61 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             continue;
         }
         // ---- alone: the rows out of the registers, finished, or as a partial result
-        const bool whole = cur.whole();
-        {
-            constexpr int h = 0;                // up to 8 rows
-            const bool live_row = la;
-            if (!whole) {
-                float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + r0 + 8 * h) * paged_part_floats(DV);
-                if (live_row) {
-                    if ((lane & 3) == 0) *reinterpret_cast<float4*>(part) = make_float4(m[0][h], l[0][h], m[1][h], l[1][h]);
+        if (!cur.whole()) {
+            float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + r0) * paged_part_floats(DV);
+            if (la) {
+                if ((lane & 3) == 0) *reinterpret_cast<float4*>(part) = make_float4(m[0][0], l[0][0], m[1][0], l[1][0]);
 #pragma unroll
-                    for (int br = 0; br < 2; ++br)
+                for (int br = 0; br < 2; ++br)
 #pragma unroll
-                        for (int n = 0; n < DV / 8; ++n)
-                            *reinterpret_cast<float2*>(part + 4 + br * DV + 8 * n + 2 * (lane & 3)) =
-                                make_float2(o[br][n][2 * h], o[br][n][2 * h + 1]);
-                }
-                __syncwarp();                   // before the next unit's queries overwrite these
-                continue;
+                    for (int n = 0; n < DV / 8; ++n)
+                        *reinterpret_cast<float2*>(part + 4 + br * DV + 8 * n + 2 * (lane & 3)) =
+                            make_float2(o[br][n][0], o[br][n][1]);
             }
-            const PagedRow x = ra;
-            const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
-            const float i1 = l[0][h] == 0.f ? 0.f : 1.f / l[0][h], i2 = l[1][h] == 0.f ? 0.f : 1.f / l[1][h];
-            float sum = 0.f;
+            __syncwarp();                   // before the next unit's queries overwrite these
+            continue;
+        }
+        const PagedRow x = ra;
+        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float i1 = l[0][0] == 0.f ? 0.f : 1.f / l[0][0], i2 = l[1][0] == 0.f ? 0.f : 1.f / l[1][0];
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < DV / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                o[0][n][e] = fmaf(-lam, __fmul_rn(o[1][n][e], i2), __fmul_rn(o[0][n][e], i1));
+                sum += o[0][n][e];
+            }
+        if (p.norm != kNormNone) {          // of the row's four threads
+            float mean = 0.f, ss = 0.f;
+            if (p.norm == kNormGroup) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                mean = sum / DV;
+            }
 #pragma unroll
             for (int n = 0; n < DV / 8; ++n)
 #pragma unroll
-                for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                    o[0][n][e] = fmaf(-lam, __fmul_rn(o[1][n][e], i2), __fmul_rn(o[0][n][e], i1));
-                    sum += o[0][n][e];
+                for (int e = 0; e < 2; ++e) {
+                    o[0][n][e] -= mean;
+                    ss = fmaf(o[0][n][e], o[0][n][e], ss);
                 }
-            if (p.norm != kNormNone) {          // of the row's four threads
-                float mean = 0.f, ss = 0.f;
-                if (p.norm == kNormGroup) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    mean = sum / DV;
-                }
-#pragma unroll
-                for (int n = 0; n < DV / 8; ++n)
-#pragma unroll
-                    for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                        o[0][n][e] -= mean;
-                        ss = fmaf(o[0][n][e], o[0][n][e], ss);
-                    }
-                ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-                ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-                const float r = 1.0f / sqrtf(ss / DV + p.norm_eps);
-#pragma unroll
-                for (int n = 0; n < DV / 8; ++n) {
-                    o[0][n][2 * h] *= r;
-                    o[0][n][2 * h + 1] *= r;
-                }
-            }
-            const int64_t at = cur.b * p.s_o[0] + x.h * p.s_o[1] + x.q * p.s_o[2] + 2 * (lane & 3);
-            const int64_t ch = (int64_t)x.h * DV + 2 * (lane & 3);
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
-            if (live_row)
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            const float r = 1.0f / sqrtf(ss / DV + p.norm_eps);
 #pragma unroll
             for (int n = 0; n < DV / 8; ++n) {
-                float y0 = o[0][n][2 * h], y1 = o[0][n][2 * h + 1];
+                o[0][n][0] *= r;
+                o[0][n][1] *= r;
+            }
+        }
+        const int64_t at = cur.b * p.s_o[0] + x.h * p.s_o[1] + x.q * p.s_o[2] + 2 * (lane & 3);
+        const int64_t ch = (int64_t)x.h * DV + 2 * (lane & 3);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+        if (la) {
+#pragma unroll
+            for (int n = 0; n < DV / 8; ++n) {
+                float y0 = o[0][n][0], y1 = o[0][n][1];
                 if (p.norm_weight) { y0 *= p.norm_weight[ch + 8 * n]; y1 *= p.norm_weight[ch + 8 * n + 1]; }
                 if (p.norm_bias) { y0 += p.norm_bias[ch + 8 * n]; y1 += p.norm_bias[ch + 8 * n + 1]; }
                 y0 *= p.out_scale;
