@@ -28,8 +28,8 @@
 // Weights are 2^(s - m) against a running maximum that moves only when some weight would
 // pass 2^8.  They go to the product with V as two bf16 parts, the rounded weight and what
 // the rounding left (2^-16 together): with one part the branches' difference was off by
-// 2.1e-3 of itself, more than the output's own rounding (1.7e-3), and the second product
-// costs nothing here, since the tile's bytes take longer (5 % at 4 rows of head width 128).
+// 2.1e-3 of itself, more than the output's own rounding (1.7e-3).  The second product passes
+// while the tile's bytes arrive; where it does not quite, at 4 rows of head width 128, it costs 5 %.
 //
 // Measured, both launches: 16 sequences of up to 8192 keys, 16 heads, D = 64, 710 MB of
 // cache: 122 us, 0.86 of the copy rate; 4 of 65536, 8 key/value heads, shared keys, D = 128:

@@ -145,7 +145,8 @@ __device__ __forceinline__ void split2(uint64_t w, uint32_t& hi, uint32_t& lo) {
 }
 // P = 2^(s * scale_log2 - m) for 32 scores, and the sum of P.  Rounded to one bf16, P would
 // put an error of 2e-3 of the result's size into long caches, where the means of the two
-// branches cancel; so it is the sum of two: pk[0..15] and what is left, pk[16..31].
+// branches cancel; so it is the sum of two: pk[0..15] and what is left, pk[16..31], 2^-16 together
+// (and as much once more for a tile's first half where the maximum moves in its second).
 __device__ __forceinline__ float half_weights(const uint32_t (&s)[32], float sl2, float m, uint32_t (&pk)[32]) {
     const uint64_t scale2 = f2_pack(sl2, sl2);
     const uint64_t negm2 = f2_pack(-m, -m);

@@ -36,6 +36,9 @@ constexpr int THREADS = 256;
 constexpr int MAX_D = 128;
 constexpr int BWD_STEPS = 3;    // rows of each group of lanes in an item of the backward,
 constexpr int BWD_STAGES = 3;   // and rows on their way
+// Blocks of the backward for any layout, and partial rows that they leave, in all: a number of its
+// own (16 for each of 152 SMs), since the workspace's size must not depend on the current device.
+constexpr int BWD_ANY_BLOCKS = 2432;
 
 // 16 bytes of elements, N of them, as N / 2 packed pairs of floats (two elements an
 // instruction: at an SM's share of the HBM rate the arithmetic is half of the time).
@@ -281,6 +284,8 @@ rotary_kernel(const RotaryParams p) {
                 uint64_t sq[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) sq[e] = f2_mul(c[e], c[e]);
+                // (off by 2 units in the last place at most: float32 rows 1.5e-7 where a root and
+                // a division give 1.2e-7)
                 const float r = rsqrtf(group_sum<G>(pair_sum<V>(sq)) * p.inv_D + p.eps);
                 const uint64_t r2 = f2_pack(r, r);
                 if (weighted) {             // from L1: the registers are worth more blocks an SM
@@ -380,10 +385,6 @@ rotary_any_kernel(const RotaryParams p) {
 // own 2 V channels in registers, and an item leaves one partial row: the sum's order is
 // fixed, without atomics.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
 // Shared memory of a backward block, in floats: ring, tables, sums, weights, flags.
 struct BwdLayout {
     int turns, red, weights, fine, total;
@@ -754,7 +755,7 @@ void plan_rotary_bwd(RotaryParams* p, int num_sms) {
     const int64_t tokens = (int64_t)p->B * p->T;
     if (!p->fast) {                         // a head a block, and chunks in strides
         rot::set_head_blocks(p, 1);
-        const int64_t steps = (tokens + 7) / 8, chunks = (2432 + p->heads - 1) / p->heads;
+        const int64_t steps = (tokens + 7) / 8, chunks = (rot::BWD_ANY_BLOCKS + p->heads - 1) / p->heads;
         p->chunks = (int)(chunks < steps ? chunks : steps);
         return;
     }
@@ -767,7 +768,7 @@ void plan_rotary_bwd(RotaryParams* p, int num_sms) {
 size_t rotary_bwd_floats(int64_t B, int64_t T, int64_t D, int64_t heads) {
     // at most: chunks of the fewest tokens a block takes (16 groups a step), a row a head
     const int64_t chunks = (B * T + 16 * rot::BWD_STEPS - 1) / (16 * rot::BWD_STEPS);
-    const int64_t fast = chunks * heads, any = 2432 + heads;
+    const int64_t fast = chunks * heads, any = rot::BWD_ANY_BLOCKS + heads;
     return (size_t)((fast > any ? fast : any) * D);
 }
 
