@@ -216,8 +216,8 @@ void plan_mma(const diffattn_paged_desc& d, const diffattn_pages& g, int sms, Pa
 
 // The tcgen05 kernel, for more than 16 rows: the 16-row kernel reads the cache once for each
 // 16 of them.  Measured on both sides (16 sequences of up to 8192 keys; D = 128 with 8
-// key/value heads, D = 64 with 16): 16 rows take 95 and 148 us there and 101 and 175 here,
-// 18 to 32 rows 140 to 154 and 244 to 257 there, 99 to 100 and 173 here.
+// key/value heads and shared keys, D = 64 with 16): 16 rows take 86 and 139 us there and 100 and
+// 170 here, 18 to 32 rows 128 to 139 and 232 to 245 there, 98 and 168 here.
 bool wants_tc(const diffattn_paged_desc& d) {
     const int64_t group = d.kv_group > 1 ? d.kv_group : 1;
     return group * d.Tq > kMmaRows;

@@ -19,8 +19,8 @@
 // products 149 and 242, no arithmetic between scores and weights 139 and 207, the cache in
 // L2 147 and 246.  Sixteen warps for the weights in place of eight, half of a tile's keys
 // each with a barrier a pair, took 6 % longer, and 4 % with everything unrolled over 64 keys
-// (the warps then wait for instructions).  The row count hardly matters: 99 us with 9 tokens
-// (ragged, 8 heads), 117 with 64.
+// (the warps then wait for instructions).  The row count hardly matters: 98 us with 9 tokens
+// (ragged, 8 heads), 116 with 64.  Chunks of 512 and 1024 tokens run at 600 to 630 TFLOP/s.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7   weights and results of branch 1, 2 (TMEM lanes 0-127)
