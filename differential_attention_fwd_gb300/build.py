@@ -21,7 +21,6 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
-import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -98,11 +97,12 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def torch_version():
-    """The version of the torch that is installed (without importing it), or None."""
+    """The version of the torch that imports, or None."""
     try:
-        return importlib.metadata.version("torch")
-    except importlib.metadata.PackageNotFoundError:
+        import torch
+    except ImportError:
         return None
+    return str(torch.__version__)
 
 
 def _stamp() -> str:

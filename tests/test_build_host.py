@@ -1,10 +1,12 @@
 """CPU tests of the build: the library does not wait for the binding, and each is made again
 when what it was made from or for has changed.  The compilers are stood in for."""
+import importlib.metadata
 import os
 import subprocess
 from types import SimpleNamespace
 
 import pytest
+import torch
 
 from differential_attention_fwd_gb300 import _paged
 from differential_attention_fwd_gb300 import build as build_mod
@@ -73,6 +75,14 @@ def test_another_torch_makes_the_binding_again(fake, monkeypatch):
     assert fake.ran == ["binding.cpp.o", "binding.so.tmp"]
     build_mod.build()
     assert len(fake.ran) == 2
+
+
+def test_the_torch_that_imports_decides(monkeypatch):
+    """Not what a package index knows of it, which may know nothing."""
+    def unknown(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(importlib.metadata, "version", unknown)
+    assert build_mod.torch_version() == str(torch.__version__)
 
 
 def test_a_binding_for_another_torch_is_not_loaded(monkeypatch):
