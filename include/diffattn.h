@@ -471,7 +471,8 @@ int diffattn_decode_noalloc(const diffattn_kv_desc *desc, const void *q1,
  *
  * B, T, D: batch, tokens, row width (1 .. 128).  H, Hk: heads of Q1, Q2 and of
  * K1, K2 (0 or more where both are left out).  dtype: of the rows.  rotary_dim: R,
- * even, 0 .. D (0: no rotation, cos and sin may be NULL).  norm: DIFFATTN_NORM_NONE or DIFFATTN_NORM_RMS, eps > 0.
+ * even, 0 .. D (0: no rotation, cos and sin may be NULL).  norm: DIFFATTN_NORM_NONE
+ * or DIFFATTN_NORM_RMS, eps > 0.
  * q_weight_stride, k_weight_stride: 0 (one weight row [D] for all heads) or D (a
  * row for each head, [H, D] or [Hk, D]).  table_rows: rows of cos and sin
  * ([table_rows, R/2] float32, dense).  pos64: positions are int64 (else int32);
