@@ -45,6 +45,9 @@ EXPORTED = (
     "diffattn_paged_append",
     "diffattn_paged_decode",
     "diffattn_paged_workspace_bytes",
+    "diffattn_head_norm",
+    "diffattn_head_norm_bwd",
+    "diffattn_head_norm_bwd_workspace_bytes",
     "diffattn_select_kernel",
     "diffattn_get_device_error",
     "diffattn_selftest_timeout",
@@ -120,6 +123,16 @@ class DiffattnPagedDesc(ctypes.Structure):
     ]
 
 
+class DiffattnNormDesc(ctypes.Structure):
+    """Mirror of diffattn_norm_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("T", ctypes.c_int64), ("C", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("out_scale", ctypes.c_float),
+        ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3),
+        ("dy_stride", ctypes.c_int64 * 3), ("dx_stride", ctypes.c_int64 * 3),
+    ]
+
+
 class DiffattnError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -190,6 +203,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_paged_decode.restype = ctypes.c_int
     lib.diffattn_paged_workspace_bytes.argtypes = [vp, vp]
     lib.diffattn_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.diffattn_head_norm.argtypes = [vp] * 6
+    lib.diffattn_head_norm.restype = ctypes.c_int
+    lib.diffattn_head_norm_bwd.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.diffattn_head_norm_bwd.restype = ctypes.c_int
+    lib.diffattn_head_norm_bwd_workspace_bytes.argtypes = [vp]
+    lib.diffattn_head_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_workspace_bytes.argtypes = []
     lib.diffattn_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_fwd.restype = ctypes.c_int

@@ -469,6 +469,139 @@ PyObject* rotary(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------------------
+// the norm of each head's output
+// ---------------------------------------------------------------------------
+// An uninitialised tensor laid out as `t` where that is dense in some order of its dimensions
+// (with rows of the innermost one), contiguous else.
+Tensor fresh_like(const Tensor& t) {
+    if (t.is_contiguous() || !inner_ok(t) || !t.is_non_overlapping_and_dense())
+        return fresh_tensor(t.sizes(), t.scalar_type(), t.device());
+    return Tensor(at::detail::empty_strided_cuda(t.sizes(), t.strides(), t.scalar_type(), t.device()));
+}
+
+// An affine parameter [H, C] or [H * C]: float32 and dense.
+Tensor affine(PyObject* o, const char* name, int64_t H, int64_t C, at::Device dev, Tensor* given) {
+    if (is_none(o)) return {};
+    const Tensor& t = tensor(o, name);
+    if (t.device() != dev || !((t.dim() == 2 && t.size(0) == H && t.size(1) == C) || (t.dim() == 1 && t.size(0) == H * C)))
+        bad_value(std::string(name) + " must be [H, Dv] = (" + std::to_string(H) + ", " + std::to_string(C) +
+                  ") on the inputs' device, got " + text(t.sizes()));
+    if (!at::isFloatingType(t.scalar_type())) bad_value(std::string(name) + " must be a floating tensor");
+    *given = t;
+    return plain_f32(t);
+}
+
+// The autograd node: backward through diffattn_head_norm_bwd.  Its inputs are x, then the
+// weight and the bias where they were given.
+struct HeadNormBackward : public torch::autograd::Node {
+    diffattn_norm_desc d{};
+    torch::autograd::SavedVariable x, w;
+    bool has[2] = {};                       // weight, bias
+    std::vector<int64_t> shape[2];
+    at::ScalarType type[2] = {};
+    std::optional<at::Device> dev;
+    bool released = false;
+
+    torch::autograd::variable_list apply(torch::autograd::variable_list&& grads) override {
+        std::lock_guard<std::mutex> lock(mutex_);
+        TORCH_CHECK(!released, "differential_head_norm: backward a second time through a graph whose saved tensors were "
+                               "freed; pass retain_graph=True the first time");
+        TORCH_CHECK(!at::GradMode::is_enabled(), "differential_head_norm is differentiable once (no create_graph)");
+        TORCH_CHECK(!joins_default_stream(*this), "differential_head_norm: this captured backward pass would add to the "
+                    ".grad of a leaf that a graph made outside the capture, on the default stream, still holds; drop that "
+                    "graph (or make it on another stream), or take the gradients with torch.autograd.grad");
+        torch::autograd::variable_list result(1 + has[0] + has[1]);
+        if (!grads[0].defined()) return result;
+        const Tensor xs = inner(x.unpack());
+        const Tensor ws = has[0] ? plain_f32(w.unpack()) : Tensor();
+        const Tensor g = inner(grads[0].scalar_type() == xs.scalar_type() ? grads[0] : grads[0].to(xs.scalar_type()));
+        const c10::cuda::OptionalCUDAGuard guard(*dev);
+        diffattn_norm_desc c = d;
+        Tensor dx, da[2];
+        if (task_should_compute_output(0)) dx = fresh_like(xs);
+        for (int i = 0, out = 1; i < 2; ++i)
+            if (has[i] && task_should_compute_output(out++)) da[i] = fresh_tensor({c.H, c.C}, at::kFloat, *dev);
+        if (!dx.defined() && !da[0].defined() && !da[1].defined()) return result;
+        strides3(c.x_stride, xs);
+        strides3(c.dy_stride, g);
+        if (dx.defined()) strides3(c.dx_stride, dx);
+        const size_t bytes = da[0].defined() || da[1].defined() ? diffattn_head_norm_bwd_workspace_bytes(&c) : 0;
+        const Tensor space = bytes ? fresh_tensor({(int64_t)bytes}, at::kByte, *dev) : Tensor();
+        const int rc = diffattn_head_norm_bwd(&c, ptr(xs), fptr(ws), ptr(g), ptr(dx), (float*)ptr(da[0]), (float*)ptr(da[1]),
+                                              ptr(space), bytes, stream_of(*dev));
+        TORCH_CHECK(rc == DIFFATTN_OK, "diffattn_head_norm_bwd: ", diffattn_strerror(rc), " (", rc, ")");
+        result[0] = dx;
+        for (int i = 0, out = 1; i < 2; ++i) {
+            if (!has[i]) continue;
+            if (da[i].defined()) result[out] = da[i].to(type[i]).view(shape[i]);
+            ++out;
+        }
+        return result;
+    }
+    void release_variables() override {
+        std::lock_guard<std::mutex> lock(mutex_);
+        x.reset_data();
+        w.reset_data();
+        released = true;
+    }
+    std::string name() const override { return "HeadNormBackward"; }
+};
+
+PyObject* head_norm(PyObject* const* a) {
+    // x, norm, norm_eps, norm_weight, norm_bias, out_scale
+    const Tensor& x = need(a[0], "x", 4);
+    const at::Device dev = x.device();
+    diffattn_norm_desc d{};
+    d.dtype = dtype_code(x);
+    d.B = x.size(0);
+    d.H = x.size(1);
+    d.T = x.size(2);
+    d.C = x.size(3);
+    if (d.B < 1 || d.H < 1 || d.T < 1 || d.C < 1 || d.C > 256)
+        bad_value("x must be [B, H, T, Dv] with B, H, T >= 1 and Dv <= 256, got " + text(x.sizes()));
+    d.norm = norm_code(a[1], true);
+    if (d.norm == DIFFATTN_NORM_NONE) bad_value("norm must be 'rms' or 'group'");
+    d.eps = (float)number(a[2], "norm_eps");
+    if (!(std::isfinite(d.eps) && d.eps > 0.f)) bad_value("norm_eps must be positive and finite");
+    d.out_scale = (float)number(a[5], "out_scale");
+    if (!std::isfinite(d.out_scale)) bad_value("out_scale must be finite");
+    const c10::cuda::OptionalCUDAGuard guard(dev);
+    Tensor given[2];
+    const Tensor w = affine(a[3], "norm_weight", d.H, d.C, dev, &given[0]);
+    const Tensor b = affine(a[4], "norm_bias", d.H, d.C, dev, &given[1]);
+    no_tangent({&x, &given[0], &given[1]}, "differential_head_norm");
+    const bool grad = at::GradMode::is_enabled() && (x.requires_grad() || (given[0].defined() && given[0].requires_grad()) ||
+                                                     (given[1].defined() && given[1].requires_grad()));
+    Tensor xs, y;
+    {
+        at::NoGradGuard no_grad;
+        xs = inner(x);
+        y = fresh_like(xs);
+        strides3(d.x_stride, xs);
+        strides3(d.y_stride, y);
+        check(diffattn_head_norm(&d, ptr(xs), fptr(w), fptr(b), ptr(y), stream_of(dev)), "diffattn_head_norm");
+    }
+    if (grad) {
+        auto node = std::shared_ptr<HeadNormBackward>(new HeadNormBackward(), torch::autograd::deleteNode);
+        torch::autograd::variable_list from{x};
+        node->d = d;
+        node->dev = dev;
+        node->x = torch::autograd::SavedVariable(x, false);
+        for (int i = 0; i < 2; ++i) {
+            node->has[i] = given[i].defined();
+            if (!given[i].defined()) continue;
+            from.push_back(given[i]);
+            node->shape[i] = given[i].sizes().vec();
+            node->type[i] = given[i].scalar_type();
+        }
+        if (given[0].defined()) node->w = torch::autograd::SavedVariable(given[0], false);
+        node->set_next_edges(torch::autograd::collect_next_edges(from));
+        torch::autograd::set_history(y, node);
+    }
+    return THPVariable_Wrap(y);
+}
+
+// ---------------------------------------------------------------------------
 // the paged cache
 // ---------------------------------------------------------------------------
 struct Cache {
@@ -730,6 +863,7 @@ PyCFunction as_function(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t))
 
 PyMethodDef methods[] = {
     {"rotary", as_function(entry<rotary, 12>), METH_FASTCALL, nullptr},
+    {"head_norm", as_function(entry<head_norm, 6>), METH_FASTCALL, nullptr},
     {"append", as_function(entry<append, 16>), METH_FASTCALL, nullptr},
     {"attention", as_function(entry<attention, 16>), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},

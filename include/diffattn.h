@@ -644,6 +644,58 @@ int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages 
                           void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
 
 /*
+ * The norm of each head's output: the epilogue above as an operator of its own, with
+ * its gradients.  For a row x of C channels (1 .. 256) of head h, with mu = mean(x)
+ * (DIFFATTN_NORM_GROUP) or 0 (DIFFATTN_NORM_RMS), r = (mean((x - mu)^2) + eps)^-1/2,
+ *
+ *     y = out_scale (w[h] (x - mu) r + b[h])
+ *
+ * B, H, T, C: sizes; dtype: of x, y and their gradients; eps > 0, out_scale finite.
+ * *_stride: element strides of B, heads and T (innermost stride 1; >= 0) of x, y, and
+ * (backward) dy and dx.  float32 arithmetic, one rounding of y.
+ */
+typedef struct {
+    int64_t B, H, T, C;
+    int32_t dtype;
+    int32_t norm;
+    float eps, out_scale;
+    int64_t x_stride[3], y_stride[3], dy_stride[3], dx_stride[3];
+} diffattn_norm_desc;
+
+/*
+ * diffattn_head_norm -- y from x.  weight, bias: float32 [H, C], dense, NULL = 1 and 0.
+ * y must not overlap x, unless it is x with the same strides.  One launch.
+ * Rows of a multiple of 16 bytes that start on 16-byte boundaries run on the vector
+ * kernel, others a warp a row.
+ * Errors: DIFFATTN_ERR_INVALID (NULL pointers, sizes, strides, dtype, norm, eps,
+ * out_scale, a stride of 0 between rows of y); DIFFATTN_ERR_UNSUPPORTED (beyond 65535
+ * heads or 2^30 tokens); DIFFATTN_ERR_CUDA.
+ */
+int diffattn_head_norm(const diffattn_norm_desc *desc, const void *x, const float *weight,
+                       const float *bias, void *y, diffattn_stream_t stream);
+
+/* Bytes of workspace diffattn_head_norm_bwd needs, 0 for an invalid descriptor. */
+size_t diffattn_head_norm_bwd_workspace_bytes(const diffattn_norm_desc *desc);
+
+/*
+ * diffattn_head_norm_bwd -- gradients of diffattn_head_norm, from x and dy alone.  With
+ * h = (x - mu) r and g = out_scale w dy,
+ *
+ *     dx = r (g - mean(g) - h mean(g h))       (without mean(g) for the RMS norm)
+ *     dweight = out_scale sum of dy h          dbias = out_scale sum of dy
+ *
+ * the sums over a head's rows.  dx, dweight, dbias (float32 [H, C]): overwritten; NULL
+ * where not wanted, one at least given.  workspace: at least
+ * diffattn_head_norm_bwd_workspace_bytes bytes, 16-byte aligned, no initialisation
+ * needed; not read with neither dweight nor dbias.  No atomics: the result is
+ * reproducible bit for bit.  Errors as diffattn_head_norm, and a missing, small or
+ * misaligned workspace.
+ */
+int diffattn_head_norm_bwd(const diffattn_norm_desc *desc, const void *x, const float *weight,
+                           const void *dy, void *dx, float *dweight, float *dbias,
+                           void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
+
+/*
  * diffattn_select_kernel -- which kernel diffattn_fwd would launch for this
  * descriptor and these pointers (DIFFATTN_KERNEL_*), or a negative error code
  * if the arguments are invalid.  Host only; touches no GPU state.
