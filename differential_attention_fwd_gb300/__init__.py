@@ -33,7 +33,7 @@ __all__ = ["differential_lambda", "differential_attention", "differential_attent
            "differential_attention_decode",
            "rotary_tables", "qk_norm_rotary", "paged_cache_append",
            "differential_attention_paged", "differential_attention_tree",
-           "differential_head_norm",
+           "differential_cross_attention", "differential_head_norm",
            "make_desc", "make_kv_desc", "select_kernel", "get_device_error", "version",
            "DiffattnError"]
 
@@ -588,6 +588,6 @@ def get_device_error(device=None) -> int:
         return _lib.load().diffattn_get_device_error(_stream_handle(dev))
 
 
-from ._block import differential_head_norm  # noqa: E402
+from ._block import differential_cross_attention, differential_head_norm  # noqa: E402
 from ._paged import (differential_attention_paged, differential_attention_tree,  # noqa: E402
                      paged_cache_append, qk_norm_rotary, rotary_tables)

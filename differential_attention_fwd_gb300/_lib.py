@@ -45,6 +45,10 @@ EXPORTED = (
     "diffattn_paged_append",
     "diffattn_paged_decode",
     "diffattn_paged_workspace_bytes",
+    "diffattn_cross_fwd",
+    "diffattn_cross_workspace_bytes",
+    "diffattn_cross_bwd",
+    "diffattn_cross_bwd_workspace_bytes",
     "diffattn_head_norm",
     "diffattn_head_norm_bwd",
     "diffattn_head_norm_bwd_workspace_bytes",
@@ -120,6 +124,17 @@ class DiffattnPagedDesc(ctypes.Structure):
         ("q1_stride", ctypes.c_int64 * 3), ("q2_stride", ctypes.c_int64 * 3),
         ("o_stride", ctypes.c_int64 * 3), ("mask_stride", ctypes.c_int64 * 2),
         ("zero_rest", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class DiffattnCrossDesc(ctypes.Structure):
+    """Mirror of diffattn_cross_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("Tq", ctypes.c_int64), ("Tk", ctypes.c_int64),
+        ("D", ctypes.c_int64), ("Dv", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kv_group", ctypes.c_int32),
+        ("q1_stride", ctypes.c_int64 * 3), ("k1_stride", ctypes.c_int64 * 3),
+        ("q2_stride", ctypes.c_int64 * 3), ("k2_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3), ("o_stride", ctypes.c_int64 * 3), ("dout_stride", ctypes.c_int64 * 3),
     ]
 
 
@@ -203,6 +218,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_paged_decode.restype = ctypes.c_int
     lib.diffattn_paged_workspace_bytes.argtypes = [vp, vp]
     lib.diffattn_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.diffattn_cross_fwd.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 6 + [ctypes.c_size_t, vp]
+    lib.diffattn_cross_fwd.restype = ctypes.c_int
+    lib.diffattn_cross_bwd.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 12 + [ctypes.c_size_t, vp]
+    lib.diffattn_cross_bwd.restype = ctypes.c_int
+    for f in (lib.diffattn_cross_workspace_bytes, lib.diffattn_cross_bwd_workspace_bytes):
+        f.argtypes = [vp]
+        f.restype = ctypes.c_size_t
     lib.diffattn_head_norm.argtypes = [vp] * 6
     lib.diffattn_head_norm.restype = ctypes.c_int
     lib.diffattn_head_norm_bwd.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]

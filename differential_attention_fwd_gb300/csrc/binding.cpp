@@ -173,6 +173,35 @@ Tensor norm_weight(PyObject* o, const char* name, int64_t heads, int64_t D, at::
     return plain_f32(w);
 }
 
+bool wants_grad(std::initializer_list<const Tensor*> ts) {
+    if (!at::GradMode::is_enabled()) return false;
+    for (const Tensor* t : ts)
+        if (t->defined() && t->requires_grad()) return true;
+    return false;
+}
+
+// lambda: a number, or one value on the host or the device.
+struct Lambda {
+    float host = 0.f;
+    Tensor dev;             // float32, where it is on the device
+    Tensor given;           // the tensor, if it is one
+    Lambda(PyObject* o, at::Device on, const char* what) {
+        if (!THPVariable_Check(o)) {
+            host = (float)number(o, "coefficient");
+            return;
+        }
+        given = THPVariable_Unpack(o);
+        if (given.numel() != 1) bad_value("coefficient must be a scalar");
+        no_tangent({&given}, what);
+        if (given.is_cuda()) {
+            if (given.device() != on) bad_value("coefficient tensor must be on the inputs' device");
+            dev = plain_f32(given);
+        } else {
+            host = (float)given.item().toDouble();
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // norm and rotation
 // ---------------------------------------------------------------------------
@@ -507,9 +536,9 @@ struct HeadNormBackward : public torch::autograd::Node {
         TORCH_CHECK(!released, "differential_head_norm: backward a second time through a graph whose saved tensors were "
                                "freed; pass retain_graph=True the first time");
         TORCH_CHECK(!at::GradMode::is_enabled(), "differential_head_norm is differentiable once (no create_graph)");
-        TORCH_CHECK(!joins_default_stream(*this), "differential_head_norm: this captured backward pass would add to the "
-                    ".grad of a leaf that a graph made outside the capture, on the default stream, still holds; drop that "
-                    "graph (or make it on another stream), or take the gradients with torch.autograd.grad");
+        TORCH_CHECK(!joins_default_stream(*this), "differential_head_norm: this captured backward pass would add to the .grad "
+                    "of a leaf that a graph made outside the capture, on the default stream, still holds; drop that graph, "
+                    "or make it on another stream");
         torch::autograd::variable_list result(1 + has[0] + has[1]);
         if (!grads[0].defined()) return result;
         const Tensor xs = inner(x.unpack());
@@ -651,13 +680,6 @@ struct Cache {
     const int32_t* table_ptr() const { return table.const_data_ptr<int32_t>(); }
 };
 
-bool wants_grad(std::initializer_list<const Tensor*> ts) {
-    if (!at::GradMode::is_enabled()) return false;
-    for (const Tensor* t : ts)
-        if (t->defined() && t->requires_grad()) return true;
-    return false;
-}
-
 PyObject* append(PyObject* const* a) {
     // k1, k2, value, k1_cache, k2_cache, v_cache, block_table, lengths, new_lengths, cos, sin, positions, norm, norm_eps,
     // k_weight, interleaved
@@ -752,23 +774,8 @@ PyObject* attention(PyObject* const* a) {
         d.mask_stride[0] = n == 3 ? mask.stride(0) : 0;
         d.mask_stride[1] = mask.stride(-2);
     }
-    // lambda: a number, or one value on the host or the device
-    float lam = 0.f;
-    Tensor lam_dev;
-    if (THPVariable_Check(a[9])) {
-        const Tensor& t = THPVariable_Unpack(a[9]);
-        if (t.numel() != 1) bad_value("coefficient must be a scalar");
-        no_tangent({&t}, kAttention);
-        if (wants_grad({&t})) bad_value("attention over a paged cache is forward only: detach the coefficient");
-        if (t.is_cuda()) {
-            if (t.device() != dev) bad_value("coefficient tensor must be on the inputs' device");
-            lam_dev = plain_f32(t);
-        } else {
-            lam = (float)t.item().toDouble();
-        }
-    } else {
-        lam = (float)number(a[9], "coefficient");
-    }
+    const Lambda lam(a[9], dev, kAttention);
+    if (wants_grad({&lam.given})) bad_value("attention over a paged cache is forward only: detach the coefficient");
     no_tangent({&q1, &q2, &c.k1, &c.k2, &c.v}, kAttention);
     if (wants_grad({&q1, &q2, &c.k1, &c.k2, &c.v}))
         bad_value("attention over a paged cache is forward only: call it under torch.no_grad() or detach its inputs");
@@ -814,12 +821,205 @@ PyObject* attention(PyObject* const* a) {
     check(diffattn_paged_decode(&d, &c.pages, ptr(q1), ptr(c.k1), ptr(q2), ptr(c.k2), ptr(c.v), c.table_ptr(),
                                 lengths.const_data_ptr<int32_t>(),
                                 q_lengths.defined() ? q_lengths.const_data_ptr<int32_t>() : nullptr,
-                                static_cast<const uint8_t*>(ptr(mask)), lam, fptr(lam_dev), &e, ptr(out), ws.data_ptr(),
+                                static_cast<const uint8_t*>(ptr(mask)), lam.host, fptr(lam.dev), &e, ptr(out), ws.data_ptr(),
                                 (size_t)ws.numel(), stream_of(dev)),
           "diffattn_paged_decode");
     if (!is_none(a[10])) {
         Py_INCREF(a[10]);
         return a[10];
+    }
+    return THPVariable_Wrap(out);
+}
+
+// ---------------------------------------------------------------------------
+// attention over an encoder's states
+// ---------------------------------------------------------------------------
+const char* const kCross = "differential_cross_attention";
+
+// The autograd node: backward through diffattn_cross_bwd.  Its inputs are q1, k1, q2, k2 (not
+// where it is k1), value, and the coefficient where that is a tensor.
+struct CrossBackward : public torch::autograd::Node {
+    diffattn_cross_desc d{};
+    float host = 0.f;
+    bool shared = false, tensor_lambda = false;
+    torch::autograd::SavedVariable x[5], lam, lens, results[3];     // q1, k1, q2, k2, value; out, out2, lse
+    std::vector<int64_t> lam_shape;
+    std::optional<at::TensorOptions> lam_options;
+    std::optional<at::Device> dev;
+    bool released = false;
+
+    torch::autograd::variable_list apply(torch::autograd::variable_list&& grads) override {
+        std::lock_guard<std::mutex> lock(mutex_);
+        TORCH_CHECK(!released, "differential_cross_attention: backward a second time through a graph whose saved tensors "
+                               "were freed; pass retain_graph=True the first time");
+        TORCH_CHECK(!at::GradMode::is_enabled(), "differential_cross_attention is differentiable once (no create_graph)");
+        TORCH_CHECK(!joins_default_stream(*this), "differential_cross_attention: this captured backward pass would add to the .grad "
+                    "of a leaf that a graph made outside the capture, on the default stream, still holds; drop that graph, "
+                    "or make it on another stream");
+        const int inputs = shared ? 4 : 5;
+        torch::autograd::variable_list result(inputs + tensor_lambda);
+        if (!grads[0].defined()) return result;
+        Tensor t[5];
+        for (int i = 0; i < 5; ++i)
+            if (!(shared && i == 3)) t[i] = inner(x[i].unpack());
+        if (shared) t[3] = t[1];
+        const Tensor out = results[0].unpack(shared_from_this()), out2 = results[1].unpack(), lse = results[2].unpack();
+        const Tensor n = lens.unpack();
+        const Tensor l = tensor_lambda ? lam.unpack() : Tensor();
+        const Tensor l32 = l.defined() && l.is_cuda() ? plain_f32(l) : Tensor();
+        const at::ScalarType type = t[0].scalar_type();
+        const Tensor g = inner(grads[0].scalar_type() == type ? grads[0] : grads[0].to(type));
+        const c10::cuda::OptionalCUDAGuard guard(*dev);
+        diffattn_cross_desc c = d;
+        strides3(c.dout_stride, g);
+        // position of each input among the node's
+        const int at[5] = {0, 1, 2, shared ? 1 : 3, shared ? 3 : 4};
+        Tensor dx[5], dlam;
+        for (int i : {0, 2})
+            if (task_should_compute_output(at[i])) dx[i] = fresh_tensor(t[i].sizes(), type, *dev);
+        if (task_should_compute_output(at[1]) || task_should_compute_output(at[3]) || task_should_compute_output(at[4]))
+            for (int i : {1, 3, 4})
+                if (!(shared && i == 3)) dx[i] = fresh_tensor(t[i].sizes(), type, *dev);
+        if (tensor_lambda && task_should_compute_output(inputs)) dlam = fresh_tensor({}, at::kFloat, *dev);
+        const size_t bytes = diffattn_cross_bwd_workspace_bytes(&c);
+        const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
+        const int rc = diffattn_cross_bwd(&c, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
+                                          n.defined() ? n.const_data_ptr<int32_t>() : nullptr, host, fptr(l32), ptr(out),
+                                          ptr(out2), fptr(lse), ptr(g), ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), ptr(dx[3]),
+                                          ptr(dx[4]), dlam.defined() ? dlam.data_ptr<float>() : nullptr, ws.data_ptr(), bytes,
+                                          stream_of(*dev));
+        TORCH_CHECK(rc == DIFFATTN_OK, "diffattn_cross_bwd: ", diffattn_strerror(rc), " (", rc, ")");
+        for (int i = 0; i < 5; ++i)
+            if (!(shared && i == 3)) result[at[i]] = dx[i];
+        if (dlam.defined()) result[inputs] = dlam.to(*lam_options).view(lam_shape);
+        return result;
+    }
+    void release_variables() override {
+        std::lock_guard<std::mutex> lock(mutex_);
+        for (auto& v : x) v.reset_data();
+        for (auto& v : results) v.reset_data();
+        lam.reset_data();
+        lens.reset_data();
+        released = true;
+    }
+    std::string name() const override { return "CrossAttentionBackward"; }
+};
+
+PyObject* cross(PyObject* const* a) {
+    // q1, k1, q2, k2, value, coefficient, kv_lengths, out, norm, norm_eps, norm_weight, norm_bias, out_scale
+    const bool shared = is_none(a[3]) || a[3] == a[1];
+    Tensor given[5] = {need(a[0], "q1", 4)};
+    const at::Device dev = given[0].device();
+    const at::ScalarType type = given[0].scalar_type();
+    const char* const names[5] = {"q1", "k1", "q2", "k2", "value"};
+    for (int i = 1; i < 5; ++i) given[i] = shared && i == 3 ? given[1] : need(a[i], names[i], 4, type, dev);
+    const Tensor &q1 = given[0], &k1 = given[1], &v = given[4];
+    diffattn_cross_desc d{};
+    d.dtype = dtype_code(q1);
+    d.B = q1.size(0);
+    d.H = q1.size(1);
+    d.Tq = q1.size(2);
+    d.D = q1.size(3);
+    d.Tk = k1.size(2);
+    d.Dv = v.size(3);
+    const int64_t Hk = k1.size(1);
+    if (given[2].sizes() != q1.sizes() || q1.numel() == 0 || d.D > 128)
+        bad_value("q1, q2 must be [B, H, Tq, D] with no size of 0 and D <= 128, got " + text(q1.sizes()) + ", " +
+                  text(given[2].sizes()));
+    if (given[3].sizes() != k1.sizes() || k1.size(0) != d.B || k1.size(3) != d.D || k1.numel() == 0 || d.H % Hk != 0)
+        bad_value("k1, k2 must be [B, H_kv, Tk, D] with H_kv dividing H = " + std::to_string(d.H) + ", got " + text(k1.sizes()) +
+                  ", " + text(given[3].sizes()));
+    if (v.size(0) != d.B || v.size(1) != Hk || v.size(2) != d.Tk || d.Dv < 1 || d.Dv > 256)
+        bad_value("value must be [B, H_kv, Tk, Dv] with Dv <= 256, got " + text(v.sizes()));
+    d.kv_group = (int32_t)(d.H / Hk);
+    const c10::cuda::OptionalCUDAGuard guard(dev);
+    Tensor lens;
+    if (!is_none(a[6])) {
+        lens = need(a[6], "kv_lengths", 1, at::kInt, dev);
+        if (lens.size(0) != d.B) bad_value("kv_lengths must be [B] = (" + std::to_string(d.B) + ",), got " + text(lens.sizes()));
+        if (!lens.is_contiguous()) lens = lens.contiguous();
+    }
+    const Lambda lam(a[5], dev, kCross);
+    no_tangent({&given[0], &given[1], &given[2], &given[3], &given[4]}, kCross);
+    const bool grad = wants_grad({&given[0], &given[1], &given[2], &given[3], &given[4], &lam.given});
+    diffattn_epilogue e{};
+    e.norm = norm_code(a[8], true);
+    e.eps = (float)number(a[9], "norm_eps");
+    e.out_scale = (float)number(a[12], "out_scale");
+    Tensor w_given, b_given;
+    const Tensor w = affine(a[10], "norm_weight", d.H, d.Dv, dev, &w_given);
+    const Tensor b = affine(a[11], "norm_bias", d.H, d.Dv, dev, &b_given);
+    no_tangent({&w_given, &b_given}, kCross);
+    const bool epilogue = e.norm != DIFFATTN_NORM_NONE || w.defined() || b.defined() || e.out_scale != 1.f;
+    if ((grad && (epilogue || !is_none(a[7]))) || wants_grad({&w_given, &b_given}))
+        bad_value("gradients are available for the bare operation only (no out=, norm or out_scale): apply "
+                  "differential_head_norm to its result");
+    e.weight = fptr(w);
+    e.bias = fptr(b);
+    Tensor t[5], out, out2, lse;
+    {
+        at::NoGradGuard no_grad;
+        for (int i = 0; i < 5; ++i) t[i] = shared && i == 3 ? t[1] : inner(given[i]);
+        if (is_none(a[7])) {
+            out = fresh_tensor({d.B, d.H, d.Tq, d.Dv}, type, dev);
+        } else {
+            out = need(a[7], "out", 4, type, dev);
+            if (out.size(0) != d.B || out.size(1) != d.H || out.size(2) != d.Tq || out.size(3) != d.Dv || !inner_ok(out))
+                bad_value("out must be [B, H, Tq, Dv] with a contiguous innermost dimension");
+            no_tangent({&out}, kCross);
+            if (out.requires_grad()) bad_value("out takes no gradient");
+            out.unsafeGetTensorImpl()->bump_version();
+        }
+        strides3(d.q1_stride, t[0]);
+        strides3(d.k1_stride, t[1]);
+        strides3(d.q2_stride, t[2]);
+        strides3(d.k2_stride, t[3]);
+        strides3(d.v_stride, t[4]);
+        strides3(d.o_stride, out);
+        if (grad) {
+            out2 = fresh_tensor(out.sizes(), type, dev);
+            lse = fresh_tensor({d.B, d.H, d.Tq, 2}, at::kFloat, dev);
+        }
+        // from torch's allocator for every call: calls on other streams, and graphs captured one
+        // after another, never share it
+        const size_t bytes = diffattn_cross_workspace_bytes(&d);
+        const Tensor ws = fresh_tensor({(int64_t)(bytes ? bytes : 16)}, at::kByte, dev);
+        check(diffattn_cross_fwd(&d, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
+                                 lens.defined() ? lens.const_data_ptr<int32_t>() : nullptr, lam.host, fptr(lam.dev), &e, ptr(out),
+                                 ptr(out2), lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.numel(),
+                                 stream_of(dev)),
+              "diffattn_cross_fwd");
+    }
+    if (grad) {
+        auto node = std::shared_ptr<CrossBackward>(new CrossBackward(), torch::autograd::deleteNode);
+        torch::autograd::variable_list from;
+        for (int i = 0; i < 5; ++i) {
+            if (shared && i == 3) continue;
+            from.push_back(given[i]);
+            // as the kernels read it: a copy where the innermost dimension was not contiguous
+            node->x[i] = torch::autograd::SavedVariable(t[i], false);
+        }
+        if (lam.given.defined()) {
+            from.push_back(lam.given);
+            node->tensor_lambda = true;
+            node->lam = torch::autograd::SavedVariable(lam.given, false);
+            node->lam_shape = lam.given.sizes().vec();
+            node->lam_options = lam.given.options();
+        }
+        if (lens.defined()) node->lens = torch::autograd::SavedVariable(lens, false);
+        node->d = d;
+        node->host = lam.host;
+        node->shared = shared;
+        node->dev = dev;
+        node->set_next_edges(torch::autograd::collect_next_edges(from));
+        torch::autograd::set_history(out, node);
+        node->results[0] = torch::autograd::SavedVariable(out, true);
+        node->results[1] = torch::autograd::SavedVariable(out2, false);
+        node->results[2] = torch::autograd::SavedVariable(lse, false);
+    }
+    if (!is_none(a[7])) {
+        Py_INCREF(a[7]);
+        return a[7];
     }
     return THPVariable_Wrap(out);
 }
@@ -863,6 +1063,7 @@ PyCFunction as_function(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t))
 
 PyMethodDef methods[] = {
     {"rotary", as_function(entry<rotary, 12>), METH_FASTCALL, nullptr},
+    {"cross", as_function(entry<cross, 13>), METH_FASTCALL, nullptr},
     {"head_norm", as_function(entry<head_norm, 6>), METH_FASTCALL, nullptr},
     {"append", as_function(entry<append, 16>), METH_FASTCALL, nullptr},
     {"attention", as_function(entry<attention, 16>), METH_FASTCALL, nullptr},

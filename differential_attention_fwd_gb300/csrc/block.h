@@ -37,4 +37,50 @@ int launch_head_norm_bwd(const HeadNormParams& p, cudaStream_t stream);
 void plan_head_norm_bwd(HeadNormParams* p);
 size_t head_norm_bwd_floats(int64_t H, int64_t C);
 
+// Attention over an encoder's states, forward and backward.  Gradients are dense: dq
+// [B, H, Tq, D], dk [B, Hk, Tk, D], dv [B, Hk, Tk, Dv].
+struct CrossParams {
+    int B, H, Hk, group, Tq, Tk, D, Dv;
+    int bf16;
+    int k_shared;               // K1 and K2 are one tensor, and dk1 takes both branches' gradient
+    float scale;                // 1 / sqrt(D)
+    float lambda;
+    const float* lambda_dev;
+    const int32_t* lengths;     // [B], nullptr: Tk each
+    uint32_t* status;
+    const void* q1; const void* k1; const void* q2; const void* k2; const void* v;
+    void* out;
+    int64_t s_q1[3], s_k1[3], s_q2[3], s_k2[3], s_v[3], s_o[3];
+    int norm;                   // the output epilogue
+    float norm_eps;
+    const float* norm_weight;
+    const float* norm_bias;
+    float out_scale;
+    void* out2;                 // training: A_2 V with out's strides,
+    float* lse;                 // and [B, H, Tq, 2] log-sum-exps (natural), -inf without a key
+    // backward
+    const void* dout;
+    int64_t s_do[3];
+    void* dq1; void* dq2; void* dk1; void* dk2; void* dv;   // nullptr: not wanted
+    float* stats;               // [B, H, Tq, 4]: log-sum-exps, Dd_1, Dd_2; then 128 floats
+};
+
+#ifdef __CUDACC__
+// A sequence's states, and whether its length is outside 0 .. Tk (then 0 states, and
+// everything of the sequence is NaN).
+struct CrossLen {
+    int n;
+    bool bad;
+};
+__device__ __forceinline__ CrossLen cross_len(const int32_t* lengths, int b, int Tk) {
+    const int n = lengths ? __ldg(lengths + b) : Tk;
+    const bool bad = n < 0 || n > Tk;
+    return {bad ? 0 : n, bad};
+}
+#endif
+
+// The CUDA-core kernels: any D <= 128, Dv <= 256, type and layout.
+int launch_cross_simt(const CrossParams& p, cudaStream_t stream);
+int launch_cross_simt_bwd(const CrossParams& p, cudaStream_t stream);
+
 }  // namespace diffattn

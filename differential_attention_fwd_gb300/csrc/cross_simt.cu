@@ -1,0 +1,530 @@
+// cross_simt.cu -- differential attention over an encoder's states on the CUDA cores,
+// forward and backward: any D <= 128 and Dv <= 256, float32 (exact float32 arithmetic) and
+// bf16, any layout.  Sequence b has its first n_b of Tk states.
+//
+//     S_b = Q_b K_b^T / sqrt(D) over the n states,  A_b = softmax(S_b)
+//     O   = (A_1 - lambda A_2) V                    (a row with no state: 0)
+//     dP  = dO V^T,   Dd_b = rowsum(A_b dP)
+//     dS_1 = A_1 (dP - Dd_1),  dS_2 = -lambda A_2 (dP - Dd_2)
+//     dQ_b = dS_b K_b / sqrt(D),  dK_b = dS_b^T Q_b / sqrt(D),  dV = (A_1 - lambda A_2)^T dO
+//     dlambda = -sum Dd_2
+//
+// Blocks of 256 threads work on tiles of 32 query rows and 32 states in shared memory, in
+// float32: the forward and the dQ kernel walk the states for 32 rows of a head, the dK/dV
+// kernel walks the rows of every query head of its key/value head for 32 states.  A
+// thread's part of each product is a small tile of registers (2 x 4 scores; 2 x 4 to 8 x 4
+// of an output), so that a float4 read of shared memory feeds 5 to 10 multiplications.
+// What lies behind a sequence's states is never read: those rows of the tiles are zeros,
+// and their weights 0.
+//
+// Dd comes from the forward's saved results in float32 (Dd_2 = dO . (A_2 V), Dd_1 = dO .
+// (O + lambda A_2 V)); in bf16 their rounding would stay in every dS of the row, so the dQ
+// kernel walks the states twice and sums A_b dP first.
+#include "block.h"
+#include "kernels.h"
+#include "pdl.cuh"
+#include "rows.cuh"
+
+#include <cmath>
+
+namespace diffattn {
+namespace xsimt {
+
+constexpr int THREADS = 256;
+constexpr int BM = 32;          // query rows of a tile
+constexpr int BN = 32;          // states of a tile
+constexpr int LP = BM + 4;      // row stride of the score tiles
+
+// Sizes by class: 0: D <= 32, Dv <= 64; 1: D <= 64, Dv <= 128; 2: D <= 128, Dv <= 256.
+template <int S>
+struct Size {
+    static constexpr int D = 32 << S, DV = 64 << S;
+    // products of width Dv over all threads: CV threads of NV float4 columns, RV rows each
+    static constexpr int CV = S == 0 ? 16 : 32, NV = DV / 4 / CV, RV = BM / (THREADS / CV);
+    // products of width D, a branch on each half: CD threads of a float4, RD rows each
+    static constexpr int CD = D / 4, RD = BM / (THREADS / 2 / CD);
+};
+
+__host__ __device__ constexpr int padded(int n) { return (n + 3) / 4 * 4 + 4; }
+
+// `count` rows of `width` elements (the rest of 32 rows zeros, and of the padding) into
+// shared memory as floats; a warp a row.
+template <typename T>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t stride, int count, int width) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = warp; r < 32; r += THREADS / 32) {
+        const T* row = src + (int64_t)r * stride;
+        for (int c = lane; c < ld; c += 32) dst[r * ld + c] = r < count && c < width ? Vec<T>::get(row[c]) : 0.f;
+    }
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+}
+
+// Scores of both branches, branch b by half b of the block: dst[branch] is [state][row]
+// where `by_state`, else [row][state].
+__device__ __forceinline__ void scores(const float* q, const float* k, int ld, int D, float* dst, bool by_state) {
+    const int br = threadIdx.x >> 7, t = threadIdx.x & 127, r = t >> 3, c = t & 7;
+    q += br * BM * ld;
+    k += br * BN * ld;
+    float s[2][4] = {};
+    for (int d = 0; d < D; d += 4) {
+        float4 x[2], y[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const float4*>(q + (r + 16 * i) * ld + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(k + (c + 8 * j) * ld + d);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+    }
+    dst += br * BN * LP;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = r + 16 * i, key = c + 8 * j;
+            dst[by_state ? key * LP + row : row * LP + key] = s[i][j];
+        }
+}
+
+// dO V^T of a tile by the whole block, laid out as scores'.
+__device__ __forceinline__ void products(const float* g, const float* v, int ld, int Dv, float* dst, bool by_state) {
+    const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
+    float s[2][2] = {};
+    for (int d = 0; d < Dv; d += 4) {
+        float4 x[2], y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[i] = *reinterpret_cast<const float4*>(g + (r + 16 * i) * ld + d);
+            y[i] = *reinterpret_cast<const float4*>(v + (c + 16 * i) * ld + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = r + 16 * i, key = c + 16 * j;
+            dst[by_state ? key * LP + row : row * LP + key] = s[i][j];
+        }
+}
+
+// acc[i][n] += sum over k < 32 of w[k][r0 + i] x[k][columns of n], w with rows of LP.
+template <int R, int N>
+__device__ __forceinline__ void accumulate(const float* w, int r0, const float* x, int ld, int c0, int step, int width,
+                                           float4 (&acc)[R][N]) {
+    static_assert(R == 2 || R % 4 == 0, "rows of a thread");
+#pragma unroll 4
+    for (int k = 0; k < 32; ++k) {
+        float a[R];
+        if constexpr (R == 2) {
+            const float2 t = *reinterpret_cast<const float2*>(w + k * LP + r0);
+            a[0] = t.x;
+            a[1] = t.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; i += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(w + k * LP + r0 + i);
+                a[i] = t.x;
+                a[i + 1] = t.y;
+                a[i + 2] = t.z;
+                a[i + 3] = t.w;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if (c0 + n * step >= width) break;
+            const float4 y = *reinterpret_cast<const float4*>(x + k * ld + c0 + n * step);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                acc[i][n].x = fmaf(a[i], y.x, acc[i][n].x);
+                acc[i][n].y = fmaf(a[i], y.y, acc[i][n].y);
+                acc[i][n].z = fmaf(a[i], y.z, acc[i][n].z);
+                acc[i][n].w = fmaf(a[i], y.w, acc[i][n].w);
+            }
+        }
+    }
+}
+
+// Four columns of a dense or strided row, as many as there are.
+template <typename T>
+__device__ __forceinline__ void put4(T* row, int c, int width, float4 x, float s) {
+    const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < width) row[c + i] = Vec<T>::put(v[i] * s);
+}
+
+// A block's 32 query rows: batch, head, key/value head and first row.
+struct Rows {
+    int b, h, hk, q0, count;
+};
+__device__ __forceinline__ Rows rows_of(const CrossParams& p) {
+    const int tiles = (p.Tq + BM - 1) / BM;
+    const int bh = blockIdx.x / tiles;
+    Rows r;
+    r.b = bh / p.H;
+    r.h = bh - r.b * p.H;
+    r.hk = r.h / p.group;
+    r.q0 = (blockIdx.x - bh * tiles) * BM;
+    r.count = min(BM, p.Tq - r.q0);
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* head(const void* x, const int64_t (&s)[3], int b, int h) {
+    return static_cast<const T*>(x) + b * s[0] + h * s[1];
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+template <typename T, int S>
+__global__ void __launch_bounds__(THREADS)
+cross_fwd_kernel(const CrossParams p) {
+    using Z = Size<S>;
+    extern __shared__ __align__(16) float sm[];
+    const int ld = padded(p.D), lv = padded(p.Dv);
+    float* qs = sm;                             // [branch][row][ld]
+    float* ks = qs + 2 * BM * ld;               // [branch][state][ld]
+    float* vs = ks + 2 * BN * ld;               // [state][lv]
+    float* ps = vs + BN * lv;                   // [branch][state][LP]
+    float* fix = ps + 2 * BN * LP;              // [branch][row]: the tile's rescaling, then 1 / l
+    pdl_wait();
+    pdl_launch_dependents();
+    const Rows r = rows_of(p);
+    const CrossLen len = cross_len(p.lengths, r.b, p.Tk);
+    if (len.bad && threadIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    load_rows(qs, ld, head<T>(p.q1, p.s_q1, r.b, r.h) + r.q0 * p.s_q1[2], p.s_q1[2], r.count, p.D);
+    load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, r.b, r.h) + r.q0 * p.s_q2[2], p.s_q2[2], r.count, p.D);
+    // the softmax: four threads a row and branch
+    const int br = threadIdx.x >> 7, row = (threadIdx.x >> 2) & 31, sub = threadIdx.x & 3;
+    float m = -INFINITY, l = 0.f;
+    // the output: RV rows by NV float4 columns a thread
+    const int r0 = threadIdx.x / Z::CV * Z::RV, c0 = threadIdx.x % Z::CV * 4;
+    float4 o1[Z::RV][Z::NV] = {}, o2[Z::RV][Z::NV] = {};
+    for (int k0 = 0; k0 < len.n; k0 += BN) {
+        const int live = min(BN, len.n - k0);
+        __syncthreads();                        // the last tile has been read
+        load_rows(ks, ld, head<T>(p.k1, p.s_k1, r.b, r.hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
+        load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, r.b, r.hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
+        load_rows(vs, lv, head<T>(p.v, p.s_v, r.b, r.hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
+        __syncthreads();
+        scores(qs, ks, ld, p.D, ps, true);
+        __syncthreads();
+        {
+            float* w = ps + br * BN * LP + row;
+            float s[8], top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[j] = sub + 4 * j < live ? w[(sub + 4 * j) * LP] * p.scale : -INFINITY;
+                top = fmaxf(top, s[j]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float next = fmaxf(m, top);
+            const float base = next == -INFINITY ? 0.f : next;      // every score so far is -inf
+            const float a = expf(m - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[j] = sub + 4 * j < live ? expf(s[j] - base) : 0.f;
+                sum += s[j];
+                w[(sub + 4 * j) * LP] = s[j];
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            l = l * a + sum;
+            m = next;
+            if (sub == 0) fix[br * BM + row] = a;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < Z::RV; ++i) {
+            const float a1 = fix[r0 + i], a2 = fix[BM + r0 + i];
+#pragma unroll
+            for (int n = 0; n < Z::NV; ++n) {
+                o1[i][n].x *= a1; o1[i][n].y *= a1; o1[i][n].z *= a1; o1[i][n].w *= a1;
+                o2[i][n].x *= a2; o2[i][n].y *= a2; o2[i][n].z *= a2; o2[i][n].w *= a2;
+            }
+        }
+        accumulate<Z::RV, Z::NV>(ps, r0, vs, lv, c0, 4 * Z::CV, p.Dv, o1);
+        accumulate<Z::RV, Z::NV>(ps + BN * LP, r0, vs, lv, c0, 4 * Z::CV, p.Dv, o2);
+    }
+    __syncthreads();
+    const float nan = __int_as_float(0x7fc00000);
+    if (sub == 0) {
+        fix[br * BM + row] = len.bad ? nan : l == 0.f ? 0.f : 1.0f / l;      // no weight at all: 0
+        if (p.lse && row < r.count)
+            p.lse[(((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + row) * 2 + br] = len.bad ? nan : m + logf(l);
+    }
+    __syncthreads();
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    T* out2 = p.out2 ? static_cast<T*>(p.out2) + r.b * p.s_o[0] + r.h * p.s_o[1] + r.q0 * p.s_o[2] : nullptr;
+#pragma unroll
+    for (int i = 0; i < Z::RV; ++i) {
+        const float i1 = fix[r0 + i], i2 = fix[BM + r0 + i];
+#pragma unroll
+        for (int n = 0; n < Z::NV; ++n) {
+            const int c = c0 + n * 4 * Z::CV;
+            if (c >= p.Dv) break;
+            const float4 x = o1[i][n], y = o2[i][n];
+            const float4 b = make_float4(__fmul_rn(y.x, i2), __fmul_rn(y.y, i2), __fmul_rn(y.z, i2), __fmul_rn(y.w, i2));
+            // the branches rounded alike, so that alike branches cancel exactly at lambda = 1
+            *reinterpret_cast<float4*>(vs + (r0 + i) * lv + c) =
+                make_float4(fmaf(-lam, b.x, __fmul_rn(x.x, i1)), fmaf(-lam, b.y, __fmul_rn(x.y, i1)),
+                            fmaf(-lam, b.z, __fmul_rn(x.z, i1)), fmaf(-lam, b.w, __fmul_rn(x.w, i1)));
+            if (out2 && r0 + i < r.count) put4(out2 + (r0 + i) * p.s_o[2], c, p.Dv, b, 1.f);
+        }
+    }
+    __syncthreads();
+    // the epilogue, a warp a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = warp; i < r.count; i += THREADS / 32) {
+        const float* y = vs + i * lv;
+        float mu = 0.f, rs = 1.f;
+        if (p.norm != kNormNone) {
+            if (p.norm == kNormGroup) {
+                float sum = 0.f;
+                for (int c = lane; c < p.Dv; c += 32) sum += y[c];
+                mu = group_sum<32>(sum) / p.Dv;
+            }
+            float ss = 0.f;
+            for (int c = lane; c < p.Dv; c += 32) ss = fmaf(y[c] - mu, y[c] - mu, ss);
+            rs = 1.0f / sqrtf(group_sum<32>(ss) / p.Dv + p.norm_eps);
+        }
+        T* dst = static_cast<T*>(p.out) + r.b * p.s_o[0] + r.h * p.s_o[1] + (r.q0 + i) * p.s_o[2];
+        for (int c = lane; c < p.Dv; c += 32) {
+            float x = (y[c] - mu) * rs;
+            if (p.norm_weight) x *= __ldg(p.norm_weight + (int64_t)r.h * p.Dv + c);
+            if (p.norm_bias) x += __ldg(p.norm_bias + (int64_t)r.h * p.Dv + c);
+            dst[c] = Vec<T>::put(x * p.out_scale);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dQ, and the rows' Dd
+// ---------------------------------------------------------------------------
+template <typename T, int S>
+__global__ void __launch_bounds__(THREADS)
+cross_dq_kernel(const CrossParams p) {
+    using Z = Size<S>;
+    constexpr bool TWICE = sizeof(T) == 2;
+    extern __shared__ __align__(16) float sm[];
+    const int ld = padded(p.D), lv = padded(p.Dv);
+    float* qs = sm;
+    float* gs = qs + 2 * BM * ld;               // [row][lv]
+    float* ks = gs + BM * lv;
+    float* vs = ks + 2 * BN * ld;
+    float* ps = vs + BN * lv;                   // [branch][state][LP]: scores, then dS
+    float* ds = ps + 2 * BN * LP;               // [state][LP]: dP
+    pdl_wait();
+    pdl_launch_dependents();
+    const Rows r = rows_of(p);
+    const CrossLen len = cross_len(p.lengths, r.b, p.Tk);
+    if (len.bad && threadIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    load_rows(qs, ld, head<T>(p.q1, p.s_q1, r.b, r.h) + r.q0 * p.s_q1[2], p.s_q1[2], r.count, p.D);
+    load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, r.b, r.h) + r.q0 * p.s_q2[2], p.s_q2[2], r.count, p.D);
+    load_rows(gs, lv, head<T>(p.dout, p.s_do, r.b, r.h) + r.q0 * p.s_do[2], p.s_do[2], r.count, p.Dv);
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const int br = threadIdx.x >> 7, row = (threadIdx.x >> 2) & 31, sub = threadIdx.x & 3;
+    const int64_t at = ((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + row;
+    const float lse = row < r.count ? p.lse[at * 2 + br] : 0.f;
+    float dd = 0.f;
+    if (!TWICE && row < r.count && len.n > 0) {
+        // from the saved results, four threads a row
+        const int64_t o = r.b * p.s_o[0] + r.h * p.s_o[1] + (r.q0 + row) * p.s_o[2];
+        const T* o1 = static_cast<const T*>(p.out) + o;
+        const T* o2 = static_cast<const T*>(p.out2) + o;
+        const T* g = head<T>(p.dout, p.s_do, r.b, r.h) + (r.q0 + row) * p.s_do[2];
+        for (int c = sub; c < p.Dv; c += 4) {
+            const float x = Vec<T>::get(o2[c]);
+            dd = fmaf(Vec<T>::get(g[c]), br ? x : fmaf(lam, x, Vec<T>::get(o1[c])), dd);
+        }
+    }
+    if (!TWICE) {
+        dd += __shfl_xor_sync(0xffffffffu, dd, 1);
+        dd += __shfl_xor_sync(0xffffffffu, dd, 2);
+    }
+    const int half = threadIdx.x & 127, r0 = half / Z::CD * Z::RD, c0 = half % Z::CD * 4;
+    float4 acc[Z::RD][1] = {};
+    for (int sweep = TWICE ? 0 : 1; sweep < 2; ++sweep) {
+        for (int k0 = 0; k0 < len.n; k0 += BN) {
+            const int live = min(BN, len.n - k0);
+            __syncthreads();
+            load_rows(ks, ld, head<T>(p.k1, p.s_k1, r.b, r.hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
+            load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, r.b, r.hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
+            load_rows(vs, lv, head<T>(p.v, p.s_v, r.b, r.hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
+            __syncthreads();
+            scores(qs, ks, ld, p.D, ps, true);
+            products(gs, vs, lv, p.Dv, ds, true);
+            __syncthreads();
+            float* w = ps + br * BN * LP + row;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int key = sub + 4 * j;
+                const float a = key < live && row < r.count ? expf(w[key * LP] * p.scale - lse) : 0.f;
+                const float dp = ds[key * LP + row];
+                if (sweep == 0) dd = fmaf(a, dp, dd);
+                else w[key * LP] = (br ? -lam : 1.f) * a * (dp - dd);
+            }
+            if (sweep == 0) continue;
+            __syncthreads();
+            accumulate<Z::RD, 1>(ps + br * BN * LP, r0, ks + br * BN * ld, ld, c0, 0, p.D, acc);
+        }
+        if (sweep == 0) {
+            dd += __shfl_xor_sync(0xffffffffu, dd, 1);
+            dd += __shfl_xor_sync(0xffffffffu, dd, 2);
+        }
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    if (sub == 0 && row < r.count) {
+        p.stats[at * 4 + br] = lse;
+        p.stats[at * 4 + 2 + br] = len.bad ? nan : dd;
+    }
+    T* dq = static_cast<T*>(br ? p.dq2 : p.dq1);
+    if (!dq || c0 >= p.D) return;
+#pragma unroll
+    for (int i = 0; i < Z::RD; ++i)
+        if (r0 + i < r.count)
+            put4(dq + (((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + r0 + i) * p.D, c0, p.D, acc[i][0], len.bad ? nan : p.scale);
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV
+// ---------------------------------------------------------------------------
+template <typename T, int S>
+__global__ void __launch_bounds__(THREADS)
+cross_dkdv_kernel(const CrossParams p) {
+    using Z = Size<S>;
+    extern __shared__ __align__(16) float sm[];
+    const int ld = padded(p.D), lv = padded(p.Dv);
+    float* qs = sm;
+    float* gs = qs + 2 * BM * ld;
+    float* ks = gs + BM * lv;
+    float* vs = ks + 2 * BN * ld;
+    float* ps = vs + BN * lv;                   // [branch][row][LP]: scores, then dS
+    float* ds = ps + 2 * BM * LP;               // [row][LP]: dP, then W = A_1 - lambda A_2
+    const int tiles = (p.Tk + BN - 1) / BN;
+    const int bh = blockIdx.x / tiles, b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int k0 = (blockIdx.x - bh * tiles) * BN, count = min(BN, p.Tk - k0);
+    pdl_wait();
+    pdl_launch_dependents();
+    const CrossLen len = cross_len(p.lengths, b, p.Tk);
+    const int live = max(0, min(count, len.n - k0));
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const int half = threadIdx.x & 127, br = threadIdx.x >> 7;
+    const int rd = half / Z::CD * Z::RD, cd = half % Z::CD * 4;
+    const int rv = threadIdx.x / Z::CV * Z::RV, cv = threadIdx.x % Z::CV * 4;
+    float4 dk[Z::RD][1] = {}, dv[Z::RV][Z::NV] = {};
+    if (live > 0) {
+        load_rows(ks, ld, head<T>(p.k1, p.s_k1, b, hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
+        load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, b, hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
+        load_rows(vs, lv, head<T>(p.v, p.s_v, b, hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
+        for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+            for (int q0 = 0; q0 < p.Tq; q0 += BM) {
+                const int rows = min(BM, p.Tq - q0);
+                __syncthreads();
+                load_rows(qs, ld, head<T>(p.q1, p.s_q1, b, h) + q0 * p.s_q1[2], p.s_q1[2], rows, p.D);
+                load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, b, h) + q0 * p.s_q2[2], p.s_q2[2], rows, p.D);
+                load_rows(gs, lv, head<T>(p.dout, p.s_do, b, h) + q0 * p.s_do[2], p.s_do[2], rows, p.Dv);
+                __syncthreads();
+                scores(qs, ks, ld, p.D, ps, false);
+                products(gs, vs, lv, p.Dv, ds, false);
+                __syncthreads();
+                const int row = threadIdx.x >> 3;
+                float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row < rows)
+                    st = *reinterpret_cast<const float4*>(p.stats + (((int64_t)b * p.H + h) * p.Tq + q0 + row) * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = (threadIdx.x & 7) + 8 * j, i = row * LP + key;
+                    const bool seen = row < rows && key < live;
+                    const float a1 = seen ? expf(ps[i] * p.scale - st.x) : 0.f;
+                    const float a2 = seen ? lam * expf(ps[BM * LP + i] * p.scale - st.y) : 0.f;
+                    const float dp = ds[i];
+                    ps[i] = a1 * (dp - st.z);
+                    ps[BM * LP + i] = -a2 * (dp - st.w);
+                    ds[i] = a1 - a2;
+                }
+                __syncthreads();
+                accumulate<Z::RV, Z::NV>(ds, rv, gs, lv, cv, 4 * Z::CV, p.Dv, dv);
+                accumulate<Z::RD, 1>(ps + br * BM * LP, rd, qs + br * BM * ld, ld, cd, 0, p.D, dk);
+            }
+        }
+    }
+    const float fill = len.bad ? __int_as_float(0x7fc00000) : 1.f;
+    const int64_t at = ((int64_t)b * p.Hk + hk) * p.Tk + k0;
+#pragma unroll
+    for (int i = 0; i < Z::RV; ++i)
+#pragma unroll
+        for (int n = 0; n < Z::NV; ++n)
+            if (rv + i < count && cv + n * 4 * Z::CV < p.Dv)
+                put4(static_cast<T*>(p.dv) + (at + rv + i) * p.Dv, cv + n * 4 * Z::CV, p.Dv, dv[i][n], fill);
+    if (p.k_shared) {                           // one tensor: the branches' gradients before the rounding
+        __syncthreads();
+        if (br == 1 && cd < p.D)
+#pragma unroll
+            for (int i = 0; i < Z::RD; ++i) *reinterpret_cast<float4*>(qs + (rd + i) * ld + cd) = dk[i][0];
+        __syncthreads();
+        if (br == 0 && cd < p.D)
+#pragma unroll
+            for (int i = 0; i < Z::RD; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(qs + (rd + i) * ld + cd);
+                dk[i][0] = make_float4(dk[i][0].x + x.x, dk[i][0].y + x.y, dk[i][0].z + x.z, dk[i][0].w + x.w);
+            }
+        if (br == 1) return;
+    }
+    if (cd >= p.D) return;
+#pragma unroll
+    for (int i = 0; i < Z::RD; ++i)
+        if (rd + i < count)
+            put4(static_cast<T*>(br ? p.dk2 : p.dk1) + (at + rd + i) * p.D, cd, p.D, dk[i][0], fill * p.scale);
+}
+
+template <typename K>
+int launch_smem(K kernel, int64_t blocks, int floats, const CrossParams& p, cudaStream_t stream) {
+    if (blocks > INT32_MAX ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, floats * 4) != cudaSuccess)
+        return -1;
+    return pdl_launch(kernel, dim3((unsigned)blocks), THREADS, (size_t)floats * 4, stream, p);
+}
+
+template <typename T, int S>
+int launch(const CrossParams& p, bool backward, cudaStream_t stream) {
+    const int ld = padded(p.D), lv = padded(p.Dv);
+    const int64_t row_blocks = (int64_t)p.B * p.H * ((p.Tq + BM - 1) / BM);
+    if (!backward)
+        return launch_smem(cross_fwd_kernel<T, S>, row_blocks, 2 * BM * ld + 2 * BN * ld + BN * lv + 2 * BN * LP + 2 * BM, p, stream);
+    const int floats = 2 * BM * ld + BM * lv + 2 * BN * ld + BN * lv + 3 * BN * LP;
+    if (launch_smem(cross_dq_kernel<T, S>, row_blocks, floats, p, stream) != 0) return -1;
+    if (!p.dv) return 0;
+    return launch_smem(cross_dkdv_kernel<T, S>, (int64_t)p.B * p.Hk * ((p.Tk + BN - 1) / BN), floats, p, stream);
+}
+
+template <typename T>
+int launch_type(const CrossParams& p, bool backward, cudaStream_t stream) {
+    if (p.D <= 32 && p.Dv <= 64) return launch<T, 0>(p, backward, stream);
+    if (p.D <= 64 && p.Dv <= 128) return launch<T, 1>(p, backward, stream);
+    return launch<T, 2>(p, backward, stream);
+}
+
+}  // namespace xsimt
+
+int launch_cross_simt(const CrossParams& p, cudaStream_t stream) {
+    return p.bf16 ? xsimt::launch_type<__nv_bfloat16>(p, false, stream) : xsimt::launch_type<float>(p, false, stream);
+}
+
+int launch_cross_simt_bwd(const CrossParams& p, cudaStream_t stream) {
+    return p.bf16 ? xsimt::launch_type<__nv_bfloat16>(p, true, stream) : xsimt::launch_type<float>(p, true, stream);
+}
+
+}  // namespace diffattn

@@ -644,6 +644,75 @@ int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages 
                           void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
 
 /*
+ * Attention over an encoder's states (cross attention): queries of one sequence over keys
+ * and values of another, of another length, without a causal mask,
+ *
+ *     O = (softmax(Q1 K1^T / sqrt(D)) - lambda softmax(Q2 K2^T / sqrt(D))) V
+ *
+ * over the first kv_lengths[b] of the Tk states of sequence b.  The others (a batch's
+ * padding) are not looked at, NaN and infinities included; a sequence without a state
+ * (length 0) gives zeros.
+ *
+ * Q1, Q2: [B, H, Tq, D]; K1, K2: [B, H / kv_group, Tk, D]; V: [B, H / kv_group, Tk, Dv];
+ * O: [B, H, Tq, Dv].  D <= 128, Dv <= 256 (0: 2D), dtype, kv_group as in diffattn_desc;
+ * *_stride: element strides of B, heads and rows (innermost 1; >= 0); o_stride of O (and
+ * of out2), dout_stride of its gradient (the backward only).
+ */
+typedef struct {
+    int64_t B, H, Tq, Tk, D, Dv;
+    int32_t dtype;
+    int32_t kv_group;
+    int64_t q1_stride[3], k1_stride[3], q2_stride[3], k2_stride[3], v_stride[3];
+    int64_t o_stride[3], dout_stride[3];
+} diffattn_cross_desc;
+
+/* Bytes of workspace diffattn_cross_fwd and diffattn_cross_bwd need, 0 for an invalid
+ * descriptor. */
+size_t diffattn_cross_workspace_bytes(const diffattn_cross_desc *desc);
+size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc *desc);
+
+/*
+ * diffattn_cross_fwd -- the forward.  kv_lengths: device int32 [B], or NULL (Tk each).  A
+ * length outside 0 .. Tk gives that sequence rows of NaN and is recorded
+ * (DIFFATTN_ERR_INDEX from diffattn_get_device_error); nothing outside the tensors is read.
+ * lambda, lambda_dev, epi as diffattn_decode.
+ * For a training step: out2 (A_2 V, dtype and strides of O; 0 without a state) and lse
+ * (float32 [B, H, Tq, 2], each branch's natural-log log-sum-exp of the scaled scores, -inf
+ * without a state), both or neither, and then no epilogue.
+ * O and out2 must not overlap the inputs.
+ * workspace: at least diffattn_cross_workspace_bytes bytes, 16-byte aligned, no
+ * initialisation needed; calls that may run at the same time use different ones.
+ * Errors: DIFFATTN_ERR_INVALID (NULL pointers, sizes, strides, dtype, kv_group, a stride
+ * of 0 between rows of O, non-finite lambda, bad epilogue, an epilogue with the training
+ * outputs, a missing, small or misaligned workspace); DIFFATTN_ERR_UNSUPPORTED (sizes
+ * beyond the int32 index range); DIFFATTN_ERR_CUDA.
+ */
+int diffattn_cross_fwd(const diffattn_cross_desc *desc, const void *q1, const void *k1,
+                       const void *q2, const void *k2, const void *v,
+                       const int32_t *kv_lengths, float lambda, const float *lambda_dev,
+                       const diffattn_epilogue *epi, void *out, void *out2, float *lse,
+                       void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
+
+/*
+ * diffattn_cross_bwd -- gradients, given dout = dL/dO and the training forward's results
+ * (out, out2, lse) for the same inputs.  dq1, dq2 [B, H, Tq, D], dk1, dk2 [B, Hk, Tk, D], dv
+ * [B, Hk, Tk, Dv]: dense, of the inputs' dtype, overwritten; rows of states that a sequence
+ * does not have are zeros.  dlambda: one float.  dq1, dq2 and dlambda are NULL where not
+ * wanted, and dk1, dk2 and dv all are or none is -- but dk2 alone may be NULL where K2 is
+ * K1 (the same pointer and strides): then dk1 takes both branches' gradient, summed before
+ * the rounding.  No atomics: the result is reproducible bit for bit.  A length outside 0 ..
+ * Tk gives that sequence gradients of NaN, and is recorded.
+ * workspace: at least diffattn_cross_bwd_workspace_bytes bytes, as above.  Errors as
+ * diffattn_cross_fwd.
+ */
+int diffattn_cross_bwd(const diffattn_cross_desc *desc, const void *q1, const void *k1,
+                       const void *q2, const void *k2, const void *v,
+                       const int32_t *kv_lengths, float lambda, const float *lambda_dev,
+                       const void *out, const void *out2, const float *lse, const void *dout,
+                       void *dq1, void *dk1, void *dq2, void *dk2, void *dv, float *dlambda,
+                       void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
+
+/*
  * The norm of each head's output: the epilogue above as an operator of its own, with
  * its gradients.  For a row x of C channels (1 .. 256) of head h, with mu = mean(x)
  * (DIFFATTN_NORM_GROUP) or 0 (DIFFATTN_NORM_RMS), r = (mean((x - mu)^2) + eps)^-1/2,

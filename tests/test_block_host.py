@@ -99,7 +99,93 @@ def test_norm_reference_gradients(group):
         torch.testing.assert_close(differences(f, t, dy), want, rtol=0, atol=1e-7)
 
 
+# ------------------------------------------------------------------ cross attention
+def cross_desc(**kw):
+    d = _lib.DiffattnCrossDesc()
+    d.B, d.H, d.Tq, d.Tk, d.D, d.Dv, d.dtype, d.kv_group = 2, 4, 5, 7, 64, 128, 0, 2
+    for f, rows, width in (("q1_stride", 5, 64), ("q2_stride", 5, 64), ("k1_stride", 7, 64), ("k2_stride", 7, 64),
+                           ("v_stride", 7, 128), ("o_stride", 5, 128), ("dout_stride", 5, 128)):
+        heads = 4 if rows == 5 else 2
+        getattr(d, f)[:] = (heads * rows * width, rows * width, width)
+    return fill(d, **kw)
+
+
+def cross_fwd(lib, d=None, lam=0.5, epi=None, out2=None, lse=None, ws=p(40), n=1 << 30, **miss):
+    a = dict(q1=p(0), k1=p(1), q2=p(2), k2=p(3), v=p(4), out=p(5))
+    a.update(miss)
+    return lib.diffattn_cross_fwd(ctypes.byref(d or cross_desc()), a["q1"], a["k1"], a["q2"], a["k2"], a["v"], None, lam, None,
+                                  None if epi is None else ctypes.byref(epi), a["out"], out2, lse, ws, n, None)
+
+
+def cross_bwd(lib, d=None, lam=0.5, ws=p(40), n=1 << 30, **other):
+    a = dict(q1=p(0), k1=p(1), q2=p(2), k2=p(3), v=p(4), out=p(5), out2=p(6), lse=p(7), dout=p(8), dq1=p(9), dk1=p(10),
+             dq2=p(11), dk2=p(12), dv=p(13), dlam=p(14))
+    a.update(other)
+    return lib.diffattn_cross_bwd(ctypes.byref(d or cross_desc()), a["q1"], a["k1"], a["q2"], a["k2"], a["v"], None, lam, None,
+                                  a["out"], a["out2"], a["lse"], a["dout"], a["dq1"], a["dk1"], a["dq2"], a["dk2"], a["dv"],
+                                  a["dlam"], ws, n, None)
+
+
+def test_cross_descriptor_layout():
+    C = _lib.DiffattnCrossDesc
+    assert ctypes.sizeof(C) == 6 * 8 + 2 * 4 + 7 * 3 * 8 and C.q1_stride.offset == 56
+
+
+BAD_CROSS = [dict(B=0), dict(H=0), dict(Tq=0), dict(Tk=0), dict(D=0), dict(D=129), dict(Dv=-1), dict(Dv=257), dict(dtype=2),
+             dict(kv_group=-1), dict(kv_group=3), dict(q1_stride=(-1, 0, 0)), dict(k2_stride=(0, -1, 0)), dict(v_stride=(0, 0, -1)),
+             dict(dout_stride=(-1, 0, 0))]
+
+
+@pytest.mark.parametrize("kw", BAD_CROSS)
+def test_cross_refusals(lib, kw):
+    d = cross_desc(**kw)
+    assert cross_fwd(lib, d) == INVALID and cross_bwd(lib, d) == INVALID
+    assert lib.diffattn_cross_workspace_bytes(ctypes.byref(d)) == 0
+    assert lib.diffattn_cross_bwd_workspace_bytes(ctypes.byref(d)) == 0
+
+
+def test_cross_argument_refusals(lib):
+    for miss in ("q1", "k1", "q2", "k2", "v", "out"):
+        assert cross_fwd(lib, **{miss: None}) == INVALID and cross_bwd(lib, **{miss: None}) == INVALID
+    for miss in ("out2", "lse", "dout", "dk1", "dv"):
+        assert cross_bwd(lib, **{miss: None}) == INVALID
+    assert cross_bwd(lib, dk2=None) == INVALID                          # two key tensors, one gradient
+    assert cross_bwd(lib, dq1=None, dq2=None, dk1=None, dk2=None, dv=None, dlam=None) == INVALID
+    assert cross_fwd(lib, out2=p(6)) == INVALID and cross_fwd(lib, lse=p(7)) == INVALID
+    assert cross_fwd(lib, lam=float("nan")) == INVALID and cross_bwd(lib, lam=float("inf")) == INVALID
+    for epi in (_lib.DiffattnEpilogue(norm=1, eps=1e-5, out_scale=1.0), _lib.DiffattnEpilogue(out_scale=0.5)):
+        assert cross_fwd(lib, epi=epi, out2=p(6), lse=p(7)) == INVALID
+    assert cross_fwd(lib, epi=_lib.DiffattnEpilogue(norm=9, eps=1e-5, out_scale=1.0)) == INVALID
+    assert cross_fwd(lib, cross_desc(o_stride=(0, 640, 128))) == INVALID
+    need = lib.diffattn_cross_bwd_workspace_bytes(ctypes.byref(cross_desc()))
+    assert need >= 2 * 4 * 5 * 16
+    for f in (cross_fwd, cross_bwd):
+        assert f(lib, ws=None) == INVALID and f(lib, ws=p(40) + 8) == INVALID and f(lib, n=0) == INVALID
+    assert cross_bwd(lib, n=need - 1) == INVALID
+    for big in (dict(Tq=1 << 31), dict(Tk=1 << 31), dict(B=1 << 20, Tq=1 << 18)):
+        assert cross_fwd(lib, cross_desc(**big)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("lens", [[4, 2], [3, 0]])
+def test_cross_reference_gradients(lens):
+    g = torch.Generator().manual_seed(1)
+    q1, q2 = (torch.randn(2, 4, 3, 5, generator=g, dtype=torch.float64) for _ in range(2))
+    k1, k2 = (torch.randn(2, 2, 4, 5, generator=g, dtype=torch.float64) for _ in range(2))
+    v, do = torch.randn(2, 2, 4, 6, generator=g, dtype=torch.float64), torch.randn(2, 4, 3, 6, generator=g, dtype=torch.float64)
+    x = [q1, k1, q2, k2, v]
+    lam = torch.tensor(0.7, dtype=torch.float64)
+    f = lambda: ref.Cross(*x, lam, lens, ref.U).o                      # noqa: E731
+    got = ref.Cross(*x, lam, lens, ref.U).backward(do)
+    for t, name in list(zip(x, ("q1", "k1", "q2", "k2", "v"))) + [(lam, "lam")]:
+        torch.testing.assert_close(differences(f, t, do), got[name][0], rtol=0, atol=1e-7)
+    k2.copy_(k1)                                                       # one key tensor: moved together
+    x[3] = k1
+    torch.testing.assert_close(differences(f, k1, do), ref.Cross(*x, lam, lens, ref.U).backward(do)["k"][0], rtol=0, atol=1e-7)
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(1, 2, 3, 64)
+    with pytest.raises(ValueError, match="no CPU path"):
+        da.differential_cross_attention(x, x, x, x, x, 0.5)
     with pytest.raises(ValueError, match="no CPU path"):
         da.differential_head_norm(x)

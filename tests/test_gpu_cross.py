@@ -1,0 +1,408 @@
+"""GPU tests of differential_cross_attention, forward and backward, against its formulas in
+float64.  tests/block_reference.py derives each element's bound."""
+import pytest
+import torch
+
+import differential_attention_fwd_gb300 as da
+from differential_attention_fwd_gb300 import build as build_mod
+from tests import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+H_OF = {torch.bfloat16: 2.0 ** -8, torch.float32: ref.U}
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build_mod.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    da.get_device_error()
+    yield
+    assert da.get_device_error() == 0
+
+
+def d64(t):
+    return t.detach().cpu().double()
+
+
+def check(name, got, want, tol):
+    got = d64(got)
+    assert got.shape == want.shape, name
+    worst = ((got - want).abs() - tol - 1e-30).max()
+    assert not worst > 0 and not got.isnan().any(), f"{name}: {worst.item():.3g} beyond its bound"
+
+
+def inputs(seed, dtype, B, H, Hk, Tq, Tk, D, Dv, shared, lens=None, layout="dense", poison=True):
+    """q1, k1, q2, k2, v and kv_lengths; NaN and infinities behind each sequence's states."""
+    g = torch.Generator().manual_seed(seed)
+
+    def rows(heads, T, width):
+        t = torch.randn(B, heads, T, width, generator=g).to(dtype).cuda()
+        if layout == "token":                       # [B, T, heads, width] seen as [B, heads, T, width]
+            t = t.transpose(1, 2).contiguous().transpose(1, 2)
+        if layout == "odd":                         # a row stride that no vector load takes
+            big = torch.full((B, heads, T, width + 1), float("nan"), dtype=dtype, device="cuda")
+            big[..., :width] = t
+            t = big[..., :width]
+        return t
+    x = [rows(H, Tq, D), rows(Hk, Tk, D), rows(H, Tq, D), None, rows(Hk, Tk, Dv)]
+    x[3] = x[1] if shared else rows(Hk, Tk, D)
+    n = None
+    if lens is not None:
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for t in {id(t): t for t in (x[1], x[3], x[4])}.values():
+            for b, k in enumerate(lens):
+                if poison and k < Tk:
+                    t[b, :, k:] = float("nan")
+                    t[b, :, k::2] = float("inf")
+    return x, n
+
+
+def reference(x, lam, lens, saved=True):
+    clean = [torch.nan_to_num(d64(t), 0.0, 0.0, 0.0) for t in x]
+    return ref.Cross(*clean, lam, lens or [x[1].shape[2]] * x[1].shape[0], H_OF[x[0].dtype], saved)
+
+
+def train(x, n, lam, do):
+    leaves = [x[0], x[1], x[2]] + ([] if x[3] is x[1] else [x[3]]) + [x[4]]
+    for t in leaves:
+        t.requires_grad_()
+    lam_t = torch.tensor(lam, device="cuda", requires_grad=True)
+    o = da.differential_cross_attention(*x, lam_t, kv_lengths=n)
+    grads = torch.autograd.grad(o, leaves + [lam_t], do)
+    names = ["q1", "k1", "q2"] + ([] if x[3] is x[1] else ["k2"]) + ["v", "lam"]
+    for t in leaves:
+        t.requires_grad_(False)
+    return o.detach(), dict(zip(names, grads))
+
+
+def compare(x, n, lens, lam, seed=0):
+    g = torch.Generator().manual_seed(seed + 99)
+    B, H, Tq, _ = x[0].shape
+    do = torch.randn(B, H, Tq, x[4].shape[3], generator=g).to(x[0].dtype).cuda()
+    lam = float(torch.tensor(lam, dtype=torch.float32))
+    o, grads = train(x, n, lam, do)
+    with torch.no_grad():
+        served = da.differential_cross_attention(*x, lam, kv_lengths=n)
+    want = reference(x, lam, lens)
+    check("o", o, want.o, want.o_tol)
+    check("served o", served, want.o, want.o_tol)
+    back = want.backward(d64(do))
+    if x[3] is x[1]:
+        back["k1"] = back["k"]
+    for name, got in grads.items():
+        check("d" + name, got, *back[name])
+    for b, k in enumerate(lens or []):              # states that are not there, and rows over none
+        for name in ("k1", "k2", "v"):
+            assert name not in grads or not grads[name][b, :, k:].any()
+        if k == 0:
+            assert not o[b].any() and not served[b].any() and not grads["q1"][b].any() and not grads["q2"][b].any()
+    return o, served, grads
+
+
+WIDE = [(BF, 64, 128), (BF, 128, 128), (F32, 32, 64), (F32, 64, 128), (F32, 128, 256), (BF, 32, 64), (BF, 48, 30),
+        (F32, 10, 7), (BF, 128, 256), (F32, 1, 1), (BF, 64, 64)]
+
+
+@pytest.mark.parametrize("dtype,D,Dv", WIDE)
+@pytest.mark.parametrize("shared", [False, True])
+def test_widths(dtype, D, Dv, shared):
+    lens = [75, 0, 33]
+    x, n = inputs(D + Dv, dtype, 3, 4, 2, 41, 75, D, Dv, shared, lens)
+    compare(x, n, lens, 0.8)
+
+
+@pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 64, 128, True), (BF, 128, 128, True), (F32, 32, 64, False)])
+@pytest.mark.parametrize("Tq,Tk,lens", [
+    (1, 1, [1, 1]), (1, 77, None), (3, 64, [64, 63]), (130, 5, [5, 1]), (128, 128, [128, 65]), (257, 65, [1, 64]),
+    (7, 300, [300, 129]), (300, 513, [512, 0]), (64, 64, None), (129, 200, [0, 0])])
+def test_lengths(dtype, D, Dv, shared, Tq, Tk, lens):
+    x, n = inputs(Tq + Tk, dtype, 2, 4, 4, Tq, Tk, D, Dv, shared, lens)
+    compare(x, n, lens, 0.3)
+
+
+@pytest.mark.parametrize("H,Hk", [(1, 1), (3, 1), (6, 3), (16, 2)])
+@pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 128, 128, True), (F32, 64, 128, False)])
+@pytest.mark.parametrize("Tq", [1, 70])
+def test_grouped_heads(H, Hk, dtype, D, Dv, shared, Tq):
+    lens = [130, 200]
+    x, n = inputs(H, dtype, 2, H, Hk, Tq, 200, D, Dv, shared, lens)
+    compare(x, n, lens, 0.8)
+
+
+@pytest.mark.parametrize("layout", ["token", "odd"])
+@pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 128, 128, True), (F32, 64, 128, False)])
+def test_layouts(layout, dtype, D, Dv, shared):
+    lens = [90, 17]
+    x, n = inputs(3, dtype, 2, 4, 2, 40, 90, D, Dv, shared, lens, layout)
+    compare(x, n, lens, 0.8)
+
+
+@pytest.mark.parametrize("lam", [0.0, 1.0, -0.35, 1.7])
+def test_coefficients(lam):
+    lens = [90, 64]
+    x, n = inputs(4, BF, 2, 4, 2, 40, 90, 64, 128, False, lens)
+    compare(x, n, lens, lam)
+
+
+@pytest.mark.parametrize("dtype,D,Dv", [(BF, 64, 128), (BF, 128, 128), (F32, 64, 128)])
+@pytest.mark.parametrize("Tq", [1, 20, 200])
+def test_alike_branches_cancel(dtype, D, Dv, Tq):
+    x, n = inputs(5, dtype, 2, 4, 2, Tq, 150, D, Dv, True, [150, 31])
+    x[2] = x[0]
+    with torch.no_grad():
+        assert not da.differential_cross_attention(*x, 1.0, kv_lengths=n).any()
+    o, _ = train([x[0], x[1], x[0].clone(), x[1], x[4]], n, 1.0, torch.ones(2, 4, Tq, Dv, dtype=dtype, device="cuda"))
+    assert not o.any()
+
+
+@pytest.mark.parametrize("dtype,D,Dv", [(BF, 64, 128), (F32, 64, 128), (BF, 128, 128)])
+@pytest.mark.parametrize("norm", ["rms", "group", None])
+@pytest.mark.parametrize("Tq", [1, 33, 260])
+def test_epilogue(dtype, D, Dv, norm, Tq):
+    """The fused norm, weight, bias and scale, from the reference's O: its bound goes through
+    the norm, whose own roundings are K = 32 U (as in the head norm's tests)."""
+    lens = [100, 0, 64]
+    x, n = inputs(6, dtype, 3, 4, 2, Tq, 100, D, Dv, True, lens)
+    g = torch.Generator().manual_seed(7)
+    w, b = (1 + 0.2 * torch.randn(4, Dv, generator=g)), 0.2 * torch.randn(4, Dv, generator=g)
+    eps = 1e-3
+    kw = {} if norm is None else dict(norm=norm, norm_eps=eps)
+    with torch.no_grad():
+        y = da.differential_cross_attention(*x, 0.8, kv_lengths=n, norm_weight=w.cuda(), norm_bias=b.cuda(), out_scale=0.2, **kw)
+    r = reference(x, float(torch.tensor(0.8)), lens)
+    w, b = w.double()[:, None], b.double()[:, None]
+    tol = r.o_tol - r.h * r.o.abs()                         # O is not rounded on the way
+    o = r.o
+    if norm is not None:
+        if norm == "group":
+            tol = tol + tol.mean(-1, keepdim=True)
+            o = o - o.mean(-1, keepdim=True)
+        rs = (o.pow(2).mean(-1, keepdim=True) + eps).rsqrt()
+        # h = o rs: its own error, and rs's through the mean square: d rs = rs^3 mean(o d o)
+        hat = o * rs
+        tol = rs * tol + hat.abs() * rs * rs * (o.abs() * tol).mean(-1, keepdim=True) + 32 * ref.U * (hat.abs() + r.o.abs().mean(-1, keepdim=True) * rs)
+        # second order: the bound holds where a row's error is small beside its size
+        tol = 1.5 * tol
+        o = hat
+    want = 0.2 * (o * w + b)
+    check("y", y, want, 0.2 * (w.abs() * tol + 4 * ref.U * (b.abs() + (o * w).abs())) + r.h * want.abs())
+
+
+def test_one_answer_for_full_lengths_and_none():
+    for dtype, D, Dv in ((BF, 64, 128), (F32, 64, 128)):
+        for Tq in (1, 40):
+            x, _ = inputs(8, dtype, 2, 4, 2, Tq, 90, D, Dv, False)
+            full = torch.full((2,), 90, dtype=torch.int32, device="cuda")
+            with torch.no_grad():
+                assert torch.equal(da.differential_cross_attention(*x, 0.8), da.differential_cross_attention(*x, 0.8, full))
+                lens = torch.tensor([90, 0, 0, 90], dtype=torch.int32, device="cuda")[::3]      # not contiguous
+                assert torch.equal(da.differential_cross_attention(*x, 0.8), da.differential_cross_attention(*x, 0.8, lens))
+
+
+@pytest.mark.parametrize("dtype,D,Dv", [(BF, 64, 128), (F32, 64, 128), (BF, 128, 128)])
+@pytest.mark.parametrize("Tq", [1, 40, 200])
+def test_lengths_out_of_range(dtype, D, Dv, Tq):
+    """A bad length: that sequence alone is NaN, and it is reported."""
+    x, _ = inputs(9, dtype, 4, 4, 2, Tq, 90, D, Dv, True)
+    good, bad = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([50, 90, 7, 90], [50, 91, 7, -1]))
+    do = torch.randn(4, 4, Tq, Dv, device="cuda").to(dtype)
+    want, wg = train(x, good, 0.8, do)
+    with torch.no_grad():
+        served = da.differential_cross_attention(*x, 0.8, kv_lengths=good)
+    assert da.get_device_error() == 0
+    got, gg = train(x, bad, 0.8, do)
+    assert da.get_device_error() == da._lib.DIFFATTN_ERR_INDEX
+    with torch.no_grad():
+        other = da.differential_cross_attention(*x, 0.8, kv_lengths=bad)
+    assert da.get_device_error() == da._lib.DIFFATTN_ERR_INDEX
+    for a, b in [(got, want), (other, served)] + [(gg[k], wg[k]) for k in ("q1", "k1", "q2", "v")]:
+        assert torch.equal(a[0::2], b[0::2]) and a[1::2].isnan().all()
+
+
+def test_out_and_strided_results():
+    x, n = inputs(10, BF, 2, 4, 2, 30, 90, 64, 128, False, [90, 0])
+    with torch.no_grad():
+        want = da.differential_cross_attention(*x, 0.8, kv_lengths=n)
+        out = torch.full((2, 30, 4, 128), 7.0, dtype=BF, device="cuda").transpose(1, 2)
+        assert da.differential_cross_attention(*x, 0.8, kv_lengths=n, out=out) is out and torch.equal(out, want)
+        big = torch.full((2, 4, 30, 131), 7.0, dtype=BF, device="cuda")
+        da.differential_cross_attention(*x, 0.8, kv_lengths=n, out=big[..., 1:129])
+        assert (big[..., 0] == 7).all() and (big[..., 129:] == 7).all()
+        check("odd out", big[..., 1:129], *(lambda r: (r.o, r.o_tol))(reference(x, float(torch.tensor(0.8)), [90, 0])))
+        for Tq in (1, 5, 200):                  # every path of the same call
+            y, m = inputs(11, BF, 2, 4, 2, Tq, 90, 64, 128, False, [90, 3])
+            want = da.differential_cross_attention(*y, 0.8, kv_lengths=m)
+            out = torch.full((2, Tq, 4, 128), 7.0, dtype=BF, device="cuda").transpose(1, 2)
+            da.differential_cross_attention(*y, 0.8, kv_lengths=m, out=out)
+            assert torch.equal(out, want)
+
+
+def test_some_gradients_alone():
+    """Frozen queries, a frozen encoder, a trained coefficient: what asks for a gradient gets the
+    same one."""
+    x, n = inputs(12, BF, 2, 4, 2, 70, 90, 64, 128, False, [90, 20])
+    do = torch.randn(2, 4, 70, 128, device="cuda").to(BF)
+    _, want = train(x, n, 0.8, do)
+    names = ["q1", "k1", "q2", "k2", "v"]
+    for which in (["q1"], ["q2", "lam"], ["k2"], ["v"], ["lam"], ["k1", "v"]):
+        ts = [t.detach().requires_grad_(name in which) for name, t in zip(names, x)]
+        lam = torch.tensor(0.8, device="cuda", requires_grad="lam" in which)
+        o = da.differential_cross_attention(*ts, lam, kv_lengths=n)
+        every = dict(zip(names + ["lam"], ts + [lam]))
+        got = torch.autograd.grad(o, [every[w] for w in which], do)
+        for w, g in zip(which, got):
+            assert torch.equal(g, want[w]), w
+
+
+def test_coefficient_kinds():
+    x, n = inputs(13, BF, 2, 4, 2, 20, 90, 64, 128, False, [90, 20])
+    do = torch.randn(2, 4, 20, 128, device="cuda").to(BF)
+    _, want = train(x, n, 0.75, do)
+    with torch.no_grad():
+        o = da.differential_cross_attention(*x, 0.75, kv_lengths=n)
+        for lam in (torch.tensor(0.75), torch.tensor([[0.75]], dtype=torch.float64, device="cuda"), torch.tensor(0.75, device="cuda").bfloat16()):
+            assert torch.equal(o, da.differential_cross_attention(*x, lam, kv_lengths=n))
+    for lam in (torch.tensor(0.75), torch.tensor([0.75], dtype=torch.float64, device="cuda"), torch.tensor(0.75, device="cuda").bfloat16()):
+        lam.requires_grad_()
+        g, = torch.autograd.grad(da.differential_cross_attention(*x, lam, kv_lengths=n), lam, do)
+        assert g.shape == lam.shape and g.dtype == lam.dtype and g.device == lam.device
+        assert torch.equal(g.reshape(()).cpu(), want["lam"].cpu().to(lam.dtype))
+
+
+def test_same_bits_on_other_streams_and_in_graphs():
+    """Each time the same bits; calls on two streams at once; a captured training step replayed on
+    new inputs and new lengths; two graphs that run at the same time."""
+    x, n = inputs(14, BF, 3, 4, 2, 150, 300, 64, 128, False, [300, 120, 0], poison=False)
+    do = torch.randn(3, 4, 150, 128, device="cuda").to(BF)
+    o, want = train(x, n, 0.8, do)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(train(x, n, 0.8, do))
+    torch.cuda.synchronize()
+    for o2, g in got:
+        assert torch.equal(o, o2) and all(torch.equal(want[k], g[k]) for k in want)
+    leaves = [t.requires_grad_() for t in x]
+    lam = torch.tensor(0.8, device="cuda")
+    graphs, held = [], []
+    with torch.cuda.stream(streams[0]):
+        torch.autograd.grad(da.differential_cross_attention(*x, lam, kv_lengths=n), leaves, do)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = da.differential_cross_attention(*x, lam, kv_lengths=n)
+            gs = torch.autograd.grad(y, leaves, do)
+            with torch.no_grad():
+                served = da.differential_cross_attention(*[t[:, :, :1] if i in (0, 2) else t for i, t in enumerate(x)], lam, kv_lengths=n)
+        graphs.append(graph)
+        held.append((y, *gs, served))
+    with torch.no_grad():
+        for t in x:
+            t.copy_(torch.randn_like(t))
+    n.copy_(torch.tensor([0, 299, 64], dtype=torch.int32))
+    torch.cuda.synchronize()
+    for s, graph in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                graph.replay()
+    torch.cuda.synchronize()
+    o3, g3 = train([t.detach() for t in x], n, 0.8, do)
+    with torch.no_grad():
+        served = da.differential_cross_attention(*[t[:, :, :1] if i in (0, 2) else t for i, t in enumerate(x)], lam, kv_lengths=n)
+    for h in held:
+        for a, b in zip(h, (o3, g3["q1"], g3["k1"], g3["q2"], g3["k2"], g3["v"], served)):
+            assert torch.equal(a, b)
+
+
+def test_non_finite_states_that_are_seen_stay_in_their_sequence():
+    x, n = inputs(15, BF, 2, 4, 2, 40, 90, 64, 128, False, [90, 50], poison=False)
+    with torch.no_grad():
+        want = da.differential_cross_attention(*x, 0.8, kv_lengths=n)
+        x[4][0, 0, 3, 5] = float("nan")
+        x[1][0, 1, 4] = float("nan")
+        got = da.differential_cross_attention(*x, 0.8, kv_lengths=n)
+    assert torch.equal(got[1], want[1])
+    assert got[0, :2, :, 5].isnan().all() and got[0, 2:].isnan().all()
+
+
+def test_offsets_past_32_bits():
+    """States of a batch more than 2^31 elements apart."""
+    Tk, D, Dv = 70, 64, 128
+    store = torch.zeros(2 ** 31 + 4096 + Tk * Dv, dtype=BF, device="cuda")
+    x, _ = inputs(16, BF, 2, 2, 2, 40, Tk, D, Dv, True)
+    far = 2 ** 31 + 4096
+    for i, width in ((1, D), (4, Dv)):
+        view = store.as_strided((2, 1, Tk, width), (far, Tk * width, width, 1), 0 if i == 1 else 0)
+        view.copy_(x[i][:, :1])
+        y = list(x)
+        y[1] = y[3] = x[1][:, :1]
+        y[4] = x[4][:, :1]
+        with torch.no_grad():
+            want = [da.differential_cross_attention(*[t[:, :, :q] if k in (0, 2) else t for k, t in enumerate(y)], 0.8) for q in (1, 40)]
+            if i == 1:
+                y[1] = y[3] = view
+            else:
+                y[4] = view
+            got = [da.differential_cross_attention(*[t[:, :, :q] if k in (0, 2) else t for k, t in enumerate(y)], 0.8) for q in (1, 40)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_autograd_refusals():
+    x, n = inputs(17, F32, 1, 2, 2, 5, 9, 32, 64, False)
+    f = da.differential_cross_attention
+    q = x[0].clone().requires_grad_()
+    w = torch.ones(2, 64, device="cuda", requires_grad=True)
+    for kw in (dict(norm="rms"), dict(out_scale=0.5), dict(out=torch.empty(1, 2, 5, 64, device="cuda"))):
+        with pytest.raises(ValueError, match="bare operation"):
+            f(q, *x[1:], 0.5, **kw)
+    with pytest.raises(ValueError, match="bare operation"):
+        f(*x, 0.5, norm="rms", norm_weight=w)
+    o = f(q, *x[1:], 0.5)
+    torch.autograd.grad(o, q, torch.ones_like(o))
+    with pytest.raises(RuntimeError, match="second time"):
+        torch.autograd.grad(o, q, torch.ones_like(o))
+    o = f(q, *x[1:], 0.5)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(o, q, torch.ones_like(o), create_graph=True)
+    o = f(q, *x[1:], 0.5)
+    with torch.no_grad():
+        o.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(o, q, torch.ones_like(o))
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises(ValueError, match="forward-mode"):
+            f(torch.autograd.forward_ad.make_dual(x[0], x[0]), *x[1:], 0.5)
+
+
+def test_refusals():
+    x, _ = inputs(18, BF, 2, 4, 2, 5, 9, 64, 128, False)
+    f = da.differential_cross_attention
+    q1, k1, q2, k2, v = x
+    lens = torch.tensor([9, 9], dtype=torch.int32, device="cuda")
+    for bad in ((q1[0], k1, q2, k2, v), (q1, k1, q2[:, :2], k2, v), (q1, k1[:, :, :8], q2, k2, v), (q1, k1, q2, k2, v[:1]),
+                (q1[:, :3], k1, q2[:, :3], k2, v), (q1.float(), k1, q2, k2, v), (q1.half(), k1.half(), q2.half(), k2.half(), v.half()),
+                (q1, k1.cpu(), q2, k2, v), (q1[:, :, :0], k1, q2[:, :, :0], k2, v), (q1, k1[:, :, :0], q2, k2[:, :, :0], v[:, :, :0])):
+        with pytest.raises(ValueError):
+            f(*bad, 0.5)
+    for kw in (dict(kv_lengths=lens.long()), dict(kv_lengths=lens[:1]), dict(kv_lengths=lens.cpu()), dict(norm="layer"),
+               dict(out=torch.empty(2, 4, 5, 64, dtype=BF, device="cuda")), dict(norm_weight=torch.ones(3, 128, device="cuda"))):
+        with pytest.raises(ValueError):
+            f(*x, 0.5, **kw)
+    with pytest.raises(TypeError):
+        f(*x, "0.5")
+    with pytest.raises(TypeError):
+        f(q1, None, q2, k2, v, 0.5)
+    with pytest.raises(ValueError):
+        f(*x, torch.ones(2))
+    with pytest.raises(da.DiffattnError):
+        f(*x, float("nan"))
+    with pytest.raises(da.DiffattnError):
+        f(*x, 0.5, out=torch.empty(1, 4, 5, 128, dtype=BF, device="cuda").expand(2, -1, -1, -1))
