@@ -20,6 +20,8 @@ DIFFATTN_F32 = 1
 DIFFATTN_KERNEL_TCGEN05 = 1
 DIFFATTN_KERNEL_SIMT = 2
 
+DIFFATTN_MAX_AXES = 4
+
 DIFFATTN_NORM_NONE = 0
 DIFFATTN_NORM_RMS = 1
 DIFFATTN_NORM_GROUP = 2
@@ -42,7 +44,10 @@ EXPORTED = (
     "diffattn_rotary",
     "diffattn_rotary_bwd",
     "diffattn_rotary_bwd_workspace_bytes",
+    "diffattn_rotary_axes",
+    "diffattn_rotary_axes_bwd",
     "diffattn_paged_append",
+    "diffattn_paged_append_axes",
     "diffattn_paged_decode",
     "diffattn_paged_workspace_bytes",
     "diffattn_cross_fwd",
@@ -104,6 +109,14 @@ class DiffattnRotaryDesc(ctypes.Structure):
         ("q2_stride", ctypes.c_int64 * 3), ("k2_stride", ctypes.c_int64 * 3),
         ("q1_grad_stride", ctypes.c_int64 * 3), ("k1_grad_stride", ctypes.c_int64 * 3),
         ("q2_grad_stride", ctypes.c_int64 * 3), ("k2_grad_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class DiffattnAxes(ctypes.Structure):
+    """Mirror of diffattn_axes."""
+    _fields_ = [
+        ("n", ctypes.c_int32), ("pairs", ctypes.c_int32 * DIFFATTN_MAX_AXES), ("reserved", ctypes.c_int32),
+        ("pos_stride", ctypes.c_int64),
     ]
 
 
@@ -214,6 +227,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_rotary_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.diffattn_paged_append.argtypes = [vp, i64] + [vp] * 16
     lib.diffattn_paged_append.restype = ctypes.c_int
+    lib.diffattn_rotary_axes.argtypes = [vp] * 16
+    lib.diffattn_rotary_axes.restype = ctypes.c_int
+    lib.diffattn_rotary_axes_bwd.argtypes = [vp] * 22 + [ctypes.c_size_t, vp]
+    lib.diffattn_rotary_axes_bwd.restype = ctypes.c_int
+    lib.diffattn_paged_append_axes.argtypes = [vp, vp, i64] + [vp] * 16
+    lib.diffattn_paged_append_axes.restype = ctypes.c_int
     lib.diffattn_paged_decode.argtypes = [vp] * 11 + [ctypes.c_float, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.diffattn_paged_decode.restype = ctypes.c_int
     lib.diffattn_paged_workspace_bytes.argtypes = [vp, vp]

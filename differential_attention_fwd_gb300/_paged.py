@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import importlib
 import os
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
@@ -35,14 +35,22 @@ def _load():
     return _native
 
 
-def rotary_tables(positions: int, rotary_dim: int, base: float = 10000.0, device=None):
+def rotary_tables(positions: int, rotary_dim: int, base: float = 10000.0, device=None,
+                  sections: Optional[Sequence[int]] = None):
     """(cos, sin) tables of the position rotation, float32 [positions,
     rotary_dim / 2]: entry (p, i) is the cosine (sine) of p * base^(-2 i /
     rotary_dim).  The angles are formed in float64, since a float32 angle is
-    already off by 2^-8 at position 100,000.  Made once, at set-up."""
+    already off by 2^-8 at position 100,000.  Made once, at set-up.
+    sections: with several axes, each of which has frequencies of its own: the i-th of its n
+    pairs turns by p * base^(-i / n).  (Without them the axes share one row of frequencies.)"""
     if positions < 1 or rotary_dim < 2 or rotary_dim % 2 != 0:
         raise ValueError("positions must be at least 1 and rotary_dim even and at least 2")
-    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    if sections is None:
+        f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    else:
+        if not sections or min(sections) < 1 or 2 * sum(sections) != rotary_dim:
+            raise ValueError("sections must be positive and add up to rotary_dim / 2")
+        f = torch.cat([base ** (-torch.arange(n, dtype=torch.float64, device=device) / n) for n in sections])
     a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
     return a.cos().float(), a.sin().float()
 
@@ -51,7 +59,7 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
                    k2: Optional[torch.Tensor], cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
                    positions: Optional[torch.Tensor] = None, norm: Optional[str] = "rms", norm_eps: float = 1e-6,
                    q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
-                   interleaved: bool = False):
+                   interleaved: bool = False, sections: Optional[Sequence[int]] = None):
     """The step before the operation: the RMS norm of each query and key head and
     the rotation of its pairs by the token's position, in one launch.
 
@@ -66,6 +74,9 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
     interleaved=True; None for both: no rotation.  positions: int32 or int64, [T] or
     [B, T]; None: 0 .. T-1.  A position outside the tables gives a row of NaN and is
     reported by get_device_error.
+    sections: positions with several axes (time, height and width of an image's or a video's
+    tokens; up to 4): the pairs of each axis, in turn, R / 2 in all.  positions are then [T,
+    axes] or [B, T, axes], and a pair is turned by its own axis's row of the tables.
     norm: "rms" or None; q_weight and k_weight: [D] (for every head) or [heads, D],
     None = 1; one whose rows are left out is not used and gets no gradient.
     Arithmetic in float32, one rounding at the end.
@@ -77,7 +88,7 @@ def qk_norm_rotary(q1: Optional[torch.Tensor], k1: Optional[torch.Tensor], q2: O
     that stream to the capture, so this is an error.  torch.autograd.grad is free of it.)
     """
     return (_native or _load()).rotary(q1, k1, q2, k2, cos, sin, positions, norm, norm_eps, q_weight, k_weight,
-                                       interleaved)
+                                       interleaved, sections)
 
 
 def paged_cache_append(k1: torch.Tensor, k2: Optional[torch.Tensor], value: torch.Tensor, k1_cache: torch.Tensor,
@@ -85,7 +96,8 @@ def paged_cache_append(k1: torch.Tensor, k2: Optional[torch.Tensor], value: torc
                        lengths: torch.Tensor, new_lengths: Optional[torch.Tensor] = None,
                        cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
                        positions: Optional[torch.Tensor] = None, norm: Optional[str] = None, norm_eps: float = 1e-6,
-                       k_weight: Optional[torch.Tensor] = None, interleaved: bool = False) -> None:
+                       k_weight: Optional[torch.Tensor] = None, interleaved: bool = False,
+                       sections: Optional[Sequence[int]] = None) -> None:
     """Write new keys and values into a paged cache, in place, the keys normed and
     rotated on the way (arguments of qk_norm_rotary; by default neither).  One launch.
 
@@ -95,12 +107,13 @@ def paged_cache_append(k1: torch.Tensor, k2: Optional[torch.Tensor], value: torc
     sequence.  k2 and k2_cache None (or k1 and k1_cache again): the branches share
     their keys.  lengths: [B] int32, tokens cached before the call; token t goes to
     index lengths[b] + t.  new_lengths: [B] int32, the first new_lengths[b] tokens are
-    written (None: all T).  positions: for the rotation, None = the index.  No two
+    written (None: all T).  positions: for the rotation, None = the index (with sections
+    they must be given).  No two
     tokens of a call may have one slot, and the new rows may not lie in the caches.
     A token whose index, page or position is out of range is not written and is
     reported by get_device_error.  Forward only."""
     (_native or _load()).append(k1, k2, value, k1_cache, k2_cache, v_cache, block_table, lengths, new_lengths, cos, sin,
-                                positions, norm, norm_eps, k_weight, interleaved)
+                                positions, norm, norm_eps, k_weight, interleaved, sections)
 
 
 def differential_attention_paged(q1: torch.Tensor, k1_cache: torch.Tensor, q2: torch.Tensor,

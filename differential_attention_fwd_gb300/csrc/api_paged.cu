@@ -68,6 +68,22 @@ void fill_rotary(RotaryParams* p, const diffattn_rotary_desc& d, const float* co
               (p->R == 0 || (aligned16(cos) && aligned16(sin)));
 }
 
+// Several axes a position, if there are; false if they do not fit the descriptor.
+bool add_axes(RotaryParams* p, const diffattn_axes* axes) {
+    if (!axes) return true;
+    if (axes->n < 1 || axes->n > DIFFATTN_MAX_AXES || axes->reserved != 0 || axes->pos_stride < 0 || !p->pos) return false;
+    int end = 0;
+    for (int a = 0; a < axes->n; ++a) {
+        if (axes->pairs[a] < 1 || axes->pairs[a] > p->R / 2) return false;
+        end += axes->pairs[a];
+        p->axis_end[a] = end;
+        if (end % 4 != 0) p->fast = 0;
+    }
+    p->axes = axes->n;
+    p->axis_stride = axes->pos_stride;
+    return end == p->R / 2;
+}
+
 // One of Q1, K1, Q2, K2 as a stream; false if its arguments do not fit.
 bool add_stream(RotaryParams* p, const void* x, const int64_t sx[3], int64_t heads, void* y, const float* w,
                 int64_t w_stride, int slot) {
@@ -94,7 +110,7 @@ bool add_stream(RotaryParams* p, const void* x, const int64_t sx[3], int64_t hea
 
 constexpr int64_t kMaxHeads = 65535;
 
-int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const void* q1, const void* k1, const void* q2,
+int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const diffattn_axes* axes, const void* q1, const void* k1, const void* q2,
                  const void* k2, const float* qw, const float* kw, const float* cos, const float* sin,
                  const void* positions, void* yq1, void* yk1, void* yq2, void* yk2) {
     const int rc = check_rotary(d, cos, sin, true);
@@ -105,7 +121,7 @@ int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const void* q1,
     if (!add_stream(p, q1, d->q1_stride, d->H, yq1, qw, d->q_weight_stride, 0) ||
         !add_stream(p, k1, d->k1_stride, d->Hk, yk1, kw, d->k_weight_stride, 1) ||
         !add_stream(p, q2, d->q2_stride, d->H, yq2, qw, d->q_weight_stride, 0) ||
-        !add_stream(p, k2, d->k2_stride, d->Hk, yk2, kw, d->k_weight_stride, 1) || p->n == 0)
+        !add_stream(p, k2, d->k2_stride, d->Hk, yk2, kw, d->k_weight_stride, 1) || p->n == 0 || !add_axes(p, axes))
         return DIFFATTN_ERR_INVALID;
     return DIFFATTN_OK;
 }
@@ -263,8 +279,16 @@ int diffattn_rotary(const diffattn_rotary_desc* desc, const void* q1, const void
                     const void* k2, const float* q_weight, const float* k_weight, const float* cos,
                     const float* sin, const void* positions, void* q1_out, void* k1_out, void* q2_out,
                     void* k2_out, diffattn_stream_t stream) {
+    return diffattn_rotary_axes(desc, nullptr, q1, k1, q2, k2, q_weight, k_weight, cos, sin, positions, q1_out, k1_out,
+                                q2_out, k2_out, stream);
+}
+
+int diffattn_rotary_axes(const diffattn_rotary_desc* desc, const diffattn_axes* axes, const void* q1, const void* k1,
+                         const void* q2, const void* k2, const float* q_weight, const float* k_weight, const float* cos,
+                         const float* sin, const void* positions, void* q1_out, void* k1_out, void* q2_out,
+                         void* k2_out, diffattn_stream_t stream) {
     RotaryParams p{};
-    int rc = build_rotary(&p, desc, q1, k1, q2, k2, q_weight, k_weight, cos, sin, positions, q1_out, k1_out,
+    int rc = build_rotary(&p, desc, axes, q1, k1, q2, k2, q_weight, k_weight, cos, sin, positions, q1_out, k1_out,
                           q2_out, k2_out);
     if (rc != DIFFATTN_OK) return rc;
     int sms = 0;
@@ -287,6 +311,17 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc* desc, const void* q1, const 
                         const void* dq2_out, const void* dk2_out, void* dq1, void* dk1, void* dq2, void* dk2,
                         float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
                         diffattn_stream_t stream) {
+    return diffattn_rotary_axes_bwd(desc, nullptr, q1, k1, q2, k2, q_weight, k_weight, cos, sin, positions, dq1_out, dk1_out,
+                                    dq2_out, dk2_out, dq1, dk1, dq2, dk2, dq_weight, dk_weight, workspace, workspace_bytes,
+                                    stream);
+}
+
+int diffattn_rotary_axes_bwd(const diffattn_rotary_desc* desc, const diffattn_axes* axes, const void* q1, const void* k1,
+                             const void* q2, const void* k2, const float* q_weight, const float* k_weight,
+                             const float* cos, const float* sin, const void* positions, const void* dq1_out,
+                             const void* dk1_out, const void* dq2_out, const void* dk2_out, void* dq1, void* dk1,
+                             void* dq2, void* dk2, float* dq_weight, float* dk_weight, void* workspace,
+                             size_t workspace_bytes, diffattn_stream_t stream) {
     if (!desc) return DIFFATTN_ERR_INVALID;
     diffattn_rotary_desc d = *desc;
     const void* x[4] = {q1, k1, q2, k2};
@@ -302,7 +337,7 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc* desc, const void* q1, const 
         if ((x[i] != nullptr) != (g[i] != nullptr)) return DIFFATTN_ERR_INVALID;
     }
     RotaryParams p{};
-    int rc = build_rotary(&p, &d, x[0], x[1], x[2], x[3], q_weight, k_weight, cos, sin, positions, dq1, dk1, dq2, dk2);
+    int rc = build_rotary(&p, &d, axes, x[0], x[1], x[2], x[3], q_weight, k_weight, cos, sin, positions, dq1, dk1, dq2, dk2);
     if (rc != DIFFATTN_OK) return rc;
     for (int i = 0, n = 0; i < 4; ++i) {
         if (!x[i]) continue;
@@ -332,6 +367,15 @@ int diffattn_paged_append(const diffattn_rotary_desc* desc, int64_t Dv, const in
                           const float* k_weight, const float* cos, const float* sin, const void* positions,
                           const int32_t* lengths, const int32_t* new_lengths, const int32_t* block_table,
                           void* k1_cache, void* k2_cache, void* v_cache, diffattn_stream_t stream) {
+    return diffattn_paged_append_axes(desc, nullptr, Dv, v_stride, pages, k1, k2, v, k_weight, cos, sin, positions, lengths,
+                                      new_lengths, block_table, k1_cache, k2_cache, v_cache, stream);
+}
+
+int diffattn_paged_append_axes(const diffattn_rotary_desc* desc, const diffattn_axes* axes, int64_t Dv, const int64_t v_stride[3],
+                          const diffattn_pages* pages, const void* k1, const void* k2, const void* v,
+                          const float* k_weight, const float* cos, const float* sin, const void* positions,
+                          const int32_t* lengths, const int32_t* new_lengths, const int32_t* block_table,
+                          void* k1_cache, void* k2_cache, void* v_cache, diffattn_stream_t stream) {
     if (!desc) return DIFFATTN_ERR_INVALID;
     diffattn_rotary_desc d = *desc;
     d.H = 0;                            // not read
@@ -357,7 +401,7 @@ int diffattn_paged_append(const diffattn_rotary_desc* desc, int64_t Dv, const in
     const int es = p.bf16 ? 2 : 4;
     if (!add_stream(&p, k1, d.k1_stride, d.Hk, k1_cache, k_weight, d.k_weight_stride, 1) ||
         (!shared && !add_stream(&p, k2, d.k2_stride, d.Hk, k2_cache, k_weight, d.k_weight_stride, 1)) ||
-        !add_stream(&p, v, v_stride, d.Hk, v_cache, nullptr, 0, 1))
+        !add_stream(&p, v, v_stride, d.Hk, v_cache, nullptr, 0, 1) || !add_axes(&p, axes))
         return DIFFATTN_ERR_INVALID;
     for (int i = 0; i < p.n; ++i) {
         const int64_t* s = i == p.n - 1 ? pages->v_stride : i == 0 ? pages->k1_stride : pages->k2_stride;

@@ -211,6 +211,7 @@ struct Rotary {
     int32_t dtype = 0, norm = 0, interleaved = 0, pos64 = 0;
     int64_t pos_stride[2] = {0, 0}, qws = 0, kws = 0;
     float eps = 0.f;
+    diffattn_axes axes{};                   // n = 0: a position a token
     Tensor cos, sin, pos, qw, kw;           // as the kernels read them
     Tensor qw_given, kw_given;              // as the caller has them
 
@@ -227,7 +228,8 @@ struct Rotary {
         R = 2 * cos.size(1);
         rows = cos.size(0);
     }
-    void positions(PyObject* o, at::Device dev) {
+    void positions(PyObject* o, PyObject* sections, at::Device dev) {
+        if (!is_none(sections)) return axis_positions(o, sections, dev);
         if (is_none(o)) return;
         pos = tensor(o, "positions");
         const bool flat = pos.dim() == 1;
@@ -239,6 +241,37 @@ struct Rotary {
         pos_stride[0] = flat ? 0 : pos.stride(0);
         pos_stride[1] = pos.stride(-1);
     }
+    // positions [T, axes] or [B, T, axes], and the pairs of each axis
+    void axis_positions(PyObject* o, PyObject* sections, at::Device dev) {
+        if (!PyTuple_Check(sections) && !PyList_Check(sections)) bad_type("sections must be a tuple or a list of whole numbers");
+        const Py_ssize_t n = PySequence_Size(sections);
+        if (n < 1 || n > DIFFATTN_MAX_AXES)
+            bad_value("sections must name 1 to " + std::to_string(DIFFATTN_MAX_AXES) + " axes, got " + std::to_string(n));
+        int64_t sum = 0;
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            PyObject* item = PyTuple_Check(sections) ? PyTuple_GET_ITEM(sections, i) : PyList_GET_ITEM(sections, i);
+            if (!PyLong_Check(item)) bad_type("sections must be a tuple or a list of whole numbers");
+            const long v = PyLong_AsLong(item);
+            if (v == -1 && PyErr_Occurred()) PyErr_Clear();
+            if (v < 1 || v > R / 2) bad_value("sections must be positive and add up to rotary_dim / 2 = " + std::to_string(R / 2));
+            axes.pairs[i] = (int32_t)v;
+            sum += v;
+        }
+        if (sum != R / 2) bad_value("sections must add up to rotary_dim / 2 = " + std::to_string(R / 2) + ", got " + std::to_string(sum));
+        if (is_none(o)) bad_value("sections need positions [T, axes] or [B, T, axes]");
+        pos = tensor(o, "positions");
+        const bool flat = pos.dim() == 2;
+        if (pos.device() != dev || (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong) || pos.dim() < 2 ||
+            pos.dim() > 3 || pos.size(-1) != n || pos.size(-2) != T || (!flat && pos.size(0) != B))
+            bad_value("with sections, positions must be an int32 or int64 tensor [T, axes] or [B, T, axes] = (" +
+                      std::to_string(B) + ", " + std::to_string(T) + ", " + std::to_string(n) + ") on the inputs' device");
+        axes.n = (int32_t)n;
+        axes.pos_stride = pos.stride(-1);
+        pos64 = pos.scalar_type() == at::kLong;
+        pos_stride[0] = flat ? 0 : pos.stride(0);
+        pos_stride[1] = pos.stride(-2);
+    }
+    const diffattn_axes* axes_ptr() const { return axes.n ? &axes : nullptr; }
     void set_norm(PyObject* name, PyObject* e) {
         norm = norm_code(name, false);
         eps = (float)number(e, "norm_eps");
@@ -279,7 +312,7 @@ void rotary_forward(const Rotary& r, const Tensor (&x)[4], Tensor (&y)[4], at::D
         strides3(row_stride(d, i), x[i]);
         y[i] = fresh_tensor(x[i].sizes(), x[i].scalar_type(), dev);
     }
-    check(diffattn_rotary(&d, ptr(x[0]), ptr(x[1]), ptr(x[2]), ptr(x[3]), fptr(r.qw), fptr(r.kw), fptr(r.cos), fptr(r.sin),
+    check(diffattn_rotary_axes(&d, r.axes_ptr(), ptr(x[0]), ptr(x[1]), ptr(x[2]), ptr(x[3]), fptr(r.qw), fptr(r.kw), fptr(r.cos), fptr(r.sin),
                           ptr(r.pos), ptr(y[0]), ptr(y[1]), ptr(y[2]), ptr(y[3]), stream_of(dev)),
           "diffattn_rotary");
 }
@@ -370,8 +403,8 @@ struct RotaryBackward : public torch::autograd::Node {
         const c10::cuda::OptionalCUDAGuard guard(*dev);
         const size_t bytes = diffattn_rotary_bwd_workspace_bytes(&d);
         const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
-        const int rc = diffattn_rotary_bwd(
-            &d, ptr(xs[0]), ptr(xs[1]), ptr(xs[2]), ptr(xs[3]), fptr(c.qw), fptr(c.kw), fptr(c.cos), fptr(c.sin), ptr(c.pos),
+        const int rc = diffattn_rotary_axes_bwd(
+            &d, c.axes_ptr(), ptr(xs[0]), ptr(xs[1]), ptr(xs[2]), ptr(xs[3]), fptr(c.qw), fptr(c.kw), fptr(c.cos), fptr(c.sin), ptr(c.pos),
             ptr(gs[0]), ptr(gs[1]), ptr(gs[2]), ptr(gs[3]), ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), ptr(dx[3]),
             dw[0].defined() ? dw[0].data_ptr<float>() : nullptr, dw[1].defined() ? dw[1].data_ptr<float>() : nullptr,
             ws.data_ptr(), bytes, stream_of(*dev));
@@ -396,7 +429,7 @@ struct RotaryBackward : public torch::autograd::Node {
 };
 
 PyObject* rotary(PyObject* const* a) {
-    // q1, k1, q2, k2, cos, sin, positions, norm, norm_eps, q_weight, k_weight, interleaved
+    // q1, k1, q2, k2, cos, sin, positions, norm, norm_eps, q_weight, k_weight, interleaved, sections
     const bool shared = !is_none(a[3]) && a[3] == a[1];
     Tensor in[4];
     const Tensor* first = nullptr;
@@ -424,7 +457,7 @@ PyObject* rotary(PyObject* const* a) {
         heads = in[i].size(1);
     }
     r.tables(a[4], a[5], dev);
-    r.positions(a[6], dev);
+    r.positions(a[6], a[12], dev);
     r.set_norm(a[7], a[8]);
     if (!r.norm && !(is_none(a[9]) && is_none(a[10]))) bad_value("q_weight and k_weight need norm='rms'");
     r.qw = norm_weight(a[9], "q_weight", r.H, r.D, dev, &r.qw_given, &r.qws);
@@ -682,7 +715,7 @@ struct Cache {
 
 PyObject* append(PyObject* const* a) {
     // k1, k2, value, k1_cache, k2_cache, v_cache, block_table, lengths, new_lengths, cos, sin, positions, norm, norm_eps,
-    // k_weight, interleaved
+    // k_weight, interleaved, sections
     const Tensor& first = need(a[0], "k1", 4);
     Cache c(a[3], a[4], a[5], a[6], first.size(0));
     const at::Device dev = c.k1.device();
@@ -703,7 +736,7 @@ PyObject* append(PyObject* const* a) {
     if (v.size(0) != c.B || v.size(1) != c.Hk || v.size(2) != r.T || v.size(3) != c.Dv || r.T < 1)
         bad_value("value must be [B, H_kv, T, Dv] with the cache's H_kv and Dv, got " + text(v.sizes()));
     r.tables(a[9], a[10], dev);
-    r.positions(a[11], dev);
+    r.positions(a[11], a[16], dev);
     r.set_norm(a[12], a[13]);
     if (!r.norm && !is_none(a[14])) bad_value("k_weight needs norm='rms'");
     r.kw = norm_weight(a[14], "k_weight", r.Hk, r.D, dev, &r.kw_given, &r.kws);
@@ -727,7 +760,7 @@ PyObject* append(PyObject* const* a) {
     c.k1.unsafeGetTensorImpl()->bump_version();
     if (!shared) c.k2.unsafeGetTensorImpl()->bump_version();
     c.v.unsafeGetTensorImpl()->bump_version();
-    check(diffattn_paged_append(&d, c.Dv, vs, &c.pages, ptr(k[0]), ptr(k[1]), ptr(v), fptr(r.kw), fptr(r.cos), fptr(r.sin),
+    check(diffattn_paged_append_axes(&d, r.axes_ptr(), c.Dv, vs, &c.pages, ptr(k[0]), ptr(k[1]), ptr(v), fptr(r.kw), fptr(r.cos), fptr(r.sin),
                                 ptr(r.pos), lengths.const_data_ptr<int32_t>(),
                                 fresh.defined() ? fresh.const_data_ptr<int32_t>() : nullptr, c.table_ptr(), ptr(c.k1),
                                 shared ? nullptr : ptr(c.k2), ptr(c.v), stream_of(dev)),
@@ -1062,10 +1095,10 @@ PyCFunction as_function(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t))
 }
 
 PyMethodDef methods[] = {
-    {"rotary", as_function(entry<rotary, 12>), METH_FASTCALL, nullptr},
+    {"rotary", as_function(entry<rotary, 13>), METH_FASTCALL, nullptr},
     {"cross", as_function(entry<cross, 13>), METH_FASTCALL, nullptr},
     {"head_norm", as_function(entry<head_norm, 6>), METH_FASTCALL, nullptr},
-    {"append", as_function(entry<append, 16>), METH_FASTCALL, nullptr},
+    {"append", as_function(entry<append, 17>), METH_FASTCALL, nullptr},
     {"attention", as_function(entry<attention, 16>), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},

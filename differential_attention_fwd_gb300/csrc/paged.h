@@ -63,6 +63,9 @@ struct RotaryParams {
     const void* pos;            // nullptr: the slot (paged) or t
     int pos64;
     int64_t pos_stride[2];      // B, T
+    int axes;                   // 0: a position a token; else so many, the pairs in sections,
+    int axis_end[DIFFATTN_MAX_AXES];    // each turned by its own axis's: where they end
+    int64_t axis_stride;        // of a token's positions
     // the paged cache
     const int32_t* lengths;     // [B] tokens before the call
     const int32_t* new_lengths; // [B] or nullptr (T each)

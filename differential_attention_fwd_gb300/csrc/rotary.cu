@@ -12,6 +12,12 @@
 // angles need more than 32 bits at far positions, which the table's maker spends
 // once.  All arithmetic is in float32, with one rounding of y at the end.
 //
+// With several axes (time, height and width of image and video tokens) a token has a
+// position for each, and the pairs fall into sections, one an axis: pair i is turned by
+// entry i of its own axis's row.  The rows are then read in pieces of 4 entries (sections
+// of other widths run a warp a row); all else is the same, in instances of their own, so
+// that a position a token costs what it did.
+//
 // The pass is bound by HBM: x in, y out.  A group of D / (2 V) lanes holds one row,
 // V = 16 bytes of elements twice a lane: the two halves of its pairs, so a pair never
 // leaves its lane and the only exchange is the sum of squares.  A group walks several
@@ -48,6 +54,11 @@ struct Token {
     int64_t pos, page, slot;
 };
 
+__device__ __forceinline__ int64_t position_at(const RotaryParams& p, int64_t i) {
+    return p.pos64 ? static_cast<const int64_t*>(p.pos)[i] : static_cast<const int32_t*>(p.pos)[i];
+}
+
+template <bool AXES>
 __device__ __forceinline__ Token find_token(const RotaryParams& p, int b, int t, bool paged) {
     Token k{true, true, t, 0, 0};
     if (paged) {
@@ -64,12 +75,29 @@ __device__ __forceinline__ Token find_token(const RotaryParams& p, int b, int t,
             k.ok = k.page >= 0 && k.page < p.num_pages;
         }
     }
-    if (p.pos) {
+    if constexpr (AXES) {
         const int64_t i = b * p.pos_stride[0] + t * p.pos_stride[1];
-        k.pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[i] : static_cast<const int32_t*>(p.pos)[i];
+        for (int a = 0; a < p.axes; ++a) {
+            const int64_t at = position_at(p, i + a * p.axis_stride);
+            if (at < 0 || at >= p.table_rows) k.ok = false;
+        }
+    } else {
+        if (p.pos) k.pos = position_at(p, b * p.pos_stride[0] + t * p.pos_stride[1]);
+        if (p.R > 0 && (k.pos < 0 || k.pos >= p.table_rows)) k.ok = false;
     }
-    if (p.R > 0 && (k.pos < 0 || k.pos >= p.table_rows)) k.ok = false;
     return k;
+}
+
+// The table row of a pair: with axes its own axis's.
+template <bool AXES>
+__device__ __forceinline__ int64_t pair_row(const RotaryParams& p, const Token& k, int b, int t, int pair) {
+    if constexpr (AXES) {
+        int a = 0;
+        while (a < p.axes - 1 && pair >= p.axis_end[a]) ++a;
+        return position_at(p, b * p.pos_stride[0] + t * p.pos_stride[1] + a * p.axis_stride);
+    } else {
+        return k.pos;
+    }
 }
 
 // Stream and first head of a head block.
@@ -140,7 +168,7 @@ __device__ __forceinline__ void rotate(uint64_t* c, const uint64_t* cs, const ui
 // ---------------------------------------------------------------------------
 constexpr int AHEAD = 4;        // heads
 
-template <typename T, int G, bool INTER>
+template <typename T, int G, bool INTER, bool AXES>
 __global__ void __launch_bounds__(THREADS, 3)
 rotary_kernel(const RotaryParams p) {
     constexpr int V = Vec<T>::N;
@@ -161,7 +189,7 @@ rotary_kernel(const RotaryParams p) {
     const int t = in ? tok - b * p.T : 0;
     const T* x0 = static_cast<const T*>(s.x) + b * s.sx[0] + t * s.sx[2];
     if (s.kind == kRowsCopy) {
-        const Token k = find_token(p, b, t, true);
+        const Token k = find_token<AXES>(p, b, t, true);
         if (in && k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
         if (!in || !k.live || !k.ok) return;
         T* y0 = static_cast<T*>(s.y) + k.page * s.sy[0] + k.slot * s.sy[2];
@@ -198,7 +226,7 @@ rotary_kernel(const RotaryParams p) {
         }
     };
     load(head0);
-    Token k = find_token(p, b, t, paged);
+    Token k = find_token<AXES>(p, b, t, paged);
     k.live = k.live && in;
     if (k.live && !k.ok && g == 0) atomicOr(p.status, kStatusIndex);
     const bool write = k.live && (k.ok || !paged);
@@ -206,8 +234,17 @@ rotary_kernel(const RotaryParams p) {
     uint64_t cs[V / 2], sn[V / 2];
     const bool turned = turn && k.live && k.ok;
     if (turned) {
-        load_pairs<V>(p.cos + k.pos * (p.R / 2) + g * V, cs);
-        load_pairs<V>(p.sin + k.pos * (p.R / 2) + g * V, sn);
+        if constexpr (AXES) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const int64_t at = pair_row<true>(p, k, b, t, g * V + i) * (p.R / 2) + g * V + i;
+                load_pairs<4>(p.cos + at, cs + i / 2);
+                load_pairs<4>(p.sin + at, sn + i / 2);
+            }
+        } else {
+            load_pairs<V>(p.cos + k.pos * (p.R / 2) + g * V, cs);
+            load_pairs<V>(p.sin + k.pos * (p.R / 2) + g * V, sn);
+        }
     }
     const bool weighted = p.norm && s.weight;
     for (int h0 = head0; h0 < head1; h0 += AHEAD) {
@@ -252,7 +289,7 @@ rotary_kernel(const RotaryParams p) {
 }
 
 // Any width up to 128, any alignment: a warp a row.
-template <typename T>
+template <typename T, bool AXES>
 __global__ void __launch_bounds__(THREADS)
 rotary_any_kernel(const RotaryParams p) {
     constexpr int WARPS = THREADS / 32;
@@ -269,7 +306,7 @@ rotary_any_kernel(const RotaryParams p) {
     if (tok >= (int64_t)p.B * p.T) return;
     const int b = (int)(tok / p.T);
     const int t = (int)(tok - (int64_t)b * p.T);
-    const Token k = find_token(p, b, t, paged);
+    const Token k = find_token<AXES>(p, b, t, paged);
     if (!k.live) return;
     if (!k.ok && lane == 0) atomicOr(p.status, kStatusIndex);
     if (!k.ok && paged) return;
@@ -303,7 +340,8 @@ rotary_any_kernel(const RotaryParams p) {
             const int j = p.interleaved ? i / 2 : (i < half ? i : i - half);
             const bool first = p.interleaved ? (i & 1) == 0 : i < half;
             const float other = row[p.interleaved ? i ^ 1 : (first ? i + half : i - half)];
-            const float cs = p.cos[k.pos * half + j], sn = p.sin[k.pos * half + j];
+            const int64_t at = pair_row<AXES>(p, k, b, t, j) * half + j;
+            const float cs = p.cos[at], sn = p.sin[at];
             v = first ? v * cs - other * sn : v * cs + other * sn;
         }
         y[i] = Vec<T>::put(v);
@@ -338,7 +376,7 @@ __host__ __device__ constexpr BwdLayout bwd_layout(int groups, int D, int R) {
     return l;
 }
 
-template <typename T, int G, bool INTER>
+template <typename T, int G, bool INTER, bool AXES>
 __global__ void __launch_bounds__(THREADS, 2)
 rotary_bwd_kernel(const RotaryParams p) {
     constexpr int V = Vec<T>::N;
@@ -405,15 +443,16 @@ rotary_bwd_kernel(const RotaryParams p) {
         for (int i = tid; i < BWD_STEPS * GROUPS * per; i += THREADS) {
             const int k = i / per, c = (i - k * per) * 4;
             if (tok0 + k >= tokens) continue;
-            const int b = p.by_T.div(tok0 + k);
-            const Token at = find_token(p, b, tok0 + k - b * p.T, false);
+            const int b = p.by_T.div(tok0 + k), t = tok0 + k - b * p.T;
+            const Token at = find_token<AXES>(p, b, t, false);
             if (c == 0) {
                 fine[k] = at.ok;
                 if (!at.ok) atomicOr(p.status, kStatusIndex);
             }
             if (!at.ok || half == 0) continue;
-            *reinterpret_cast<float4*>(turns + k * p.R + c) = *reinterpret_cast<const float4*>(p.cos + at.pos * half + c);
-            *reinterpret_cast<float4*>(turns + k * p.R + half + c) = *reinterpret_cast<const float4*>(p.sin + at.pos * half + c);
+            const int64_t row = pair_row<AXES>(p, at, b, t, c) * half + c;
+            *reinterpret_cast<float4*>(turns + k * p.R + c) = *reinterpret_cast<const float4*>(p.cos + row);
+            *reinterpret_cast<float4*>(turns + k * p.R + half + c) = *reinterpret_cast<const float4*>(p.sin + row);
         }
     };
     // The item's partial row: sums of the groups in a fixed order.  (The next write of `red`
@@ -503,7 +542,7 @@ rotary_bwd_kernel(const RotaryParams p) {
     }
 }
 
-template <typename T>
+template <typename T, bool AXES>
 __global__ void __launch_bounds__(THREADS)
 rotary_bwd_any_kernel(const RotaryParams p) {
     constexpr int WARPS = THREADS / 32;
@@ -522,7 +561,7 @@ rotary_bwd_any_kernel(const RotaryParams p) {
     for (int64_t tok = (int64_t)blockIdx.x * WARPS + warp; tok < tokens; tok += (int64_t)gridDim.x * WARPS) {
         const int b = (int)(tok / p.T);
         const int t = (int)(tok - (int64_t)b * p.T);
-        const Token k = find_token(p, b, t, false);
+        const Token k = find_token<AXES>(p, b, t, false);
         if (!k.ok && lane == 0) atomicOr(p.status, kStatusIndex);
         const T* x = static_cast<const T*>(s.x) + b * s.sx[0] + head0 * s.sx[1] + t * s.sx[2];
         const T* gr = static_cast<const T*>(s.g) + b * s.sg[0] + head0 * s.sg[1] + t * s.sg[2];
@@ -542,7 +581,8 @@ rotary_bwd_any_kernel(const RotaryParams p) {
                 const int j = p.interleaved ? i / 2 : (i < half ? i : i - half);
                 const bool first = p.interleaved ? (i & 1) == 0 : i < half;
                 const float other = row[p.interleaved ? i ^ 1 : (first ? i + half : i - half)];
-                const float cs = p.cos[k.pos * half + j], sn = p.sin[k.pos * half + j];
+                const int64_t at = pair_row<AXES>(p, k, b, t, j) * half + j;
+                const float cs = p.cos[at], sn = p.sin[at];
                 v = first ? v * cs + other * sn : v * cs - other * sn;
             }
             u[e] = v;
@@ -615,18 +655,18 @@ rotary_dw_kernel(const RotaryParams p, int q_rows) {
     }
 }
 
-template <typename T, int G, bool INTER>
+template <typename T, int G, bool INTER, bool AXES>
 int launch_bwd(const RotaryParams& p, dim3 grid, cudaStream_t stream) {
     constexpr int D = G * 2 * Vec<T>::N, GROUPS = THREADS / G;
     const auto bytes = [](int R) { return bwd_layout(GROUPS, D, R).total * 4; };
-    if (cudaFuncSetAttribute(rotary_bwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(D)) !=
+    if (cudaFuncSetAttribute(rotary_bwd_kernel<T, G, INTER, AXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(D)) !=
         cudaSuccess)
         return -1;
-    rotary_bwd_kernel<T, G, INTER><<<grid, THREADS, bytes(p.R), stream>>>(p);
+    rotary_bwd_kernel<T, G, INTER, AXES><<<grid, THREADS, bytes(p.R), stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
     constexpr int V = Vec<T>::N;
     const int G = p.D / (2 * V);
@@ -635,8 +675,8 @@ int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
                     backward ? 1u : (unsigned)p.head_blocks);
 #define DIFFATTN_ROTARY(GG)                                                               \
     if (G == GG) {                                                                        \
-        if (backward) return launch_bwd<T, GG, INTER>(p, grid, stream);                   \
-        return pdl_launch(rotary_kernel<T, GG, INTER>, grid, THREADS, 0, stream, p);      \
+        if (backward) return launch_bwd<T, GG, INTER, AXES>(p, grid, stream);             \
+        return pdl_launch(rotary_kernel<T, GG, INTER, AXES>, grid, THREADS, 0, stream, p); \
     }
     DIFFATTN_ROTARY(2)
     DIFFATTN_ROTARY(4)
@@ -646,21 +686,22 @@ int launch_fast(const RotaryParams& p, bool backward, cudaStream_t stream) {
     return -1;
 }
 
-int launch(const RotaryParams& p, bool backward, cudaStream_t stream) {
-    if (p.fast) {
-        if (p.bf16) return p.interleaved ? launch_fast<__nv_bfloat16, true>(p, backward, stream)
-                                         : launch_fast<__nv_bfloat16, false>(p, backward, stream);
-        return p.interleaved ? launch_fast<float, true>(p, backward, stream)
-                             : launch_fast<float, false>(p, backward, stream);
-    }
+template <typename T, bool AXES>
+int launch_type(const RotaryParams& p, bool backward, cudaStream_t stream) {
+    if (p.fast)
+        return p.interleaved ? launch_fast<T, true, AXES>(p, backward, stream) : launch_fast<T, false, AXES>(p, backward, stream);
     constexpr int WARPS = THREADS / 32;
     const int64_t tokens = (int64_t)p.B * p.T;
     const dim3 grid((unsigned)(backward ? p.chunks : (tokens + WARPS - 1) / WARPS), (unsigned)p.head_blocks);
-    if (!backward)
-        return pdl_launch(p.bf16 ? rotary_any_kernel<__nv_bfloat16> : rotary_any_kernel<float>, grid, THREADS, 0, stream, p);
-    if (p.bf16) rotary_bwd_any_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p);
-    else rotary_bwd_any_kernel<float><<<grid, THREADS, 0, stream>>>(p);
+    if (!backward) return pdl_launch(rotary_any_kernel<T, AXES>, grid, THREADS, 0, stream, p);
+    rotary_bwd_any_kernel<T, AXES><<<grid, THREADS, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch(const RotaryParams& p, bool backward, cudaStream_t stream) {
+    if (p.axes > 0)
+        return p.bf16 ? launch_type<__nv_bfloat16, true>(p, backward, stream) : launch_type<float, true>(p, backward, stream);
+    return p.bf16 ? launch_type<__nv_bfloat16, false>(p, backward, stream) : launch_type<float, false>(p, backward, stream);
 }
 
 void set_head_blocks(RotaryParams* p, int hpb) {

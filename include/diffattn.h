@@ -546,6 +546,43 @@ int diffattn_rotary_bwd(const diffattn_rotary_desc *desc, const void *q1, const 
 size_t diffattn_rotary_bwd_workspace_bytes(const diffattn_rotary_desc *desc);
 
 /*
+ * Positions with several axes: time, height and width of an image's or a video's tokens.
+ * The R / 2 rotated pairs fall into n sections (1 .. DIFFATTN_MAX_AXES), pairs[a] >= 1 of
+ * them for axis a, in turn, R / 2 in all; a pair i of section a is turned by entry i of the
+ * tables' row positions[b, t, a].  pos_stride: element stride of a token's positions (>= 0;
+ * along B and T they go by the descriptor's pos_stride).
+ */
+#define DIFFATTN_MAX_AXES 4
+typedef struct {
+    int32_t n;
+    int32_t pairs[DIFFATTN_MAX_AXES];
+    int32_t reserved;
+    int64_t pos_stride;
+} diffattn_axes;
+
+/*
+ * diffattn_rotary_axes, diffattn_rotary_axes_bwd, diffattn_paged_append_axes -- as
+ * diffattn_rotary, diffattn_rotary_bwd and diffattn_paged_append, with positions [B, T, n]
+ * of `axes`, which must be given.  A token with any position outside the tables is one
+ * whose position is.  axes NULL: the calls without it.  The workspace is that of
+ * diffattn_rotary_bwd.  Sections of other widths than multiples of 4 run a warp a row.
+ * Errors: theirs, and DIFFATTN_ERR_INVALID for bad axes or missing positions.
+ */
+int diffattn_rotary_axes(const diffattn_rotary_desc *desc, const diffattn_axes *axes,
+                         const void *q1, const void *k1, const void *q2, const void *k2,
+                         const float *q_weight, const float *k_weight, const float *cos,
+                         const float *sin, const void *positions, void *q1_out, void *k1_out,
+                         void *q2_out, void *k2_out, diffattn_stream_t stream);
+int diffattn_rotary_axes_bwd(const diffattn_rotary_desc *desc, const diffattn_axes *axes,
+                             const void *q1, const void *k1, const void *q2, const void *k2,
+                             const float *q_weight, const float *k_weight, const float *cos,
+                             const float *sin, const void *positions, const void *dq1_out,
+                             const void *dk1_out, const void *dq2_out, const void *dk2_out,
+                             void *dq1, void *dk1, void *dq2, void *dk2, float *dq_weight,
+                             float *dk_weight, void *workspace, size_t workspace_bytes,
+                             diffattn_stream_t stream);
+
+/*
  * A paged key/value cache.  K1, K2: [num_pages, Hk, page_size, D], V:
  * [num_pages, Hk, page_size, Dv], by element strides ([0] = page, [1] = head, [2] =
  * slot; innermost 1).  The cached token i of sequence b is in slot i % page_size of
@@ -580,6 +617,14 @@ typedef struct {
  * one pointer for two caches, and a stride of 0 between slots of a cache.
  */
 int diffattn_paged_append(const diffattn_rotary_desc *desc, int64_t Dv,
+                          const int64_t v_stride[3], const diffattn_pages *pages,
+                          const void *k1, const void *k2, const void *v,
+                          const float *k_weight, const float *cos, const float *sin,
+                          const void *positions, const int32_t *lengths,
+                          const int32_t *new_lengths, const int32_t *block_table,
+                          void *k1_cache, void *k2_cache, void *v_cache,
+                          diffattn_stream_t stream);
+int diffattn_paged_append_axes(const diffattn_rotary_desc *desc, const diffattn_axes *axes, int64_t Dv,
                           const int64_t v_stride[3], const diffattn_pages *pages,
                           const void *k1, const void *k2, const void *v,
                           const float *k_weight, const float *cos, const float *sin,

@@ -189,3 +189,41 @@ def test_binding_refuses_cpu_tensors():
         da.differential_cross_attention(x, x, x, x, x, 0.5)
     with pytest.raises(ValueError, match="no CPU path"):
         da.differential_head_norm(x)
+
+
+# ------------------------------------------------------------------ positions with several axes
+def test_axes_layout_and_refusals(lib):
+    assert ctypes.sizeof(_lib.DiffattnAxes) == 4 * 6 + 8
+
+    def axes(n, *pairs, reserved=0, stride=1):
+        a = _lib.DiffattnAxes()
+        a.n, a.reserved, a.pos_stride = n, reserved, stride
+        for i, v in enumerate(pairs):
+            a.pairs[i] = v
+        return a
+
+    def rotary(a, R=64, pos=p(30)):
+        d = _lib.DiffattnRotaryDesc()
+        d.B, d.T, d.D, d.H, d.Hk, d.dtype, d.rotary_dim, d.norm, d.eps, d.table_rows = 2, 5, 64, 4, 2, 0, R, 1, 1e-6, 100
+        return [lib.diffattn_rotary_axes(ctypes.byref(d), ctypes.byref(a), p(0), None, None, None, None, None, p(20), p(21), pos,
+                                         p(4), None, None, None, None),
+                lib.diffattn_rotary_axes_bwd(ctypes.byref(d), ctypes.byref(a), p(0), None, None, None, None, None, p(20), p(21), pos,
+                                             p(8), None, None, None, p(4), None, None, None, None, None, p(40), 1 << 30, None)]
+    for a in (axes(0), axes(5, 8, 8, 8, 8), axes(2, 16, 15), axes(2, 16, 17), axes(2, 32, 0), axes(2, -1, 33), axes(1, 33),
+              axes(1, 32, reserved=1), axes(1, 32, stride=-1), axes(-1)):
+        assert rotary(a) == [INVALID, INVALID]
+    assert rotary(axes(1, 32), pos=None) == [INVALID, INVALID]
+    assert rotary(axes(1, 1), R=0) == [INVALID, INVALID]
+
+
+def test_tables_of_sections():
+    cos, sin = da.rotary_tables(300, 24, sections=(2, 4, 6))
+    f = [100.0 ** -i for i in range(2)] + [10.0 ** -i for i in range(4)] + [10000.0 ** (-i / 6) for i in range(6)]
+    a = torch.arange(300, dtype=torch.float64)[:, None] * torch.tensor(f, dtype=torch.float64)
+    # half a step of a float32 below 1, and the float64 angles' own errors
+    assert ((cos.double() - a.cos()).abs() <= 2.0 ** -25 + 1e-11).all() and ((sin.double() - a.sin()).abs() <= 2.0 ** -25 + 1e-11).all()
+    one = da.rotary_tables(50, 16, sections=(8,))
+    assert all(torch.equal(x, y) for x, y in zip(one, da.rotary_tables(50, 16)))
+    for bad in ((), (4, 5), (8, 0), (12,)):
+        with pytest.raises(ValueError):
+            da.rotary_tables(50, 16, sections=bad)
