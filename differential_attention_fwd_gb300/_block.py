@@ -27,7 +27,8 @@ def differential_cross_attention(q1: torch.Tensor, k1: torch.Tensor, q2: torch.T
     tensor for both branches.  kv_lengths: [B] int32 on the device, sequence b has only its
     first kv_lengths[b] states (None: all Tk), and what lies behind them has no influence,
     NaN included; one with none gives zeros (before the epilogue).  coefficient, out and the
-    epilogue (norm .. out_scale) as differential_attention; out may not overlap the inputs.
+    epilogue (norm .. out_scale) as differential_attention, norm_weight and norm_bias with a
+    norm alone; out may not overlap the inputs.
 
     Returns [B, H, Tq, Dv].  Differentiable in q1, q2, k1, k2, value and a tensor coefficient,
     backward and once, without out and the epilogue (differential_head_norm has gradients);

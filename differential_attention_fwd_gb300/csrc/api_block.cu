@@ -120,6 +120,138 @@ bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
 
 int64_t cross_rows(const diffattn_cross_desc& d) { return d.B * d.H * d.Tq; }
 
+// Strides that TMA takes, of the dimensions that are stepped.
+bool tma_rows(const void* p, const int64_t n[3], const int64_t s[3]) {
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] % 8 != 0 || s[i] <= 0 || s[i] >= (int64_t(1) << 38))) return false;
+    return aligned16(p);
+}
+
+// Whether the tensor cores take the shape: bf16, value width 128, Q/K width 64 or 128.
+bool tc_shape(const diffattn_cross_desc& d) {
+    return d.dtype == DIFFATTN_BF16 && width_of(d) == 128 && (d.D == 64 || d.D == 128);
+}
+// And the call's layout.
+bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, const void* q2, const void* k2, const void* v) {
+    const int64_t nq[3] = {d.B, d.H, d.Tq}, nk[3] = {d.B, d.H / group_of(d), d.Tk};
+    return tc_shape(d) && tma_rows(q1, nq, d.q1_stride) && tma_rows(q2, nq, d.q2_stride) && tma_rows(k1, nk, d.k1_stride) &&
+           tma_rows(k2, nk, d.k2_stride) && tma_rows(v, nk, d.v_stride);
+}
+
+// Heads that the persistent kernels work on at a time, each streaming `bytes`: about 48 MiB of
+// them (they then share the L2), with an item of `tiles` for every SM.
+int heads_at_once(int64_t heads, int64_t bytes, int64_t tiles, int sms) {
+    int64_t g = (48ll << 20) / (bytes > 0 ? bytes : 1);
+    const int64_t least = (sms + tiles - 1) / tiles;
+    if (g < least) g = least;
+    return (int)(g < 1 ? 1 : g > heads ? heads : g);
+}
+
+// Maps of Q1, K1, Q2, K2, V and a tensor of O's shape, with boxes of 64 columns and so many rows.
+int cross_maps(CUtensorMap* m, const CrossParams& p, const void* o, const int64_t so[3], int q_rows, int k_rows, int o_rows) {
+    const int64_t qd[4] = {p.D, p.Tq, p.H, p.B}, kd[4] = {p.D, p.Tk, p.Hk, p.B};
+    const int64_t vd[4] = {p.Dv, p.Tk, p.Hk, p.B}, od[4] = {p.Dv, p.Tq, p.H, p.B};
+    return encode_map_4d(&m[0], p.q1, qd, p.s_q1, 64, q_rows) == DIFFATTN_OK &&
+                   encode_map_4d(&m[1], p.k1, kd, p.s_k1, 64, k_rows) == DIFFATTN_OK &&
+                   encode_map_4d(&m[2], p.q2, qd, p.s_q2, 64, q_rows) == DIFFATTN_OK &&
+                   encode_map_4d(&m[3], p.k2, kd, p.s_k2, 64, k_rows) == DIFFATTN_OK &&
+                   encode_map_4d(&m[4], p.v, vd, p.s_v, 64, k_rows) == DIFFATTN_OK &&
+                   encode_map_4d(&m[5], o, od, so, 64, o_rows) == DIFFATTN_OK
+               ? DIFFATTN_OK
+               : DIFFATTN_ERR_CUDA;
+}
+
+// The forward on the tensor cores; `counter`: 64 bytes of workspace.
+int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream) {
+    CUtensorMap maps[6];
+    if (cross_maps(maps, c, c.out, c.s_o, 128, 64, 32) != DIFFATTN_OK) return DIFFATTN_ERR_CUDA;
+    TcParams p{};
+    p.B = c.B;
+    p.H = c.H;
+    p.T = c.Tq;
+    p.Tk = c.Tk;
+    p.nq = (c.Tq + 127) / 128;
+    p.nk = (c.Tk + 63) / 64;
+    p.total_items = c.B * c.H * p.nq;
+    p.group = heads_at_once((int64_t)c.B * c.H, (int64_t)c.Tk * ((c.k_shared ? 1 : 2) * c.D + c.Dv) * 2, p.nq, sms);
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.D));
+    p.lambda = c.lambda;
+    p.lambda_dev = c.lambda_dev;
+    p.out = static_cast<__nv_bfloat16*>(c.out);
+    p.o_sB = c.s_o[0];
+    p.o_sH = c.s_o[1];
+    p.o_sT = c.s_o[2];
+    p.status = c.status;
+    p.norm = c.norm;
+    p.norm_eps = c.norm_eps;
+    p.norm_weight = c.norm_weight;
+    p.norm_bias = c.norm_bias;
+    p.out_scale = c.out_scale;
+    p.kv_group = c.group;
+    p.k_shared = c.k_shared;
+    p.out2 = static_cast<__nv_bfloat16*>(c.out2);
+    p.lse = c.lse;
+    p.lengths = c.lengths;
+    const int grid = p.total_items < sms ? p.total_items : sms;
+    if (p.total_items > sms) {          // items are claimed from a counter: sequences differ in length
+        p.sched = static_cast<uint32_t*>(counter);
+        if (cudaMemsetAsync(counter, 0, 64, stream) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+    }
+    return launch_cross_tc(maps, p, c.D, grid, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+}
+
+// The backward on the tensor cores; `counters`: two words of workspace.
+int backward_tc(const CrossParams& c, int sms, uint32_t* counters, cudaStream_t stream) {
+    PrepParams pp{};
+    pp.B = c.B;
+    pp.H = c.H;
+    pp.T = c.Tq;
+    pp.Dv = c.Dv;
+    pp.bf16 = 1;
+    pp.log2_negated = 1;
+    pp.lambda = c.lambda;
+    pp.lambda_dev = c.lambda_dev;
+    pp.out = c.out;
+    pp.out2 = c.out2;
+    pp.dout = c.dout;
+    copy3(pp.s_o, c.s_o);
+    copy3(pp.s_do, c.s_do);
+    pp.lse = c.lse;
+    pp.stats = c.stats;
+    pp.counters = counters;
+    CUtensorMap maps[12];
+    if (cross_maps(maps, c, c.dout, c.s_do, 128, 64, 128) != DIFFATTN_OK ||
+        cross_maps(maps + 6, c, c.dout, c.s_do, 64, 128, 64) != DIFFATTN_OK || launch_bwd_prep(pp, stream) != 0)
+        return DIFFATTN_ERR_CUDA;
+    CrossTcParams p{};
+    p.B = c.B;
+    p.H = c.H;
+    p.Hk = c.Hk;
+    p.group = c.group;
+    p.Tq = c.Tq;
+    p.Tk = c.Tk;
+    p.nq128 = (c.Tq + 127) / 128;
+    p.nq64 = (c.Tq + 63) / 64;
+    p.nk128 = (c.Tk + 127) / 128;
+    p.k_shared = c.k_shared;
+    p.group_q = heads_at_once((int64_t)c.B * c.H, (int64_t)c.Tk * ((c.k_shared ? 1 : 2) * c.D + c.Dv) * 2, p.nq128, sms);
+    p.group_k = heads_at_once((int64_t)c.B * c.Hk, (int64_t)c.Tq * c.group * (2 * c.D + c.Dv) * 2, p.nk128, sms);
+    p.scale = c.scale;
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.D));
+    p.lambda = c.lambda;
+    p.lambda_dev = c.lambda_dev;
+    p.lengths = c.lengths;
+    p.status = c.status;
+    p.sched = counters;
+    p.stats = c.stats;
+    p.dq1 = c.dq1;
+    p.dq2 = c.dq2;
+    p.dk1 = c.dk1;
+    p.dk2 = c.dk2;
+    p.dv = c.dv;
+    return launch_cross_bwd_tc(maps, p, c.D, sms, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace diffattn
 
@@ -129,13 +261,13 @@ extern "C" {
 
 size_t diffattn_cross_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
-    return 16;
+    return 64;                          // an item counter
 }
 
 size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
-    // the rows' statistics, and partial sums of dlambda
-    return (size_t)(cross_rows(*desc) * 4 + 128) * sizeof(float);
+    // the rows' statistics, partial sums of dlambda, and item counters
+    return (size_t)(cross_rows(*desc) * 4 + 128 + 4) * sizeof(float);
 }
 
 int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
@@ -152,7 +284,8 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     diffattn_epilogue e;
     rc = check_epilogue(epi, &e);
     if (rc != DIFFATTN_OK) return rc;
-    if (out2 && (e.norm != DIFFATTN_NORM_NONE || e.weight || e.bias || e.out_scale != 1.f)) return DIFFATTN_ERR_INVALID;
+    if (e.norm == DIFFATTN_NORM_NONE && (e.weight || e.bias)) return DIFFATTN_ERR_INVALID;
+    if (out2 && (e.norm != DIFFATTN_NORM_NONE || e.out_scale != 1.f)) return DIFFATTN_ERR_INVALID;
     if (!workspace_ok(workspace, workspace_bytes, diffattn_cross_workspace_bytes(desc))) return DIFFATTN_ERR_INVALID;
     CrossParams p{};
     fill_cross(&p, d, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev);
@@ -167,7 +300,10 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     int sms = 0;
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
-    return launch_cross_simt(p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(out, rows, d.o_stride) && (!out2 || aligned16(out2)))
+        return forward_tc(p, sms, workspace, st);
+    return launch_cross_simt(p, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
 int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
@@ -200,9 +336,19 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (launch_cross_simt_bwd(p, st) != 0) return DIFFATTN_ERR_CUDA;
+    // two key tensors 128 wide leave no TMEM for their gradients' accumulators
+    const int64_t rows[3] = {d.B, d.H, d.Tq};
+    const bool tc = tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(dout, rows, d.dout_stride) && (d.D == 64 || p.k_shared) &&
+                    aligned16(dq1) && aligned16(dk1) && aligned16(dq2) && aligned16(dk2) && aligned16(dv);
+    if (tc) {
+        rc = backward_tc(p, sms, reinterpret_cast<uint32_t*>(p.stats + cross_rows(d) * 4 + 128), st);
+        if (rc != DIFFATTN_OK) return rc;
+    } else if (launch_cross_simt_bwd(p, st) != 0) {
+        return DIFFATTN_ERR_CUDA;
+    }
     if (!dlambda) return DIFFATTN_OK;
-    return launch_bwd_dlambda(p.stats, cross_rows(d), -1.0f, dlambda, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+    // the tensor-core path's rows hold -Dd_2
+    return launch_bwd_dlambda(p.stats, cross_rows(d), tc ? 1.0f : -1.0f, dlambda, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
 int diffattn_head_norm(const diffattn_norm_desc* desc, const void* x, const float* weight, const float* bias, void* y,

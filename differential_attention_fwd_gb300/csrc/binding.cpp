@@ -983,6 +983,7 @@ PyObject* cross(PyObject* const* a) {
     const Tensor w = affine(a[10], "norm_weight", d.H, d.Dv, dev, &w_given);
     const Tensor b = affine(a[11], "norm_bias", d.H, d.Dv, dev, &b_given);
     no_tangent({&w_given, &b_given}, kCross);
+    if (e.norm == DIFFATTN_NORM_NONE && (w.defined() || b.defined())) bad_value("norm_weight and norm_bias need norm='rms' or 'group'");
     const bool epilogue = e.norm != DIFFATTN_NORM_NONE || w.defined() || b.defined() || e.out_scale != 1.f;
     if ((grad && (epilogue || !is_none(a[7]))) || wants_grad({&w_given, &b_given}))
         bad_value("gradients are available for the bare operation only (no out=, norm or out_scale): apply "

@@ -79,6 +79,24 @@ __device__ __forceinline__ CrossLen cross_len(const int32_t* lengths, int b, int
 }
 #endif
 
+// Parameters of the tensor-core backward (bf16, Dv = 128, D = 64, or 128 with one key tensor).
+struct CrossTcParams {
+    int B, H, Hk, group, Tq, Tk;
+    int nq128, nq64, nk128;     // tiles along Tq and Tk
+    int group_q, group_k;       // heads, and key/value heads, that are worked on at a time
+    int k_shared;
+    float scale, scale_log2;
+    float lambda;
+    const float* lambda_dev;
+    const int32_t* lengths;
+    uint32_t* status;
+    uint32_t* sched;            // 2 item counters, zero
+    float* stats;               // rows of -lse_1, -lse_2 (log2), -Dd_1, -Dd_2; the exact Dd out
+    void* dq1; void* dq2; void* dk1; void* dk2; void* dv;
+};
+int launch_cross_bwd_tc(const CUtensorMap* maps /*dq: q1,k1,q2,k2,v,do; dkdv: the same*/, const CrossTcParams& p,
+                        int head_dim, int num_sms, cudaStream_t stream);
+
 // The CUDA-core kernels: any D <= 128, Dv <= 256, type and layout.
 int launch_cross_simt(const CrossParams& p, cudaStream_t stream);
 int launch_cross_simt_bwd(const CrossParams& p, cudaStream_t stream);

@@ -29,7 +29,7 @@
 //   warp  8     TMA producer
 //   warp  9     TMEM allocation; MMA issue for branch 1
 //   warp  10    MMA issue for branch 2
-//   warp  11    idle (it completes the third warpgroup)
+//   warp  11    idle (it completes the third warpgroup); CROSS: cleans value tiles
 // One MMA-issuing thread per branch, so each branch's PV and next score
 // product go to the tensor core as soon as that branch's P is ready.
 // Registers: launched at 168 per thread (384 x 168 = 64512); the third
@@ -58,6 +58,13 @@
 // loaded; tiles that cross the diagonal mask key > query with -inf before the
 // row max.
 //
+// Cross attention (the CROSS instances): the keys and values of batch b are the first
+// lengths[b] of Tk rows, without a causal mask.  Items take as many key tiles as their
+// sequence has; its last tile's scores are masked, and warp 11 turns the value rows behind
+// the last state into zeros before the product reads them (a weight of 0 times what a
+// batch's padding holds, NaN or infinite, would not be 0).  An item without a state is
+// written by the softmax warps alone.
+//
 // Streaming softmax: the running max m is kept in log2 units of the scaled
 // scores.  O and l are rescaled only when a tile's row max exceeds m by more
 // than 8 (a factor 256), so P stays <= 256 and the rescale (a TMEM
@@ -65,6 +72,8 @@
 // conditional-rescale idea of FlashAttention-4; the final O / l is exact
 // whichever m was used.
 #include "ptx.cuh"
+#include "block.h"
+#include "item_ring.cuh"
 #include "kernels.h"
 
 namespace diffattn {
@@ -133,7 +142,8 @@ constexpr int BAR_ITEM_EMPTY = BAR_ITEM_FULL + ITEM_RING;  // [ITEM_RING] 10 con
 constexpr int NUM_ITEM_CONSUMERS = 10;                  // 2 MMA warps + 8 softmax warps
 constexpr int BAR_NORM_A = BAR_ITEM_EMPTY + ITEM_RING;  // per-row partial sums of both halves
 constexpr int BAR_NORM_B = BAR_NORM_A + 1;              // per-row partial squared deviations
-constexpr int NUM_BARS = BAR_NORM_B + 1;
+constexpr int BAR_V_CLEAN = BAR_NORM_B + 1;             // CROSS: [stage] value tile without foreign rows
+constexpr int NUM_BARS = BAR_V_CLEAN + VSTAGES_MAX;
 // small state after the barriers (offsets from OFF_BAR)
 constexpr uint32_t REL_TMEM_PTR = NUM_BARS * 8;
 constexpr uint32_t REL_ABORT = REL_TMEM_PTR + 4;
@@ -155,6 +165,8 @@ __device__ __forceinline__ uint32_t tm_s(int br, int buf) { return br * 128 + bu
 
 struct Item {
     int qt, b, h, n_kv;
+    int len;        // CROSS: the sequence's states,
+    bool bad;       // and whether its length is outside 0 .. Tk (then 0 states and NaN)
 };
 
 // The CTA's k-th work item in a boustrophedon order over the item list, so
@@ -168,6 +180,7 @@ __device__ __forceinline__ int item_index(int k, int cta, int grid) {
 // fits comfortably in L2, so the CTAs working at the same time share it);
 // within a group, items run longest first (causal: last query tile first),
 // then head by head.
+template <bool CROSS>
 __device__ __forceinline__ Item decode_item(int idx, const TcParams& p) {
     const int BH = p.B * p.H;
     const int per_group = p.group * p.nq;
@@ -178,6 +191,16 @@ __device__ __forceinline__ Item decode_item(int idx, const TcParams& p) {
     const int r = w / gsize;
     const int bh = g0 + (w - r * gsize);
     Item it;
+    if constexpr (CROSS) {
+        it.qt = r;
+        it.b = bh / p.H;
+        it.h = bh - it.b * p.H;
+        const CrossLen len = cross_len(p.lengths, it.b, p.Tk);
+        it.len = len.n;
+        it.bad = len.bad;
+        it.n_kv = (len.n + BN - 1) / BN;
+        return it;
+    }
     it.qt = p.causal ? (p.nq - 1 - r) : r;
     it.b = bh / p.H;
     it.h = bh - it.b * p.H;
@@ -186,35 +209,6 @@ __device__ __forceinline__ Item decode_item(int idx, const TcParams& p) {
     it.n_kv = p.causal ? min((it.qt * BM + BM - 1 + p.kv_off) / BN + 1, p.nk) : p.nk;
     return it;
 }
-
-// Work items are published by the producer thread into a small ring in shared
-// memory; every consumer warp reads the same sequence.  With a scheduler
-// counter (p.sched != nullptr) each CTA claims its next item from a global
-// counter when it needs one, so SMs that run slower simply take fewer items;
-// without one, CTA c takes the static boustrophedon sequence.  -1 ends the
-// sequence.
-struct ItemRing {
-    uint64_t* bars;
-    volatile int* slots;
-    const AbortState* ab;
-    // consumer side, single thread (the MMA-issuing thread of its warp)
-    __device__ __forceinline__ bool get_one(int k, int& idx) const {
-        const int s = k % ITEM_RING;
-        if (!mbar_wait(&bars[BAR_ITEM_FULL + s], (uint32_t)(k / ITEM_RING) & 1u, *ab)) return false;
-        idx = slots[s];
-        mbar_arrive(&bars[BAR_ITEM_EMPTY + s]);
-        return true;
-    }
-    // consumer side, whole warp (all lanes call; lane 0 arrives for the warp)
-    __device__ __forceinline__ bool get(int k, int& idx) const {
-        const int s = k % ITEM_RING;
-        if (!mbar_wait_warp(&bars[BAR_ITEM_FULL + s], (uint32_t)(k / ITEM_RING) & 1u, *ab)) return false;
-        idx = slots[s];
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&bars[BAR_ITEM_EMPTY + s]);
-        return true;
-    }
-};
 
 // Wait profile (only in a separate build of the library compiled with
 // -DDIFFATTN_WAIT_PROFILE; the regular build has none of it): each role's
@@ -341,7 +335,7 @@ __device__ __forceinline__ float tile_exp2(const float (&s)[64], float sl2, floa
     return f2_lo(r) + f2_hi(r);
 }
 
-template <int HD>
+template <int HD, bool CROSS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                        const __grid_constant__ CUtensorMap tm_k1,
@@ -395,8 +389,10 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
         mbar_init(&bars[BAR_FINAL + 1], 1);
         for (int i = 0; i < ITEM_RING; ++i) {
             mbar_init(&bars[BAR_ITEM_FULL + i], 1);
-            mbar_init(&bars[BAR_ITEM_EMPTY + i], NUM_ITEM_CONSUMERS);
+            mbar_init(&bars[BAR_ITEM_EMPTY + i], NUM_ITEM_CONSUMERS + (CROSS ? 1 : 0));
         }
+        if constexpr (CROSS)
+            for (int s = 0; s < C::VSTAGES; ++s) mbar_init(&bars[BAR_V_CLEAN + s], 1);
         mbar_init(&bars[BAR_NORM_A], 8);
         mbar_init(&bars[BAR_NORM_B], 8);
         *abort_flag = 0;
@@ -413,7 +409,8 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
 
     const int grid = gridDim.x;
     const int cta = blockIdx.x;
-    const ItemRing ring{bars, reinterpret_cast<volatile int*>(smem + C::OFF_BAR + REL_RING), &ab};
+    const ItemRing<ITEM_RING> ring{bars + BAR_ITEM_FULL, bars + BAR_ITEM_EMPTY,
+                                   reinterpret_cast<volatile int*>(smem + C::OFF_BAR + REL_RING), &ab};
 
     if (warp >= 8) {
       regs_dec<REGS_OTHER>();
@@ -460,7 +457,12 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 ring.slots[slot] = idx;
                 mbar_arrive(&bars[BAR_ITEM_FULL + slot]);
                 if (idx < 0) break;
-                const Item it = decode_item(idx, p);
+                const Item it = decode_item<CROSS>(idx, p);
+                if (CROSS && it.n_kv == 0) {
+                    if (it.bad) atomicOr(p.status, kStatusIndex);
+                    idx = claim();
+                    continue;
+                }
                 if (!first) {
                     if (!(ok = TIMED_WAIT(wp, kWaitItemStart, mbar_wait(&bars[BAR_Q_EMPTY], qph, ab)))) break;
                     qph ^= 1;
@@ -558,8 +560,9 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             for (int k = 0; ok; ++k) {
                 int idx = -1;
                 if (!(ok = TIMED_WAIT(wp, kWaitPeer, ring.get_one(k, idx))) || idx < 0) break;
-                const Item it = decode_item(idx, p);
+                const Item it = decode_item<CROSS>(idx, p);
                 const int n = it.n_kv;
+                if (CROSS && n == 0) continue;
                 if (!(ok = TIMED_WAIT(wp, kWaitQ, mbar_wait(&bars[BAR_Q_FULL], qph, ab)))) break;
                 qph ^= 1;
                 // S_b(0), S_b(1) into buffers 0 and 1
@@ -581,6 +584,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     // their barriers are checked first: once P_b(j) arrives,
                     // both products issue with no other wait in between.
                     if (!(ok = TIMED_WAIT(wp, kWaitV, mbar_wait(&bars[BAR_V_FULL + vst], vph, ab)))) break;
+                    if (CROSS && p.lengths && !(ok = mbar_wait(&bars[BAR_V_CLEAN + vst], vph, ab))) break;
                     if (j + 2 < n &&
                         !(ok = KEY_WAIT(wp, kst, mbar_wait(&bars[BAR_K_FULL + kst], kph, ab))))
                         break;
@@ -617,6 +621,34 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             wp.flush(1, true);
         }
         __syncwarp();
+      } else if (CROSS) {
+        // ------------------------------- value rows behind a sequence's last state
+        // This warp sees every value tile land, in turn, before the products take it.
+        int vst = 0;
+        uint32_t vph = 0;
+        int idx = -1;
+        for (int k = 0; ring.get(k, idx) && idx >= 0; ++k) {
+            if (!p.lengths) continue;
+            const Item it = decode_item<CROSS>(idx, p);
+            bool ok = true;
+            for (int j = 0; j < it.n_kv; ++j) {
+                if (!(ok = mbar_wait_warp(&bars[BAR_V_FULL + vst], vph, ab))) break;
+                const int live = it.len - j * BN;
+                if (live < BN && it.len < p.Tk) {
+                    // rows of 128 bytes in each half: the swizzle stays inside a row
+                    uint8_t* v = smem + C::OFF_V + vst * V_BYTES;
+                    for (int i = live * 8 + lane; i < BN * 8; i += 32) {
+                        reinterpret_cast<uint4*>(v)[i] = make_uint4(0, 0, 0, 0);
+                        reinterpret_cast<uint4*>(v + V_HALF_BYTES)[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&bars[BAR_V_CLEAN + vst]);
+                if (++vst == C::VSTAGES) { vst = 0; vph ^= 1; }
+            }
+            if (!ok) break;
+        }
       }
     } else {
         regs_inc<REGS_SOFTMAX>();
@@ -639,7 +671,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
         int idx = -1;
         Item next{};
         ok = TIMED_WAIT(wp, kWaitPeer, ring.get(0, idx));
-        if (ok && idx >= 0) next = decode_item(idx, p);
+        if (ok && idx >= 0) next = decode_item<CROSS>(idx, p);
         for (int k = 0; ok && idx >= 0; ++k) {
             const Item it = next;
             const int q = it.qt * BM + row;
@@ -664,7 +696,13 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
 
                 const int kv0 = j * BN;
-                if (p.causal) {
+                if constexpr (CROSS) {
+                    if (kv0 + BN > it.len) {
+                        const int lim = it.len - kv0;         // keys behind the sequence's states
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) s[c] = (c >= lim) ? -INFINITY : s[c];
+                    }
+                } else if (p.causal) {
                     if (kv0 + BN - 1 > it.qt * BM + p.kv_off) {   // the tile crosses the diagonal
                         const int lim = q + p.kv_off - kv0;        // keys kv0 + c with c > lim are in the future
 #pragma unroll
@@ -737,14 +775,30 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             // The next item is fetched and decoded here, while the item's last
             // PV products complete, rather than after the epilogue.
             if (!(ok = TIMED_WAIT(wp, kWaitPeer, ring.get(k + 1, idx)))) break;
-            if (idx >= 0) next = decode_item(idx, p);
+            if (idx >= 0) next = decode_item<CROSS>(idx, p);
 
             // ---------------------------------------------------- epilogue
+            const int c0 = br * 64;          // this warpgroup writes output columns [c0, c0+64)
+            float r[64];
+            const bool none = CROSS && it.n_kv == 0;
+            if (none) {
+                // no state: zeros (NaN for a bad length), from these warps alone
+                const float fill = it.bad ? __int_as_float(0x7fc00000) : 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) r[c] = fill;
+                if (p.out2 && q < p.T) {
+                    const uint32_t w = pack_bf16x2(fill, fill);
+                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + it.h * p.o_sH + (int64_t)q * p.o_sT + c0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(o2row + 8 * i) = make_uint4(w, w, w, w);
+                    p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] = it.bad ? fill : -INFINITY;
+                }
+            } else {
             if (!(ok = TIMED_WAIT(wp, kWaitEpilogue, mbar_wait_warp(&bars[BAR_O_FULL], ofph, ab)))) break;
             PROF_MARK(epi_t0);
             ofph ^= 1;
             tc_fence_after();
-            if (p.stats) {
+            if (!CROSS && p.stats) {
                 // Row statistics for the backward: this branch's log2-sum-exp
                 // and Dd_b = dO . (O_b / l_b), 32 columns at a time.
                 const bool live = q < p.T;
@@ -784,7 +838,6 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 continue;
             }
             inv_l[br * BM + row] = 1.0f / l;
-            const int c0 = br * 64;          // this warpgroup writes output columns [c0, c0+64)
             uint32_t o1[64], o2[64];
             tmem_ld32(lane_base + TM_O + c0, &o1[0]);
             tmem_ld32(lane_base + TM_O + c0 + 32, &o1[32]);
@@ -825,13 +878,16 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             // O = O1 / l1 - lambda O2 / l2 for this thread's 64 columns: a = O1 / l1
             // and b = O2 / l2 rounded, then a - lambda b in one fused step
             // (identical branches at lambda = 1 give a = b, hence exactly 0)
-            float r[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
                 const float a = __fmul_rn(__uint_as_float(o1[c]), inv1);
                 const float bb = __fmul_rn(__uint_as_float(o2[c]), inv2);
                 r[c] = __fmaf_rn(bb, -lam, a);
             }
+            PROF_ADD(wp, kEpiMath, math_t0);
+            PROF_ADD(wp, kEpilogueBusy, epi_t0);
+            }
+            PROF_MARK(norm_t0);
             if (p.norm != kNormNone) {
                 // Per-head normalisation over the row's 2D = 128 channels; the
                 // two warpgroups hold 64 channels each and exchange partial
@@ -883,7 +939,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             // swizzled rows, as the output tensor map expects) and write them
             // with one TMA store; rows at or past T are clipped by the TMA unit.
             uint8_t* stage = smem + C::OFF_OUT + br * (OUT_BYTES / 2) + quad * 4096;
-            PROF_ADD(wp, kEpiMath, math_t0);
+            PROF_ADD(wp, kEpiMath, norm_t0);
             PROF_MARK(stage_t0);
             if (lane == 0) bulk_wait_read_all();     // the previous store has read the buffer
             __syncwarp();
@@ -903,7 +959,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 bulk_commit();
             }
             PROF_ADD(wp, kEpiStore, store_t0);
-            PROF_ADD(wp, kEpilogueBusy, epi_t0);
+            PROF_ADD(wp, kEpilogueBusy, norm_t0);
         }
         // Every output store must be complete before the CTA exits.
         if (lane == 0) bulk_wait_all();
@@ -932,13 +988,13 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
 }  // namespace tc
 
 namespace {
-template <int HD>
+template <int HD, bool CROSS>
 int launch_hd(const CUtensorMap* maps, const TcParams& p, int grid, cudaStream_t stream) {
     constexpr uint32_t smem = tc::smem_bytes<HD>();
-    cudaError_t e = cudaFuncSetAttribute(tc::diffattn_fwd_tc_kernel<HD>,
+    cudaError_t e = cudaFuncSetAttribute(tc::diffattn_fwd_tc_kernel<HD, CROSS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return -1;
-    tc::diffattn_fwd_tc_kernel<HD><<<grid, tc::NUM_THREADS, smem, stream>>>(
+    tc::diffattn_fwd_tc_kernel<HD, CROSS><<<grid, tc::NUM_THREADS, smem, stream>>>(
         maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -969,8 +1025,14 @@ extern "C" int diffattn_wait_profile(unsigned long long* out, int n) {
 int launch_fwd_tc(const CUtensorMap* maps, const TcParams& p, int head_dim, int grid,
                   cudaStream_t stream) {
     static_assert(sizeof(CUtensorMap) == 128, "tensor map size");
-    if (head_dim == 64) return launch_hd<64>(maps, p, grid, stream);
-    if (head_dim == 128) return launch_hd<128>(maps, p, grid, stream);
+    if (head_dim == 64) return launch_hd<64, false>(maps, p, grid, stream);
+    if (head_dim == 128) return launch_hd<128, false>(maps, p, grid, stream);
+    return -1;
+}
+
+int launch_cross_tc(const CUtensorMap* maps, const TcParams& p, int head_dim, int grid, cudaStream_t stream) {
+    if (head_dim == 64) return launch_hd<64, true>(maps, p, grid, stream);
+    if (head_dim == 128) return launch_hd<128, true>(maps, p, grid, stream);
     return -1;
 }
 

@@ -56,6 +56,7 @@ struct TcParams {
     // + t][branch].
     __nv_bfloat16* out2;
     float* lse;
+    const int32_t* lengths;     // the cross instances: [B], nullptr: Tk each
 };
 
 // Parameters of the CUDA-core kernel (any D <= 128, value width Dv <= 256,
@@ -167,9 +168,11 @@ struct PrepParams {
     float lambda;
     const float* lambda_dev;
     const void* out; const void* out2; const void* dout;
-    int64_t s_o[3];         // shared by out, out2 and dout
+    int64_t s_o[3];         // of out and out2
+    int64_t s_do[3];
     const float* lse;       // [B, H, T, 2]
     float* stats;           // [B, H, T, 4]
+    uint32_t* counters;     // two words to be zeroed, nullptr: none
 };
 
 // Decode helpers: query-row bucket (rows rounded up to 1, 2, 4 or 8; 0 if
@@ -191,6 +194,8 @@ size_t decode_tc_work_floats(int64_t units, int64_t Tk, int tq_bucket);
 // head_dim: the Q/K width, 64 or 128 (the value width is 128 either way).
 int launch_fwd_tc(const CUtensorMap* maps /*q1,k1,q2,k2,v,out*/, const TcParams& p, int head_dim,
                   int grid, cudaStream_t stream);
+// The same over an encoder's states (p.lengths; no causal mask, no row statistics).
+int launch_cross_tc(const CUtensorMap* maps, const TcParams& p, int head_dim, int grid, cudaStream_t stream);
 int launch_bwd_tc(const CUtensorMap* maps /*dq: q1,k1,q2,k2,v,do; dkdv: the same*/,
                   const BwdTcParams& p, int num_sms, cudaStream_t stream);
 // dlambda = sign * (sum over rows of stats[row][3]) (sign -1 when the rows hold

@@ -156,6 +156,7 @@ def test_cross_argument_refusals(lib):
     for epi in (_lib.DiffattnEpilogue(norm=1, eps=1e-5, out_scale=1.0), _lib.DiffattnEpilogue(out_scale=0.5)):
         assert cross_fwd(lib, epi=epi, out2=p(6), lse=p(7)) == INVALID
     assert cross_fwd(lib, epi=_lib.DiffattnEpilogue(norm=9, eps=1e-5, out_scale=1.0)) == INVALID
+    assert cross_fwd(lib, epi=_lib.DiffattnEpilogue(weight=p(50), out_scale=1.0)) == INVALID       # of no norm
     assert cross_fwd(lib, cross_desc(o_stride=(0, 640, 128))) == INVALID
     need = lib.diffattn_cross_bwd_workspace_bytes(ctypes.byref(cross_desc()))
     assert need >= 2 * 4 * 5 * 16

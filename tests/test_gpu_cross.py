@@ -171,9 +171,11 @@ def test_epilogue(dtype, D, Dv, norm, Tq):
     g = torch.Generator().manual_seed(7)
     w, b = (1 + 0.2 * torch.randn(4, Dv, generator=g)), 0.2 * torch.randn(4, Dv, generator=g)
     eps = 1e-3
-    kw = {} if norm is None else dict(norm=norm, norm_eps=eps)
+    kw = {} if norm is None else dict(norm=norm, norm_eps=eps, norm_weight=w.cuda(), norm_bias=b.cuda())
+    if norm is None:                                        # a scale alone
+        w, b = torch.ones(4, Dv), torch.zeros(4, Dv)
     with torch.no_grad():
-        y = da.differential_cross_attention(*x, 0.8, kv_lengths=n, norm_weight=w.cuda(), norm_bias=b.cuda(), out_scale=0.2, **kw)
+        y = da.differential_cross_attention(*x, 0.8, kv_lengths=n, out_scale=0.2, **kw)
     r = reference(x, float(torch.tensor(0.8)), lens)
     w, b = w.double()[:, None], b.double()[:, None]
     tol = r.o_tol - r.h * r.o.abs()                         # O is not rounded on the way
@@ -393,7 +395,8 @@ def test_refusals():
         with pytest.raises(ValueError):
             f(*bad, 0.5)
     for kw in (dict(kv_lengths=lens.long()), dict(kv_lengths=lens[:1]), dict(kv_lengths=lens.cpu()), dict(norm="layer"),
-               dict(out=torch.empty(2, 4, 5, 64, dtype=BF, device="cuda")), dict(norm_weight=torch.ones(3, 128, device="cuda"))):
+               dict(out=torch.empty(2, 4, 5, 64, dtype=BF, device="cuda")), dict(norm="rms", norm_weight=torch.ones(3, 128, device="cuda")),
+               dict(norm_weight=torch.ones(4, 128, device="cuda")), dict(norm="none", norm_bias=torch.ones(4, 128, device="cuda"))):
         with pytest.raises(ValueError):
             f(*x, 0.5, **kw)
     with pytest.raises(TypeError):
