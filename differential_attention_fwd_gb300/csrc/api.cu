@@ -693,7 +693,6 @@ int backward_impl(const diffattn_desc* desc, const void* q1, const void* k1, con
             pp.out2 = out2;
             pp.dout = dout;
             copy3(pp.s_o, d.o_stride);
-            copy3(pp.s_do, d.o_stride);
             pp.lse = lse;
             pp.stats = stats;
             if (launch_bwd_prep(pp, st) != 0) return DIFFATTN_ERR_CUDA;
@@ -826,7 +825,6 @@ int backward_impl(const diffattn_desc* desc, const void* q1, const void* k1, con
         pp.out2 = out2;
         pp.dout = dout;
         copy3(pp.s_o, d.o_stride);
-        copy3(pp.s_do, d.o_stride);
         pp.lse = lse;
         pp.stats = p.stats;
         if (launch_bwd_prep(pp, st) != 0) return DIFFATTN_ERR_CUDA;

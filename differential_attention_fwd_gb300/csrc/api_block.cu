@@ -200,28 +200,11 @@ int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream
     return launch_cross_tc(maps, p, c.D, grid, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
-// The backward on the tensor cores; `counters`: two words of workspace.
-int backward_tc(const CrossParams& c, int sms, uint32_t* counters, cudaStream_t stream) {
-    PrepParams pp{};
-    pp.B = c.B;
-    pp.H = c.H;
-    pp.T = c.Tq;
-    pp.Dv = c.Dv;
-    pp.bf16 = 1;
-    pp.log2_negated = 1;
-    pp.lambda = c.lambda;
-    pp.lambda_dev = c.lambda_dev;
-    pp.out = c.out;
-    pp.out2 = c.out2;
-    pp.dout = c.dout;
-    copy3(pp.s_o, c.s_o);
-    copy3(pp.s_do, c.s_do);
-    pp.lse = c.lse;
-    pp.stats = c.stats;
-    pp.counters = counters;
+// The backward on the tensor cores; `counters`: two words of workspace, `parts`: what follows them.
+int backward_tc(const CrossParams& c, int sms, uint32_t* counters, float* parts, cudaStream_t stream) {
     CUtensorMap maps[12];
     if (cross_maps(maps, c, c.dout, c.s_do, 128, 64, 128) != DIFFATTN_OK ||
-        cross_maps(maps + 6, c, c.dout, c.s_do, 64, 128, 64) != DIFFATTN_OK || launch_bwd_prep(pp, stream) != 0)
+        cross_maps(maps + 6, c, c.dout, c.s_do, 64, 128, 64) != DIFFATTN_OK)
         return DIFFATTN_ERR_CUDA;
     CrossTcParams p{};
     p.B = c.B;
@@ -243,7 +226,15 @@ int backward_tc(const CrossParams& c, int sms, uint32_t* counters, cudaStream_t 
     p.lengths = c.lengths;
     p.status = c.status;
     p.sched = counters;
+    p.out = static_cast<const __nv_bfloat16*>(c.out);
+    p.out2 = static_cast<const __nv_bfloat16*>(c.out2);
+    p.dout = static_cast<const __nv_bfloat16*>(c.dout);
+    copy3(p.s_o, c.s_o);
+    copy3(p.s_do, c.s_do);
+    p.lse = c.lse;
     p.stats = c.stats;
+    p.splits = cross_bwd_splits(c.B, c.Hk, c.group, c.Tq, c.Tk);
+    p.parts = parts;
     p.dq1 = c.dq1;
     p.dq2 = c.dq2;
     p.dk1 = c.dk1;
@@ -266,8 +257,15 @@ size_t diffattn_cross_workspace_bytes(const diffattn_cross_desc* desc) {
 
 size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
-    // the rows' statistics, partial sums of dlambda, and item counters
-    return (size_t)(cross_rows(*desc) * 4 + 128 + 4) * sizeof(float);
+    // the rows' statistics, partial sums of dlambda and item counters; the tensor cores' partial
+    // sums of dK and dV
+    size_t floats = cross_rows(*desc) * 4 + 128 + 4;
+    if (tc_shape(*desc)) {
+        const int64_t Hk = desc->H / group_of(*desc);
+        const int splits = cross_bwd_splits(desc->B, Hk, group_of(*desc), desc->Tq, desc->Tk);
+        if (splits > 1) floats += (size_t)splits * desc->B * Hk * desc->Tk * 256;
+    }
+    return floats * sizeof(float);
 }
 
 int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
@@ -338,10 +336,12 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // two key tensors 128 wide leave no TMEM for their gradients' accumulators
     const int64_t rows[3] = {d.B, d.H, d.Tq};
-    const bool tc = tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(dout, rows, d.dout_stride) && (d.D == 64 || p.k_shared) &&
+    const bool tc = tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(dout, rows, d.dout_stride) && tma_rows(out, rows, d.o_stride) &&
+                    aligned16(out2) && (d.D == 64 || p.k_shared) && d.B * d.H <= 65535 &&
                     aligned16(dq1) && aligned16(dk1) && aligned16(dq2) && aligned16(dk2) && aligned16(dv);
     if (tc) {
-        rc = backward_tc(p, sms, reinterpret_cast<uint32_t*>(p.stats + cross_rows(d) * 4 + 128), st);
+        float* counters = p.stats + cross_rows(d) * 4 + 128;
+        rc = backward_tc(p, sms, reinterpret_cast<uint32_t*>(counters), counters + 4, st);
         if (rc != DIFFATTN_OK) return rc;
     } else if (launch_cross_simt_bwd(p, st) != 0) {
         return DIFFATTN_ERR_CUDA;

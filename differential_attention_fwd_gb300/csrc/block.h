@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "diffattn.h"
@@ -90,10 +91,17 @@ struct CrossTcParams {
     const float* lambda_dev;
     const int32_t* lengths;
     uint32_t* status;
-    uint32_t* sched;            // 2 item counters, zero
-    float* stats;               // rows of -lse_1, -lse_2 (log2), -Dd_1, -Dd_2; the exact Dd out
+    uint32_t* sched;            // 2 item counters
+    const __nv_bfloat16* out; const __nv_bfloat16* out2; const __nv_bfloat16* dout;
+    int64_t s_o[3], s_do[3];
+    const float* lse;
+    float* stats;               // rows of -lse_1, -lse_2 (log2), -Dd_1, -Dd_2
+    int splits;                 // of the query rows of a tile of states
+    float* parts;               // [splits][B, Hk, Tk][256] where there are several
     void* dq1; void* dq2; void* dk1; void* dk2; void* dv;
 };
+// How many splits, for sizes alone.
+int cross_bwd_splits(int64_t B, int64_t Hk, int64_t group, int64_t Tq, int64_t Tk);
 int launch_cross_bwd_tc(const CUtensorMap* maps /*dq: q1,k1,q2,k2,v,do; dkdv: the same*/, const CrossTcParams& p,
                         int head_dim, int num_sms, cudaStream_t stream);
 

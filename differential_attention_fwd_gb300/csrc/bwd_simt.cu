@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(WARPS * 32) bwd_prep_kernel(const PrepParams p
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
     const int64_t rows = (int64_t)p.B * p.H * p.T;
-    if (p.counters && blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
     if (row >= rows) return;
     const int64_t bh = row / p.T;
     const int t = (int)(row - bh * p.T);
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(WARPS * 32) bwd_prep_kernel(const PrepParams p
     const int64_t off = b * p.s_o[0] + h * p.s_o[1] + (int64_t)t * p.s_o[2];
     const T* o = static_cast<const T*>(p.out) + off;
     const T* o2 = static_cast<const T*>(p.out2) + off;
-    const T* g = static_cast<const T*>(p.dout) + b * p.s_do[0] + h * p.s_do[1] + (int64_t)t * p.s_do[2];
+    const T* g = static_cast<const T*>(p.dout) + off;
     float d0 = 0.f, d2 = 0.f;
     for (int c = lane; c < p.Dv; c += 32) {
         const float gc = ld(g, c);

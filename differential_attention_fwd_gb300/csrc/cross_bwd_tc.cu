@@ -24,8 +24,8 @@
 //   which the dK/dV kernel and dlambda take.  dS itself needs Dd before that sum is known,
 //   and takes the saved one, whose error (2^-9 of |dO| |O|) is small beside dP where O is a
 //   mean over many states; over a single tile, where it is not, the sum comes first.
-// dkdv: item (b, key/value head, 128 states in TMEM lanes); over every 64 query rows of the
-//   group's heads: S_1^T, S_2^T, dP^T, then dV += W^T dO, dK_b += dS_b^T Q_b (one accumulator
+// dkdv: item (b, key/value head, 128 states in TMEM lanes, a split of the query rows where there
+//   are few such tiles); over every 64 query rows of the group's heads: S_1^T, S_2^T, dP^T, then dV += W^T dO, dK_b += dS_b^T Q_b (one accumulator
 //   for both branches where they share their keys: one rounding).  States behind the
 //   sequence's own are lanes whose results are replaced by zeros.
 //
@@ -40,6 +40,7 @@
 #include "kernels.h"
 #include "pdl.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 #include <cmath>
 
@@ -74,6 +75,54 @@ __device__ __forceinline__ void locate(int idx, int heads, int tiles, int group,
     const int w = idx - g0 * tiles;
     *tile = w / size;
     *head = g0 + (w - *tile * size);
+}
+
+// ---------------------------------------------------------------------------
+// The rows' statistics from the forward's saved results: Dd_2 = dO . (A_2 V), Dd_1 = dO . (O +
+// lambda A_2 V), stored negated with the log2-sum-exps.  16 lanes a row, 16 bytes a lane: HBM
+// (39 us with a lane for every fourth pair of bytes, at 131,000 rows).
+// ---------------------------------------------------------------------------
+constexpr int PREP_THREADS = 256;
+constexpr int PREP_ROWS = 4;            // of a group of lanes, loaded together
+__global__ void __launch_bounds__(PREP_THREADS)
+cross_prep_kernel(const CrossTcParams p) {
+    constexpr int GROUPS = PREP_THREADS / 16;
+    const int g = threadIdx.x % 16, h = blockIdx.y % p.H, b = blockIdx.y / p.H;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) p.sched[threadIdx.x] = 0;
+    const int q0 = blockIdx.x * (GROUPS * PREP_ROWS) + threadIdx.x / 16;
+    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    uint4 raw[PREP_ROWS][3];
+#pragma unroll
+    for (int i = 0; i < PREP_ROWS; ++i) {
+        const int q = q0 + i * GROUPS;
+        const int64_t o = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2] + 8 * g;
+        const int64_t d = b * p.s_do[0] + h * p.s_do[1] + q * p.s_do[2] + 8 * g;
+        raw[i][0] = raw[i][1] = raw[i][2] = make_uint4(0, 0, 0, 0);
+        if (q < p.Tq) {
+            raw[i][0] = *reinterpret_cast<const uint4*>(p.dout + d);
+            raw[i][1] = *reinterpret_cast<const uint4*>(p.out + o);
+            raw[i][2] = *reinterpret_cast<const uint4*>(p.out2 + o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PREP_ROWS; ++i) {
+        const int q = q0 + i * GROUPS;
+        uint64_t x[3][4];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) Vec<__nv_bfloat16>::unpack(raw[i][j], x[j]);
+        uint64_t d0 = 0, d2 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            d0 = f2_fma(x[0][e], x[1][e], d0);
+            d2 = f2_fma(x[0][e], x[2][e], d2);
+        }
+        const float s0 = group_sum<16>(f2_lo(d0) + f2_hi(d0)), s2 = group_sum<16>(f2_lo(d2) + f2_hi(d2));
+        if (g != 0 || q >= p.Tq) continue;
+        const int64_t row = ((int64_t)b * p.H + h) * p.Tq + q;
+        const float2 lse = *reinterpret_cast<const float2*>(p.lse + row * 2);
+        constexpr float LOG2E = 1.4426950408889634f;
+        *reinterpret_cast<float4*>(p.stats + row * 4) = make_float4(-lse.x * LOG2E, -lse.y * LOG2E, -fmaf(lam, s2, s0), -s2);
+    }
 }
 
 // ===========================================================================
@@ -562,15 +611,16 @@ struct Cfg {
     static constexpr int PANELS = HD / 64;
     static constexpr uint32_t K_BYTES = PANELS * K_PANEL;
     static constexpr uint32_t Q_BYTES = PANELS * Q_PANEL;
-    static constexpr int QSTAGES = HD == 64 ? 4 : 2;               // (Q1, Q2, dO) ring
-    static constexpr uint32_t STAGE = 2 * Q_BYTES + 2 * Q_PANEL;
-    static constexpr uint32_t QS_Q1 = 0, QS_Q2 = Q_BYTES, QS_DO = 2 * Q_BYTES;
+    // rings of (Q1, Q2) and of dO: what fits (D = 128: a third stage of both does not)
+    static constexpr int QSTAGES = HD == 64 ? 4 : 3, GSTAGES = HD == 64 ? 4 : 2;
+    static constexpr uint32_t Q_STAGE = 2 * Q_BYTES, G_STAGE = 2 * Q_PANEL;
     // D = 128: one key tensor
     static constexpr uint32_t OFF_K1 = 0, OFF_K2 = HD == 64 ? K_BYTES : 0;
     static constexpr uint32_t OFF_V = HD == 64 ? 2 * K_BYTES : K_BYTES;
     static constexpr uint32_t OFF_QS = OFF_V + 2 * K_PANEL;
     // dS_2^T [128 states x 64 rows] as a K-major operand (W^T and dS_1^T go to TMEM)
-    static constexpr uint32_t OFF_PK = OFF_QS + QSTAGES * STAGE;
+    static constexpr uint32_t OFF_GS = OFF_QS + QSTAGES * Q_STAGE;
+    static constexpr uint32_t OFF_PK = OFF_GS + GSTAGES * G_STAGE;
     // per elementwise warp: the statistics of its 32 query rows by quantity
     static constexpr uint32_t OFF_SCR = OFF_PK + BM * 128;
     static constexpr uint32_t OFF_BAR = OFF_SCR + 8 * 4 * 32 * 4;
@@ -582,7 +632,8 @@ constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, 0, 0);         // K x Q^T, V
 constexpr uint32_t IDESC_DV = idesc_bf16_f32(BM, VD, 0, 1);        // W^T (TMEM) x dO (MN-major)
 
 enum : int {
-    KV_FULL, KV_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + QSTAGES_MAX, S_FULL = Q_EMPTY + QSTAGES_MAX,
+    KV_FULL, KV_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + QSTAGES_MAX, G_FULL = Q_EMPTY + QSTAGES_MAX,
+    G_EMPTY = G_FULL + QSTAGES_MAX, S_FULL = G_EMPTY + QSTAGES_MAX,
     S_FREE,                         // 8 warps: scores in registers
     DS_FULL,                        // 8 warps: operands written
     PK_FREE,                        // the operands have been read
@@ -597,19 +648,24 @@ static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448, "shared
 
 struct Item {
     int b, hk, kt, len;
-    int n;          // query tiles of all the group's heads
+    int split;      // of the query tiles of all the group's heads,
+    int t0, n;      // the split's first one and its tiles
     bool bad;
 };
 __device__ __forceinline__ Item decode(int idx, const CrossTcParams& p) {
     Item it;
     int head;
-    locate(idx, p.B * p.Hk, p.nk128, p.group_k, &head, &it.kt);
+    locate(idx, p.B * p.Hk, p.nk128 * p.splits, p.group_k, &head, &it.kt);
+    it.split = it.kt % p.splits;
+    it.kt /= p.splits;
     it.b = head / p.Hk;
     it.hk = head - it.b * p.Hk;
     const CrossLen len = cross_len(p.lengths, it.b, p.Tk);
     it.len = len.n;
     it.bad = len.bad;
-    it.n = it.kt * BM < len.n ? p.group * p.nq64 : 0;
+    const int64_t tiles = (int64_t)p.group * p.nq64;
+    it.t0 = (int)(tiles * it.split / p.splits);
+    it.n = it.kt * BM < len.n ? (int)(tiles * (it.split + 1) / p.splits) - it.t0 : 0;
     return it;
 }
 
@@ -627,7 +683,7 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_BAR + REL_ABORT);
     const uint32_t warp = warp_id(), lane = threadIdx.x & 31;
     const AbortState ab{abort_flag, p.status};
-    const int total = p.B * p.Hk * p.nk128;
+    const int total = p.B * p.Hk * p.nk128 * p.splits;
     const bool shared = HD == 128 || p.k_shared;
 
     if (threadIdx.x == 0) {
@@ -636,6 +692,10 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
         for (int s = 0; s < C::QSTAGES; ++s) {
             mbar_init(&bars[Q_FULL + s], 1);
             mbar_init(&bars[Q_EMPTY + s], 1);
+        }
+        for (int s = 0; s < C::GSTAGES; ++s) {
+            mbar_init(&bars[G_FULL + s], 1);
+            mbar_init(&bars[G_EMPTY + s], 1);
         }
         mbar_init(&bars[S_FULL], 1);
         mbar_init(&bars[S_FREE], 8);
@@ -667,8 +727,8 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
         if (warp == 8) {
             // ------------------------------------------------------ producer
             if (elect_one()) {
-                uint32_t qs = 0, qph = 0, kvph = 0;
-                uint32_t armed_kv = 0, armed_q[QSTAGES_MAX] = {};
+                uint32_t qs = 0, qph = 0, gs = 0, gph = 0, kvph = 0;
+                uint32_t armed_kv = 0, armed_q[QSTAGES_MAX] = {}, armed_g[QSTAGES_MAX] = {};
                 bool ok = true;
                 for (int k = 0; ok; ++k) {
                     int idx = (int)atomicAdd(p.sched + 1, 1u);
@@ -692,28 +752,35 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                     for (int pn = 0; pn < 2; ++pn)
                         tma_load_4d(smem + C::OFF_V + pn * K_PANEL, &tm_v, &bars[KV_FULL], pn * 64, k0, it.hk, it.b);
                     ++armed_kv;
-                    int h = it.hk * p.group, qt = 0;
+                    int h = it.hk * p.group + it.t0 / p.nq64, qt = it.t0 % p.nq64;
                     for (int t = 0; t < it.n && ok; ++t) {
                         if (!(ok = mbar_wait(&bars[Q_EMPTY + qs], qph ^ 1, ab))) break;
-                        uint8_t* st = smem + C::OFF_QS + qs * C::STAGE;
+                        uint8_t* st = smem + C::OFF_QS + qs * C::Q_STAGE;
                         const int q0 = qt * BN;
-                        mbar_arrive_expect_tx(&bars[Q_FULL + qs], C::STAGE);
+                        mbar_arrive_expect_tx(&bars[Q_FULL + qs], C::Q_STAGE);
 #pragma unroll
                         for (int pn = 0; pn < C::PANELS; ++pn) {
-                            tma_load_4d(st + C::QS_Q1 + pn * Q_PANEL, &tm_q1, &bars[Q_FULL + qs], pn * 64, q0, h, it.b);
-                            tma_load_4d(st + C::QS_Q2 + pn * Q_PANEL, &tm_q2, &bars[Q_FULL + qs], pn * 64, q0, h, it.b);
+                            tma_load_4d(st + pn * Q_PANEL, &tm_q1, &bars[Q_FULL + qs], pn * 64, q0, h, it.b);
+                            tma_load_4d(st + C::Q_BYTES + pn * Q_PANEL, &tm_q2, &bars[Q_FULL + qs], pn * 64, q0, h, it.b);
                         }
-#pragma unroll
-                        for (int pn = 0; pn < 2; ++pn)
-                            tma_load_4d(st + C::QS_DO + pn * Q_PANEL, &tm_do, &bars[Q_FULL + qs], pn * 64, q0, h, it.b);
                         ++armed_q[qs];
                         if (++qs == C::QSTAGES) { qs = 0; qph ^= 1; }
+                        if (!(ok = mbar_wait(&bars[G_EMPTY + gs], gph ^ 1, ab))) break;
+                        mbar_arrive_expect_tx(&bars[G_FULL + gs], C::G_STAGE);
+#pragma unroll
+                        for (int pn = 0; pn < 2; ++pn)
+                            tma_load_4d(smem + C::OFF_GS + gs * C::G_STAGE + pn * Q_PANEL, &tm_do, &bars[G_FULL + gs], pn * 64,
+                                        q0, h, it.b);
+                        ++armed_g[gs];
+                        if (++gs == C::GSTAGES) { gs = 0; gph ^= 1; }
                         if (++qt == p.nq64) { qt = 0; ++h; }
                     }
                 }
                 if (armed_kv) mbar_wait_teardown(&bars[KV_FULL], (armed_kv - 1) & 1, TEARDOWN_NS);
                 for (int s = 0; s < C::QSTAGES; ++s)
                     if (armed_q[s]) mbar_wait_teardown(&bars[Q_FULL + s], (armed_q[s] - 1) & 1, TEARDOWN_NS);
+                for (int s = 0; s < C::GSTAGES; ++s)
+                    if (armed_g[s]) mbar_wait_teardown(&bars[G_FULL + s], (armed_g[s] - 1) & 1, TEARDOWN_NS);
             }
             __syncwarp();
         } else if (warp == 9) {
@@ -724,6 +791,8 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                 const uint64_t vd = sdesc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
                 const uint64_t qk = sdesc_sw128(smem_u32(smem + C::OFF_QS), 16, 1024);         // K-major
                 const uint64_t qm = sdesc_sw128(smem_u32(smem + C::OFF_QS), Q_PANEL, 1024);    // MN-major
+                const uint64_t gk = sdesc_sw128(smem_u32(smem + C::OFF_GS), 16, 1024);
+                const uint64_t gm = sdesc_sw128(smem_u32(smem + C::OFF_GS), Q_PANEL, 1024);
                 const uint64_t pkd = sdesc_sw128(smem_u32(smem + C::OFF_PK), 16, 1024);        // K-major
                 const uint32_t dk2 = tmem_base + (shared ? TM_DK1 : TM_DK2);
                 uint32_t kvph = 0, accph = 0;
@@ -733,19 +802,21 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                 // S_1^T, S_2^T, dP^T of the next query tile; the previous tile's scores must have
                 // been read out of TMEM
                 auto issue_s = [&](bool last) -> bool {
-                    const uint32_t qs = tiles % C::QSTAGES;
+                    const uint32_t qs = tiles % C::QSTAGES, gs = tiles % C::GSTAGES;
                     if (tiles > 0 && !mbar_wait(&bars[S_FREE], (tiles - 1) & 1u, ab)) return false;
                     if (!mbar_wait(&bars[Q_FULL + qs], (tiles / C::QSTAGES) & 1u, ab)) return false;
                     tc_fence_after();
-                    const uint64_t sb = qk + ((qs * C::STAGE) >> 4);
+                    const uint64_t sb = qk + ((qs * C::Q_STAGE) >> 4), gb = gk + ((gs * C::G_STAGE) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
-                        mma_ss(tmem_base + TM_S1, k1d + kstep(kk, K_PANEL), sb + (C::QS_Q1 >> 4) + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
-                        mma_ss(tmem_base + TM_S2, k2d + kstep(kk, K_PANEL), sb + (C::QS_Q2 >> 4) + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
+                        mma_ss(tmem_base + TM_S1, k1d + kstep(kk, K_PANEL), sb + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
+                        mma_ss(tmem_base + TM_S2, k2d + kstep(kk, K_PANEL), sb + (C::Q_BYTES >> 4) + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
                     }
+                    if (!mbar_wait(&bars[G_FULL + gs], (tiles / C::GSTAGES) & 1u, ab)) return false;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < VD / 16; ++kk)
-                        mma_ss(tmem_base + TM_DP, vd + kstep(kk, K_PANEL), sb + (C::QS_DO >> 4) + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
+                        mma_ss(tmem_base + TM_DP, vd + kstep(kk, K_PANEL), gb + kstep(kk, Q_PANEL), IDESC_S, kk > 0);
                     mma_commit(&bars[S_FULL]);
                     if (last) mma_commit(&bars[KV_EMPTY]);
                     ++tiles;
@@ -768,17 +839,18 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                             accph ^= 1;
                         }
                         tc_fence_after();
-                        const uint32_t qs = done % C::QSTAGES;
-                        const uint64_t sb = qm + ((qs * C::STAGE) >> 4);
+                        const uint32_t qs = done % C::QSTAGES, gs = done % C::GSTAGES;
+                        const uint64_t sb = qm + ((qs * C::Q_STAGE) >> 4), gb = gm + ((gs * C::G_STAGE) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk) {
                             const uint32_t acc = (t > 0 || kk > 0) ? 1u : 0u;
-                            mma_ts(tmem_base + TM_DV, tmem_base + TM_W + kk * 8, sb + (C::QS_DO >> 4) + 128 * kk, IDESC_DV, acc);
-                            mma_ts(tmem_base + TM_DK1, tmem_base + TM_DS1 + kk * 8, sb + (C::QS_Q1 >> 4) + 128 * kk, C::IDESC_DK, acc);
-                            mma_ss(dk2, pkd + 2 * kk, sb + (C::QS_Q2 >> 4) + 128 * kk, C::IDESC_DK, shared ? 1u : acc);
+                            mma_ts(tmem_base + TM_DV, tmem_base + TM_W + kk * 8, gb + 128 * kk, IDESC_DV, acc);
+                            mma_ts(tmem_base + TM_DK1, tmem_base + TM_DS1 + kk * 8, sb + 128 * kk, C::IDESC_DK, acc);
+                            mma_ss(dk2, pkd + 2 * kk, sb + (C::Q_BYTES >> 4) + 128 * kk, C::IDESC_DK, shared ? 1u : acc);
                         }
                         mma_commit(&bars[PK_FREE]);
                         mma_commit(&bars[Q_EMPTY + qs]);
+                        mma_commit(&bars[G_EMPTY + gs]);
                         ++done;
                     }
                     if (!ok) break;
@@ -823,7 +895,7 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
             __nv_bfloat16* dk = HD == 128 ? static_cast<__nv_bfloat16*>(p.dk1) + krow * HD + 64 * half
                                           : static_cast<__nv_bfloat16*>(half ? p.dk2 : p.dk1) + krow * HD;
             const bool has_dk = HD == 128 || half == 0 || !shared;
-            if (key >= it.len && key < p.Tk) {      // not the sequence's: zeros (NaN for a bad length)
+            if (p.splits == 1 && key >= it.len && key < p.Tk) {     // not the sequence's: zeros (NaN for a bad length)
                 const uint32_t w = it.bad ? 0x7fc07fc0u : 0u;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -832,7 +904,7 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                 }
             }
             if (it.n == 0) continue;
-            int h = it.hk * p.group, qt = 0;
+            int h = it.hk * p.group + it.t0 / p.nq64, qt = it.t0 % p.nq64;
             float4 nst = stats_of(it.b, h, qt);
             for (int t = 0; t < it.n; ++t, ++qc) {
                 const int qbase = qt * BN + (int)c0;
@@ -938,7 +1010,17 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[ACC_EMPTY]);
-            if (key < it.len) {
+            if (p.splits > 1) {         // partial sums, for the pass that joins them
+                constexpr int W = VD + 2 * 64;
+                float* part = p.parts + ((int64_t)it.split * p.B * p.Hk * p.Tk + krow) * W;
+                if (key < it.len) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        *reinterpret_cast<uint4*>(part + 64 * half + i) = make_uint4(gv[i], gv[i + 1], gv[i + 2], gv[i + 3]);
+                        *reinterpret_cast<uint4*>(part + VD + 64 * half + i) = make_uint4(gk[i], gk[i + 1], gk[i + 2], gk[i + 3]);
+                    }
+                }
+            } else if (key < it.len) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dv + 8 * i) = pack8(&gv[8 * i], 1.f);
                 if (has_dk)
@@ -953,6 +1035,44 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
     if (warp == 9) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
+// The splits' partial sums joined, in their order: a thread 8 of a state's 256 columns (dV, then
+// dK_1 and dK_2 or the D = 128 columns of dK).
+constexpr int JOIN_THREADS = 256;
+template <int HD>
+__global__ void __launch_bounds__(JOIN_THREADS)
+cross_join_kernel(const CrossTcParams p) {
+    pdl_wait();
+    constexpr int W = VD + 2 * 64;
+    const int64_t rows = (int64_t)p.B * p.Hk * p.Tk;
+    const int64_t row = (int64_t)blockIdx.x * (JOIN_THREADS / 32) + threadIdx.x / 32;
+    if (row >= rows) return;
+    const int c = (threadIdx.x % 32) * 8;
+    const int b = (int)(row / ((int64_t)p.Hk * p.Tk)), key = (int)(row % p.Tk);
+    const CrossLen len = cross_len(p.lengths, b, p.Tk);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dv) + row * VD + c;
+    if (c >= VD) {
+        if (HD == 128) dst = static_cast<__nv_bfloat16*>(p.dk1) + row * HD + (c - VD);
+        else if (c < VD + 64) dst = static_cast<__nv_bfloat16*>(p.dk1) + row * HD + (c - VD);
+        else if (p.dk2) dst = static_cast<__nv_bfloat16*>(p.dk2) + row * HD + (c - VD - 64);
+        else return;
+    }
+    if (key >= len.n) {
+        const uint32_t w = len.bad ? 0x7fc07fc0u : 0u;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w, w, w, w);
+        return;
+    }
+    float x[8] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float* part = p.parts + (s * rows + row) * W + c;
+        const float4 a = *reinterpret_cast<const float4*>(part), d = *reinterpret_cast<const float4*>(part + 4);
+        x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
+        x[4] += d.x; x[5] += d.y; x[6] += d.z; x[7] += d.w;
+    }
+    const float f = c >= VD ? p.scale : 1.f;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                                                pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
+}
+
 }  // namespace dkdv
 
 template <int HD>
@@ -962,17 +1082,45 @@ int launch(const CUtensorMap* maps, const CrossTcParams& p, int num_sms, cudaStr
         cudaFuncSetAttribute(dkdv::diffattn_cross_dkdv_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)dkdv::smem_bytes<HD>()) != cudaSuccess)
         return -1;
-    const int dq_items = p.B * p.H * p.nq128, kv_items = p.B * p.Hk * p.nk128;
+    const int dq_items = p.B * p.H * p.nq128, kv_items = p.B * p.Hk * p.nk128 * p.splits;
+    constexpr int PER = PREP_THREADS / 16 * PREP_ROWS;
+    cross_prep_kernel<<<dim3((p.Tq + PER - 1) / PER, p.B * p.H), PREP_THREADS, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -1;
     dq::diffattn_cross_dq_kernel<HD><<<dq_items < num_sms ? dq_items : num_sms, NUM_THREADS, dq::smem_bytes<HD>(), stream>>>(
         maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
     if (cudaGetLastError() != cudaSuccess) return -1;
     if (!p.dv) return 0;
     // One CTA of either kernel takes a whole SM's registers, so they never share one.
-    return pdl_launch(dkdv::diffattn_cross_dkdv_kernel<HD>, dim3(kv_items < num_sms ? kv_items : num_sms), NUM_THREADS,
-                      dkdv::smem_bytes<HD>(), stream, maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p);
+    if (pdl_launch(dkdv::diffattn_cross_dkdv_kernel<HD>, dim3(kv_items < num_sms ? kv_items : num_sms), NUM_THREADS,
+                   dkdv::smem_bytes<HD>(), stream, maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p) != 0)
+        return -1;
+    if (p.splits == 1) return 0;
+    constexpr int ROWS = dkdv::JOIN_THREADS / 32;
+    const int64_t rows = (int64_t)p.B * p.Hk * p.Tk;
+    return pdl_launch(dkdv::cross_join_kernel<HD>, dim3((unsigned)((rows + ROWS - 1) / ROWS)), dkdv::JOIN_THREADS, 0, stream, p);
 }
 
 }  // namespace xbwd
+
+// Items of all of a head's query rows keep 152 SMs busy when there are many; few leave the last
+// round of items half empty.  The estimate, in tiles of 64 rows (about 0.9 us): the rounds of
+// items, 4 tiles for an item's start and end, and the partial sums' way to HBM and back.
+int cross_bwd_splits(int64_t B, int64_t Hk, int64_t group, int64_t Tq, int64_t Tk) {
+    constexpr double SMS = 152;
+    const double items = (double)B * Hk * ((Tk + 127) / 128), tiles = (double)group * ((Tq + 63) / 64);
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 8; ++s) {
+        if (s > 1 && tiles < 4 * s) break;
+        const double join = s > 1 ? (double)s * B * Hk * Tk * 256 * 4 * 2 / 4.5e12 / 0.9e-6 + 3 : 0;
+        const double t = std::ceil(items * s / SMS) * (std::ceil(tiles / s) + 4) + join;
+        if (s == 1 || t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
+}
 
 int launch_cross_bwd_tc(const CUtensorMap* maps, const CrossTcParams& p, int head_dim, int num_sms, cudaStream_t stream) {
     if (head_dim == 64) return xbwd::launch<64>(maps, p, num_sms, stream);

@@ -168,11 +168,9 @@ struct PrepParams {
     float lambda;
     const float* lambda_dev;
     const void* out; const void* out2; const void* dout;
-    int64_t s_o[3];         // of out and out2
-    int64_t s_do[3];
+    int64_t s_o[3];         // shared by out, out2 and dout
     const float* lse;       // [B, H, T, 2]
     float* stats;           // [B, H, T, 4]
-    uint32_t* counters;     // two words to be zeroed, nullptr: none
 };
 
 // Decode helpers: query-row bucket (rows rounded up to 1, 2, 4 or 8; 0 if

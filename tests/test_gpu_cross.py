@@ -125,6 +125,17 @@ def test_lengths(dtype, D, Dv, shared, Tq, Tk, lens):
     compare(x, n, lens, 0.3)
 
 
+@pytest.mark.parametrize("D,shared", [(64, False), (64, True), (128, True)])
+@pytest.mark.parametrize("H,Hk,Tq,Tk,lens", [(2, 1, 700, 130, [130, 0]), (1, 1, 1100, 20, [20, 7]), (2, 2, 600, 300, [1, 300])])
+def test_query_rows_in_splits(D, shared, H, Hk, Tq, Tk, lens):
+    """Few tiles of states: dK and dV come from several blocks' partial sums."""
+    x, n = inputs(Tq, BF, 2, H, Hk, Tq, Tk, D, 128, shared, lens)
+    o, _, first = compare(x, n, lens, 0.8)
+    do = torch.randn(o.shape, device="cuda").to(BF)
+    first, again = train(x, n, 0.8, do)[1], train(x, n, 0.8, do)[1]
+    assert all(torch.equal(first[k], again[k]) for k in first)
+
+
 @pytest.mark.parametrize("H,Hk", [(1, 1), (3, 1), (6, 3), (16, 2)])
 @pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 128, 128, True), (F32, 64, 128, False)])
 @pytest.mark.parametrize("Tq", [1, 70])
