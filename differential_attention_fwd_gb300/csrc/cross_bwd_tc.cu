@@ -169,6 +169,7 @@ enum : int {
     DO_READY, DO_FREE,              // dO in TMEM: 4 warps; the item's last dP product done
     FINAL, ITEM_FULL, ITEM_EMPTY = ITEM_FULL + RING, NUM_BARS = ITEM_EMPTY + RING
 };
+constexpr int CHAINS = 2;           // of a row's sum of A_b dP
 constexpr int CONSUMERS = 10;       // of the items: the MMA thread, 8 warps, the cleaning warp
 constexpr uint32_t REL_TMEM = NUM_BARS * 8, REL_ABORT = REL_TMEM + 4, REL_RING = REL_ABORT + 4, REL_END = REL_RING + RING * 4;
 template <int HD>
@@ -288,6 +289,8 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
                     ++armed_q;
                     for (int j = 0; j < it.n; ++j) {
                         if (!(ok = mbar_wait(&bars[K_EMPTY + kst], kph ^ 1, ab))) break;
+                        // the MMA thread waits for the cleaning of some tiles only: no phase may be skipped
+                        if (cleaned && !(ok = mbar_wait(&bars[K_CLEAN + kst], kph ^ 1, ab))) break;
                         uint8_t* kd = smem + C::OFF_K + kst * C::K_STAGE;
                         mbar_arrive_expect_tx(&bars[K_FULL + kst], (shared ? 1 : 2) * C::K_BYTES);
 #pragma unroll
@@ -299,6 +302,7 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
                         ++armed_k[kst];
                         if (++kst == C::KSTAGES) { kst = 0; kph ^= 1; }
                         if (!(ok = mbar_wait(&bars[V_EMPTY + vst], vph ^ 1, ab))) break;
+                        if (cleaned && !(ok = mbar_wait(&bars[V_CLEAN + vst], vph ^ 1, ab))) break;
                         uint8_t* vd = smem + C::OFF_V + vst * V_BYTES;
                         mbar_arrive_expect_tx(&bars[V_FULL + vst], V_BYTES);
                         tma_load_4d(vd, &tm_v, &bars[V_FULL + vst], 0, j * BN, hk, it.b);
@@ -332,7 +336,7 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
                 auto issue_s = [&](uint32_t kt, int buf, bool first_tile, bool last_tile) -> bool {
                     const uint32_t ks = kt % C::KSTAGES, kp = (kt / C::KSTAGES) & 1u;
                     if (!mbar_wait(&bars[K_FULL + ks], kp, ab) || !mbar_wait(&bars[V_FULL + vst], vph, ab)) return false;
-                    if (cleaned && (!mbar_wait(&bars[K_CLEAN + ks], kp, ab) || !mbar_wait(&bars[V_CLEAN + vst], vph, ab)))
+                    if (cleaned && last_tile && (!mbar_wait(&bars[K_CLEAN + ks], kp, ab) || !mbar_wait(&bars[V_CLEAN + vst], vph, ab)))
                         return false;
                     if (!TWO && kt > 0 && !mbar_wait(&bars[DP_FREE], (kt - 1) & 1u, ab)) return false;
                     tc_fence_after();
@@ -507,7 +511,7 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
             }
             const uint64_t nlse2 = f2_pack(nlse, nlse);
             uint64_t cndd2 = f2_pack(coef * ndd, coef * ndd);
-            uint64_t sum2[2] = {0, 0};          // of A_b dP
+            uint64_t sum2[CHAINS] = {};         // of A_b dP
             for (int j = 0; j < it.n; ++j, ++cnt) {
                 const int buf = TWO ? j & 1 : 0;
                 const uint32_t tS = lane_base + buf * 128 + br * 64;
@@ -523,31 +527,38 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[DP_FREE]);
-                // in three phases, in place in the score registers: the exponents, the
-                // exponentials, then dS_b = coef A_b (dP - Dd_b)
+                const int lim = it.len - j * BN;        // columns from it on are no states
+                if (lim < BN) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                }
+                if (it.n == 1) {                        // one tile: the row's exact Dd comes first
+                    uint64_t t[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const uint64_t x = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), sl2x2, nlse2);
+                        t[c & 3] = f2_fma(f2_pack(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x))), f2_from_bits(dp[2 * c], dp[2 * c + 1]),
+                                          t[c & 3]);
+                    }
+                    const uint64_t sum = f2_add(f2_add(t[0], t[1]), f2_add(t[2], t[3]));
+                    const float x = -coef * (f2_lo(sum) + f2_hi(sum));
+                    cndd2 = f2_pack(x, x);
+                }
+                // one run of code for the compiler to order, in phases of independent operations in
+                // place in the score registers: the exponents, the exponentials, the row's sum, dS_b =
+                // coef A_b (dP - Dd_b).  (A branch between the phases, for the mask or the exact Dd,
+                // took a fifth of the kernel's time.)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const uint64_t x = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), sl2x2, nlse2);
                     s[2 * c] = static_cast<uint32_t>(x);
                     s[2 * c + 1] = static_cast<uint32_t>(x >> 32);
                 }
-                const int lim = it.len - j * BN;        // columns below it are states
-                if (lim < BN) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        s[c] = c < lim ? __float_as_uint(ex2_approx(__uint_as_float(s[c]))) : 0u;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_approx(__uint_as_float(s[c])));
-                }
+                for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_approx(__uint_as_float(s[c])));
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                    sum2[c & 1] = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), f2_from_bits(dp[2 * c], dp[2 * c + 1]), sum2[c & 1]);
-                if (it.n == 1) {                        // the row's whole sum: exact before dS
-                    const uint64_t t = f2_add(sum2[0], sum2[1]);
-                    const float x = -coef * (f2_lo(t) + f2_hi(t));
-                    cndd2 = f2_pack(x, x);
-                }
+                    sum2[c % CHAINS] = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), f2_from_bits(dp[2 * c], dp[2 * c + 1]), sum2[c % CHAINS]);
                 uint32_t pk[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
@@ -565,7 +576,9 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
             if (!ok) break;
             ++items;
             if (live) {
-                const uint64_t t = f2_add(sum2[0], sum2[1]);
+                uint64_t t = sum2[0];
+#pragma unroll
+                for (int i = 1; i < CHAINS; ++i) t = f2_add(t, sum2[i]);
                 p.stats[at * 4 + 2 + br] = -(f2_lo(t) + f2_hi(t));
             }
             // dQ_b = scale * (dS_b K_b)
@@ -927,6 +940,14 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[S_FREE]);
                 uint32_t w1[16], w2[16], w3[16];
+                const int qlim = p.Tq - qbase;              // columns from it on are no query rows
+                if (qlim < 32) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        s1[c] = c < qlim ? s1[c] : 0xff800000u;
+                        s2[c] = c < qlim ? s2[c] : 0xff800000u;
+                    }
+                }
                 // in three phases, in place: the exponents, the exponentials, then dS_1, dS_2 and W
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
@@ -944,19 +965,10 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                         s2[cc + 1] = static_cast<uint32_t>(x2 >> 32);
                     }
                 }
-                const int qlim = p.Tq - qbase;              // columns below it are query rows
-                if (qlim < 32) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        s1[c] = c < qlim ? __float_as_uint(ex2_approx(__uint_as_float(s1[c]))) : 0u;
-                        s2[c] = c < qlim ? __float_as_uint(ex2_approx(__uint_as_float(s2[c]))) : 0u;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        s1[c] = __float_as_uint(ex2_approx(__uint_as_float(s1[c])));
-                        s2[c] = __float_as_uint(ex2_approx(__uint_as_float(s2[c])));
-                    }
+                for (int c = 0; c < 32; ++c) {
+                    s1[c] = __float_as_uint(ex2_approx(__uint_as_float(s1[c])));
+                    s2[c] = __float_as_uint(ex2_approx(__uint_as_float(s2[c])));
                 }
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {

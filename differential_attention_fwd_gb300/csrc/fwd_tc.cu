@@ -512,6 +512,8 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
 
                     if (!(ok = TIMED_WAIT(wp, kWaitTensor, mbar_wait(&bars[BAR_V_EMPTY + vst], vph ^ 1, ab))))
                         break;
+                    // the MMA threads wait for the cleaning of an item's last tile only: no phase may be skipped
+                    if (CROSS && p.lengths && !(ok = mbar_wait(&bars[BAR_V_CLEAN + vst], vph ^ 1, ab))) break;
                     uint8_t* vdst = smem + C::OFF_V + vst * V_BYTES;
                     mbar_arrive_expect_tx(&bars[BAR_V_FULL + vst], V_BYTES);
                     tma_load_4d(vdst, &tm_v, &bars[BAR_V_FULL + vst], 0, j * BN, hk, it.b);
@@ -601,7 +603,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     // their barriers are checked first: once P_b(j) arrives,
                     // both products issue with no other wait in between.
                     if (!(ok = TIMED_WAIT(wp, kWaitV, mbar_wait(&bars[BAR_V_FULL + vst], vph, ab)))) break;
-                    if (CROSS && p.lengths && !(ok = mbar_wait(&bars[BAR_V_CLEAN + vst], vph, ab))) break;
+                    if (CROSS && p.lengths && j + 1 == n && !(ok = mbar_wait(&bars[BAR_V_CLEAN + vst], vph, ab))) break;
                     if (j + 2 < n &&
                         !(ok = KEY_WAIT(wp, kst, mbar_wait(&bars[BAR_K_FULL + kst], kph, ab))))
                         break;
