@@ -138,6 +138,39 @@ bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, con
            tma_rows(k2, nk, d.k2_stride) && tma_rows(v, nk, d.v_stride);
 }
 
+// Whether the kernels of the paged cache take a serving call.  They divide the states of all
+// sequences evenly over the SMs and join the parts in a second launch, where the forward's
+// blocks each walk a whole sequence for 128 rows of a head.  By estimates, in us, for lengths
+// of Tk, from what either measured (bf16; the forward, then the split):
+//   one sequence, 16 heads of 64, 32 rows:  77 states 6.8, 15.9; 1500 19.9, 20.3; 6000 62, 29.5
+//   16 sequences, the same:                 77 states 16.2, 23.5; 1500 47, 74; 6000 142, 180
+//   16 sequences, 16 over 4 heads, 32 rows: 77 states 15.3, 21.8; 1500 41, 43; 6000 121, 73
+//   the V2 head, 16 over 8 heads, 64 rows:  77 states 7.3, 17.8; 1500 23, 30; 6000 84, 37
+// Up to 16 rows a key/value head the split is bound by HBM, beyond by its products.
+bool wants_split(const diffattn_cross_desc& d) {
+    if (!cross_paged_ok(d)) return false;
+    constexpr double SMS = 152;
+    const int64_t rows = group_of(d) * d.Tq, Hk = d.H / group_of(d);
+    const double tiles = (double)((d.Tk + 63) / 64);
+    if (!tc_shape(d)) {
+        // CUDA cores: blocks of 32 rows of a head (about 1.5 us a tile of 32 states) against shares
+        // of all tiles, 4 to an SM (3 us for 16 rows)
+        const double items = (double)d.B * d.H * ((d.Tq + 31) / 32), units = (double)d.B * Hk * ((rows + 15) / 16);
+        const double whole = 6 + std::ceil(items / (2 * SMS)) * 2 * tiles * 1.5;
+        return 20 + units * 2 * tiles / (4 * SMS) * 3 < whole;
+    }
+    const double items = (double)d.B * d.H * ((d.Tq + 127) / 128);
+    const double whole = 5 + std::ceil(items / SMS) * tiles * (d.D == 64 ? 0.65 : 0.87);
+    if (rows <= 16) {
+        const double bytes = (double)d.B * Hk * d.Tk * (4 * d.D + 256);
+        return 12.5 + bytes / 5.8e6 < whole;
+    }
+    const int64_t head_rows = (d.Tq + 7) / 8 * 8;
+    const double chunks = d.Tq <= 128 ? std::ceil(group_of(d) / std::floor(128.0 / head_rows))
+                                      : (double)group_of(d) * ((d.Tq + 127) / 128);
+    return 16 + d.B * Hk * chunks * tiles / SMS * 0.95 < whole;
+}
+
 // Heads that the persistent kernels work on at a time, each streaming `bytes`: about 48 MiB of
 // them (they then share the L2), with an item of `tiles` for every SM.
 int heads_at_once(int64_t heads, int64_t bytes, int64_t tiles, int sms) {
@@ -252,7 +285,8 @@ extern "C" {
 
 size_t diffattn_cross_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
-    return 64;                          // an item counter
+    const size_t paged = wants_split(*desc) ? cross_paged_bytes(*desc) : 0;
+    return paged > 64 ? paged : 64;     // or an item counter
 }
 
 size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc* desc) {
@@ -299,6 +333,8 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!out2 && wants_split(d))
+        return cross_paged(d, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev, e, out, workspace, workspace_bytes, st);
     if (tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(out, rows, d.o_stride) && (!out2 || aligned16(out2)))
         return forward_tc(p, sms, workspace, st);
     return launch_cross_simt(p, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;

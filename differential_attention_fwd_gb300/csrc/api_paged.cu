@@ -209,10 +209,11 @@ bool tma_strides(const int64_t n[3], const int64_t s[3]) {
 
 // Whether the tensor-core kernels take the shape and the cache's layout: bf16, value
 // width 128, Q/K width 64 or 128, pages of a multiple of 16 slots, and strides (with the
-// bases, checked at the call) that TMA takes.
-bool tc_shape(const diffattn_paged_desc& d, const diffattn_pages& g) {
+// bases, checked at the call) that TMA takes.  (A box of slots then lies in one page; where a
+// page is a whole sequence, `cross`, one that passes its end reads zeros there.)
+bool tc_shape(const diffattn_paged_desc& d, const diffattn_pages& g, bool cross) {
     if (d.dtype != DIFFATTN_BF16 || (d.Dv == 0 ? 2 * d.D : d.Dv) != 128 || (d.D != 64 && d.D != 128) ||
-        g.page_size % 16 != 0)
+        (g.page_size % 16 != 0 && !cross))
         return false;
     const int64_t n[3] = {g.num_pages, d.H / (d.kv_group > 1 ? d.kv_group : 1), g.page_size};
     return tma_strides(n, g.k1_stride) && tma_strides(n, g.k2_stride) && tma_strides(n, g.v_stride);
@@ -268,7 +269,169 @@ int device_sms() {
     return sms;
 }
 
+// Bytes of workspace for the sizes, whatever kernel the call's layout leads to.
+size_t paged_bytes(const diffattn_paged_desc& d, const diffattn_pages& g, bool cross) {
+    PagedPlan n;
+    const int sms = device_sms();
+    plan_simt(d, g, sms, &n);
+    size_t bytes = n.bytes;
+    if (tc_shape(d, g, cross)) {
+        plan_mma(d, g, sms, &n);
+        if (n.bytes > bytes) bytes = n.bytes;
+        if (wants_tc(d)) {
+            plan_tc(d, g, sms, &n);
+            if (n.bytes > bytes) bytes = n.bytes;
+        }
+    }
+    return bytes;
+}
+
+// The call, its arguments checked.
+int paged_attention(const diffattn_paged_desc& d, const diffattn_pages& g, bool cross, const void* q1, const void* k1_cache,
+                    const void* q2, const void* k2_cache, const void* v_cache, const int32_t* block_table,
+                    const int32_t* lengths, const int32_t* q_lengths, const uint8_t* tree_mask, float lambda,
+                    const float* lambda_dev, const diffattn_epilogue& e, void* out, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+    const int64_t rows[3] = {d.B, d.H, d.Tq};
+    const int64_t es = d.dtype == DIFFATTN_BF16 ? 2 : 4;
+    PagedParams p{};
+    int sms = 0;
+    const int rc = device_info(&p.status, &sms);
+    if (rc != DIFFATTN_OK) return rc;
+    PagedPlan n;
+    const bool tc = tc_shape(d, g, cross) && aligned16(k1_cache) && aligned16(k2_cache) && aligned16(v_cache);
+    // the queries go through TMA too, from 16-byte aligned rows
+    const bool tcgen = tc && wants_tc(d) && aligned16(q1) && aligned16(q2) && tma_strides(rows, d.q1_stride) &&
+                       tma_strides(rows, d.q2_stride);
+    if (tcgen) plan_tc(d, g, sms, &n);
+    else if (tc) plan_mma(d, g, sms, &n);
+    else plan_simt(d, g, sms, &n);
+    if (workspace_bytes < n.bytes) return DIFFATTN_ERR_INVALID;
+    p.B = (int)d.B;
+    p.H = (int)d.H;
+    p.group = d.kv_group > 1 ? d.kv_group : 1;
+    p.Hk = p.H / p.group;
+    p.Tq = (int)d.Tq;
+    p.D = (int)d.D;
+    p.Dv = (int)(d.Dv == 0 ? 2 * d.D : d.Dv);
+    p.bf16 = d.dtype == DIFFATTN_BF16;
+    p.k_shared = k1_cache == k2_cache && same3(g.k1_stride, g.k2_stride);
+    p.page = (int)g.page_size;
+    p.max_pages = g.max_pages;
+    p.num_pages = g.num_pages;
+    p.q1 = q1;
+    p.q2 = q2;
+    p.k1 = k1_cache;
+    p.k2 = k2_cache;
+    p.v = v_cache;
+    p.out = out;
+    copy3(p.s_q1, d.q1_stride);
+    copy3(p.s_q2, d.q2_stride);
+    copy3(p.s_o, d.o_stride);
+    copy3(p.s_k1, g.k1_stride);
+    copy3(p.s_k2, g.k2_stride);
+    copy3(p.s_v, g.v_stride);
+    p.table = block_table;
+    p.table_stride = g.block_table_stride;
+    p.lengths = lengths;
+    p.cross = cross;
+    p.q_lengths = q_lengths;
+    p.zero_rest = q_lengths && d.zero_rest;
+    p.mask = tree_mask;
+    p.mask_stride[0] = d.mask_stride[0];
+    p.mask_stride[1] = d.mask_stride[1];
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d.D));
+    p.lambda = lambda;
+    p.lambda_dev = lambda_dev;
+    p.norm = e.norm;
+    p.norm_eps = e.eps;
+    p.norm_weight = e.weight;
+    p.norm_bias = e.bias;
+    p.out_scale = e.out_scale;
+    p.vec16 = p.D * es % 16 == 0 && p.Dv * es % 16 == 0 && rows16(p.k1, p.s_k1, es) && rows16(p.k2, p.s_k2, es) &&
+              rows16(p.v, p.s_v, es);
+    p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
+    p.o4 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(d.o_stride[0] * es) | (uintptr_t)(d.o_stride[1] * es) |
+            (uintptr_t)(d.o_stride[2] * es)) % 4 == 0;
+    p.o16 = rows16(out, d.o_stride, es);
+    p.joins = static_cast<PagedJoin*>(workspace);
+    p.part = reinterpret_cast<float*>(p.joins + n.workers);
+    p.head_rows = n.head_rows;
+    p.chunk_rows = n.chunk_rows;
+    p.row_chunks = n.row_chunks;
+    p.workers = n.workers;
+    p.sparse_joins = tc && !tcgen && n.chunk_rows <= paged_solo_rows(p.D);
+    p.solo_workers = sms * kMmaBlocks * kMmaWarps;
+    if (tc) {
+        // boxes that stay inside one page and divide the tile
+        int box = tcgen ? kTcTile : 16;          // a slice of the 16-row kernel
+        while (!cross && p.page % box != 0) box /= 2;
+        CUtensorMap maps[5];
+        const int64_t kd[4] = {p.D, p.page, p.Hk, p.num_pages}, vd[4] = {p.Dv, p.page, p.Hk, p.num_pages};
+        if (encode_map_4d(&maps[0], p.k1, kd, p.s_k1, 64, box) != DIFFATTN_OK ||
+            encode_map_4d(&maps[1], p.k2, kd, p.s_k2, 64, box) != DIFFATTN_OK ||
+            encode_map_4d(&maps[2], p.v, vd, p.s_v, 64, box) != DIFFATTN_OK)
+            return DIFFATTN_ERR_CUDA;
+        if (tcgen) {
+            const int q_box = p.head_rows < kTcRows ? p.head_rows : kTcRows;
+            const int64_t qd[4] = {p.D, p.Tq, p.H, p.B};
+            if (encode_map_4d(&maps[3], q1, qd, p.s_q1, 64, q_box) != DIFFATTN_OK ||
+                encode_map_4d(&maps[4], q2, qd, p.s_q2, 64, q_box) != DIFFATTN_OK)
+                return DIFFATTN_ERR_CUDA;
+            return launch_paged_tc(maps, p, box, q_box, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+        }
+        return launch_paged_mma(maps, p, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+    }
+    return launch_paged_simt(p, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+}
+
+// An encoder's states as a cache whose pages are whole sequences.
+void as_pages(const diffattn_cross_desc& c, diffattn_paged_desc* d, diffattn_pages* g) {
+    *d = diffattn_paged_desc{};
+    d->B = c.B;
+    d->H = c.H;
+    d->Tq = c.Tq;
+    d->D = c.D;
+    d->Dv = c.Dv;
+    d->dtype = c.dtype;
+    d->kv_group = c.kv_group;
+    copy3(d->q1_stride, c.q1_stride);
+    copy3(d->q2_stride, c.q2_stride);
+    copy3(d->o_stride, c.o_stride);
+    *g = diffattn_pages{};
+    g->num_pages = c.B;
+    g->page_size = c.Tk;
+    g->max_pages = 1;
+    copy3(g->k1_stride, c.k1_stride);
+    copy3(g->k2_stride, c.k2_stride);
+    copy3(g->v_stride, c.v_stride);
+}
 }  // namespace
+
+bool cross_paged_ok(const diffattn_cross_desc& c) {
+    diffattn_paged_desc d;
+    diffattn_pages g;
+    as_pages(c, &d, &g);
+    return check_paged(&d, &g) == DIFFATTN_OK;
+}
+
+size_t cross_paged_bytes(const diffattn_cross_desc& c) {
+    diffattn_paged_desc d;
+    diffattn_pages g;
+    as_pages(c, &d, &g);
+    return paged_bytes(d, g, true);
+}
+
+int cross_paged(const diffattn_cross_desc& c, const void* q1, const void* k1, const void* q2, const void* k2, const void* v,
+                const int32_t* lengths, float lambda, const float* lambda_dev, const diffattn_epilogue& e, void* out,
+                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    diffattn_paged_desc d;
+    diffattn_pages g;
+    as_pages(c, &d, &g);
+    return paged_attention(d, g, true, q1, k1, q2, k2, v, nullptr, lengths, nullptr, nullptr, lambda, lambda_dev, e, out,
+                           workspace, workspace_bytes, stream);
+}
+
 }  // namespace diffattn
 
 using namespace diffattn;
@@ -426,20 +589,7 @@ int diffattn_paged_append_axes(const diffattn_rotary_desc* desc, const diffattn_
 }
 
 size_t diffattn_paged_workspace_bytes(const diffattn_paged_desc* desc, const diffattn_pages* pages) {
-    if (check_paged(desc, pages) != DIFFATTN_OK) return 0;
-    PagedPlan n;
-    const int sms = device_sms();
-    plan_simt(*desc, *pages, sms, &n);
-    size_t bytes = n.bytes;
-    if (tc_shape(*desc, *pages)) {
-        plan_mma(*desc, *pages, sms, &n);
-        if (n.bytes > bytes) bytes = n.bytes;
-        if (wants_tc(*desc)) {
-            plan_tc(*desc, *pages, sms, &n);
-            if (n.bytes > bytes) bytes = n.bytes;
-        }
-    }
-    return bytes;
+    return check_paged(desc, pages) == DIFFATTN_OK ? paged_bytes(*desc, *pages, false) : 0;
 }
 
 int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages* pages, const void* q1,
@@ -461,97 +611,8 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     const diffattn_paged_desc& d = *desc;
     const int64_t rows[3] = {d.B, d.H, d.Tq};
     if (!apart(rows, d.o_stride)) return DIFFATTN_ERR_INVALID;
-    const int64_t es = d.dtype == DIFFATTN_BF16 ? 2 : 4;
-    PagedParams p{};
-    int sms = 0;
-    rc = device_info(&p.status, &sms);
-    if (rc != DIFFATTN_OK) return rc;
-    PagedPlan n;
-    const bool tc = tc_shape(d, *pages) && aligned16(k1_cache) && aligned16(k2_cache) && aligned16(v_cache);
-    // the queries go through TMA too, from 16-byte aligned rows
-    const bool tcgen = tc && wants_tc(d) && aligned16(q1) && aligned16(q2) && tma_strides(rows, d.q1_stride) &&
-                       tma_strides(rows, d.q2_stride);
-    if (tcgen) plan_tc(d, *pages, sms, &n);
-    else if (tc) plan_mma(d, *pages, sms, &n);
-    else plan_simt(d, *pages, sms, &n);
-    if (workspace_bytes < n.bytes) return DIFFATTN_ERR_INVALID;
-    p.B = (int)d.B;
-    p.H = (int)d.H;
-    p.group = d.kv_group > 1 ? d.kv_group : 1;
-    p.Hk = p.H / p.group;
-    p.Tq = (int)d.Tq;
-    p.D = (int)d.D;
-    p.Dv = (int)(d.Dv == 0 ? 2 * d.D : d.Dv);
-    p.bf16 = d.dtype == DIFFATTN_BF16;
-    p.k_shared = k1_cache == k2_cache && same3(pages->k1_stride, pages->k2_stride);
-    p.page = (int)pages->page_size;
-    p.max_pages = pages->max_pages;
-    p.num_pages = pages->num_pages;
-    p.q1 = q1;
-    p.q2 = q2;
-    p.k1 = k1_cache;
-    p.k2 = k2_cache;
-    p.v = v_cache;
-    p.out = out;
-    copy3(p.s_q1, d.q1_stride);
-    copy3(p.s_q2, d.q2_stride);
-    copy3(p.s_o, d.o_stride);
-    copy3(p.s_k1, pages->k1_stride);
-    copy3(p.s_k2, pages->k2_stride);
-    copy3(p.s_v, pages->v_stride);
-    p.table = block_table;
-    p.table_stride = pages->block_table_stride;
-    p.lengths = lengths;
-    p.q_lengths = q_lengths;
-    p.zero_rest = q_lengths && d.zero_rest;
-    p.mask = tree_mask;
-    p.mask_stride[0] = d.mask_stride[0];
-    p.mask_stride[1] = d.mask_stride[1];
-    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d.D));
-    p.lambda = lambda;
-    p.lambda_dev = lambda_dev;
-    p.norm = e.norm;
-    p.norm_eps = e.eps;
-    p.norm_weight = e.weight;
-    p.norm_bias = e.bias;
-    p.out_scale = e.out_scale;
-    p.vec16 = p.D * es % 16 == 0 && p.Dv * es % 16 == 0 && rows16(p.k1, p.s_k1, es) && rows16(p.k2, p.s_k2, es) &&
-              rows16(p.v, p.s_v, es);
-    p.q16 = rows16(q1, d.q1_stride, es) && rows16(q2, d.q2_stride, es);
-    p.o4 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(d.o_stride[0] * es) | (uintptr_t)(d.o_stride[1] * es) |
-            (uintptr_t)(d.o_stride[2] * es)) % 4 == 0;
-    p.o16 = rows16(out, d.o_stride, es);
-    p.joins = static_cast<PagedJoin*>(workspace);
-    p.part = reinterpret_cast<float*>(p.joins + n.workers);
-    p.head_rows = n.head_rows;
-    p.chunk_rows = n.chunk_rows;
-    p.row_chunks = n.row_chunks;
-    p.workers = n.workers;
-    p.sparse_joins = tc && !tcgen && n.chunk_rows <= paged_solo_rows(p.D);
-    p.solo_workers = sms * kMmaBlocks * kMmaWarps;
-    if (tc) {
-        // boxes that stay inside one page and divide the tile
-        int box = tcgen ? kTcTile : 16;          // a slice of the 16-row kernel
-        while (p.page % box != 0) box /= 2;
-        CUtensorMap maps[5];
-        const int64_t kd[4] = {p.D, p.page, p.Hk, p.num_pages}, vd[4] = {p.Dv, p.page, p.Hk, p.num_pages};
-        if (encode_map_4d(&maps[0], p.k1, kd, p.s_k1, 64, box) != DIFFATTN_OK ||
-            encode_map_4d(&maps[1], p.k2, kd, p.s_k2, 64, box) != DIFFATTN_OK ||
-            encode_map_4d(&maps[2], p.v, vd, p.s_v, 64, box) != DIFFATTN_OK)
-            return DIFFATTN_ERR_CUDA;
-        if (tcgen) {
-            const int q_box = p.head_rows < kTcRows ? p.head_rows : kTcRows;
-            const int64_t qd[4] = {p.D, p.Tq, p.H, p.B};
-            if (encode_map_4d(&maps[3], q1, qd, p.s_q1, 64, q_box) != DIFFATTN_OK ||
-                encode_map_4d(&maps[4], q2, qd, p.s_q2, 64, q_box) != DIFFATTN_OK)
-                return DIFFATTN_ERR_CUDA;
-            return launch_paged_tc(maps, p, box, q_box, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
-                                                                                                     : DIFFATTN_ERR_CUDA;
-        }
-        return launch_paged_mma(maps, p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK
-                                                                                           : DIFFATTN_ERR_CUDA;
-    }
-    return launch_paged_simt(p, reinterpret_cast<cudaStream_t>(stream)) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+    return paged_attention(d, *pages, false, q1, k1_cache, q2, k2_cache, v_cache, block_table, lengths, q_lengths, tree_mask,
+                           lambda, lambda_dev, e, out, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -34,6 +34,9 @@ constexpr int THREADS = 256;
 constexpr int BM = 32;          // query rows of a tile
 constexpr int BN = 32;          // states of a tile
 constexpr int LP = BM + 4;      // row stride of the score tiles
+// Stages of the operands that a block walks: float32 tiles arrive while the last is worked on.
+template <typename T>
+constexpr int STAGES = sizeof(T) == 4 ? 2 : 1;
 
 // Sizes by class: 0: D <= 32, Dv <= 64; 1: D <= 64, Dv <= 128; 2: D <= 128, Dv <= 256.
 template <int S>
@@ -47,16 +50,79 @@ struct Size {
 
 __host__ __device__ constexpr int padded(int n) { return (n + 3) / 4 * 4 + 4; }
 
-// `count` rows of `width` elements (the rest of 32 rows zeros, and of the padding) into
-// shared memory as floats; a warp a row.
+// 4 or 16 bytes from global to shared memory by cp.async, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void async_copy(float* dst, const void* src, bool there) {
+    const int n = there ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// `count` rows of `width` elements into 32 rows of `ld` floats; the other rows, and the columns
+// up to 4 past the width's multiple of 4, are zeros.  float32 goes by cp.async, so that a tile
+// arrives while the last one is worked on (async_wait, then a barrier); bf16 through registers,
+// four pieces of a row at a time.  vec: rows of whole 16-byte pieces on 16-byte boundaries.
 template <typename T>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t stride, int count, int width) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t stride, int count, int width, bool vec) {
+    constexpr int V = 16 / sizeof(T);
+    const int step = vec ? V : 1, pieces = width / step;
+    // lanes of a row: a power of two, as many as it has pieces, 32 at most
+    const int lanes = pieces > 16 ? 32 : pieces > 8 ? 16 : pieces > 4 ? 8 : 4;
+    const int sub = threadIdx.x & (lanes - 1);
+    const int rows = THREADS / lanes;
+    if constexpr (sizeof(T) == 4) {
+        for (int r = threadIdx.x / lanes; r < 32; r += rows) {
+            const T* row = src + (int64_t)(r < count ? r : 0) * stride;
+            for (int c = sub; c < pieces; c += lanes) {
+                if (vec) async_copy<16>(dst + r * ld + 4 * c, row + 4 * c, r < count);
+                else async_copy<4>(dst + r * ld + c, row + c, r < count);
+            }
+            for (int c = width + sub; c < ld; c += lanes) dst[r * ld + c] = 0.f;
+        }
+    } else {
+        for (int r = threadIdx.x / lanes; r < 32; r += rows) {
+            const T* row = src + (int64_t)(r < count ? r : 0) * stride;
+            float* to = dst + r * ld;
+            for (int c0 = sub; c0 < pieces; c0 += 4 * lanes) {
+                if (vec) {
+                    uint4 x[4];
 #pragma unroll
-    for (int r = warp; r < 32; r += THREADS / 32) {
-        const T* row = src + (int64_t)r * stride;
-        for (int c = lane; c < ld; c += 32) dst[r * ld + c] = r < count && c < width ? Vec<T>::get(row[c]) : 0.f;
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = r < count && c0 + i * lanes < pieces ? *reinterpret_cast<const uint4*>(row + V * (c0 + i * lanes))
+                                                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (c0 + i * lanes >= pieces) break;
+                        uint64_t f[4];
+                        Vec<__nv_bfloat16>::unpack(x[i], f);
+                        float4* at = reinterpret_cast<float4*>(to + V * (c0 + i * lanes));
+                        at[0] = make_float4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1]));
+                        at[1] = make_float4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3]));
+                    }
+                } else {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = r < count && c0 + i * lanes < pieces ? Vec<T>::get(row[c0 + i * lanes]) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c0 + i * lanes < pieces) to[c0 + i * lanes] = x[i];
+                }
+            }
+            for (int c = width + sub; c < ld; c += lanes) to[c] = 0.f;
+        }
     }
+}
+
+// Whether rows of this width, base and strides are whole 16-byte pieces.
+template <typename T>
+__device__ __forceinline__ bool pieces16(const void* p, const int64_t (&s)[3], int width) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)(s[0] * sizeof(T)) | (uint64_t)(s[1] * sizeof(T)) |
+             (uint64_t)(s[2] * sizeof(T)) | (uint64_t)(width * sizeof(T))) & 15) == 0;
 }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
@@ -178,10 +244,52 @@ __device__ __forceinline__ Rows rows_of(const CrossParams& p) {
     return r;
 }
 
+// A head's rows in global memory, and how they are read.
 template <typename T>
-__device__ __forceinline__ const T* head(const void* x, const int64_t (&s)[3], int b, int h) {
-    return static_cast<const T*>(x) + b * s[0] + h * s[1];
-}
+struct Source {
+    const T* at;
+    int64_t stride;
+    int width;
+    bool vec;
+    __device__ __forceinline__ Source(const void* x, const int64_t (&s)[3], int b, int h, int w)
+        : at(static_cast<const T*>(x) + b * s[0] + h * s[1]), stride(s[2]), width(w), vec(pieces16<T>(x, s, w)) {}
+    __device__ __forceinline__ void load(float* dst, int ld, int row, int count) const {
+        load_rows(dst, ld, at + row * stride, stride, count, width, vec);
+    }
+};
+
+// A sequence's states, tile by tile.
+template <typename T>
+struct States {
+    Source<T> k1, k2, v;
+    int n, ld, lv;
+    __device__ __forceinline__ States(const CrossParams& p, int b, int hk, int n_, int ld_, int lv_)
+        : k1(p.k1, p.s_k1, b, hk, p.D), k2(p.k2, p.s_k2, b, hk, p.D), v(p.v, p.s_v, b, hk, p.Dv), n(n_), ld(ld_), lv(lv_) {}
+    __device__ __forceinline__ void fetch(float* to, int k0) const {
+        const int live = min(BN, n - k0);
+        k1.load(to, ld, k0, live);
+        k2.load(to + BN * ld, ld, k0, live);
+        v.load(to + 2 * BN * ld, lv, k0, live);
+        async_commit();
+    }
+    // Before the first tile, and for each: where tile k0 is, with the next one on its way.
+    __device__ __forceinline__ void begin(float* kv) const {
+        if (STAGES<T> == 2) fetch(kv, 0);
+    }
+    __device__ __forceinline__ float* next(float* kv, int stage, int k0) const {
+        if (STAGES<T> == 1) {
+            __syncthreads();                    // the last tile has been read
+            fetch(kv, k0);
+            __syncthreads();
+            return kv;
+        }
+        const int now = (k0 / BN) & 1;
+        async_wait();
+        __syncthreads();                        // the tile is there, and the last one has been read
+        if (k0 + BN < n) fetch(kv + (now ^ 1) * stage, k0 + BN);
+        return kv + now * stage;
+    }
+};
 
 // ---------------------------------------------------------------------------
 // forward
@@ -193,30 +301,29 @@ cross_fwd_kernel(const CrossParams p) {
     extern __shared__ __align__(16) float sm[];
     const int ld = padded(p.D), lv = padded(p.Dv);
     float* qs = sm;                             // [branch][row][ld]
-    float* ks = qs + 2 * BM * ld;               // [branch][state][ld]
-    float* vs = ks + 2 * BN * ld;               // [state][lv]
-    float* ps = vs + BN * lv;                   // [branch][state][LP]
+    float* kv = qs + 2 * BM * ld;               // [stage]: keys [branch][state][ld], values [state][lv]
+    const int stage = 2 * BN * ld + BN * lv;
+    float* ps = kv + STAGES<T> * stage;         // [branch][state][LP]
     float* fix = ps + 2 * BN * LP;              // [branch][row]: the tile's rescaling, then 1 / l
     pdl_wait();
     pdl_launch_dependents();
     const Rows r = rows_of(p);
     const CrossLen len = cross_len(p.lengths, r.b, p.Tk);
     if (len.bad && threadIdx.x == 0) atomicOr(p.status, kStatusIndex);
-    load_rows(qs, ld, head<T>(p.q1, p.s_q1, r.b, r.h) + r.q0 * p.s_q1[2], p.s_q1[2], r.count, p.D);
-    load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, r.b, r.h) + r.q0 * p.s_q2[2], p.s_q2[2], r.count, p.D);
+    Source<T>(p.q1, p.s_q1, r.b, r.h, p.D).load(qs, ld, r.q0, r.count);
+    Source<T>(p.q2, p.s_q2, r.b, r.h, p.D).load(qs + BM * ld, ld, r.q0, r.count);
     // the softmax: four threads a row and branch
     const int br = threadIdx.x >> 7, row = (threadIdx.x >> 2) & 31, sub = threadIdx.x & 3;
     float m = -INFINITY, l = 0.f;
     // the output: RV rows by NV float4 columns a thread
     const int r0 = threadIdx.x / Z::CV * Z::RV, c0 = threadIdx.x % Z::CV * 4;
     float4 o1[Z::RV][Z::NV] = {}, o2[Z::RV][Z::NV] = {};
+    const States<T> states(p, r.b, r.hk, len.n, ld, lv);
+    if (len.n > 0) states.begin(kv);
     for (int k0 = 0; k0 < len.n; k0 += BN) {
         const int live = min(BN, len.n - k0);
-        __syncthreads();                        // the last tile has been read
-        load_rows(ks, ld, head<T>(p.k1, p.s_k1, r.b, r.hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
-        load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, r.b, r.hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
-        load_rows(vs, lv, head<T>(p.v, p.s_v, r.b, r.hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
-        __syncthreads();
+        const float* ks = states.next(kv, stage, k0);
+        const float* vs = ks + 2 * BN * ld;
         scores(qs, ks, ld, p.D, ps, true);
         __syncthreads();
         {
@@ -258,6 +365,7 @@ cross_fwd_kernel(const CrossParams p) {
         accumulate<Z::RV, Z::NV>(ps, r0, vs, lv, c0, 4 * Z::CV, p.Dv, o1);
         accumulate<Z::RV, Z::NV>(ps + BN * LP, r0, vs, lv, c0, 4 * Z::CV, p.Dv, o2);
     }
+    async_wait();                               // (the queries, where there was no state)
     __syncthreads();
     const float nan = __int_as_float(0x7fc00000);
     if (sub == 0) {
@@ -278,7 +386,7 @@ cross_fwd_kernel(const CrossParams p) {
             const float4 x = o1[i][n], y = o2[i][n];
             const float4 b = make_float4(__fmul_rn(y.x, i2), __fmul_rn(y.y, i2), __fmul_rn(y.z, i2), __fmul_rn(y.w, i2));
             // the branches rounded alike, so that alike branches cancel exactly at lambda = 1
-            *reinterpret_cast<float4*>(vs + (r0 + i) * lv + c) =
+            *reinterpret_cast<float4*>(kv + (r0 + i) * lv + c) =
                 make_float4(fmaf(-lam, b.x, __fmul_rn(x.x, i1)), fmaf(-lam, b.y, __fmul_rn(x.y, i1)),
                             fmaf(-lam, b.z, __fmul_rn(x.z, i1)), fmaf(-lam, b.w, __fmul_rn(x.w, i1)));
             if (out2 && r0 + i < r.count) put4(out2 + (r0 + i) * p.s_o[2], c, p.Dv, b, 1.f);
@@ -288,7 +396,7 @@ cross_fwd_kernel(const CrossParams p) {
     // the epilogue, a warp a row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = warp; i < r.count; i += THREADS / 32) {
-        const float* y = vs + i * lv;
+        const float* y = kv + i * lv;
         float mu = 0.f, rs = 1.f;
         if (p.norm != kNormNone) {
             if (p.norm == kNormGroup) {
@@ -322,18 +430,19 @@ cross_dq_kernel(const CrossParams p) {
     const int ld = padded(p.D), lv = padded(p.Dv);
     float* qs = sm;
     float* gs = qs + 2 * BM * ld;               // [row][lv]
-    float* ks = gs + BM * lv;
-    float* vs = ks + 2 * BN * ld;
-    float* ps = vs + BN * lv;                   // [branch][state][LP]: scores, then dS
+    float* kv = gs + BM * lv;
+    const int stage = 2 * BN * ld + BN * lv;
+    float* ps = kv + STAGES<T> * stage;         // [branch][state][LP]: scores, then dS
     float* ds = ps + 2 * BN * LP;               // [state][LP]: dP
     pdl_wait();
     pdl_launch_dependents();
     const Rows r = rows_of(p);
     const CrossLen len = cross_len(p.lengths, r.b, p.Tk);
     if (len.bad && threadIdx.x == 0) atomicOr(p.status, kStatusIndex);
-    load_rows(qs, ld, head<T>(p.q1, p.s_q1, r.b, r.h) + r.q0 * p.s_q1[2], p.s_q1[2], r.count, p.D);
-    load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, r.b, r.h) + r.q0 * p.s_q2[2], p.s_q2[2], r.count, p.D);
-    load_rows(gs, lv, head<T>(p.dout, p.s_do, r.b, r.h) + r.q0 * p.s_do[2], p.s_do[2], r.count, p.Dv);
+    Source<T>(p.q1, p.s_q1, r.b, r.h, p.D).load(qs, ld, r.q0, r.count);
+    Source<T>(p.q2, p.s_q2, r.b, r.h, p.D).load(qs + BM * ld, ld, r.q0, r.count);
+    const Source<T> grads(p.dout, p.s_do, r.b, r.h, p.Dv);
+    grads.load(gs, lv, r.q0, r.count);
     const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
     const int br = threadIdx.x >> 7, row = (threadIdx.x >> 2) & 31, sub = threadIdx.x & 3;
     const int64_t at = ((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + row;
@@ -344,7 +453,7 @@ cross_dq_kernel(const CrossParams p) {
         const int64_t o = r.b * p.s_o[0] + r.h * p.s_o[1] + (r.q0 + row) * p.s_o[2];
         const T* o1 = static_cast<const T*>(p.out) + o;
         const T* o2 = static_cast<const T*>(p.out2) + o;
-        const T* g = head<T>(p.dout, p.s_do, r.b, r.h) + (r.q0 + row) * p.s_do[2];
+        const T* g = grads.at + (r.q0 + row) * grads.stride;
         for (int c = sub; c < p.Dv; c += 4) {
             const float x = Vec<T>::get(o2[c]);
             dd = fmaf(Vec<T>::get(g[c]), br ? x : fmaf(lam, x, Vec<T>::get(o1[c])), dd);
@@ -356,14 +465,13 @@ cross_dq_kernel(const CrossParams p) {
     }
     const int half = threadIdx.x & 127, r0 = half / Z::CD * Z::RD, c0 = half % Z::CD * 4;
     float4 acc[Z::RD][1] = {};
+    const States<T> states(p, r.b, r.hk, len.n, ld, lv);
     for (int sweep = TWICE ? 0 : 1; sweep < 2; ++sweep) {
+        if (len.n > 0) states.begin(kv);
         for (int k0 = 0; k0 < len.n; k0 += BN) {
             const int live = min(BN, len.n - k0);
-            __syncthreads();
-            load_rows(ks, ld, head<T>(p.k1, p.s_k1, r.b, r.hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
-            load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, r.b, r.hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
-            load_rows(vs, lv, head<T>(p.v, p.s_v, r.b, r.hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
-            __syncthreads();
+            const float* ks = states.next(kv, stage, k0);
+            const float* vs = ks + 2 * BN * ld;
             scores(qs, ks, ld, p.D, ps, true);
             products(gs, vs, lv, p.Dv, ds, true);
             __syncthreads();
@@ -385,6 +493,7 @@ cross_dq_kernel(const CrossParams p) {
             dd += __shfl_xor_sync(0xffffffffu, dd, 2);
         }
     }
+    async_wait();
     const float nan = __int_as_float(0x7fc00000);
     if (sub == 0 && row < r.count) {
         p.stats[at * 4 + br] = lse;
@@ -407,11 +516,11 @@ cross_dkdv_kernel(const CrossParams p) {
     using Z = Size<S>;
     extern __shared__ __align__(16) float sm[];
     const int ld = padded(p.D), lv = padded(p.Dv);
-    float* qs = sm;
-    float* gs = qs + 2 * BM * ld;
-    float* ks = gs + BM * lv;
-    float* vs = ks + 2 * BN * ld;
-    float* ps = vs + BN * lv;                   // [branch][row][LP]: scores, then dS
+    float* ks = sm;                             // [branch][state][ld]
+    float* vs = ks + 2 * BN * ld;               // [state][lv]
+    float* rows_at = vs + BN * lv;              // [stage]: queries [branch][row][ld], dO [row][lv]
+    const int stage = 2 * BM * ld + BM * lv;
+    float* ps = rows_at + STAGES<T> * stage;    // [branch][row][LP]: scores, then dS
     float* ds = ps + 2 * BM * LP;               // [row][LP]: dP, then W = A_1 - lambda A_2
     const int tiles = (p.Tk + BN - 1) / BN;
     const int bh = blockIdx.x / tiles, b = bh / p.Hk, hk = bh - b * p.Hk;
@@ -426,39 +535,52 @@ cross_dkdv_kernel(const CrossParams p) {
     const int rv = threadIdx.x / Z::CV * Z::RV, cv = threadIdx.x % Z::CV * 4;
     float4 dk[Z::RD][1] = {}, dv[Z::RV][Z::NV] = {};
     if (live > 0) {
-        load_rows(ks, ld, head<T>(p.k1, p.s_k1, b, hk) + k0 * p.s_k1[2], p.s_k1[2], live, p.D);
-        load_rows(ks + BN * ld, ld, head<T>(p.k2, p.s_k2, b, hk) + k0 * p.s_k2[2], p.s_k2[2], live, p.D);
-        load_rows(vs, lv, head<T>(p.v, p.s_v, b, hk) + k0 * p.s_v[2], p.s_v[2], live, p.Dv);
-        for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
-            for (int q0 = 0; q0 < p.Tq; q0 += BM) {
-                const int rows = min(BM, p.Tq - q0);
+        Source<T>(p.k1, p.s_k1, b, hk, p.D).load(ks, ld, k0, live);
+        Source<T>(p.k2, p.s_k2, b, hk, p.D).load(ks + BN * ld, ld, k0, live);
+        Source<T>(p.v, p.s_v, b, hk, p.Dv).load(vs, lv, k0, live);
+        const int per_head = (p.Tq + BM - 1) / BM, total = p.group * per_head;
+        auto fetch = [&](float* to, int i) {
+            const int h = hk * p.group + i / per_head, q0 = i % per_head * BM, rows = min(BM, p.Tq - q0);
+            Source<T>(p.q1, p.s_q1, b, h, p.D).load(to, ld, q0, rows);
+            Source<T>(p.q2, p.s_q2, b, h, p.D).load(to + BM * ld, ld, q0, rows);
+            Source<T>(p.dout, p.s_do, b, h, p.Dv).load(to + 2 * BM * ld, lv, q0, rows);
+            async_commit();
+        };
+        if (STAGES<T> == 2) fetch(rows_at, 0);
+        for (int i = 0; i < total; ++i) {
+            const int h = hk * p.group + i / per_head, q0 = i % per_head * BM, rows = min(BM, p.Tq - q0);
+            const float* qs = rows_at + (STAGES<T> == 2 ? (i & 1) * stage : 0);
+            const float* gs = qs + 2 * BM * ld;
+            if (STAGES<T> == 2) {
+                async_wait();
+                __syncthreads();                // the rows are there, and the last ones have been read
+                if (i + 1 < total) fetch(rows_at + ((i & 1) ^ 1) * stage, i + 1);
+            } else {
                 __syncthreads();
-                load_rows(qs, ld, head<T>(p.q1, p.s_q1, b, h) + q0 * p.s_q1[2], p.s_q1[2], rows, p.D);
-                load_rows(qs + BM * ld, ld, head<T>(p.q2, p.s_q2, b, h) + q0 * p.s_q2[2], p.s_q2[2], rows, p.D);
-                load_rows(gs, lv, head<T>(p.dout, p.s_do, b, h) + q0 * p.s_do[2], p.s_do[2], rows, p.Dv);
+                fetch(rows_at, i);
                 __syncthreads();
-                scores(qs, ks, ld, p.D, ps, false);
-                products(gs, vs, lv, p.Dv, ds, false);
-                __syncthreads();
-                const int row = threadIdx.x >> 3;
-                float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row < rows)
-                    st = *reinterpret_cast<const float4*>(p.stats + (((int64_t)b * p.H + h) * p.Tq + q0 + row) * 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = (threadIdx.x & 7) + 8 * j, i = row * LP + key;
-                    const bool seen = row < rows && key < live;
-                    const float a1 = seen ? expf(ps[i] * p.scale - st.x) : 0.f;
-                    const float a2 = seen ? lam * expf(ps[BM * LP + i] * p.scale - st.y) : 0.f;
-                    const float dp = ds[i];
-                    ps[i] = a1 * (dp - st.z);
-                    ps[BM * LP + i] = -a2 * (dp - st.w);
-                    ds[i] = a1 - a2;
-                }
-                __syncthreads();
-                accumulate<Z::RV, Z::NV>(ds, rv, gs, lv, cv, 4 * Z::CV, p.Dv, dv);
-                accumulate<Z::RD, 1>(ps + br * BM * LP, rd, qs + br * BM * ld, ld, cd, 0, p.D, dk);
             }
+            scores(qs, ks, ld, p.D, ps, false);
+            products(gs, vs, lv, p.Dv, ds, false);
+            __syncthreads();
+            const int row = threadIdx.x >> 3;
+            float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows)
+                st = *reinterpret_cast<const float4*>(p.stats + (((int64_t)b * p.H + h) * p.Tq + q0 + row) * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = (threadIdx.x & 7) + 8 * j, at = row * LP + key;
+                const bool seen = row < rows && key < live;
+                const float a1 = seen ? expf(ps[at] * p.scale - st.x) : 0.f;
+                const float a2 = seen ? lam * expf(ps[BM * LP + at] * p.scale - st.y) : 0.f;
+                const float dp = ds[at];
+                ps[at] = a1 * (dp - st.z);
+                ps[BM * LP + at] = -a2 * (dp - st.w);
+                ds[at] = a1 - a2;
+            }
+            __syncthreads();
+            accumulate<Z::RV, Z::NV>(ds, rv, gs, lv, cv, 4 * Z::CV, p.Dv, dv);
+            accumulate<Z::RD, 1>(ps + br * BM * LP, rd, qs + br * BM * ld, ld, cd, 0, p.D, dk);
         }
     }
     const float fill = len.bad ? __int_as_float(0x7fc00000) : 1.f;
@@ -473,12 +595,12 @@ cross_dkdv_kernel(const CrossParams p) {
         __syncthreads();
         if (br == 1 && cd < p.D)
 #pragma unroll
-            for (int i = 0; i < Z::RD; ++i) *reinterpret_cast<float4*>(qs + (rd + i) * ld + cd) = dk[i][0];
+            for (int i = 0; i < Z::RD; ++i) *reinterpret_cast<float4*>(rows_at + (rd + i) * ld + cd) = dk[i][0];
         __syncthreads();
         if (br == 0 && cd < p.D)
 #pragma unroll
             for (int i = 0; i < Z::RD; ++i) {
-                const float4 x = *reinterpret_cast<const float4*>(qs + (rd + i) * ld + cd);
+                const float4 x = *reinterpret_cast<const float4*>(rows_at + (rd + i) * ld + cd);
                 dk[i][0] = make_float4(dk[i][0].x + x.x, dk[i][0].y + x.y, dk[i][0].z + x.z, dk[i][0].w + x.w);
             }
         if (br == 1) return;
@@ -502,9 +624,9 @@ template <typename T, int S>
 int launch(const CrossParams& p, bool backward, cudaStream_t stream) {
     const int ld = padded(p.D), lv = padded(p.Dv);
     const int64_t row_blocks = (int64_t)p.B * p.H * ((p.Tq + BM - 1) / BM);
-    if (!backward)
-        return launch_smem(cross_fwd_kernel<T, S>, row_blocks, 2 * BM * ld + 2 * BN * ld + BN * lv + 2 * BN * LP + 2 * BM, p, stream);
-    const int floats = 2 * BM * ld + BM * lv + 2 * BN * ld + BN * lv + 3 * BN * LP;
+    const int walked = STAGES<T> * (2 * BN * ld + BN * lv);
+    if (!backward) return launch_smem(cross_fwd_kernel<T, S>, row_blocks, 2 * BM * ld + walked + 2 * BN * LP + 2 * BM, p, stream);
+    const int floats = 2 * BM * ld + BM * lv + walked + 3 * BN * LP;
     if (launch_smem(cross_dq_kernel<T, S>, row_blocks, floats, p, stream) != 0) return -1;
     if (!p.dv) return 0;
     return launch_smem(cross_dkdv_kernel<T, S>, (int64_t)p.B * p.Hk * ((p.Tk + BN - 1) / BN), floats, p, stream);

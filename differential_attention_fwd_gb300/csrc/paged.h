@@ -110,9 +110,11 @@ struct PagedParams {
     void* out;
     int64_t s_q1[3], s_q2[3], s_o[3];
     int64_t s_k1[3], s_k2[3], s_v[3];   // page, head, slot
-    const int32_t* table;
+    const int32_t* table;       // nullptr: sequence b is page b
     int64_t table_stride;
     const int32_t* lengths;
+    int cross;                  // over an encoder's states: every row sees the lengths[b] keys (nullptr: a
+                                // page's) and no other
     const int32_t* q_lengths;   // nullptr: Tq each
     const uint8_t* mask;        // tree: [B, Tq, Tq] bytes, nullptr: causal
     int64_t mask_stride[2];
@@ -168,6 +170,14 @@ constexpr int kTcTile = 64;
 int launch_paged_tc(const CUtensorMap* maps, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream);
 // Merges the partial results of the units that several blocks share.
 int launch_paged_combine(const PagedParams& p, cudaStream_t stream);
+
+// Attention over an encoder's states on the kernels of the paged cache (api_paged.cu): whether they
+// take the sizes, the workspace for them, and the call (k, v: the states, as pages of Tk slots).
+bool cross_paged_ok(const diffattn_cross_desc& d);
+size_t cross_paged_bytes(const diffattn_cross_desc& d);
+int cross_paged(const diffattn_cross_desc& d, const void* q1, const void* k1, const void* q2, const void* k2,
+                const void* v, const int32_t* lengths, float lambda, const float* lambda_dev,
+                const diffattn_epilogue& e, void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 // Checks an output epilogue and fills in what a NULL one means (api.cu).
 int check_epilogue(const diffattn_epilogue* epi, diffattn_epilogue* e);

@@ -32,6 +32,16 @@ struct PagedSeq {
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
     PagedSeq s;
+    if (p.cross) {
+        const int n = p.lengths ? p.lengths[b] : p.page;
+        s.n_new = p.Tq;
+        s.bad = n < 0 || n > p.page;
+        // a sequence without a state (and one whose length is bad) still has its rows: one key, seen by
+        // none of them
+        s.total = n > 0 && !s.bad ? n : 1;
+        s.before = s.bad ? 0 : n > 0 ? n : -p.Tq;
+        return s;
+    }
     s.n_new = p.q_lengths ? p.q_lengths[b] : p.Tq;
     s.before = p.lengths[b];
     s.total = 0;
@@ -54,6 +64,7 @@ __device__ __forceinline__ int paged_seq_tiles(const PagedSeq& s, int kt) { retu
 // The page of a key's slot, or -1 if its table entry is out of range.  `key` is below
 // the sequence's total, so the entry exists.
 __device__ __forceinline__ int paged_page(const PagedParams& p, int b, int index) {
+    if (!p.table) return b;
     const int32_t pg = __ldg(p.table + b * p.table_stride + index);
     return pg >= 0 && pg < p.num_pages ? pg : -1;
 }
