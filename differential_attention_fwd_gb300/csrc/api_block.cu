@@ -69,7 +69,8 @@ int64_t width_of(const diffattn_cross_desc& d) { return d.Dv == 0 ? 2 * d.D : d.
 
 int check_cross(const diffattn_cross_desc* d) {
     if (!d || d->B < 1 || d->H < 1 || d->Tq < 1 || d->Tk < 1 || d->D < 1 || d->D > 128 || d->Dv < 0 ||
-        (d->dtype != DIFFATTN_BF16 && d->dtype != DIFFATTN_F32) || d->kv_group < 0)
+        (d->dtype != DIFFATTN_BF16 && d->dtype != DIFFATTN_F32) || d->kv_group < 0 ||
+        (d->lambda_dtype != DIFFATTN_BF16 && d->lambda_dtype != DIFFATTN_F32) || d->reserved != 0)
         return DIFFATTN_ERR_INVALID;
     if (width_of(*d) > 256 || d->H % group_of(*d) != 0 || !nonneg(d->q1_stride) || !nonneg(d->k1_stride) ||
         !nonneg(d->q2_stride) || !nonneg(d->k2_stride) || !nonneg(d->v_stride) || !nonneg(d->o_stride) ||
@@ -85,7 +86,7 @@ int check_cross(const diffattn_cross_desc* d) {
 bool same3(const int64_t a[3], const int64_t b[3]) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
 
 void fill_cross(CrossParams* p, const diffattn_cross_desc& d, const void* q1, const void* k1, const void* q2, const void* k2,
-                const void* v, const int32_t* lengths, float lambda, const float* lambda_dev) {
+                const void* v, const int32_t* lengths, float lambda, const void* lambda_dev) {
     p->B = (int)d.B;
     p->H = (int)d.H;
     p->group = (int)group_of(d);
@@ -98,7 +99,8 @@ void fill_cross(CrossParams* p, const diffattn_cross_desc& d, const void* q1, co
     p->k_shared = k1 == k2 && same3(d.k1_stride, d.k2_stride);
     p->scale = (float)(1.0 / std::sqrt((double)d.D));
     p->lambda = lambda;
-    p->lambda_dev = lambda_dev;
+    p->lambda_dev = static_cast<const float*>(lambda_dev);
+    p->lambda_bf16 = d.lambda_dtype == DIFFATTN_BF16;
     p->lengths = lengths;
     p->q1 = q1;
     p->k1 = k1;
@@ -138,6 +140,12 @@ bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, con
            tma_rows(k2, nk, d.k2_stride) && tma_rows(v, nk, d.v_stride);
 }
 
+// What the tensor-core forward takes for sequences of Tk states, about, in us.
+double whole_us(int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t D) {
+    const double items = (double)B * H * ((Tq + 127) / 128), tiles = (double)((Tk + 63) / 64);
+    return 5 + std::ceil(items / 152) * tiles * (D == 64 ? 0.65 : 0.87);
+}
+
 // Whether the kernels of the paged cache take a serving call.  They divide the states of all
 // sequences evenly over the SMs and join the parts in a second launch, where the forward's
 // blocks each walk a whole sequence for 128 rows of a head.  By estimates, in us, for lengths
@@ -159,12 +167,9 @@ bool wants_split(const diffattn_cross_desc& d) {
         const double whole = 6 + std::ceil(items / (2 * SMS)) * 2 * tiles * 1.5;
         return 20 + units * 2 * tiles / (4 * SMS) * 3 < whole;
     }
-    const double items = (double)d.B * d.H * ((d.Tq + 127) / 128);
-    const double whole = 5 + std::ceil(items / SMS) * tiles * (d.D == 64 ? 0.65 : 0.87);
-    if (rows <= 16) {
-        const double bytes = (double)d.B * Hk * d.Tk * (4 * d.D + 256);
-        return 12.5 + bytes / 5.8e6 < whole;
-    }
+    const double bytes = (double)d.B * Hk * d.Tk * (4 * d.D + 256);
+    const double least = 5 + bytes / 5.5e6, whole = whole_us(d.B, d.H, d.Tq, d.Tk, d.D);
+    if (rows <= 16) return 12.5 + bytes / 5.2e6 < (whole > least ? whole : least);
     const int64_t head_rows = (d.Tq + 7) / 8 * 8;
     const double chunks = d.Tq <= 128 ? std::ceil(group_of(d) / std::floor(128.0 / head_rows))
                                       : (double)group_of(d) * ((d.Tq + 127) / 128);
@@ -210,6 +215,7 @@ int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.D));
     p.lambda = c.lambda;
     p.lambda_dev = c.lambda_dev;
+    p.lambda_bf16 = c.lambda_bf16;
     p.out = static_cast<__nv_bfloat16*>(c.out);
     p.o_sB = c.s_o[0];
     p.o_sH = c.s_o[1];
@@ -226,15 +232,17 @@ int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream
     p.lse = c.lse;
     p.lengths = c.lengths;
     const int grid = p.total_items < sms ? p.total_items : sms;
-    if (p.total_items > sms) {          // items are claimed from a counter: sequences differ in length
+    // Long calls claim their items from a counter, since sequences differ in length.  To zero it
+    // takes 7 us between the stream's kernels, so short ones deal them out.
+    if (p.total_items > sms && whole_us(c.B, c.H, c.Tq, c.Tk, c.D) > 60) {
         p.sched = static_cast<uint32_t*>(counter);
         if (cudaMemsetAsync(counter, 0, 64, stream) != cudaSuccess) return DIFFATTN_ERR_CUDA;
     }
     return launch_cross_tc(maps, p, c.D, grid, stream) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
-// The backward on the tensor cores; `counters`: two words of workspace, `parts`: what follows them.
-int backward_tc(const CrossParams& c, int sms, uint32_t* counters, float* parts, cudaStream_t stream) {
+// The backward on the tensor cores; `parts`: workspace for the splits' partial sums.
+int backward_tc(const CrossParams& c, int sms, float* parts, cudaStream_t stream) {
     CUtensorMap maps[12];
     if (cross_maps(maps, c, c.dout, c.s_do, 128, 64, 128) != DIFFATTN_OK ||
         cross_maps(maps + 6, c, c.dout, c.s_do, 64, 128, 64) != DIFFATTN_OK)
@@ -256,9 +264,10 @@ int backward_tc(const CrossParams& c, int sms, uint32_t* counters, float* parts,
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.D));
     p.lambda = c.lambda;
     p.lambda_dev = c.lambda_dev;
+    p.lambda_bf16 = c.lambda_bf16;
     p.lengths = c.lengths;
     p.status = c.status;
-    p.sched = counters;
+    p.sched = c.counters;
     p.out = static_cast<const __nv_bfloat16*>(c.out);
     p.out2 = static_cast<const __nv_bfloat16*>(c.out2);
     p.dout = static_cast<const __nv_bfloat16*>(c.dout);
@@ -293,7 +302,7 @@ size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
     // the rows' statistics, partial sums of dlambda and item counters; the tensor cores' partial
     // sums of dK and dV
-    size_t floats = cross_rows(*desc) * 4 + 128 + 4;
+    size_t floats = cross_rows(*desc) * 4 + kLambdaBlocks + 4;
     if (tc_shape(*desc)) {
         const int64_t Hk = desc->H / group_of(*desc);
         const int splits = cross_bwd_splits(desc->B, Hk, group_of(*desc), desc->Tq, desc->Tk);
@@ -303,7 +312,7 @@ size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc* desc) {
 }
 
 int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
-                       const void* v, const int32_t* kv_lengths, float lambda, const float* lambda_dev,
+                       const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev,
                        const diffattn_epilogue* epi, void* out, void* out2, float* lse, void* workspace,
                        size_t workspace_bytes, diffattn_stream_t stream) {
     int rc = check_cross(desc);
@@ -334,16 +343,16 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     if (rc != DIFFATTN_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!out2 && wants_split(d))
-        return cross_paged(d, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev, e, out, workspace, workspace_bytes, st);
+        return cross_paged(d, q1, k1, q2, k2, v, kv_lengths, lambda, p.lambda_dev, e, out, workspace, workspace_bytes, st);
     if (tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(out, rows, d.o_stride) && (!out2 || aligned16(out2)))
         return forward_tc(p, sms, workspace, st);
     return launch_cross_simt(p, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
 int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
-                       const void* v, const int32_t* kv_lengths, float lambda, const float* lambda_dev, const void* out,
+                       const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev, const void* out,
                        const void* out2, const float* lse, const void* dout, void* dq1, void* dk1, void* dq2, void* dk2,
-                       void* dv, float* dlambda, void* workspace, size_t workspace_bytes, diffattn_stream_t stream) {
+                       void* dv, void* dlambda, void* workspace, size_t workspace_bytes, diffattn_stream_t stream) {
     int rc = check_cross(desc);
     if (rc != DIFFATTN_OK) return rc;
     const diffattn_cross_desc& d = *desc;
@@ -366,6 +375,9 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
     p.dk2 = dk2;
     p.dv = dv;
     p.stats = static_cast<float*>(workspace);
+    p.dlambda = dlambda;
+    p.lambda_parts = p.stats + cross_rows(d) * 4;
+    p.counters = reinterpret_cast<uint32_t*>(p.lambda_parts + kLambdaBlocks);
     int sms = 0;
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
@@ -376,15 +388,14 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
                     aligned16(out2) && (d.D == 64 || p.k_shared) && d.B * d.H <= 65535 &&
                     aligned16(dq1) && aligned16(dk1) && aligned16(dq2) && aligned16(dk2) && aligned16(dv);
     if (tc) {
-        float* counters = p.stats + cross_rows(d) * 4 + 128;
-        rc = backward_tc(p, sms, reinterpret_cast<uint32_t*>(counters), counters + 4, st);
+        rc = backward_tc(p, sms, p.lambda_parts + kLambdaBlocks + 4, st);
         if (rc != DIFFATTN_OK) return rc;
     } else if (launch_cross_simt_bwd(p, st) != 0) {
         return DIFFATTN_ERR_CUDA;
     }
     if (!dlambda) return DIFFATTN_OK;
     // the tensor-core path's rows hold -Dd_2
-    return launch_bwd_dlambda(p.stats, cross_rows(d), tc ? 1.0f : -1.0f, dlambda, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+    return launch_cross_dlambda(p, tc ? 1.0f : -1.0f, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
 int diffattn_head_norm(const diffattn_norm_desc* desc, const void* x, const float* weight, const float* bias, void* y,

@@ -290,8 +290,8 @@ size_t paged_bytes(const diffattn_paged_desc& d, const diffattn_pages& g, bool c
 int paged_attention(const diffattn_paged_desc& d, const diffattn_pages& g, bool cross, const void* q1, const void* k1_cache,
                     const void* q2, const void* k2_cache, const void* v_cache, const int32_t* block_table,
                     const int32_t* lengths, const int32_t* q_lengths, const uint8_t* tree_mask, float lambda,
-                    const float* lambda_dev, const diffattn_epilogue& e, void* out, void* workspace, size_t workspace_bytes,
-                    cudaStream_t stream) {
+                    const float* lambda_dev, bool lambda_bf16, const diffattn_epilogue& e, void* out, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
     const int64_t rows[3] = {d.B, d.H, d.Tq};
     const int64_t es = d.dtype == DIFFATTN_BF16 ? 2 : 4;
     PagedParams p{};
@@ -343,6 +343,7 @@ int paged_attention(const diffattn_paged_desc& d, const diffattn_pages& g, bool 
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d.D));
     p.lambda = lambda;
     p.lambda_dev = lambda_dev;
+    p.lambda_bf16 = lambda_bf16;
     p.norm = e.norm;
     p.norm_eps = e.eps;
     p.norm_weight = e.weight;
@@ -428,8 +429,8 @@ int cross_paged(const diffattn_cross_desc& c, const void* q1, const void* k1, co
     diffattn_paged_desc d;
     diffattn_pages g;
     as_pages(c, &d, &g);
-    return paged_attention(d, g, true, q1, k1, q2, k2, v, nullptr, lengths, nullptr, nullptr, lambda, lambda_dev, e, out,
-                           workspace, workspace_bytes, stream);
+    return paged_attention(d, g, true, q1, k1, q2, k2, v, nullptr, lengths, nullptr, nullptr, lambda, lambda_dev,
+                           c.lambda_dtype == DIFFATTN_BF16, e, out, workspace, workspace_bytes, stream);
 }
 
 }  // namespace diffattn
@@ -612,7 +613,8 @@ int diffattn_paged_decode(const diffattn_paged_desc* desc, const diffattn_pages*
     const int64_t rows[3] = {d.B, d.H, d.Tq};
     if (!apart(rows, d.o_stride)) return DIFFATTN_ERR_INVALID;
     return paged_attention(d, *pages, false, q1, k1_cache, q2, k2_cache, v_cache, block_table, lengths, q_lengths, tree_mask,
-                           lambda, lambda_dev, e, out, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+                           lambda, lambda_dev, false, e, out, workspace, workspace_bytes,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

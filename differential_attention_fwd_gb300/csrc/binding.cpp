@@ -183,9 +183,9 @@ bool wants_grad(std::initializer_list<const Tensor*> ts) {
 // lambda: a number, or one value on the host or the device.
 struct Lambda {
     float host = 0.f;
-    Tensor dev;             // float32, where it is on the device
+    Tensor dev;             // float32 (or bf16 where the kernels take that), where it is on the device
     Tensor given;           // the tensor, if it is one
-    Lambda(PyObject* o, at::Device on, const char* what) {
+    Lambda(PyObject* o, at::Device on, const char* what, bool bf16 = false) {
         if (!THPVariable_Check(o)) {
             host = (float)number(o, "coefficient");
             return;
@@ -195,7 +195,7 @@ struct Lambda {
         no_tangent({&given}, what);
         if (given.is_cuda()) {
             if (given.device() != on) bad_value("coefficient tensor must be on the inputs' device");
-            dev = plain_f32(given);
+            dev = bf16 && given.scalar_type() == at::kBFloat16 ? given : plain_f32(given);
         } else {
             host = (float)given.item().toDouble();
         }
@@ -875,7 +875,8 @@ struct CrossBackward : public torch::autograd::Node {
     diffattn_cross_desc d{};
     float host = 0.f;
     bool shared = false, tensor_lambda = false;
-    torch::autograd::SavedVariable x[5], lam, lens, results[3];     // q1, k1, q2, k2, value; out, out2, lse
+    torch::autograd::SavedVariable x[5], lens, results[3];          // q1, k1, q2, k2, value; out, out2, lse
+    torch::autograd::SavedVariable lam, lam_read;                   // as given, and as the kernels read it
     std::vector<int64_t> lam_shape;
     std::optional<at::TensorOptions> lam_options;
     std::optional<at::Device> dev;
@@ -898,8 +899,8 @@ struct CrossBackward : public torch::autograd::Node {
         if (shared) t[3] = t[1];
         const Tensor out = results[0].unpack(shared_from_this()), out2 = results[1].unpack(), lse = results[2].unpack();
         const Tensor n = lens.unpack();
-        const Tensor l = tensor_lambda ? lam.unpack() : Tensor();
-        const Tensor l32 = l.defined() && l.is_cuda() ? plain_f32(l) : Tensor();
+        const Tensor l = lam_read.unpack();
+        if (tensor_lambda) lam.unpack();        // checks that it was not changed in place
         const at::ScalarType type = t[0].scalar_type();
         const Tensor g = inner(grads[0].scalar_type() == type ? grads[0] : grads[0].to(type));
         const c10::cuda::OptionalCUDAGuard guard(*dev);
@@ -913,18 +914,21 @@ struct CrossBackward : public torch::autograd::Node {
         if (task_should_compute_output(at[1]) || task_should_compute_output(at[3]) || task_should_compute_output(at[4]))
             for (int i : {1, 3, 4})
                 if (!(shared && i == 3)) dx[i] = fresh_tensor(t[i].sizes(), type, *dev);
-        if (tensor_lambda && task_should_compute_output(inputs)) dlam = fresh_tensor({}, at::kFloat, *dev);
+        if (tensor_lambda && task_should_compute_output(inputs)) dlam = fresh_tensor({}, d.lambda_dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev);
         const size_t bytes = diffattn_cross_bwd_workspace_bytes(&c);
         const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
         const int rc = diffattn_cross_bwd(&c, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
-                                          n.defined() ? n.const_data_ptr<int32_t>() : nullptr, host, fptr(l32), ptr(out),
+                                          n.defined() ? n.const_data_ptr<int32_t>() : nullptr, host, ptr(l), ptr(out),
                                           ptr(out2), fptr(lse), ptr(g), ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), ptr(dx[3]),
-                                          ptr(dx[4]), dlam.defined() ? dlam.data_ptr<float>() : nullptr, ws.data_ptr(), bytes,
+                                          ptr(dx[4]), ptr(dlam), ws.data_ptr(), bytes,
                                           stream_of(*dev));
         TORCH_CHECK(rc == DIFFATTN_OK, "diffattn_cross_bwd: ", diffattn_strerror(rc), " (", rc, ")");
         for (int i = 0; i < 5; ++i)
             if (!(shared && i == 3)) result[at[i]] = dx[i];
-        if (dlam.defined()) result[inputs] = dlam.to(*lam_options).view(lam_shape);
+        if (dlam.defined()) {
+            if (lam_options->device() != *dev || lam_options->dtype() != dlam.dtype()) dlam = dlam.to(*lam_options);
+            result[inputs] = lam_shape.empty() ? dlam : dlam.view(lam_shape);
+        }
         return result;
     }
     void release_variables() override {
@@ -932,6 +936,7 @@ struct CrossBackward : public torch::autograd::Node {
         for (auto& v : x) v.reset_data();
         for (auto& v : results) v.reset_data();
         lam.reset_data();
+        lam_read.reset_data();
         lens.reset_data();
         released = true;
     }
@@ -972,7 +977,8 @@ PyObject* cross(PyObject* const* a) {
         if (lens.size(0) != d.B) bad_value("kv_lengths must be [B] = (" + std::to_string(d.B) + ",), got " + text(lens.sizes()));
         if (!lens.is_contiguous()) lens = lens.contiguous();
     }
-    const Lambda lam(a[5], dev, kCross);
+    const Lambda lam(a[5], dev, kCross, true);
+    d.lambda_dtype = lam.dev.defined() && lam.dev.scalar_type() == at::kBFloat16 ? DIFFATTN_BF16 : DIFFATTN_F32;
     no_tangent({&given[0], &given[1], &given[2], &given[3], &given[4]}, kCross);
     const bool grad = wants_grad({&given[0], &given[1], &given[2], &given[3], &given[4], &lam.given});
     diffattn_epilogue e{};
@@ -1019,7 +1025,7 @@ PyObject* cross(PyObject* const* a) {
         const size_t bytes = diffattn_cross_workspace_bytes(&d);
         const Tensor ws = fresh_tensor({(int64_t)(bytes ? bytes : 16)}, at::kByte, dev);
         check(diffattn_cross_fwd(&d, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
-                                 lens.defined() ? lens.const_data_ptr<int32_t>() : nullptr, lam.host, fptr(lam.dev), &e, ptr(out),
+                                 lens.defined() ? lens.const_data_ptr<int32_t>() : nullptr, lam.host, ptr(lam.dev), &e, ptr(out),
                                  ptr(out2), lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.numel(),
                                  stream_of(dev)),
               "diffattn_cross_fwd");
@@ -1037,6 +1043,7 @@ PyObject* cross(PyObject* const* a) {
             from.push_back(lam.given);
             node->tensor_lambda = true;
             node->lam = torch::autograd::SavedVariable(lam.given, false);
+            if (lam.dev.defined()) node->lam_read = torch::autograd::SavedVariable(lam.dev, false);
             node->lam_shape = lam.given.sizes().vec();
             node->lam_options = lam.given.options();
         }

@@ -47,6 +47,7 @@ struct CrossParams {
     float scale;                // 1 / sqrt(D)
     float lambda;
     const float* lambda_dev;
+    int lambda_bf16;            // it points to a bf16, and so does dlambda
     const int32_t* lengths;     // [B], nullptr: Tk each
     uint32_t* status;
     const void* q1; const void* k1; const void* q2; const void* k2; const void* v;
@@ -63,7 +64,10 @@ struct CrossParams {
     const void* dout;
     int64_t s_do[3];
     void* dq1; void* dq2; void* dk1; void* dk2; void* dv;   // nullptr: not wanted
-    float* stats;               // [B, H, Tq, 4]: log-sum-exps, Dd_1, Dd_2; then 128 floats
+    float* stats;               // [B, H, Tq, 4]: log-sum-exps, Dd_1, Dd_2
+    void* dlambda;              // nullptr: not wanted
+    float* lambda_parts;        // [kLambdaBlocks]
+    uint32_t* counters;         // two of items, then one of dlambda's blocks
 };
 
 #ifdef __CUDACC__
@@ -89,9 +93,10 @@ struct CrossTcParams {
     float scale, scale_log2;
     float lambda;
     const float* lambda_dev;
+    int lambda_bf16;
     const int32_t* lengths;
     uint32_t* status;
-    uint32_t* sched;            // 2 item counters
+    uint32_t* sched;            // 2 item counters, and dlambda's
     const __nv_bfloat16* out; const __nv_bfloat16* out2; const __nv_bfloat16* dout;
     int64_t s_o[3], s_do[3];
     const float* lse;
@@ -104,6 +109,10 @@ struct CrossTcParams {
 int cross_bwd_splits(int64_t B, int64_t Hk, int64_t group, int64_t Tq, int64_t Tk);
 int launch_cross_bwd_tc(const CUtensorMap* maps /*dq: q1,k1,q2,k2,v,do; dkdv: the same*/, const CrossTcParams& p,
                         int head_dim, int num_sms, cudaStream_t stream);
+
+// dlambda = sign * (the sum of the rows' last statistic), after either backward.
+constexpr int kLambdaBlocks = 128;
+int launch_cross_dlambda(const CrossParams& p, float sign, cudaStream_t stream);
 
 // The CUDA-core kernels: any D <= 128, Dv <= 256, type and layout.
 int launch_cross_simt(const CrossParams& p, cudaStream_t stream);

@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(PREP_THREADS)
 cross_prep_kernel(const CrossTcParams p) {
     constexpr int GROUPS = PREP_THREADS / 16;
     const int g = threadIdx.x % 16, h = blockIdx.y % p.H, b = blockIdx.y / p.H;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) p.sched[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 3) p.sched[threadIdx.x] = 0;
     const int q0 = blockIdx.x * (GROUPS * PREP_ROWS) + threadIdx.x / 16;
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     uint4 raw[PREP_ROWS][3];
 #pragma unroll
     for (int i = 0; i < PREP_ROWS; ++i) {
@@ -454,7 +454,7 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
         const uint32_t quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
-        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
         const float coef = br ? -lam : 1.0f;
         const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2), coef2 = f2_pack(coef, coef);
         uint32_t sph = 0, dqph = 0, cnt = 0;        // cnt: tiles so far
@@ -883,7 +883,7 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
         const int row = quad * 32 + lane;    // state within the tile
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t c0 = 32 * half;
-        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
         const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2), nlam2 = f2_pack(-lam, -lam);
         uint32_t accph = 0, qc = 0;          // qc: query tiles consumed (whole launch)
         // the rows' exact Dd are the dQ kernel's

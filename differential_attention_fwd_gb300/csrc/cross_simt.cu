@@ -374,7 +374,7 @@ cross_fwd_kernel(const CrossParams p) {
             p.lse[(((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + row) * 2 + br] = len.bad ? nan : m + logf(l);
     }
     __syncthreads();
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     T* out2 = p.out2 ? static_cast<T*>(p.out2) + r.b * p.s_o[0] + r.h * p.s_o[1] + r.q0 * p.s_o[2] : nullptr;
 #pragma unroll
     for (int i = 0; i < Z::RV; ++i) {
@@ -439,11 +439,12 @@ cross_dq_kernel(const CrossParams p) {
     const Rows r = rows_of(p);
     const CrossLen len = cross_len(p.lengths, r.b, p.Tk);
     if (len.bad && threadIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.counters[2] = 0;
     Source<T>(p.q1, p.s_q1, r.b, r.h, p.D).load(qs, ld, r.q0, r.count);
     Source<T>(p.q2, p.s_q2, r.b, r.h, p.D).load(qs + BM * ld, ld, r.q0, r.count);
     const Source<T> grads(p.dout, p.s_do, r.b, r.h, p.Dv);
     grads.load(gs, lv, r.q0, r.count);
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     const int br = threadIdx.x >> 7, row = (threadIdx.x >> 2) & 31, sub = threadIdx.x & 3;
     const int64_t at = ((int64_t)r.b * p.H + r.h) * p.Tq + r.q0 + row;
     const float lse = row < r.count ? p.lse[at * 2 + br] : 0.f;
@@ -529,7 +530,7 @@ cross_dkdv_kernel(const CrossParams p) {
     pdl_launch_dependents();
     const CrossLen len = cross_len(p.lengths, b, p.Tk);
     const int live = max(0, min(count, len.n - k0));
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     const int half = threadIdx.x & 127, br = threadIdx.x >> 7;
     const int rd = half / Z::CD * Z::RD, cd = half % Z::CD * 4;
     const int rv = threadIdx.x / Z::CV * Z::RV, cv = threadIdx.x % Z::CV * 4;
@@ -612,6 +613,46 @@ cross_dkdv_kernel(const CrossParams p) {
             put4(static_cast<T*>(br ? p.dk2 : p.dk1) + (at + rd + i) * p.D, cd, p.D, dk[i][0], fill * p.scale);
 }
 
+// ---------------------------------------------------------------------------
+// dlambda: blocks sum their shares of the rows, the last of them the blocks' sums; the order
+// of either is fixed.  One launch (two were 10 us of the host's time).
+// ---------------------------------------------------------------------------
+constexpr int LAMBDA_THREADS = 256;
+__device__ __forceinline__ float block_sum(float s, float* part) {
+    s = group_sum<32>(s);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    float t = 0.f;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < LAMBDA_THREADS / 32; ++w) t += part[w];
+    return t;
+}
+__global__ void __launch_bounds__(LAMBDA_THREADS)
+cross_dlambda_kernel(const CrossParams p, float sign) {
+    __shared__ float part[LAMBDA_THREADS / 32];
+    __shared__ bool last;
+    pdl_wait();
+    const int64_t rows = (int64_t)p.B * p.H * p.Tq, per = (rows + gridDim.x - 1) / gridDim.x;
+    const int64_t r1 = min(rows, (blockIdx.x + 1) * per);
+    float s = 0.f;
+    for (int64_t r = blockIdx.x * per + threadIdx.x; r < r1; r += LAMBDA_THREADS) s += p.stats[r * 4 + 3];
+    const float mine = block_sum(s, part);
+    if (threadIdx.x == 0) {
+        p.lambda_parts[blockIdx.x] = mine;
+        __threadfence();
+        last = atomicAdd(p.counters + 2, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    s = threadIdx.x < gridDim.x ? *static_cast<volatile float*>(p.lambda_parts + threadIdx.x) : 0.f;
+    const float total = sign * block_sum(s, part);
+    if (threadIdx.x != 0) return;
+    if (p.lambda_bf16) *static_cast<__nv_bfloat16*>(p.dlambda) = __float2bfloat16_rn(total);
+    else *static_cast<float*>(p.dlambda) = total;
+}
+static_assert(kLambdaBlocks <= LAMBDA_THREADS, "a block's sum a thread");
+
 template <typename K>
 int launch_smem(K kernel, int64_t blocks, int floats, const CrossParams& p, cudaStream_t stream) {
     if (blocks > INT32_MAX ||
@@ -640,6 +681,12 @@ int launch_type(const CrossParams& p, bool backward, cudaStream_t stream) {
 }
 
 }  // namespace xsimt
+
+int launch_cross_dlambda(const CrossParams& p, float sign, cudaStream_t stream) {
+    const int64_t blocks = ((int64_t)p.B * p.H * p.Tq + 1023) / 1024;
+    return pdl_launch(xsimt::cross_dlambda_kernel, dim3((unsigned)(blocks < kLambdaBlocks ? blocks : kLambdaBlocks)),
+                      xsimt::LAMBDA_THREADS, 0, stream, p, sign);
+}
 
 int launch_cross_simt(const CrossParams& p, cudaStream_t stream) {
     return p.bf16 ? xsimt::launch_type<__nv_bfloat16>(p, false, stream) : xsimt::launch_type<float>(p, false, stream);

@@ -75,6 +75,7 @@
 #include "block.h"
 #include "item_ring.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 
 namespace diffattn {
 namespace tc {
@@ -420,6 +421,10 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
+    if constexpr (CROSS) {              // launched while the stream's last kernel ends
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 
     const int grid = gridDim.x;
     const int cta = blockIdx.x;
@@ -678,7 +683,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t tO = lane_base + TM_O + br * 128;
         const float sl2 = p.scale_log2;
-        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float lam = CROSS ? lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda) : p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
         uint32_t sph = 0;          // bit buf: phase of S_FULL[br][buf]
         uint32_t ofph = 0, lph = 0, naph = 0, nbph = 0;
         float* stat = reinterpret_cast<float*>(smem + C::OFF_BAR + REL_STAT);
@@ -1016,6 +1021,9 @@ int launch_hd(const CUtensorMap* maps, const TcParams& p, int grid, cudaStream_t
     cudaError_t e = cudaFuncSetAttribute(tc::diffattn_fwd_tc_kernel<HD, CROSS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return -1;
+    if (CROSS)
+        return pdl_launch(tc::diffattn_fwd_tc_kernel<HD, CROSS>, dim3(grid), tc::NUM_THREADS, smem, stream, maps[0], maps[1],
+                          maps[2], maps[3], maps[4], maps[5], p);
     tc::diffattn_fwd_tc_kernel<HD, CROSS><<<grid, tc::NUM_THREADS, smem, stream>>>(
         maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;

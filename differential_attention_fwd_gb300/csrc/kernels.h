@@ -15,6 +15,14 @@ namespace diffattn {
 // DIFFATTN_NORM_* in the public header).
 enum : int { kNormNone = 0, kNormRms = 1, kNormGroup = 2 };
 
+#ifdef __CUDACC__
+// lambda from the device, a float or a bf16, or the host's.
+__device__ __forceinline__ float lambda_of(const float* dev, int bf16, float host) {
+    if (!dev) return host;
+    return bf16 ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dev)) : __ldg(dev);
+}
+#endif
+
 // Parameters of the tensor-core kernel (bf16; D = 64 or 128, value width 128).
 // Queries and keys may be sequences of different lengths: query row i sits at
 // position i + kv_off of the key sequence (kv_off = Tk - Tq for queries at the
@@ -57,6 +65,7 @@ struct TcParams {
     __nv_bfloat16* out2;
     float* lse;
     const int32_t* lengths;     // the cross instances: [B], nullptr: Tk each
+    int lambda_bf16;            // lambda_dev points to a bf16 (the cross instances)
 };
 
 // Parameters of the CUDA-core kernel (any D <= 128, value width Dv <= 256,

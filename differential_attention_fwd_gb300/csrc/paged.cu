@@ -107,7 +107,7 @@ paged_simt_kernel(const PagedParams p) {
     pdl_wait();                     // before the merging pass may start, which writes too
     pdl_launch_dependents();
     paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
     const int CG = Dv <= 32 ? 32 : Dv <= 64 ? 64 : 128;
@@ -417,7 +417,7 @@ paged_combine_kernel(const PagedParams p) {
     if (p.zero_rest)
         zero_rest(p, (blockIdx.y * gridDim.x + blockIdx.x) * C_WARPS + warp, gridDim.x * gridDim.y * C_WARPS, lane);
     pdl_wait();
-    const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
     // the words of this block's workers, all at once: most of them say that there is nothing
     int4 joins[kJoinsPerBlock];

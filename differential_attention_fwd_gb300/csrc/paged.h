@@ -120,6 +120,7 @@ struct PagedParams {
     int64_t mask_stride[2];
     float scale_log2, lambda;
     const float* lambda_dev;
+    int lambda_bf16;            // it points to a bf16
     int norm;
     float norm_eps;
     const float* norm_weight;

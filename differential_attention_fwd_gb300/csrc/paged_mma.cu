@@ -550,7 +550,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                                     a[br][j] = fmaf(wt[br][k], bufs[k * (C::RING / 4) + (r * 2 + br) * DV + lane + 32 * j], a[br][j]);
                     }
                     if (cur.whole()) {
-                        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+                        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
                         paged_finish_row<DV / 32>(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
                     } else {
                         float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row0 + r) * paged_part_floats(DV);
@@ -586,7 +586,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             continue;
         }
         const PagedRow x = ra;
-        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
         const float i1 = l[0][0] == 0.f ? 0.f : 1.f / l[0][0], i2 = l[1][0] == 0.f ? 0.f : 1.f / l[1][0];
         float sum = 0.f;
 #pragma unroll

@@ -489,7 +489,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t tO = lane_base + TM_O + br * 128;     // this branch's O
         const float sl2 = p.scale_log2;
-        const float lam = p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
+        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
         uint32_t sph = 0, ofph = 0, wph = 0;
         uint32_t pv_count = 0;
         bool ok = true;

@@ -700,13 +700,16 @@ int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages 
  *
  * Q1, Q2: [B, H, Tq, D]; K1, K2: [B, H / kv_group, Tk, D]; V: [B, H / kv_group, Tk, Dv];
  * O: [B, H, Tq, Dv].  D <= 128, Dv <= 256 (0: 2D), dtype, kv_group as in diffattn_desc;
+ * lambda_dtype: of the value that lambda_dev points to, and of dlambda.
  * *_stride: element strides of B, heads and rows (innermost 1; >= 0); o_stride of O (and
- * of out2), dout_stride of its gradient (the backward only).
+ * of out2), dout_stride of its gradient (the backward only).  reserved: 0.
  */
 typedef struct {
     int64_t B, H, Tq, Tk, D, Dv;
     int32_t dtype;
     int32_t kv_group;
+    int32_t lambda_dtype;
+    int32_t reserved;
     int64_t q1_stride[3], k1_stride[3], q2_stride[3], k2_stride[3], v_stride[3];
     int64_t o_stride[3], dout_stride[3];
 } diffattn_cross_desc;
@@ -720,7 +723,7 @@ size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc *desc);
  * diffattn_cross_fwd -- the forward.  kv_lengths: device int32 [B], or NULL (Tk each).  A
  * length outside 0 .. Tk gives that sequence rows of NaN and is recorded
  * (DIFFATTN_ERR_INDEX from diffattn_get_device_error); nothing outside the tensors is read.
- * lambda, lambda_dev, epi as diffattn_decode.
+ * lambda: used where lambda_dev, a value on the device, is NULL.  epi as diffattn_decode.
  * For a training step: out2 (A_2 V, dtype and strides of O; 0 without a state) and lse
  * (float32 [B, H, Tq, 2], each branch's natural-log log-sum-exp of the scaled scores, -inf
  * without a state), both or neither, and then no epilogue.
@@ -734,7 +737,7 @@ size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc *desc);
  */
 int diffattn_cross_fwd(const diffattn_cross_desc *desc, const void *q1, const void *k1,
                        const void *q2, const void *k2, const void *v,
-                       const int32_t *kv_lengths, float lambda, const float *lambda_dev,
+                       const int32_t *kv_lengths, float lambda, const void *lambda_dev,
                        const diffattn_epilogue *epi, void *out, void *out2, float *lse,
                        void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
 
@@ -742,7 +745,7 @@ int diffattn_cross_fwd(const diffattn_cross_desc *desc, const void *q1, const vo
  * diffattn_cross_bwd -- gradients, given dout = dL/dO and the training forward's results
  * (out, out2, lse) for the same inputs.  dq1, dq2 [B, H, Tq, D], dk1, dk2 [B, Hk, Tk, D], dv
  * [B, Hk, Tk, Dv]: dense, of the inputs' dtype, overwritten; rows of states that a sequence
- * does not have are zeros.  dlambda: one float.  dq1, dq2 and dlambda are NULL where not
+ * does not have are zeros.  dlambda: one value.  dq1, dq2 and dlambda are NULL where not
  * wanted, and dk1, dk2 and dv all are or none is -- but dk2 alone may be NULL where K2 is
  * K1 (the same pointer and strides): then dk1 takes both branches' gradient, summed before
  * the rounding.  No atomics: the result is reproducible bit for bit.  A length outside 0 ..
@@ -752,9 +755,9 @@ int diffattn_cross_fwd(const diffattn_cross_desc *desc, const void *q1, const vo
  */
 int diffattn_cross_bwd(const diffattn_cross_desc *desc, const void *q1, const void *k1,
                        const void *q2, const void *k2, const void *v,
-                       const int32_t *kv_lengths, float lambda, const float *lambda_dev,
+                       const int32_t *kv_lengths, float lambda, const void *lambda_dev,
                        const void *out, const void *out2, const float *lse, const void *dout,
-                       void *dq1, void *dk1, void *dq2, void *dk2, void *dv, float *dlambda,
+                       void *dq1, void *dk1, void *dq2, void *dk2, void *dv, void *dlambda,
                        void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
 
 /*

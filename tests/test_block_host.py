@@ -128,10 +128,10 @@ def cross_bwd(lib, d=None, lam=0.5, ws=p(40), n=1 << 30, **other):
 
 def test_cross_descriptor_layout():
     C = _lib.DiffattnCrossDesc
-    assert ctypes.sizeof(C) == 6 * 8 + 2 * 4 + 7 * 3 * 8 and C.q1_stride.offset == 56
+    assert ctypes.sizeof(C) == 6 * 8 + 4 * 4 + 7 * 3 * 8 and C.q1_stride.offset == 64
 
 
-BAD_CROSS = [dict(B=0), dict(H=0), dict(Tq=0), dict(Tk=0), dict(D=0), dict(D=129), dict(Dv=-1), dict(Dv=257), dict(dtype=2),
+BAD_CROSS = [dict(lambda_dtype=2), dict(reserved=1), dict(B=0), dict(H=0), dict(Tq=0), dict(Tk=0), dict(D=0), dict(D=129), dict(Dv=-1), dict(Dv=257), dict(dtype=2),
              dict(kv_group=-1), dict(kv_group=3), dict(q1_stride=(-1, 0, 0)), dict(k2_stride=(0, -1, 0)), dict(v_stride=(0, 0, -1)),
              dict(dout_stride=(-1, 0, 0))]
 
