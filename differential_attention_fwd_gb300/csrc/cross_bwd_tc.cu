@@ -548,23 +548,27 @@ diffattn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid
                 // place in the score registers: the exponents, the exponentials, the row's sum, dS_b =
                 // coef A_b (dP - Dd_b).  (A branch between the phases, for the mask or the exact Dd,
                 // took a fifth of the kernel's time.)
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const uint64_t x = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), sl2x2, nlse2);
-                    s[2 * c] = static_cast<uint32_t>(x);
-                    s[2 * c + 1] = static_cast<uint32_t>(x >> 32);
-                }
-#pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_approx(__uint_as_float(s[c])));
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    sum2[c % CHAINS] = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), f2_from_bits(dp[2 * c], dp[2 * c + 1]), sum2[c % CHAINS]);
                 uint32_t pk[32];
+                constexpr int CH = 4;          // column pairs of a step
+                auto exps = [&](int c0) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const uint64_t y = f2_fma(f2_from_bits(dp[2 * c], dp[2 * c + 1]), coef2, cndd2);
-                    const uint64_t z = f2_mul(f2_from_bits(s[2 * c], s[2 * c + 1]), y);
-                    pk[c] = pack_bf16x2(f2_lo(z), f2_hi(z));
+                    for (int c = c0; c < c0 + CH; ++c) {
+                        const uint64_t x = f2_fma(f2_from_bits(s[2 * c], s[2 * c + 1]), sl2x2, nlse2);
+                        s[2 * c] = __float_as_uint(ex2_approx(f2_lo(x)));
+                        s[2 * c + 1] = __float_as_uint(ex2_approx(f2_hi(x)));
+                    }
+                };
+                exps(0);
+#pragma unroll
+                for (int c0 = 0; c0 < 32; c0 += CH) {
+                    if (c0 + CH < 32) exps(c0 + CH);
+#pragma unroll
+                    for (int c = c0; c < c0 + CH; ++c) {
+                        const uint64_t a = f2_from_bits(s[2 * c], s[2 * c + 1]), d = f2_from_bits(dp[2 * c], dp[2 * c + 1]);
+                        sum2[c % CHAINS] = f2_fma(a, d, sum2[c % CHAINS]);
+                        const uint64_t z = f2_mul(a, f2_fma(d, coef2, cndd2));
+                        pk[c] = pack_bf16x2(f2_lo(z), f2_hi(z));
+                    }
                 }
                 if (!TWO && cnt > 0 && !(ok = mbar_wait_warp(&bars[DS_FREE], (cnt - 1) & 1u, ab))) break;
                 tmem_st32(TWO ? tS : lane_base + C::TM_DS + br * 32, pk);
@@ -948,45 +952,46 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                         s2[c] = c < qlim ? s2[c] : 0xff800000u;
                     }
                 }
-                // in three phases, in place: the exponents, the exponentials, then dS_1, dS_2 and W
+                auto exps = [&](int c0) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 l1 = pl[c / 4], l2 = pl[8 + c / 4];
+                    for (int c = c0; c < c0 + 4; c += 4) {
+                        const float4 l1 = pl[c / 4], l2 = pl[8 + c / 4];
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int cc = c + 2 * hh;
-                        const uint64_t L1 = hh ? f2_pack(l1.z, l1.w) : f2_pack(l1.x, l1.y);
-                        const uint64_t L2 = hh ? f2_pack(l2.z, l2.w) : f2_pack(l2.x, l2.y);
-                        const uint64_t x1 = f2_fma(f2_from_bits(s1[cc], s1[cc + 1]), sl2x2, L1);
-                        const uint64_t x2 = f2_fma(f2_from_bits(s2[cc], s2[cc + 1]), sl2x2, L2);
-                        s1[cc] = static_cast<uint32_t>(x1);
-                        s1[cc + 1] = static_cast<uint32_t>(x1 >> 32);
-                        s2[cc] = static_cast<uint32_t>(x2);
-                        s2[cc + 1] = static_cast<uint32_t>(x2 >> 32);
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int cc = c + 2 * hh;
+                            const uint64_t L1 = hh ? f2_pack(l1.z, l1.w) : f2_pack(l1.x, l1.y);
+                            const uint64_t L2 = hh ? f2_pack(l2.z, l2.w) : f2_pack(l2.x, l2.y);
+                            const uint64_t x1 = f2_fma(f2_from_bits(s1[cc], s1[cc + 1]), sl2x2, L1);
+                            const uint64_t x2 = f2_fma(f2_from_bits(s2[cc], s2[cc + 1]), sl2x2, L2);
+                            s1[cc] = __float_as_uint(ex2_approx(f2_lo(x1)));
+                            s1[cc + 1] = __float_as_uint(ex2_approx(f2_hi(x1)));
+                            s2[cc] = __float_as_uint(ex2_approx(f2_lo(x2)));
+                            s2[cc + 1] = __float_as_uint(ex2_approx(f2_hi(x2)));
+                        }
                     }
-                }
+                };
+                exps(0);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    s1[c] = __float_as_uint(ex2_approx(__uint_as_float(s1[c])));
-                    s2[c] = __float_as_uint(ex2_approx(__uint_as_float(s2[c])));
-                }
+                for (int b0 = 0; b0 < 32; b0 += 4) {
+                    if (b0 + 4 < 32) exps(b0 + 4);
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 e1 = pl[16 + c / 4], e2 = pl[24 + c / 4];
+                    for (int c = b0; c < b0 + 4; c += 4) {
+                        const float4 e1 = pl[16 + c / 4], e2 = pl[24 + c / 4];
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int cc = c + 2 * hh;
-                        const uint64_t E1 = hh ? f2_pack(e1.z, e1.w) : f2_pack(e1.x, e1.y);
-                        const uint64_t E2 = hh ? f2_pack(e2.z, e2.w) : f2_pack(e2.x, e2.y);
-                        const uint64_t a1 = f2_from_bits(s1[cc], s1[cc + 1]);
-                        const uint64_t a2n = f2_mul(f2_from_bits(s2[cc], s2[cc + 1]), nlam2);
-                        const uint64_t dp2 = f2_from_bits(dp[cc], dp[cc + 1]);
-                        const uint64_t d1 = f2_mul(a1, f2_add(dp2, E1));
-                        const uint64_t d2 = f2_mul(a2n, f2_add(dp2, E2));
-                        const uint64_t w = f2_add(a1, a2n);
-                        w1[cc / 2] = pack_bf16x2(f2_lo(d1), f2_hi(d1));
-                        w2[cc / 2] = pack_bf16x2(f2_lo(d2), f2_hi(d2));
-                        w3[cc / 2] = pack_bf16x2(f2_lo(w), f2_hi(w));
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int cc = c + 2 * hh;
+                            const uint64_t E1 = hh ? f2_pack(e1.z, e1.w) : f2_pack(e1.x, e1.y);
+                            const uint64_t E2 = hh ? f2_pack(e2.z, e2.w) : f2_pack(e2.x, e2.y);
+                            const uint64_t a1 = f2_from_bits(s1[cc], s1[cc + 1]);
+                            const uint64_t a2n = f2_mul(f2_from_bits(s2[cc], s2[cc + 1]), nlam2);
+                            const uint64_t dp2 = f2_from_bits(dp[cc], dp[cc + 1]);
+                            const uint64_t d1 = f2_mul(a1, f2_add(dp2, E1));
+                            const uint64_t d2 = f2_mul(a2n, f2_add(dp2, E2));
+                            const uint64_t w = f2_add(a1, a2n);
+                            w1[cc / 2] = pack_bf16x2(f2_lo(d1), f2_hi(d1));
+                            w2[cc / 2] = pack_bf16x2(f2_lo(d2), f2_hi(d2));
+                            w3[cc / 2] = pack_bf16x2(f2_lo(w), f2_hi(w));
+                        }
                     }
                 }
                 // the previous tile's dV/dK products must have read the operands

@@ -14,8 +14,8 @@
 // arithmetic, one rounding of y and dx at the end.
 //
 // The passes are bound by HBM: x in, y out; x and dy in, dx out.  A group of lanes holds a
-// row, 16 bytes a lane (twice where a row has more than 32 such), so the row stays in
-// registers and the only exchanges are its sums.  A block works on one head, whose weights
+// row, twice 16 bytes a lane (the exchanges of the row's sums are a third of the backward's
+// instructions with 16), so the row stays in registers and the only exchanges are its sums.  A block works on one head, whose weights
 // stay in registers, and takes ROWS rows a group at a time: their loads go out together.
 // In the backward every block walks a chunk of the tokens, each lane adding up dw and db
 // of its own channels, and leaves one partial row of each: the sums' order is fixed,
@@ -30,12 +30,15 @@ namespace hnorm {
 
 constexpr int THREADS = 256;
 constexpr int MAX_C = 256;
-constexpr int ROWS = 4;             // of a group, loaded together
-constexpr int BWD_BLOCKS = 1216;    // of the backward, about: 8 for each of 152 SMs
+constexpr int ROWS = 2;             // of a group, loaded together
+constexpr int BWD_ROWS = 2;
+constexpr int BWD_AN_SM = 2;
+constexpr int CH = 2;               // pieces of 16 bytes a lane
+constexpr int BWD_BLOCKS = 304;     // of the backward, about: the two that each of 152 SMs holds
 
 // The lanes' part of a row: CH pieces of 16 bytes, V elements each, piece j of lane g at
 // element (g + j G) V.
-template <typename T, int G, int CH>
+template <typename T, int G>
 struct Part {
     static constexpr int V = Vec<T>::N;
     static constexpr int P = CH * V / 2;    // pairs
@@ -94,10 +97,10 @@ __device__ __forceinline__ float dot(const uint64_t (&a)[P], const uint64_t (&b)
     return f2_lo(s) + f2_hi(s);
 }
 
-template <typename T, int G, int CH>
+template <typename T, int G>
 __global__ void __launch_bounds__(THREADS)
 head_norm_kernel(const HeadNormParams p) {
-    using L = Part<T, G, CH>;
+    using L = Part<T, G>;
     constexpr int GROUPS = THREADS / G;
     const L part(threadIdx.x % G, p.C);
     const int h = blockIdx.y;
@@ -131,10 +134,10 @@ head_norm_kernel(const HeadNormParams p) {
     }
 }
 
-template <typename T, int G, int CH>
-__global__ void __launch_bounds__(THREADS)
+template <typename T, int G>
+__global__ void __launch_bounds__(THREADS, BWD_AN_SM)
 head_norm_bwd_kernel(const HeadNormParams p) {
-    using L = Part<T, G, CH>;
+    using L = Part<T, G>;
     constexpr int GROUPS = THREADS / G;
     constexpr int V = L::V;
     __shared__ float red[2][THREADS / 32][32 * CH * V];     // [dw, db][warp][lane's channels]
@@ -151,11 +154,11 @@ head_norm_bwd_kernel(const HeadNormParams p) {
         dw[e] = db[e] = 0;
     }
     const int end = min(p.tokens, (blockIdx.x + 1) * p.per_chunk);
-    for (int tok0 = blockIdx.x * p.per_chunk + threadIdx.x / G; tok0 - (int)(threadIdx.x / G) < end; tok0 += GROUPS * ROWS) {
-        uint4 rx[ROWS][CH], rg[ROWS][CH];
-        int64_t to[ROWS];
+    for (int tok0 = blockIdx.x * p.per_chunk + threadIdx.x / G; tok0 - (int)(threadIdx.x / G) < end; tok0 += GROUPS * BWD_ROWS) {
+        uint4 rx[BWD_ROWS][CH], rg[BWD_ROWS][CH];
+        int64_t to[BWD_ROWS];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < BWD_ROWS; ++i) {
             const int tok = tok0 + i * GROUPS;
             const bool in = tok < end;
             const int b = in ? p.by_T.div(tok) : 0, t = in ? tok - b * p.T : 0;
@@ -164,7 +167,7 @@ head_norm_bwd_kernel(const HeadNormParams p) {
             to[i] = in ? b * p.sdx[0] + h * p.sdx[1] + t * p.sdx[2] : -1;
         }
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < BWD_ROWS; ++i) {
             uint64_t x[L::P], dy[L::P], g[L::P];
             L::unpack(rx[i], x);
             L::unpack(rg[i], dy);
@@ -338,19 +341,19 @@ head_norm_dw_kernel(const HeadNormParams p) {
     if (out) out[(int64_t)h * p.C + (c < p.C ? c : c - p.C)] = total * p.scale;
 }
 
-template <typename T, int G, int CH>
+template <typename T, int G>
 int launch_one(const HeadNormParams& p, bool backward, cudaStream_t stream) {
     constexpr int PER = THREADS / G * ROWS;
     if (backward)
-        return pdl_launch(head_norm_bwd_kernel<T, G, CH>, dim3((unsigned)p.chunks, (unsigned)p.H), THREADS, 0, stream, p);
-    return pdl_launch(head_norm_kernel<T, G, CH>, dim3((unsigned)((p.tokens + PER - 1) / PER), (unsigned)p.H), THREADS, 0,
+        return pdl_launch(head_norm_bwd_kernel<T, G>, dim3((unsigned)p.chunks, (unsigned)p.H), THREADS, 0, stream, p);
+    return pdl_launch(head_norm_kernel<T, G>, dim3((unsigned)((p.tokens + PER - 1) / PER), (unsigned)p.H), THREADS, 0,
                       stream, p);
 }
 
-// Lanes of a row: the fewest, a power of two, that hold it in a piece each (32 in two).
+// Lanes of a row: the fewest, a power of two, that hold it in two pieces each.
 int lanes_of(const HeadNormParams& p) {
     const int pieces = p.C / (p.bf16 ? 8 : 4);
-    return pieces <= 4 ? 4 : pieces <= 8 ? 8 : pieces <= 16 ? 16 : 32;
+    return pieces <= 8 ? 4 : pieces <= 16 ? 8 : pieces <= 32 ? 16 : 32;
 }
 
 template <typename T>
@@ -361,13 +364,11 @@ int launch_type(const HeadNormParams& p, bool backward, cudaStream_t stream) {
         return pdl_launch(kernel, dim3(blocks, (unsigned)p.H), THREADS, 0, stream, p);
     }
     switch (lanes_of(p)) {
-        case 4: return launch_one<T, 4, 1>(p, backward, stream);
-        case 8: return launch_one<T, 8, 1>(p, backward, stream);
-        case 16: return launch_one<T, 16, 1>(p, backward, stream);
+        case 4: return launch_one<T, 4>(p, backward, stream);
+        case 8: return launch_one<T, 8>(p, backward, stream);
+        case 16: return launch_one<T, 16>(p, backward, stream);
     }
-    if constexpr (sizeof(T) == 4)
-        if (p.C > 128) return launch_one<T, 32, 2>(p, backward, stream);
-    return launch_one<T, 32, 1>(p, backward, stream);
+    return launch_one<T, 32>(p, backward, stream);
 }
 
 int launch(const HeadNormParams& p, bool backward, cudaStream_t stream) {
@@ -378,7 +379,7 @@ int launch(const HeadNormParams& p, bool backward, cudaStream_t stream) {
 
 // Blocks along the tokens: about BWD_BLOCKS over all heads, each with whole steps.
 void plan_head_norm_bwd(HeadNormParams* p) {
-    const int step = p->fast ? hnorm::THREADS / hnorm::lanes_of(*p) * hnorm::ROWS : hnorm::THREADS / 32;
+    const int step = p->fast ? hnorm::THREADS / hnorm::lanes_of(*p) * hnorm::BWD_ROWS : hnorm::THREADS / 32;
     const int64_t steps = ((int64_t)p->tokens + step - 1) / step, most = (hnorm::BWD_BLOCKS + p->H - 1) / p->H;
     const int64_t each = (steps + most - 1) / most;
     p->per_chunk = (int)(each * step);
