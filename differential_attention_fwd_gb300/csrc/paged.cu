@@ -88,7 +88,7 @@ __host__ __device__ inline Layout simt_layout(int D, int Dv, int es, int rc, boo
 // TWO: value widths above 128 (a thread has two columns).  Without, four blocks an SM, whose
 // latencies hide one another: 9 rows a key/value head (4 sequences of up to 8348 keys, 16
 // heads, D = 32, float32) take 272 us with two, which 255 registers leave, 151 with four.
-template <typename T, int RC, bool TWO>
+template <typename T, int RC, bool TWO, bool X>
 __global__ void __launch_bounds__(THREADS, TWO ? 1 : kSimtBlocksPerSm)
 paged_simt_kernel(const PagedParams p) {
     constexpr int V = 16 / sizeof(T), PS = weights_row(RC);
@@ -106,16 +106,16 @@ paged_simt_kernel(const PagedParams p) {
     float* st_a = st_l + 2 * RC;
     pdl_wait();                     // before the merging pass may start, which writes too
     pdl_launch_dependents();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);
-    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+    paged_locate<1, X>(p, paged_scan<THREADS, X>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);
+    const float lam = paged_lambda<X>(p);
 
     // output columns of this thread: c0, and c0 + 128 for Dv > 128; its keys: kg, kg + KG, ...
     const int CG = Dv <= 32 ? 32 : Dv <= 64 ? 64 : 128;
     const int KG = THREADS / CG;
     const int c0 = tid % CG, kg = tid / CG;
 
-    PagedCursor cur;
-    if (tid == 0) PagedCursor::no_join(p, blockIdx.x);
+    PagedCursor<X> cur;
+    if (tid == 0) PagedCursor<X>::no_join(p, blockIdx.x);
     for (cur.begin(p, blk, 0, blockIdx.x, KT, EXTRA); !cur.done(); cur.next(p, KT, EXTRA)) {
         const int live = cur.live_tiles(p, KT);
         const int n_new = cur.s.n_new;
@@ -125,7 +125,7 @@ paged_simt_kernel(const PagedParams p) {
         // ahead; the first two beside the queries.
         auto look = [&](int tile) -> int {
             const int key = (cur.tile0 + tile) * KT + (tid >> 2);
-            return tile < live && key < cur.s.total ? paged_page(p, cur.b, key / p.page) : -2;
+            return tile < live && key < cur.s.total ? paged_page<X>(p, cur.b, key / p.page) : -2;
         };
         int page = look(0), next = look(1);
         // the rows' queries and state
@@ -393,7 +393,7 @@ __device__ __forceinline__ void zero_rest(const PagedParams& p, int warp, int wa
     for (int64_t i = warp; i < rows; i += warps) {
         const int64_t bh = i / p.Tq;
         const int q = (int)(i - bh * p.Tq), b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
-        if (q < paged_seq(p, b).n_new) continue;
+        if (q < paged_seq<false>(p, b).n_new) continue;
         const int64_t at = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2];
         for (int c = lane; c < p.Dv; c += 32) {
             if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at + c] = __float2bfloat16_rn(0.f);
@@ -407,17 +407,17 @@ __device__ __forceinline__ void zero_rest(const PagedParams& p, int warp, int wa
 // units of up to 16 rows, which may have many parts and leave the SMs empty (one sequence
 // of 517 keys: 14.1 us in all with two, 13.2 with four); two for those of 128, whose rows
 // want the warps that fewer registers allow (61 tokens over 16 x 8192: 117.5, 118.2 with four).
-template <int J, bool VEC, int AHEAD>
+template <int J, bool VEC, int AHEAD, bool X>
 __global__ void __launch_bounds__(C_WARPS * 32, J > 4 ? 2 : AHEAD > 2 ? 3 : 4)
 paged_combine_kernel(const PagedParams p) {
     __shared__ float share[C_WARPS][2 * 32 * J];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     // before the first pass is over: it does not touch these rows
-    if (p.zero_rest)
+    if (!X && p.zero_rest)
         zero_rest(p, (blockIdx.y * gridDim.x + blockIdx.x) * C_WARPS + warp, gridDim.x * gridDim.y * C_WARPS, lane);
     pdl_wait();
-    const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+    const float lam = paged_lambda<X>(p);
     const int stride = paged_part_floats(p.Dv), width = paged_part_width(p.Dv);
     // the words of this block's workers, all at once: most of them say that there is nothing
     int4 joins[kJoinsPerBlock];
@@ -546,10 +546,19 @@ paged_combine_kernel(const PagedParams p) {
     }
 }
 
+template <bool X>
+auto combine_kernel(const PagedParams& p, int most) {
+    return p.Dv == 128 && p.bf16 ? (most > 16 ? paged_combine_kernel<4, true, 2, X> : paged_combine_kernel<4, true, 4, X>)
+           : p.Dv <= 128         ? paged_combine_kernel<4, false, 4, X>
+                                 : paged_combine_kernel<8, false, 2, X>;
+}
+
 template <typename T, int RC>
 int launch_rc(const PagedParams& p, cudaStream_t stream) {
     const Layout L = simt_layout(p.D, p.Dv, sizeof(T), RC, p.k_shared != 0);
-    const auto kernel = p.Dv > 128 ? paged_simt_kernel<T, RC, true> : paged_simt_kernel<T, RC, false>;
+    const auto kernel = p.cross ? (p.Dv > 128 ? paged_simt_kernel<T, RC, true, true> : paged_simt_kernel<T, RC, false, true>)
+                        : p.Dv > 128 ? paged_simt_kernel<T, RC, true, false>
+                                     : paged_simt_kernel<T, RC, false, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) != cudaSuccess) return -1;
     return pdl_launch(kernel, dim3(p.workers), THREADS, L.total, stream, p);
 }
@@ -602,10 +611,7 @@ int launch_paged_combine(const PagedParams& params, cudaStream_t stream) {
     const int joins = (int)(units < p.workers ? units : p.workers), fit = p.solo_workers / 2;
     const int most = p.chunk_rows, least = most <= 16 ? most : (most + paged::C_WARPS - 1) / paged::C_WARPS;
     const int rows = fit / joins < least ? least : fit / joins > most ? most : fit / joins;
-    const auto kernel = p.Dv == 128 && p.bf16 ? (most > 16 ? paged::paged_combine_kernel<4, true, 2>
-                                                           : paged::paged_combine_kernel<4, true, 4>)
-                        : p.Dv <= 128         ? paged::paged_combine_kernel<4, false, 4>
-                                              : paged::paged_combine_kernel<8, false, 2>;
+    const auto kernel = p.cross ? paged::combine_kernel<true>(p, most) : paged::combine_kernel<false>(p, most);
     return pdl_launch(kernel, dim3((unsigned)blocks, (unsigned)rows), paged::C_WARPS * 32, 0, stream, p);
 }
 

@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t slice_mask(const PagedParams& p, const Paged
 }
 
 // HR: 1 for units of up to 8 rows, whose threads have no second row, else 2.
-template <int HD, bool KS, int HR>
+template <int HD, bool KS, int HR, bool X>
 __global__ void __launch_bounds__(THREADS, 2)
 paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -150,15 +150,15 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     pdl_launch_dependents();
     // One warp a worker where that makes at most two workers a unit, and if the unit's rows
     // allow it.  (The barriers in here order the above.)
-    const PagedScan found = paged_scan<THREADS>(p, KT, EXTRA, scan);
+    const PagedScan found = paged_scan<THREADS, X>(p, KT, EXTRA, scan);
     const bool solo = HR == 1 && p.chunk_rows <= C::WARP_ROWS && 2ll * found.units >= p.solo_workers;
     const int nw = solo ? WARPS : 1;                            // workers of the block
-    paged_locate<WARPS>(p, found, KT, EXTRA, nw, gridDim.x * nw, SNAP, &blk);
+    paged_locate<WARPS, X>(p, found, KT, EXTRA, nw, gridDim.x * nw, SNAP, &blk);
     const int mine = solo ? w : 0;
     const int worker = blockIdx.x * nw + mine;
     // the warp's slices in a tile: all four, or one
     const int slices = solo ? KT / SLICE : 1, slice0 = solo ? 0 : w;
-    PagedCursor cur;
+    PagedCursor<X> cur;
 
     if (warp >= WARPS) {
         // ---------------------------------------------------------------- producer
@@ -171,10 +171,10 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             tma_prefetch_desc(&tm_v);
         }
         if (scribe) {
-            PagedCursor::no_join(p, worker);
+            PagedCursor<X>::no_join(p, worker);
             // the words of workers that there are not
             if (!solo)
-                for (int c = gridDim.x + worker; c < p.workers; c += gridDim.x) PagedCursor::no_join(p, c);
+                for (int c = gridDim.x + worker; c < p.workers; c += gridDim.x) PagedCursor<X>::no_join(p, c);
         }
         uint32_t armed = 0;                     // slices issued
         int st = 0;
@@ -190,7 +190,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                 if ((i & 31) == 0) {
                     const int key = key_of(i + lane);
                     page = -2;                  // nothing to load
-                    if (i + lane < live && key < cur.s.total) page = paged_page(p, cur.b, key / p.page);
+                    if (i + lane < live && key < cur.s.total) page = paged_page<X>(p, cur.b, key / p.page);
                 }
                 const int now = __shfl_sync(0xffffffffu, page, i & 31);
                 if (!(ok = mbar_wait_warp(&empty[st], ph, ab))) break;
@@ -550,7 +550,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
                                     a[br][j] = fmaf(wt[br][k], bufs[k * (C::RING / 4) + (r * 2 + br) * DV + lane + 32 * j], a[br][j]);
                     }
                     if (cur.whole()) {
-                        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+                        const float lam = paged_lambda<X>(p);
                         paged_finish_row<DV / 32>(p, lam, cur.b, x.h, x.q, lane, a[0], lt[0], a[1], lt[1]);
                     } else {
                         float* part = p.part + ((int64_t)cur.slot() * p.chunk_rows + row0 + r) * paged_part_floats(DV);
@@ -586,7 +586,7 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
             continue;
         }
         const PagedRow x = ra;
-        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+        const float lam = paged_lambda<X>(p);
         const float i1 = l[0][0] == 0.f ? 0.f : 1.f / l[0][0], i2 = l[1][0] == 0.f ? 0.f : 1.f / l[1][0];
         float sum = 0.f;
 #pragma unroll
@@ -642,20 +642,22 @@ paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k1, const __grid_constan
     }
 }
 
-template <int HD, bool KS, int HR>
+template <int HD, bool KS, int HR, bool X>
 int launch_rows(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
     constexpr int smem = Cfg<HD, KS>::SMEM;
     // workers are warps where one warp may be one
     const int blocks = p.workers / (p.chunk_rows <= Cfg<HD, KS>::WARP_ROWS ? WARPS : 1);
-    if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS, HR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(paged_mma_kernel<HD, KS, HR, X>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    const int rc = pdl_launch(paged_mma_kernel<HD, KS, HR>, dim3(blocks), THREADS, smem, stream, maps[0], maps[1], maps[2], p);
+    const int rc = pdl_launch(paged_mma_kernel<HD, KS, HR, X>, dim3(blocks), THREADS, smem, stream, maps[0], maps[1], maps[2], p);
     return rc == 0 ? launch_paged_combine(p, stream) : rc;
 }
 
 template <int HD, bool KS>
 int launch_hd(const CUtensorMap* maps, const PagedParams& p, cudaStream_t stream) {
-    return p.chunk_rows <= 8 ? launch_rows<HD, KS, 1>(maps, p, stream) : launch_rows<HD, KS, 2>(maps, p, stream);
+    if (p.cross)
+        return p.chunk_rows <= 8 ? launch_rows<HD, KS, 1, true>(maps, p, stream) : launch_rows<HD, KS, 2, true>(maps, p, stream);
+    return p.chunk_rows <= 8 ? launch_rows<HD, KS, 1, false>(maps, p, stream) : launch_rows<HD, KS, 2, false>(maps, p, stream);
 }
 
 }  // namespace pmma

@@ -30,9 +30,12 @@ struct PagedSeq {
     bool bad;           // lengths outside the table: rows of NaN (n_new and total are stand-ins)
 };
 
+// X, here and below: over an encoder's states (instances of their own: a branch in these cost
+// the cache's calls 2 to 3 %).
+template <bool X>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
     PagedSeq s;
-    if (p.cross) {
+    if constexpr (X) {
         const int n = p.lengths ? p.lengths[b] : p.page;
         s.n_new = p.Tq;
         s.bad = n < 0 || n > p.page;
@@ -63,10 +66,17 @@ __device__ __forceinline__ int paged_seq_tiles(const PagedSeq& s, int kt) { retu
 
 // The page of a key's slot, or -1 if its table entry is out of range.  `key` is below
 // the sequence's total, so the entry exists.
+template <bool X>
 __device__ __forceinline__ int paged_page(const PagedParams& p, int b, int index) {
-    if (!p.table) return b;
+    if constexpr (X) return b;
     const int32_t pg = __ldg(p.table + b * p.table_stride + index);
     return pg >= 0 && pg < p.num_pages ? pg : -1;
+}
+
+template <bool X>
+__device__ __forceinline__ float paged_lambda(const PagedParams& p) {
+    if constexpr (X) return lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+    return p.lambda_dev ? __ldg(p.lambda_dev) : p.lambda;
 }
 
 // The division of a launch.  All counts are below 2^31 (checked on the host).
@@ -113,7 +123,7 @@ struct PagedScan {
     int tiles;          // of a unit of its last sequence with any
     int total, units;   // of the launch
 };
-template <int THREADS>
+template <int THREADS, bool X>
 __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, int extra, int* scratch) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,7 +135,7 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
     s.sum = s.tiles = 0;
     int active = 0;
     for (int b = s.b0; b < s.b1; ++b) {
-        const int tiles = paged_seq_tiles(paged_seq(p, b), kt);
+        const int tiles = paged_seq_tiles(paged_seq<X>(p, b), kt);
         s.sum += tiles ? (tiles + extra) * per_seq : 0;
         active += tiles ? per_seq : 0;
         s.tiles = tiles ? tiles : s.tiles;
@@ -156,7 +166,7 @@ __device__ __forceinline__ PagedScan paged_scan(const PagedParams& p, int kt, in
 
 // Where the block's `nw` <= NW workers start, of `most` in the launch, and the one after.
 // Every thread calls this, and it ends with a barrier.
-template <int NW>
+template <int NW, bool X>
 __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedScan& s, int kt, int extra, int nw, int most,
                                              int snap, PagedBlock<NW>* out) {
     const int tid = threadIdx.x;
@@ -171,7 +181,7 @@ __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedSc
         int at = s.at;
         for (int b = s.b0; b < s.b1; ++b) {
             // with a sequence a thread its tiles are known
-            int tiles = s.b1 - s.b0 == 1 ? s.tiles : paged_seq_tiles(paged_seq(p, b), kt);
+            int tiles = s.b1 - s.b0 == 1 ? s.tiles : paged_seq_tiles(paged_seq<X>(p, b), kt);
             if (tiles == 0) continue;
             tiles += extra;
             if (first < at + tiles * units) {
@@ -187,6 +197,7 @@ __device__ __forceinline__ void paged_locate(const PagedParams& p, const PagedSc
 }
 
 // A worker's segments in turn.
+template <bool X>
 struct PagedCursor {
     int left;                   // tiles of the worker's range not yet handed out
     int local;                  // place among the sequence's tiles
@@ -206,7 +217,7 @@ struct PagedCursor {
         b = blk.start[w].b;
         local = blk.start[w].local;
         if (left <= 0) return;
-        s = paged_seq(p, b);
+        s = paged_seq<X>(p, b);
         tiles = paged_seq_tiles(s, kt);
         enter(p, kt, extra);
     }
@@ -215,7 +226,7 @@ struct PagedCursor {
             local = 0;
             do {
                 if (++b >= p.B) { left = 0; return; }   // never with tiles left
-                s = paged_seq(p, b);
+                s = paged_seq<X>(p, b);
             } while (s.n_new == 0);
             tiles = paged_seq_tiles(s, kt);
         }

@@ -183,7 +183,7 @@ __device__ __forceinline__ uint64_t tile_mask(const PagedParams& p, const PagedS
     return m & low((int64_t)s.total - k0);
 }
 
-template <int HD, bool KS>
+template <int HD, bool KS, bool X>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
                 const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
@@ -225,11 +225,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     tc_fence_before();
     pdl_wait();                                 // before the merging pass may start, which writes too
     pdl_launch_dependents();
-    paged_locate<1>(p, paged_scan<THREADS>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);    // with their barriers
+    paged_locate<1, X>(p, paged_scan<THREADS, X>(p, KT, EXTRA, scan), KT, EXTRA, 1, p.workers, SNAP, &blk);    // with their barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_ptr;
     const uint64_t lim = 200ull * 1000ull * 1000ull;
-    PagedCursor cur;
+    PagedCursor<X> cur;
 
     if (warp >= 8) {
         regs_dec<REGS_OTHER>();
@@ -247,7 +247,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
             const int boxes = KT / box_rows;
             uint32_t kst = 0, kph = 1, vst = 0, vph = 1, nk = 0, nv = 0, nq = 0;
             bool ok = true;
-            if (lane == 0) PagedCursor::no_join(p, blockIdx.x);
+            if (lane == 0) PagedCursor<X>::no_join(p, blockIdx.x);
             int seg = -1;                       // segments with tiles, as every role counts them
             for (; ok && !cur.done(); cur.next(p, KT, EXTRA)) {
                 const int live = cur.live_tiles(p, KT);
@@ -289,7 +289,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                 auto look = [&](int i) -> int {     // the page of this lane's box
                     const int key = (cur.tile0 + i) * KT + (int)lane * box_rows;
                     if (i >= live || (int)lane >= boxes || key >= cur.s.total) return -2;
-                    return paged_page(p, cur.b, key / p.page);
+                    return paged_page<X>(p, cur.b, key / p.page);
                 };
                 int page = look(0);
                 for (int i = 0; i < live; ++i) {
@@ -489,7 +489,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t tO = lane_base + TM_O + br * 128;     // this branch's O
         const float sl2 = p.scale_log2;
-        const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
+        const float lam = paged_lambda<X>(p);
         uint32_t sph = 0, ofph = 0, wph = 0;
         uint32_t pv_count = 0;
         bool ok = true;
@@ -653,7 +653,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
                         while (keys) {
                             const int key = (edge0 + f) * KT + __ffsll(keys) - 1;
                             keys &= keys - 1;
-                            const int page = paged_page(p, cur.b, key / p.page);
+                            const int page = paged_page<X>(p, cur.b, key / p.page);
                             if (page < 0) continue;
                             const uint16_t* v = reinterpret_cast<const uint16_t*>(
                                 static_cast<const __nv_bfloat16*>(p.v) + page * p.s_v[0] + cur.hk * p.s_v[1] +
@@ -763,12 +763,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant
     if (warp == 9) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <int HD, bool KS>
+template <int HD, bool KS, bool X>
 int launch_hd(const CUtensorMap* m, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream) {
     constexpr uint32_t smem = smem_bytes<HD, KS>();
-    if (cudaFuncSetAttribute(paged_tc_kernel<HD, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(paged_tc_kernel<HD, KS, X>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return -1;
-    const int rc = pdl_launch(paged_tc_kernel<HD, KS>, dim3(p.workers), THREADS, smem, stream, m[3], m[4], m[0], m[1], m[2],
+    const int rc = pdl_launch(paged_tc_kernel<HD, KS, X>, dim3(p.workers), THREADS, smem, stream, m[3], m[4], m[0], m[1], m[2],
                               p, box_rows, q_box);
     return rc == 0 ? launch_paged_combine(p, stream) : rc;
 }
@@ -776,10 +776,11 @@ int launch_hd(const CUtensorMap* m, const PagedParams& p, int box_rows, int q_bo
 }  // namespace ptc
 
 int launch_paged_tc(const CUtensorMap* maps, const PagedParams& p, int box_rows, int q_box, cudaStream_t stream) {
-    if (p.D == 64) return p.k_shared ? ptc::launch_hd<64, true>(maps, p, box_rows, q_box, stream)
-                                     : ptc::launch_hd<64, false>(maps, p, box_rows, q_box, stream);
-    return p.k_shared ? ptc::launch_hd<128, true>(maps, p, box_rows, q_box, stream)
-                      : ptc::launch_hd<128, false>(maps, p, box_rows, q_box, stream);
+    const auto launch = p.D == 64 ? (p.k_shared ? (p.cross ? ptc::launch_hd<64, true, true> : ptc::launch_hd<64, true, false>)
+                                                : (p.cross ? ptc::launch_hd<64, false, true> : ptc::launch_hd<64, false, false>))
+                                  : (p.k_shared ? (p.cross ? ptc::launch_hd<128, true, true> : ptc::launch_hd<128, true, false>)
+                                                : (p.cross ? ptc::launch_hd<128, false, true> : ptc::launch_hd<128, false, false>));
+    return launch(maps, p, box_rows, q_box, stream);
 }
 
 }  // namespace diffattn
