@@ -133,10 +133,13 @@ bool tma_rows(const void* p, const int64_t n[3], const int64_t s[3]) {
 bool tc_shape(const diffattn_cross_desc& d) {
     return d.dtype == DIFFATTN_BF16 && width_of(d) == 128 && (d.D == 64 || d.D == 128);
 }
+// The longest sequence that they take: the dK/dV kernel's blocks may wait for as long as the dQ
+// kernel walks one (0.8 us for 64 states), and a wait ends after 2 s.
+constexpr int64_t kMaxTiledStates = 1 << 26;
 // And the call's layout.
 bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, const void* q2, const void* k2, const void* v) {
     const int64_t nq[3] = {d.B, d.H, d.Tq}, nk[3] = {d.B, d.H / group_of(d), d.Tk};
-    return tc_shape(d) && tma_rows(q1, nq, d.q1_stride) && tma_rows(q2, nq, d.q2_stride) && tma_rows(k1, nk, d.k1_stride) &&
+    return tc_shape(d) && d.Tk <= kMaxTiledStates && tma_rows(q1, nq, d.q1_stride) && tma_rows(q2, nq, d.q2_stride) && tma_rows(k1, nk, d.k1_stride) &&
            tma_rows(k2, nk, d.k2_stride) && tma_rows(v, nk, d.v_stride);
 }
 
@@ -175,6 +178,11 @@ bool wants_split(const diffattn_cross_desc& d) {
                                       : (double)group_of(d) * ((d.Tq + 127) / 128);
     return 16 + d.B * Hk * chunks * tiles / SMS * 0.95 < whole;
 }
+
+// A few rows, of a shape for the tensor cores but in a layout that TMA does not take, are split
+// on the CUDA cores: 16 sequences of 1500 states, one row of 4 heads, all reading one sequence's
+// states: 33 us, where copies for the tensor cores take 64 (and for 4 rows each 70, against 77).
+bool few_rows(const diffattn_cross_desc& d) { return tc_shape(d) && group_of(d) * d.Tq <= 4 && cross_paged_ok(d); }
 
 // Heads that the persistent kernels work on at a time, each streaming `bytes`: about 48 MiB of
 // them (they then share the L2), with an item of `tiles` for every SM.
@@ -294,7 +302,7 @@ extern "C" {
 
 size_t diffattn_cross_workspace_bytes(const diffattn_cross_desc* desc) {
     if (check_cross(desc) != DIFFATTN_OK) return 0;
-    const size_t paged = wants_split(*desc) ? cross_paged_bytes(*desc) : 0;
+    const size_t paged = wants_split(*desc) || few_rows(*desc) ? cross_paged_bytes(*desc) : 0;
     return paged > 64 ? paged : 64;     // or an item counter
 }
 
@@ -342,9 +350,10 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     rc = device_info(&p.status, &sms);
     if (rc != DIFFATTN_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!out2 && wants_split(d))
+    const bool tc = tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(out, rows, d.o_stride) && (!out2 || aligned16(out2));
+    if (!out2 && (wants_split(d) || (!tc && few_rows(d))))
         return cross_paged(d, q1, k1, q2, k2, v, kv_lengths, lambda, p.lambda_dev, e, out, workspace, workspace_bytes, st);
-    if (tc_inputs(d, q1, k1, q2, k2, v) && tma_rows(out, rows, d.o_stride) && (!out2 || aligned16(out2)))
+    if (tc)
         return forward_tc(p, sms, workspace, st);
     return launch_cross_simt(p, st) == 0 ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
@@ -364,7 +373,7 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
     CrossParams p{};
     fill_cross(&p, d, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev);
     if (dk1 && !dk2 && !p.k_shared) return DIFFATTN_ERR_INVALID;
-    p.k_shared = dk1 && !dk2;
+    if (dk1) p.k_shared = !dk2;
     p.out = const_cast<void*>(out);
     p.out2 = const_cast<void*>(out2);
     p.lse = const_cast<float*>(lse);

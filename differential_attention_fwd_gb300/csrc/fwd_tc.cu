@@ -821,98 +821,98 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] = it.bad ? fill : -INFINITY;
                 }
             } else {
-            if (!(ok = TIMED_WAIT(wp, kWaitEpilogue, mbar_wait_warp(&bars[BAR_O_FULL], ofph, ab)))) break;
-            PROF_MARK(epi_t0);
-            ofph ^= 1;
-            tc_fence_after();
-            if (!CROSS && p.stats) {
-                // Row statistics for the backward: this branch's log2-sum-exp
-                // and Dd_b = dO . (O_b / l_b), 32 columns at a time.
-                const bool live = q < p.T;
-                const __nv_bfloat16* g = p.dout + it.b * p.do_sB + it.h * p.do_sH +
-                                         (int64_t)(live ? q : 0) * p.do_sT;
-                float dd = 0.f;
+                if (!(ok = TIMED_WAIT(wp, kWaitEpilogue, mbar_wait_warp(&bars[BAR_O_FULL], ofph, ab)))) break;
+                PROF_MARK(epi_t0);
+                ofph ^= 1;
+                tc_fence_after();
+                if (!CROSS && p.stats) {
+                    // Row statistics for the backward: this branch's log2-sum-exp
+                    // and Dd_b = dO . (O_b / l_b), 32 columns at a time.
+                    const bool live = q < p.T;
+                    const __nv_bfloat16* g = p.dout + it.b * p.do_sB + it.h * p.do_sH +
+                                             (int64_t)(live ? q : 0) * p.do_sT;
+                    float dd = 0.f;
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + c4 * 32, o);
-                    uint4 gv[4];
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c4 * 32, o);
+                        uint4 gv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        gv[i] = live ? *reinterpret_cast<const uint4*>(g + c4 * 32 + 8 * i)
-                                     : make_uint4(0, 0, 0, 0);
-                    tmem_wait_ld();
+                        for (int i = 0; i < 4; ++i)
+                            gv[i] = live ? *reinterpret_cast<const uint4*>(g + c4 * 32 + 8 * i)
+                                         : make_uint4(0, 0, 0, 0);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t w[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            dd = fmaf(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(w[e] << 16), dd);
-                            dd = fmaf(__uint_as_float(o[8 * i + 2 * e + 1]),
-                                      __uint_as_float(w[e] & 0xffff0000u), dd);
+                            for (int e = 0; e < 4; ++e) {
+                                dd = fmaf(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(w[e] << 16), dd);
+                                dd = fmaf(__uint_as_float(o[8 * i + 2 * e + 1]),
+                                          __uint_as_float(w[e] & 0xffff0000u), dd);
+                            }
                         }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[BAR_O_EMPTY]);
+                    if (live) {
+                        // stored negated: the consumers add them
+                        float* st = p.stats + (((int64_t)it.b * p.H + it.h) * p.T + q) * 4;
+                        st[br] = -(m_run + log2f(l));
+                        st[2 + br] = -(dd / l);
+                    }
+                    continue;
                 }
+                inv_l[br * BM + row] = 1.0f / l;
+                uint32_t o1[64], o2[64];
+                tmem_ld32(lane_base + TM_O + c0, &o1[0]);
+                tmem_ld32(lane_base + TM_O + c0 + 32, &o1[32]);
+                tmem_ld32(lane_base + TM_O + 128 + c0, &o2[0]);
+                tmem_ld32(lane_base + TM_O + 128 + c0 + 32, &o2[32]);
+                tmem_wait_ld();
+                PROF_ADD(wp, kEpiLoad, epi_t0);
+                PROF_MARK(sync_t0);
+                // O is in registers: the next item's PV may overwrite TMEM.
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[BAR_O_EMPTY]);
-                if (live) {
-                    // stored negated: the consumers add them
-                    float* st = p.stats + (((int64_t)it.b * p.H + it.h) * p.T + q) * 4;
-                    st[br] = -(m_run + log2f(l));
-                    st[2 + br] = -(dd / l);
+                if (lane == 0) {
+                    mbar_arrive(&bars[BAR_O_EMPTY]);
+                    mbar_arrive(&bars[BAR_L_READY]);
                 }
-                continue;
-            }
-            inv_l[br * BM + row] = 1.0f / l;
-            uint32_t o1[64], o2[64];
-            tmem_ld32(lane_base + TM_O + c0, &o1[0]);
-            tmem_ld32(lane_base + TM_O + c0 + 32, &o1[32]);
-            tmem_ld32(lane_base + TM_O + 128 + c0, &o2[0]);
-            tmem_ld32(lane_base + TM_O + 128 + c0 + 32, &o2[32]);
-            tmem_wait_ld();
-            PROF_ADD(wp, kEpiLoad, epi_t0);
-            PROF_MARK(sync_t0);
-            // O is in registers: the next item's PV may overwrite TMEM.
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars[BAR_O_EMPTY]);
-                mbar_arrive(&bars[BAR_L_READY]);
-            }
-            if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_L_READY], lph, ab)))) break;
-            lph ^= 1;
-            PROF_ADD(wp, kEpiSync, sync_t0);
-            PROF_MARK(math_t0);
-            const float inv1 = inv_l[row];
-            const float inv2 = inv_l[BM + row];
-            if (p.out2 && q < p.T) {
-                // training outputs: A_2 V for this thread's 64 columns, and this
-                // branch's log-sum-exp (natural log) of the scaled scores
-                __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + it.h * p.o_sH + (int64_t)q * p.o_sT + c0;
+                if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_L_READY], lph, ab)))) break;
+                lph ^= 1;
+                PROF_ADD(wp, kEpiSync, sync_t0);
+                PROF_MARK(math_t0);
+                const float inv1 = inv_l[row];
+                const float inv2 = inv_l[BM + row];
+                if (p.out2 && q < p.T) {
+                    // training outputs: A_2 V for this thread's 64 columns, and this
+                    // branch's log-sum-exp (natural log) of the scaled scores
+                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + it.h * p.o_sH + (int64_t)q * p.o_sT + c0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = 8 * i;
-                    *reinterpret_cast<uint4*>(o2row + c) = make_uint4(
-                        pack_bf16x2(__uint_as_float(o2[c]) * inv2, __uint_as_float(o2[c + 1]) * inv2),
-                        pack_bf16x2(__uint_as_float(o2[c + 2]) * inv2, __uint_as_float(o2[c + 3]) * inv2),
-                        pack_bf16x2(__uint_as_float(o2[c + 4]) * inv2, __uint_as_float(o2[c + 5]) * inv2),
-                        pack_bf16x2(__uint_as_float(o2[c + 6]) * inv2, __uint_as_float(o2[c + 7]) * inv2));
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = 8 * i;
+                        *reinterpret_cast<uint4*>(o2row + c) = make_uint4(
+                            pack_bf16x2(__uint_as_float(o2[c]) * inv2, __uint_as_float(o2[c + 1]) * inv2),
+                            pack_bf16x2(__uint_as_float(o2[c + 2]) * inv2, __uint_as_float(o2[c + 3]) * inv2),
+                            pack_bf16x2(__uint_as_float(o2[c + 4]) * inv2, __uint_as_float(o2[c + 5]) * inv2),
+                            pack_bf16x2(__uint_as_float(o2[c + 6]) * inv2, __uint_as_float(o2[c + 7]) * inv2));
+                    }
+                    p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] =
+                        (m_run + log2f(l)) * 0.6931471805599453f;
                 }
-                p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] =
-                    (m_run + log2f(l)) * 0.6931471805599453f;
-            }
-            // O = O1 / l1 - lambda O2 / l2 for this thread's 64 columns: a = O1 / l1
-            // and b = O2 / l2 rounded, then a - lambda b in one fused step
-            // (identical branches at lambda = 1 give a = b, hence exactly 0)
+                // O = O1 / l1 - lambda O2 / l2 for this thread's 64 columns: a = O1 / l1
+                // and b = O2 / l2 rounded, then a - lambda b in one fused step
+                // (identical branches at lambda = 1 give a = b, hence exactly 0)
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float a = __fmul_rn(__uint_as_float(o1[c]), inv1);
-                const float bb = __fmul_rn(__uint_as_float(o2[c]), inv2);
-                r[c] = __fmaf_rn(bb, -lam, a);
-            }
-            PROF_ADD(wp, kEpiMath, math_t0);
-            PROF_ADD(wp, kEpilogueBusy, epi_t0);
+                for (int c = 0; c < 64; ++c) {
+                    const float a = __fmul_rn(__uint_as_float(o1[c]), inv1);
+                    const float bb = __fmul_rn(__uint_as_float(o2[c]), inv2);
+                    r[c] = __fmaf_rn(bb, -lam, a);
+                }
+                PROF_ADD(wp, kEpiMath, math_t0);
+                PROF_ADD(wp, kEpilogueBusy, epi_t0);
             }
             PROF_MARK(norm_t0);
             if (p.norm != kNormNone) {

@@ -272,6 +272,47 @@ def test_some_gradients_alone():
             assert torch.equal(g, want[w]), w
 
 
+@pytest.mark.parametrize("dtype,D,Dv", [(BF, 128, 128), (BF, 64, 128), (F32, 64, 128)])
+@pytest.mark.parametrize("Tq", [20, 700])
+def test_queries_alone_over_one_key_tensor(dtype, D, Dv, Tq):
+    x, n = inputs(19, dtype, 2, 4, 2, Tq, 90, D, Dv, True, [90, 20])
+    do = torch.randn(2, 4, Tq, Dv, device="cuda").to(dtype)
+    _, want = train(x, n, 0.8, do)
+    q1, q2 = x[0].clone().requires_grad_(), x[2].clone().requires_grad_()
+    got = torch.autograd.grad(da.differential_cross_attention(q1, x[1], q2, x[1], x[4], 0.8, kv_lengths=n), (q1, q2), do)
+    assert torch.equal(got[0], want["q1"]) and torch.equal(got[1], want["q2"])
+
+
+@pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 128, 128, True), (F32, 32, 64, False)])
+@pytest.mark.parametrize("H,Hk,Tq", [(4, 4, 1), (4, 2, 2), (4, 2, 3), (4, 4, 70)])
+def test_states_that_all_sequences_read(dtype, D, Dv, shared, H, Hk, Tq):
+    """One encoder's states expanded over the batch, and a gradient expanded over the heads: the
+    answers of copies, and the states' gradients summed by autograd."""
+    x, n = inputs(20, dtype, 3, H, Hk, Tq, 90, D, Dv, shared)
+    n = torch.tensor([90, 0, 41], dtype=torch.int32, device="cuda")
+    one = [t[:1].clone().requires_grad_() for t in (x[1], x[3], x[4])]
+    k1 = one[0].expand(3, -1, -1, -1)
+    k2 = k1 if shared else one[1].expand(3, -1, -1, -1)
+    y = [x[0], k1, x[2], k2, one[2].expand(3, -1, -1, -1)]
+    dense = [t.detach().contiguous() for t in y]
+    dense[3] = dense[1] if shared else dense[3]
+    do = torch.randn(3, 1, Tq, Dv, device="cuda").to(dtype).expand(-1, H, -1, -1)
+    o = da.differential_cross_attention(*y, 0.8, kv_lengths=n)
+    lens = n.tolist()
+    lam = float(torch.tensor(0.8))
+    want = reference(dense, lam, lens)
+    check("o", o, want.o, want.o_tol)
+    with torch.no_grad():
+        check("served o", da.differential_cross_attention(*y, 0.8, kv_lengths=n), want.o, want.o_tol)
+    got = torch.autograd.grad(o, one if not shared else [one[0], one[2]], do)
+    back = want.backward(d64(do))
+    names = ["k", "v"] if shared else ["k1", "k2", "v"]
+    for name, g in zip(names, got):
+        # the sum over the batch: each sequence's gradient was rounded, and so is the sum
+        w, tol = back[name]
+        check("d" + name, g, w.sum(0, keepdim=True), tol.sum(0, keepdim=True) + H_OF[dtype] * (w.sum(0, keepdim=True).abs() + tol.sum(0, keepdim=True)))
+
+
 def test_coefficient_kinds():
     x, n = inputs(13, BF, 2, 4, 2, 20, 90, 64, 128, False, [90, 20])
     do = torch.randn(2, 4, 20, 128, device="cuda").to(BF)
