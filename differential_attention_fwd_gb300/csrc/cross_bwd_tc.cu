@@ -888,7 +888,10 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t c0 = 32 * half;
         const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
-        const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2), nlam2 = f2_pack(-lam, -lam);
+        // |lambda| goes into branch 2's exponents, -sign(lambda) into its Dd and the two sums: no
+        // product with lambda is left (2 x 16 heads x 4096 rows over 4096 states: 946 -> 927 thousand cycles)
+        const float log_lam = log2f(fabsf(lam)), nsgn = lam < 0.f ? 1.f : -1.f;
+        const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2), nsgn2 = f2_pack(nsgn, nsgn);
         uint32_t accph = 0, qc = 0;          // qc: query tiles consumed (whole launch)
         // the rows' exact Dd are the dQ kernel's
         pdl_wait();
@@ -928,9 +931,9 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                 if (++qt == p.nq64) { qt = 0; ++h; }
                 __syncwarp();               // the previous tile's reads of the scratch are done
                 scr[lane] = nst.x;
-                scr[32 + lane] = nst.y;
+                scr[32 + lane] = nst.y + log_lam;
                 scr[64 + lane] = nst.z;
-                scr[96 + lane] = nst.w;
+                scr[96 + lane] = nsgn * nst.w;
                 __syncwarp();
                 if (t + 1 < it.n) nst = stats_of(it.b, h, qt);
                 if (!(ok = mbar_wait_warp(&bars[S_FULL], qc & 1u, ab))) break;
@@ -983,11 +986,11 @@ diffattn_cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __gr
                             const uint64_t E1 = hh ? f2_pack(e1.z, e1.w) : f2_pack(e1.x, e1.y);
                             const uint64_t E2 = hh ? f2_pack(e2.z, e2.w) : f2_pack(e2.x, e2.y);
                             const uint64_t a1 = f2_from_bits(s1[cc], s1[cc + 1]);
-                            const uint64_t a2n = f2_mul(f2_from_bits(s2[cc], s2[cc + 1]), nlam2);
+                            const uint64_t a2 = f2_from_bits(s2[cc], s2[cc + 1]);      // |lambda| A_2
                             const uint64_t dp2 = f2_from_bits(dp[cc], dp[cc + 1]);
                             const uint64_t d1 = f2_mul(a1, f2_add(dp2, E1));
-                            const uint64_t d2 = f2_mul(a2n, f2_add(dp2, E2));
-                            const uint64_t w = f2_add(a1, a2n);
+                            const uint64_t d2 = f2_mul(a2, f2_fma(dp2, nsgn2, E2));
+                            const uint64_t w = f2_fma(a2, nsgn2, a1);
                             w1[cc / 2] = pack_bf16x2(f2_lo(d1), f2_hi(d1));
                             w2[cc / 2] = pack_bf16x2(f2_lo(d2), f2_hi(d2));
                             w3[cc / 2] = pack_bf16x2(f2_lo(w), f2_hi(w));
