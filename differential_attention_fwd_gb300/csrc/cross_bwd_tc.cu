@@ -25,9 +25,16 @@
 //   and takes the saved one, whose error (2^-9 of |dO| |O|) is small beside dP where O is a
 //   mean over many states; over a single tile, where it is not, the sum comes first.
 // dkdv: item (b, key/value head, 128 states in TMEM lanes, a split of the query rows where there
-//   are few such tiles); over every 64 query rows of the group's heads: S_1^T, S_2^T, dP^T, then dV += W^T dO, dK_b += dS_b^T Q_b (one accumulator
-//   for both branches where they share their keys: one rounding).  States behind the
-//   sequence's own are lanes whose results are replaced by zeros.
+//   are few such tiles); over every 64 query rows of the group's heads: S_1^T, S_2^T, dP^T, then
+//   dV += W^T dO, dK_b += dS_b^T Q_b (one accumulator for both branches where they share their
+//   keys: one rounding).  States behind the sequence's own are lanes whose results are replaced
+//   by zeros.
+//
+// Bound by the elementwise warps, at D = 64 in both (dq 1,500 cycles a tile against 770 of the
+// tensor core; dkdv 2,150 against 1,020), and at D = 128 in dkdv; dq there by its operand reads
+// from shared memory and the hand-offs of its one score buffer.  2 x 16 heads of 64, 4096 rows
+// over 4096 states: 334 us and 474 us, with the V2 head (8 key/value heads) 523 and 686: 850 and
+// 909 TFLOP/s of the five products that a backward needs.
 //
 // What a batch's padding holds must not reach a sum: in dq the rows of K and V behind a
 // sequence's last state would meet weights of 0, and 0 times NaN is NaN, so a warp turns
@@ -79,12 +86,13 @@ __device__ __forceinline__ void locate(int idx, int heads, int tiles, int group,
 
 // ---------------------------------------------------------------------------
 // The rows' statistics from the forward's saved results: Dd_2 = dO . (A_2 V), Dd_1 = dO . (O +
-// lambda A_2 V), stored negated with the log2-sum-exps.  16 lanes a row, 16 bytes a lane: HBM
-// (39 us with a lane for every fourth pair of bytes, at 131,000 rows).
+// lambda A_2 V), stored negated with the log2-sum-exps.  16 lanes a row, 16 bytes a lane, two rows
+// a group: HBM, 19 us at 131,000 rows, 0.78 of the copy rate (22 us with four rows and half the
+// blocks an SM, 39 with a lane for every fourth pair of bytes).
 // ---------------------------------------------------------------------------
 constexpr int PREP_THREADS = 256;
-constexpr int PREP_ROWS = 4;            // of a group of lanes, loaded together
-__global__ void __launch_bounds__(PREP_THREADS)
+constexpr int PREP_ROWS = 2;            // of a group of lanes, loaded together
+__global__ void __launch_bounds__(PREP_THREADS, 6)
 cross_prep_kernel(const CrossTcParams p) {
     constexpr int GROUPS = PREP_THREADS / 16;
     const int g = threadIdx.x % 16, h = blockIdx.y % p.H, b = blockIdx.y / p.H;
