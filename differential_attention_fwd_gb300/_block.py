@@ -23,7 +23,9 @@ def differential_cross_attention(q1: torch.Tensor, k1: torch.Tensor, q2: torch.T
 
     q1, q2: [B, H, Tq, D]; k1, k2: [B, H_kv, Tk, D], value: [B, H_kv, Tk, Dv], the encoder's
     states as the layer projected them, H_kv dividing H, D <= 128, Dv <= 256; bfloat16 or
-    float32; other strides than the innermost pass through.  k2 None or k1 again: one key
+    float32; other strides than the innermost pass through (in bf16 with Dv = 128 and D = 64 or
+    128, rows with a stride of 0 or not of whole 16-byte pieces are copied first, beyond a few
+    rows).  k2 None or k1 again: one key
     tensor for both branches.  kv_lengths: [B] int32 on the device, sequence b has only its
     first kv_lengths[b] states (None: all Tk), and what lies behind them has no influence,
     NaN included; one with none gives zeros (before the epilogue).  coefficient, out and the

@@ -34,7 +34,7 @@
 // tensor core; dkdv 2,150 against 1,020), and at D = 128 in dkdv; dq there by its operand reads
 // from shared memory and the hand-offs of its one score buffer.  2 x 16 heads of 64, 4096 rows
 // over 4096 states: 334 us and 474 us, with the V2 head (8 key/value heads) 523 and 686: 850 and
-// 909 TFLOP/s of the five products that a backward needs.
+// 909 TFLOP/s of the products that a backward needs.
 //
 // What a batch's padding holds must not reach a sum: in dq the rows of K and V behind a
 // sequence's last state would meet weights of 0, and 0 times NaN is NaN, so a warp turns

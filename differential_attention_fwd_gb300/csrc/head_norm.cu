@@ -15,11 +15,15 @@
 //
 // The passes are bound by HBM: x in, y out; x and dy in, dx out.  A group of lanes holds a
 // row, twice 16 bytes a lane (the exchanges of the row's sums are a third of the backward's
-// instructions with 16), so the row stays in registers and the only exchanges are its sums.  A block works on one head, whose weights
-// stay in registers, and takes ROWS rows a group at a time: their loads go out together.
-// In the backward every block walks a chunk of the tokens, each lane adding up dw and db
-// of its own channels, and leaves one partial row of each: the sums' order is fixed,
-// without atomics.
+// instructions with 16), so the row stays in registers and the only exchanges are its sums.
+// A block works on one head, whose weights stay in registers, and takes ROWS rows a group at a
+// time: their loads go out together.  In the backward every block walks a chunk of the tokens,
+// each lane adding up dw and db of its own channels, and leaves one partial row of each: the
+// sums' order is fixed, without atomics.
+//
+// 2 x 8192 tokens, 16 heads of 128, bf16, layer norm: forward 22.6 us (5.9 TB/s), backward 36.8
+// us (5.5 TB/s) and 3.5 us for dw and db; with 16 bytes a lane 27 and 50 us.  One token of 16
+// sequences: 3.2 us, a launch's latency.
 #include "block.h"
 #include "pdl.cuh"
 #include "ptx.cuh"
