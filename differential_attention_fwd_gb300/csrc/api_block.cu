@@ -143,21 +143,40 @@ bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, con
            tma_rows(k2, nk, d.k2_stride) && tma_rows(v, nk, d.v_stride);
 }
 
+// A short head's rows, a power of two and at least 8 (what a swizzled tile's rows repeat in), and
+// how many heads of a group the tensor-core forward's items take together: as few as leave one
+// item an SM, if they fit into 128 rows.  16 sequences of 1500 states, 32 rows of 16 over 4 heads:
+// 20 us with two heads an item, 41 with one.
+int short_rows_log2(int64_t Tq) {
+    int s = 3;
+    while (s < 7 && (int64_t(1) << s) < Tq) ++s;
+    return s;
+}
+int packed_heads(int64_t B, int64_t H, int64_t group, int64_t Tq) {
+    int pack = 1;
+    for (int64_t n = 2; n <= group && (n << short_rows_log2(Tq)) <= 128 && Tq <= 64 && B * H / pack > 152; ++n)
+        if (group % n == 0) pack = (int)n;
+    return pack;
+}
+
 // What the tensor-core forward takes for sequences of Tk states, about, in us.
-double whole_us(int64_t B, int64_t H, int64_t Tq, int64_t Tk, int64_t D) {
-    const double items = (double)B * H * ((Tq + 127) / 128), tiles = (double)((Tk + 63) / 64);
-    return 5 + std::ceil(items / 152) * tiles * (D == 64 ? 0.65 : 0.87);
+double whole_us(int64_t B, int64_t H, int64_t group, int64_t Tq, int64_t Tk, int64_t D) {
+    const double items = (double)B * H / packed_heads(B, H, group, Tq) * ((Tq + 127) / 128), tiles = (double)((Tk + 63) / 64);
+    return 5 + std::ceil(items / 152) * tiles * (D == 64 ? 0.63 : 0.92);
 }
 
 // Whether the kernels of the paged cache take a serving call.  They divide the states of all
 // sequences evenly over the SMs and join the parts in a second launch, where the forward's
-// blocks each walk a whole sequence for 128 rows of a head.  By estimates, in us, for lengths
-// of Tk, from what either measured (bf16; the forward, then the split):
-//   one sequence, 16 heads of 64, 32 rows:  77 states 6.8, 15.9; 1500 19.9, 20.3; 6000 62, 29.5
-//   16 sequences, the same:                 77 states 16.2, 23.5; 1500 47, 74; 6000 142, 180
-//   16 sequences, 16 over 4 heads, 32 rows: 77 states 15.3, 21.8; 1500 41, 43; 6000 121, 73
-//   the V2 head, 16 over 8 heads, 64 rows:  77 states 7.3, 17.8; 1500 23, 30; 6000 84, 37
-// Up to 16 rows a key/value head the split is bound by HBM, beyond by its products.
+// blocks each walk a whole sequence for 128 rows.  By estimates, in us, for lengths of Tk, from
+// what either measured (bf16; the forward, then the split):
+//   one sequence, 16 heads of 64, 32 rows:   77 states 6.8, 15.9; 1500 19.9, 20.3; 6000 62, 29.5
+//   16 sequences, the same:                  77 states 16.2, 23.5; 1500 47, 74; 6000 142, 180
+//   16 sequences, 16 over 4 heads, one row:  77 states 7.7, 14.2; 1500 19.8, 21.2; 6000 63, 44
+//   the same, 32 rows:                       77 states 7.6, 20.9; 1500 19.9, 39; 6000 64, 69
+//   the V2 head, 16 over 8 heads, 64 rows:   77 states 7.3, 17.8; 1500 23, 30; 6000 84, 37
+//   16 sequences, the same:                  1500 states 29.6, 56; 6000 93, 116
+//   4 sequences, 64 over 4 heads, 4 rows:    3000 states 32.7, 25.5
+// Up to 16 rows a key/value head the split is bound by HBM, beyond by its products and starts.
 bool wants_split(const diffattn_cross_desc& d) {
     if (!cross_paged_ok(d)) return false;
     constexpr double SMS = 152;
@@ -170,13 +189,15 @@ bool wants_split(const diffattn_cross_desc& d) {
         const double whole = 6 + std::ceil(items / (2 * SMS)) * 2 * tiles * 1.5;
         return 20 + units * 2 * tiles / (4 * SMS) * 3 < whole;
     }
-    const double bytes = (double)d.B * Hk * d.Tk * (4 * d.D + 256);
-    const double least = 5 + bytes / 5.5e6, whole = whole_us(d.B, d.H, d.Tq, d.Tk, d.D);
-    if (rows <= 16) return 12.5 + bytes / 5.2e6 < (whole > least ? whole : least);
+    const double bytes = (double)d.B * Hk * d.Tk * 512;     // of a state's keys (the V2 head's: one tensor) and value
+    const double least = 5 + bytes / 5.5e6, by_tiles = whole_us(d.B, d.H, group_of(d), d.Tq, d.Tk, d.D);
+    const double whole = by_tiles > least ? by_tiles : least;
+    if (rows <= 16) return 12.5 + bytes / 5.2e6 * (rows > 8 ? 1.5 : 1.0) < whole;
     const int64_t head_rows = (d.Tq + 7) / 8 * 8;
     const double chunks = d.Tq <= 128 ? std::ceil(group_of(d) / std::floor(128.0 / head_rows))
                                       : (double)group_of(d) * ((d.Tq + 127) / 128);
-    return 16 + d.B * Hk * chunks * tiles / SMS * 0.95 < whole;
+    const double units = d.B * Hk * chunks;
+    return (d.D == 64 ? 18 : 26) + units * tiles / SMS * 1.2 + units * 0.08 < whole;
 }
 
 // A few rows, of a shape for the tensor cores but in a layout that TMA does not take, are split
@@ -209,17 +230,21 @@ int cross_maps(CUtensorMap* m, const CrossParams& p, const void* o, const int64_
 
 // The forward on the tensor cores; `counter`: 64 bytes of workspace.
 int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream) {
-    CUtensorMap maps[6];
-    if (cross_maps(maps, c, c.out, c.s_o, 128, 64, 32) != DIFFATTN_OK) return DIFFATTN_ERR_CUDA;
     TcParams p{};
+    p.pack = packed_heads(c.B, c.H, c.group, c.Tq);
+    p.item_heads = c.H / p.pack;
+    p.pack_shift = p.pack > 1 ? short_rows_log2(c.Tq) : 7;
+    CUtensorMap maps[6];
+    const int rows = 1 << p.pack_shift;
+    if (cross_maps(maps, c, c.out, c.s_o, rows, 64, rows < 32 ? rows : 32) != DIFFATTN_OK) return DIFFATTN_ERR_CUDA;
     p.B = c.B;
     p.H = c.H;
     p.T = c.Tq;
     p.Tk = c.Tk;
     p.nq = (c.Tq + 127) / 128;
     p.nk = (c.Tk + 63) / 64;
-    p.total_items = c.B * c.H * p.nq;
-    p.group = heads_at_once((int64_t)c.B * c.H, (int64_t)c.Tk * ((c.k_shared ? 1 : 2) * c.D + c.Dv) * 2, p.nq, sms);
+    p.total_items = c.B * p.item_heads * p.nq;
+    p.group = heads_at_once((int64_t)c.B * p.item_heads, (int64_t)c.Tk * ((c.k_shared ? 1 : 2) * c.D + c.Dv) * 2, p.nq, sms);
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.D));
     p.lambda = c.lambda;
     p.lambda_dev = c.lambda_dev;
@@ -242,7 +267,7 @@ int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream
     const int grid = p.total_items < sms ? p.total_items : sms;
     // Long calls claim their items from a counter, since sequences differ in length.  To zero it
     // takes 7 us between the stream's kernels, so short ones deal them out.
-    if (p.total_items > sms && whole_us(c.B, c.H, c.Tq, c.Tk, c.D) > 60) {
+    if (p.total_items > sms && whole_us(c.B, c.H, c.group, c.Tq, c.Tk, c.D) > 60) {
         p.sched = static_cast<uint32_t*>(counter);
         if (cudaMemsetAsync(counter, 0, 64, stream) != cudaSuccess) return DIFFATTN_ERR_CUDA;
     }

@@ -63,7 +63,9 @@
 // sequence has; its last tile's scores are masked, and warp 11 turns the value rows behind
 // the last state into zeros before the product reads them (a weight of 0 times what a
 // batch's padding holds, NaN or infinite, would not be 0).  An item without a state is
-// written by the softmax warps alone.  Instances of their own: the others keep their code.
+// written by the softmax warps alone.  Where a head has few rows and a key/value head several
+// heads, an item takes the rows of some of them (p.pack: 8, 16, 32 or 64 rows each).
+// Instances of their own: the others keep their code.
 // 2 x 16 heads, 4096 rows over 4096 states: D = 64 289 us (1428 TFLOP/s), the V2 head 359 us
 // (1531), bound as the others by the hand-offs between the softmax and the products.
 //
@@ -185,7 +187,8 @@ __device__ __forceinline__ int item_index(int k, int cta, int grid) {
 // then head by head.
 template <bool CROSS>
 __device__ __forceinline__ Item decode_item(int idx, const TcParams& p) {
-    const int BH = p.B * p.H;
+    const int heads = CROSS ? p.item_heads : p.H;
+    const int BH = p.B * heads;
     const int per_group = p.group * p.nq;
     const int g = idx / per_group;
     const int g0 = g * p.group;
@@ -196,8 +199,8 @@ __device__ __forceinline__ Item decode_item(int idx, const TcParams& p) {
     Item it;
     if constexpr (CROSS) {
         it.qt = r;
-        it.b = bh / p.H;
-        it.h = bh - it.b * p.H;
+        it.b = bh / heads;
+        it.h = (bh - it.b * heads) * p.pack;
         const CrossLen len = cross_len(p.lengths, it.b, p.Tk);
         it.len = len.n;
         it.bad = len.bad;
@@ -490,12 +493,21 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 }
                 first = false;
                 mbar_arrive_expect_tx(&bars[BAR_Q_FULL], 2 * C::Q_BYTES);
+                auto load_q = [&](int at, int h) {
 #pragma unroll
-                for (int pn = 0; pn < C::PANELS; ++pn) {
-                    tma_load_4d(smem + C::OFF_Q1 + pn * Q_PANEL, &tm_q1, &bars[BAR_Q_FULL], pn * 64,
-                                it.qt * BM, it.h, it.b);
-                    tma_load_4d(smem + C::OFF_Q2 + pn * Q_PANEL, &tm_q2, &bars[BAR_Q_FULL], pn * 64,
-                                it.qt * BM, it.h, it.b);
+                    for (int pn = 0; pn < C::PANELS; ++pn) {
+                        tma_load_4d(smem + C::OFF_Q1 + pn * Q_PANEL + at * 128, &tm_q1, &bars[BAR_Q_FULL], pn * 64,
+                                    it.qt * BM, h, it.b);
+                        tma_load_4d(smem + C::OFF_Q2 + pn * Q_PANEL + at * 128, &tm_q2, &bars[BAR_Q_FULL], pn * 64,
+                                    it.qt * BM, h, it.b);
+                    }
+                };
+                if (!CROSS || p.pack == 1) {
+                    load_q(0, it.h);
+                } else {
+                    // several heads' rows, the last head's again in what is left (rows of their own that
+                    // nothing reads, but of the same values in every run)
+                    for (int at = 0; at < BM; at += 1 << p.pack_shift) load_q(at, it.h + min(at >> p.pack_shift, p.pack - 1));
                 }
                 ++armed_q;
                 const int hk = it.h / p.kv_group;     // key/value head of this query head
@@ -682,6 +694,9 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
         const int br = warp >> 2;            // branch
         const uint32_t quad = warp & 3;      // TMEM lane quadrant
         const int row = quad * 32 + lane;    // query row within the tile
+        // CROSS: its head among the item's, and its row of that head (none: past every length)
+        const int slot = CROSS ? min(row >> p.pack_shift, p.pack - 1) : 0;
+        const int hrow = !CROSS ? row : row >> p.pack_shift >= p.pack ? 1 << 30 : row & ((1 << p.pack_shift) - 1);
         const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
         const uint32_t tO = lane_base + TM_O + br * 128;
         const float sl2 = p.scale_log2;
@@ -700,7 +715,8 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
         if (ok && idx >= 0) next = decode_item<CROSS>(idx, p);
         for (int k = 0; ok && idx >= 0; ++k) {
             const Item it = next;
-            const int q = it.qt * BM + row;
+            const int q = it.qt * BM + hrow;
+            const int h = it.h + slot;
             float m_run = -INFINITY;
             float l = 0.f;
 
@@ -817,10 +833,10 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 for (int c = 0; c < 64; ++c) r[c] = fill;
                 if (p.out2 && q < p.T) {
                     const uint32_t w = pack_bf16x2(fill, fill);
-                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + it.h * p.o_sH + (int64_t)q * p.o_sT + c0;
+                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + h * p.o_sH + (int64_t)q * p.o_sT + c0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(o2row + 8 * i) = make_uint4(w, w, w, w);
-                    p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] = it.bad ? fill : -INFINITY;
+                    p.lse[(((int64_t)it.b * p.H + h) * p.T + q) * 2 + br] = it.bad ? fill : -INFINITY;
                 }
             } else {
                 if (!(ok = TIMED_WAIT(wp, kWaitEpilogue, mbar_wait_warp(&bars[BAR_O_FULL], ofph, ab)))) break;
@@ -891,7 +907,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 if (p.out2 && q < p.T) {
                     // training outputs: A_2 V for this thread's 64 columns, and this
                     // branch's log-sum-exp (natural log) of the scaled scores
-                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + it.h * p.o_sH + (int64_t)q * p.o_sT + c0;
+                    __nv_bfloat16* o2row = p.out2 + it.b * p.o_sB + h * p.o_sH + (int64_t)q * p.o_sT + c0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int c = 8 * i;
@@ -901,7 +917,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                             pack_bf16x2(__uint_as_float(o2[c + 4]) * inv2, __uint_as_float(o2[c + 5]) * inv2),
                             pack_bf16x2(__uint_as_float(o2[c + 6]) * inv2, __uint_as_float(o2[c + 7]) * inv2));
                     }
-                    p.lse[(((int64_t)it.b * p.H + it.h) * p.T + q) * 2 + br] =
+                    p.lse[(((int64_t)it.b * p.H + h) * p.T + q) * 2 + br] =
                         (m_run + log2f(l)) * 0.6931471805599453f;
                 }
                 // O = O1 / l1 - lambda O2 / l2 for this thread's 64 columns: a = O1 / l1
@@ -951,8 +967,8 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     const float var = (stat[2 * BM + row] + stat[3 * BM + row]) * (1.0f / VD);
                     rinv = rsqrtf(var + p.norm_eps);
                 }
-                const float* wrow = p.norm_weight ? p.norm_weight + it.h * VD + c0 : nullptr;
-                const float* brow = p.norm_bias ? p.norm_bias + it.h * VD + c0 : nullptr;
+                const float* wrow = p.norm_weight ? p.norm_weight + h * VD + c0 : nullptr;
+                const float* brow = p.norm_bias ? p.norm_bias + h * VD + c0 : nullptr;
 #pragma unroll
                 for (int c = 0; c < 64; ++c) {
                     float y = (r[c] - mu) * rinv;
@@ -984,7 +1000,15 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_4d(&tm_o, stage, c0, it.qt * BM + (int)quad * 32, it.h, it.b);
+                if (!CROSS || p.pack == 1) {
+                    tma_store_4d(&tm_o, stage, c0, it.qt * BM + (int)quad * 32, it.h, it.b);
+                } else {
+                    const int rows = 1 << p.pack_shift, box = min(rows, 32);
+                    for (int i = 0; i < 32; i += box) {
+                        const int r0 = (int)quad * 32 + i, s = r0 >> p.pack_shift;
+                        if (s < p.pack) tma_store_4d(&tm_o, stage + i * 128, c0, r0 & (rows - 1), it.h + s, it.b);
+                    }
+                }
                 bulk_commit();
             }
             PROF_ADD(wp, kEpiStore, store_t0);

@@ -65,6 +65,9 @@ struct TcParams {
     __nv_bfloat16* out2;
     float* lse;
     const int32_t* lengths;     // the cross instances: [B], nullptr: Tk each
+    int pack, pack_shift;       // and heads of a group that an item takes, 2^pack_shift rows of its
+                                // 128 each (1, 7: a head)
+    int item_heads;             // H / pack
     int lambda_bf16;            // lambda_dev points to a bf16 (the cross instances)
 };
 

@@ -145,6 +145,29 @@ def test_grouped_heads(H, Hk, dtype, D, Dv, shared, Tq):
     compare(x, n, lens, 0.8)
 
 
+@pytest.mark.parametrize("H,Hk", [(16, 4), (18, 3), (32, 1), (10, 5), (16, 16)])
+@pytest.mark.parametrize("D,shared", [(64, False), (128, True)])
+@pytest.mark.parametrize("Tq", [1, 8, 9, 33, 64, 65])
+def test_short_rows_of_many_heads(H, Hk, D, shared, Tq):
+    """More heads than SMs: items take several heads of a group."""
+    B = 160 // H + 2
+    lens = [70, 0, 64, 3] + [70] * (B - 4)
+    x, n = inputs(Tq, BF, B, H, Hk, Tq, 70, D, 128, shared, lens)
+    compare(x, n, lens, 0.8)
+    w = 1 + torch.arange(H * 128, device="cuda").reshape(H, 128) / 1000
+    with torch.no_grad():                           # a weight a head, and rows of their own strides
+        out = torch.full((B, Tq, H, 128), 7.0, dtype=BF, device="cuda").transpose(1, 2)
+        got = da.differential_cross_attention(*x, 0.8, kv_lengths=n, norm="rms", norm_weight=w, out_scale=0.5, out=out)
+        one = torch.cat([da.differential_cross_attention(*[t[b:b + 1] for t in x], 0.8, kv_lengths=n[b:b + 1], norm="rms",
+                                                         norm_weight=w, out_scale=0.5) for b in range(B)])
+    # one sequence may go another way: each is within its bound, which a norm of O spreads over the row
+    o = reference(x, float(torch.tensor(0.8)), lens)
+    rs = (o.o.pow(2).mean(-1, keepdim=True) + 1e-5).rsqrt()
+    tol = o.o_tol - o.h * o.o.abs()
+    tol = 1.5 * rs * (tol + o.o.abs() * rs * rs * (o.o.abs() * tol).mean(-1, keepdim=True)) + 64 * ref.U
+    check("normed", got, d64(one), 2 * 0.5 * d64(w)[:, None] * tol + 4 * o.h * d64(one).abs())
+
+
 @pytest.mark.parametrize("layout", ["token", "odd"])
 @pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 128, 128, True), (F32, 64, 128, False)])
 def test_layouts(layout, dtype, D, Dv, shared):
