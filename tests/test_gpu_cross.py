@@ -399,6 +399,52 @@ def test_same_bits_on_other_streams_and_in_graphs():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("B,H,Hk,Tq,Tk,D", [(4, 16, 16, 700, 3000, 64), (3, 16, 8, 700, 3000, 128), (24, 16, 4, 20, 900, 64)])
+def test_long_calls_in_graphs_and_at_once(B, H, Hk, Tq, Tk, D):
+    """Items claimed from a counter, and several heads an item: two replayed graphs at once and two
+    streams at once, on new lengths, have the bits of a call alone."""
+    x, _ = inputs(21, BF, B, H, Hk, Tq, Tk, D, 128, D == 128)
+    n = torch.full((B,), Tk, dtype=torch.int32, device="cuda")
+    x = [t.requires_grad_() for t in x]
+    leaves = x[:3] + ([] if D == 128 else [x[3]]) + [x[4]]
+    do = torch.randn(B, H, Tq, 128, device="cuda").to(BF)
+    lam = torch.tensor(0.8, device="cuda")
+
+    def step():
+        o = da.differential_cross_attention(*x, lam, kv_lengths=n)
+        with torch.no_grad():
+            served = da.differential_cross_attention(*x, lam, kv_lengths=n, norm="rms")
+        return o, served, *torch.autograd.grad(o, leaves, do)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    with torch.cuda.stream(streams[0]):
+        step()
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append([t.detach() for t in step()])
+        graphs.append(graph)
+    n.copy_(torch.arange(B, dtype=torch.int32) * (Tk // B))         # the first without a state
+    want = [t.detach() for t in step()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for h in held:
+        assert all(torch.equal(a, b) for a, b in zip(h, want))
+    got = []
+    for stream in streams:
+        with torch.cuda.stream(stream):
+            got.append(step())
+    torch.cuda.synchronize()
+    for h in got:
+        assert all(torch.equal(a, b) for a, b in zip(h, want))
+    assert not want[0][0].any() and want[0][-1].isfinite().all()
+
+
 def test_non_finite_states_that_are_seen_stay_in_their_sequence():
     x, n = inputs(15, BF, 2, 4, 2, 40, 90, 64, 128, False, [90, 50], poison=False)
     with torch.no_grad():
