@@ -110,7 +110,8 @@ bool add_stream(RotaryParams* p, const void* x, const int64_t sx[3], int64_t hea
 
 constexpr int64_t kMaxHeads = 65535;
 
-int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const diffattn_axes* axes, const void* q1, const void* k1, const void* q2,
+int build_rotary(RotaryParams* p, const diffattn_rotary_desc* d, const diffattn_axes* axes, const void* q1, const void* k1,
+                 const void* q2,
                  const void* k2, const float* qw, const float* kw, const float* cos, const float* sin,
                  const void* positions, void* yq1, void* yk1, void* yq2, void* yk2) {
     const int rc = check_rotary(d, cos, sin, true);

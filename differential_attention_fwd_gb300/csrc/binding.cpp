@@ -931,7 +931,8 @@ struct CrossBackward : public torch::autograd::Node {
         if (task_should_compute_output(at[1]) || task_should_compute_output(at[3]) || task_should_compute_output(at[4]))
             for (int i : {1, 3, 4})
                 if (!(shared && i == 3)) dx[i] = fresh_tensor(t[i].sizes(), type, *dev);
-        if (tensor_lambda && task_should_compute_output(inputs)) dlam = fresh_tensor({}, d.lambda_dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev);
+        if (tensor_lambda && task_should_compute_output(inputs))
+            dlam = fresh_tensor({}, d.lambda_dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev);
         const size_t bytes = diffattn_cross_bwd_workspace_bytes(&c);
         const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
         const int rc = diffattn_cross_bwd(&c, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
@@ -1006,7 +1007,8 @@ PyObject* cross(PyObject* const* a) {
     const Tensor w = affine(a[10], "norm_weight", d.H, d.Dv, dev, &w_given);
     const Tensor b = affine(a[11], "norm_bias", d.H, d.Dv, dev, &b_given);
     no_tangent({&w_given, &b_given}, kCross);
-    if (e.norm == DIFFATTN_NORM_NONE && (w.defined() || b.defined())) bad_value("norm_weight and norm_bias need norm='rms' or 'group'");
+    if (e.norm == DIFFATTN_NORM_NONE && (w.defined() || b.defined()))
+        bad_value("norm_weight and norm_bias need norm='rms' or 'group'");
     const bool epilogue = e.norm != DIFFATTN_NORM_NONE || w.defined() || b.defined() || e.out_scale != 1.f;
     if ((grad && (epilogue || !is_none(a[7]))) || wants_grad({&w_given, &b_given}))
         bad_value("gradients are available for the bare operation only (no out=, norm or out_scale): apply "

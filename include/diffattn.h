@@ -732,8 +732,8 @@ size_t diffattn_cross_bwd_workspace_bytes(const diffattn_cross_desc *desc);
  * initialisation needed; calls that may run at the same time use different ones.
  * Errors: DIFFATTN_ERR_INVALID (NULL pointers, sizes, strides, dtype, kv_group, a stride
  * of 0 between rows of O, non-finite lambda, bad epilogue, a weight or bias without a norm,
- * an epilogue with the training outputs, a missing, small or misaligned workspace); DIFFATTN_ERR_UNSUPPORTED (sizes
- * beyond the int32 index range); DIFFATTN_ERR_CUDA.
+ * an epilogue with the training outputs, a missing, small or misaligned workspace);
+ * DIFFATTN_ERR_UNSUPPORTED (sizes beyond the int32 index range); DIFFATTN_ERR_CUDA.
  */
 int diffattn_cross_fwd(const diffattn_cross_desc *desc, const void *q1, const void *k1,
                        const void *q2, const void *k2, const void *v,
