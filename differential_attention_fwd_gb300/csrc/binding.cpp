@@ -173,6 +173,24 @@ Tensor norm_weight(PyObject* o, const char* name, int64_t heads, int64_t D, at::
     return plain_f32(w);
 }
 
+// What a node saved, for its backward pass.  A hook of saved tensors (save_on_cpu, or a user's)
+// may give it back in another layout, so strides are those of what comes back; of other sizes,
+// another type or on another device it is not what was saved.
+Tensor restored(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type, at::Device dev, const char* what) {
+    TORCH_CHECK(t.defined() && t.sizes() == sizes && t.scalar_type() == type && t.device() == dev, what,
+                ": a hook of saved tensors gave back ", t.defined() ? text(t.sizes()) : "nothing",
+                t.defined() ? std::string(" ") + at::toString(t.scalar_type()) + " on " + t.device().str() : "", " for ",
+                text(sizes), " ", at::toString(type), " on ", dev.str());
+    return t;
+}
+// The same for tensors that the kernels take dense: contiguous, from a 16-byte boundary.
+Tensor restored_dense(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type, at::Device dev, const char* what) {
+    const Tensor r = restored(t, sizes, type, dev, what);
+    return r.is_contiguous() && reinterpret_cast<uintptr_t>(r.const_data_ptr()) % 16 == 0
+               ? r
+               : r.clone(at::MemoryFormat::Contiguous);
+}
+
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
     if (!at::GradMode::is_enabled()) return false;
     for (const Tensor* t : ts)
@@ -889,9 +907,9 @@ bool on_tensor_cores(const diffattn_cross_desc& d) {
 // The autograd node: backward through diffattn_cross_bwd.  Its inputs are q1, k1, q2, k2 (not
 // where it is k1), value, and the coefficient where that is a tensor.
 struct CrossBackward : public torch::autograd::Node {
-    diffattn_cross_desc d{};
+    diffattn_cross_desc d{};                // its strides are the forward's: what is unpacked has its own
     float host = 0.f;
-    bool shared = false, tensor_lambda = false;
+    bool shared = false, tensor_lambda = false, device_lambda = false, has_lens = false;
     torch::autograd::SavedVariable x[5], lens, results[3];          // q1, k1, q2, k2, value; out, out2, lse
     torch::autograd::SavedVariable lam, lam_read;                   // as given, and as the kernels read it
     std::vector<int64_t> lam_shape;
@@ -910,18 +928,33 @@ struct CrossBackward : public torch::autograd::Node {
         const int inputs = shared ? 4 : 5;
         torch::autograd::variable_list result(inputs + tensor_lambda);
         if (!grads[0].defined()) return result;
+        const at::ScalarType type = d.dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat;
+        const bool tensor_cores = on_tensor_cores(d);
+        const c10::cuda::OptionalCUDAGuard guard(*dev);
+        const int64_t Hk = d.H / d.kv_group;
+        const int64_t rows[5][4] = {{d.B, d.H, d.Tq, d.D}, {d.B, Hk, d.Tk, d.D}, {d.B, d.H, d.Tq, d.D},
+                                    {d.B, Hk, d.Tk, d.D}, {d.B, Hk, d.Tk, d.Dv}};
         Tensor t[5];
         for (int i = 0; i < 5; ++i)
-            if (!(shared && i == 3)) t[i] = inner(x[i].unpack());
+            if (!(shared && i == 3)) t[i] = rows_for(restored(x[i].unpack(), rows[i], type, *dev, kCross), tensor_cores);
         if (shared) t[3] = t[1];
-        const Tensor out = results[0].unpack(shared_from_this()), out2 = results[1].unpack(), lse = results[2].unpack();
-        const Tensor n = lens.unpack();
-        const Tensor l = lam_read.unpack();
+        const int64_t result_rows[4] = {d.B, d.H, d.Tq, d.Dv}, sums[4] = {d.B, d.H, d.Tq, 2};
+        const Tensor out = restored_dense(results[0].unpack(shared_from_this()), result_rows, type, *dev, kCross);
+        const Tensor out2 = restored_dense(results[1].unpack(), result_rows, type, *dev, kCross);
+        const Tensor lse = restored_dense(results[2].unpack(), sums, at::kFloat, *dev, kCross);
+        const Tensor n = has_lens ? restored(lens.unpack(), d.B, at::kInt, *dev, kCross).contiguous() : Tensor();
+        Tensor l;
+        if (device_lambda)
+            l = restored(lam_read.unpack(), lam_shape, d.lambda_dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev, kCross);
         if (tensor_lambda) lam.unpack();        // checks that it was not changed in place
-        const at::ScalarType type = t[0].scalar_type();
-        const c10::cuda::OptionalCUDAGuard guard(*dev);
-        const Tensor g = rows_for(grads[0].scalar_type() == type ? grads[0] : grads[0].to(type), on_tensor_cores(d));
+        const Tensor g = rows_for(grads[0].scalar_type() == type ? grads[0] : grads[0].to(type), tensor_cores);
         diffattn_cross_desc c = d;
+        strides3(c.q1_stride, t[0]);
+        strides3(c.k1_stride, t[1]);
+        strides3(c.q2_stride, t[2]);
+        strides3(c.k2_stride, t[3]);
+        strides3(c.v_stride, t[4]);
+        strides3(c.o_stride, out);
         strides3(c.dout_stride, g);
         // position of each input among the node's
         const int at[5] = {0, 1, 2, shared ? 1 : 3, shared ? 3 : 4};
@@ -1063,10 +1096,12 @@ PyObject* cross(PyObject* const* a) {
             from.push_back(lam.given);
             node->tensor_lambda = true;
             node->lam = torch::autograd::SavedVariable(lam.given, false);
+            node->device_lambda = lam.dev.defined();
             if (lam.dev.defined()) node->lam_read = torch::autograd::SavedVariable(lam.dev, false);
             node->lam_shape = lam.given.sizes().vec();
             node->lam_options = lam.given.options();
         }
+        node->has_lens = lens.defined();
         if (lens.defined()) node->lens = torch::autograd::SavedVariable(lens, false);
         node->d = d;
         node->host = lam.host;

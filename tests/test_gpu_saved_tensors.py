@@ -1,0 +1,120 @@
+"""GPU tests of the operators' gradients where hooks of saved tensors give them back in another
+layout (save_on_cpu does): the same bits as without hooks, and an error for what was not saved."""
+import pytest
+import torch
+
+import differential_attention_fwd_gb300 as da
+from differential_attention_fwd_gb300 import build as build_mod
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build_mod.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    da.get_device_error()
+    yield
+    assert da.get_device_error() == 0
+
+
+def reversed_order(t):
+    """The first dimension innermost."""
+    order = tuple(range(t.dim()))[::-1]
+    return t.permute(order).contiguous().permute(order)
+
+
+def swapped(t):
+    """Dense, with the second and third dimensions swapped in memory."""
+    return t.transpose(1, 2).contiguous().transpose(1, 2) if t.dim() == 4 else t.clone()
+
+
+def odd_rows(t):
+    """Rows of one element more than theirs, the rest of the store NaN."""
+    if t.dim() == 0 or not t.is_floating_point():
+        return t.clone()
+    big = torch.full((*t.shape[:-1], t.shape[-1] + 1), float("nan"), dtype=t.dtype, device=t.device)
+    big[..., :-1] = t
+    return big[..., :-1]
+
+
+def shifted(t):
+    """Contiguous, but not from a 16-byte boundary."""
+    big = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    big[1:] = t.reshape(-1)
+    return big[1:].view(t.shape)
+
+
+def unpacked(f):
+    return lambda: torch.autograd.graph.saved_tensors_hooks(lambda t: t.detach(), f)
+
+
+HOOKS = {
+    "cpu": lambda: torch.autograd.graph.save_on_cpu(),
+    "pinned": lambda: torch.autograd.graph.save_on_cpu(pin_memory=True),
+    "contiguous": unpacked(lambda t: t.clone(memory_format=torch.contiguous_format)),
+    "reversed": unpacked(reversed_order),
+    "swapped": unpacked(swapped),
+    "odd": unpacked(odd_rows),
+    "shifted": unpacked(shifted),
+}
+
+
+def projected(g, dtype, layout, B, T, widths):
+    """Rows [B, heads, T, width] for each (heads, width): "token": [B, T, heads, width] seen so;
+    "fused": slices of one projection [B, T, all of them]; "dense"."""
+    if layout == "fused":
+        total = sum(h * w for h, w in widths)
+        store = torch.randn(B, T, total, generator=g).to(dtype).cuda()
+        out, at = [], 0
+        for h, w in widths:
+            out.append(store[:, :, at:at + h * w].view(B, T, h, w).transpose(1, 2))
+            at += h * w
+        return out
+    rows = [torch.randn(B, T, h, w, generator=g).to(dtype).cuda().transpose(1, 2) for h, w in widths]
+    return rows if layout == "token" else [t.contiguous() for t in rows]
+
+
+@pytest.mark.parametrize("hook", HOOKS)
+@pytest.mark.parametrize("layout", ["token", "fused", "dense"])
+@pytest.mark.parametrize("dtype,D,Dv,shared", [(BF, 64, 128, False), (BF, 64, 128, True), (BF, 128, 128, True), (F32, 32, 64, False),
+                                               (BF, 128, 128, False), (F32, 20, 33, True)])
+def test_cross_attention(hook, layout, dtype, D, Dv, shared):
+    g = torch.Generator().manual_seed(D + Dv)
+    B, H, Hk, Tq, Tk = 3, 4, 2, 70, 90
+    q1, q2 = projected(g, dtype, layout, B, Tq, [(H, D), (H, D)])
+    k1, k2, v = projected(g, dtype, layout, B, Tk, [(Hk, D), (Hk, D), (Hk, Dv)])
+    leaves = [t.detach().requires_grad_() for t in ((q1, k1, q2, v) if shared else (q1, k1, q2, k2, v))]
+    n = torch.tensor([90, 0, 33], dtype=torch.int32, device="cuda")
+    do = torch.randn(B, H, Tq, Dv, generator=g).to(dtype).cuda()
+    for lam in (torch.tensor(0.8, device="cuda"), torch.tensor(0.8, dtype=dtype, device="cuda")):
+        lam.requires_grad_()
+
+        def step():
+            x = leaves[:3] + ([leaves[1]] if shared else [leaves[3]]) + leaves[-1:]
+            return da.differential_cross_attention(*x, lam, kv_lengths=n)
+        o = step()
+        want = torch.autograd.grad(o, leaves + [lam], do)
+        with HOOKS[hook]():
+            o2 = step()
+        got = torch.autograd.grad(o2, leaves + [lam], do)
+        assert torch.equal(o, o2)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("change", [lambda t: t.cpu(), lambda t: t[..., :-1] if t.dim() else t.cpu(), lambda t: t.double()])
+def test_cross_attention_refuses_what_was_not_saved(change):
+    g = torch.Generator().manual_seed(1)
+    q1, q2 = projected(g, BF, "token", 2, 20, [(4, 64), (4, 64)])
+    k1, k2, v = projected(g, BF, "token", 2, 30, [(2, 64), (2, 64), (2, 128)])
+    leaves = [t.detach().requires_grad_() for t in (q1, k1, q2, k2, v)]
+    with unpacked(change)():
+        o = da.differential_cross_attention(*leaves, 0.8)
+    with pytest.raises(RuntimeError, match="hook of saved tensors"):
+        torch.autograd.grad(o, leaves, torch.ones_like(o))
