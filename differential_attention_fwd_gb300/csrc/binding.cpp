@@ -255,9 +255,16 @@ struct Rotary {
             !((flat && pos.size(0) == T) || (pos.dim() == 2 && pos.size(0) == B && pos.size(1) == T)))
             bad_value("positions must be an int32 or int64 tensor [T] or [B, T] = (" + std::to_string(B) + ", " +
                       std::to_string(T) + ") on the inputs' device");
-        pos64 = pos.scalar_type() == at::kLong;
-        pos_stride[0] = flat ? 0 : pos.stride(0);
-        pos_stride[1] = pos.stride(-1);
+        set_positions(pos);
+    }
+    // The positions as the kernels read them: [T] or [B, T], with axes [T, axes] or [B, T, axes].
+    void set_positions(const Tensor& p) {
+        pos = p;
+        pos64 = p.scalar_type() == at::kLong;
+        const int64_t last = axes.n ? 1 : 0;
+        pos_stride[0] = p.dim() == 1 + last ? 0 : p.stride(0);
+        pos_stride[1] = p.stride(-1 - last);
+        if (axes.n) axes.pos_stride = p.stride(-1);
     }
     // positions [T, axes] or [B, T, axes], and the pairs of each axis
     void axis_positions(PyObject* o, PyObject* sections, at::Device dev) {
@@ -284,10 +291,7 @@ struct Rotary {
             bad_value("with sections, positions must be an int32 or int64 tensor [T, axes] or [B, T, axes] = (" +
                       std::to_string(B) + ", " + std::to_string(T) + ", " + std::to_string(n) + ") on the inputs' device");
         axes.n = (int32_t)n;
-        axes.pos_stride = pos.stride(-1);
-        pos64 = pos.scalar_type() == at::kLong;
-        pos_stride[0] = flat ? 0 : pos.stride(0);
-        pos_stride[1] = pos.stride(-2);
+        set_positions(pos);
     }
     const diffattn_axes* axes_ptr() const { return axes.n ? &axes : nullptr; }
     void set_norm(PyObject* name, PyObject* e) {
@@ -313,6 +317,7 @@ struct Rotary {
     }
 };
 
+const char* const kRotary = "qk_norm_rotary";
 const char* const kRowNames[4] = {"q1", "k1", "q2", "k2"};
 
 // The strides of a descriptor's i-th tensor, in the order q1, k1, q2, k2.
@@ -373,7 +378,8 @@ struct RotaryBackward : public torch::autograd::Node {
     torch::autograd::SavedVariable x[4], w[2], tables[3];      // tables: cos, sin, positions
     bool given[4] = {}, weight[2] = {};
     // without the norm the rows themselves are not saved: the gradient does not depend on them
-    std::vector<int64_t> sizes[4];
+    std::vector<int64_t> sizes[4], pos_sizes;
+    bool has_pos = false;
     std::optional<at::Device> dev;
     bool released = false;
 
@@ -386,13 +392,14 @@ struct RotaryBackward : public torch::autograd::Node {
                     "leaf that a graph made outside the capture, on the default stream, still holds; drop that graph (or "
                     "make it on another stream), or take the gradients with torch.autograd.grad");
         Rotary c = r;
+        const c10::cuda::OptionalCUDAGuard guard(*dev);
         // unpacking checks that nothing saved was changed in place
         if (c.R > 0) {
-            c.cos = tables[0].unpack();
-            c.sin = tables[1].unpack();
+            const int64_t table[2] = {c.rows, c.R / 2};
+            c.cos = restored_dense(tables[0].unpack(), table, at::kFloat, *dev, kRotary);
+            c.sin = restored_dense(tables[1].unpack(), table, at::kFloat, *dev, kRotary);
         }
-        const Tensor pos = tables[2].unpack();
-        c.pos = pos;
+        if (has_pos) c.set_positions(restored(tables[2].unpack(), pos_sizes, c.pos64 ? at::kLong : at::kInt, *dev, kRotary));
         Tensor wt[2];
         for (int i = 0; i < 2; ++i)
             if (weight[i]) wt[i] = w[i].unpack();
@@ -405,7 +412,7 @@ struct RotaryBackward : public torch::autograd::Node {
         for (int i = 0; i < 4; ++i) {
             if (!given[i]) continue;
             if (c.norm) {
-                xs[i] = x[i].unpack();
+                xs[i] = inner(x[i].unpack());
                 strides3(row_stride(d, i), xs[i]);
             }
             Tensor g = grads[out++];
@@ -418,7 +425,6 @@ struct RotaryBackward : public torch::autograd::Node {
         for (int i = 0; i < 2; ++i)
             if (weight[i] && task_should_compute_output(out + i - (i == 1 && !weight[0])))
                 dw[i] = fresh_tensor((i ? c.kw : c.qw).sizes(), at::kFloat, *dev);
-        const c10::cuda::OptionalCUDAGuard guard(*dev);
         const size_t bytes = diffattn_rotary_bwd_workspace_bytes(&d);
         const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
         const int rc = diffattn_rotary_axes_bwd(
@@ -518,7 +524,11 @@ PyObject* rotary(PyObject* const* a) {
             node->tables[0] = torch::autograd::SavedVariable(r.cos, false);
             node->tables[1] = torch::autograd::SavedVariable(r.sin, false);
         }
-        if (r.pos.defined()) node->tables[2] = torch::autograd::SavedVariable(r.pos, false);
+        if (r.pos.defined()) {
+            node->has_pos = true;
+            node->pos_sizes = r.pos.sizes().vec();
+            node->tables[2] = torch::autograd::SavedVariable(r.pos, false);
+        }
         node->set_next_edges(torch::autograd::collect_next_edges(from));
         for (Tensor& t : y)
             if (t.defined()) torch::autograd::set_history(t, node);

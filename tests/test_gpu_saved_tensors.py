@@ -118,3 +118,55 @@ def test_cross_attention_refuses_what_was_not_saved(change):
         o = da.differential_cross_attention(*leaves, 0.8)
     with pytest.raises(RuntimeError, match="hook of saved tensors"):
         torch.autograd.grad(o, leaves, torch.ones_like(o))
+
+
+def spread(t):
+    """Whole numbers as every other element of a larger store, the rest out of range."""
+    if t.is_floating_point():
+        return t.clone()
+    big = torch.full((*t.shape[:-1], 2 * t.shape[-1]), 2 ** 30, dtype=t.dtype, device=t.device)
+    big[..., ::2] = t
+    return big[..., ::2]
+
+
+DENSE_HOOKS = {**{k: HOOKS[k] for k in ("cpu", "pinned", "contiguous", "reversed", "swapped")}, "spread": unpacked(spread)}
+
+
+@pytest.mark.parametrize("hook", DENSE_HOOKS)
+@pytest.mark.parametrize("sections", [None, (8, 12, 12), (3, 18, 11)])
+@pytest.mark.parametrize("batched", [False, True])
+@pytest.mark.parametrize("dtype,whole", [(BF, torch.int64), (F32, torch.int32)])
+def test_norm_and_rotation(hook, sections, batched, dtype, whole):
+    """Positions as views: [axes, (B,) T] seen with the axes last, every third of a longer row."""
+    g = torch.Generator().manual_seed(7)
+    B, T, H, Hk, D = 2, 37, 4, 2, 64
+    q1, k1, q2, k2 = (t.detach().requires_grad_() for t in projected(g, dtype, "token", B, T, [(H, D), (Hk, D), (H, D), (Hk, D)]))
+    store = torch.randint(0, 90, (3, B, 3 * T), generator=g).to(whole).cuda()
+    positions = (store if sections else store[:1])[:, :, ::3]
+    positions = positions if batched else positions[:, 1]
+    positions = positions.permute(*range(1, positions.dim()), 0) if sections else positions[0]
+    cos, sin = da.rotary_tables(90, D, device="cuda", sections=sections)
+    w = (1 + 0.2 * torch.randn(H, D, generator=g)).cuda().requires_grad_()
+    leaves = [q1, k1, q2, k2, w]
+
+    def step():
+        return da.qk_norm_rotary(q1, k1, q2, k2, cos, sin, positions, q_weight=w, sections=sections)
+    do = [torch.randn(t.shape, generator=g).to(dtype).cuda() for t in leaves[:4]]
+    want = torch.autograd.grad(step(), leaves, do)
+    with DENSE_HOOKS[hook]():
+        y = step()
+    for a, b in zip(torch.autograd.grad(y, leaves, do), want):
+        assert torch.equal(a, b)
+
+
+def test_norm_and_rotation_refuses_positions_that_were_not_saved():
+    g = torch.Generator().manual_seed(8)
+    q1, k1 = (t.detach().requires_grad_() for t in projected(g, BF, "token", 2, 9, [(4, 64), (2, 64)]))
+    cos, sin = da.rotary_tables(20, 64, device="cuda")
+    positions = torch.arange(9, device="cuda")
+    for change in (lambda t: t if t.is_floating_point() else t.cpu(), lambda t: t if t.is_floating_point() else t[:5],
+                   lambda t: t if t.is_floating_point() else t.int(), lambda t: t if t.shape != cos.shape else t[:3]):
+        with unpacked(change)():
+            y = da.qk_norm_rotary(q1, k1, None, None, cos, sin, positions)
+        with pytest.raises(RuntimeError, match="hook of saved tensors"):
+            torch.autograd.grad(y[:2], (q1, k1), (torch.ones_like(q1), torch.ones_like(k1)))
