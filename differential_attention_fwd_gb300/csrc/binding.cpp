@@ -378,7 +378,8 @@ struct RotaryBackward : public torch::autograd::Node {
     torch::autograd::SavedVariable x[4], w[2], tables[3];      // tables: cos, sin, positions
     bool given[4] = {}, weight[2] = {};
     // without the norm the rows themselves are not saved: the gradient does not depend on them
-    std::vector<int64_t> sizes[4], pos_sizes;
+    std::vector<int64_t> sizes[4], pos_sizes, w_sizes[2];
+    at::ScalarType w_type[2] = {};
     bool has_pos = false;
     std::optional<at::Device> dev;
     bool released = false;
@@ -402,7 +403,7 @@ struct RotaryBackward : public torch::autograd::Node {
         if (has_pos) c.set_positions(restored(tables[2].unpack(), pos_sizes, c.pos64 ? at::kLong : at::kInt, *dev, kRotary));
         Tensor wt[2];
         for (int i = 0; i < 2; ++i)
-            if (weight[i]) wt[i] = w[i].unpack();
+            if (weight[i]) wt[i] = restored(w[i].unpack(), w_sizes[i], w_type[i], *dev, kRotary);
         if (weight[0]) c.qw = plain_f32(wt[0]);
         if (weight[1]) c.kw = plain_f32(wt[1]);
         diffattn_rotary_desc d = c.desc();
@@ -412,7 +413,7 @@ struct RotaryBackward : public torch::autograd::Node {
         for (int i = 0; i < 4; ++i) {
             if (!given[i]) continue;
             if (c.norm) {
-                xs[i] = inner(x[i].unpack());
+                xs[i] = inner(restored(x[i].unpack(), sizes[i], type, *dev, kRotary));
                 strides3(row_stride(d, i), xs[i]);
             }
             Tensor g = grads[out++];
@@ -518,6 +519,8 @@ PyObject* rotary(PyObject* const* a) {
             node->weight[i] = ws[i].defined();
             if (!ws[i].defined()) continue;
             from.push_back(ws[i]);
+            node->w_sizes[i] = ws[i].sizes().vec();
+            node->w_type[i] = ws[i].scalar_type();
             node->w[i] = torch::autograd::SavedVariable(ws[i], false);
         }
         if (r.R > 0) {
@@ -581,6 +584,8 @@ Tensor affine(PyObject* o, const char* name, int64_t H, int64_t C, at::Device de
     return plain_f32(t);
 }
 
+const char* const kHeadNorm = "differential_head_norm";
+
 // The autograd node: backward through diffattn_head_norm_bwd.  Its inputs are x, then the
 // weight and the bias where they were given.
 struct HeadNormBackward : public torch::autograd::Node {
@@ -602,10 +607,11 @@ struct HeadNormBackward : public torch::autograd::Node {
                     "or make it on another stream");
         torch::autograd::variable_list result(1 + has[0] + has[1]);
         if (!grads[0].defined()) return result;
-        const Tensor xs = inner(x.unpack());
-        const Tensor ws = has[0] ? plain_f32(w.unpack()) : Tensor();
-        const Tensor g = inner(grads[0].scalar_type() == xs.scalar_type() ? grads[0] : grads[0].to(xs.scalar_type()));
         const c10::cuda::OptionalCUDAGuard guard(*dev);
+        const int64_t sizes[4] = {d.B, d.H, d.T, d.C};
+        const Tensor xs = inner(restored(x.unpack(), sizes, d.dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev, kHeadNorm));
+        const Tensor ws = has[0] ? plain_f32(restored(w.unpack(), shape[0], type[0], *dev, kHeadNorm)) : Tensor();
+        const Tensor g = inner(grads[0].scalar_type() == xs.scalar_type() ? grads[0] : grads[0].to(xs.scalar_type()));
         diffattn_norm_desc c = d;
         Tensor dx, da[2];
         if (task_should_compute_output(0)) dx = fresh_like(xs);

@@ -170,3 +170,34 @@ def test_norm_and_rotation_refuses_positions_that_were_not_saved():
             y = da.qk_norm_rotary(q1, k1, None, None, cos, sin, positions)
         with pytest.raises(RuntimeError, match="hook of saved tensors"):
             torch.autograd.grad(y[:2], (q1, k1), (torch.ones_like(q1), torch.ones_like(k1)))
+
+
+@pytest.mark.parametrize("change", [lambda t: t.cpu(), lambda t: t[:1], lambda t: t.double()])
+@pytest.mark.parametrize("which", ["rows", "weight"])
+def test_rows_and_weights_that_were_not_saved(change, which):
+    g = torch.Generator().manual_seed(9)
+    x, = (t.detach().requires_grad_() for t in projected(g, BF, "token", 2, 9, [(4, 64)]))
+    w = torch.ones(4, 64, device="cuda", requires_grad=True)
+    only = lambda t: change(t) if (t.dim() == 4) == (which == "rows") else t            # noqa: E731
+    for f in (lambda: da.qk_norm_rotary(x, None, None, None, None, None, q_weight=w)[0],
+              lambda: da.differential_head_norm(x, norm_weight=w)):
+        with unpacked(only)():
+            y = f()
+        with pytest.raises(RuntimeError, match="hook of saved tensors"):
+            torch.autograd.grad(y, (x, w), torch.ones_like(y))
+
+
+@pytest.mark.parametrize("hook", ["cpu", "pinned", "contiguous", "reversed", "swapped"])
+@pytest.mark.parametrize("layout", ["token", "fused", "dense"])
+@pytest.mark.parametrize("dtype,norm", [(BF, "rms"), (BF, "group"), (F32, "group")])
+def test_head_norm(hook, layout, dtype, norm):
+    g = torch.Generator().manual_seed(10)
+    x, _ = (t.detach().requires_grad_() for t in projected(g, dtype, layout, 3, 50, [(4, 128), (2, 64)]))
+    w, b = ((1 + 0.2 * torch.randn(4, 128, generator=g)).cuda().requires_grad_() for _ in range(2))
+    do = torch.randn(x.shape, generator=g).to(dtype).cuda()
+    f = lambda: da.differential_head_norm(x, norm=norm, norm_weight=w, norm_bias=b, out_scale=0.2)      # noqa: E731
+    want = torch.autograd.grad(f(), (x, w, b), do)
+    with HOOKS[hook]():
+        y = f()
+    for a, c in zip(torch.autograd.grad(y, (x, w, b), do), want):
+        assert torch.equal(a, c)
