@@ -945,12 +945,17 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
 #pragma unroll
                     for (int c = 0; c < 64; ++c) part += r[c];
                 }
-                stat[br * BM + row] = part;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[BAR_NORM_A]);
-                if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_NORM_A], naph, ab)))) break;
-                naph ^= 1;
-                const float tot = stat[row] + stat[BM + row];
+                // (A row without a state needs no exchange, its halves are alike.  And there must be
+                // none: what orders the sums' next writes after their reads here is an item's products,
+                // which such an item does not have.)
+                if (!none) {
+                    stat[br * BM + row] = part;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[BAR_NORM_A]);
+                    if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_NORM_A], naph, ab)))) break;
+                    naph ^= 1;
+                }
+                const float tot = none ? 2.f * part : stat[row] + stat[BM + row];
                 float mu = 0.f, rinv;
                 if (p.norm == kNormRms) {
                     rinv = rsqrtf(tot * (1.0f / VD) + p.norm_eps);
@@ -959,12 +964,14 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     float dev = 0.f;
 #pragma unroll
                     for (int c = 0; c < 64; ++c) dev = fmaf(r[c] - mu, r[c] - mu, dev);
-                    stat[2 * BM + br * BM + row] = dev;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[BAR_NORM_B]);
-                    if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_NORM_B], nbph, ab)))) break;
-                    nbph ^= 1;
-                    const float var = (stat[2 * BM + row] + stat[3 * BM + row]) * (1.0f / VD);
+                    if (!none) {
+                        stat[2 * BM + br * BM + row] = dev;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[BAR_NORM_B]);
+                        if (!(ok = TIMED_WAIT(wp, kWaitPeer, mbar_wait_warp(&bars[BAR_NORM_B], nbph, ab)))) break;
+                        nbph ^= 1;
+                    }
+                    const float var = (none ? 2.f * dev : stat[2 * BM + row] + stat[3 * BM + row]) * (1.0f / VD);
                     rinv = rsqrtf(var + p.norm_eps);
                 }
                 const float* wrow = p.norm_weight ? p.norm_weight + h * VD + c0 : nullptr;

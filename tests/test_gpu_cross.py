@@ -229,6 +229,29 @@ def test_epilogue(dtype, D, Dv, norm, Tq):
     check("y", y, want, 0.2 * (w.abs() * tol + 4 * ref.U * (b.abs() + (o * w).abs())) + r.h * want.abs())
 
 
+@pytest.mark.parametrize("norm", ["rms", "group"])
+@pytest.mark.parametrize("D,shared", [(64, False), (128, True)])
+@pytest.mark.parametrize("H,Hk,Tq", [(16, 16, 130), (16, 4, 20)])
+def test_norm_between_sequences_without_states(norm, D, shared, H, Hk, Tq):
+    """Several items an SM, with sequences of no state before and after each that has some: the rows
+    have the bits of a call over the latter alone."""
+    B = 96
+    lens = [64 if b % 3 == 1 else 0 for b in range(B)]
+    x, n = inputs(22, BF, B, H, Hk, Tq, 70, D, 128, shared, lens)
+    some = [b for b in range(B) if lens[b]]
+    y = [t[some].contiguous() for t in x]
+    if shared:
+        y[3] = y[1]
+    w, b = 1 + torch.arange(H * 128, device="cuda").reshape(H, 128) / 1000, torch.ones(H, 128, device="cuda")
+    kw = dict(norm=norm, norm_weight=w, norm_bias=b, out_scale=0.5)
+    with torch.no_grad():
+        want = da.differential_cross_attention(*y, 0.8, kv_lengths=n[some].contiguous(), **kw)
+        for _ in range(20):
+            got = da.differential_cross_attention(*x, 0.8, kv_lengths=n, **kw)
+            assert torch.equal(got[some], want)
+            assert (got[[b for b in range(B) if not lens[b]]] == 0.5).all()
+
+
 def test_one_answer_for_full_lengths_and_none():
     for dtype, D, Dv in ((BF, 64, 128), (F32, 64, 128)):
         for Tq in (1, 40):
