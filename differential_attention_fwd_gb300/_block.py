@@ -32,11 +32,12 @@ def differential_cross_attention(q1: torch.Tensor, k1: torch.Tensor, q2: torch.T
     epilogue (norm .. out_scale) as differential_attention, norm_weight and norm_bias with a
     norm alone; out may not overlap the inputs.
 
-    Returns [B, H, Tq, Dv].  Differentiable in q1, q2, k1, k2, value and a tensor coefficient,
-    backward and once, without out and the epilogue (differential_head_norm has gradients);
-    states that a sequence does not have get zeros.  What qk_norm_rotary says of captured
-    backward passes and of forward mode holds here too.  A length outside 0 .. Tk gives that
-    sequence rows (and gradients) of NaN and is reported by get_device_error."""
+    Returns [B, H, Tq, Dv].  In bfloat16 the weights keep 16 bits on every path, so that what
+    branches that cancel leave is off by its own rounding alone.  Differentiable in q1, q2, k1,
+    k2, value and a tensor coefficient, backward and once, without out and the epilogue
+    (differential_head_norm has gradients); states that a sequence does not have get zeros.  What
+    qk_norm_rotary says of captured backward passes and of forward mode holds here too.  A
+    length outside 0 .. Tk gives that sequence rows (and gradients) of NaN and is reported by get_device_error."""
     return (_paged._native or _paged._load()).cross(q1, k1, q2, k2, value, coefficient, kv_lengths, out, norm, norm_eps,
                                                     norm_weight, norm_bias, out_scale)
 

@@ -146,7 +146,7 @@ bool tc_inputs(const diffattn_cross_desc& d, const void* q1, const void* k1, con
 // A short head's rows, a power of two and at least 8 (what a swizzled tile's rows repeat in), and
 // how many heads of a group the tensor-core forward's items take together: as few as leave one
 // item an SM, if they fit into 128 rows.  16 sequences of 1500 states, 32 rows of 16 over 4 heads:
-// 20 us with two heads an item, 41 with one.
+// 24 us with two heads an item, 43 with one.
 int short_rows_log2(int64_t Tq) {
     int s = 3;
     while (s < 7 && (int64_t(1) << s) < Tq) ++s;
@@ -162,20 +162,21 @@ int packed_heads(int64_t B, int64_t H, int64_t group, int64_t Tq) {
 // What the tensor-core forward takes for sequences of Tk states, about, in us.
 double whole_us(int64_t B, int64_t H, int64_t group, int64_t Tq, int64_t Tk, int64_t D) {
     const double items = (double)B * H / packed_heads(B, H, group, Tq) * ((Tq + 127) / 128), tiles = (double)((Tk + 63) / 64);
-    return 5 + std::ceil(items / 152) * tiles * (D == 64 ? 0.63 : 0.92);
+    return 5 + std::ceil(items / 152) * tiles * (D == 64 ? 0.70 : 0.96);
 }
 
 // Whether the kernels of the paged cache take a serving call.  They divide the states of all
 // sequences evenly over the SMs and join the parts in a second launch, where the forward's
 // blocks each walk a whole sequence for 128 rows.  By estimates, in us, for lengths of Tk, from
 // what either measured (bf16; the forward, then the split):
-//   one sequence, 16 heads of 64, 32 rows:   77 states 6.8, 15.9; 1500 19.9, 20.3; 6000 62, 29.5
-//   16 sequences, the same:                  77 states 16.2, 23.5; 1500 47, 74; 6000 142, 180
-//   16 sequences, 16 over 4 heads, one row:  77 states 7.7, 14.2; 1500 19.8, 21.2; 6000 63, 44
-//   the same, 32 rows:                       77 states 7.6, 20.9; 1500 19.9, 39; 6000 64, 69
-//   the V2 head, 16 over 8 heads, 64 rows:   77 states 7.3, 17.8; 1500 23, 30; 6000 84, 37
-//   16 sequences, the same:                  1500 states 29.6, 56; 6000 93, 116
-//   4 sequences, 64 over 4 heads, 4 rows:    3000 states 32.7, 25.5
+//   one sequence, 16 heads of 64, 32 rows:   77 states 6.3, 15.0; 1500 22.0, 19.3; 6000 71, 28
+//   16 sequences, the same:                  77 states 11.1, 21.7; 1500 47, 69; 6000 158, 175
+//   16 sequences, 16 heads, one row:         1500 states 46.3, 44.3; of two thirds on average 36.0, 38.1
+//   16 sequences, 16 over 4 heads, one row:  77 states 8.0, 14.1; 1500 24.2, 23.3; 6000 74, 48
+//   the same, 32 rows:                       77 states 8.0, 20.9; 1500 24.9, 41; 6000 75, 69
+//   the V2 head, 16 over 8 heads, 64 rows:   77 states 6.7, 16.7; 1500 25.7, 28.7; 6000 95, 33
+//   16 sequences, the same:                  1500 states 33.3, 56; 6000 106, 115
+//   4 sequences, 64 over 4 heads, 4 rows:    3000 states 40.3, 25.7
 // Up to 16 rows a key/value head the split is bound by HBM, beyond by its products and starts.
 bool wants_split(const diffattn_cross_desc& d) {
     if (!cross_paged_ok(d)) return false;
@@ -190,9 +191,9 @@ bool wants_split(const diffattn_cross_desc& d) {
         return 20 + units * 2 * tiles / (4 * SMS) * 3 < whole;
     }
     const double bytes = (double)d.B * Hk * d.Tk * 512;     // of a state's keys (the V2 head's: one tensor) and value
-    const double least = 5 + bytes / 5.5e6, by_tiles = whole_us(d.B, d.H, group_of(d), d.Tq, d.Tk, d.D);
+    const double least = 5 + bytes / 5.0e6, by_tiles = whole_us(d.B, d.H, group_of(d), d.Tq, d.Tk, d.D);
     const double whole = by_tiles > least ? by_tiles : least;
-    if (rows <= 16) return 12.5 + bytes / 5.2e6 * (rows > 8 ? 1.5 : 1.0) < whole;
+    if (rows <= 16) return 12.5 + bytes / 5.6e6 * (rows > 8 ? 1.5 : 1.0) < whole;
     const int64_t head_rows = (d.Tq + 7) / 8 * 8;
     const double chunks = d.Tq <= 128 ? std::ceil(group_of(d) / std::floor(128.0 / head_rows))
                                       : (double)group_of(d) * ((d.Tq + 127) / 128);

@@ -66,8 +66,8 @@
 // written by the softmax warps alone.  Where a head has few rows and a key/value head several
 // heads, an item takes the rows of some of them (p.pack: 8, 16, 32 or 64 rows each).
 // Instances of their own: the others keep their code.
-// 2 x 16 heads, 4096 rows over 4096 states: D = 64 289 us (1428 TFLOP/s), the V2 head 359 us
-// (1531), bound as the others by the hand-offs between the softmax and the products.
+// 2 x 16 heads, 4096 rows over 4096 states: D = 64 373 us (1105 TFLOP/s of the operation's, 1842 of
+// the products, 0.95 of cuBLAS's rate), the V2 head 444 us (1238, 1857): bound by the tensor cores.
 //
 // Streaming softmax: the running max m is kept in log2 units of the scaled
 // scores.  O and l are rescaled only when a tile's row max exceeds m by more
@@ -324,10 +324,10 @@ __device__ __forceinline__ float tile_row_max(const float (&s)[64]) {
 
 // P = 2^(s * scale_log2 - m) for one thread's 64 scores, two columns per
 // packed operation: P rounded to bf16 pairs into pk, and the sum of the
-// unrounded P returned.  The first REST pairs' rounded rests go into rest.
-template <int REST>
+// unrounded P returned.  TWO: what the rounding leaves of each goes into rest.
+template <bool TWO>
 __device__ __forceinline__ float tile_exp2(const float (&s)[64], float sl2, float m, uint32_t (&pk)[32],
-                                           uint32_t (&rest)[REST > 0 ? REST : 1]) {
+                                           uint32_t (&rest)[TWO ? 32 : 1]) {
     const uint64_t scale2 = f2_pack(sl2, sl2);
     const uint64_t negm2 = f2_pack(-m, -m);
     uint64_t rsum[4] = {0, 0, 0, 0};     // four short addition chains
@@ -338,7 +338,7 @@ __device__ __forceinline__ float tile_exp2(const float (&s)[64], float sl2, floa
         const float p1 = ex2_approx(f2_hi(x));
         rsum[c & 3] = f2_add(rsum[c & 3], f2_pack(p0, p1));
         pk[c] = pack_bf16x2(p0, p1);
-        if (c < REST) {
+        if constexpr (TWO) {
             const uint64_t r = f2_sub(f2_pack(p0, p1), f2_from_bits(pk[c] << 16, pk[c] & 0xffff0000u));
             rest[c] = pack_bf16x2(f2_lo(r), f2_hi(r));
         }
@@ -347,14 +347,13 @@ __device__ __forceinline__ float tile_exp2(const float (&s)[64], float sl2, floa
     return f2_lo(r) + f2_hi(r);
 }
 
-// CROSS: the weights of so many of a tile's four k-steps (16 keys each) enter the product
-// with V in two bf16 parts.  The branches' weights of a key cancel in part, their roundings
-// do not: with none O is off by 2.64e-3 of its size (N(0, 1) inputs, lambda = 0.8; its own
-// rounding is 1.66e-3 of that), with one by 2.42e-3, with two by 2.20e-3, with all four by
-// 1.66e-3.  One keeps the whole below 1.5 of the output's own rounding, for 6 % of the time
-// on the DIFF V2 head and 3 % at D = 64 (4 x 4099 over 1500 states: 184, 196, 208, 232 us with
-// 0, 1, 2, 4; 4 x 2047 over 4096: 213, 220, 240, 271).
-constexpr int SECOND_STEPS = 1;
+// CROSS: the weights enter the product with V in two bf16 parts, as in the kernels of the paged
+// cache, which take the same calls where they are faster.  The branches' weights of a key cancel, and
+// the more the better the operation does what it is for; their roundings do not.  With one part O
+// is off by 2.64e-3 of its size for independent branches (N(0, 1) inputs, lambda = 0.8; its own
+// rounding is 1.66e-3), and by 7.5e-3 for ones whose queries differ by a fifth; with two by 1.66e-3 for
+// both.  The second parts' products are three tenths of the tensor core's work at D = 64, a quarter
+// with the V2 head's.
 template <int HD, bool CROSS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
@@ -591,7 +590,7 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     mma_ts(d_o, pa + kk * 8, vd + 128 * kk, IDESC_PV, (acc || kk > 0) ? 1u : 0u);
                 if constexpr (CROSS)
 #pragma unroll
-                    for (int kk = 0; kk < SECOND_STEPS; ++kk) mma_ts(d_o, pa + 32 + kk * 8, vd + 128 * kk, IDESC_PV, 1u);
+                    for (int kk = 0; kk < BN / 16; ++kk) mma_ts(d_o, pa + 32 + kk * 8, vd + 128 * kk, IDESC_PV, 1u);
             };
 
             bool first = true;
@@ -768,13 +767,12 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                 float alpha = 1.0f;
                 bool rescale = false;
                 if (j == 0) m_run = tile_row_max(s) * sl2;
-                constexpr int REST = CROSS ? 8 * SECOND_STEPS : 0;
-                uint32_t pk[32], rest[REST > 0 ? REST : 1];
-                float tsum = tile_exp2<REST>(s, sl2, m_run, pk, rest);
+                uint32_t pk[32], rest[CROSS ? 32 : 1];
+                float tsum = tile_exp2<CROSS>(s, sl2, m_run, pk, rest);
                 // P goes to TMEM at once; the sum check overlaps the store,
                 // and a rescale (rare) stores the recomputed P over it.
                 tmem_st32(tS, &pk[0]);
-                if constexpr (REST > 0) tmem_st<REST>(tS + 32, rest);
+                if constexpr (CROSS) tmem_st32(tS + 32, rest);
                 if (j > 0 && __any_sync(0xffffffffu, !(tsum <= 256.0f))) {
                     const float mxs = tile_row_max(s) * sl2;
                     if (__any_sync(0xffffffffu, mxs > m_run + 8.0f)) {
@@ -783,10 +781,10 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                         l *= alpha;
                         m_run = m_new;
                         rescale = true;
-                        tsum = tile_exp2<REST>(s, sl2, m_run, pk, rest);
+                        tsum = tile_exp2<CROSS>(s, sl2, m_run, pk, rest);
                         tmem_wait_st();
                         tmem_st32(tS, &pk[0]);
-                        if constexpr (REST > 0) tmem_st<REST>(tS + 32, rest);
+                        if constexpr (CROSS) tmem_st32(tS + 32, rest);
                     }
                 }
                 if (rescale) {

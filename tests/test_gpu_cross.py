@@ -229,6 +229,37 @@ def test_epilogue(dtype, D, Dv, norm, Tq):
     check("y", y, want, 0.2 * (w.abs() * tol + 4 * ref.U * (b.abs() + (o * w).abs())) + r.h * want.abs())
 
 
+@pytest.mark.parametrize("D,shared", [(64, False), (64, True), (128, True)])
+@pytest.mark.parametrize("Tq,Tk", [(1, 300), (1, 4000), (9, 4000), (40, 300), (200, 300), (200, 64)])
+@pytest.mark.parametrize("kind", ["alike", "late keys"])
+def test_weights_in_two_parts(D, shared, Tq, Tk, kind):
+    """On every route O is off by its own rounding and little else: each weight by 2^-16 (two bf16
+    parts, half a step 2^-8 each), with branches that cancel, and with rows that attend to the
+    keys 16 to 63 of each 64."""
+    lens = [Tk, Tk // 4]
+    x, n = inputs(23, BF, 2, 4, 2, Tq, Tk, D, 128, shared, lens)
+    g = torch.Generator().manual_seed(24)
+    if kind == "alike":
+        x[0] = (2 * x[0]).contiguous()
+        x[2] = x[0] + (0.2 * torch.randn(x[0].shape, generator=g)).to(BF).cuda()
+        if not shared:
+            x[3] = x[1] + (0.2 * torch.randn(x[1].shape, generator=g)).to(BF).cuda()
+    else:                                           # a direction that queries share and late keys have
+        u = torch.randn(D, generator=g).cuda()
+        x[0], x[2] = (x[0] + u).to(BF), (x[2] + u).to(BF)
+        late = (torch.arange(Tk, device="cuda") % 64 >= 16)[:, None] * (6 * D ** 0.5 / u.square().sum() * u)
+        x[1] = (x[1] + late).to(BF)
+        x[3] = x[1] if shared else (x[3] + late).to(BF)
+    lam = float(torch.tensor(0.8))
+    with torch.no_grad():
+        got = da.differential_cross_attention(*x, lam, kv_lengths=n)
+    clean = [torch.nan_to_num(d64(t), 0.0, 0.0, 0.0) for t in x]
+    want = ref.Cross(*clean, lam, lens, 2.0 ** -16)
+    check("o", got, want.o, want.o_tol + 2.0 ** -8 * want.o.abs())
+    o, _ = train(x, n, lam, torch.ones(2, 4, Tq, 128, dtype=BF, device="cuda"))
+    check("training o", o, want.o, want.o_tol + 2.0 ** -8 * want.o.abs())
+
+
 @pytest.mark.parametrize("norm", ["rms", "group"])
 @pytest.mark.parametrize("D,shared", [(64, False), (128, True)])
 @pytest.mark.parametrize("H,Hk,Tq", [(16, 16, 130), (16, 4, 20)])
