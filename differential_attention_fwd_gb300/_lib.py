@@ -51,8 +51,10 @@ EXPORTED = (
     "diffattn_paged_decode",
     "diffattn_paged_workspace_bytes",
     "diffattn_cross_fwd",
+    "diffattn_cross_fwd_ex",
     "diffattn_cross_workspace_bytes",
     "diffattn_cross_bwd",
+    "diffattn_cross_bwd_ex",
     "diffattn_cross_bwd_workspace_bytes",
     "diffattn_head_norm",
     "diffattn_head_norm_bwd",
@@ -242,6 +244,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_cross_fwd.restype = ctypes.c_int
     lib.diffattn_cross_bwd.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 12 + [ctypes.c_size_t, vp]
     lib.diffattn_cross_bwd.restype = ctypes.c_int
+    lib.diffattn_cross_fwd_ex.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 7 + [ctypes.c_size_t, vp]
+    lib.diffattn_cross_fwd_ex.restype = ctypes.c_int
+    lib.diffattn_cross_bwd_ex.argtypes = [vp] * 7 + [ctypes.c_float] + [vp] * 13 + [ctypes.c_size_t, vp]
+    lib.diffattn_cross_bwd_ex.restype = ctypes.c_int
     for f in (lib.diffattn_cross_workspace_bytes, lib.diffattn_cross_bwd_workspace_bytes):
         f.argtypes = [vp]
         f.restype = ctypes.c_size_t

@@ -264,6 +264,7 @@ int forward_tc(const CrossParams& c, int sms, void* counter, cudaStream_t stream
     p.k_shared = c.k_shared;
     p.out2 = static_cast<__nv_bfloat16*>(c.out2);
     p.lse = c.lse;
+    p.rests = static_cast<__nv_bfloat16*>(c.rests);
     p.lengths = c.lengths;
     const int grid = p.total_items < sms ? p.total_items : sms;
     // Long calls claim their items from a counter, since sequences differ in length.  To zero it
@@ -304,6 +305,7 @@ int backward_tc(const CrossParams& c, int sms, float* parts, cudaStream_t stream
     p.sched = c.counters;
     p.out = static_cast<const __nv_bfloat16*>(c.out);
     p.out2 = static_cast<const __nv_bfloat16*>(c.out2);
+    p.rests = static_cast<const __nv_bfloat16*>(c.rests);
     p.dout = static_cast<const __nv_bfloat16*>(c.dout);
     copy3(p.s_o, c.s_o);
     copy3(p.s_do, c.s_do);
@@ -349,12 +351,21 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
                        const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev,
                        const diffattn_epilogue* epi, void* out, void* out2, float* lse, void* workspace,
                        size_t workspace_bytes, diffattn_stream_t stream) {
+    return diffattn_cross_fwd_ex(desc, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev, epi, out, out2, lse, nullptr,
+                                 workspace, workspace_bytes, stream);
+}
+
+int diffattn_cross_fwd_ex(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
+                          const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev,
+                          const diffattn_epilogue* epi, void* out, void* out2, float* lse, void* rests, void* workspace,
+                          size_t workspace_bytes, diffattn_stream_t stream) {
     int rc = check_cross(desc);
     if (rc != DIFFATTN_OK) return rc;
     const diffattn_cross_desc& d = *desc;
     const int64_t rows[3] = {d.B, d.H, d.Tq};
     if (!q1 || !k1 || !q2 || !k2 || !v || !out || (out2 != nullptr) != (lse != nullptr) || !apart(rows, d.o_stride))
         return DIFFATTN_ERR_INVALID;
+    if (rests && (!out2 || d.dtype != DIFFATTN_BF16 || !aligned16(rests))) return DIFFATTN_ERR_INVALID;
     if (!lambda_dev && !std::isfinite(lambda)) return DIFFATTN_ERR_INVALID;
     diffattn_epilogue e;
     rc = check_epilogue(epi, &e);
@@ -367,6 +378,7 @@ int diffattn_cross_fwd(const diffattn_cross_desc* desc, const void* q1, const vo
     p.out = out;
     p.out2 = out2;
     p.lse = lse;
+    p.rests = rests;
     p.norm = e.norm;
     p.norm_eps = e.eps;
     p.norm_weight = e.weight;
@@ -388,9 +400,19 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
                        const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev, const void* out,
                        const void* out2, const float* lse, const void* dout, void* dq1, void* dk1, void* dq2, void* dk2,
                        void* dv, void* dlambda, void* workspace, size_t workspace_bytes, diffattn_stream_t stream) {
+    return diffattn_cross_bwd_ex(desc, q1, k1, q2, k2, v, kv_lengths, lambda, lambda_dev, out, out2, lse, nullptr, dout, dq1,
+                                 dk1, dq2, dk2, dv, dlambda, workspace, workspace_bytes, stream);
+}
+
+int diffattn_cross_bwd_ex(const diffattn_cross_desc* desc, const void* q1, const void* k1, const void* q2, const void* k2,
+                          const void* v, const int32_t* kv_lengths, float lambda, const void* lambda_dev, const void* out,
+                          const void* out2, const float* lse, const void* rests, const void* dout, void* dq1, void* dk1,
+                          void* dq2, void* dk2, void* dv, void* dlambda, void* workspace, size_t workspace_bytes,
+                          diffattn_stream_t stream) {
     int rc = check_cross(desc);
     if (rc != DIFFATTN_OK) return rc;
     const diffattn_cross_desc& d = *desc;
+    if (rests && (d.dtype != DIFFATTN_BF16 || !aligned16(rests))) return DIFFATTN_ERR_INVALID;
     if (!q1 || !k1 || !q2 || !k2 || !v || !out || !out2 || !lse || !dout) return DIFFATTN_ERR_INVALID;
     if (!lambda_dev && !std::isfinite(lambda)) return DIFFATTN_ERR_INVALID;
     if (!dq1 && !dq2 && !dv && !dlambda) return DIFFATTN_ERR_INVALID;
@@ -403,6 +425,7 @@ int diffattn_cross_bwd(const diffattn_cross_desc* desc, const void* q1, const vo
     p.out = const_cast<void*>(out);
     p.out2 = const_cast<void*>(out2);
     p.lse = const_cast<float*>(lse);
+    p.rests = const_cast<void*>(rests);
     p.dout = dout;
     p.dq1 = dq1;
     p.dk1 = dk1;

@@ -926,7 +926,7 @@ struct CrossBackward : public torch::autograd::Node {
     diffattn_cross_desc d{};                // its strides are the forward's: what is unpacked has its own
     float host = 0.f;
     bool shared = false, tensor_lambda = false, device_lambda = false, has_lens = false;
-    torch::autograd::SavedVariable x[5], lens, results[3];          // q1, k1, q2, k2, value; out, out2, lse
+    torch::autograd::SavedVariable x[5], lens, results[4];  // q1, k1, q2, k2, value; out, out2, lse, rests
     torch::autograd::SavedVariable lam, lam_read;                   // as given, and as the kernels read it
     std::vector<int64_t> lam_shape;
     std::optional<at::TensorOptions> lam_options;
@@ -958,6 +958,9 @@ struct CrossBackward : public torch::autograd::Node {
         const Tensor out = restored_dense(results[0].unpack(shared_from_this()), result_rows, type, *dev, kCross);
         const Tensor out2 = restored_dense(results[1].unpack(), result_rows, type, *dev, kCross);
         const Tensor lse = restored_dense(results[2].unpack(), sums, at::kFloat, *dev, kCross);
+        const int64_t rest_rows[5] = {2, d.B, d.H, d.Tq, d.Dv};
+        const Tensor rests =
+            tensor_cores ? restored_dense(results[3].unpack(), rest_rows, type, *dev, kCross) : Tensor();
         const Tensor n = has_lens ? restored(lens.unpack(), d.B, at::kInt, *dev, kCross).contiguous() : Tensor();
         Tensor l;
         if (device_lambda)
@@ -984,9 +987,9 @@ struct CrossBackward : public torch::autograd::Node {
             dlam = fresh_tensor({}, d.lambda_dtype == DIFFATTN_BF16 ? at::kBFloat16 : at::kFloat, *dev);
         const size_t bytes = diffattn_cross_bwd_workspace_bytes(&c);
         const Tensor ws = fresh_tensor({(int64_t)bytes}, at::kByte, *dev);
-        const int rc = diffattn_cross_bwd(&c, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
+        const int rc = diffattn_cross_bwd_ex(&c, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
                                           n.defined() ? n.const_data_ptr<int32_t>() : nullptr, host, ptr(l), ptr(out),
-                                          ptr(out2), fptr(lse), ptr(g), ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), ptr(dx[3]),
+                                          ptr(out2), fptr(lse), ptr(rests), ptr(g), ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), ptr(dx[3]),
                                           ptr(dx[4]), ptr(dlam), ws.data_ptr(), bytes,
                                           stream_of(*dev));
         TORCH_CHECK(rc == DIFFATTN_OK, "diffattn_cross_bwd: ", diffattn_strerror(rc), " (", rc, ")");
@@ -1064,7 +1067,7 @@ PyObject* cross(PyObject* const* a) {
                   "differential_head_norm to its result");
     e.weight = fptr(w);
     e.bias = fptr(b);
-    Tensor t[5], out, out2, lse;
+    Tensor t[5], out, out2, lse, rests;
     {
         at::NoGradGuard no_grad;
         const bool tensor_cores = on_tensor_cores(d) && (grad || d.kv_group * d.Tq > 4);
@@ -1088,14 +1091,15 @@ PyObject* cross(PyObject* const* a) {
         if (grad) {
             out2 = fresh_tensor(out.sizes(), type, dev);
             lse = fresh_tensor({d.B, d.H, d.Tq, 2}, at::kFloat, dev);
+            if (on_tensor_cores(d)) rests = fresh_tensor({2, d.B, d.H, d.Tq, d.Dv}, type, dev);
         }
         // from torch's allocator for every call: calls on other streams, and graphs captured one
         // after another, never share it
         const size_t bytes = diffattn_cross_workspace_bytes(&d);
         const Tensor ws = fresh_tensor({(int64_t)(bytes ? bytes : 16)}, at::kByte, dev);
-        check(diffattn_cross_fwd(&d, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
+        check(diffattn_cross_fwd_ex(&d, ptr(t[0]), ptr(t[1]), ptr(t[2]), ptr(t[3]), ptr(t[4]),
                                  lens.defined() ? lens.const_data_ptr<int32_t>() : nullptr, lam.host, ptr(lam.dev), &e, ptr(out),
-                                 ptr(out2), lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.numel(),
+                                 ptr(out2), lse.defined() ? lse.data_ptr<float>() : nullptr, ptr(rests), ws.data_ptr(), (size_t)ws.numel(),
                                  stream_of(dev)),
               "diffattn_cross_fwd");
     }
@@ -1128,6 +1132,7 @@ PyObject* cross(PyObject* const* a) {
         node->results[0] = torch::autograd::SavedVariable(out, true);
         node->results[1] = torch::autograd::SavedVariable(out2, false);
         node->results[2] = torch::autograd::SavedVariable(lse, false);
+        if (rests.defined()) node->results[3] = torch::autograd::SavedVariable(rests, false);
     }
     if (!is_none(a[7])) {
         Py_INCREF(a[7]);

@@ -60,6 +60,7 @@ struct CrossParams {
     float out_scale;
     void* out2;                 // training: A_2 V with out's strides,
     float* lse;                 // and [B, H, Tq, 2] log-sum-exps (natural), -inf without a key
+    void* rests;                // bf16: dense [2][B, H, Tq, Dv], what the rounding of out and out2 left; or nullptr
     // backward
     const void* dout;
     int64_t s_do[3];
@@ -98,6 +99,7 @@ struct CrossTcParams {
     uint32_t* status;
     uint32_t* sched;            // 2 item counters, and dlambda's
     const __nv_bfloat16* out; const __nv_bfloat16* out2; const __nv_bfloat16* dout;
+    const __nv_bfloat16* rests; // [2][B, H, Tq, 128] of out and out2, or nullptr
     int64_t s_o[3], s_do[3];
     const float* lse;
     float* stats;               // rows of -lse_1, -lse_2 (log2), -Dd_1, -Dd_2

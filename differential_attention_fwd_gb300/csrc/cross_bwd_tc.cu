@@ -8,8 +8,8 @@
 //   dQ_b = dS_b K_b / sqrt(D)       dK_b = dS_b^T Q_b / sqrt(D)
 //   dV   = (A_1 - lambda A_2)^T dO  dlambda = -sum Dd_2
 //
-// stats holds each row's negated log2-sum-exps and, from the forward's saved bf16 results,
-// its negated Dd_b.  Two kernels, as in the backward of self-attention (bwd_tc.cu), both
+// stats holds each row's negated log2-sum-exps and, from the forward's saved results, its
+// negated Dd_b.  Two kernels, as in the backward of self-attention (bwd_tc.cu), both
 // persistent (one CTA an SM, items claimed from a counter, since sequences are of different
 // lengths) with a TMA producer, an MMA-issuing thread and two warpgroups that turn scores
 // into their gradients:
@@ -21,9 +21,12 @@
 //   warpgroups release as soon as it is in registers, dS_b has columns of its own and dO
 //   is read from shared memory.
 //   The warpgroups also sum A_b dP in float32: the row's Dd_b without the roundings of O,
-//   which the dK/dV kernel and dlambda take.  dS itself needs Dd before that sum is known,
-//   and takes the saved one, whose error (2^-9 of |dO| |O|) is small beside dP where O is a
-//   mean over many states; over a single tile, where it is not, the sum comes first.
+//   which the dK/dV kernel and dlambda take.  dS itself needs Dd before that sum is known (but
+//   over a single tile, where the sum comes first), and takes the saved one.  An error of Dd is
+//   every dS's of the row, and dQ's times the keys' weighted mean: from bf16 results alone (2^-8 of
+//   |dO| |O|) it was 13 % of dQ over 4096 states where keys and values have offsets of 2 and 1 of
+//   their spread.  So the forward also leaves the rests of its roundings (18 us of 390 there, 9 here):
+//   0.4 %, what dS's own rounding leaves of so much cancellation.
 // dkdv: item (b, key/value head, 128 states in TMEM lanes, a split of the query rows where there
 //   are few such tiles); over every 64 query rows of the group's heads: S_1^T, S_2^T, dP^T, then
 //   dV += W^T dO, dK_b += dS_b^T Q_b (one accumulator for both branches where they share their
@@ -35,6 +38,11 @@
 // from shared memory and the hand-offs of its one score buffer.  2 x 16 heads of 64, 4096 rows
 // over 4096 states: 334 us and 474 us, with the V2 head (8 key/value heads) 523 and 686: 850 and
 // 909 TFLOP/s of the products that a backward needs.
+//
+// dS_b and W = A_1 - lambda A_2 are rounded once, to bf16, for their products: errors of their own for
+// each element, 2.4e-3 of a gradient with its own rounding.  Where alike branches share their keys,
+// dK is the difference of two products that cancel, and off by 7e-3 of what is left; second parts of
+// both dS would be two of the dK/dV kernel's seven products again.
 //
 // What a batch's padding holds must not reach a sum: in dq the rows of K and V behind a
 // sequence's last state would meet weights of 0, and 0 times NaN is NaN, so a warp turns
@@ -86,43 +94,55 @@ __device__ __forceinline__ void locate(int idx, int heads, int tiles, int group,
 
 // ---------------------------------------------------------------------------
 // The rows' statistics from the forward's saved results: Dd_2 = dO . (A_2 V), Dd_1 = dO . (O +
-// lambda A_2 V), stored negated with the log2-sum-exps.  16 lanes a row, 16 bytes a lane, two rows
-// a group: HBM, 19 us at 131,000 rows, 0.78 of the copy rate (22 us with four rows and half the
-// blocks an SM, 39 with a lane for every fourth pair of bytes).
+// lambda A_2 V), stored negated with the log2-sum-exps.  RESTS: with what the results' rounding left
+// (two bf16 together, 2^-16).  16 lanes a row, 16 bytes a lane, two rows a group: HBM, 28 to 30 us at
+// 131,000 rows with the rests, 0.85 to 0.9 of the copy rate (19 without).
 // ---------------------------------------------------------------------------
 constexpr int PREP_THREADS = 256;
 constexpr int PREP_ROWS = 2;            // of a group of lanes, loaded together
-__global__ void __launch_bounds__(PREP_THREADS, 6)
+template <bool RESTS>
+__global__ void __launch_bounds__(PREP_THREADS, RESTS ? 4 : 6)
 cross_prep_kernel(const CrossTcParams p) {
-    constexpr int GROUPS = PREP_THREADS / 16;
+    constexpr int GROUPS = PREP_THREADS / 16, N = RESTS ? 5 : 3;
     const int g = threadIdx.x % 16, h = blockIdx.y % p.H, b = blockIdx.y / p.H;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 3) p.sched[threadIdx.x] = 0;
     const int q0 = blockIdx.x * (GROUPS * PREP_ROWS) + threadIdx.x / 16;
     const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
-    uint4 raw[PREP_ROWS][3];
+    const int64_t second = (int64_t)p.B * p.H * p.Tq * VD;      // of the rests
+    uint4 raw[PREP_ROWS][N];
 #pragma unroll
     for (int i = 0; i < PREP_ROWS; ++i) {
         const int q = q0 + i * GROUPS;
         const int64_t o = b * p.s_o[0] + h * p.s_o[1] + q * p.s_o[2] + 8 * g;
         const int64_t d = b * p.s_do[0] + h * p.s_do[1] + q * p.s_do[2] + 8 * g;
-        raw[i][0] = raw[i][1] = raw[i][2] = make_uint4(0, 0, 0, 0);
+        const int64_t row = ((int64_t)b * p.H + h) * p.Tq + q;
+#pragma unroll
+        for (int j = 0; j < N; ++j) raw[i][j] = make_uint4(0, 0, 0, 0);
         if (q < p.Tq) {
             raw[i][0] = *reinterpret_cast<const uint4*>(p.dout + d);
             raw[i][1] = *reinterpret_cast<const uint4*>(p.out + o);
             raw[i][2] = *reinterpret_cast<const uint4*>(p.out2 + o);
+            if constexpr (RESTS) {
+                raw[i][3] = *reinterpret_cast<const uint4*>(p.rests + row * VD + 8 * g);
+                raw[i][4] = *reinterpret_cast<const uint4*>(p.rests + second + row * VD + 8 * g);
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < PREP_ROWS; ++i) {
         const int q = q0 + i * GROUPS;
-        uint64_t x[3][4];
+        uint64_t x[N][4];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) Vec<__nv_bfloat16>::unpack(raw[i][j], x[j]);
+        for (int j = 0; j < N; ++j) Vec<__nv_bfloat16>::unpack(raw[i][j], x[j]);
         uint64_t d0 = 0, d2 = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             d0 = f2_fma(x[0][e], x[1][e], d0);
             d2 = f2_fma(x[0][e], x[2][e], d2);
+            if constexpr (RESTS) {
+                d0 = f2_fma(x[0][e], x[3][e], d0);
+                d2 = f2_fma(x[0][e], x[4][e], d2);
+            }
         }
         const float s0 = group_sum<16>(f2_lo(d0) + f2_hi(d0)), s2 = group_sum<16>(f2_lo(d2) + f2_hi(d2));
         if (g != 0 || q >= p.Tq) continue;
@@ -1112,7 +1132,8 @@ int launch(const CUtensorMap* maps, const CrossTcParams& p, int num_sms, cudaStr
         return -1;
     const int dq_items = p.B * p.H * p.nq128, kv_items = p.B * p.Hk * p.nk128 * p.splits;
     constexpr int PER = PREP_THREADS / 16 * PREP_ROWS;
-    cross_prep_kernel<<<dim3((p.Tq + PER - 1) / PER, p.B * p.H), PREP_THREADS, 0, stream>>>(p);
+    const auto prep = p.rests ? cross_prep_kernel<true> : cross_prep_kernel<false>;
+    prep<<<dim3((p.Tq + PER - 1) / PER, p.B * p.H), PREP_THREADS, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -1;
     dq::diffattn_cross_dq_kernel<HD><<<dq_items < num_sms ? dq_items : num_sms, NUM_THREADS, dq::smem_bytes<HD>(), stream>>>(
         maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);

@@ -233,6 +233,13 @@ __device__ __forceinline__ void put4(T* row, int c, int width, float4 x, float s
         if (c + i < width) row[c + i] = Vec<T>::put(v[i] * s);
 }
 
+// What the rounding to T leaves.
+template <typename T>
+__device__ __forceinline__ float4 left(float4 x) {
+    const auto f = [](float v) { return v - Vec<T>::get(Vec<T>::put(v)); };
+    return make_float4(f(x.x), f(x.y), f(x.z), f(x.w));
+}
+
 // A block's 32 query rows: batch, head, key/value head and first row.
 struct Rows {
     int b, h, hk, q0, count;
@@ -381,6 +388,9 @@ cross_fwd_kernel(const CrossParams p) {
     __syncthreads();
     const float lam = lambda_of(p.lambda_dev, p.lambda_bf16, p.lambda);
     T* out2 = p.out2 ? static_cast<T*>(p.out2) + r.b * p.s_o[0] + r.h * p.s_o[1] + r.q0 * p.s_o[2] : nullptr;
+    // dense rows of what the roundings of O and A_2 V leave
+    T* rest = p.rests ? static_cast<T*>(p.rests) + (((int64_t)r.b * p.H + r.h) * p.Tq + r.q0) * p.Dv : nullptr;
+    T* rest2 = rest + (int64_t)p.B * p.H * p.Tq * p.Dv;
 #pragma unroll
     for (int i = 0; i < Z::RV; ++i) {
         const float i1 = fix[r0 + i], i2 = fix[BM + r0 + i];
@@ -395,6 +405,7 @@ cross_fwd_kernel(const CrossParams p) {
                 make_float4(fmaf(-lam, b.x, __fmul_rn(x.x, i1)), fmaf(-lam, b.y, __fmul_rn(x.y, i1)),
                             fmaf(-lam, b.z, __fmul_rn(x.z, i1)), fmaf(-lam, b.w, __fmul_rn(x.w, i1)));
             if (out2 && r0 + i < r.count) put4(out2 + (r0 + i) * p.s_o[2], c, p.Dv, b, 1.f);
+            if (rest && r0 + i < r.count) put4(rest2 + (int64_t)(r0 + i) * p.Dv, c, p.Dv, left<T>(b), 1.f);
         }
     }
     __syncthreads();
@@ -419,6 +430,7 @@ cross_fwd_kernel(const CrossParams p) {
             if (p.norm_weight) x *= __ldg(p.norm_weight + (int64_t)r.h * p.Dv + c);
             if (p.norm_bias) x += __ldg(p.norm_bias + (int64_t)r.h * p.Dv + c);
             dst[c] = Vec<T>::put(x * p.out_scale);
+            if (rest) rest[(int64_t)i * p.Dv + c] = Vec<T>::put(x * p.out_scale - Vec<T>::get(dst[c]));
         }
     }
 }

@@ -322,6 +322,21 @@ __device__ __forceinline__ float tile_row_max(const float (&s)[64]) {
     return fmax3(mx0, mx1, fmaxf(mx2, mx3));
 }
 
+// What the rounding of a thread's 64 columns of a row leaves, rounded.
+__device__ __forceinline__ void put_rests(__nv_bfloat16* row, const float (&x)[64]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = x[8 * i + 2 * e], b = x[8 * i + 2 * e + 1];
+            const uint32_t hi = pack_bf16x2(a, b);
+            w[e] = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+        }
+        *reinterpret_cast<uint4*>(row + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // P = 2^(s * scale_log2 - m) for one thread's 64 scores, two columns per
 // packed operation: P rounded to bf16 pairs into pk, and the sum of the
 // unrounded P returned.  TWO: what the rounding leaves of each goes into rest.
@@ -835,6 +850,14 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
 #pragma unroll
                     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(o2row + 8 * i) = make_uint4(w, w, w, w);
                     p.lse[(((int64_t)it.b * p.H + h) * p.T + q) * 2 + br] = it.bad ? fill : -INFINITY;
+                    if (p.rests) {
+                        __nv_bfloat16* rest = p.rests + (((int64_t)it.b * p.H + h) * p.T + q) * VD + c0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            *reinterpret_cast<uint4*>(rest + 8 * i) = make_uint4(w, w, w, w);
+                            *reinterpret_cast<uint4*>(rest + (int64_t)p.B * p.H * p.T * VD + 8 * i) = make_uint4(w, w, w, w);
+                        }
+                    }
                 }
             } else {
                 if (!(ok = TIMED_WAIT(wp, kWaitEpilogue, mbar_wait_warp(&bars[BAR_O_FULL], ofph, ab)))) break;
@@ -926,6 +949,16 @@ diffattn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q1,
                     const float a = __fmul_rn(__uint_as_float(o1[c]), inv1);
                     const float bb = __fmul_rn(__uint_as_float(o2[c]), inv2);
                     r[c] = __fmaf_rn(bb, -lam, a);
+                }
+                if constexpr (CROSS) {
+                    if (p.rests && q < p.T) {
+                        __nv_bfloat16* rest = p.rests + (((int64_t)it.b * p.H + h) * p.T + q) * VD + c0;
+                        put_rests(rest, r);
+                        float x[64];
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = __fmul_rn(__uint_as_float(o2[c]), inv2);
+                        put_rests(rest + (int64_t)p.B * p.H * p.T * VD, x);
+                    }
                 }
                 PROF_ADD(wp, kEpiMath, math_t0);
                 PROF_ADD(wp, kEpilogueBusy, epi_t0);

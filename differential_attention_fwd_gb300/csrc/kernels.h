@@ -64,7 +64,9 @@ struct TcParams {
     // + t][branch].
     __nv_bfloat16* out2;
     float* lse;
-    const int32_t* lengths;     // the cross instances: [B], nullptr: Tk each
+    __nv_bfloat16* rests;       // the cross instances: dense [2][B, H, T, 128], what the rounding of out and
+                                // out2 left (training), or nullptr
+    const int32_t* lengths;     // and [B], nullptr: Tk each
     int pack, pack_shift;       // and heads of a group that an item takes, 2^pack_shift rows of its
                                 // 128 each (1, 7: a head)
     int item_heads;             // H / pack

@@ -761,6 +761,32 @@ int diffattn_cross_bwd(const diffattn_cross_desc *desc, const void *q1, const vo
                        void *workspace, size_t workspace_bytes, diffattn_stream_t stream);
 
 /*
+ * diffattn_cross_fwd_ex, diffattn_cross_bwd_ex -- the two of a training step in bf16 with
+ * `rests`, what the roundings of O and of A_2 V left, rounded themselves: dense, [2][B, H, Tq,
+ * Dv] of the inputs' dtype, 16-byte aligned, written by the forward and read by the backward.
+ * dS of the tensor cores' dQ kernel takes rowsum(A_b dP) = dO . (A_b V) from the saved results: from
+ * O and out2 alone it is off by 2^-8 of |dO| |O|, and dQ by that times the keys' weighted mean,
+ * which is much where keys and values have offsets (13 % of dQ over 4096 states, offsets of
+ * 2 and 1 of their spread); with `rests` by 2^-16.  NULL: the calls without.  The CUDA cores sum A_b dP
+ * itself, and need none.
+ * Errors: theirs, and DIFFATTN_ERR_INVALID for rests that are misaligned, of another dtype
+ * than bf16, or (the forward) without out2 and lse.
+ */
+int diffattn_cross_fwd_ex(const diffattn_cross_desc *desc, const void *q1, const void *k1,
+                          const void *q2, const void *k2, const void *v,
+                          const int32_t *kv_lengths, float lambda, const void *lambda_dev,
+                          const diffattn_epilogue *epi, void *out, void *out2, float *lse,
+                          void *rests, void *workspace, size_t workspace_bytes,
+                          diffattn_stream_t stream);
+int diffattn_cross_bwd_ex(const diffattn_cross_desc *desc, const void *q1, const void *k1,
+                          const void *q2, const void *k2, const void *v,
+                          const int32_t *kv_lengths, float lambda, const void *lambda_dev,
+                          const void *out, const void *out2, const float *lse, const void *rests,
+                          const void *dout, void *dq1, void *dk1, void *dq2, void *dk2, void *dv,
+                          void *dlambda, void *workspace, size_t workspace_bytes,
+                          diffattn_stream_t stream);
+
+/*
  * The norm of each head's output: the epilogue above as an operator of its own, with
  * its gradients.  For a row x of C channels (1 .. 256) of head h, with mu = mean(x)
  * (DIFFATTN_NORM_GROUP) or 0 (DIFFATTN_NORM_RMS), r = (mean((x - mu)^2) + eps)^-1/2,

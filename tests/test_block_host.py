@@ -167,6 +167,19 @@ def test_cross_argument_refusals(lib):
         assert cross_fwd(lib, cross_desc(**big)) == UNSUPPORTED
 
 
+def test_cross_rests_refusals(lib):
+    def fwd(d=None, out2=p(6), lse=p(7), rests=p(8)):
+        return lib.diffattn_cross_fwd_ex(ctypes.byref(d or cross_desc()), *map(p, range(5)), None, 0.5, None, None, p(5), out2, lse,
+                                         rests, p(40), 1 << 30, None)
+
+    def bwd(d=None, rests=p(8)):
+        return lib.diffattn_cross_bwd_ex(ctypes.byref(d or cross_desc()), *map(p, range(5)), None, 0.5, None, p(5), p(6), p(7), rests,
+                                         p(9), *map(p, range(10, 15)), p(15), p(40), 1 << 30, None)
+    assert fwd(out2=None, lse=None) == INVALID                         # nothing to leave a rest of
+    for kw in (dict(rests=p(8) + 8), dict(d=cross_desc(dtype=1))):
+        assert fwd(**kw) == INVALID and bwd(**kw) == INVALID
+
+
 @pytest.mark.parametrize("lens", [[4, 2], [3, 0]])
 def test_cross_reference_gradients(lens):
     g = torch.Generator().manual_seed(1)

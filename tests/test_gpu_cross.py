@@ -260,6 +260,89 @@ def test_weights_in_two_parts(D, shared, Tq, Tk, kind):
     check("training o", o, want.o, want.o_tol + 2.0 ** -8 * want.o.abs())
 
 
+@pytest.mark.parametrize("D,shared", [(64, False), (64, True), (128, True), (128, False)])
+@pytest.mark.parametrize("Tk", [65, 130, 300, 1500])
+@pytest.mark.parametrize("kind", ["offsets", "peaks", "alike"])
+def test_query_gradients_where_rows_share_an_error(D, shared, Tk, kind):
+    """dQ where keys and values have offsets, where one state takes nearly all of a row, and where
+    the branches are alike, against what roundings of dS allow if each is its own.
+
+    dS_j and dQ are rounded by 2^-8 at most each, of either sign, so that a row's error is a
+    sum of independent terms e_j K_j with |e_j| <= 2^-8 |dS_j|: its squared norm is on average at
+    most sum_j (2^-8 |dS_j| |K_j|)^2, and (2^-8 |dQ|)^2 for the result's.  (Uniform errors have a third of
+    these squares, so a tensor of 400 rows stays below the sum, and a row below three times its root.)
+    What a row's dS share, the error of Dd, is the bound of a forward that rounds by 2^-16."""
+    lens = [Tk, Tk - 40]
+    H, Tq = 2, 100
+    x, n = inputs(25, BF, 2, H, 1, Tq, Tk, D, 128, shared, lens)
+    g = torch.Generator().manual_seed(26)
+    normal = lambda *shape: torch.randn(*shape, generator=g).cuda()                 # noqa: E731
+    if kind == "offsets":
+        x[1] = (x[1] + 2 * normal(D)).to(BF)
+        x[3] = x[1] if shared else (x[3] + 2 * normal(D)).to(BF)
+        x[4] = (x[4] + 2 * normal(128)).to(BF)
+    else:
+        x[0], x[2] = 4 * x[0], 4 * x[2]
+        if kind == "alike":
+            x[2] = (x[0] + 0.2 * normal(2, H, Tq, D)).to(BF)
+            x[3] = x[1] if shared else (x[1] + 0.2 * normal(2, 1, Tk, D)).to(BF)
+    lam = float(torch.tensor(0.8))
+    do = torch.randn(2, H, Tq, 128, generator=g).to(BF).cuda()
+    _, grads = train(x, n, lam, do)
+    clean = [torch.nan_to_num(d64(t), 0.0, 0.0, 0.0) for t in x]
+    want = ref.Cross(*clean, lam, lens, 2.0 ** -16)
+    shares = want.backward(d64(do))
+    for name, j in (("q1", 0), ("q2", 1)):
+        w, share = shares[name]
+        own = (2.0 ** -8 * w).square().sum(-1)
+        for (b, i), (A, _, _, _) in want.heads.items():
+            K = clean[1 + 2 * j][b, 0, :lens[b]]
+            dP = d64(do)[b, i] @ clean[4][b, 0, :lens[b]].T
+            dS = (1.0, lam)[j] * A[j] * (dP - (A[j] * dP).sum(-1, keepdim=True)) * D ** -0.5
+            own[b, i] += (2.0 ** -8 * dS).square() @ K.square().sum(-1)
+        err = (d64(grads[name]) - w)
+        excess = (err.abs() - share).clamp(min=0).square().sum(-1)
+        assert excess.sum() <= own.sum(), (name, excess.sum().item() / own.sum().item())
+        assert (excess <= 9 * own + 1e-30).all(), (name, (excess / own).max().item())
+
+
+def test_training_without_rests():
+    """The C ABI's calls without the rests of the forward's roundings: a row's Dd from O and A_2 V as
+    they were rounded."""
+    import ctypes
+    from differential_attention_fwd_gb300 import _lib
+    lib = _lib.load()
+    lens = [300, 140]
+    for D, shared in ((64, False), (128, True)):
+        x, n = inputs(27, BF, 2, 4, 2, 70, 300, D, 128, shared, lens)
+        do = torch.randn(2, 4, 70, 128, device="cuda").to(BF)
+        d = _lib.DiffattnCrossDesc()
+        d.B, d.H, d.Tq, d.Tk, d.D, d.Dv, d.dtype, d.kv_group, d.lambda_dtype = 2, 4, 70, 300, D, 128, _lib.DIFFATTN_BF16, 2, _lib.DIFFATTN_F32
+        o, o2 = torch.empty_like(do), torch.empty_like(do)
+        lse = torch.empty(2, 4, 70, 2, device="cuda")
+        for f, t in zip(("q1", "k1", "q2", "k2", "v", "o", "dout"), x + [o, do]):
+            getattr(d, f + "_stride")[:] = t.stride()[:3]
+        grads = [torch.empty_like(t) for t in x]
+        if shared:
+            grads[3] = None
+        dlam = torch.empty((), device="cuda")
+        p = lambda t: None if t is None else t.data_ptr()                           # noqa: E731
+        ws = torch.empty(max(lib.diffattn_cross_workspace_bytes(ctypes.byref(d)), lib.diffattn_cross_bwd_workspace_bytes(ctypes.byref(d))),
+                         dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.current_stream().cuda_stream
+        assert lib.diffattn_cross_fwd(ctypes.byref(d), *map(p, x), p(n), 0.8, None, None, p(o), p(o2), p(lse), p(ws), ws.numel(), stream) == 0
+        assert lib.diffattn_cross_bwd(ctypes.byref(d), *map(p, x), p(n), 0.8, None, p(o), p(o2), p(lse), p(do), *map(p, grads), p(dlam),
+                                      p(ws), ws.numel(), stream) == 0
+        want = reference(x, float(torch.tensor(0.8)), lens)
+        back = want.backward(d64(do))
+        if shared:
+            back["k1"] = back["k"]
+        check("o", o, want.o, want.o_tol)
+        for name, t in zip(("q1", "k1", "q2", "k2", "v", "lam"), grads + [dlam]):
+            if t is not None:
+                check("d" + name, t, *back[name])
+
+
 @pytest.mark.parametrize("norm", ["rms", "group"])
 @pytest.mark.parametrize("D,shared", [(64, False), (128, True)])
 @pytest.mark.parametrize("H,Hk,Tq", [(16, 16, 130), (16, 4, 20)])
