@@ -23,14 +23,17 @@ def differential_cross_attention(q1: torch.Tensor, k1: torch.Tensor, q2: torch.T
 
     q1, q2: [B, H, Tq, D]; k1, k2: [B, H_kv, Tk, D], value: [B, H_kv, Tk, Dv], the encoder's
     states as the layer projected them, H_kv dividing H, D <= 128, Dv <= 256; bfloat16 or
-    float32; other strides than the innermost pass through (in bf16 with Dv = 128 and D = 64 or
-    128, rows with a stride of 0 or not of whole 16-byte pieces are copied first, beyond a few
-    rows).  k2 None or k1 again: one key
-    tensor for both branches.  kv_lengths: [B] int32 on the device, sequence b has only its
-    first kv_lengths[b] states (None: all Tk), and what lies behind them has no influence,
-    NaN included; one with none gives zeros (before the epilogue).  coefficient, out and the
-    epilogue (norm .. out_scale) as differential_attention, norm_weight and norm_bias with a
-    norm alone; out may not overlap the inputs.
+    float32; other strides than the innermost pass through.  k2 None or k1 again (the same
+    object): one key tensor for both branches.  kv_lengths: [B] int32 on the device, sequence b
+    has only its first kv_lengths[b] states (None: all Tk), and what lies behind them has no
+    influence, NaN included; one with none gives zeros (before the epilogue).  coefficient, out
+    and the epilogue (norm .. out_scale) as differential_attention, norm_weight and norm_bias
+    with a norm alone; out may not overlap the inputs.
+
+    The tensor cores take bfloat16 with Dv = 128 and D = 64 or 128, in training D = 128 with one
+    key tensor.  Inputs whose rows have a stride of 0 or are not of whole 16-byte pieces are
+    copied for them, beyond a few rows.  Other widths, an out of such rows, and a training step
+    of more than 65535 sequences times heads run on the CUDA cores, about forty times slower.
 
     Returns [B, H, Tq, Dv].  In bfloat16 the weights keep 16 bits on every path, so that what
     branches that cancel leave is off by its own rounding alone.  Differentiable in q1, q2, k1,

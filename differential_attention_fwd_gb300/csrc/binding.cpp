@@ -925,7 +925,7 @@ bool on_tensor_cores(const diffattn_cross_desc& d) {
 struct CrossBackward : public torch::autograd::Node {
     diffattn_cross_desc d{};                // its strides are the forward's: what is unpacked has its own
     float host = 0.f;
-    bool shared = false, tensor_lambda = false, device_lambda = false, has_lens = false;
+    bool shared = false, tensor_lambda = false, device_lambda = false, has_lens = false, has_rests = false;
     torch::autograd::SavedVariable x[5], lens, results[4];  // q1, k1, q2, k2, value; out, out2, lse, rests
     torch::autograd::SavedVariable lam, lam_read;                   // as given, and as the kernels read it
     std::vector<int64_t> lam_shape;
@@ -960,7 +960,7 @@ struct CrossBackward : public torch::autograd::Node {
         const Tensor lse = restored_dense(results[2].unpack(), sums, at::kFloat, *dev, kCross);
         const int64_t rest_rows[5] = {2, d.B, d.H, d.Tq, d.Dv};
         const Tensor rests =
-            tensor_cores ? restored_dense(results[3].unpack(), rest_rows, type, *dev, kCross) : Tensor();
+            has_rests ? restored_dense(results[3].unpack(), rest_rows, type, *dev, kCross) : Tensor();
         const Tensor n = has_lens ? restored(lens.unpack(), d.B, at::kInt, *dev, kCross).contiguous() : Tensor();
         Tensor l;
         if (device_lambda)
@@ -1091,7 +1091,8 @@ PyObject* cross(PyObject* const* a) {
         if (grad) {
             out2 = fresh_tensor(out.sizes(), type, dev);
             lse = fresh_tensor({d.B, d.H, d.Tq, 2}, at::kFloat, dev);
-            if (on_tensor_cores(d)) rests = fresh_tensor({2, d.B, d.H, d.Tq, d.Dv}, type, dev);
+            // (two key tensors 128 wide have their backward on the CUDA cores, which need none)
+            if (on_tensor_cores(d) && (d.D == 64 || ptr(t[1]) == ptr(t[3]))) rests = fresh_tensor({2, d.B, d.H, d.Tq, d.Dv}, type, dev);
         }
         // from torch's allocator for every call: calls on other streams, and graphs captured one
         // after another, never share it
@@ -1132,6 +1133,7 @@ PyObject* cross(PyObject* const* a) {
         node->results[0] = torch::autograd::SavedVariable(out, true);
         node->results[1] = torch::autograd::SavedVariable(out2, false);
         node->results[2] = torch::autograd::SavedVariable(lse, false);
+        node->has_rests = rests.defined();
         if (rests.defined()) node->results[3] = torch::autograd::SavedVariable(rests, false);
     }
     if (!is_none(a[7])) {

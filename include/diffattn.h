@@ -703,6 +703,11 @@ int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages 
  * lambda_dtype: of the value that lambda_dev points to, and of dlambda.
  * *_stride: element strides of B, heads and rows (innermost 1; >= 0); o_stride of O (and
  * of out2), dout_stride of its gradient (the backward only).  reserved: 0.
+ * The tensor cores take bf16 with Dv = 128 and D = 64 or 128 (the backward: D = 128 with one
+ * key tensor, and B H <= 65535), where every tensor is 16-byte aligned and its strides, of
+ * the dimensions longer than 1, are positive multiples of 8; a few rows over many states also
+ * with other strides of Q and O.  Other calls run on the CUDA cores, about forty times slower:
+ * copy what does not fit.
  */
 typedef struct {
     int64_t B, H, Tq, Tk, D, Dv;
