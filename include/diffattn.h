@@ -696,7 +696,8 @@ int diffattn_paged_decode(const diffattn_paged_desc *desc, const diffattn_pages 
  *
  * over the first kv_lengths[b] of the Tk states of sequence b.  The others (a batch's
  * padding) are not looked at, NaN and infinities included; a sequence without a state
- * (length 0) gives zeros.
+ * (length 0) gives zeros.  A value of a state that is not finite makes its column NaN for the
+ * sequence's rows (at lambda < 0 it may be an infinity).
  *
  * Q1, Q2: [B, H, Tq, D]; K1, K2: [B, H / kv_group, Tk, D]; V: [B, H / kv_group, Tk, Dv];
  * O: [B, H, Tq, Dv].  D <= 128, Dv <= 256 (0: 2D), dtype, kv_group as in diffattn_desc;

@@ -201,3 +201,24 @@ def test_head_norm(hook, layout, dtype, norm):
         y = f()
     for a, c in zip(torch.autograd.grad(y, (x, w, b), do), want):
         assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype,D,Dv", [(BF, 64, 128), (BF, 128, 128), (F32, 32, 64)])
+def test_recomputed_block(dtype, D, Dv):
+    """Rotation, attention and head norm under activation checkpointing: the bits of the block itself."""
+    from torch.utils.checkpoint import checkpoint
+    g = torch.Generator().manual_seed(11)
+    q1, q2 = projected(g, dtype, "fused", 2, 40, [(4, D), (4, D)])
+    k, v = projected(g, dtype, "fused", 2, 70, [(2, D), (2, Dv)])
+    leaves = [t.detach().requires_grad_() for t in (q1, k, q2, v)] + [torch.tensor(0.8, dtype=dtype, device="cuda").requires_grad_()]
+    cos, sin = da.rotary_tables(90, D, device="cuda")
+    n = torch.tensor([70, 31], dtype=torch.int32, device="cuda")
+
+    def block(q1, k, q2, v, lam):
+        q1, _, q2, _ = da.qk_norm_rotary(q1, None, q2, None, cos, sin)
+        return da.differential_head_norm(da.differential_cross_attention(q1, k, q2, None, v, lam, kv_lengths=n), out_scale=0.2)
+    do = torch.randn(2, 4, 40, Dv, generator=g).to(dtype).cuda()
+    want = torch.autograd.grad(block(*leaves), leaves, do)
+    got = torch.autograd.grad(checkpoint(block, *leaves, use_reentrant=False), leaves, do)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
